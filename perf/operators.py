@@ -339,7 +339,7 @@ def _tables(st):
     granted = (need == 0) | (upto <= free)
     new = torch.where(granted, new, 0)
     pages = torch.where(granted, want, have)
-    taken = torch.where(granted, upto, 0).amax()
+    taken = torch.where(granted & (need > 0), upto, 0).amax()  # a run of the list without holes
     kv_len = cached + new
     zero = torch.zeros(1, dtype=torch.int64, device=cached.device)
     kv_ptr, qo_ptr, tok_ptr = (torch.cat([zero, x.cumsum(0)]) for x in (pages, new, kv_len))
