@@ -92,6 +92,11 @@ enum { PDA_KERNEL_AUTO = 0, PDA_KERNEL_MMA = 1, PDA_KERNEL_TC = 2 };
 #define PDA_STATUS_WAIT_TIMEOUT 0x20u   /* a pipeline wait ran past its bound; the CTA gave up */
 #define PDA_STATUS_SMEM_MISALIGNED 0x40u /* a stage-1 CTA's shared-memory window was not 1024-byte
                                             aligned; that CTA wrote nothing */
+#define PDA_STATUS_TABLE_INVALID 0x80u  /* pda_build_tables: a negative length, or a block-table row or
+                                           column out of range */
+#define PDA_STATUS_NO_PAGES 0x100u      /* pda_build_tables: the free list ran out */
+#define PDA_STATUS_TABLE_FULL 0x200u    /* pda_build_tables: page_table_cap or rows_cap reached */
+#define PDA_STATUS_TOKENS_GT_CAP 0x400u /* tok_indptr[batch] > the call's tokens */
 
 /* Everything the planner needs; plain values, no device pointers. */
 typedef struct {
@@ -293,6 +298,189 @@ int pda_decode_static(const pda_plan_t* plan, const void* q, const void* k_pages
                       const int32_t* kv_len, const int32_t* qo_indptr, int32_t max_q_len,
                       const int32_t* window, float sm_scale, const float* k_scale,
                       const float* v_scale, void* out, float* lse, pda_stream_t stream);
+
+/* ------------------------------------------------- around the decode step
+ *
+ * Block tables, append for any number of rows, and latent attention (MLA) in
+ * its absorbed and its expanded form. The pages have no counterpart of these
+ * calls; they make what pda_decode reads and use what it writes. Like
+ * pda_decode they allocate nothing, never synchronise and enqueue work only
+ * on `stream` (current device = the plan's device), so they can be captured
+ * in a CUDA graph; every pointer is borrowed device memory unless it says
+ * otherwise. split_scratch: the plan's scratch, of which they use only the
+ * status word (pda_mla_prefill: its own scratch). No rows (or tokens): PDA_OK,
+ * nothing launched, the row pointers may be NULL. Index arrays hold int32
+ * unless stated. Outputs must not overlap inputs. */
+
+/* Arrays of pda_build_tables (device pointers, plain counts). */
+typedef struct {
+  const int32_t* cached_len; /* [batch] tokens of each request already cached, >= 0 */
+  const int32_t* new_len;    /* [batch] tokens this step adds, >= 0 */
+  const int32_t* request;    /* [batch] block_table row of each request, all different; NULL = row b */
+  int32_t* block_table;      /* [table_rows, table_cols] page ids, rows table_stride apart: entry j of a
+                                row holds tokens [jP, jP + P); entries below ceil(cached / P) are read,
+                                the grown ones written */
+  int64_t table_stride;      /* entries between rows, >= table_cols */
+  const int32_t* free_pages; /* free list, taken from its end; at least free_count[0] entries */
+  const int32_t* free_count; /* [1] */
+  int32_t* free_left;        /* [1] written: free_count minus the pages taken; not free_count itself */
+  int32_t* kv_len;           /* [batch] written: cached + new; neither of the two arrays themselves */
+  int32_t* kv_indptr;        /* [batch + 1] written: CSR offsets into page_table */
+  int32_t* page_table;       /* [page_table_cap] written: pages of every request, in order */
+  int32_t* qo_indptr;        /* [batch + 1] written: offsets of the new rows */
+  int32_t* tok_indptr;       /* [batch + 1] written: offsets of kv_len (pda_mla_expand); or NULL */
+  int64_t* slot_map;         /* [rows_cap] written: page * P + slot of each new row; or NULL */
+  int32_t* positions;        /* [rows_cap] written: position of each new row; or NULL */
+  int32_t table_rows, table_cols, page_table_cap, rows_cap;
+} pda_tables;
+
+/* Block tables and slot maps of one step, from the request lengths. Request
+ * b of plan->batch grows from cached_len[b] to kv_len[b] = cached + new
+ * tokens; its new pages ceil(kv_len / P) - ceil(cached / P) come off the end
+ * of the free list (request by request, in the order of b, the first page
+ * from the list's last entry), go into its block_table row, and the request's
+ * pages into page_table. Row i of the request is token cached + i.
+ * The call reads free_count and writes free_left, so running it again with
+ * the same inputs gives the same outputs; the next step passes free_left as
+ * free_count (two words used in turn).
+ * What a request cannot have, it does not get in part:
+ *  - a request whose new pages end past the free list (counted over all the
+ *    requests up to it, refused ones too) is left as it was: kv_len = cached,
+ *    no rows, no new pages, its old pages listed; PDA_STATUS_NO_PAGES;
+ *  - an invalid request (negative length, row or columns out of range,
+ *    kv_len above the plan's max_kv_len: PDA_STATUS_KV_LEN_GT_MAX) is listed
+ *    with kv_len 0, no rows and no pages; PDA_STATUS_TABLE_INVALID;
+ *  - from the first request on whose pages, rows or tokens would pass
+ *    page_table_cap, rows_cap or an int32 offset, every request is listed with
+ *    kv_len 0, no rows and no pages; PDA_STATUS_TABLE_FULL.
+ * Entries of page_table, slot_map and positions behind the last request are
+ * left as they were. A page id outside [0, num_pages) is listed as it is; the
+ * new rows in it get slot -1, and PDA_STATUS_PAGE_OOB is set. plan->batch may
+ * be at most 65536. */
+int pda_build_tables(const pda_plan_t* plan, const pda_tables* tables, void* split_scratch,
+                     pda_stream_t stream);
+
+/* Append through a slot map: row i of k_new / v_new goes to slot
+ * slot_map[i] = page * P + slot of the plan's cache, every kv head of it, in
+ * the formats of pda_append_kv, for any number of rows (a prefill). The MLA
+ * latents (head_dim 576) are appended too: bf16, E4M3 per tensor or per token
+ * (over all 576 channels), or records; their v arguments are not used and may
+ * be NULL.
+ *   k_new, v_new  bf16 [rows, Hkv, D], rows k_stride / v_stride elements apart
+ *                 (multiples of 8, >= Hkv * D)
+ *   slot_map      int64 [rows]; -1 = skip the row; other values outside
+ *                 [0, num_pages * P) skip it and set PDA_STATUS_PAGE_OOB. Two
+ *                 rows of one slot leave a mix of both there.
+ *   rows          rows of k_new and slot_map; num_rows, when not NULL, is one
+ *                 device int32: only rows [0, min(rows, *num_rows)) are taken
+ *                 (&qo_indptr[batch] in a captured step) */
+int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64_t k_stride,
+                     const void* v_new, int64_t v_stride, const int64_t* slot_map, int32_t rows,
+                     const int32_t* num_rows, void* k_pages, void* v_pages, float* k_scale,
+                     float* v_scale, void* split_scratch, pda_stream_t stream);
+
+/* Latent attention. A head's query has 192 channels: 128 without position
+ * (nope) and 64 rotated (rope); a token's latent c has 512 channels beside its
+ * 64-channel rope key, shared by all heads. With a head's weights W_UK and
+ * W_UV [128, 512], its key is [W_UK c, rope] and its value W_UV c:
+ *   absorbed: q_lat = [W_UK^T q_nope, q_rope] meets the latent itself
+ *             (pda_decode, head_dim 576), and out = W_UV o_lat;
+ *   expanded: k = W_UK c and v = W_UV c are made once for a prefill.
+ * The plan is an MLA plan (head_dim 576, head_dim_v 512, one kv head);
+ * num_qo_heads is the number of heads. Weights are bf16, heads w_stride_head
+ * elements apart (a multiple of 8), rows of 512 contiguous: [Hq, 256, 512] with
+ * W_UK first is w_uk = w, w_uv = w + 128 * 512, w_stride_head = 256 * 512.
+ * num_rows (device int32 [1], or NULL) bounds the rows as in
+ * pda_append_slots; rows past it are left as they were. All sums are fp32,
+ * rounded once to the output type. */
+
+/* q_lat[t, h, :512] = sum_d q[t, h, d] W_UK[h, d, :] (d < 128), and
+ * q_lat[t, h, 512:] = q[t, h, 128:].
+ *   q      bf16 [rows, Hq, 192], strides in elements (multiples of 8)
+ *   q_lat  [rows, Hq, 576] contiguous, the plan's q_dtype: bf16, or E4M3 codes
+ *          RNE(sat(x / q_scale)) (q_scale > 0; pda_decode's sm_scale takes it) */
+int pda_mla_absorb(const pda_plan_t* plan, const void* q, int64_t q_stride_row,
+                   int64_t q_stride_head, const void* w_uk, int64_t w_stride_head, float q_scale,
+                   void* q_lat, int32_t rows, const int32_t* num_rows, void* split_scratch,
+                   pda_stream_t stream);
+
+/* out[t, h, d] = sum_c o_lat[t, h, c] W_UV[h, d, c]: o_lat bf16 [rows, Hq, 512]
+ * as pda_decode wrote it, out bf16 [rows, Hq, 128], both contiguous. */
+int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const void* w_uv,
+                    int64_t w_stride_head, void* out, int32_t rows, const int32_t* num_rows,
+                    void* split_scratch, pda_stream_t stream);
+
+/* Keys and values of cached tokens, through the page table: token i of
+ * request b (i < tok_indptr[b + 1] - tok_indptr[b]) is row tok_indptr[b] + i.
+ *   k_pages     the latent cache as planned (bf16, E4M3 or records); k_scale as
+ *               for pda_decode (NULL for bf16)
+ *   tok_indptr  [batch + 1], non-decreasing, from 0
+ *   latent      bf16 [tokens, 576] contiguous, written: the dequantised latents
+ *               (their last 64 channels are the rope keys). The products read
+ *               these rounded values.
+ *   k, v        bf16 [tokens, Hq, 128], written; strides in elements (multiples
+ *               of 8) shared by both
+ *   tokens      rows of latent, k and v; rows past tok_indptr[batch] are left
+ *               as they were
+ * A token whose page id is out of range (PDA_STATUS_PAGE_OOB) or whose request
+ * has more than the plan's max_kv_len tokens (PDA_STATUS_KV_LEN_GT_MAX) reads
+ * as zeros. tok_indptr[batch] > tokens sets PDA_STATUS_TOKENS_GT_CAP and
+ * writes the first `tokens` rows. */
+int pda_mla_expand(const pda_plan_t* plan, const void* k_pages, const int32_t* page_table,
+                   const int32_t* kv_indptr, const int32_t* tok_indptr, const float* k_scale,
+                   const void* w_uk, const void* w_uv, int64_t w_stride_head, void* latent,
+                   void* k, void* v, int64_t kv_stride_token, int64_t kv_stride_head,
+                   int32_t tokens, void* split_scratch, pda_stream_t stream);
+
+/* The plan of a prefill: plain data, as pda_plan_t. */
+typedef struct {
+  uint32_t magic;         /* PDA_PREFILL_MAGIC once planned */
+  uint32_t struct_bytes;  /* sizeof(pda_prefill_plan_t) as compiled */
+  int32_t num_qo_heads, batch, max_kv_len, num_sms, device;
+  int32_t rows, tokens;   /* capacities: rows of q, tokens of k / v */
+  int32_t tiles;          /* bound on the 256-row tiles of all requests */
+  int32_t splits;         /* bound on the key chunks of a tile; 1: not split */
+  int32_t chunk_tokens;   /* keys per chunk, a multiple of 128 */
+  int32_t wait_limit_us;
+  int32_t reserved[3];
+  int64_t scratch_bytes;
+} pda_prefill_plan_t;
+
+#define PDA_PREFILL_MAGIC 0x50444631u /* "PDF1" */
+
+/* Plan prefills of up to `rows` query rows and `tokens` keys in all, for the
+ * heads, batch, max_kv_len and device of `plan` (an MLA plan); both >= 1. Host-only.
+ * Writes *out_plan and, when non-NULL, *scratch_bytes (>= 256): device bytes
+ * that the caller allocates as for pda_plan (256-byte aligned, zeroed once);
+ * pda_get_status reads and pda_reset_status clears its status word. */
+int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t tokens,
+                     pda_prefill_plan_t* out_plan, size_t* scratch_bytes);
+
+/* Expanded latent attention of ragged requests: request b has the query rows
+ * [qo_indptr[b], qo_indptr[b + 1]), any number of them, and the keys
+ * [tok_indptr[b], tok_indptr[b + 1]); with R rows and L keys, row i sits at
+ * p_i = L - R + i and sees, when causal, the keys j <= p_i, and with window[b]
+ * = W > 0 also only j >= p_i - W + 1; when not causal (window must be NULL) all
+ * L keys. s_j = sm_scale (q_nope . k_j + q_rope . k_rope_j), out = sum_j
+ * softmax(s)_j v_j (bf16), lse = ln sum_j exp(s_j) (fp32 or NULL). A row that
+ * sees no key (not causal, L = 0) gets out = 0 and lse = -inf.
+ *   q       bf16 [rows, Hq, 192], strides in elements (multiples of 8)
+ *   k, v    bf16 [tokens, Hq, 128], strides in elements shared by both
+ *   k_rope  bf16 [tokens, 64], k_rope_stride elements apart (latent + 512, 576)
+ *   out     bf16 [rows, Hq, 128] contiguous; lse fp32 [rows, Hq]
+ * Keys and values of a request must be finite for its own rows to be; other
+ * requests' and unused rows may hold anything. A request is left unwritten,
+ * and its bit set, when its rows are negative (PDA_STATUS_ROWS_GT_MAX), when
+ * it is causal with L < R (PDA_STATUS_KV_LEN_LT_ROWS), has L above the plan's
+ * max_kv_len (PDA_STATUS_KV_LEN_GT_MAX), or ends past `rows`
+ * (PDA_STATUS_ROWS_GT_CAP) or `tokens` (PDA_STATUS_TOKENS_GT_CAP). The weights
+ * meet the values in bf16; their sum stays fp32. */
+int pda_mla_prefill(const pda_prefill_plan_t* plan, const void* q, int64_t q_stride_row,
+                    int64_t q_stride_head, const void* k, const void* v, int64_t kv_stride_token,
+                    int64_t kv_stride_head, const void* k_rope, int64_t k_rope_stride,
+                    const int32_t* qo_indptr, const int32_t* tok_indptr, const int32_t* window,
+                    int32_t causal, float sm_scale, void* out, float* lse, void* scratch,
+                    pda_stream_t stream);
 
 /* Copy the device status word of `split_scratch` to *host_bits. Synchronises
  * `stream`. split_scratch = NULL reads the status of pda_decode_static's

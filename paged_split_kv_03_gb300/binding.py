@@ -31,12 +31,18 @@ PDA_STATUS_PAGE_OOB = 0x8
 PDA_STATUS_ROWS_GT_CAP = 0x10
 PDA_STATUS_WAIT_TIMEOUT = 0x20
 PDA_STATUS_SMEM_MISALIGNED = 0x40
+PDA_STATUS_TABLE_INVALID = 0x80
+PDA_STATUS_NO_PAGES = 0x100
+PDA_STATUS_TABLE_FULL = 0x200
+PDA_STATUS_TOKENS_GT_CAP = 0x400
 PDA_PLAN_MAGIC = 0x50444131
+PDA_PREFILL_MAGIC = 0x50444631
 PDA_INJECT_WITHHOLD_KV = 0x1
 
 # every entry point include/pda.h declares
 EXPORTED = ("pda_plan", "pda_decode", "pda_decode_stages", "pda_decode_static", "pda_append_kv",
-            "pda_get_status", "pda_reset_status", "pda_strerror", "pda_version",
+            "pda_build_tables", "pda_append_slots", "pda_mla_absorb", "pda_mla_project",
+            "pda_mla_expand", "pda_prefill_plan", "pda_mla_prefill", "pda_get_status", "pda_reset_status", "pda_strerror", "pda_version",
             "pda_struct_sizes")
 
 _i32, _i64, _u32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_void_p
@@ -68,6 +74,22 @@ class PdaPlan(ctypes.Structure):
                 ("tail_from", _i32), ("tail_chunk_pages", _i32), ("head_splits", _i32),
                 ("tail_splits", _i32), ("head_dim_v", _i32), ("device", _i32),
                 ("wait_limit_us", _i32), ("inject", _u32), ("reserved", _i32 * 7)]
+
+
+class PdaTables(ctypes.Structure):
+    _fields_ = [("cached_len", _vp), ("new_len", _vp), ("request", _vp), ("block_table", _vp),
+                ("table_stride", _i64), ("free_pages", _vp), ("free_count", _vp),
+                ("free_left", _vp), ("kv_len", _vp), ("kv_indptr", _vp), ("page_table", _vp),
+                ("qo_indptr", _vp), ("tok_indptr", _vp), ("slot_map", _vp), ("positions", _vp),
+                ("table_rows", _i32), ("table_cols", _i32), ("page_table_cap", _i32),
+                ("rows_cap", _i32)]
+
+
+class PdaPrefillPlan(ctypes.Structure):
+    _fields_ = [("magic", _u32), ("struct_bytes", _u32), ("num_qo_heads", _i32), ("batch", _i32),
+                ("max_kv_len", _i32), ("num_sms", _i32), ("device", _i32), ("rows", _i32),
+                ("tokens", _i32), ("tiles", _i32), ("splits", _i32), ("chunk_tokens", _i32),
+                ("wait_limit_us", _i32), ("reserved", _i32 * 3), ("scratch_bytes", _i64)]
 
 
 class PdaError(RuntimeError):
@@ -105,6 +127,28 @@ def load_library(path: Optional[str] = None):
     lib.pda_append_kv.argtypes = [ctypes.POINTER(PdaPlan), _vp, _vp, _vp, _vp, _vp, _vp, _i32,
                                   _vp, _vp, _vp, _vp, _vp, _vp]
     lib.pda_append_kv.restype = ctypes.c_int
+    lib.pda_build_tables.argtypes = [ctypes.POINTER(PdaPlan), ctypes.POINTER(PdaTables), _vp, _vp]
+    lib.pda_build_tables.restype = ctypes.c_int
+    lib.pda_append_slots.argtypes = [ctypes.POINTER(PdaPlan), _vp, _i64, _vp, _i64, _vp, _i32, _vp,
+                                     _vp, _vp, _vp, _vp, _vp, _vp]
+    lib.pda_append_slots.restype = ctypes.c_int
+    lib.pda_mla_absorb.argtypes = [ctypes.POINTER(PdaPlan), _vp, _i64, _i64, _vp, _i64,
+                                   ctypes.c_float, _vp, _i32, _vp, _vp, _vp]
+    lib.pda_mla_absorb.restype = ctypes.c_int
+    lib.pda_mla_project.argtypes = [ctypes.POINTER(PdaPlan), _vp, _vp, _i64, _vp, _i32, _vp, _vp,
+                                    _vp]
+    lib.pda_mla_project.restype = ctypes.c_int
+    lib.pda_mla_expand.argtypes = [ctypes.POINTER(PdaPlan), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                   _vp, _vp, _vp, _i64, _i64, _i32, _vp, _vp]
+    lib.pda_mla_expand.restype = ctypes.c_int
+    lib.pda_prefill_plan.argtypes = [ctypes.POINTER(PdaPlan), _i32, _i32,
+                                     ctypes.POINTER(PdaPrefillPlan),
+                                     ctypes.POINTER(ctypes.c_size_t)]
+    lib.pda_prefill_plan.restype = ctypes.c_int
+    lib.pda_mla_prefill.argtypes = [ctypes.POINTER(PdaPrefillPlan), _vp, _i64, _i64, _vp, _vp, _i64,
+                                    _i64, _vp, _i64, _vp, _vp, _vp, _i32, ctypes.c_float, _vp, _vp,
+                                    _vp, _vp]
+    lib.pda_mla_prefill.restype = ctypes.c_int
     lib.pda_get_status.argtypes = [ctypes.POINTER(PdaPlan), _vp, ctypes.POINTER(_u32), _vp]
     lib.pda_get_status.restype = ctypes.c_int
     lib.pda_reset_status.argtypes = [ctypes.POINTER(PdaPlan), _vp, _vp]
@@ -210,6 +254,189 @@ def pda_append_kv(plan: PdaPlan, k_new, v_new, page_table, kv_indptr, kv_len, qo
     return rc
 
 
+_DTYPES: dict = {}
+
+
+def _shape(where: str, **tensors) -> None:
+    """The sizes, types and strides that a call with raw pointers assumes and the library
+    cannot see: name=(tensor, dtype names, shape[, n]), None in a shape for any size, the
+    last n dimensions contiguous (default: all)."""
+    for name, (t, dtype, shape, *inner) in tensors.items():
+        if t is None:
+            continue
+        if dtype not in _DTYPES:
+            import torch
+            _DTYPES[dtype] = tuple(getattr(torch, d) for d in dtype.split())
+        if t.dtype not in _DTYPES[dtype]:
+            raise ValueError(f"{where}: {name} is {t.dtype}, not {dtype}")
+        if not t.is_cuda:
+            raise ValueError(f"{where}: {name} is not on a CUDA device")
+        got = t.shape
+        if len(got) != len(shape) or any(s is not None and s != n for s, n in zip(shape, got)):
+            raise ValueError(f"{where}: {name} has shape {tuple(got)}, not {shape}")
+        want, strides, n = 1, t.stride(), len(shape)
+        for d in range(n - 1, n - 1 - (inner[0] if inner else n), -1):
+            if strides[d] != want and got[d] > 1:
+                raise ValueError(f"{where}: {name} is not contiguous in dimension {d}")
+            want *= got[d]
+
+
+def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, free_pages,
+                     free_count, free_left, kv_len, kv_indptr, page_table, qo_indptr, tok_indptr,
+                     slot_map, positions, split_scratch, stream=None, check: bool = True) -> int:
+    """Block tables and slot maps of one step from the request lengths, on the GPU (see
+    include/pda.h). ``block_table`` is [rows, cols] int32, ``slot_map`` int64, the others int32;
+    ``request``, ``tok_indptr``, ``slot_map`` and ``positions`` may be None."""
+    n = plan.batch
+    _shape("pda_build_tables", cached_len=(cached_len, "int32", (n,)),
+           new_len=(new_len, "int32", (n,)), request=(request, "int32", (n,)),
+           block_table=(block_table, "int32", (None, None), 1),
+           free_pages=(free_pages, "int32", (None,)), free_count=(free_count, "int32", (1,)),
+           free_left=(free_left, "int32", (1,)), kv_len=(kv_len, "int32", (n,)),
+           kv_indptr=(kv_indptr, "int32", (n + 1,)), page_table=(page_table, "int32", (None,)),
+           qo_indptr=(qo_indptr, "int32", (n + 1,)), tok_indptr=(tok_indptr, "int32", (n + 1,)),
+           slot_map=(slot_map, "int64", (None,)), positions=(positions, "int32", (None,)))
+    rows = min(x.shape[0] for x in (slot_map, positions) if x is not None) \
+        if slot_map is not None or positions is not None else 0x7fffffff
+    t = PdaTables(_ptr(cached_len), _ptr(new_len), _ptr(request), _ptr(block_table),
+                  block_table.stride(0), _ptr(free_pages), _ptr(free_count), _ptr(free_left),
+                  _ptr(kv_len), _ptr(kv_indptr), _ptr(page_table), _ptr(qo_indptr),
+                  _ptr(tok_indptr), _ptr(slot_map), _ptr(positions), block_table.shape[0],
+                  block_table.shape[1], page_table.shape[0], rows)
+    rc = load_library().pda_build_tables(ctypes.byref(plan), ctypes.byref(t), _ptr(split_scratch),
+                                         _stream(stream))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, "pda_build_tables")
+    return rc
+
+
+def pda_append_slots(plan: PdaPlan, k_new, v_new, slot_map, num_rows, k_pages, v_pages, k_scale,
+                     v_scale, split_scratch, stream=None, check: bool = True) -> int:
+    """Append rows (bf16 [rows, Hkv, D], any row stride) through a slot map (int64 [rows]);
+    ``num_rows``: an int32 device tensor bounding the rows, or None."""
+    rows = slot_map.shape[0]
+    new = (rows, plan.num_kv_heads, plan.head_dim)
+    _shape("pda_append_slots", k_new=(k_new, "bfloat16", new, 2), v_new=(v_new, "bfloat16", new, 2),
+           slot_map=(slot_map, "int64", (rows,)))
+    rc = load_library().pda_append_slots(
+        ctypes.byref(plan), _ptr(k_new), _row_stride(k_new), _ptr(v_new),
+        0 if v_new is None else _row_stride(v_new), _ptr(slot_map), rows, _ptr(num_rows),
+        _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(split_scratch),
+        _stream(stream))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, "pda_append_slots")
+    return rc
+
+
+def _row_stride(x) -> int:
+    """Elements between rows; a lone row's stride has no meaning in torch."""
+    n = 1
+    for s in x.shape[1:]:
+        n *= s
+    return x.stride(0) if x.shape[0] > 1 else n
+
+
+def _head_strides(x):
+    """(row, head) strides in elements of [rows, heads, channels]."""
+    head = x.stride(1) if x.shape[1] > 1 else x.shape[2]
+    return (x.stride(0) if x.shape[0] > 1 else x.shape[1] * head), head
+
+
+def pda_mla_absorb(plan: PdaPlan, q, w_uk, q_scale: float, q_lat, num_rows, split_scratch,
+                   stream=None, check: bool = True) -> int:
+    """The query absorbed into the latent space: q bf16 [rows, Hq, 192], w_uk bf16
+    [Hq, 128, 512] (any head stride), q_lat [rows, Hq, 576] bf16 or E4M3 codes."""
+    rows, h = q.shape[0], plan.num_qo_heads
+    _shape("pda_mla_absorb", q=(q, "bfloat16", (rows, h, 192), 1),
+           w_uk=(w_uk, "bfloat16", (h, 128, 512), 2),
+           q_lat=(q_lat, "bfloat16" if plan.q_dtype == PDA_BF16 else "float8_e4m3fn uint8",
+                  (rows, h, 576)))
+    row, head = _head_strides(q)
+    rc = load_library().pda_mla_absorb(
+        ctypes.byref(plan), _ptr(q), row, head, _ptr(w_uk), _row_stride(w_uk), float(q_scale),
+        _ptr(q_lat), rows, _ptr(num_rows), _ptr(split_scratch), _stream(stream))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, "pda_mla_absorb")
+    return rc
+
+
+def pda_mla_project(plan: PdaPlan, o_lat, w_uv, out, num_rows, split_scratch, stream=None,
+                    check: bool = True) -> int:
+    """The decode's latent output projected: o_lat bf16 [rows, Hq, 512], w_uv bf16
+    [Hq, 128, 512] (any head stride), out bf16 [rows, Hq, 128]."""
+    rows, h = o_lat.shape[0], plan.num_qo_heads
+    _shape("pda_mla_project", o_lat=(o_lat, "bfloat16", (rows, h, 512)),
+           w_uv=(w_uv, "bfloat16", (h, 128, 512), 2), out=(out, "bfloat16", (rows, h, 128)))
+    rc = load_library().pda_mla_project(
+        ctypes.byref(plan), _ptr(o_lat), _ptr(w_uv), _row_stride(w_uv), _ptr(out), rows,
+        _ptr(num_rows), _ptr(split_scratch), _stream(stream))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, "pda_mla_project")
+    return rc
+
+
+def _same_strides(where: str, k, v):
+    if k.shape[0] > 1 and k.stride(0) != v.stride(0) or k.shape[1] > 1 and k.stride(1) != v.stride(1):
+        raise ValueError(f"{where}: k and v differ in their strides")
+    return _head_strides(k)
+
+
+def pda_mla_expand(plan: PdaPlan, k_pages, page_table, kv_indptr, tok_indptr, k_scale, w_uk, w_uv,
+                   latent, k, v, split_scratch, stream=None, check: bool = True) -> int:
+    """Keys and values of cached tokens: latent bf16 [tokens, 576], k and v bf16
+    [tokens, Hq, 128] (strided alike) are written; w_uk and w_uv bf16 [Hq, 128, 512]."""
+    tokens, h, n = latent.shape[0], plan.num_qo_heads, plan.batch + 1
+    _shape("pda_mla_expand", w_uk=(w_uk, "bfloat16", (h, 128, 512), 2),
+           w_uv=(w_uv, "bfloat16", (h, 128, 512), 2), latent=(latent, "bfloat16", (tokens, 576)),
+           k=(k, "bfloat16", (tokens, h, 128), 1), v=(v, "bfloat16", (tokens, h, 128), 1),
+           kv_indptr=(kv_indptr, "int32", (n,)), tok_indptr=(tok_indptr, "int32", (n,)),
+           page_table=(page_table, "int32", (None,)))
+    if _row_stride(w_uk) != _row_stride(w_uv):
+        raise ValueError("pda_mla_expand: w_uk and w_uv differ in their head strides")
+    tok, head = _same_strides("pda_mla_expand", k, v)
+    rc = load_library().pda_mla_expand(
+        ctypes.byref(plan), _ptr(k_pages), _ptr(page_table), _ptr(kv_indptr), _ptr(tok_indptr),
+        _ptr(k_scale), _ptr(w_uk), _ptr(w_uv), _row_stride(w_uk), _ptr(latent), _ptr(k), _ptr(v),
+        tok, head, tokens, _ptr(split_scratch), _stream(stream))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, "pda_mla_expand")
+    return rc
+
+
+def pda_prefill_plan(plan: PdaPlan, rows: int, tokens: int, check: bool = True):
+    """-> (PdaPrefillPlan, scratch_bytes, rc)."""
+    pre = PdaPrefillPlan()
+    nbytes = ctypes.c_size_t(0)
+    rc = load_library().pda_prefill_plan(ctypes.byref(plan), int(rows), int(tokens),
+                                         ctypes.byref(pre), ctypes.byref(nbytes))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, "pda_prefill_plan")
+    return pre, int(nbytes.value), rc
+
+
+def pda_mla_prefill(pre: PdaPrefillPlan, q, k, v, k_rope, qo_indptr, tok_indptr, window,
+                    causal: bool, sm_scale: float, out, lse, scratch, stream=None,
+                    check: bool = True) -> int:
+    """Expanded latent attention of ragged requests: q bf16 [rows, Hq, 192], k and v bf16
+    [tokens, Hq, 128] (strided alike), k_rope bf16 [tokens, 64], out bf16 [rows, Hq, 128],
+    lse fp32 [rows, Hq] or None; rows and tokens are the plan's."""
+    rows, tokens, h, n = pre.rows, pre.tokens, pre.num_qo_heads, pre.batch
+    _shape("pda_mla_prefill", q=(q, "bfloat16", (rows, h, 192), 1),
+           k=(k, "bfloat16", (tokens, h, 128), 1), v=(v, "bfloat16", (tokens, h, 128), 1),
+           k_rope=(k_rope, "bfloat16", (tokens, 64), 1), qo_indptr=(qo_indptr, "int32", (n + 1,)),
+           tok_indptr=(tok_indptr, "int32", (n + 1,)), window=(window, "int32", (n,)),
+           out=(out, "bfloat16", (rows, h, 128)), lse=(lse, "float32", (rows, h)))
+    tok, head = _same_strides("pda_mla_prefill", k, v)
+    row, qhead = _head_strides(q)
+    rc = load_library().pda_mla_prefill(
+        ctypes.byref(pre), _ptr(q), row, qhead, _ptr(k), _ptr(v), tok, head, _ptr(k_rope),
+        _row_stride(k_rope), _ptr(qo_indptr), _ptr(tok_indptr), _ptr(window), int(bool(causal)),
+        float(sm_scale), _ptr(out), _ptr(lse), _ptr(scratch), _stream(stream))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, "pda_mla_prefill")
+    return rc
+
+
 def pda_get_status(plan: PdaPlan, split_scratch, stream=None) -> int:
     """Device status bits; ``split_scratch=None`` reads those of the
     built-in array that pda_decode_static uses."""
@@ -296,3 +523,25 @@ class Decoder:
 
     def reset_status(self, stream=None) -> None:
         pda_reset_status(self.plan, self.scratch, stream)
+
+
+class Prefill:
+    """A prefill plan plus its scratch (allocated once with torch), for up to ``rows`` query
+    rows and ``tokens`` keys of the MLA plan's requests; ``run`` enqueues one pda_mla_prefill."""
+
+    def __init__(self, plan: PdaPlan, rows: int, tokens: int, device="cuda"):
+        import torch
+        self.decode_plan = plan
+        self.plan, self.scratch_bytes, _ = pda_prefill_plan(plan, rows, tokens)
+        self.scratch = torch.zeros(self.scratch_bytes, dtype=torch.uint8, device=device)
+
+    def run(self, q, k, v, k_rope, qo_indptr, tok_indptr, sm_scale, out, lse, window=None,
+            causal=True, stream=None):
+        return pda_mla_prefill(self.plan, q, k, v, k_rope, qo_indptr, tok_indptr, window, causal,
+                               sm_scale, out, lse, self.scratch, stream)
+
+    def status(self, stream=None) -> int:
+        return pda_get_status(self.decode_plan, self.scratch, stream)
+
+    def reset_status(self, stream=None) -> None:
+        pda_reset_status(self.decode_plan, self.scratch, stream)

@@ -216,6 +216,178 @@ AppendFn pick_mode(int mode) {
   }
 }
 
+// ------------------------------------------------- append through a slot map
+//
+// Any number of rows, each with its cache slot given (a prefill). The row's D
+// values are D / 8 chunks of 16 bytes, one per lane and load, so a vector of
+// head_dim 128 takes half a warp and every load and store is a full 16-byte
+// (codes: 8-byte) access; K and V of a vector are loaded together before
+// either is converted. Bound: HBM (rows x Hkv x D x (2 + elt) bytes of K and
+// V).
+
+struct SlotArgs {
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  int64_t k_stride, v_stride;  // elements between rows
+  const int64_t* slot_map;
+  const int32_t* num_rows;
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  float* k_scale;
+  float* v_scale;
+  uint32_t* status;
+  int64_t sp, st, sh;  // cache strides, elements
+  int64_t num_slots;
+  int rows, hkv, page_shift;
+};
+
+template <int D>
+struct SlotCfg {
+  static constexpr int kChunks = D / 8;                          // of 8 values
+  static constexpr int kLanes = kChunks < 32 ? kChunks : 32;     // lanes per vector
+  static constexpr int kIters = (kChunks + kLanes - 1) / kLanes; // chunks per lane
+  static constexpr int kPerWarp = 32 / kLanes;                   // vectors per warp
+};
+
+__device__ __forceinline__ void unpack8(uint4 w, float* x) {
+  const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x[2 * e] = __uint_as_float(r[e] << 16);
+    x[2 * e + 1] = __uint_as_float(r[e] & 0xFFFF0000u);
+  }
+}
+
+// Eight values over `s` as eight codes.
+template <bool kInt8>
+__device__ __forceinline__ uint2 codes8(const float* x, float s) {
+  uint32_t c[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float y0 = __fdiv_rn(x[2 * e], s), y1 = __fdiv_rn(x[2 * e + 1], s);
+    c[e] = kInt8 ? int8x2(y0, y1) : e4m3x2(y0, y1);
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+
+__device__ __forceinline__ float amax8(const float* x) {
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+  return m;
+}
+
+// One vector into the cache: `w` holds this lane's chunks, `ok` whether the
+// vector is written (every lane runs the shuffles). MODE as in put_row.
+template <int D, int MODE>
+__device__ __forceinline__ void put_slot(const uint4* w, bool ok, uint8_t* pages, int64_t elt_off,
+                                         const float* scale_in, float* scale_out, int sub) {
+  using C = SlotCfg<D>;
+  if constexpr (MODE == 0) {
+#pragma unroll
+    for (int k = 0; k < C::kIters; ++k)
+      if (ok && sub + 32 * k < C::kChunks)
+        *reinterpret_cast<uint4*>(pages + elt_off * 2 + (sub + 32 * k) * 16) = w[k];
+  } else if constexpr (MODE == 5) {
+    // a record: chunks 0..63 are the nope (16 lanes a 128-channel block), 64..71 the rope
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float x[8];
+      unpack8(w[k], x);
+      float amax = amax8(x);
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      // a zero block: scale 0 (no weight in the decode's sums) and zero codes
+      const float sc = amax > 0.f ? __fdiv_rn(amax, 448.f) : 0.f;
+      if (!ok) continue;
+      if ((sub & 15) == 0) scale_out[k * 2 + (sub >> 4)] = sc;
+      *reinterpret_cast<uint2*>(pages + elt_off + (sub + 32 * k) * 8) =
+          codes8<false>(x, amax > 0.f ? sc : 1.f);
+    }
+    if (ok && sub < 8) *reinterpret_cast<uint4*>(pages + elt_off + 512 + sub * 16) = w[2];
+  } else {
+    constexpr bool kInt8 = MODE >= 3;
+    float s;
+    if constexpr (MODE == 1 || MODE == 3) {
+      s = __ldg(scale_in);
+    } else {
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < C::kIters; ++k) {
+        float x[8];
+        unpack8(w[k], x);
+        if (sub + 32 * k < C::kChunks) amax = fmaxf(amax, amax8(x));
+      }
+#pragma unroll
+      for (int off = C::kLanes / 2; off; off >>= 1)
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      s = amax > 0.f ? __fdiv_rn(amax, kInt8 ? 127.f : 448.f) : 1.f;
+      if (ok && sub == 0) *scale_out = s;
+    }
+#pragma unroll
+    for (int k = 0; k < C::kIters; ++k) {
+      if (!ok || sub + 32 * k >= C::kChunks) continue;
+      float x[8];
+      unpack8(w[k], x);
+      *reinterpret_cast<uint2*>(pages + elt_off + (sub + 32 * k) * 8) = codes8<kInt8>(x, s);
+    }
+  }
+}
+
+template <int D, int MODE, bool kTwo>
+__global__ void __launch_bounds__(256) append_slots(const __grid_constant__ SlotArgs a) {
+  using C = SlotCfg<D>;
+  const int lane = threadIdx.x & 31, sub = lane % C::kLanes;
+  const int64_t item =
+      ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * C::kPerWarp + lane / C::kLanes;
+  const int64_t i = item / a.hkv;
+  const int h = static_cast<int>(item % a.hkv);
+  int rows = a.rows;
+  if (a.num_rows) rows = min(rows, __ldg(a.num_rows));
+  bool ok = i < rows;
+  const int64_t slot = ok ? __ldg(a.slot_map + i) : -1;
+  if (ok && (slot < -1 || slot >= a.num_slots) && sub == 0) atomicOr(a.status, PDA_STATUS_PAGE_OOB);
+  ok = slot >= 0 && slot < a.num_slots;
+  if (!__any_sync(0xffffffffu, ok)) return;
+  uint4 wk[C::kIters], wv[C::kIters];
+#pragma unroll
+  for (int k = 0; k < C::kIters; ++k) {
+    wk[k] = wv[k] = make_uint4(0, 0, 0, 0);
+    if (ok && sub + 32 * k < C::kChunks) {
+      wk[k] = __ldg(reinterpret_cast<const uint4*>(a.k_new + i * a.k_stride + h * D) + sub + 32 * k);
+      if constexpr (kTwo)
+        wv[k] = __ldg(reinterpret_cast<const uint4*>(a.v_new + i * a.v_stride + h * D) + sub + 32 * k);
+    }
+  }
+  const int64_t page = slot >> a.page_shift;
+  const int64_t off = page * a.sp + (slot - (page << a.page_shift)) * a.st + h * a.sh;
+  const int64_t sidx = (slot * a.hkv + h) * (MODE == 5 ? 4 : 1);
+  constexpr bool kOwnScale = MODE == 2 || MODE == 4 || MODE == 5;
+  put_slot<D, MODE>(wk, ok, a.k_pages, off, a.k_scale, a.k_scale + (kOwnScale ? sidx : 0), sub);
+  if constexpr (kTwo)
+    put_slot<D, MODE>(wv, ok, a.v_pages, off, a.v_scale, a.v_scale + (kOwnScale ? sidx : 0), sub);
+}
+
+using SlotFn = void (*)(SlotArgs);
+
+template <int D>
+SlotFn pick_slot_mode(int mode) {
+  if constexpr (D == 576) {  // the MLA latent: one vector, no V of its own
+    return mode == 0 ? append_slots<576, 0, false>
+                     : mode == 5 ? append_slots<576, 5, false>
+                     : mode == 1 ? append_slots<576, 1, false> : append_slots<576, 2, false>;
+  } else {
+    if (mode == 0) return append_slots<D, 0, true>;
+    if (mode == 1) return append_slots<D, 1, true>;
+    if constexpr (D <= 256) {  // no plan has int8 above 256
+      if (mode == 3) return append_slots<D, 3, true>;
+      if (mode == 4) return append_slots<D, 4, true>;
+    }
+    return append_slots<D, 2, true>;
+  }
+}
+
 }  // namespace
 }  // namespace pda
 
@@ -283,6 +455,70 @@ extern "C" int pda_append_kv(const pda_plan_t* plan, const void* k_new, const vo
                                 : pda::pick_mode<576>(mode);
   const int64_t warps = (int64_t)plan->batch * max_q_len * plan->num_kv_heads;
   const int64_t blocks = (warps + 7) / 8;
+  if (blocks > 0x7fffffffLL) return PDA_ERR_INVALID;
+  fn<<<static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+  return PDA_OK;
+}
+
+extern "C" int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64_t k_stride,
+                                const void* v_new, int64_t v_stride, const int64_t* slot_map,
+                                int32_t rows, const int32_t* num_rows, void* k_pages,
+                                void* v_pages, float* k_scale, float* v_scale,
+                                void* split_scratch, pda_stream_t stream) {
+  if (!plan) return PDA_ERR_NULL;
+  if (plan->magic != PDA_PLAN_MAGIC) return PDA_ERR_PLAN;
+  const int D = plan->head_dim;
+  const bool mla = D == 576;  // one latent per token: the v arguments are not used
+  const bool rec = plan->scale_mode == PDA_SCALE_MLA_BLOCK;
+  const bool codes = plan->kv_dtype != PDA_BF16;
+  if (rows < 0) return PDA_ERR_INVALID;
+  if (rows == 0) return PDA_OK;
+  if (!k_new || !slot_map || !k_pages || (!mla && (!v_new || !v_pages))) return PDA_ERR_NULL;
+  if (codes && (!k_scale || (!mla && !v_scale))) return PDA_ERR_NULL;
+  if (!split_scratch || reinterpret_cast<uintptr_t>(split_scratch) % 256) return PDA_ERR_SCRATCH;
+  const int64_t width = static_cast<int64_t>(plan->num_kv_heads) * D;
+  if (k_stride < width || (!mla && v_stride < width)) return PDA_ERR_INVALID;
+  auto a16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  auto a4 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; };
+  if (!a16(k_new) || !a16(k_pages) || k_stride % 8 || reinterpret_cast<uintptr_t>(slot_map) % 8 ||
+      !a4(num_rows))
+    return PDA_ERR_ALIGNMENT;
+  if (!mla && (!a16(v_new) || !a16(v_pages) || v_stride % 8)) return PDA_ERR_ALIGNMENT;
+  if (codes && (rec ? !a16(k_scale) : !a4(k_scale) || (!mla && !a4(v_scale))))
+    return PDA_ERR_ALIGNMENT;
+
+  pda::SlotArgs a;
+  std::memset(&a, 0, sizeof a);
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.slot_map = slot_map;
+  a.num_rows = num_rows;
+  a.k_pages = static_cast<uint8_t*>(k_pages);
+  a.v_pages = static_cast<uint8_t*>(v_pages);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.status = static_cast<uint32_t*>(split_scratch);
+  a.sp = plan->kv_stride_page;
+  a.st = plan->kv_stride_token;
+  a.sh = plan->kv_stride_head;
+  a.num_slots = static_cast<int64_t>(plan->num_pages) * plan->page_size;
+  a.rows = rows;
+  a.hkv = plan->num_kv_heads;
+  while ((1 << a.page_shift) < plan->page_size) ++a.page_shift;
+  const int mode = rec ? 5
+                 : !codes ? 0
+                          : (plan->kv_dtype == PDA_INT8 ? 2 : 0) +
+                                (plan->scale_mode == PDA_SCALE_TENSOR ? 1 : 2);
+  pda::SlotFn fn = D == 64 ? pda::pick_slot_mode<64>(mode)
+                   : D == 128 ? pda::pick_slot_mode<128>(mode)
+                   : D == 256 ? pda::pick_slot_mode<256>(mode)
+                   : D == 512 ? pda::pick_slot_mode<512>(mode)
+                              : pda::pick_slot_mode<576>(mode);
+  const int per_cta = 8 * (D == 64 ? 4 : D == 128 ? 2 : 1);
+  const int64_t blocks = (static_cast<int64_t>(rows) * a.hkv + per_cta - 1) / per_cta;
   if (blocks > 0x7fffffffLL) return PDA_ERR_INVALID;
   fn<<<static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
