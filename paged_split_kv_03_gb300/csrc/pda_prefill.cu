@@ -1,14 +1,47 @@
-// pda_prefill.cu -- expanded latent attention of ragged requests (prefill).
-
+// pda_prefill.cu -- expanded latent attention of ragged requests (prefill), on
+// the 5th-generation tensor cores.
+//
+// Mathematics: for 256 query rows of one request and head, over tiles of 128
+// keys: S = Q K^T with K = [k | k_rope] (192 channels, the rope part shared by
+// all heads and read from the latents), an online softmax in log2 units,
+// O += P V. The running maximum is lazy: a row moves it only when a logit
+// passes it by more than 8, so P <= 2^8, and the sum l of the fp32 weights and
+// O are rescaled then; O / l is exact in it. P is rounded to bf16, V's type (2^-9
+// relative on average, random), while l sums the unrounded weights.
+//
+// Bound: the tensor cores (640 flops per row, key and head). A tile of 128 rows
+// x 128 keys takes 12 + 8 MMAs, 1280 cycles; its softmax is 16384 exponentials
+// plus about four instructions each, which two warpgroups hide behind each
+// other's MMAs. So a CTA holds two 128-row tiles (96 KB of Q, shared K and V:
+// half the L2 reads of one tile), whose S take turns:
+//   PV(0, j)  QK(0, j+1)  PV(1, j)  QK(1, j+1)  ...
+// S, P (over S, bf16, the MMA's A operand) and O of both fill the 512 TMEM
+// columns, so neither P nor O touches shared memory.
+//
+// Roles: warps 0-3 and 4-7 are the softmax of tile 0 and 1 (a thread per row);
+// warp 8 loads (TMA), warp 9 issues the MMAs, warp 10 clears V rows behind the
+// last key (0 x NaN), warp 11 finds the work: a CTA takes (head, tile, chunk)
+// items in steps of the grid, and the warps hand items on through a ring, so
+// that the loads and MMAs of the next item start while this one's rows are
+// written. K and V pass through a ring of 16 KB units: three of K (128 keys x 64
+// channels), two of V (64 keys x 128 channels) a tile.
+//
+// Few rows: where heads x tiles are fewer than the SMs, a tile's keys are cut
+// into chunks (pda_prefill_plan), whose normalised partial outputs and log2 sums
+// a second kernel joins.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
 
 #include "pda.h"
 #include "pda_internal.h"
+#include "pda_ptx.cuh"
 
 namespace pda {
 namespace {
@@ -16,76 +49,676 @@ namespace {
 constexpr int kNope = 128, kRope = 64, kQDim = kNope + kRope, kDv = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMInit = -1.0e30f;  // before any key: finite, so that ex2(-inf - m) = 0
+constexpr float kTh = 8.0f;         // lazy rescale threshold, log2 units
+
+constexpr int kRowsTile = 128;                // rows of one softmax warpgroup
+constexpr int kRowsItem = 2 * kRowsTile;      // rows of an item
+constexpr int kKeys = 128;                    // keys of a tile
+constexpr int kUnit = 16384;                  // bytes of a ring unit
+constexpr int kRing = 8;                      // units
+constexpr int kUnitsK = 3, kUnitsV = 2, kUnitsTile = kUnitsK + kUnitsV;
+constexpr int kQBytes = 2 * 3 * kUnit;        // two tiles of three 64-channel blocks
+constexpr int kItems = 3;                     // slots of the item ring
+constexpr int kThreads = 384;
+constexpr int kCoarse = 256;                  // prefix entries, 32 requests each
+constexpr int kMaxBatch = 32 * kCoarse;
+constexpr int kReaders = 11;                  // arrivals that free an item slot
+constexpr int kTmemCols = 512;
 
 struct PrefillArgs {
-  const __nv_bfloat16* q;
-  int64_t q_row, q_head;
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
-  int64_t kv_tok, kv_head;
-  const __nv_bfloat16* k_rope;
-  int64_t rope_tok;
   const int32_t* qo_indptr;
   const int32_t* tok_indptr;
   const int32_t* window;
   __nv_bfloat16* out;
   float* lse;
+  float* part_o;    // [splits][rows][heads][128] fp32, normalised
+  float* part_lse;  // [splits][rows][heads] fp32, log2 units
   uint32_t* status;
+  uint64_t wait_limit_ns;
   float sm_scale;
-  int heads, batch, max_kv_len, rows, tokens, causal;
+  int heads, batch, max_kv_len, rows, tokens, causal, splits, chunk_tiles;
 };
 
-// One warp per (row, head): six query channels a lane, an online softmax over
-// the visible keys, four value channels a lane.
-__global__ void __launch_bounds__(256) prefill(const __grid_constant__ PrefillArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t r = item / a.heads;
-  const int h = static_cast<int>(item % a.heads);
-  if (r >= a.rows) return;
-  int lo = 0, hi = a.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (a.qo_indptr[mid] <= r) lo = mid;
-    else hi = mid - 1;
+// One request's geometry, and whether it takes part (else its status bits).
+struct Request {
+  int q0, rows, k0, keys, win;
+  uint32_t bad;
+};
+__device__ __forceinline__ Request request_of(const PrefillArgs& a, int b) {
+  Request r;
+  r.q0 = __ldg(a.qo_indptr + b);
+  r.k0 = __ldg(a.tok_indptr + b);
+  const int64_t q1 = __ldg(a.qo_indptr + b + 1), k1 = __ldg(a.tok_indptr + b + 1);
+  r.win = a.window ? __ldg(a.window + b) : 0;
+  r.bad = 0u;
+  if (q1 < r.q0 || r.q0 < 0) r.bad |= PDA_STATUS_ROWS_GT_MAX;
+  if (q1 > a.rows) r.bad |= PDA_STATUS_ROWS_GT_CAP;
+  if (k1 < r.k0 || r.k0 < 0 || k1 > a.tokens) r.bad |= PDA_STATUS_TOKENS_GT_CAP;
+  if (k1 - r.k0 > a.max_kv_len) r.bad |= PDA_STATUS_KV_LEN_GT_MAX;
+  if (a.causal && k1 - r.k0 < q1 - r.q0) r.bad |= PDA_STATUS_KV_LEN_LT_ROWS;
+  if (q1 == r.q0) r.bad = 0u;  // no rows: nothing to refuse
+  r.rows = r.bad ? 0 : static_cast<int>(q1 - r.q0);
+  r.keys = r.bad || q1 == r.q0 ? 0 : static_cast<int>(k1 - r.k0);
+  return r;
+}
+
+// Key tiles [lo, hi) that rows [i, i + n) of a request see (n > 0).
+__device__ __forceinline__ void key_tiles(const PrefillArgs& a, const Request& r, int i, int n,
+                                          int& lo, int& hi) {
+  int first = 0, end = r.keys;
+  if (a.causal) {
+    const int p = r.keys - r.rows + i;  // position of row i
+    end = p + n;
+    if (r.win > 0 && p >= r.win) first = p - r.win + 1;
   }
-  const int b = lo, q0 = a.qo_indptr[b], R = a.qo_indptr[b + 1] - q0;
-  const int k0 = a.tok_indptr[b], L = a.tok_indptr[b + 1] - k0;
-  const int i = static_cast<int>(r) - q0;
-  if (i < 0 || i >= R) return;
-  uint32_t bad = 0;
-  if (q0 + R > a.rows) bad |= PDA_STATUS_ROWS_GT_CAP;
-  if (L < 0 || k0 + L > a.tokens) bad |= PDA_STATUS_TOKENS_GT_CAP;
-  if (L > a.max_kv_len) bad |= PDA_STATUS_KV_LEN_GT_MAX;
-  if (a.causal && L < R) bad |= PDA_STATUS_KV_LEN_LT_ROWS;
-  if (bad) {
-    if (lane == 0) atomicOr(a.status, bad);
+  lo = first / kKeys;
+  hi = (end + kKeys - 1) / kKeys;
+}
+
+// One item: 256 rows of a request and head, over the key tiles of one chunk.
+struct Item {
+  int head;       // -1: no more items
+  int row0;       // first row in q / out
+  int rows;       // 1..256
+  int pos;        // position of the first row
+  int keys;       // L of the request
+  int k0;         // its first token in k / v
+  int win;
+  int lo[2], hi[2];  // key tiles of each 128-row tile in this chunk (empty: lo = hi)
+  int split;      // chunk, or -1: the only one, out is final
+};
+
+struct Shared {
+  uint64_t q_full[2], q_empty[2], full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2],
+      o_free[2], item_full[kItems], item_empty[kItems], v_tail, drain;
+  uint32_t tmem;
+  int abort_flag;
+  Item items[kItems];
+  int coarse[kCoarse];
+};
+constexpr int kSmem = kQBytes + kRing * kUnit + static_cast<int>(sizeof(Shared));
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+// The item ring from a reader's side.
+struct ItemReader {
+  Shared* sh;
+  uint32_t n = 0;
+  __device__ explicit ItemReader(Shared* s) : sh(s) {}
+  // One thread: the next item, or false after the last one (or an abort).
+  __device__ bool next_one(Item& it, const PrefillArgs& a) {
+    const uint32_t slot = n % kItems;
+    if (!bar_wait(sh->item_full + slot, (n / kItems) & 1u, &sh->abort_flag, a)) return false;
+    it = sh->items[slot];
+    bar_arrive(sh->item_empty + slot);
+    ++n;
+    return it.head >= 0;
+  }
+  // A whole warp (one arrival); warp-uniform.
+  __device__ bool next_warp(Item& it, const PrefillArgs& a) {
+    const uint32_t slot = n % kItems;
+    const bool ok = bar_wait(sh->item_full + slot, (n / kItems) & 1u, &sh->abort_flag, a);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    it = sh->items[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(sh->item_empty + slot);
+    ++n;
+    return it.head >= 0;
+  }
+};
+
+// ------------------------------------------------------------------- loads
+__device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring,
+                          const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tr,
+                          const CUtensorMap* tv) {
+  volatile int* abort_flag = &sh->abort_flag;
+  ItemReader reader(sh);
+  Item it;
+  uint32_t u = 0, tails = 0, nq[2] = {0, 0};
+  bool alive = true;
+  auto slot_for = [&](uint32_t x) {
+    return bar_wait(sh->empty + x % kRing, ((x / kRing) & 1u) ^ 1u, abort_flag, a);
+  };
+  while (alive && reader.next_one(it, a)) {
+    const int lo = min(it.lo[0], it.lo[1]), hi = max(it.hi[0], it.hi[1]);
+    const int tail = it.keys % kKeys ? it.keys / kKeys : -1;
+    auto load_q = [&](int g) {
+      if (it.lo[g] >= it.hi[g]) return;
+      if (nq[g] > 0) alive = bar_wait(sh->q_empty + g, (nq[g] - 1) & 1u, abort_flag, a);
+      if (!alive) return;
+      bar_expect_tx(sh->q_full + g, 3 * kUnit);
+      for (int c = 0; c < 3; ++c)
+        tma_load3(su32(q_s + (g * 3 + c) * kUnit), tq, c * 64, it.head, it.row0 + g * kRowsTile,
+                  sh->q_full + g);
+      ++nq[g];
+    };
+    load_q(0);
+    for (int j = lo; j < hi && alive; ++j) {
+      const int tok = it.k0 + j * kKeys;
+      for (int c = 0; c < kUnitsK && alive; ++c, ++u) {
+        if (!(alive = slot_for(u))) break;
+        const uint32_t dst = su32(ring + (u % kRing) * kUnit);
+        uint64_t* bar = sh->full + u % kRing;
+        bar_expect_tx(bar, kUnit);
+        if (c < 2) tma_load3(dst, tk, c * 64, it.head, tok, bar);
+        else tma_load3(dst, tr, 0, 0, tok, bar);
+      }
+      if (j == lo && alive) load_q(1);
+      for (int c = 0; c < kUnitsV && alive; ++c, ++u) {
+        if (!(alive = slot_for(u))) break;
+        const uint32_t dst = su32(ring + (u % kRing) * kUnit);
+        // the last tile's V lands for the clearing warp, which passes it on
+        uint64_t* bar = j == tail ? &sh->v_tail : sh->full + u % kRing;
+        if (j != tail) {
+          bar_expect_tx(bar, kUnit);
+        } else if (c == 0) {
+          bar_expect_tx(bar, kUnitsV * kUnit);
+          ++tails;
+        }
+        tma_load3(dst, tv, 0, it.head, tok + c * 64, bar);
+        tma_load3(dst + kUnit / 2, tv, 64, it.head, tok + c * 64, bar);
+      }
+    }
+  }
+  // every box issued must have landed before the CTA can exit
+  if (!alive || *abort_flag) {
+    if (tails) bar_drain(&sh->v_tail, (tails - 1) & 1u);
+    for (uint32_t x = u > kRing ? u - kRing : 0u; x < u; ++x)
+      bar_drain(sh->full + x % kRing, (x / kRing) & 1u);
+    for (int g = 0; g < 2; ++g)
+      if (nq[g]) bar_drain(sh->q_full + g, (nq[g] - 1) & 1u);
+  }
+}
+
+// -------------------------------------------------------------------- MMAs
+__device__ void mma_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring,
+                         uint32_t tmem) {
+  volatile int* abort_flag = &sh->abort_flag;
+  const uint32_t id_s = idesc(1u, 0, kKeys), id_o = idesc(1u, 0, kDv, 1u);
+  const uint32_t q_addr = su32(q_s), r_addr = su32(ring);
+  ItemReader reader(sh);
+  Item it;
+  uint32_t base = 0;                 // first ring unit of the item
+  uint32_t nq[2] = {0, 0};           // items a tile took part in
+  uint32_t np[2] = {0, 0};           // key tiles its softmax has seen
+  bool alive = true;
+  while (alive && reader.next_one(it, a)) {
+    const int lo = min(it.lo[0], it.lo[1]), hi = max(it.hi[0], it.hi[1]);
+    auto sees = [&](int g, int j) { return j >= it.lo[g] && j < it.hi[g]; };
+    auto unit_ready = [&](uint32_t x) {
+      return bar_wait(sh->full + x % kRing, (x / kRing) & 1u, abort_flag, a);
+    };
+    auto free_units = [&](uint32_t x, int n) {
+      for (int c = 0; c < n; ++c) mma_commit(sh->empty + (x + c) % kRing);
+    };
+    auto qk = [&](int g, int j) {
+      if (!alive || !sees(g, j)) return;
+      if (j == it.lo[g]) alive = bar_wait(sh->q_full + g, nq[g] & 1u, abort_flag, a);
+      const uint32_t x = base + kUnitsTile * static_cast<uint32_t>(j - lo);
+      for (int c = 0; c < kUnitsK && alive; ++c) {
+        if (!(alive = unit_ready(x + c))) return;
+        fence_after();
+        const uint32_t qa = q_addr + (g * 3 + c) * kUnit, ka = r_addr + (x + c) % kRing * kUnit;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma<false>(tmem + g * kKeys, sdesc(qa + kk * 32, 16, 1024), sdesc(ka + kk * 32, 16, 1024),
+                     id_s, (c | kk) != 0);
+      }
+      if (!alive) return;
+      mma_commit(sh->s_full + g);
+      if (j + 1 == it.hi[g]) mma_commit(sh->q_empty + g);
+    };
+    auto pv = [&](int g, int j) {
+      if (!alive || !sees(g, j)) return;
+      if (!(alive = bar_wait(sh->p_full + g, np[g] & 1u, abort_flag, a))) return;
+      ++np[g];
+      if (j == it.lo[g]) {
+        // the previous item's output has been read
+        if (nq[g] > 0 && !(alive = bar_wait(sh->o_free + g, (nq[g] - 1) & 1u, abort_flag, a))) return;
+        ++nq[g];
+      }
+      const uint32_t x = base + kUnitsTile * static_cast<uint32_t>(j - lo) + kUnitsK;
+      for (int c = 0; c < kUnitsV; ++c) {
+        if (!(alive = unit_ready(x + c))) return;
+        fence_after();
+        const uint32_t va = r_addr + (x + c) % kRing * kUnit;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts(tmem + 2 * kKeys + g * kDv, tmem + g * kKeys + (c * 4 + kk) * 8,
+                 sdesc(va + kk * 2048, kUnit / 2, 1024), id_o, j != it.lo[g] || (c | kk) != 0);
+      }
+      mma_commit(sh->o_done + g);
+    };
+    if (lo < hi) {
+      qk(0, lo);
+      qk(1, lo);
+      if (alive) free_units(base, kUnitsK);
+    }
+    for (int j = lo; j < hi && alive; ++j) {
+      const uint32_t x = base + kUnitsTile * static_cast<uint32_t>(j - lo);
+      pv(0, j);
+      if (j + 1 < hi) qk(0, j + 1);
+      pv(1, j);
+      if (alive) free_units(x + kUnitsK, kUnitsV);
+      if (j + 1 < hi) {
+        qk(1, j + 1);
+        if (alive) free_units(x + kUnitsTile, kUnitsK);
+      }
+    }
+    base += kUnitsTile * static_cast<uint32_t>(max(0, hi - lo));
+  }
+  // nothing issued may still run when TMEM is released
+  mma_commit(&sh->drain);
+  bar_drain(&sh->drain, 0);
+}
+
+// ------------------------------------------------- V rows behind the last key
+__device__ void clear_role(const PrefillArgs& a, Shared* sh, uint8_t* ring) {
+  const int lane = threadIdx.x & 31;
+  ItemReader reader(sh);
+  Item it;
+  uint32_t base = 0, tails = 0;
+  while (reader.next_warp(it, a)) {
+    const int lo = min(it.lo[0], it.lo[1]), hi = max(it.hi[0], it.hi[1]);
+    const int tail = it.keys % kKeys ? it.keys / kKeys : -1;
+    if (tail >= lo && tail < hi) {
+      const bool ok = bar_wait(&sh->v_tail, tails & 1u, &sh->abort_flag, a);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      ++tails;
+      const uint32_t x = base + kUnitsTile * static_cast<uint32_t>(tail - lo) + kUnitsK;
+      for (int r = it.keys % kKeys; r < kKeys; r += 2) {
+        // two rows x 16 pieces of 16 bytes (two 64-channel atoms) a step
+        const int row = r + (lane >> 4), piece = lane & 15;
+        if (row < kKeys)
+          *reinterpret_cast<uint4*>(ring + (x + (row >> 6)) % kRing * kUnit +
+                                    (piece >> 3) * (kUnit / 2) + (row & 63) * 128 + (piece & 7) * 16) =
+              make_uint4(0, 0, 0, 0);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        for (int c = 0; c < kUnitsV; ++c) bar_arrive(sh->full + (x + c) % kRing);
+    }
+    base += kUnitsTile * static_cast<uint32_t>(max(0, hi - lo));
+  }
+}
+
+// --------------------------------------------------------------- the work list
+__device__ void work_role(const PrefillArgs& a, Shared* sh) {
+  const int lane = threadIdx.x & 31;
+  // tiles in front of every 32 requests, and in all
+  int64_t total = 0;
+  uint32_t bits = 0u;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    int n = 0;
+    if (b0 + lane < a.batch) {
+      const Request r = request_of(a, b0 + lane);
+      bits |= r.bad;
+      n = (r.rows + kRowsItem - 1) / kRowsItem;
+    }
+    if (lane == 0) sh->coarse[b0 >> 5] = static_cast<int>(total);
+    total += __reduce_add_sync(0xffffffffu, n);
+  }
+  __syncwarp();
+  if (blockIdx.x == 0) {
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0 && bits) atomicOr(a.status, bits);
+  }
+  const int64_t items = total * a.heads * a.splits;
+  uint32_t n = 0;
+  // Chunks of a tile are neighbours, then a head's tiles from the last one
+  // (the most keys) to the first, so that concurrent CTAs share K and V in L2.
+  for (int64_t x = blockIdx.x;; x += gridDim.x) {
+    Item it;
+    it.head = -1;
+    if (x < items) {
+      const int split = static_cast<int>(x % a.splits);
+      const int64_t y = x / a.splits;
+      const int t = static_cast<int>(total - 1 - y % total);
+      it.head = static_cast<int>(y / total);
+      int c = 0, top = (a.batch + 31) / 32 - 1;
+      while (c < top) {
+        const int mid = (c + top + 1) >> 1;
+        if (sh->coarse[mid] <= t) c = mid;
+        else top = mid - 1;
+      }
+      const int b = 32 * c + lane;
+      Request r = {};
+      if (b < a.batch) r = request_of(a, b);
+      const int mine = (r.rows + kRowsItem - 1) / kRowsItem;
+      int upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y2 = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y2;
+      }
+      const int want = t - sh->coarse[c];
+      const int src = __ffs(__ballot_sync(0xffffffffu, upto > want)) - 1;
+      const int i = (want - __shfl_sync(0xffffffffu, upto - mine, src)) * kRowsItem;
+      r.q0 = __shfl_sync(0xffffffffu, r.q0, src);
+      r.rows = __shfl_sync(0xffffffffu, r.rows, src);
+      r.k0 = __shfl_sync(0xffffffffu, r.k0, src);
+      r.keys = __shfl_sync(0xffffffffu, r.keys, src);
+      r.win = __shfl_sync(0xffffffffu, r.win, src);
+      it.row0 = r.q0 + i;
+      it.rows = min(kRowsItem, r.rows - i);
+      it.pos = r.keys - r.rows + i;
+      it.keys = r.keys;
+      it.k0 = r.k0;
+      it.win = a.causal ? r.win : 0;
+      int lo, hi;
+      key_tiles(a, r, i, it.rows, lo, hi);
+      const int chunks = (hi - lo + a.chunk_tiles - 1) / a.chunk_tiles;
+      if (split >= max(1, chunks)) continue;  // no such chunk of this tile
+      it.split = chunks > 1 ? split : -1;
+      const int from = lo + split * a.chunk_tiles, to = min(hi, from + a.chunk_tiles);
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        it.lo[g] = it.hi[g] = g ? it.lo[0] : from;
+        const int rows = min(kRowsTile, it.rows - g * kRowsTile);
+        if (rows <= 0) continue;
+        int l, h;
+        key_tiles(a, r, i + g * kRowsTile, rows, l, h);
+        l = max(l, from);
+        h = min(h, to);
+        if (l < h) {
+          it.lo[g] = l;
+          it.hi[g] = h;
+        }
+      }
+      // an empty tile stands at the other's first key tile
+      if (it.lo[0] >= it.hi[0]) it.lo[0] = it.hi[0] = it.lo[1];
+      if (it.lo[1] >= it.hi[1]) it.lo[1] = it.hi[1] = it.lo[0];
+    }
+    const uint32_t slot = n % kItems;
+    bool ok = true;
+    if (n >= kItems)
+      ok = bar_wait(sh->item_empty + slot, ((n / kItems) - 1) & 1u, &sh->abort_flag, a);
+    if (!__all_sync(0xffffffffu, ok)) return;
+    if (lane == 0) {
+      sh->items[slot] = it;
+      bar_arrive(sh->item_full + slot);
+    }
+    __syncwarp();
+    ++n;
+    if (it.head < 0) return;
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+__device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, int g) {
+  volatile int* abort_flag = &sh->abort_flag;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t t_s = tmem + lanes + g * kKeys, t_o = tmem + lanes + 2 * kKeys + g * kDv;
+  // logits in log2 units: s * scale, with the sign (or zero) applied to s first
+  const float sign = a.sm_scale > 0.f ? 1.f : a.sm_scale < 0.f ? -1.f : 0.f;
+  const float scale = sign != 0.f ? fabsf(a.sm_scale) * kLog2e : 1.f;
+  ItemReader reader(sh);
+  Item it;
+  uint32_t n = 0;  // key tiles seen
+  while (reader.next_warp(it, a)) {
+    const int row = g * kRowsTile + quad * 32 + lane;
+    const int tile_rows = min(kRowsTile, it.rows - g * kRowsTile);
+    if (tile_rows <= 0) continue;
+    const int lo = g ? it.lo[1] : it.lo[0], hi = g ? it.hi[1] : it.hi[0];
+    const int p = it.pos + row;
+    const int last_key = a.causal ? min(p, it.keys - 1) : it.keys - 1;
+    const int first_key = it.win > 0 ? p - it.win + 1 : 0;
+    // the tile's rows all see the keys [all_lo, all_hi]
+    const int all_hi = a.causal ? it.pos + g * kRowsTile : it.keys - 1;
+    const int all_lo = it.win > 0 ? it.pos + g * kRowsTile + tile_rows - it.win : 0;
+    float m = kMInit, l = 0.f;
+    for (int j = lo; j < hi; ++j, ++n) {
+      bool ok = bar_wait(sh->s_full + g, n & 1u, abort_flag, a);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      fence_after();
+      uint32_t s[kKeys];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
+      tmem_wait_ld<kKeys>(s);
+      if (sign != 1.f) {
+#pragma unroll
+        for (int e = 0; e < kKeys; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * sign);
+      }
+      const int k0 = j * kKeys;
+      if (k0 + kKeys - 1 > all_hi || k0 < all_lo) {
+#pragma unroll
+        for (int e = 0; e < kKeys; ++e)
+          if (k0 + e > last_key || k0 + e < first_key) s[e] = 0xff800000u;
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
+#pragma unroll
+      for (int e = 4; e < kKeys; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+      const float ms = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+      const bool move = ms > m + kTh;
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? ex2(m - ms) : 1.f;
+        if (move) m = ms;
+        l *= f;
+        if (j > lo) {  // O holds something: the MMA in front of this one must be done
+          ok = bar_wait(sh->o_done + g, (n - 1) & 1u, abort_flag, a);
+          if (!__all_sync(0xffffffffu, ok)) return;
+          fence_after();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c * 32, o);
+            tmem_wait_ld<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st32(t_o + c * 32, o);
+          }
+        }
+      }
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t w[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int k = c * 64 + e * 2;
+          const float x0 = ex2(fmaf(__uint_as_float(s[k]), scale, -m));
+          const float x1 = ex2(fmaf(__uint_as_float(s[k + 1]), scale, -m));
+          sum[(e & 1) * 2] += x0;
+          sum[(e & 1) * 2 + 1] += x1;
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(x1), "f"(x0));
+        }
+        tmem_st32(t_s + c * 32, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(sh->p_full + g);
+    }
+    // the rows' outputs: final, or this chunk's partial
+    const bool any = lo < hi;
+    if (any) {
+      const bool ok = bar_wait(sh->o_done + g, (n - 1) & 1u, abort_flag, a);
+      if (!__all_sync(0xffffffffu, ok)) return;
+      fence_after();
+    }
+    const float inv = l > 0.f ? 1.f / l : l;  // no key: 0; NaN stays
+    const int64_t at = static_cast<int64_t>(it.row0 + row) * a.heads + it.head;
+    const bool mine = row - g * kRowsTile < tile_rows;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      __syncwarp();
+      if (any) {
+        tmem_ld32(t_o + c * 32, o);
+        tmem_wait_ld<32>(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0u;
+      }
+      if (!mine) continue;
+      if (it.split < 0) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + at * kDv + c * 32);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __nv_bfloat162 r =
+                __floats2bfloat162_rn(__uint_as_float(o[v * 8 + e * 2]) * inv,
+                                      __uint_as_float(o[v * 8 + e * 2 + 1]) * inv);
+            w[e] = *reinterpret_cast<const uint32_t*>(&r);
+          }
+          dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else {
+        float4* dst = reinterpret_cast<float4*>(
+            a.part_o + (static_cast<int64_t>(it.split) * a.rows * a.heads + at) * kDv + c * 32);
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          dst[v] = make_float4(__uint_as_float(o[v * 4]) * inv, __uint_as_float(o[v * 4 + 1]) * inv,
+                               __uint_as_float(o[v * 4 + 2]) * inv,
+                               __uint_as_float(o[v * 4 + 3]) * inv);
+      }
+    }
+    if (any) {
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(sh->o_free + g);
+    }
+    if (mine) {
+      const float log2_sum = l == 0.f ? -INFINITY : m + __log2f(l);
+      if (it.split >= 0)
+        a.part_lse[static_cast<int64_t>(it.split) * a.rows * a.heads + at] = log2_sum;
+      else if (a.lse)
+        a.lse[at] = log2_sum * kLn2;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tq,
+            const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tr,
+            const __grid_constant__ CUtensorMap tv) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* q_s = smem;
+  uint8_t* ring = smem + kQBytes;
+  Shared* sh = reinterpret_cast<Shared*>(smem + kQBytes + kRing * kUnit);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (su32(smem) % 1024u) {  // the swizzled tiles need it
+    if (tid == 0) atomicOr(a.status, PDA_STATUS_SMEM_MISALIGNED);
     return;
   }
-  const int p = L - R + i, W = a.window ? a.window[b] : 0;
-  const int end = a.causal ? p + 1 : L;
-  const int begin = a.causal && W > 0 && p - W + 1 > 0 ? p - W + 1 : 0;
-  float q[6], o[4] = {};
-  const __nv_bfloat16* qp = a.q + r * a.q_row + h * a.q_head;
-  for (int e = 0; e < 6; ++e) q[e] = __bfloat162float(qp[lane + 32 * e]) * a.sm_scale * kLog2e;
-  float m = -INFINITY, l = 0.f;
-  for (int j = begin; j < end; ++j) {
-    const int64_t t = k0 + j;
-    const __nv_bfloat16* kp = a.k + t * a.kv_tok + h * a.kv_head;
-    const __nv_bfloat16* rp = a.k_rope + t * a.rope_tok;
-    float s = 0.f;
-    for (int e = 0; e < 4; ++e) s = fmaf(q[e], __bfloat162float(kp[lane + 32 * e]), s);
-    for (int e = 0; e < 2; ++e) s = fmaf(q[4 + e], __bfloat162float(rp[lane + 32 * e]), s);
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = fmaf(l, f, w);
-    const __nv_bfloat16* vp = a.v + t * a.kv_tok + h * a.kv_head;
-    for (int e = 0; e < 4; ++e) o[e] = fmaf(o[e], f, w * __bfloat162float(vp[lane + 32 * e]));
+  if (tid == 0) {
+    for (int g = 0; g < 2; ++g) {
+      bar_init(sh->q_full + g, 1);
+      bar_init(sh->q_empty + g, 1);
+      bar_init(sh->s_full + g, 1);
+      bar_init(sh->p_full + g, 4);
+      bar_init(sh->o_done + g, 1);
+      bar_init(sh->o_free + g, 4);
+    }
+    for (int s = 0; s < kRing; ++s) {
+      bar_init(sh->full + s, 1);
+      bar_init(sh->empty + s, 1);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      bar_init(sh->item_full + s, 1);
+      bar_init(sh->item_empty + s, kReaders);
+    }
+    bar_init(&sh->v_tail, 1);
+    bar_init(&sh->drain, 1);
+    sh->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  for (int e = 0; e < 4; ++e) a.out[(r * a.heads + h) * kDv + lane + 32 * e] = __float2bfloat16(o[e] * inv);
-  if (a.lse && lane == 0) a.lse[r * a.heads + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     su32(&sh->tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh->tmem;
+  // registers: 208 a thread for the softmax (a row of S), 88 for the others; in
+  // all the 168 x 384 of the launch
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  }
+  if (warp < 8) {
+    softmax_role(a, sh, tmem, warp >> 2);
+  } else if (warp == 8) {
+    if (lane == 0) load_role(a, sh, q_s, ring, &tq, &tk, &tr, &tv);
+  } else if (warp == 9) {
+    if (lane == 0) mma_role(a, sh, q_s, ring, tmem);
+  } else if (warp == 10) {
+    clear_role(a, sh, ring);
+  } else {
+    work_role(a, sh);
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(kTmemCols)
+                 : "memory");
+}
+
+// ------------------------------------------------------------ join of chunks
+//
+// One warp per (row, head): four output channels a lane, the chunks' weights
+// 2^(lse_s - max) summed in order. Bound: reading the partials (L2).
+__global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ PrefillArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t row = item / a.heads;
+  if (row >= a.rows) return;
+  // the last request that starts at or before the row
+  int b = 0, top = a.batch - 1;
+  while (b < top) {
+    const int mid = (b + top + 1) >> 1;
+    if (__ldg(a.qo_indptr + mid) <= row) b = mid;
+    else top = mid - 1;
+  }
+  const Request r = request_of(a, b);
+  const int i = static_cast<int>(row) - r.q0;
+  if (i < 0 || i >= r.rows) return;
+  int lo, hi;
+  const int i0 = i / kRowsItem * kRowsItem;
+  key_tiles(a, r, i0, min(kRowsItem, r.rows - i0), lo, hi);
+  const int chunks = (hi - lo + a.chunk_tiles - 1) / a.chunk_tiles;
+  if (chunks <= 1) return;  // the only chunk wrote the result
+  const int64_t stride = static_cast<int64_t>(a.rows) * a.heads;
+  float m = -INFINITY;
+  for (int s = lane; s < chunks; s += 32) m = fmaxf(m, a.part_lse[s * stride + item]);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  float sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < chunks; ++s) {
+    const float x = a.part_lse[s * stride + item];
+    const float4 v = *reinterpret_cast<const float4*>(a.part_o + (s * stride + item) * kDv + lane * 4);
+    const float w = x == -INFINITY ? 0.f : exp2f(x - m);
+    sum += w;
+    if (w != 0.f) {  // a chunk without a visible key counts for nothing
+      o[0] = fmaf(w, v.x, o[0]);
+      o[1] = fmaf(w, v.y, o[1]);
+      o[2] = fmaf(w, v.z, o[2]);
+      o[3] = fmaf(w, v.w, o[3]);
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : sum;
+  const __nv_bfloat162 w0 = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
+  const __nv_bfloat162 w1 = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
+  *reinterpret_cast<uint2*>(a.out + item * kDv + lane * 4) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&w0), *reinterpret_cast<const uint32_t*>(&w1));
+  if (lane == 0 && a.lse) a.lse[item] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2;
 }
 
 }  // namespace
@@ -96,7 +729,7 @@ extern "C" int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t to
   if (!plan || !out_plan) return PDA_ERR_NULL;
   if (plan->magic != PDA_PLAN_MAGIC) return PDA_ERR_PLAN;
   if (plan->head_dim != pda::kQDim + 384 || plan->num_kv_heads != 1) return PDA_ERR_UNSUPPORTED;
-  if (rows < 1 || tokens < 1) return PDA_ERR_INVALID;
+  if (rows < 1 || tokens < 1 || plan->batch > pda::kMaxBatch) return PDA_ERR_INVALID;
   pda_prefill_plan_t p;
   std::memset(&p, 0, sizeof p);
   p.magic = PDA_PREFILL_MAGIC;
@@ -108,9 +741,31 @@ extern "C" int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t to
   p.device = plan->device;
   p.rows = rows;
   p.tokens = tokens;
-  p.splits = 1;
+  // 256-row tiles of all requests: a request's last one may hold one row
+  const int64_t tiles = std::min<int64_t>(
+      rows, (static_cast<int64_t>(rows) + static_cast<int64_t>(pda::kRowsItem - 1) * plan->batch) /
+                pda::kRowsItem);
+  p.tiles = static_cast<int32_t>(tiles);
+  // Key chunks. With fewer items (heads x tiles) than SMs, as many chunks as
+  // fill them once, of at least four key tiles (a chunk costs its start and
+  // its partials about three tiles' time).
+  const int64_t items = tiles * plan->num_qo_heads;
+  const int64_t max_tiles =
+      (std::min<int64_t>(plan->max_kv_len, tokens) + pda::kKeys - 1) / pda::kKeys;
+  int64_t splits = std::max<int64_t>(1, plan->num_sms / std::max<int64_t>(1, items));
+  splits = std::min<int64_t>(splits, std::max<int64_t>(1, max_tiles / 4));
+  const int64_t chunk = (max_tiles + splits - 1) / splits;
+  splits = (max_tiles + chunk - 1) / chunk;
+  p.splits = static_cast<int32_t>(splits);
+  p.chunk_tokens = static_cast<int32_t>(chunk * pda::kKeys);
   p.wait_limit_us = plan->wait_limit_us;
   p.scratch_bytes = pda::kStatusHeaderBytes;
+  if (splits > 1) {
+    const int64_t cells = splits * rows * plan->num_qo_heads;
+    p.scratch_bytes += (cells * 4 + 255) / 256 * 256 + cells * pda::kDv * 4;
+  }
+  // (chunk_tokens is an int32: max_kv_len within 127 of 2^31 would pass it)
+  if (chunk * pda::kKeys > INT_MAX || items * splits > INT_MAX) return PDA_ERR_INVALID;
   *out_plan = p;
   if (scratch_bytes) *scratch_bytes = static_cast<size_t>(p.scratch_bytes);
   return PDA_OK;
@@ -141,21 +796,17 @@ extern "C" int pda_mla_prefill(const pda_prefill_plan_t* plan, const void* q, in
     return PDA_ERR_ALIGNMENT;
   if (plan->batch == 0) return PDA_OK;
   PrefillArgs a = {};
-  a.q = static_cast<const __nv_bfloat16*>(q);
-  a.q_row = q_stride_row;
-  a.q_head = q_stride_head;
-  a.k = static_cast<const __nv_bfloat16*>(k);
-  a.v = static_cast<const __nv_bfloat16*>(v);
-  a.kv_tok = kv_stride_token;
-  a.kv_head = kv_stride_head;
-  a.k_rope = static_cast<const __nv_bfloat16*>(k_rope);
-  a.rope_tok = k_rope_stride;
   a.qo_indptr = qo_indptr;
   a.tok_indptr = tok_indptr;
   a.window = window;
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = lse;
-  a.status = static_cast<uint32_t*>(scratch);
+  char* base = static_cast<char*>(scratch);
+  const int64_t cells = static_cast<int64_t>(plan->splits) * plan->rows * plan->num_qo_heads;
+  a.status = reinterpret_cast<uint32_t*>(base);
+  a.part_lse = reinterpret_cast<float*>(base + kStatusHeaderBytes);
+  a.part_o = reinterpret_cast<float*>(base + kStatusHeaderBytes + (cells * 4 + 255) / 256 * 256);
+  a.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us) * 1000ull;
   a.sm_scale = sm_scale;
   a.heads = plan->num_qo_heads;
   a.batch = plan->batch;
@@ -163,8 +814,28 @@ extern "C" int pda_mla_prefill(const pda_prefill_plan_t* plan, const void* q, in
   a.rows = plan->rows;
   a.tokens = plan->tokens;
   a.causal = causal ? 1 : 0;
-  const int64_t blocks = (static_cast<int64_t>(plan->rows) * plan->num_qo_heads + 7) / 8;
-  if (blocks > 0x7fffffffLL) return PDA_ERR_INVALID;
-  prefill<<<static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  a.splits = plan->splits;
+  a.chunk_tiles = plan->chunk_tokens / kKeys;
+  CUtensorMap tq, tk, tr, tv;
+  if (!make_map3(&tq, q, kQDim, a.heads, a.rows, q_stride_head, q_stride_row, 64, 1, kRowsTile) ||
+      !make_map3(&tk, k, kNope, a.heads, a.tokens, kv_stride_head, kv_stride_token, 64, 1, kKeys) ||
+      !make_map3(&tr, k_rope, kRope, 1, a.tokens, k_rope_stride, k_rope_stride, 64, 1, kKeys) ||
+      !make_map3(&tv, v, kDv, a.heads, a.tokens, kv_stride_head, kv_stride_token, 64, 1, 64))
+    return PDA_ERR_CUDA;
+  if (cudaFuncSetAttribute(reinterpret_cast<const void*>(prefill),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return PDA_ERR_CUDA;
+  }
+  const int64_t items = static_cast<int64_t>(plan->tiles) * a.heads * a.splits;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(items, plan->num_sms));
+  prefill<<<grid, kThreads, kSmem, s>>>(a, tq, tk, tr, tv);
+  if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+  if (a.splits > 1) {
+    const int64_t warps = static_cast<int64_t>(a.rows) * a.heads;
+    prefill_join<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(a);
+    if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+  }
+  return PDA_OK;
 }

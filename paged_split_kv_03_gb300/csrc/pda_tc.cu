@@ -52,6 +52,7 @@
 #include <mutex>
 
 #include "pda_internal.h"
+#include "pda_ptx.cuh"
 
 namespace pda {
 namespace {
@@ -67,16 +68,6 @@ constexpr float kMInit = -1.0e30f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ------------------------------------------------------------------ helpers
-__device__ __forceinline__ uint32_t su32(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-// Byte offset of byte `b` (< 128) of row `r` inside a 128-byte-swizzled atom
-// (rows of 128 B, 16-byte chunks XORed with the row's low 3 bits).
-__device__ __forceinline__ uint32_t sw128(uint32_t r, uint32_t b) {
-  return r * 128u + ((((b >> 4) ^ r) & 7u) << 4) + (b & 15u);
-}
-
 // NB bytes (a multiple of 4, packed little-endian in `w`) at byte b0 of row
 // r of a 128-byte-swizzled buffer; b0 is a multiple of NB's alignment (16,
 // 8 or 4), so no store crosses a 16-byte chunk.
@@ -95,48 +86,6 @@ __device__ __forceinline__ void store_row(uint8_t* base, int r, int b0, const ui
 #pragma unroll
     for (int q = 0; q < NB / 4; ++q) *reinterpret_cast<uint32_t*>(base + sw128(r, b0 + 4 * q)) = w[q];
   }
-}
-
-// Shared-memory matrix descriptor, 128-byte swizzle (sm_100 family format).
-__device__ __forceinline__ uint64_t sdesc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
-}
-
-// Instruction descriptor: f32 accumulate, A/B format `fmt` (kind::f16: 0 =
-// f16, 1 = bf16; kind::f8f6f4: 0 = E4M3), A (B) MN-major if `a_mn` (`b_mn`),
-// M = 128, N = n.
-__device__ __forceinline__ uint32_t idesc(uint32_t fmt, uint32_t a_mn, uint32_t n,
-                                          uint32_t b_mn = 0) {
-  return (1u << 4) | (fmt << 7) | (fmt << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) |
-         ((128u >> 4) << 24);
-}
-
-template <bool kF8>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
-  if constexpr (kF8)
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;"
-                 " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p; }" ::"r"(d),
-                 "l"(a), "l"(b), "r"(id), "r"(acc));
-  else
-    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0;"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d), "l"(a),
-                 "l"(b), "r"(id), "r"(acc));
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   su32(bar))
-               : "memory");
-}
-__device__ __forceinline__ void fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // Four int8 codes (byte k = element k) -> two f16 pairs, exactly: with
@@ -160,22 +109,6 @@ __device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
   return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
 }
 
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                 "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const float* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
-               "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-               "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-               "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7]))
-               : "memory");
-}
 __device__ __forceinline__ void tmem_ld4(uint32_t taddr, float* v) {
   uint32_t r[4];
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
@@ -200,76 +133,6 @@ __device__ __forceinline__ void tmem_stk(uint32_t taddr, const float* v) {
   if constexpr (K == 8) tmem_st8(taddr, v);
   else tmem_st4(taddr, v);
 }
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(uint64_t* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
-}
-__device__ __forceinline__ void bar_expect_tx(uint64_t* b, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-      : "=r"(done)
-      : "r"(su32(b)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-// try_wait that lets the hardware suspend the thread (up to `ns`) until the
-// phase completes, so waiting warps stop competing for issue slots.
-__device__ __forceinline__ bool bar_try_sleep(uint64_t* b, uint32_t parity, uint32_t ns) {
-  uint32_t done;
-  asm volatile(
-      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, "
-      "0, p; }"
-      : "=r"(done)
-      : "r"(su32(b)), "r"(parity), "r"(ns)
-      : "memory");
-  return done != 0;
-}
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// Bound of a drain (a wait for copies already issued) and the default bound
-// of every other pipeline wait: 2 s of wall time.
-constexpr uint64_t kWaitLimitNs = 2000000000ull;
-// Bounded wait: false if another role aborted or the call's wait limit
-// (a.wait_limit_ns) ran out, which records PDA_STATUS_WAIT_TIMEOUT and
-// aborts the CTA.
-__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile int* abort_flag,
-                                         const DecodeArgs& a) {
-  if (bar_try(b, parity)) return true;
-  const uint64_t t0 = global_ns();
-  for (;;) {
-    if (bar_try_sleep(b, parity, 20000u)) return true;
-    if (*abort_flag) return false;
-    if (global_ns() - t0 > a.wait_limit_ns) {
-      *abort_flag = 1;
-      atomicOr(a.status, PDA_STATUS_WAIT_TIMEOUT);
-      return false;
-    }
-  }
-}
-// Bounded wait that ignores the abort flag (draining work already issued).
-__device__ __forceinline__ void bar_drain(uint64_t* b, uint32_t parity) {
-  const uint64_t t0 = global_ns();
-  while (!bar_try_sleep(b, parity, 20000u) && global_ns() - t0 < kWaitLimitNs) {
-  }
-}
-
 // 4-D tiled TMA load of one box into shared memory, completing on `bar`.
 __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int c0, int c1,
                                          int c2, int c3, uint64_t* bar) {
@@ -278,13 +141,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       "{%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(su32(bar))
       : "memory");
-}
-
-// 2^x by the SFU (ex2.approx.ftz): about 2 ulp, -inf -> 0.
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 
 // Two floats -> two E4M3 codes (RNE, saturating): low byte from `lo`.
@@ -1931,27 +1787,6 @@ struct GetSmem {
   template <int D, int KVT, int QT, int SMODE, int NMAX>
   int get() { return tc_smem<D, KVT, QT, SMODE, NMAX>(); }
 };
-
-// cuTensorMapEncodeTiled, fetched once from the driver through the runtime.
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encoder() {
-  static std::once_flag once;
-  static EncodeFn fn = nullptr;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(p);
-    cudaGetLastError();
-  });
-  return fn;
-}
 
 // Tensor map over the paged cache: dims (c, slot, head, page) or
 // (c, head, slot, page), ordered by stride; one box = one page's (<= 128)
