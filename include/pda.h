@@ -452,7 +452,9 @@ typedef struct {
  * heads, batch, max_kv_len and device of `plan` (an MLA plan); both >= 1. Host-only.
  * Writes *out_plan and, when non-NULL, *scratch_bytes (>= 256): device bytes
  * that the caller allocates as for pda_plan (256-byte aligned, zeroed once);
- * pda_get_status reads and pda_reset_status clears its status word. */
+ * pda_get_status reads and pda_reset_status clears its status word. Calls that
+ * share a scratch must not overlap: the work counters and the partial outputs
+ * are in it. */
 int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t tokens,
                      pda_prefill_plan_t* out_plan, size_t* scratch_bytes);
 

@@ -11,19 +11,17 @@
 //
 // Bound: the tensor cores (640 flops per row, key and head). A tile of 128 rows
 // x 128 keys takes 12 + 8 MMAs, 1280 cycles; its softmax is 16384 exponentials
-// plus about four instructions each, which two warpgroups hide behind each
-// other's MMAs. So a CTA holds two 128-row tiles (96 KB of Q, shared K and V:
+// plus about four instructions each, hidden behind the other tile's MMAs. So a CTA holds two 128-row tiles (96 KB of Q, shared K and V:
 // half the L2 reads of one tile), whose S take turns:
 //   PV(0, j)  QK(0, j+1)  PV(1, j)  QK(1, j+1)  ...
 // S, P (over S, bf16, the MMA's A operand) and O of both fill the 512 TMEM
 // columns, so neither P nor O touches shared memory.
 //
-// Roles: warps 0-3 and 4-7 are the softmax of tile 0 and 1 (a thread per row);
-// warp 8 loads (TMA), warp 9 issues the MMAs, warp 10 clears V rows behind the
-// last key (0 x NaN), warp 11 finds the work: a CTA takes (head, tile, chunk)
-// items in steps of the grid, and the warps hand items on through a ring, so
-// that the loads and MMAs of the next item start while this one's rows are
-// written. K and V pass through a ring of 16 KB units: three of K (128 keys x 64
+// Roles: warps 0-3 and 4-7 are the softmax of tile 0 and 1; warp 8 loads (TMA),
+// warp 9 issues the MMAs, warp 10 clears V rows behind the last key (0 x NaN),
+// warp 11 takes (head, tile, chunk) items off a counter in
+// the scratch; the warps pass items on through a ring, so that the loads and
+// MMAs of the next item start while this one's rows are written. K and V pass through a ring of 16 KB units: three of K (128 keys x 64
 // channels), two of V (64 keys x 128 channels) a tile.
 //
 // Few rows: where heads x tiles are fewer than the SMs, a tile's keys are cut
@@ -60,10 +58,12 @@ constexpr int kRing = 8;                      // units
 constexpr int kUnitsK = 3, kUnitsV = 2, kUnitsTile = kUnitsK + kUnitsV;
 constexpr int kQBytes = 2 * 3 * kUnit;        // two tiles of three 64-channel blocks
 constexpr int kItems = 3;                     // slots of the item ring
-constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;              // a thread per row
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr int kCoarse = 256;                  // prefix entries, 32 requests each
 constexpr int kMaxBatch = 32 * kCoarse;
-constexpr int kReaders = 11;                  // arrivals that free an item slot
+constexpr int kLoadWarp = kSoftmaxWarps, kMmaWarp = kLoadWarp + 1, kClearWarp = kLoadWarp + 2;
+constexpr int kReaders = kSoftmaxWarps + 3;                  // arrivals that free an item slot
 constexpr int kTmemCols = 512;
 
 struct PrefillArgs {
@@ -75,6 +75,8 @@ struct PrefillArgs {
   float* part_o;    // [splits][rows][heads][128] fp32, normalised
   float* part_lse;  // [splits][rows][heads] fp32, log2 units
   uint32_t* status;
+  uint32_t* taken;  // items handed out beyond the first of each CTA; 0 between calls
+  uint32_t* done;   // CTAs that have found no more; 0 between calls
   uint64_t wait_limit_ns;
   float sm_scale;
   int heads, batch, max_kv_len, rows, tokens, causal, splits, chunk_tiles;
@@ -125,13 +127,13 @@ struct Item {
   int keys;       // L of the request
   int k0;         // its first token in k / v
   int win;
-  int lo[2], hi[2];  // key tiles of each 128-row tile in this chunk (empty: lo = hi)
+  int lo0, hi0, lo1, hi1;  // key tiles of both 128-row tiles in this chunk (empty: lo = hi)
   int split;      // chunk, or -1: the only one, out is final
 };
 
 struct Shared {
-  uint64_t q_full[2], q_empty[2], full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2],
-      o_free[2], item_full[kItems], item_empty[kItems], v_tail, drain;
+  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
+      p_full[2], o_done[2], o_free[2], item_full[kItems], item_empty[kItems], v_tail, drain;
   uint32_t tmem;
   int abort_flag;
   Item items[kItems];
@@ -168,144 +170,147 @@ struct ItemReader {
 };
 
 // ------------------------------------------------------------------- loads
+//
+// Ring units in the order K_j (3), V_j (2), K_{j+1}, ...: V_{j+1} and the first
+// unit of K_{j+2} take the places of K_j, its other two those of V_j, so a
+// tile's units share one barrier and tile t (counted over all items) uses
+// barriers t & 1.
 __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring,
                           const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tr,
                           const CUtensorMap* tv) {
   volatile int* abort_flag = &sh->abort_flag;
+  const uint32_t ring_addr = su32(ring);
   ItemReader reader(sh);
-  Item it;
-  uint32_t u = 0, tails = 0, nq[2] = {0, 0};
-  bool alive = true;
-  auto slot_for = [&](uint32_t x) {
-    return bar_wait(sh->empty + x % kRing, ((x / kRing) & 1u) ^ 1u, abort_flag, a);
+  Item it{};
+  uint32_t t = 0, x = 0, tails = 0, nq0 = 0, nq1 = 0;  // key tiles, ring unit, Q tiles
+  bool alive = true, half = false;  // half: K of tile t is loading, V not yet
+  auto dst = [&](uint32_t unit) { return ring_addr + unit % kRing * kUnit; };
+  auto load_q = [&](int g) {
+    if ((g ? it.lo1 >= it.hi1 : it.lo0 >= it.hi0) || !alive) return;
+    uint32_t& nq = g ? nq1 : nq0;
+    if (!(alive = bar_wait(sh->q_empty + g, (nq & 1u) ^ 1u, abort_flag, a))) return;
+    bar_expect_tx(sh->q_full + g, 3 * kUnit);
+    for (int c = 0; c < 3; ++c)
+      tma_load3(su32(q_s + (g * 3 + c) * kUnit), tq, c * 64, it.head, it.row0 + g * kRowsTile,
+                sh->q_full + g);
+    ++nq;
   };
   while (alive && reader.next_one(it, a)) {
-    const int lo = min(it.lo[0], it.lo[1]), hi = max(it.hi[0], it.hi[1]);
+    const int lo = min(it.lo0, it.lo1), hi = max(it.hi0, it.hi1);
     const int tail = it.keys % kKeys ? it.keys / kKeys : -1;
-    auto load_q = [&](int g) {
-      if (it.lo[g] >= it.hi[g]) return;
-      if (nq[g] > 0) alive = bar_wait(sh->q_empty + g, (nq[g] - 1) & 1u, abort_flag, a);
-      if (!alive) return;
-      bar_expect_tx(sh->q_full + g, 3 * kUnit);
-      for (int c = 0; c < 3; ++c)
-        tma_load3(su32(q_s + (g * 3 + c) * kUnit), tq, c * 64, it.head, it.row0 + g * kRowsTile,
-                  sh->q_full + g);
-      ++nq[g];
-    };
     load_q(0);
     for (int j = lo; j < hi && alive; ++j) {
       const int tok = it.k0 + j * kKeys;
-      for (int c = 0; c < kUnitsK && alive; ++c, ++u) {
-        if (!(alive = slot_for(u))) break;
-        const uint32_t dst = su32(ring + (u % kRing) * kUnit);
-        uint64_t* bar = sh->full + u % kRing;
-        bar_expect_tx(bar, kUnit);
-        if (c < 2) tma_load3(dst, tk, c * 64, it.head, tok, bar);
-        else tma_load3(dst, tr, 0, 0, tok, bar);
-      }
-      if (j == lo && alive) load_q(1);
-      for (int c = 0; c < kUnitsV && alive; ++c, ++u) {
-        if (!(alive = slot_for(u))) break;
-        const uint32_t dst = su32(ring + (u % kRing) * kUnit);
-        // the last tile's V lands for the clearing warp, which passes it on
-        uint64_t* bar = j == tail ? &sh->v_tail : sh->full + u % kRing;
-        if (j != tail) {
-          bar_expect_tx(bar, kUnit);
-        } else if (c == 0) {
-          bar_expect_tx(bar, kUnitsV * kUnit);
-          ++tails;
-        }
-        tma_load3(dst, tv, 0, it.head, tok + c * 64, bar);
-        tma_load3(dst + kUnit / 2, tv, 64, it.head, tok + c * 64, bar);
-      }
+      const uint32_t s = t & 1u;
+      // K_t: a place of K_{t-2}, then those of V_{t-2}
+      if (!(alive = bar_wait(sh->k_empty + s, ((t >> 1) & 1u) ^ 1u, abort_flag, a))) break;
+      half = true;
+      bar_expect_tx(sh->k_full + s, kUnitsK * kUnit);
+      tma_load3(dst(x), tk, 0, it.head, tok, sh->k_full + s);
+      if (!(alive = bar_wait(sh->v_empty + s, ((t >> 1) & 1u) ^ 1u, abort_flag, a))) break;
+      tma_load3(dst(x + 1), tk, 64, it.head, tok, sh->k_full + s);
+      tma_load3(dst(x + 2), tr, 0, 0, tok, sh->k_full + s);
+      if (j == lo) load_q(1);
+      // V_t: two places of K_{t-1}
+      if (t > 0 && alive)
+        alive = bar_wait(sh->k_empty + (s ^ 1u), ((t - 1) >> 1) & 1u, abort_flag, a);
+      if (!alive) break;
+      // the last tile's V lands for the clearing warp, which passes it on
+      uint64_t* bar = j == tail ? &sh->v_tail : sh->v_full + s;
+      if (j == tail) ++tails;
+      bar_expect_tx(bar, kUnitsV * kUnit);
+      for (int c = 0; c < kUnitsV; ++c)
+        for (int d = 0; d < 2; ++d)
+          tma_load3(dst(x + kUnitsK + c) + d * (kUnit / 2), tv, d * 64, it.head, tok + c * 64, bar);
+      half = false;
+      ++t;
+      x += kUnitsTile;
     }
   }
   // every box issued must have landed before the CTA can exit
   if (!alive || *abort_flag) {
     if (tails) bar_drain(&sh->v_tail, (tails - 1) & 1u);
-    for (uint32_t x = u > kRing ? u - kRing : 0u; x < u; ++x)
-      bar_drain(sh->full + x % kRing, (x / kRing) & 1u);
-    for (int g = 0; g < 2; ++g)
-      if (nq[g]) bar_drain(sh->q_full + g, (nq[g] - 1) & 1u);
+    for (uint32_t k = t > 1 ? t - 2 : 0u; k < t; ++k) {
+      bar_drain(sh->k_full + (k & 1u), (k >> 1) & 1u);
+      bar_drain(sh->v_full + (k & 1u), (k >> 1) & 1u);
+    }
+    if (half) bar_drain(sh->k_full + (t & 1u), (t >> 1) & 1u);
+    if (nq0) bar_drain(sh->q_full, (nq0 - 1) & 1u);
+    if (nq1) bar_drain(sh->q_full + 1, (nq1 - 1) & 1u);
   }
 }
 
 // -------------------------------------------------------------------- MMAs
-__device__ void mma_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring,
-                         uint32_t tmem) {
+//
+// One thread. Everything it does between MMAs counts: four MMAs wait in the
+// tensor cores' queue, so 256 cycles a half step are hidden and the rest is
+// lost. So it waits once a half step, for P of one tile: a softmax warp that
+// hands over P has seen V of this tile and K of the next one.
+__device__ void mma_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring) {
   volatile int* abort_flag = &sh->abort_flag;
+  constexpr uint32_t tmem = 0;  // all columns are ours: they start at 0
   const uint32_t id_s = idesc(1u, 0, kKeys), id_o = idesc(1u, 0, kDv, 1u);
-  const uint32_t q_addr = su32(q_s), r_addr = su32(ring);
+  // descriptors count in 16 bytes
+  const uint64_t q_desc = sdesc(su32(q_s), 16, 1024), k_desc = sdesc(su32(ring), 16, 1024),
+                 v_desc = sdesc(su32(ring), kUnit / 2, 1024);
   ItemReader reader(sh);
-  Item it;
-  uint32_t base = 0;                 // first ring unit of the item
-  uint32_t nq[2] = {0, 0};           // items a tile took part in
-  uint32_t np[2] = {0, 0};           // key tiles its softmax has seen
+  Item it{};
+  uint32_t t = 0, x = 0;       // key tile (of j) and its first ring unit
+  uint32_t pp = 0u, qp = 0u;   // parities of p_full and of the items, a bit per row tile
   bool alive = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    alive = bar_try(bar, parity & 1u) || bar_wait_slow(bar, parity & 1u, abort_flag, a);
+    return alive;
+  };
   while (alive && reader.next_one(it, a)) {
-    const int lo = min(it.lo[0], it.lo[1]), hi = max(it.hi[0], it.hi[1]);
-    auto sees = [&](int g, int j) { return j >= it.lo[g] && j < it.hi[g]; };
-    auto unit_ready = [&](uint32_t x) {
-      return bar_wait(sh->full + x % kRing, (x / kRing) & 1u, abort_flag, a);
-    };
-    auto free_units = [&](uint32_t x, int n) {
-      for (int c = 0; c < n; ++c) mma_commit(sh->empty + (x + c) % kRing);
-    };
-    auto qk = [&](int g, int j) {
-      if (!alive || !sees(g, j)) return;
-      if (j == it.lo[g]) alive = bar_wait(sh->q_full + g, nq[g] & 1u, abort_flag, a);
-      const uint32_t x = base + kUnitsTile * static_cast<uint32_t>(j - lo);
-      for (int c = 0; c < kUnitsK && alive; ++c) {
-        if (!(alive = unit_ready(x + c))) return;
-        fence_after();
-        const uint32_t qa = q_addr + (g * 3 + c) * kUnit, ka = r_addr + (x + c) % kRing * kUnit;
+    const int lo0 = it.lo0, hi0 = it.hi0, lo1 = it.lo1, hi1 = it.hi1;
+    const int lo = min(lo0, lo1), hi = max(hi0, hi1);
+    if (lo >= hi) continue;
+    if (!wait(sh->k_full + (t & 1u), t >> 1)) break;
+    // step j: P V of tile j, then Q K of tile j + 1, for both row tiles
+    for (int j = lo - 1; j < hi && alive; ++j) {
+      const uint32_t t1 = j < lo ? t : t + 1, x1 = j < lo ? x : x + kUnitsTile;
+      const uint64_t v0 = v_desc + (x + kUnitsK) % kRing * (kUnit / 16);
+      const uint64_t v1 = v_desc + (x + kUnitsK + 1) % kRing * (kUnit / 16);
+      const uint64_t k0 = k_desc + x1 % kRing * (kUnit / 16);
+      const uint64_t k1 = k_desc + (x1 + 1) % kRing * (kUnit / 16);
+      const uint64_t k2 = k_desc + (x1 + 2) % kRing * (kUnit / 16);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma<false>(tmem + g * kKeys, sdesc(qa + kk * 32, 16, 1024), sdesc(ka + kk * 32, 16, 1024),
-                     id_s, (c | kk) != 0);
-      }
-      if (!alive) return;
-      mma_commit(sh->s_full + g);
-      if (j + 1 == it.hi[g]) mma_commit(sh->q_empty + g);
-    };
-    auto pv = [&](int g, int j) {
-      if (!alive || !sees(g, j)) return;
-      if (!(alive = bar_wait(sh->p_full + g, np[g] & 1u, abort_flag, a))) return;
-      ++np[g];
-      if (j == it.lo[g]) {
-        // the previous item's output has been read
-        if (nq[g] > 0 && !(alive = bar_wait(sh->o_free + g, (nq[g] - 1) & 1u, abort_flag, a))) return;
-        ++nq[g];
-      }
-      const uint32_t x = base + kUnitsTile * static_cast<uint32_t>(j - lo) + kUnitsK;
-      for (int c = 0; c < kUnitsV; ++c) {
-        if (!(alive = unit_ready(x + c))) return;
-        fence_after();
-        const uint32_t va = r_addr + (x + c) % kRing * kUnit;
+      for (int g = 0; g < 2; ++g) {
+        const int from = g ? lo1 : lo0, to = g ? hi1 : hi0;
+        if (j >= from && j < to) {
+          if (j == from && !wait(sh->o_free + g, qp >> g)) break;  // the last item's O is read
+          if (!wait(sh->p_full + g, pp >> g)) break;
+          pp ^= 1u << g;
+          fence_after();
+          const uint32_t acc = j != from;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_ts(tmem + 2 * kKeys + g * kDv, tmem + g * kKeys + (c * 4 + kk) * 8,
-                 sdesc(va + kk * 2048, kUnit / 2, 1024), id_o, j != it.lo[g] || (c | kk) != 0);
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + 2 * kKeys + g * kDv, tmem + g * kKeys + kk * 8,
+                   (kk < 4 ? v0 : v1) + (kk & 3) * 128, id_o, kk ? 1u : acc);
+          mma_commit(sh->o_done + g);
+        }
+        if (g == 1 && j >= lo) mma_commit(sh->v_empty + (t & 1u));
+        if (j + 1 >= from && j + 1 < to) {
+          if (j + 1 == from) {
+            if (!wait(sh->q_full + g, qp >> g)) break;
+            // (a tile that sees its first keys late: no P has vouched for these)
+            if (!wait(sh->k_full + (t1 & 1u), t1 >> 1)) break;
+            qp ^= 1u << g;
+            fence_after();
+          }
+#pragma unroll
+          for (int kk = 0; kk < 12; ++kk)
+            mma<false>(tmem + g * kKeys, q_desc + (g * 3 + kk / 4) * (kUnit / 16) + (kk & 3) * 2,
+                       (kk < 4 ? k0 : kk < 8 ? k1 : k2) + (kk & 3) * 2, id_s, kk != 0);
+          mma_commit(sh->s_full + g);
+          if (j + 2 == to) mma_commit(sh->q_empty + g);
+        }
+        if (g == 1 && j + 1 < hi) mma_commit(sh->k_empty + (t1 & 1u));
       }
-      mma_commit(sh->o_done + g);
-    };
-    if (lo < hi) {
-      qk(0, lo);
-      qk(1, lo);
-      if (alive) free_units(base, kUnitsK);
+      t = t1;
+      x = x1;
     }
-    for (int j = lo; j < hi && alive; ++j) {
-      const uint32_t x = base + kUnitsTile * static_cast<uint32_t>(j - lo);
-      pv(0, j);
-      if (j + 1 < hi) qk(0, j + 1);
-      pv(1, j);
-      if (alive) free_units(x + kUnitsK, kUnitsV);
-      if (j + 1 < hi) {
-        qk(1, j + 1);
-        if (alive) free_units(x + kUnitsTile, kUnitsK);
-      }
-    }
-    base += kUnitsTile * static_cast<uint32_t>(max(0, hi - lo));
   }
   // nothing issued may still run when TMEM is released
   mma_commit(&sh->drain);
@@ -316,16 +321,16 @@ __device__ void mma_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t
 __device__ void clear_role(const PrefillArgs& a, Shared* sh, uint8_t* ring) {
   const int lane = threadIdx.x & 31;
   ItemReader reader(sh);
-  Item it;
-  uint32_t base = 0, tails = 0;
+  Item it{};
+  uint32_t t = 0, tails = 0;  // key tiles in front of the item
   while (reader.next_warp(it, a)) {
-    const int lo = min(it.lo[0], it.lo[1]), hi = max(it.hi[0], it.hi[1]);
+    const int lo = min(it.lo0, it.lo1), hi = max(it.hi0, it.hi1);
     const int tail = it.keys % kKeys ? it.keys / kKeys : -1;
     if (tail >= lo && tail < hi) {
       const bool ok = bar_wait(&sh->v_tail, tails & 1u, &sh->abort_flag, a);
       if (!__all_sync(0xffffffffu, ok)) return;
       ++tails;
-      const uint32_t x = base + kUnitsTile * static_cast<uint32_t>(tail - lo) + kUnitsK;
+      const uint32_t tt = t + static_cast<uint32_t>(tail - lo), x = tt * kUnitsTile + kUnitsK;
       for (int r = it.keys % kKeys; r < kKeys; r += 2) {
         // two rows x 16 pieces of 16 bytes (two 64-channel atoms) a step
         const int row = r + (lane >> 4), piece = lane & 15;
@@ -336,10 +341,9 @@ __device__ void clear_role(const PrefillArgs& a, Shared* sh, uint8_t* ring) {
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0)
-        for (int c = 0; c < kUnitsV; ++c) bar_arrive(sh->full + (x + c) % kRing);
+      if (lane == 0) bar_arrive(sh->v_full + (tt & 1u));
     }
-    base += kUnitsTile * static_cast<uint32_t>(max(0, hi - lo));
+    t += static_cast<uint32_t>(max(0, hi - lo));
   }
 }
 
@@ -365,17 +369,30 @@ __device__ void work_role(const PrefillArgs& a, Shared* sh) {
     if (lane == 0 && bits) atomicOr(a.status, bits);
   }
   const int64_t items = total * a.heads * a.splits;
+  // Heads go in groups whose tiles fill the GPU about once, so that their K
+  // and V stay in L2; a group's items from the last tiles (the most keys) to
+  // the first, chunks of a tile side by side. CTAs take items one by one, as
+  // causal tiles differ: in steps of the grid, 4096 x 128 heads took a third
+  // longer.
+  const int64_t group = max(static_cast<int64_t>(1), (gridDim.x + total - 1) / max(total, static_cast<int64_t>(1)));
   uint32_t n = 0;
-  // Chunks of a tile are neighbours, then a head's tiles from the last one
-  // (the most keys) to the first, so that concurrent CTAs share K and V in L2.
-  for (int64_t x = blockIdx.x;; x += gridDim.x) {
+  int64_t x = blockIdx.x;
+  auto take = [&]() {
+    uint32_t v = 0;
+    if (lane == 0) v = atomicAdd(a.taken, 1u);
+    x = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xffffffffu, v, 0);
+  };
+  for (;;) {
     Item it;
     it.head = -1;
     if (x < items) {
       const int split = static_cast<int>(x % a.splits);
       const int64_t y = x / a.splits;
-      const int t = static_cast<int>(total - 1 - y % total);
-      it.head = static_cast<int>(y / total);
+      const int64_t first = y / (group * total) * group;  // the group's first head
+      const int64_t wide = min(group, a.heads - first), z = y - first * total;
+      const int t = static_cast<int>(total - 1 - z / wide);
+      it.head = static_cast<int>(first + z % wide);
+      take();
       int c = 0, top = (a.batch + 31) / 32 - 1;
       while (c < top) {
         const int mid = (c + top + 1) >> 1;
@@ -412,57 +429,66 @@ __device__ void work_role(const PrefillArgs& a, Shared* sh) {
       if (split >= max(1, chunks)) continue;  // no such chunk of this tile
       it.split = chunks > 1 ? split : -1;
       const int from = lo + split * a.chunk_tiles, to = min(hi, from + a.chunk_tiles);
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        it.lo[g] = it.hi[g] = g ? it.lo[0] : from;
+      auto part = [&](int g, int& l, int& h) {
         const int rows = min(kRowsTile, it.rows - g * kRowsTile);
-        if (rows <= 0) continue;
-        int l, h;
-        key_tiles(a, r, i + g * kRowsTile, rows, l, h);
+        l = h = 0;
+        if (rows > 0) key_tiles(a, r, i + g * kRowsTile, rows, l, h);
         l = max(l, from);
         h = min(h, to);
-        if (l < h) {
-          it.lo[g] = l;
-          it.hi[g] = h;
-        }
-      }
+      };
+      part(0, it.lo0, it.hi0);
+      part(1, it.lo1, it.hi1);
       // an empty tile stands at the other's first key tile
-      if (it.lo[0] >= it.hi[0]) it.lo[0] = it.hi[0] = it.lo[1];
-      if (it.lo[1] >= it.hi[1]) it.lo[1] = it.hi[1] = it.lo[0];
+      if (it.lo0 >= it.hi0) it.lo0 = it.hi0 = it.lo1 < it.hi1 ? it.lo1 : from;
+      if (it.lo1 >= it.hi1) it.lo1 = it.hi1 = it.lo0;
     }
     const uint32_t slot = n % kItems;
     bool ok = true;
     if (n >= kItems)
       ok = bar_wait(sh->item_empty + slot, ((n / kItems) - 1) & 1u, &sh->abort_flag, a);
-    if (!__all_sync(0xffffffffu, ok)) return;
+    if (!__all_sync(0xffffffffu, ok)) break;
     if (lane == 0) {
       sh->items[slot] = it;
       bar_arrive(sh->item_full + slot);
     }
     __syncwarp();
     ++n;
-    if (it.head < 0) return;
+    if (it.head < 0) break;
+  }
+  // the last CTA to get here clears the counters for the next call
+  if (lane == 0) {
+    __threadfence();
+    if (atomicInc(a.done, gridDim.x - 1) == gridDim.x - 1) atomicExch(a.taken, 0u);
   }
 }
 
 // ------------------------------------------------------------------ softmax
-__device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, int g) {
+//
+// A thread per row, its 128 logits in registers.
+__device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, int warp) {
   volatile int* abort_flag = &sh->abort_flag;
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31, quad = warp & 3, g = warp >> 2;
+  const int r = quad * 32 + lane;  // row of the tile
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t t_s = tmem + lanes + g * kKeys, t_o = tmem + lanes + 2 * kKeys + g * kDv;
   // logits in log2 units: s * scale, with the sign (or zero) applied to s first
   const float sign = a.sm_scale > 0.f ? 1.f : a.sm_scale < 0.f ? -1.f : 0.f;
   const float scale = sign != 0.f ? fabsf(a.sm_scale) * kLog2e : 1.f;
   ItemReader reader(sh);
-  Item it;
-  uint32_t n = 0;  // key tiles seen
+  Item it{};
+  uint32_t n = 0, t = 0;  // key tiles seen by this row tile; of all items before this one
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = bar_wait(bar, parity & 1u, abort_flag, a);
+    return __all_sync(0xffffffffu, ok);
+  };
   while (reader.next_warp(it, a)) {
-    const int row = g * kRowsTile + quad * 32 + lane;
     const int tile_rows = min(kRowsTile, it.rows - g * kRowsTile);
+    const int lo = g ? it.lo1 : it.lo0, hi = g ? it.hi1 : it.hi0;
+    const int item_lo = min(it.lo0, it.lo1), item_hi = max(it.hi0, it.hi1);
+    const uint32_t t0 = t - static_cast<uint32_t>(item_lo);  // tile j is t0 + j of all
+    t += static_cast<uint32_t>(max(0, item_hi - item_lo));
     if (tile_rows <= 0) continue;
-    const int lo = g ? it.lo[1] : it.lo[0], hi = g ? it.hi[1] : it.hi[0];
-    const int p = it.pos + row;
+    const int row = g * kRowsTile + r, p = it.pos + row;
     const int last_key = a.causal ? min(p, it.keys - 1) : it.keys - 1;
     const int first_key = it.win > 0 ? p - it.win + 1 : 0;
     // the tile's rows all see the keys [all_lo, all_hi]
@@ -470,28 +496,40 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
     const int all_lo = it.win > 0 ? it.pos + g * kRowsTile + tile_rows - it.win : 0;
     float m = kMInit, l = 0.f;
     for (int j = lo; j < hi; ++j, ++n) {
-      bool ok = bar_wait(sh->s_full + g, n & 1u, abort_flag, a);
-      if (!__all_sync(0xffffffffu, ok)) return;
+      if (!wait(sh->s_full + g, n)) return;
       fence_after();
+      const int k0 = j * kKeys;
+      if (k0 + kKeys - 1 > all_hi || k0 < all_lo || sign != 1.f) {
+        // some row does not see the whole tile: mask S where it stands
+#pragma unroll 1
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t s[32];
+          tmem_ld32(t_s + c, s);
+          tmem_wait_ld<32>(s);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float x = __uint_as_float(s[e]) * sign;
+            s[e] = k0 + c + e > last_key || k0 + c + e < first_key ? 0xff800000u
+                                                                   : __float_as_uint(x);
+          }
+          tmem_st32(t_s + c, s);
+        }
+        tmem_wait_st();
+      }
       uint32_t s[kKeys];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(t_s + c * 32, s + c * 32);
+      for (int c = 0; c < kKeys; c += 32) tmem_ld32(t_s + c, s + c);
       tmem_wait_ld<kKeys>(s);
-      if (sign != 1.f) {
-#pragma unroll
-        for (int e = 0; e < kKeys; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * sign);
-      }
-      const int k0 = j * kKeys;
-      if (k0 + kKeys - 1 > all_hi || k0 < all_lo) {
-#pragma unroll
-        for (int e = 0; e < kKeys; ++e)
-          if (k0 + e > last_key || k0 + e < first_key) s[e] = 0xff800000u;
-      }
       float mx[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
 #pragma unroll
-      for (int e = 4; e < kKeys; ++e) mx[e & 3] = fmaxf(mx[e & 3], __uint_as_float(s[e]));
+      for (int e = 4; e < kKeys - 4; e += 8)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mx[c] = max3(mx[c], __uint_as_float(s[e + c]), __uint_as_float(s[e + 4 + c]));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(s[kKeys - 4 + c]));
       const float ms = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
       const bool move = ms > m + kTh;
       if (__any_sync(0xffffffffu, move)) {
@@ -499,36 +537,45 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
         if (move) m = ms;
         l *= f;
         if (j > lo) {  // O holds something: the MMA in front of this one must be done
-          ok = bar_wait(sh->o_done + g, (n - 1) & 1u, abort_flag, a);
-          if (!__all_sync(0xffffffffu, ok)) return;
+          if (!wait(sh->o_done + g, n - 1)) return;
           fence_after();
+#pragma unroll 1
+          for (int c = 0; c < kDv; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(t_o + c, o);
+            tmem_wait_ld<16>(o);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(t_o + c * 32, o);
-            tmem_wait_ld<32>(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st32(t_o + c * 32, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(t_o + c, o);
           }
         }
       }
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      // P over the columns of S, two keys a column
+      const uint64_t scale2 = pack2(scale, scale), m2 = pack2(-m, -m);
+      uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[32];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const int k = c * 64 + e * 2;
-          const float x0 = ex2(fmaf(__uint_as_float(s[k]), scale, -m));
-          const float x1 = ex2(fmaf(__uint_as_float(s[k + 1]), scale, -m));
-          sum[(e & 1) * 2] += x0;
-          sum[(e & 1) * 2 + 1] += x1;
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(x1), "f"(x0));
+        for (int e = 0; e < 16; ++e) {
+          const int k = c * 32 + e * 2;
+          float p0, p1;
+          unpack2(fma2(pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), scale2, m2), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(p1), "f"(p0));
         }
-        tmem_st32(t_s + c * 32, w);
+        tmem_st16(t_s + c * 16, w);
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      float l0, l1;
+      unpack2(add2(sum[0], sum[1]), l0, l1);
+      l += l0 + l1;
+      if (quad == 0) {  // for the MMAs that P starts: V of this tile, K of the next
+        const uint32_t tj = t0 + static_cast<uint32_t>(j);
+        if (!wait(sh->v_full + (tj & 1u), tj >> 1)) return;
+        if (j + 1 < item_hi && !wait(sh->k_full + ((tj + 1) & 1u), (tj + 1) >> 1)) return;
+      }
       tmem_wait_st();
       fence_before();
       __syncwarp();
@@ -536,43 +583,40 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
     }
     // the rows' outputs: final, or this chunk's partial
     const bool any = lo < hi;
-    if (any) {
-      const bool ok = bar_wait(sh->o_done + g, (n - 1) & 1u, abort_flag, a);
-      if (!__all_sync(0xffffffffu, ok)) return;
-      fence_after();
-    }
+    if (any && !wait(sh->o_done + g, n - 1)) return;
+    fence_after();
     const float inv = l > 0.f ? 1.f / l : l;  // no key: 0; NaN stays
     const int64_t at = static_cast<int64_t>(it.row0 + row) * a.heads + it.head;
-    const bool mine = row - g * kRowsTile < tile_rows;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    const bool live = r < tile_rows;
+#pragma unroll 1
+    for (int c = 0; c < kDv; c += 32) {
       uint32_t o[32];
       __syncwarp();
       if (any) {
-        tmem_ld32(t_o + c * 32, o);
+        tmem_ld32(t_o + c, o);
         tmem_wait_ld<32>(o);
       } else {
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
-      if (!mine) continue;
+      if (!live) continue;
       if (it.split < 0) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + at * kDv + c * 32);
+        uint4* dst = reinterpret_cast<uint4*>(a.out + at * kDv + c);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          uint32_t w[4];
+          uint32_t b[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 r =
+            const __nv_bfloat162 h =
                 __floats2bfloat162_rn(__uint_as_float(o[v * 8 + e * 2]) * inv,
                                       __uint_as_float(o[v * 8 + e * 2 + 1]) * inv);
-            w[e] = *reinterpret_cast<const uint32_t*>(&r);
+            b[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[v] = make_uint4(b[0], b[1], b[2], b[3]);
         }
       } else {
         float4* dst = reinterpret_cast<float4*>(
-            a.part_o + (static_cast<int64_t>(it.split) * a.rows * a.heads + at) * kDv + c * 32);
+            a.part_o + (static_cast<int64_t>(it.split) * a.rows * a.heads + at) * kDv + c);
 #pragma unroll
         for (int v = 0; v < 8; ++v)
           dst[v] = make_float4(__uint_as_float(o[v * 4]) * inv, __uint_as_float(o[v * 4 + 1]) * inv,
@@ -580,12 +624,12 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
                                __uint_as_float(o[v * 4 + 3]) * inv);
       }
     }
+    __syncwarp();
     if (any) {
       fence_before();
-      __syncwarp();
       if (lane == 0) bar_arrive(sh->o_free + g);
     }
-    if (mine) {
+    if (live) {
       const float log2_sum = l == 0.f ? -INFINITY : m + __log2f(l);
       if (it.split >= 0)
         a.part_lse[static_cast<int64_t>(it.split) * a.rows * a.heads + at] = log2_sum;
@@ -613,13 +657,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(sh->q_full + g, 1);
       bar_init(sh->q_empty + g, 1);
       bar_init(sh->s_full + g, 1);
-      bar_init(sh->p_full + g, 4);
+      bar_init(sh->p_full + g, kSoftmaxWarps / 2);
       bar_init(sh->o_done + g, 1);
-      bar_init(sh->o_free + g, 4);
-    }
-    for (int s = 0; s < kRing; ++s) {
-      bar_init(sh->full + s, 1);
-      bar_init(sh->empty + s, 1);
+      bar_init(sh->o_free + g, kSoftmaxWarps / 2);
+      bar_init(sh->k_full + g, 1);
+      bar_init(sh->k_empty + g, 1);
+      bar_init(sh->v_full + g, 1);
+      bar_init(sh->v_empty + g, 1);
     }
     for (int s = 0; s < kItems; ++s) {
       bar_init(sh->item_full + s, 1);
@@ -630,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      su32(&sh->tmem)),
                  "r"(kTmemCols)
@@ -642,20 +686,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh->tmem;
-  // registers: 208 a thread for the softmax (a row of S), 88 for the others; in
-  // all the 168 x 384 of the launch
-  if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+  // registers: 200 a thread for the softmax, 96 for the others; together less
+  // than the 168 x 384 of the launch
+  if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
   }
-  if (warp < 8) {
-    softmax_role(a, sh, tmem, warp >> 2);
-  } else if (warp == 8) {
+  if (warp < kSoftmaxWarps) {
+    softmax_role(a, sh, tmem, warp);
+  } else if (warp == kLoadWarp) {
     if (lane == 0) load_role(a, sh, q_s, ring, &tq, &tk, &tr, &tv);
-  } else if (warp == 9) {
-    if (lane == 0) mma_role(a, sh, q_s, ring, tmem);
-  } else if (warp == 10) {
+  } else if (warp == kMmaWarp) {
+    if (elect_one()) mma_role(a, sh, q_s, ring);
+  } else if (warp == kClearWarp) {
     clear_role(a, sh, ring);
   } else {
     work_role(a, sh);
@@ -664,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 9)
+  if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(kTmemCols)
                  : "memory");
@@ -804,6 +848,8 @@ extern "C" int pda_mla_prefill(const pda_prefill_plan_t* plan, const void* q, in
   char* base = static_cast<char*>(scratch);
   const int64_t cells = static_cast<int64_t>(plan->splits) * plan->rows * plan->num_qo_heads;
   a.status = reinterpret_cast<uint32_t*>(base);
+  a.taken = a.status + 16;
+  a.done = a.status + 17;
   a.part_lse = reinterpret_cast<float*>(base + kStatusHeaderBytes);
   a.part_o = reinterpret_cast<float*>(base + kStatusHeaderBytes + (cells * 4 + 255) / 256 * 256);
   a.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us) * 1000ull;
