@@ -132,8 +132,8 @@ struct Item {
 };
 
 struct Shared {
-  uint64_t q_full[2], q_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2],
-      p_full[2], o_done[2], o_free[2], item_full[kItems], item_empty[kItems], v_tail, drain;
+  uint64_t q_full[2], q_empty[2], full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2],
+      o_free[2], item_full[kItems], item_empty[kItems], v_tail, drain;
   uint32_t tmem;
   int abort_flag;
   Item items[kItems];
@@ -171,10 +171,11 @@ struct ItemReader {
 
 // ------------------------------------------------------------------- loads
 //
-// Ring units in the order K_j (3), V_j (2), K_{j+1}, ...: V_{j+1} and the first
-// unit of K_{j+2} take the places of K_j, its other two those of V_j, so a
-// tile's units share one barrier and tile t (counted over all items) uses
-// barriers t & 1.
+// Ring units in the order K_j (3), V_j (2), K_{j+1}, ...: unit x takes the place
+// x % 8, which unit x - 8 leaves as soon as the MMAs of row tile 1 have read it.
+// V_{j+1} and the first unit of K_{j+2} follow K_j, its other two V_j. Counted
+// per unit, a load has 1800 to 3000 cycles at the tensor cores' pace until it is
+// needed; counted per tile the later units of K had 1280, less than TMA takes.
 __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring,
                           const CUtensorMap* tq, const CUtensorMap* tk, const CUtensorMap* tr,
                           const CUtensorMap* tv) {
@@ -182,9 +183,12 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
   const uint32_t ring_addr = su32(ring);
   ItemReader reader(sh);
   Item it{};
-  uint32_t t = 0, x = 0, tails = 0, nq0 = 0, nq1 = 0;  // key tiles, ring unit, Q tiles
-  bool alive = true, half = false;  // half: K of tile t is loading, V not yet
+  uint32_t x = 0, tails = 0, nq0 = 0, nq1 = 0;  // ring unit, ragged last tiles, Q tiles
+  bool alive = true;
   auto dst = [&](uint32_t unit) { return ring_addr + unit % kRing * kUnit; };
+  auto place = [&](uint32_t unit) {
+    return alive = bar_wait(sh->empty + unit % kRing, ((unit / kRing) & 1u) ^ 1u, abort_flag, a);
+  };
   auto load_q = [&](int g) {
     if ((g ? it.lo1 >= it.hi1 : it.lo0 >= it.hi0) || !alive) return;
     uint32_t& nq = g ? nq1 : nq0;
@@ -201,40 +205,32 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
     load_q(0);
     for (int j = lo; j < hi && alive; ++j) {
       const int tok = it.k0 + j * kKeys;
-      const uint32_t s = t & 1u;
-      // K_t: a place of K_{t-2}, then those of V_{t-2}
-      if (!(alive = bar_wait(sh->k_empty + s, ((t >> 1) & 1u) ^ 1u, abort_flag, a))) break;
-      half = true;
-      bar_expect_tx(sh->k_full + s, kUnitsK * kUnit);
-      tma_load3(dst(x), tk, 0, it.head, tok, sh->k_full + s);
-      if (!(alive = bar_wait(sh->v_empty + s, ((t >> 1) & 1u) ^ 1u, abort_flag, a))) break;
-      tma_load3(dst(x + 1), tk, 64, it.head, tok, sh->k_full + s);
-      tma_load3(dst(x + 2), tr, 0, 0, tok, sh->k_full + s);
+      for (int c = 0; c < kUnitsK && place(x); ++c, ++x) {
+        uint64_t* bar = sh->full + x % kRing;
+        bar_expect_tx(bar, kUnit);
+        if (c < 2) tma_load3(dst(x), tk, c * 64, it.head, tok, bar);
+        else tma_load3(dst(x), tr, 0, 0, tok, bar);
+      }
       if (j == lo) load_q(1);
-      // V_t: two places of K_{t-1}
-      if (t > 0 && alive)
-        alive = bar_wait(sh->k_empty + (s ^ 1u), ((t - 1) >> 1) & 1u, abort_flag, a);
-      if (!alive) break;
-      // the last tile's V lands for the clearing warp, which passes it on
-      uint64_t* bar = j == tail ? &sh->v_tail : sh->v_full + s;
-      if (j == tail) ++tails;
-      bar_expect_tx(bar, kUnitsV * kUnit);
-      for (int c = 0; c < kUnitsV; ++c)
+      for (int c = 0; c < kUnitsV && alive && place(x); ++c, ++x) {
+        // the last tile's V lands for the clearing warp, which passes it on
+        uint64_t* bar = j == tail ? &sh->v_tail : sh->full + x % kRing;
+        if (j != tail) {
+          bar_expect_tx(bar, kUnit);
+        } else if (c == 0) {
+          bar_expect_tx(bar, kUnitsV * kUnit);
+          ++tails;
+        }
         for (int d = 0; d < 2; ++d)
-          tma_load3(dst(x + kUnitsK + c) + d * (kUnit / 2), tv, d * 64, it.head, tok + c * 64, bar);
-      half = false;
-      ++t;
-      x += kUnitsTile;
+          tma_load3(dst(x) + d * (kUnit / 2), tv, d * 64, it.head, tok + c * 64, bar);
+      }
     }
   }
   // every box issued must have landed before the CTA can exit
   if (!alive || *abort_flag) {
     if (tails) bar_drain(&sh->v_tail, (tails - 1) & 1u);
-    for (uint32_t k = t > 1 ? t - 2 : 0u; k < t; ++k) {
-      bar_drain(sh->k_full + (k & 1u), (k >> 1) & 1u);
-      bar_drain(sh->v_full + (k & 1u), (k >> 1) & 1u);
-    }
-    if (half) bar_drain(sh->k_full + (t & 1u), (t >> 1) & 1u);
+    for (uint32_t k = x > kRing ? x - kRing : 0u; k < x; ++k)
+      bar_drain(sh->full + k % kRing, (k / kRing) & 1u);
     if (nq0) bar_drain(sh->q_full, (nq0 - 1) & 1u);
     if (nq1) bar_drain(sh->q_full + 1, (nq1 - 1) & 1u);
   }
@@ -242,10 +238,8 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
 
 // -------------------------------------------------------------------- MMAs
 //
-// One thread. Everything it does between MMAs counts: four MMAs wait in the
-// tensor cores' queue, so 256 cycles a half step are hidden and the rest is
-// lost. So it waits once a half step, for P of one tile: a softmax warp that
-// hands over P has seen V of this tile and K of the next one.
+// One thread. Everything it does between MMAs counts: about four MMAs wait in
+// the tensor cores' queue, so 256 cycles at a time are hidden and more is lost.
 __device__ void mma_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring) {
   volatile int* abort_flag = &sh->abort_flag;
   constexpr uint32_t tmem = 0;  // all columns are ours: they start at 0
@@ -255,60 +249,72 @@ __device__ void mma_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t
                  v_desc = sdesc(su32(ring), kUnit / 2, 1024);
   ItemReader reader(sh);
   Item it{};
-  uint32_t t = 0, x = 0;       // key tile (of j) and its first ring unit
+  uint32_t x = 0;              // first ring unit of tile j
   uint32_t pp = 0u, qp = 0u;   // parities of p_full and of the items, a bit per row tile
   bool alive = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    alive = bar_try(bar, parity & 1u) || bar_wait_slow(bar, parity & 1u, abort_flag, a);
-    return alive;
+    return alive = bar_try(bar, parity & 1u) || bar_wait_slow(bar, parity & 1u, abort_flag, a);
   };
   while (alive && reader.next_one(it, a)) {
     const int lo0 = it.lo0, hi0 = it.hi0, lo1 = it.lo1, hi1 = it.hi1;
     const int lo = min(lo0, lo1), hi = max(hi0, hi1);
     if (lo >= hi) continue;
-    if (!wait(sh->k_full + (t & 1u), t >> 1)) break;
     // step j: P V of tile j, then Q K of tile j + 1, for both row tiles
     for (int j = lo - 1; j < hi && alive; ++j) {
-      const uint32_t t1 = j < lo ? t : t + 1, x1 = j < lo ? x : x + kUnitsTile;
-      const uint64_t v0 = v_desc + (x + kUnitsK) % kRing * (kUnit / 16);
-      const uint64_t v1 = v_desc + (x + kUnitsK + 1) % kRing * (kUnit / 16);
-      const uint64_t k0 = k_desc + x1 % kRing * (kUnit / 16);
-      const uint64_t k1 = k_desc + (x1 + 1) % kRing * (kUnit / 16);
-      const uint64_t k2 = k_desc + (x1 + 2) % kRing * (kUnit / 16);
+      const uint32_t x1 = j < lo ? x : x + kUnitsTile;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int from = g ? lo1 : lo0, to = g ? hi1 : hi0;
-        if (j >= from && j < to) {
+        const bool do_pv = j >= from && j < to, do_qk = j + 1 >= from && j + 1 < to;
+        if (do_pv) {
           if (j == from && !wait(sh->o_free + g, qp >> g)) break;  // the last item's O is read
           if (!wait(sh->p_full + g, pp >> g)) break;
           pp ^= 1u << g;
-          fence_after();
-          const uint32_t acc = j != from;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + 2 * kKeys + g * kDv, tmem + g * kKeys + kk * 8,
-                   (kk < 4 ? v0 : v1) + (kk & 3) * 128, id_o, kk ? 1u : acc);
-          mma_commit(sh->o_done + g);
         }
-        if (g == 1 && j >= lo) mma_commit(sh->v_empty + (t & 1u));
-        if (j + 1 >= from && j + 1 < to) {
-          if (j + 1 == from) {
+        if (do_pv || (g == 1 && j >= lo)) {
+#pragma unroll
+          for (int c = 0; c < kUnitsV; ++c) {
+            const uint32_t u = x + kUnitsK + c, slot = u % kRing;
+            if (do_pv) {
+              if (!wait(sh->full + slot, u / kRing)) break;
+              if (c == 0) fence_after();
+              const uint64_t vd = v_desc + slot * (kUnit / 16);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts(tmem + 2 * kKeys + g * kDv, tmem + g * kKeys + (c * 4 + kk) * 8, vd + kk * 128,
+                       id_o, (c | kk) ? 1u : (j != from ? 1u : 0u));
+            }
+            if (g == 1) mma_commit(sh->empty + slot);
+          }
+          if (!alive) break;
+          if (do_pv) mma_commit(sh->o_done + g);
+        }
+        if (do_qk || (g == 1 && j + 1 < hi)) {
+          if (do_qk && j + 1 == from) {
             if (!wait(sh->q_full + g, qp >> g)) break;
-            // (a tile that sees its first keys late: no P has vouched for these)
-            if (!wait(sh->k_full + (t1 & 1u), t1 >> 1)) break;
             qp ^= 1u << g;
-            fence_after();
           }
 #pragma unroll
-          for (int kk = 0; kk < 12; ++kk)
-            mma<false>(tmem + g * kKeys, q_desc + (g * 3 + kk / 4) * (kUnit / 16) + (kk & 3) * 2,
-                       (kk < 4 ? k0 : kk < 8 ? k1 : k2) + (kk & 3) * 2, id_s, kk != 0);
-          mma_commit(sh->s_full + g);
-          if (j + 2 == to) mma_commit(sh->q_empty + g);
+          for (int c = 0; c < kUnitsK; ++c) {
+            const uint32_t u = x1 + c, slot = u % kRing;
+            if (do_qk) {
+              if (!wait(sh->full + slot, u / kRing)) break;
+              if (c == 0) fence_after();
+              const uint64_t kd = k_desc + slot * (kUnit / 16);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma<false>(tmem + g * kKeys, q_desc + (g * 3 + c) * (kUnit / 16) + kk * 2, kd + kk * 2,
+                           id_s, (c | kk) != 0);
+            }
+            if (g == 1) mma_commit(sh->empty + slot);
+          }
+          if (!alive) break;
+          if (do_qk) {
+            mma_commit(sh->s_full + g);
+            if (j + 2 == to) mma_commit(sh->q_empty + g);
+          }
         }
-        if (g == 1 && j + 1 < hi) mma_commit(sh->k_empty + (t1 & 1u));
       }
-      t = t1;
       x = x1;
     }
   }
@@ -330,7 +336,7 @@ __device__ void clear_role(const PrefillArgs& a, Shared* sh, uint8_t* ring) {
       const bool ok = bar_wait(&sh->v_tail, tails & 1u, &sh->abort_flag, a);
       if (!__all_sync(0xffffffffu, ok)) return;
       ++tails;
-      const uint32_t tt = t + static_cast<uint32_t>(tail - lo), x = tt * kUnitsTile + kUnitsK;
+      const uint32_t x = (t + static_cast<uint32_t>(tail - lo)) * kUnitsTile + kUnitsK;
       for (int r = it.keys % kKeys; r < kKeys; r += 2) {
         // two rows x 16 pieces of 16 bytes (two 64-channel atoms) a step
         const int row = r + (lane >> 4), piece = lane & 15;
@@ -341,7 +347,8 @@ __device__ void clear_role(const PrefillArgs& a, Shared* sh, uint8_t* ring) {
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) bar_arrive(sh->v_full + (tt & 1u));
+      if (lane == 0)
+        for (int c = 0; c < kUnitsV; ++c) bar_arrive(sh->full + (x + c) % kRing);
     }
     t += static_cast<uint32_t>(max(0, hi - lo));
   }
@@ -476,7 +483,7 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
   const float scale = sign != 0.f ? fabsf(a.sm_scale) * kLog2e : 1.f;
   ItemReader reader(sh);
   Item it{};
-  uint32_t n = 0, t = 0;  // key tiles seen by this row tile; of all items before this one
+  uint32_t n = 0;  // key tiles seen
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = bar_wait(bar, parity & 1u, abort_flag, a);
     return __all_sync(0xffffffffu, ok);
@@ -484,9 +491,6 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
   while (reader.next_warp(it, a)) {
     const int tile_rows = min(kRowsTile, it.rows - g * kRowsTile);
     const int lo = g ? it.lo1 : it.lo0, hi = g ? it.hi1 : it.hi0;
-    const int item_lo = min(it.lo0, it.lo1), item_hi = max(it.hi0, it.hi1);
-    const uint32_t t0 = t - static_cast<uint32_t>(item_lo);  // tile j is t0 + j of all
-    t += static_cast<uint32_t>(max(0, item_hi - item_lo));
     if (tile_rows <= 0) continue;
     const int row = g * kRowsTile + r, p = it.pos + row;
     const int last_key = a.causal ? min(p, it.keys - 1) : it.keys - 1;
@@ -571,11 +575,6 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
       float l0, l1;
       unpack2(add2(sum[0], sum[1]), l0, l1);
       l += l0 + l1;
-      if (quad == 0) {  // for the MMAs that P starts: V of this tile, K of the next
-        const uint32_t tj = t0 + static_cast<uint32_t>(j);
-        if (!wait(sh->v_full + (tj & 1u), tj >> 1)) return;
-        if (j + 1 < item_hi && !wait(sh->k_full + ((tj + 1) & 1u), (tj + 1) >> 1)) return;
-      }
       tmem_wait_st();
       fence_before();
       __syncwarp();
@@ -660,10 +659,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(sh->p_full + g, kSoftmaxWarps / 2);
       bar_init(sh->o_done + g, 1);
       bar_init(sh->o_free + g, kSoftmaxWarps / 2);
-      bar_init(sh->k_full + g, 1);
-      bar_init(sh->k_empty + g, 1);
-      bar_init(sh->v_full + g, 1);
-      bar_init(sh->v_empty + g, 1);
+    }
+    for (int u = 0; u < kRing; ++u) {
+      bar_init(sh->full + u, 1);
+      bar_init(sh->empty + u, 1);
     }
     for (int s = 0; s < kItems; ++s) {
       bar_init(sh->item_full + s, 1);
