@@ -398,7 +398,8 @@ int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64_t k_stride
  * q_lat[t, h, 512:] = q[t, h, 128:].
  *   q      bf16 [rows, Hq, 192], strides in elements (multiples of 8)
  *   q_lat  [rows, Hq, 576] contiguous, the plan's q_dtype: bf16, or E4M3 codes
- *          RNE(sat(x / q_scale)) (q_scale > 0; pda_decode's sm_scale takes it) */
+ *          RNE(sat(x * (1 / q_scale))) in fp32 (q_scale > 0; pda_decode's sm_scale
+ *          takes it) */
 int pda_mla_absorb(const pda_plan_t* plan, const void* q, int64_t q_stride_row,
                    int64_t q_stride_head, const void* w_uk, int64_t w_stride_head, float q_scale,
                    void* q_lat, int32_t rows, const int32_t* num_rows, void* split_scratch,

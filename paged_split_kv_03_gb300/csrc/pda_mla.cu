@@ -12,6 +12,7 @@
 
 #include "pda.h"
 #include "pda_internal.h"
+#include "pda_ptx.cuh"
 
 namespace pda {
 namespace {
@@ -21,8 +22,6 @@ constexpr int kRope = 64;
 constexpr int kLatRow = kLat + kRope;
 constexpr int kNope = 128;        // channels of a key (without rope) and of a value
 constexpr int kQDim = kNope + kRope;
-
-__device__ __forceinline__ float bf(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 // ------------------------------------------------------ gather of latents
 //
@@ -45,6 +44,7 @@ struct GatherArgs {
 // MODE: 0 bf16, 1 / 2 E4M3 per tensor / per token, 5 records.
 template <int MODE>
 __global__ void __launch_bounds__(256) gather_latent(const __grid_constant__ GatherArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the expansion may set up
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int total = __ldg(a.tok_indptr + a.batch);
@@ -111,79 +111,402 @@ __global__ void __launch_bounds__(256) gather_latent(const __grid_constant__ Gat
 
 // ------------------------------------------------------- products per head
 //
-// C_h[t, n] = sum_k A_h[t, k] B_h[n, k]: one CTA per head, 64 tokens and 64
-// columns, fp32 sums in registers (4 x 4 per thread), operands widened into
-// shared memory 32 channels at a time.
+// C_h[t, n] = sum_k A_h[t, k] B_h[n, k], fp32 sums in TMEM, one rounding:
+//   absorb   A = q_nope (K = 128), B = W_UK read the other way round: its rows
+//            are the K channels, so B is MN-major, as it lies (N = 512)
+//   project  A = o_lat (K = 512), B = W_UV (N = 128)
+// A CTA has 128 tokens of one head and kN columns. Bound: HBM (the weights at
+// few rows, A and C at many: 128 x 128 x 512 MACs a row tile and head are 2048
+// tensor cycles against 160 KB). Short rows cost nothing but idle MMA lanes,
+// as TMA reads no row behind the last. What a CTA needs in flight decides: all
+// of K at once for absorb and for few rows, a ring of three stages (two CTAs an
+// SM) for project at many. The output tile passes through the stages' memory so
+// that a warp writes whole 256-byte rows.
+
+enum { kAbsorb = 0, kProject = 1 };
 
 struct ProductArgs {
-  const __nv_bfloat16* a;
-  int64_t a_row, a_head;
-  const __nv_bfloat16* b;     // absorb: W_UK; project: W_UV; expand: W_UK
-  const __nv_bfloat16* b2;    // expand: W_UV
-  int64_t b_head;
-  void* out;                  // absorb, project: out; expand: k
-  __nv_bfloat16* out2;        // expand: v
-  int64_t o_row, o_head;
+  void* out;
+  const __nv_bfloat16* q;  // absorb: the rope channels pass through
+  int64_t q_row, q_head;
   const int32_t* num_rows;
-  float q_scale;
-  int rows, k, n, e4m3;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  float inv_scale;         // absorb to E4M3: 1 / q_scale, else 0
+  int rows, heads;
 };
 
-enum { kAbsorb = 0, kProject = 1, kExpand = 2 };
+template <int OP, int N>
+struct ProductCfg {
+  static constexpr int kK = OP == kAbsorb ? kNope : kLat;
+  static constexpr int kBlocks = kK / 64;                        // K blocks of 128 bytes
+  static constexpr int kStages = OP == kAbsorb ? kBlocks : N >= 128 ? 3 : kBlocks;
+  static constexpr int kABytes = 128 * 128, kBBytes = N * 128, kStage = kABytes + kBBytes;
+  static constexpr int kSmem = kStages * kStage + 1024;          // + alignment
+  static constexpr int kTotalN = OP == kAbsorb ? kLat : kNope;
+  static constexpr int kTmem = N < 32 ? 32 : N;
+  static_assert(kStages * kStage >= 128 * N * 2, "the output tile fits the stages");
+};
 
-template <int OP>
-__global__ void __launch_bounds__(256) product(const __grid_constant__ ProductArgs p) {
-  __shared__ float sa[32][65], sb[32][65];
-  int rows = p.rows;
-  if (p.num_rows) rows = min(rows, __ldg(p.num_rows));
-  const int t0 = blockIdx.x * 64, n0 = blockIdx.y * 64, h = blockIdx.z;
+// Two floats -> two E4M3 codes (RNE, saturating): low byte from `lo`.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+template <int OP, int N, bool E4M3>
+__global__ void __launch_bounds__(192)
+    product(const __grid_constant__ ProductArgs a, const __grid_constant__ CUtensorMap ta,
+            const __grid_constant__ CUtensorMap tb) {
+  using C = ProductCfg<OP, N>;
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t full[C::kStages], empty[C::kStages], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  uint8_t* smem = raw + ((1024u - (su32(raw) & 1023u)) & 1023u);
+  volatile int* abort_flag = &abort_word;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int rows = a.rows;
+  if (a.num_rows) rows = min(rows, __ldg(a.num_rows));
+  const int n0 = blockIdx.x * N, h = blockIdx.y, t0 = blockIdx.z * 128;
   if (t0 >= rows) return;
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.k; k0 += 32) {
-    for (int e = tid; e < 64 * 32; e += 256) {
-      const int r = e >> 5, k = k0 + (e & 31);
-      sa[e & 31][r] = t0 + r < rows ? bf(p.a + (t0 + r) * p.a_row + h * p.a_head + k) : 0.f;
-      const int n = n0 + r;
-      const __nv_bfloat16* b = p.b + h * p.b_head;
-      float v;
-      if (OP == kAbsorb) v = bf(b + static_cast<int64_t>(k) * kLat + n);
-      else if (OP == kProject) v = bf(b + static_cast<int64_t>(n) * kLat + k);
-      else v = bf((n < kNope ? b : p.b2 + h * p.b_head) + static_cast<int64_t>(n % kNope) * kLat + k);
-      sb[e & 31][r] = v;
+  if (tid == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      bar_init(full + s, 1);
+      bar_init(empty + s, 1);
     }
-    __syncthreads();
-    for (int k = 0; k < 32; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
+    bar_init(&done, 1);
+    abort_word = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = 0; i < 4; ++i) {
-    const int64_t t = t0 + ty * 4 + i;
-    if (t >= rows) break;
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + tx * 4 + j;
-      const int64_t o = t * p.o_row + h * p.o_head + n;
-      if (OP == kExpand && n >= kNope) p.out2[o - kNope] = __float2bfloat16(acc[i][j]);
-      else if (OP == kAbsorb && p.e4m3) {
-        uint16_t c;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(__fdiv_rn(acc[i][j], p.q_scale)));
-        static_cast<uint8_t*>(p.out)[o] = static_cast<uint8_t>(c);
-      } else static_cast<__nv_bfloat16*>(p.out)[o] = __float2bfloat16(acc[i][j]);
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     su32(&tmem_slot)),
+                 "r"(C::kTmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (warp == 0) {
+    if (lane == 0) {
+      bool alive = true;
+      int issued = 0;
+      for (int k = 0; k < C::kBlocks && alive; ++k) {
+        const int s = k % C::kStages;
+        if (k >= C::kStages)
+          alive = bar_wait(empty + s, ((k / C::kStages) - 1) & 1u, abort_flag, a);
+        if (!alive) break;
+        uint8_t* st = smem + s * C::kStage;
+        bar_expect_tx(full + s, C::kStage);
+        tma_load3(su32(st), &ta, k * 64, h, t0, full + s);
+        if constexpr (OP == kAbsorb) {  // 64 channels of K x N columns, 64 columns an atom
+          for (int c = 0; c < N / 64; ++c)
+            tma_load3(su32(st + C::kABytes + c * 8192), &tb, n0 + c * 64, k * 64, h, full + s);
+        } else {
+          tma_load3(su32(st + C::kABytes), &tb, k * 64, n0, h, full + s);
+        }
+        ++issued;
+      }
+      if (!alive)  // every box issued must have landed before the CTA can exit
+        for (int k = max(0, issued - C::kStages); k < issued; ++k)
+          bar_drain(full + k % C::kStages, (k / C::kStages) & 1u);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = idesc(1u, 0, N, OP == kAbsorb ? 1u : 0u);
+      bool alive = true;
+      for (int k = 0; k < C::kBlocks && alive; ++k) {
+        const int s = k % C::kStages;
+        alive = bar_wait(full + s, (k / C::kStages) & 1u, abort_flag, a);
+        if (!alive) break;
+        fence_after();
+        const uint32_t st = su32(smem + s * C::kStage);
+        const uint64_t ad = sdesc(st, 16, 1024);
+        const uint64_t bd = OP == kAbsorb ? sdesc(st + C::kABytes, 8192, 1024)
+                                          : sdesc(st + C::kABytes, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma<false>(tmem, ad + kk * 2, bd + kk * (OP == kAbsorb ? 128 : 2), id, (k | kk) != 0);
+        mma_commit(empty + s);
+      }
+      mma_commit(&done);
+      bar_drain(&done, 0);
+    }
+  } else {
+    const int quad = warp & 3;
+    if (OP == kAbsorb && n0 == 0) {  // the rope channels of this warp's rows
+      for (int r = lane >> 3; r < 32; r += 4) {
+        const int t = t0 + quad * 32 + r;
+        if (t >= rows) break;
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.q + t * a.q_row + h * a.q_head + kNope) +
+                              (lane & 7));
+        const int64_t o = (static_cast<int64_t>(t) * a.heads + h) * kLatRow + kLat + (lane & 7) * 8;
+        if constexpr (E4M3) {
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t c[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            c[e] = e4m3x2(__uint_as_float(w[e] << 16) * a.inv_scale,
+                          __uint_as_float(w[e] & 0xFFFF0000u) * a.inv_scale);
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + o) =
+              make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o) = v;
+        }
+      }
+      __syncwarp();
+    }
+    const bool ok = bar_wait(&done, 0, abort_flag, a);
+    if (__all_sync(0xffffffffu, ok) && *abort_flag == 0 && t0 + quad * 32 < rows) {
+      fence_after();
+      // rows of N values through this warp's share of the stages, 16-byte
+      // pieces exchanged by the row's low bits so that neither side conflicts
+      constexpr int kRowBytes = N * (E4M3 ? 1 : 2), kPieces = kRowBytes / 16;
+      uint8_t* mine = smem + quad * 32 * kRowBytes;
+#pragma unroll
+      for (int c = 0; c < N; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>(quad * 32) << 16) + c, v);
+        tmem_wait_ld<32>(v);
+        uint32_t w[16];
+        if constexpr (E4M3) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[4 * e + i]) * a.inv_scale;
+            w[e] = e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            w[e] = bf16x2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+        }
+#pragma unroll
+        for (int p = 0; p < (E4M3 ? 2 : 4); ++p) {
+          const int piece = (c * (E4M3 ? 1 : 2)) / 16 + p;
+          *reinterpret_cast<uint4*>(mine + lane * kRowBytes + ((piece ^ (lane & 7)) % kPieces) * 16) =
+              make_uint4(w[4 * p], w[4 * p + 1], w[4 * p + 2], w[4 * p + 3]);
+        }
+      }
+      __syncwarp();
+      for (int i = lane; i < 32 * kPieces; i += 32) {
+        const int r = i / kPieces, piece = i % kPieces, t = t0 + quad * 32 + r;
+        if (t >= rows) break;
+        const uint4 v = *reinterpret_cast<const uint4*>(mine + r * kRowBytes +
+                                                        ((piece ^ (r & 7)) % kPieces) * 16);
+        const int64_t o = (static_cast<int64_t>(t) * a.heads + h) * (OP == kAbsorb ? kLatRow : kNope) + n0;
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + o * (E4M3 ? 1 : 2) + piece * 16) = v;
+      }
     }
   }
-  if (OP == kAbsorb && n0 == 0)  // the rope channels pass through
-    for (int e = tid; e < 64 * kRope; e += 256) {
-      const int64_t t = t0 + e / kRope;
-      if (t >= rows) break;
-      const int64_t o = t * p.o_row + h * p.o_head + kLat + e % kRope;
-      const __nv_bfloat16 x = p.a[t * p.a_row + h * p.a_head + kNope + e % kRope];
-      if (p.e4m3) {
-        uint16_t c;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.f), "f"(__fdiv_rn(__bfloat162float(x), p.q_scale)));
-        static_cast<uint8_t*>(p.out)[o] = static_cast<uint8_t>(c);
-      } else static_cast<__nv_bfloat16*>(p.out)[o] = x;
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem)
+                 : "memory");
+}
+
+template <int OP, int N, bool E4M3>
+int launch_product(const ProductArgs& a, const CUtensorMap& ta, const CUtensorMap& tb,
+                   cudaStream_t s) {
+  using C = ProductCfg<OP, N>;
+  const auto fn = product<OP, N, E4M3>;
+  if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return PDA_ERR_CUDA;
+  }
+  fn<<<dim3(C::kTotalN / N, a.heads, (a.rows + 127) / 128), 192, C::kSmem, s>>>(a, ta, tb);
+  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+}
+
+// ------------------------------------------------------- keys and values
+//
+// [k | v]_h[t] = [W_UK; W_UV]_h c_t: 128 tokens x 256 columns x 512 a head and
+// row tile, 4096 tensor cycles against 64 KB written. Bound: the tensor cores
+// (8192 tokens x 128 heads: 275 GFLOP, 147 us at the measured rate; 589 MB, 87
+// us), then L2: so a CTA keeps its 128 latents (128 KB) in shared memory while
+// the heads' weights stream past through a ring of three 32 KB stages, 64 bytes
+// a cycle, a third less than with both operands in a ring. A CTA takes an equal run of
+// (row tile, head) pairs; two accumulators of 256 columns let a head's rows be
+// written while the next one's MMAs run.
+
+struct ExpandArgs {
+  __nv_bfloat16* k;
+  __nv_bfloat16* v;
+  int64_t o_row, o_head;
+  const int32_t* total;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  int tokens, heads;
+};
+
+constexpr int kExpStages = 3;
+constexpr int kExpA = 8 * 16384, kExpB = 2 * 16384;
+constexpr int kExpSmem = kExpA + kExpStages * kExpB + 1024;
+constexpr int kExpThreads = 192;
+
+__global__ void __launch_bounds__(kExpThreads, 1)
+    expand(const __grid_constant__ ExpandArgs a, const __grid_constant__ CUtensorMap ta,
+           const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t a_full, a_empty, full[kExpStages], empty[kExpStages], c_full[2], c_free[2], drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  uint8_t* smem = raw + ((1024u - (su32(raw) & 1023u)) & 1023u);
+  uint8_t* ring = smem + kExpA;
+  volatile int* abort_flag = &abort_word;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    bar_init(&a_full, 1);
+    bar_init(&a_empty, 1);
+    for (int s = 0; s < kExpStages; ++s) {
+      bar_init(full + s, 1);
+      bar_init(empty + s, 1);
     }
+    for (int c = 0; c < 2; ++c) {
+      bar_init(c_full + c, 1);
+      bar_init(c_free + c, 4);
+    }
+    bar_init(&drain, 1);
+    abort_word = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     su32(&tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = tmem_slot;
+  // this CTA's run of (row tile, head) pairs, head fastest
+  const int rows = min(a.tokens, __ldg(a.total));
+  const int64_t pairs = static_cast<int64_t>((max(rows, 0) + 127) / 128) * a.heads;
+  const int64_t f0 = pairs * blockIdx.x / gridDim.x, f1 = pairs * (blockIdx.x + 1) / gridDim.x;
+  if (warp == 0) {
+    if (lane == 0) {
+      bool alive = true;
+      uint32_t x = 0, tiles = 0;
+      int tile = -1;
+      for (int64_t f = f0; f < f1 && alive; ++f) {
+        const int h = static_cast<int>(f % a.heads), t = static_cast<int>(f / a.heads);
+        if (t != tile) {
+          if (!(alive = bar_wait(&a_empty, (tiles & 1u) ^ 1u, abort_flag, a))) break;
+          tile = t;
+          ++tiles;
+          bar_expect_tx(&a_full, kExpA);
+          // (the latents come from the kernel in front of this one)
+          if (tiles == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
+          for (int k = 0; k < 8; ++k)
+            tma_load3(su32(smem + k * 16384), &ta, k * 64, 0, t * 128, &a_full);
+        }
+        for (int k = 0; k < 8; ++k, ++x) {
+          const uint32_t s = x % kExpStages;
+          if (!(alive = bar_wait(empty + s, ((x / kExpStages) & 1u) ^ 1u, abort_flag, a))) break;
+          bar_expect_tx(full + s, kExpB);
+          tma_load3(su32(ring + s * kExpB), &tk, k * 64, 0, h, full + s);
+          tma_load3(su32(ring + s * kExpB + 16384), &tv, k * 64, 0, h, full + s);
+        }
+      }
+      if (!alive || *abort_flag) {  // every box issued must have landed before the CTA can exit
+        if (tiles) bar_drain(&a_full, (tiles - 1) & 1u);
+        for (uint32_t y = x > kExpStages ? x - kExpStages : 0u; y < x; ++y)
+          bar_drain(full + y % kExpStages, (y / kExpStages) & 1u);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id = idesc(1u, 0, 256);
+      const uint64_t ad = sdesc(su32(smem), 16, 1024), bd = sdesc(su32(ring), 16, 1024);
+      bool alive = true;
+      uint32_t x = 0, tiles = 0, n = 0;
+      int tile = -1;
+      for (int64_t f = f0; f < f1 && alive; ++f, ++n) {
+        const int t = static_cast<int>(f / a.heads);
+        if (t != tile) {
+          tile = t;
+          if (!(alive = bar_wait(&a_full, tiles & 1u, abort_flag, a))) break;
+          ++tiles;
+        }
+        const uint32_t c = n & 1u;
+        if (!(alive = bar_wait(c_free + c, ((n >> 1) & 1u) ^ 1u, abort_flag, a))) break;
+        for (int k = 0; k < 8; ++k, ++x) {
+          const uint32_t s = x % kExpStages;
+          if (!(alive = bar_wait(full + s, (x / kExpStages) & 1u, abort_flag, a))) break;
+          fence_after();
+          const uint64_t ak = ad + k * 1024, bk = bd + s * (kExpB / 16);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma<false>(tmem + c * 256, ak + kk * 2, bk + kk * 2, id, (k | kk) != 0);
+          mma_commit(empty + s);
+        }
+        if (!alive) break;
+        mma_commit(c_full + c);
+        if (f + 1 == f1 || static_cast<int>((f + 1) / a.heads) != tile) mma_commit(&a_empty);
+      }
+      mma_commit(&drain);
+      bar_drain(&drain, 0);
+    }
+  } else {
+    const int quad = warp & 3;
+    uint32_t n = 0;
+    for (int64_t f = f0; f < f1; ++f, ++n) {
+      const int h = static_cast<int>(f % a.heads);
+      const int64_t t = (f / a.heads) * 128 + quad * 32 + lane;
+      const uint32_t c = n & 1u;
+      const bool ok = bar_wait(c_full + c, (n >> 1) & 1u, abort_flag, a);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      fence_after();
+      const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c * 256;
+      const int64_t o = t * a.o_row + h * a.o_head;
+#pragma unroll
+      for (int col = 0; col < 256; col += 32) {
+        uint32_t v[32];
+        __syncwarp();
+        tmem_ld32(src + col, v);
+        tmem_wait_ld<32>(v);
+        if (t < rows) {
+          uint4* dst = reinterpret_cast<uint4*>((col < kNope ? a.k : a.v) + o + col % kNope);
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = bf16x2(__uint_as_float(v[p * 8 + 2 * e]), __uint_as_float(v[p * 8 + 2 * e + 1]));
+            dst[p] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      __syncwarp();
+      fence_before();
+      if (lane == 0) bar_arrive(c_free + c);
+    }
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
 }
 
 bool a16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
@@ -196,17 +519,11 @@ int check_mla(const pda_plan_t* plan, int64_t w_stride_head, int rows, const int
   if (plan->magic != PDA_PLAN_MAGIC) return PDA_ERR_PLAN;
   if (!split_scratch || reinterpret_cast<uintptr_t>(split_scratch) % 256) return PDA_ERR_SCRATCH;
   if (plan->head_dim != kLatRow || plan->num_kv_heads != 1) return PDA_ERR_UNSUPPORTED;
-  if (rows < 0 || w_stride_head < kNope * kLat) return PDA_ERR_INVALID;
+  // (row tiles are a grid's z, heads its y)
+  if (rows < 0 || rows > 65535 * 128 || plan->num_qo_heads > 65535 || w_stride_head < kNope * kLat)
+    return PDA_ERR_INVALID;
   if (w_stride_head % 8 || !a4(num_rows)) return PDA_ERR_ALIGNMENT;
   return PDA_OK;
-}
-
-template <int OP>
-int launch_product(const pda_plan_t* plan, ProductArgs& p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((p.rows + 63) / 64), static_cast<unsigned>(p.n / 64),
-                  static_cast<unsigned>(plan->num_qo_heads));
-  product<OP><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
 }
 
 }  // namespace
@@ -226,21 +543,23 @@ extern "C" int pda_mla_absorb(const pda_plan_t* plan, const void* q, int64_t q_s
   if (!a16(q) || !a16(w_uk) || !a16(q_lat) || q_stride_row % 8 || q_stride_head % 8)
     return PDA_ERR_ALIGNMENT;
   ProductArgs p = {};
-  p.a = static_cast<const __nv_bfloat16*>(q);
-  p.a_row = q_stride_row;
-  p.a_head = q_stride_head;
-  p.b = static_cast<const __nv_bfloat16*>(w_uk);
-  p.b_head = w_stride_head;
   p.out = q_lat;
-  p.o_row = static_cast<int64_t>(plan->num_qo_heads) * kLatRow;
-  p.o_head = kLatRow;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_row = q_stride_row;
+  p.q_head = q_stride_head;
   p.num_rows = num_rows;
-  p.q_scale = q_scale;
+  p.status = static_cast<uint32_t*>(split_scratch);
+  p.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us) * 1000ull;
+  p.inv_scale = e4m3 ? 1.f / q_scale : 0.f;
   p.rows = rows;
-  p.k = kNope;
-  p.n = kLat;
-  p.e4m3 = e4m3;
-  return launch_product<kAbsorb>(plan, p, reinterpret_cast<cudaStream_t>(stream));
+  p.heads = plan->num_qo_heads;
+  CUtensorMap ta, tb;
+  if (!make_map3(&ta, q, kNope, p.heads, rows, q_stride_head, q_stride_row, 64, 1, 128) ||
+      !make_map3(&tb, w_uk, kLat, kNope, p.heads, kLat, w_stride_head, 64, 64, 1))
+    return PDA_ERR_CUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return e4m3 ? launch_product<kAbsorb, 128, true>(p, ta, tb, s)
+              : launch_product<kAbsorb, 128, false>(p, ta, tb, s);
 }
 
 extern "C" int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const void* w_uv,
@@ -252,19 +571,23 @@ extern "C" int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const 
   if (!o_lat || !w_uv || !out) return PDA_ERR_NULL;
   if (!a16(o_lat) || !a16(w_uv) || !a16(out)) return PDA_ERR_ALIGNMENT;
   ProductArgs p = {};
-  p.a = static_cast<const __nv_bfloat16*>(o_lat);
-  p.a_row = static_cast<int64_t>(plan->num_qo_heads) * kLat;
-  p.a_head = kLat;
-  p.b = static_cast<const __nv_bfloat16*>(w_uv);
-  p.b_head = w_stride_head;
   p.out = out;
-  p.o_row = static_cast<int64_t>(plan->num_qo_heads) * kNope;
-  p.o_head = kNope;
   p.num_rows = num_rows;
+  p.status = static_cast<uint32_t*>(split_scratch);
+  p.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us) * 1000ull;
   p.rows = rows;
-  p.k = kLat;
-  p.n = kNope;
-  return launch_product<kProject>(plan, p, reinterpret_cast<cudaStream_t>(stream));
+  p.heads = plan->num_qo_heads;
+  // With fewer (head, row tile) pairs than SMs, four CTAs share a pair's
+  // columns: each streams a quarter of the weights, all of K in flight.
+  const int64_t pairs = static_cast<int64_t>(p.heads) * ((rows + 127) / 128);
+  const bool few = pairs * 2 <= plan->num_sms;
+  CUtensorMap ta, tb;
+  if (!make_map3(&ta, o_lat, kLat, p.heads, rows, kLat, static_cast<int64_t>(p.heads) * kLat, 64, 1, 128) ||
+      !make_map3(&tb, w_uv, kLat, kNope, p.heads, kLat, w_stride_head, 64, few ? 32 : 128, 1))
+    return PDA_ERR_CUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return few ? launch_product<kProject, 32, false>(p, ta, tb, s)
+             : launch_product<kProject, 128, false>(p, ta, tb, s);
 }
 
 extern "C" int pda_mla_expand(const pda_plan_t* plan, const void* k_pages,
@@ -307,19 +630,40 @@ extern "C" int pda_mla_expand(const pda_plan_t* plan, const void* k_pages,
   else if (plan->scale_mode == PDA_SCALE_TENSOR) gather_latent<1><<<blocks, 256, 0, s>>>(g);
   else gather_latent<2><<<blocks, 256, 0, s>>>(g);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-  ProductArgs p = {};
-  p.a = static_cast<const __nv_bfloat16*>(latent);
-  p.a_row = kLatRow;
-  p.b = static_cast<const __nv_bfloat16*>(w_uk);
-  p.b2 = static_cast<const __nv_bfloat16*>(w_uv);
-  p.b_head = w_stride_head;
-  p.out = k;
-  p.out2 = static_cast<__nv_bfloat16*>(v);
-  p.o_row = kv_stride_token;
-  p.o_head = kv_stride_head;
-  p.num_rows = tok_indptr + plan->batch;
-  p.rows = tokens;
-  p.k = kLat;
-  p.n = 2 * kNope;
-  return launch_product<kExpand>(plan, p, s);
+  ExpandArgs e = {};
+  e.k = static_cast<__nv_bfloat16*>(k);
+  e.v = static_cast<__nv_bfloat16*>(v);
+  e.o_row = kv_stride_token;
+  e.o_head = kv_stride_head;
+  e.total = tok_indptr + plan->batch;
+  e.status = g.status;
+  e.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us) * 1000ull;
+  e.tokens = tokens;
+  e.heads = plan->num_qo_heads;
+  CUtensorMap ta, tk, tv;
+  if (!make_map3(&ta, latent, kLat, 1, tokens, kLatRow, kLatRow, 64, 1, 128) ||
+      !make_map3(&tk, w_uk, kLat, kNope, e.heads, kLat, w_stride_head, 64, 128, 1) ||
+      !make_map3(&tv, w_uv, kLat, kNope, e.heads, kLat, w_stride_head, 64, 128, 1))
+    return PDA_ERR_CUDA;
+  if (cudaFuncSetAttribute(reinterpret_cast<const void*>(expand),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, kExpSmem) != cudaSuccess) {
+    cudaGetLastError();
+    return PDA_ERR_CUDA;
+  }
+  const int64_t pairs = static_cast<int64_t>((tokens + 127) / 128) * e.heads;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs < plan->num_sms ? pairs : plan->num_sms));
+  cfg.blockDim = dim3(kExpThreads);
+  cfg.dynamicSmemBytes = kExpSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, expand, e, ta, tk, tv) != cudaSuccess) {
+    cudaGetLastError();
+    return PDA_ERR_CUDA;
+  }
+  return PDA_OK;
 }
