@@ -174,8 +174,10 @@ def _ptr(x) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: a torch Stream object costs ten times as much
+        from torch._C import _cuda_getCurrentRawStream
+        from torch.cuda import current_device
+        return _cuda_getCurrentRawStream(current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -254,31 +256,37 @@ def pda_append_kv(plan: PdaPlan, k_new, v_new, page_table, kv_indptr, kv_len, qo
     return rc
 
 
-_DTYPES: dict = {}
+def _types():
+    """(bfloat16, int32, int64, float32, float8_e4m3fn, uint8) of torch, looked up once."""
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = (torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.float8_e4m3fn,
+                  torch.uint8)
+    return _TYPES
 
 
-def _shape(where: str, **tensors) -> None:
-    """The sizes, types and strides that a call with raw pointers assumes and the library
-    cannot see: name=(tensor, dtype names, shape[, n]), None in a shape for any size, the
-    last n dimensions contiguous (default: all)."""
-    for name, (t, dtype, shape, *inner) in tensors.items():
-        if t is None:
-            continue
-        if dtype not in _DTYPES:
-            import torch
-            _DTYPES[dtype] = tuple(getattr(torch, d) for d in dtype.split())
-        if t.dtype not in _DTYPES[dtype]:
-            raise ValueError(f"{where}: {name} is {t.dtype}, not {dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{where}: {name} is not on a CUDA device")
-        got = t.shape
-        if len(got) != len(shape) or any(s is not None and s != n for s, n in zip(shape, got)):
-            raise ValueError(f"{where}: {name} has shape {tuple(got)}, not {shape}")
-        want, strides, n = 1, t.stride(), len(shape)
-        for d in range(n - 1, n - 1 - (inner[0] if inner else n), -1):
-            if strides[d] != want and got[d] > 1:
-                raise ValueError(f"{where}: {name} is not contiguous in dimension {d}")
-            want *= got[d]
+_TYPES = None
+
+
+def _chk(where: str, name: str, t, dtype, shape, tail=None) -> None:
+    """The type, sizes and strides that a call with raw pointers assumes and the library cannot
+    see: ``tail`` are the strides of the last dimensions (None: contiguous)."""
+    if (t.dtype is dtype and t.is_cuda and t.shape == shape and
+            (t.is_contiguous() if tail is None else t.stride()[-len(tail):] == tail)):
+        return
+    if t.dtype is not dtype:
+        raise ValueError(f"{where}: {name} is {t.dtype}, not {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{where}: {name} is not on a CUDA device")
+    if t.shape != shape:
+        raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    got = t.stride()
+    for d in range(-1, -1 - len(tail or ()), -1):  # a dimension of one has any stride
+        if t.shape[d] > 1 and got[d] != tail[d]:
+            raise ValueError(f"{where}: {name} has strides {got}, its last ones not {tail}")
+    if tail is None:
+        raise ValueError(f"{where}: {name} is not contiguous")
 
 
 def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, free_pages,
@@ -287,76 +295,112 @@ def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, f
     """Block tables and slot maps of one step from the request lengths, on the GPU (see
     include/pda.h). ``block_table`` is [rows, cols] int32, ``slot_map`` int64, the others int32;
     ``request``, ``tok_indptr``, ``slot_map`` and ``positions`` may be None."""
-    n = plan.batch
-    _shape("pda_build_tables", cached_len=(cached_len, "int32", (n,)),
-           new_len=(new_len, "int32", (n,)), request=(request, "int32", (n,)),
-           block_table=(block_table, "int32", (None, None), 1),
-           free_pages=(free_pages, "int32", (None,)), free_count=(free_count, "int32", (1,)),
-           free_left=(free_left, "int32", (1,)), kv_len=(kv_len, "int32", (n,)),
-           kv_indptr=(kv_indptr, "int32", (n + 1,)), page_table=(page_table, "int32", (None,)),
-           qo_indptr=(qo_indptr, "int32", (n + 1,)), tok_indptr=(tok_indptr, "int32", (n + 1,)),
-           slot_map=(slot_map, "int64", (None,)), positions=(positions, "int32", (None,)))
-    rows = min(x.shape[0] for x in (slot_map, positions) if x is not None) \
-        if slot_map is not None or positions is not None else 0x7fffffff
-    t = PdaTables(_ptr(cached_len), _ptr(new_len), _ptr(request), _ptr(block_table),
-                  block_table.stride(0), _ptr(free_pages), _ptr(free_count), _ptr(free_left),
-                  _ptr(kv_len), _ptr(kv_indptr), _ptr(page_table), _ptr(qo_indptr),
-                  _ptr(tok_indptr), _ptr(slot_map), _ptr(positions), block_table.shape[0],
-                  block_table.shape[1], page_table.shape[0], rows)
+    _, i32, i64, _, _, _ = _types()
+    where, n = "pda_build_tables", plan.batch
+    per, ptrs, one = (n,), (n + 1,), (1,)
+    _chk(where, "cached_len", cached_len, i32, per)
+    _chk(where, "new_len", new_len, i32, per)
+    _chk(where, "kv_len", kv_len, i32, per)
+    _chk(where, "kv_indptr", kv_indptr, i32, ptrs)
+    _chk(where, "qo_indptr", qo_indptr, i32, ptrs)
+    _chk(where, "free_count", free_count, i32, one)
+    _chk(where, "free_left", free_left, i32, one)
+    _chk(where, "free_pages", free_pages, i32, (free_pages.numel(),))
+    _chk(where, "page_table", page_table, i32, (page_table.numel(),))
+    rows, cols = block_table.shape
+    _chk(where, "block_table", block_table, i32, (rows, cols), (1,))
+    cap = 0x7fffffff
+    if request is not None:
+        _chk(where, "request", request, i32, per)
+        request = request.data_ptr()
+    if tok_indptr is not None:
+        _chk(where, "tok_indptr", tok_indptr, i32, ptrs)
+        tok_indptr = tok_indptr.data_ptr()
+    if slot_map is not None:
+        cap = slot_map.numel()
+        _chk(where, "slot_map", slot_map, i64, (cap,))
+        slot_map = slot_map.data_ptr()
+    if positions is not None:
+        _chk(where, "positions", positions, i32, (positions.numel(),))
+        cap = min(cap, positions.numel())
+        positions = positions.data_ptr()
+    t = PdaTables(cached_len.data_ptr(), new_len.data_ptr(), request, block_table.data_ptr(),
+                  block_table.stride(0) if rows > 1 else cols, free_pages.data_ptr(),
+                  free_count.data_ptr(), free_left.data_ptr(), kv_len.data_ptr(),
+                  kv_indptr.data_ptr(), page_table.data_ptr(), qo_indptr.data_ptr(), tok_indptr,
+                  slot_map, positions, rows, cols, page_table.numel(), cap)
     rc = load_library().pda_build_tables(ctypes.byref(plan), ctypes.byref(t), _ptr(split_scratch),
                                          _stream(stream))
     if check and rc != PDA_OK:
-        raise PdaError(rc, "pda_build_tables")
+        raise PdaError(rc, where)
     return rc
+
+
+def _num_rows(where: str, t):
+    """Address of a one-element int32 device tensor, or None."""
+    if t is None:
+        return None
+    _chk(where, "num_rows", t, _types()[1], (1,))
+    return t.data_ptr()
 
 
 def pda_append_slots(plan: PdaPlan, k_new, v_new, slot_map, num_rows, k_pages, v_pages, k_scale,
                      v_scale, split_scratch, stream=None, check: bool = True) -> int:
     """Append rows (bf16 [rows, Hkv, D], any row stride) through a slot map (int64 [rows]);
-    ``num_rows``: an int32 device tensor bounding the rows, or None."""
-    rows = slot_map.shape[0]
-    new = (rows, plan.num_kv_heads, plan.head_dim)
-    _shape("pda_append_slots", k_new=(k_new, "bfloat16", new, 2), v_new=(v_new, "bfloat16", new, 2),
-           slot_map=(slot_map, "int64", (rows,)))
+    ``num_rows``: an int32 device tensor of one element bounding the rows, or None."""
+    bf16, _, i64, _, _, _ = _types()
+    where = "pda_append_slots"
+    rows, d = slot_map.numel(), plan.head_dim
+    new, tail = (rows, plan.num_kv_heads, d), (d, 1)
+    _chk(where, "k_new", k_new, bf16, new, tail)
+    _chk(where, "slot_map", slot_map, i64, (rows,))
+    if v_new is not None:
+        _chk(where, "v_new", v_new, bf16, new, tail)
     rc = load_library().pda_append_slots(
-        ctypes.byref(plan), _ptr(k_new), _row_stride(k_new), _ptr(v_new),
-        0 if v_new is None else _row_stride(v_new), _ptr(slot_map), rows, _ptr(num_rows),
-        _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale), _ptr(split_scratch),
-        _stream(stream))
+        ctypes.byref(plan), k_new.data_ptr(), _row_stride(k_new), _ptr(v_new),
+        0 if v_new is None else _row_stride(v_new), slot_map.data_ptr(), rows,
+        _num_rows(where, num_rows), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+        _ptr(split_scratch), _stream(stream))
     if check and rc != PDA_OK:
-        raise PdaError(rc, "pda_append_slots")
+        raise PdaError(rc, where)
     return rc
 
 
 def _row_stride(x) -> int:
     """Elements between rows; a lone row's stride has no meaning in torch."""
+    if x.shape[0] > 1:
+        return x.stride(0)
     n = 1
     for s in x.shape[1:]:
         n *= s
-    return x.stride(0) if x.shape[0] > 1 else n
+    return n
 
 
 def _head_strides(x):
     """(row, head) strides in elements of [rows, heads, channels]."""
-    head = x.stride(1) if x.shape[1] > 1 else x.shape[2]
-    return (x.stride(0) if x.shape[0] > 1 else x.shape[1] * head), head
+    row, head, _ = x.stride()
+    if x.shape[1] == 1:
+        head = x.shape[2]
+    return (row if x.shape[0] > 1 else x.shape[1] * head), head
 
 
 def pda_mla_absorb(plan: PdaPlan, q, w_uk, q_scale: float, q_lat, num_rows, split_scratch,
                    stream=None, check: bool = True) -> int:
     """The query absorbed into the latent space: q bf16 [rows, Hq, 192], w_uk bf16
     [Hq, 128, 512] (any head stride), q_lat [rows, Hq, 576] bf16 or E4M3 codes."""
+    bf16, _, _, _, e4m3, u8 = _types()
+    where = "pda_mla_absorb"
     rows, h = q.shape[0], plan.num_qo_heads
-    _shape("pda_mla_absorb", q=(q, "bfloat16", (rows, h, 192), 1),
-           w_uk=(w_uk, "bfloat16", (h, 128, 512), 2),
-           q_lat=(q_lat, "bfloat16" if plan.q_dtype == PDA_BF16 else "float8_e4m3fn uint8",
-                  (rows, h, 576)))
+    _chk(where, "q", q, bf16, (rows, h, 192), (1,))
+    _chk(where, "w_uk", w_uk, bf16, (h, 128, 512), (512, 1))
+    _chk(where, "q_lat", q_lat,
+         bf16 if plan.q_dtype == PDA_BF16 else u8 if q_lat.dtype is u8 else e4m3, (rows, h, 576))
     row, head = _head_strides(q)
     rc = load_library().pda_mla_absorb(
-        ctypes.byref(plan), _ptr(q), row, head, _ptr(w_uk), _row_stride(w_uk), float(q_scale),
-        _ptr(q_lat), rows, _ptr(num_rows), _ptr(split_scratch), _stream(stream))
+        ctypes.byref(plan), q.data_ptr(), row, head, w_uk.data_ptr(), _row_stride(w_uk), q_scale,
+        q_lat.data_ptr(), rows, _num_rows(where, num_rows), _ptr(split_scratch), _stream(stream))
     if check and rc != PDA_OK:
-        raise PdaError(rc, "pda_mla_absorb")
+        raise PdaError(rc, where)
     return rc
 
 
@@ -364,42 +408,53 @@ def pda_mla_project(plan: PdaPlan, o_lat, w_uv, out, num_rows, split_scratch, st
                     check: bool = True) -> int:
     """The decode's latent output projected: o_lat bf16 [rows, Hq, 512], w_uv bf16
     [Hq, 128, 512] (any head stride), out bf16 [rows, Hq, 128]."""
+    bf16 = _types()[0]
+    where = "pda_mla_project"
     rows, h = o_lat.shape[0], plan.num_qo_heads
-    _shape("pda_mla_project", o_lat=(o_lat, "bfloat16", (rows, h, 512)),
-           w_uv=(w_uv, "bfloat16", (h, 128, 512), 2), out=(out, "bfloat16", (rows, h, 128)))
+    _chk(where, "o_lat", o_lat, bf16, (rows, h, 512))
+    _chk(where, "w_uv", w_uv, bf16, (h, 128, 512), (512, 1))
+    _chk(where, "out", out, bf16, (rows, h, 128))
     rc = load_library().pda_mla_project(
-        ctypes.byref(plan), _ptr(o_lat), _ptr(w_uv), _row_stride(w_uv), _ptr(out), rows,
-        _ptr(num_rows), _ptr(split_scratch), _stream(stream))
+        ctypes.byref(plan), o_lat.data_ptr(), w_uv.data_ptr(), _row_stride(w_uv), out.data_ptr(),
+        rows, _num_rows(where, num_rows), _ptr(split_scratch), _stream(stream))
     if check and rc != PDA_OK:
-        raise PdaError(rc, "pda_mla_project")
+        raise PdaError(rc, where)
     return rc
 
 
 def _same_strides(where: str, k, v):
-    if k.shape[0] > 1 and k.stride(0) != v.stride(0) or k.shape[1] > 1 and k.stride(1) != v.stride(1):
+    got = _head_strides(k)
+    if got != _head_strides(v):
         raise ValueError(f"{where}: k and v differ in their strides")
-    return _head_strides(k)
+    return got
 
 
 def pda_mla_expand(plan: PdaPlan, k_pages, page_table, kv_indptr, tok_indptr, k_scale, w_uk, w_uv,
                    latent, k, v, split_scratch, stream=None, check: bool = True) -> int:
     """Keys and values of cached tokens: latent bf16 [tokens, 576], k and v bf16
     [tokens, Hq, 128] (strided alike) are written; w_uk and w_uv bf16 [Hq, 128, 512]."""
-    tokens, h, n = latent.shape[0], plan.num_qo_heads, plan.batch + 1
-    _shape("pda_mla_expand", w_uk=(w_uk, "bfloat16", (h, 128, 512), 2),
-           w_uv=(w_uv, "bfloat16", (h, 128, 512), 2), latent=(latent, "bfloat16", (tokens, 576)),
-           k=(k, "bfloat16", (tokens, h, 128), 1), v=(v, "bfloat16", (tokens, h, 128), 1),
-           kv_indptr=(kv_indptr, "int32", (n,)), tok_indptr=(tok_indptr, "int32", (n,)),
-           page_table=(page_table, "int32", (None,)))
-    if _row_stride(w_uk) != _row_stride(w_uv):
-        raise ValueError("pda_mla_expand: w_uk and w_uv differ in their head strides")
-    tok, head = _same_strides("pda_mla_expand", k, v)
+    bf16, i32, _, _, _, _ = _types()
+    where = "pda_mla_expand"
+    tokens, h, ptrs = latent.shape[0], plan.num_qo_heads, (plan.batch + 1,)
+    _chk(where, "w_uk", w_uk, bf16, (h, 128, 512), (512, 1))
+    _chk(where, "w_uv", w_uv, bf16, (h, 128, 512), (512, 1))
+    _chk(where, "latent", latent, bf16, (tokens, 576))
+    _chk(where, "k", k, bf16, (tokens, h, 128), (1,))
+    _chk(where, "v", v, bf16, (tokens, h, 128), (1,))
+    _chk(where, "kv_indptr", kv_indptr, i32, ptrs)
+    _chk(where, "tok_indptr", tok_indptr, i32, ptrs)
+    _chk(where, "page_table", page_table, i32, (page_table.numel(),))
+    w_head = _row_stride(w_uk)
+    if w_head != _row_stride(w_uv):
+        raise ValueError(f"{where}: w_uk and w_uv differ in their head strides")
+    tok, head = _same_strides(where, k, v)
     rc = load_library().pda_mla_expand(
-        ctypes.byref(plan), _ptr(k_pages), _ptr(page_table), _ptr(kv_indptr), _ptr(tok_indptr),
-        _ptr(k_scale), _ptr(w_uk), _ptr(w_uv), _row_stride(w_uk), _ptr(latent), _ptr(k), _ptr(v),
-        tok, head, tokens, _ptr(split_scratch), _stream(stream))
+        ctypes.byref(plan), _ptr(k_pages), page_table.data_ptr(), kv_indptr.data_ptr(),
+        tok_indptr.data_ptr(), _ptr(k_scale), w_uk.data_ptr(), w_uv.data_ptr(), w_head,
+        latent.data_ptr(), k.data_ptr(), v.data_ptr(), tok, head, tokens, _ptr(split_scratch),
+        _stream(stream))
     if check and rc != PDA_OK:
-        raise PdaError(rc, "pda_mla_expand")
+        raise PdaError(rc, where)
     return rc
 
 
@@ -420,20 +475,30 @@ def pda_mla_prefill(pre: PdaPrefillPlan, q, k, v, k_rope, qo_indptr, tok_indptr,
     """Expanded latent attention of ragged requests: q bf16 [rows, Hq, 192], k and v bf16
     [tokens, Hq, 128] (strided alike), k_rope bf16 [tokens, 64], out bf16 [rows, Hq, 128],
     lse fp32 [rows, Hq] or None; rows and tokens are the plan's."""
+    bf16, i32, _, f32, _, _ = _types()
+    where = "pda_mla_prefill"
     rows, tokens, h, n = pre.rows, pre.tokens, pre.num_qo_heads, pre.batch
-    _shape("pda_mla_prefill", q=(q, "bfloat16", (rows, h, 192), 1),
-           k=(k, "bfloat16", (tokens, h, 128), 1), v=(v, "bfloat16", (tokens, h, 128), 1),
-           k_rope=(k_rope, "bfloat16", (tokens, 64), 1), qo_indptr=(qo_indptr, "int32", (n + 1,)),
-           tok_indptr=(tok_indptr, "int32", (n + 1,)), window=(window, "int32", (n,)),
-           out=(out, "bfloat16", (rows, h, 128)), lse=(lse, "float32", (rows, h)))
-    tok, head = _same_strides("pda_mla_prefill", k, v)
+    _chk(where, "q", q, bf16, (rows, h, 192), (1,))
+    _chk(where, "k", k, bf16, (tokens, h, 128), (1,))
+    _chk(where, "v", v, bf16, (tokens, h, 128), (1,))
+    _chk(where, "k_rope", k_rope, bf16, (tokens, 64), (1,))
+    _chk(where, "qo_indptr", qo_indptr, i32, (n + 1,))
+    _chk(where, "tok_indptr", tok_indptr, i32, (n + 1,))
+    _chk(where, "out", out, bf16, (rows, h, 128))
+    if window is not None:
+        _chk(where, "window", window, i32, (n,))
+        window = window.data_ptr()
+    if lse is not None:
+        _chk(where, "lse", lse, f32, (rows, h))
+        lse = lse.data_ptr()
+    tok, head = _same_strides(where, k, v)
     row, qhead = _head_strides(q)
     rc = load_library().pda_mla_prefill(
-        ctypes.byref(pre), _ptr(q), row, qhead, _ptr(k), _ptr(v), tok, head, _ptr(k_rope),
-        _row_stride(k_rope), _ptr(qo_indptr), _ptr(tok_indptr), _ptr(window), int(bool(causal)),
-        float(sm_scale), _ptr(out), _ptr(lse), _ptr(scratch), _stream(stream))
+        ctypes.byref(pre), q.data_ptr(), row, qhead, k.data_ptr(), v.data_ptr(), tok, head,
+        k_rope.data_ptr(), _row_stride(k_rope), qo_indptr.data_ptr(), tok_indptr.data_ptr(), window,
+        1 if causal else 0, sm_scale, out.data_ptr(), lse, _ptr(scratch), _stream(stream))
     if check and rc != PDA_OK:
-        raise PdaError(rc, "pda_mla_prefill")
+        raise PdaError(rc, where)
     return rc
 
 
