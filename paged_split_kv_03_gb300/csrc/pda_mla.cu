@@ -335,14 +335,16 @@ int launch_product(const ProductArgs& a, const CUtensorMap& ta, const CUtensorMa
 
 // ------------------------------------------------------- keys and values
 //
-// [k | v]_h[t] = [W_UK; W_UV]_h c_t: 128 tokens x 256 columns x 512 a head and
-// row tile, 4096 tensor cycles against 64 KB written. Bound: the tensor cores
-// (8192 tokens x 128 heads: 275 GFLOP, 147 us at the measured rate; 589 MB, 87
-// us), then L2: so a CTA keeps its 128 latents (128 KB) in shared memory while
-// the heads' weights stream past through a ring of three 32 KB stages, 64 bytes
-// a cycle, a third less than with both operands in a ring. A CTA takes an equal run of
-// (row tile, head) pairs; two accumulators of 256 columns let a head's rows be
-// written while the next one's MMAs run.
+// [k | v]_h[t] = [W_UK; W_UV]_h c_t. Bound: the tensor cores (8192 tokens x 128
+// heads: 275 GFLOP, 147 us at the measured rate; 589 MB, 87 us), if operands keep
+// up: a CTA pair takes 256 tokens, M = 256 over both SMs, N = 256 (a head's k
+// and v). Each CTA keeps its 128 latents (128 KB) in shared memory while half of
+// the head's weights (CTA 0 W_UK, CTA 1 W_UV) stream past through a ring of five 16
+// KB stages: 32 bytes a cycle from L2 and 2000 cycles from a load to its use. With
+// one CTA and all of the weights it was 64 bytes a cycle and 1000 cycles, less
+// than TMA takes: 289 us, 950 TFLOP/s. A pair takes an equal run of (row tile,
+// head) pairs; two accumulators of 256 columns let a head's rows be written
+// while the next one's MMAs run.
 
 struct ExpandArgs {
   __nv_bfloat16* k;
@@ -354,12 +356,13 @@ struct ExpandArgs {
   int tokens, heads;
 };
 
-constexpr int kExpStages = 3;
-constexpr int kExpA = 8 * 16384, kExpB = 2 * 16384;
-constexpr int kExpSmem = kExpA + kExpStages * kExpB + 1024;
+constexpr int kExpStages = 5;
+constexpr int kExpA = 8 * 16384, kExpB = 16384;
+constexpr int kExpOut = 4 * 4096;  // 32 rows x 128 bytes a warp
+constexpr int kExpSmem = kExpA + kExpStages * kExpB + kExpOut + 1024;
 constexpr int kExpThreads = 192;
 
-__global__ void __launch_bounds__(kExpThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
     expand(const __grid_constant__ ExpandArgs a, const __grid_constant__ CUtensorMap ta,
            const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
   extern __shared__ uint8_t raw[];
@@ -370,6 +373,7 @@ __global__ void __launch_bounds__(kExpThreads, 1)
   uint8_t* ring = smem + kExpA;
   volatile int* abort_flag = &abort_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
   if (tid == 0) {
     bar_init(&a_full, 1);
     bar_init(&a_empty, 1);
@@ -379,30 +383,34 @@ __global__ void __launch_bounds__(kExpThreads, 1)
     }
     for (int c = 0; c < 2; ++c) {
       bar_init(c_full + c, 1);
-      bar_init(c_free + c, 4);
+      bar_init(c_free + c, 8);
     }
     bar_init(&drain, 1);
     abort_word = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      su32(&tmem_slot)),
                  "r"(512)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   __syncwarp();
   fence_before();
   __syncthreads();
+  cluster_sync();
   fence_after();
   const uint32_t tmem = tmem_slot;
-  // this CTA's run of (row tile, head) pairs, head fastest
+  // this pair's run of (row tile, head) pairs, head fastest
   const int rows = min(a.tokens, __ldg(a.total));
-  const int64_t pairs = static_cast<int64_t>((max(rows, 0) + 127) / 128) * a.heads;
-  const int64_t f0 = pairs * blockIdx.x / gridDim.x, f1 = pairs * (blockIdx.x + 1) / gridDim.x;
+  const int64_t pairs = static_cast<int64_t>((max(rows, 0) + 255) / 256) * a.heads;
+  const int64_t me = blockIdx.x / 2, of = gridDim.x / 2;
+  const int64_t f0 = pairs * me / of, f1 = pairs * (me + 1) / of;
   if (warp == 0) {
     if (lane == 0) {
+      // the leader's barriers count the bytes of both CTAs
+      const uint32_t a_bar = on_leader(&a_full);
       bool alive = true;
       uint32_t x = 0, tiles = 0;
       int tile = -1;
@@ -412,29 +420,31 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           if (!(alive = bar_wait(&a_empty, (tiles & 1u) ^ 1u, abort_flag, a))) break;
           tile = t;
           ++tiles;
-          bar_expect_tx(&a_full, kExpA);
+          if (rank == 0) bar_expect_tx(&a_full, 2 * kExpA);
           // (the latents come from the kernel in front of this one)
           if (tiles == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
           for (int k = 0; k < 8; ++k)
-            tma_load3(su32(smem + k * 16384), &ta, k * 64, 0, t * 128, &a_full);
+            tma_load3_pair(su32(smem + k * 16384), &ta, k * 64, 0, t * 256 + rank * 128, a_bar);
         }
         for (int k = 0; k < 8; ++k, ++x) {
           const uint32_t s = x % kExpStages;
           if (!(alive = bar_wait(empty + s, ((x / kExpStages) & 1u) ^ 1u, abort_flag, a))) break;
-          bar_expect_tx(full + s, kExpB);
-          tma_load3(su32(ring + s * kExpB), &tk, k * 64, 0, h, full + s);
-          tma_load3(su32(ring + s * kExpB + 16384), &tv, k * 64, 0, h, full + s);
+          if (rank == 0) bar_expect_tx(full + s, 2 * kExpB);
+          tma_load3_pair(su32(ring + s * kExpB), rank ? &tv : &tk, k * 64, 0, h, on_leader(full + s));
         }
       }
-      if (!alive || *abort_flag) {  // every box issued must have landed before the CTA can exit
-        if (tiles) bar_drain(&a_full, (tiles - 1) & 1u);
-        for (uint32_t y = x > kExpStages ? x - kExpStages : 0u; y < x; ++y)
-          bar_drain(full + y % kExpStages, (y / kExpStages) & 1u);
+      // Every box issued has landed before the CTA exits: its MMAs have read it.
+      // After a timeout the leader's barriers cannot tell this CTA, so it waits
+      // out the time that any load takes.
+      if (!alive || *abort_flag) {
+        const uint64_t t0 = global_ns();
+        while (global_ns() - t0 < 1000000ull) {
+        }
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id = idesc(1u, 0, 256);
+    if (lane == 0 && rank == 0) {
+      const uint32_t id = idesc(1u, 0, 256) + ((128u >> 4) << 24);  // M = 256
       const uint64_t ad = sdesc(su32(smem), 16, 1024), bd = sdesc(su32(ring), 16, 1024);
       bool alive = true;
       uint32_t x = 0, tiles = 0, n = 0;
@@ -455,57 +465,72 @@ __global__ void __launch_bounds__(kExpThreads, 1)
           const uint64_t ak = ad + k * 1024, bk = bd + s * (kExpB / 16);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            mma<false>(tmem + c * 256, ak + kk * 2, bk + kk * 2, id, (k | kk) != 0);
-          mma_commit(empty + s);
+            mma2(tmem + c * 256, ak + kk * 2, bk + kk * 2, id, (k | kk) != 0);
+          mma_commit2(empty + s);
         }
         if (!alive) break;
-        mma_commit(c_full + c);
-        if (f + 1 == f1 || static_cast<int>((f + 1) / a.heads) != tile) mma_commit(&a_empty);
+        mma_commit2(c_full + c);
+        if (f + 1 == f1 || static_cast<int>((f + 1) / a.heads) != tile) mma_commit2(&a_empty);
       }
-      mma_commit(&drain);
-      bar_drain(&drain, 0);
+      // nothing issued may still run when either CTA releases its TMEM
+      mma_commit2(&drain);
     }
+    if (lane == 0) bar_drain(&drain, 0);
   } else {
     const int quad = warp & 3;
     uint32_t n = 0;
     for (int64_t f = f0; f < f1; ++f, ++n) {
       const int h = static_cast<int>(f % a.heads);
-      const int64_t t = (f / a.heads) * 128 + quad * 32 + lane;
+      const int64_t t0 = (f / a.heads) * 256 + rank * 128 + quad * 32;  // this warp's rows
       const uint32_t c = n & 1u;
       const bool ok = bar_wait(c_full + c, (n >> 1) & 1u, abort_flag, a);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
       const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c * 256;
-      const int64_t o = t * a.o_row + h * a.o_head;
+      // 64 columns at a time through shared memory (16-byte pieces exchanged by
+      // the row's low bits), so that a store writes 128 bytes of a row: a row
+      // per lane, straight from the registers, wrote 16 and took twice the MMAs' time
+      uint8_t* mine = ring + kExpStages * kExpB + quad * 4096;
 #pragma unroll
-      for (int col = 0; col < 256; col += 32) {
-        uint32_t v[32];
+      for (int col = 0; col < 256; col += 64) {
         __syncwarp();
-        tmem_ld32(src + col, v);
-        tmem_wait_ld<32>(v);
-        if (t < rows) {
-          uint4* dst = reinterpret_cast<uint4*>((col < kNope ? a.k : a.v) + o + col % kNope);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t v[32];
+          tmem_ld32(src + col + half * 32, v);
+          tmem_wait_ld<32>(v);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             uint32_t w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               w[e] = bf16x2(__uint_as_float(v[p * 8 + 2 * e]), __uint_as_float(v[p * 8 + 2 * e + 1]));
-            dst[p] = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(mine + sw128(lane, half * 64 + p * 16)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
+        }
+        __syncwarp();
+        __nv_bfloat16* out = (col < kNope ? a.k : a.v) + h * a.o_head + col % kNope + (lane & 7) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 4 + (lane >> 3);
+          if (t0 + r < rows)
+            *reinterpret_cast<uint4*>(out + (t0 + r) * a.o_row) =
+                *reinterpret_cast<const uint4*>(mine + sw128(r, (lane & 7) * 16));
         }
       }
       __syncwarp();
       fence_before();
-      if (lane == 0) bar_arrive(c_free + c);
+      if (lane == 0) bar_arrive_at(on_leader(c_free + c));
     }
   }
   __syncwarp();
   fence_before();
   __syncthreads();
+  cluster_sync();  // the pair's barriers and shared memory are used until here
   fence_after();
   if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
                  : "memory");
 }
 
@@ -650,12 +675,13 @@ extern "C" int pda_mla_expand(const pda_plan_t* plan, const void* k_pages,
     cudaGetLastError();
     return PDA_ERR_CUDA;
   }
-  const int64_t pairs = static_cast<int64_t>((tokens + 127) / 128) * e.heads;
+  const int64_t pairs = static_cast<int64_t>((tokens + 255) / 256) * e.heads;
+  const int64_t clusters = plan->num_sms / 2 < 1 ? 1 : plan->num_sms / 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs < plan->num_sms ? pairs : plan->num_sms));
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (pairs < clusters ? pairs : clusters)));
   cfg.blockDim = dim3(kExpThreads);
   cfg.dynamicSmemBytes = kExpSmem;
   cfg.stream = s;
