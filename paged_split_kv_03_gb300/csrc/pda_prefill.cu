@@ -133,7 +133,7 @@ struct Item {
 
 struct Shared {
   uint64_t q_full[2], q_empty[2], full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2],
-      o_free[2], item_full[kItems], item_empty[kItems], v_tail, drain;
+      o_free[2], item_full[kItems], item_empty[kItems], landed[kRing], drain;
   uint32_t tmem;
   int abort_flag;
   Item items[kItems];
@@ -183,7 +183,8 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
   const uint32_t ring_addr = su32(ring);
   ItemReader reader(sh);
   Item it{};
-  uint32_t x = 0, tails = 0, nq0 = 0, nq1 = 0;  // ring unit, ragged last tiles, Q tiles
+  uint32_t x = 0, nq0 = 0, nq1 = 0;  // ring unit, Q tiles
+  uint32_t used = 0u, parity = 0u;   // `landed`: places used so far, uses of each mod 2
   bool alive = true;
   auto dst = [&](uint32_t unit) { return ring_addr + unit % kRing * kUnit; };
   auto place = [&](uint32_t unit) {
@@ -213,13 +214,14 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
       }
       if (j == lo) load_q(1);
       for (int c = 0; c < kUnitsV && alive && place(x); ++c, ++x) {
-        // the last tile's V lands for the clearing warp, which passes it on
-        uint64_t* bar = j == tail ? &sh->v_tail : sh->full + x % kRing;
-        if (j != tail) {
-          bar_expect_tx(bar, kUnit);
-        } else if (c == 0) {
-          bar_expect_tx(bar, kUnitsV * kUnit);
-          ++tails;
+        // the last tile's V lands for the clearing warp, which passes it on (a
+        // barrier per place: two short items' last tiles may be under way at once)
+        const uint32_t slot = x % kRing;
+        uint64_t* bar = j == tail ? sh->landed + slot : sh->full + slot;
+        bar_expect_tx(bar, kUnit);
+        if (j == tail) {
+          used |= 1u << slot;
+          parity ^= 1u << slot;
         }
         for (int d = 0; d < 2; ++d)
           tma_load3(dst(x) + d * (kUnit / 2), tv, d * 64, it.head, tok + c * 64, bar);
@@ -228,7 +230,8 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
   }
   // every box issued must have landed before the CTA can exit
   if (!alive || *abort_flag) {
-    if (tails) bar_drain(&sh->v_tail, (tails - 1) & 1u);
+    for (uint32_t s = 0; s < kRing; ++s)
+      if (used >> s & 1u) bar_drain(sh->landed + s, (parity >> s & 1u) ^ 1u);
     for (uint32_t k = x > kRing ? x - kRing : 0u; k < x; ++k)
       bar_drain(sh->full + k % kRing, (k / kRing) & 1u);
     if (nq0) bar_drain(sh->q_full, (nq0 - 1) & 1u);
@@ -328,15 +331,18 @@ __device__ void clear_role(const PrefillArgs& a, Shared* sh, uint8_t* ring) {
   const int lane = threadIdx.x & 31;
   ItemReader reader(sh);
   Item it{};
-  uint32_t t = 0, tails = 0;  // key tiles in front of the item
+  uint32_t t = 0, parity = 0u;  // key tiles in front of the item; uses of `landed` mod 2
   while (reader.next_warp(it, a)) {
     const int lo = min(it.lo0, it.lo1), hi = max(it.hi0, it.hi1);
     const int tail = it.keys % kKeys ? it.keys / kKeys : -1;
     if (tail >= lo && tail < hi) {
-      const bool ok = bar_wait(&sh->v_tail, tails & 1u, &sh->abort_flag, a);
-      if (!__all_sync(0xffffffffu, ok)) return;
-      ++tails;
       const uint32_t x = (t + static_cast<uint32_t>(tail - lo)) * kUnitsTile + kUnitsK;
+      for (int c = 0; c < kUnitsV; ++c) {
+        const uint32_t slot = (x + c) % kRing;
+        const bool ok = bar_wait(sh->landed + slot, parity >> slot & 1u, &sh->abort_flag, a);
+        if (!__all_sync(0xffffffffu, ok)) return;
+        parity ^= 1u << slot;
+      }
       for (int r = it.keys % kKeys; r < kKeys; r += 2) {
         // two rows x 16 pieces of 16 bytes (two 64-channel atoms) a step
         const int row = r + (lane >> 4), piece = lane & 15;
@@ -663,12 +669,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int u = 0; u < kRing; ++u) {
       bar_init(sh->full + u, 1);
       bar_init(sh->empty + u, 1);
+      bar_init(sh->landed + u, 1);
     }
     for (int s = 0; s < kItems; ++s) {
       bar_init(sh->item_full + s, 1);
       bar_init(sh->item_empty + s, kReaders);
     }
-    bar_init(&sh->v_tail, 1);
     bar_init(&sh->drain, 1);
     sh->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -772,7 +778,10 @@ extern "C" int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t to
   if (!plan || !out_plan) return PDA_ERR_NULL;
   if (plan->magic != PDA_PLAN_MAGIC) return PDA_ERR_PLAN;
   if (plan->head_dim != pda::kQDim + 384 || plan->num_kv_heads != 1) return PDA_ERR_UNSUPPORTED;
-  if (rows < 1 || tokens < 1 || plan->batch > pda::kMaxBatch) return PDA_ERR_INVALID;
+  // (token and row numbers of whole tiles stay int32)
+  if (rows < 1 || tokens < 1 || rows > INT_MAX - 512 || tokens > INT_MAX - 512 ||
+      plan->batch > pda::kMaxBatch)
+    return PDA_ERR_INVALID;
   pda_prefill_plan_t p;
   std::memset(&p, 0, sizeof p);
   p.magic = PDA_PREFILL_MAGIC;

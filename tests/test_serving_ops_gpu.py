@@ -533,6 +533,7 @@ PREFILL = {
     "chunk": ([(40, 700), (130, 1000), (300, 301)], 4),
     "decode_like": ([(1, 1500), (2, 900), (1, 1), (8, 64)], 16),
     "one_row_long": ([(1, 5000)], 2),
+    "short_items": ([(1 + r % 7, 8 + (r * 37) % 119) for r in range(60)], 40),
     "many": ([(r % 19, r % 19 + r * 3) for r in range(40)], 2),
 }
 
