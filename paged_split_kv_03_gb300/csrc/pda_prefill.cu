@@ -516,11 +516,11 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
           uint32_t s[32];
           tmem_ld32(t_s + c, s);
           tmem_wait_ld<32>(s);
+          const int last = last_key - k0 - c, first = first_key - k0 - c;
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
             const float x = __uint_as_float(s[e]) * sign;
-            s[e] = k0 + c + e > last_key || k0 + c + e < first_key ? 0xff800000u
-                                                                   : __float_as_uint(x);
+            s[e] = e > last || e < first ? 0xff800000u : __float_as_uint(x);
           }
           tmem_st32(t_s + c, s);
         }
@@ -593,6 +593,8 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
     const float inv = l > 0.f ? 1.f / l : l;  // no key: 0; NaN stays
     const int64_t at = static_cast<int64_t>(it.row0 + row) * a.heads + it.head;
     const bool live = r < tile_rows;
+    const bool final = it.split < 0;
+    float* part = a.part_o + static_cast<int64_t>(final ? 0 : it.split) * a.rows * a.heads * kDv;
 #pragma unroll 1
     for (int c = 0; c < kDv; c += 32) {
       uint32_t o[32];
@@ -604,29 +606,54 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = 0u;
       }
-      if (!live) continue;
-      if (it.split < 0) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + at * kDv + c);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          uint32_t b[4];
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+      // Four lanes exchange 16-byte pieces, so that a store writes 64 bytes of
+      // each of eight rows and not 16 of thirty-two (a quarter of the accesses).
+      auto put = [&](const uint32_t* w, char* base, int64_t row_bytes) {
+        uint32_t v[16];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const __nv_bfloat162 h =
-                __floats2bfloat162_rn(__uint_as_float(o[v * 8 + e * 2]) * inv,
-                                      __uint_as_float(o[v * 8 + e * 2 + 1]) * inv);
-            b[e] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int e = 0; e < 16; ++e) v[e] = w[e];
+#pragma unroll
+        for (int d = 1; d <= 2; d <<= 1) {
+          const bool hi = (lane & d) != 0;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            if (p & d) continue;  // piece p and piece p + d
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t& keep = v[p * 4 + e];
+              uint32_t& give = v[(p + d) * 4 + e];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? keep : give, d);
+              if (hi) keep = got;
+              else give = got;
+            }
           }
-          dst[v] = make_uint4(b[0], b[1], b[2], b[3]);
         }
-      } else {
-        float4* dst = reinterpret_cast<float4*>(
-            a.part_o + (static_cast<int64_t>(it.split) * a.rows * a.heads + at) * kDv + c);
+        // piece k is now this lane's piece (lane & 3) of row 4 (lane / 4) + k
 #pragma unroll
-        for (int v = 0; v < 8; ++v)
-          dst[v] = make_float4(__uint_as_float(o[v * 4]) * inv, __uint_as_float(o[v * 4 + 1]) * inv,
-                               __uint_as_float(o[v * 4 + 2]) * inv,
-                               __uint_as_float(o[v * 4 + 3]) * inv);
+        for (int k = 0; k < 4; ++k) {
+          const int rr = quad * 32 + (lane & ~3) + k;
+          if (rr < tile_rows)
+            *reinterpret_cast<uint4*>(base + rr * row_bytes + (lane & 3) * 16) =
+                make_uint4(v[k * 4], v[k * 4 + 1], v[k * 4 + 2], v[k * 4 + 3]);
+        }
+      };
+      const int64_t at0 = static_cast<int64_t>(it.row0 + g * kRowsTile) * a.heads + it.head;
+      if (final) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const __nv_bfloat162 h =
+              __floats2bfloat162_rn(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          w[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        put(w, reinterpret_cast<char*>(a.out + at0 * kDv + c), static_cast<int64_t>(a.heads) * kDv * 2);
+      } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          put(o + h * 16, reinterpret_cast<char*>(part + at0 * kDv + c + h * 16),
+              static_cast<int64_t>(a.heads) * kDv * 4);
       }
     }
     __syncwarp();
