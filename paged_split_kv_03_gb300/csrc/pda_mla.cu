@@ -176,6 +176,18 @@ __global__ void __launch_bounds__(192)
   if (a.num_rows) rows = min(rows, __ldg(a.num_rows));
   const int n0 = blockIdx.x * N, h = blockIdx.y, t0 = blockIdx.z * 128;
   if (t0 >= rows) return;
+  auto load = [&](int k) {
+    const int s = k % C::kStages;
+    uint8_t* st = smem + s * C::kStage;
+    bar_expect_tx(full + s, C::kStage);
+    tma_load3(su32(st), &ta, k * 64, h, t0, full + s);
+    if constexpr (OP == kAbsorb) {  // 64 channels of K x N columns, 64 columns an atom
+      for (int c = 0; c < N / 64; ++c)
+        tma_load3(su32(st + C::kABytes + c * 8192), &tb, n0 + c * 64, k * 64, h, full + s);
+    } else {
+      tma_load3(su32(st + C::kABytes), &tb, k * 64, n0, h, full + s);
+    }
+  };
   if (tid == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       bar_init(full + s, 1);
@@ -184,6 +196,8 @@ __global__ void __launch_bounds__(192)
     bar_init(&done, 1);
     abort_word = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    // the first loads are on their way while TMEM is allocated
+    for (int k = 0; k < C::kStages; ++k) load(k);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -200,26 +214,14 @@ __global__ void __launch_bounds__(192)
   if (warp == 0) {
     if (lane == 0) {
       bool alive = true;
-      int issued = 0;
-      for (int k = 0; k < C::kBlocks && alive; ++k) {
-        const int s = k % C::kStages;
-        if (k >= C::kStages)
-          alive = bar_wait(empty + s, ((k / C::kStages) - 1) & 1u, abort_flag, a);
-        if (!alive) break;
-        uint8_t* st = smem + s * C::kStage;
-        bar_expect_tx(full + s, C::kStage);
-        tma_load3(su32(st), &ta, k * 64, h, t0, full + s);
-        if constexpr (OP == kAbsorb) {  // 64 channels of K x N columns, 64 columns an atom
-          for (int c = 0; c < N / 64; ++c)
-            tma_load3(su32(st + C::kABytes + c * 8192), &tb, n0 + c * 64, k * 64, h, full + s);
-        } else {
-          tma_load3(su32(st + C::kABytes), &tb, k * 64, n0, h, full + s);
-        }
-        ++issued;
+      int k = C::kStages;
+      for (; k < C::kBlocks; ++k) {
+        if (!(alive = bar_wait(empty + k % C::kStages, ((k / C::kStages) - 1) & 1u, abort_flag, a))) break;
+        load(k);
       }
-      if (!alive)  // every box issued must have landed before the CTA can exit
-        for (int k = max(0, issued - C::kStages); k < issued; ++k)
-          bar_drain(full + k % C::kStages, (k / C::kStages) & 1u);
+      if (!alive || *abort_flag)  // every box issued must have landed before the CTA can exit
+        for (int i = k - C::kStages; i < k; ++i)
+          bar_drain(full + i % C::kStages, (i / C::kStages) & 1u);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -244,15 +246,25 @@ __global__ void __launch_bounds__(192)
     }
   } else {
     const int quad = warp & 3;
-    if (OP == kAbsorb && n0 == 0) {  // the rope channels of this warp's rows
-      for (int r = lane >> 3; r < 32; r += 4) {
-        const int t = t0 + quad * 32 + r;
-        if (t >= rows) break;
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(a.q + t * a.q_row + h * a.q_head + kNope) +
-                              (lane & 7));
-        const int64_t o = (static_cast<int64_t>(t) * a.heads + h) * kLatRow + kLat + (lane & 7) * 8;
+    if constexpr (OP == kAbsorb) {
+      // the rope channels pass through: each column block takes its share of the
+      // rows, all loads before the first store
+      constexpr int kShare = 8 * N / kLat;  // rows per group of eight lanes
+      uint4 v[kShare];
+      int t[kShare];
+#pragma unroll
+      for (int i = 0; i < kShare; ++i) {
+        t[i] = t0 + quad * 32 + (blockIdx.x * kShare + i) * 4 + (lane >> 3);
+        if (t[i] < rows)
+          v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + t[i] * a.q_row + h * a.q_head + kNope) +
+                       (lane & 7));
+      }
+#pragma unroll
+      for (int i = 0; i < kShare; ++i) {
+        if (t[i] >= rows) continue;
+        const int64_t o = (static_cast<int64_t>(t[i]) * a.heads + h) * kLatRow + kLat + (lane & 7) * 8;
         if constexpr (E4M3) {
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           uint32_t c[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -261,7 +273,7 @@ __global__ void __launch_bounds__(192)
           *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + o) =
               make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
         } else {
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o) = v;
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o) = v[i];
         }
       }
       __syncwarp();
