@@ -246,7 +246,8 @@ struct SlotCfg {
   static constexpr int kChunks = D / 8;                          // of 8 values
   static constexpr int kLanes = kChunks < 32 ? kChunks : 32;     // lanes per vector
   static constexpr int kIters = (kChunks + kLanes - 1) / kLanes; // chunks per lane
-  static constexpr int kPerWarp = 32 / kLanes;                   // vectors per warp
+  static constexpr int kPerWarp = 32 / kLanes;                   // vectors per warp and round
+  static constexpr int kUnroll = D <= 128 ? 2 : 1;               // rounds, loads in flight
 };
 
 __device__ __forceinline__ void unpack8(uint4 w, float* x) {
@@ -338,35 +339,49 @@ __device__ __forceinline__ void put_slot(const uint4* w, bool ok, uint8_t* pages
 template <int D, int MODE, bool kTwo>
 __global__ void __launch_bounds__(256) append_slots(const __grid_constant__ SlotArgs a) {
   using C = SlotCfg<D>;
+  constexpr int kU = C::kUnroll;
   const int lane = threadIdx.x & 31, sub = lane % C::kLanes;
-  const int64_t item =
-      ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * C::kPerWarp + lane / C::kLanes;
-  const int64_t i = item / a.hkv;
-  const int h = static_cast<int>(item % a.hkv);
+  const uint32_t hkv = a.hkv;
   int rows = a.rows;
   if (a.num_rows) rows = min(rows, __ldg(a.num_rows));
-  bool ok = i < rows;
-  const int64_t slot = ok ? __ldg(a.slot_map + i) : -1;
-  if (ok && (slot < -1 || slot >= a.num_slots) && sub == 0) atomicOr(a.status, PDA_STATUS_PAGE_OOB);
-  ok = slot >= 0 && slot < a.num_slots;
-  if (!__any_sync(0xffffffffu, ok)) return;
-  uint4 wk[C::kIters], wv[C::kIters];
+  // kU vectors a lane group, neighbours in memory side by side in a warp; every
+  // load is issued before the first value is used
+  const uint32_t first =
+      (blockIdx.x * 8 + (threadIdx.x >> 5)) * (C::kPerWarp * kU) + lane / C::kLanes;
+  int64_t slot[kU];
+  uint32_t h[kU];
+  bool ok[kU];
+  uint4 wk[kU][C::kIters], wv[kU][C::kIters];
 #pragma unroll
-  for (int k = 0; k < C::kIters; ++k) {
-    wk[k] = wv[k] = make_uint4(0, 0, 0, 0);
-    if (ok && sub + 32 * k < C::kChunks) {
-      wk[k] = __ldg(reinterpret_cast<const uint4*>(a.k_new + i * a.k_stride + h * D) + sub + 32 * k);
-      if constexpr (kTwo)
-        wv[k] = __ldg(reinterpret_cast<const uint4*>(a.v_new + i * a.v_stride + h * D) + sub + 32 * k);
+  for (int u = 0; u < kU; ++u) {
+    const uint32_t item = first + u * C::kPerWarp, i = item / hkv;
+    h[u] = item - i * hkv;
+    ok[u] = static_cast<int64_t>(i) < rows;
+    slot[u] = ok[u] ? __ldg(a.slot_map + i) : -1;
+#pragma unroll
+    for (int k = 0; k < C::kIters; ++k) {
+      wk[u][k] = wv[u][k] = make_uint4(0, 0, 0, 0);
+      if (ok[u] && sub + 32 * k < C::kChunks) {
+        wk[u][k] = __ldg(reinterpret_cast<const uint4*>(a.k_new + i * a.k_stride + h[u] * D) + sub + 32 * k);
+        if constexpr (kTwo)
+          wv[u][k] = __ldg(reinterpret_cast<const uint4*>(a.v_new + i * a.v_stride + h[u] * D) + sub + 32 * k);
+      }
     }
   }
-  const int64_t page = slot >> a.page_shift;
-  const int64_t off = page * a.sp + (slot - (page << a.page_shift)) * a.st + h * a.sh;
-  const int64_t sidx = (slot * a.hkv + h) * (MODE == 5 ? 4 : 1);
-  constexpr bool kOwnScale = MODE == 2 || MODE == 4 || MODE == 5;
-  put_slot<D, MODE>(wk, ok, a.k_pages, off, a.k_scale, a.k_scale + (kOwnScale ? sidx : 0), sub);
-  if constexpr (kTwo)
-    put_slot<D, MODE>(wv, ok, a.v_pages, off, a.v_scale, a.v_scale + (kOwnScale ? sidx : 0), sub);
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    if (ok[u] && (slot[u] < -1 || slot[u] >= a.num_slots) && sub == 0)
+      atomicOr(a.status, PDA_STATUS_PAGE_OOB);
+    const bool put = slot[u] >= 0 && slot[u] < a.num_slots;
+    if (!__any_sync(0xffffffffu, put)) continue;
+    const int64_t page = slot[u] >> a.page_shift;
+    const int64_t off = page * a.sp + (slot[u] - (page << a.page_shift)) * a.st + h[u] * a.sh;
+    const int64_t sidx = (slot[u] * hkv + h[u]) * (MODE == 5 ? 4 : 1);
+    constexpr bool kOwnScale = MODE == 2 || MODE == 4 || MODE == 5;
+    put_slot<D, MODE>(wk[u], put, a.k_pages, off, a.k_scale, a.k_scale + (kOwnScale ? sidx : 0), sub);
+    if constexpr (kTwo)
+      put_slot<D, MODE>(wv[u], put, a.v_pages, off, a.v_scale, a.v_scale + (kOwnScale ? sidx : 0), sub);
+  }
 }
 
 using SlotFn = void (*)(SlotArgs);
@@ -517,9 +532,10 @@ extern "C" int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64
                    : D == 256 ? pda::pick_slot_mode<256>(mode)
                    : D == 512 ? pda::pick_slot_mode<512>(mode)
                               : pda::pick_slot_mode<576>(mode);
-  const int per_cta = 8 * (D == 64 ? 4 : D == 128 ? 2 : 1);
+  const int per_cta = 8 * (D == 64 ? 8 : D == 128 ? 4 : 1);  // kPerWarp * kUnroll vectors a warp
+  // vectors are counted in 32 bits (more of them would not fit the device)
+  if (static_cast<int64_t>(rows) * a.hkv > 0x7fffffffLL) return PDA_ERR_INVALID;
   const int64_t blocks = (static_cast<int64_t>(rows) * a.hkv + per_cta - 1) / per_cta;
-  if (blocks > 0x7fffffffLL) return PDA_ERR_INVALID;
   fn<<<static_cast<unsigned>(blocks), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
   return PDA_OK;

@@ -307,6 +307,45 @@ def test_append_slots_rows(rows):
         assert torch.equal(s.cpu().reshape(4096, 2), wsc)
 
 
+@pytest.mark.parametrize("kind", ["e4m3_tensor", "int8_tensor", "e4m3_token", "int8_token"])
+def test_append_slots_ties(kind):
+    """Quotients at and next to the ties between codes, subnormal codes, zeros of both signs,
+    saturation, infinities and NaN, over scales of every size: each code is that of the fp32
+    quotient."""
+    dec = B.Decoder(cache_plan(kind, 128, 1, 64, 64), device=DEV)
+    g = torch.Generator().manual_seed(1)
+    rows, n = 64, 64 * 128
+    scales = [1.0, 3.0, 0.1, 2.0 ** -20, 7e-39, 1e30, 2.0 ** 126] if "tensor" in kind else [1.0]
+    for s in scales:
+        # codes' midpoints times the scale, in bf16: some quotients hit the tie exactly
+        if "int8" in kind:
+            y = torch.randint(-130, 131, (n,), generator=g).float() + 0.5
+        else:
+            v = torch.arange(256, dtype=torch.uint8).view(ref.E4M3).float()
+            v = v[torch.isfinite(v)].unique()
+            mid = (v[1:] + v[:-1]) / 2
+            y = mid[torch.randint(0, mid.numel(), (n,), generator=g)]
+        x = (y.double() * s).float().to(torch.bfloat16)
+        x[::7] = torch.randn(x[::7].shape, generator=g).to(torch.bfloat16) * s
+        if "tensor" in kind:
+            x[5], x[6], x[7], x[8] = math.inf, -math.inf, 0.0, -0.0
+            if "int8" not in kind:
+                x[9] = math.nan
+        x = x.reshape(rows, 1, 128)
+        slots = torch.randperm(64 * 64, generator=g)[:rows]
+        cache = [torch.zeros(64, 64, 1, 128, dtype=torch.uint8, device=DEV) for _ in range(2)]
+        sc = [torch.full((64, 64, 1), -1.0, device=DEV) if "token" in kind else
+              torch.tensor([s], device=DEV) for _ in range(2)]
+        B.pda_append_slots(dec.plan, x.to(DEV), x.to(DEV), slots.to(DEV), None, *cache, *sc, dec.scratch)
+        assert dec.status() == 0
+        want = torch.zeros(4096, 1, 128, dtype=torch.uint8)
+        want[slots] = stored(x, kind, None if "token" in kind else torch.tensor(s))[0]
+        for c in cache:
+            got = c.cpu().reshape(4096, 1, 128)
+            both_nan = (got & 0x7F == 0x7F) & (want & 0x7F == 0x7F) if "e4m3" in kind else False
+            assert bool(((got == want) | both_nan).all()), (kind, s)
+
+
 # ------------------------------------------------------------ absorbed form
 
 def weights(g, heads, split=False):
