@@ -172,12 +172,18 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+_RAW_STREAM = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the handle alone: a torch Stream object costs ten times as much
-        from torch._C import _cuda_getCurrentRawStream
-        from torch.cuda import current_device
-        return _cuda_getCurrentRawStream(current_device())
+        global _RAW_STREAM
+        if _RAW_STREAM is None:
+            # the handle alone: a torch Stream object costs ten times as much
+            from torch._C import _cuda_getCurrentRawStream
+            from torch.cuda import current_device
+            _RAW_STREAM = _cuda_getCurrentRawStream, current_device
+        return _RAW_STREAM[0](_RAW_STREAM[1]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

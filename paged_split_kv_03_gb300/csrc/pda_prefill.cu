@@ -382,12 +382,18 @@ __device__ void work_role(const PrefillArgs& a, Shared* sh) {
     if (lane == 0 && bits) atomicOr(a.status, bits);
   }
   const int64_t items = total * a.heads * a.splits;
-  // Heads go in groups whose tiles fill the GPU about once, so that their K
-  // and V stay in L2; a group's items from the last tiles (the most keys) to
-  // the first, chunks of a tile side by side. CTAs take items one by one, as
-  // causal tiles differ: in steps of the grid, 4096 x 128 heads took a third
-  // longer.
-  const int64_t group = max(static_cast<int64_t>(1), (gridDim.x + total - 1) / max(total, static_cast<int64_t>(1)));
+  // Heads go in groups, so that their K and V stay in L2; a group's items from the
+  // last tiles (the most keys) to the first, chunks of a tile side by side. CTAs
+  // take items one by one, as causal tiles differ: in steps of the grid, 4096 x
+  // 128 heads took a third longer. A group is worth `rounds` items a CTA: three
+  // where items differ (4096 causal rows x 128 heads, one / two / three / four / eight
+  // rounds: 559 / 545 / 521 / 534 / 517 us), one where they do not and L2 is all that
+  // counts (4096 x 4096 keys, no mask: 837 / 847 / 856 / 864 / 918 us).
+  const int64_t rounds = a.causal ? 3 : 1;
+  const int64_t tiles = max(total, static_cast<int64_t>(1));
+  const int64_t wish = max(static_cast<int64_t>(1), rounds * gridDim.x / (tiles * a.splits));
+  const int64_t groups = max(static_cast<int64_t>(1), a.heads / wish);
+  const int64_t group = (a.heads + groups - 1) / groups;
   uint32_t n = 0;
   int64_t x = blockIdx.x;
   auto take = [&]() {
@@ -510,7 +516,8 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
       fence_after();
       const int k0 = j * kKeys;
       if (k0 + kKeys - 1 > all_hi || k0 < all_lo || sign != 1.f) {
-        // some row does not see the whole tile: mask S where it stands
+        // some row does not see the whole tile: mask S where it stands (masking
+        // the registers costs the loop more than the two TMEM trips cost here)
 #pragma unroll 1
         for (int c = 0; c < kKeys; c += 32) {
           uint32_t s[32];
