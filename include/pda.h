@@ -305,8 +305,8 @@ int pda_decode_static(const pda_plan_t* plan, const void* q, const void* k_pages
  * its absorbed and its expanded form. The pages have no counterpart of these
  * calls; they make what pda_decode reads and use what it writes. Like
  * pda_decode they allocate nothing, never synchronise and enqueue work only
- * on `stream` (current device = the plan's device), so they can be captured
- * in a CUDA graph; every pointer is borrowed device memory unless it says
+ * on `stream` (the plan's device must be the current one: PDA_ERR_INVALID),
+ * so they can be captured in a CUDA graph; every pointer is borrowed device memory unless it says
  * otherwise. split_scratch: the plan's scratch, of which they use only the
  * status word (pda_mla_prefill: its own scratch). No rows (or tokens): PDA_OK,
  * nothing launched, the row pointers may be NULL. Index arrays hold int32
@@ -371,7 +371,7 @@ int pda_build_tables(const pda_plan_t* plan, const pda_tables* tables, void* spl
  *   slot_map      int64 [rows]; -1 = skip the row; other values outside
  *                 [0, num_pages * P) skip it and set PDA_STATUS_PAGE_OOB. Two
  *                 rows of one slot leave a mix of both there.
- *   rows          rows of k_new and slot_map; num_rows, when not NULL, is one
+ *   rows          rows of k_new and slot_map (rows x Hkv below 2^31); num_rows, when not NULL, is one
  *                 device int32: only rows [0, min(rows, *num_rows)) are taken
  *                 (&qo_indptr[batch] in a captured step) */
 int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64_t k_stride,
@@ -450,7 +450,8 @@ typedef struct {
 #define PDA_PREFILL_MAGIC 0x50444631u /* "PDF1" */
 
 /* Plan prefills of up to `rows` query rows and `tokens` keys in all, for the
- * heads, batch, max_kv_len and device of `plan` (an MLA plan); both >= 1. Host-only.
+ * heads, batch (at most 8192), max_kv_len and device of `plan` (an MLA plan); both
+ * >= 1. Host-only.
  * Writes *out_plan and, when non-NULL, *scratch_bytes (>= 256): device bytes
  * that the caller allocates as for pda_plan (256-byte aligned, zeroed once);
  * pda_get_status reads and pda_reset_status clears its status word. Calls that

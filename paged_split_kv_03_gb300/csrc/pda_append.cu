@@ -502,6 +502,7 @@ extern "C" int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64
   if (!mla && (!a16(v_new) || !a16(v_pages) || v_stride % 8)) return PDA_ERR_ALIGNMENT;
   if (codes && (rec ? !a16(k_scale) : !a4(k_scale) || (!mla && !a4(v_scale))))
     return PDA_ERR_ALIGNMENT;
+  if (!pda::on_device(plan->device)) return PDA_ERR_INVALID;
 
   pda::SlotArgs a;
   std::memset(&a, 0, sizeof a);

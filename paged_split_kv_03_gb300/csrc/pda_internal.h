@@ -122,6 +122,16 @@ int check_decode_args(const pda_plan_t* plan, const void* q, const void* k_pages
                       const float* k_scale, const float* v_scale, const void* out,
                       const float* lse);
 
+// Whether `device` is the current one.
+inline bool on_device(int device) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return dev == device;
+}
+
 // Device address of the library's built-in split scratch (the array behind
 // pda_decode_static) on the current device, which must be `device`; looked
 // up afresh unless `s` is capturing a graph (then the last lookup is used).

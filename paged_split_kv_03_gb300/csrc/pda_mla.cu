@@ -348,15 +348,17 @@ int launch_product(const ProductArgs& a, const CUtensorMap& ta, const CUtensorMa
 // ------------------------------------------------------- keys and values
 //
 // [k | v]_h[t] = [W_UK; W_UV]_h c_t. Bound: the tensor cores (8192 tokens x 128
-// heads: 275 GFLOP, 147 us at the measured rate; 589 MB, 87 us), if operands keep
-// up: a CTA pair takes 256 tokens, M = 256 over both SMs, N = 256 (a head's k
-// and v). Each CTA keeps its 128 latents (128 KB) in shared memory while half of
-// the head's weights (CTA 0 W_UK, CTA 1 W_UV) stream past through a ring of five 16
-// KB stages: 32 bytes a cycle from L2 and 2000 cycles from a load to its use. With
-// one CTA and all of the weights it was 64 bytes a cycle and 1000 cycles, less
-// than TMA takes: 289 us, 950 TFLOP/s. A pair takes an equal run of (row tile,
-// head) pairs; two accumulators of 256 columns let a head's rows be written
-// while the next one's MMAs run.
+// heads: 275 GFLOP, 147 us at the measured rate) and writing k and v (537 MB, 134
+// us at the 4.0 TB/s that a plain fill reaches) alike; it takes 210 us, 141
+// without the stores. So the operands must not cost anything on top: a CTA pair
+// takes 256 tokens, M = 256 over both SMs, N = 256 (a head's k and v). Each CTA
+// keeps its 128 latents (128 KB) in shared memory while half of the head's weights
+// (CTA 0 W_UK, CTA 1 W_UV) stream past through a ring of five 16 KB stages: 32
+// bytes a cycle from L2 and 2000 cycles from a load to its use. With one CTA and
+// all of the weights it was 64 bytes a cycle and 1000 cycles, less than TMA takes.
+// A pair takes an equal run of (row tile, head) pairs, head fastest (heads dealt
+// out in groups of 4 to 32: 220 to 244 us); two accumulators of 256 columns let a
+// head's rows be written while the next one's MMAs run.
 
 struct ExpandArgs {
   __nv_bfloat16* k;
@@ -370,9 +372,9 @@ struct ExpandArgs {
 
 constexpr int kExpStages = 5;
 constexpr int kExpA = 8 * 16384, kExpB = 16384;
-constexpr int kExpOut = 4 * 4096;  // 32 rows x 128 bytes a warp
+constexpr int kExpOut = 8 * 2048;  // 32 rows x 64 bytes a warp
 constexpr int kExpSmem = kExpA + kExpStages * kExpB + kExpOut + 1024;
-constexpr int kExpThreads = 192;
+constexpr int kExpThreads = 64 + 8 * 32;  // loads, MMAs, eight warps that write
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
     expand(const __grid_constant__ ExpandArgs a, const __grid_constant__ CUtensorMap ta,
@@ -395,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
     }
     for (int c = 0; c < 2; ++c) {
       bar_init(c_full + c, 1);
-      bar_init(c_free + c, 8);
+      bar_init(c_free + c, 16);
     }
     bar_init(&drain, 1);
     abort_word = 0;
@@ -489,7 +491,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
     }
     if (lane == 0) bar_drain(&drain, 0);
   } else {
-    const int quad = warp & 3;
+    // a warp writes 32 rows of k (warps 2-5) or of v (6-9)
+    const int quad = warp & 3, part = (warp - 2) >> 2;
+    uint8_t* mine = ring + kExpStages * kExpB + (warp - 2) * 2048;
+    auto place = [&](int r, int piece) {  // no two rows of a quarter warp in one bank
+      return reinterpret_cast<uint4*>(mine + r * 64 + ((piece ^ (r >> 1)) & 3) * 16);
+    };
     uint32_t n = 0;
     for (int64_t f = f0; f < f1; ++f, ++n) {
       const int h = static_cast<int>(f % a.heads);
@@ -498,37 +505,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
       const bool ok = bar_wait(c_full + c, (n >> 1) & 1u, abort_flag, a);
       if (!__all_sync(0xffffffffu, ok)) break;
       fence_after();
-      const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c * 256;
-      // 64 columns at a time through shared memory (16-byte pieces exchanged by
-      // the row's low bits), so that a store writes 128 bytes of a row: a row
-      // per lane, straight from the registers, wrote 16 and took twice the MMAs' time
-      uint8_t* mine = ring + kExpStages * kExpB + quad * 4096;
+      const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16) + c * 256 + part * kNope;
+      __nv_bfloat16* out = (part ? a.v : a.k) + h * a.o_head + (lane & 3) * 8;
+      // 32 columns at a time through shared memory, so that a store writes 64
+      // bytes of a row; a row per lane, straight from the registers, wrote 16 (297 us)
 #pragma unroll
-      for (int col = 0; col < 256; col += 64) {
+      for (int col = 0; col < kNope; col += 32) {
+        uint32_t v[32];
+        tmem_ld32(src + col, v);
+        tmem_wait_ld<32>(v);
         __syncwarp();
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t v[32];
-          tmem_ld32(src + col + half * 32, v);
-          tmem_wait_ld<32>(v);
+        for (int p = 0; p < 4; ++p) {
+          uint32_t w[4];
 #pragma unroll
-          for (int p = 0; p < 4; ++p) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = bf16x2(__uint_as_float(v[p * 8 + 2 * e]), __uint_as_float(v[p * 8 + 2 * e + 1]));
-            *reinterpret_cast<uint4*>(mine + sw128(lane, half * 64 + p * 16)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            w[e] = bf16x2(__uint_as_float(v[p * 8 + 2 * e]), __uint_as_float(v[p * 8 + 2 * e + 1]));
+          *place(lane, p) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
-        __nv_bfloat16* out = (col < kNope ? a.k : a.v) + h * a.o_head + col % kNope + (lane & 7) * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 4 + (lane >> 3);
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 8 + (lane >> 2);
           if (t0 + r < rows)
-            *reinterpret_cast<uint4*>(out + (t0 + r) * a.o_row) =
-                *reinterpret_cast<const uint4*>(mine + sw128(r, (lane & 7) * 16));
+            *reinterpret_cast<uint4*>(out + (t0 + r) * a.o_row + col) = *place(r, lane & 3);
         }
       }
       __syncwarp();
@@ -594,6 +594,7 @@ extern "C" int pda_mla_absorb(const pda_plan_t* plan, const void* q, int64_t q_s
   if (!make_map3(&ta, q, kNope, p.heads, rows, q_stride_head, q_stride_row, 64, 1, 128) ||
       !make_map3(&tb, w_uk, kLat, kNope, p.heads, kLat, w_stride_head, 64, 64, 1))
     return PDA_ERR_CUDA;
+  if (!on_device(plan->device)) return PDA_ERR_INVALID;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return e4m3 ? launch_product<kAbsorb, 128, true>(p, ta, tb, s)
               : launch_product<kAbsorb, 128, false>(p, ta, tb, s);
@@ -622,6 +623,7 @@ extern "C" int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const 
   if (!make_map3(&ta, o_lat, kLat, p.heads, rows, kLat, static_cast<int64_t>(p.heads) * kLat, 64, 1, 128) ||
       !make_map3(&tb, w_uv, kLat, kNope, p.heads, kLat, w_stride_head, 64, few ? 32 : 128, 1))
     return PDA_ERR_CUDA;
+  if (!on_device(plan->device)) return PDA_ERR_INVALID;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return few ? launch_product<kProject, 32, false>(p, ta, tb, s)
              : launch_product<kProject, 128, false>(p, ta, tb, s);
@@ -645,6 +647,7 @@ extern "C" int pda_mla_expand(const pda_plan_t* plan, const void* k_pages,
       kv_stride_token % 8 || kv_stride_head % 8 || !a4(page_table) || !a4(kv_indptr) ||
       !a4(tok_indptr) || (rec ? !a16(k_scale) : !a4(k_scale)))
     return PDA_ERR_ALIGNMENT;
+  if (!on_device(plan->device)) return PDA_ERR_INVALID;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   GatherArgs g = {};
   g.pages = static_cast<const uint8_t*>(k_pages);

@@ -47,7 +47,7 @@ namespace {
 constexpr int kNope = 128, kRope = 64, kQDim = kNope + kRope, kDv = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMInit = -1.0e30f;  // before any key: finite, so that ex2(-inf - m) = 0
+constexpr float kMInit = -3.0e38f;  // before any key: finite, so that ex2(-inf - m) = 0
 constexpr float kTh = 8.0f;         // lazy rescale threshold, log2 units
 
 constexpr int kRowsTile = 128;                // rows of one softmax warpgroup
@@ -491,7 +491,7 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
   const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
   const uint32_t t_s = tmem + lanes + g * kKeys, t_o = tmem + lanes + 2 * kKeys + g * kDv;
   // logits in log2 units: s * scale, with the sign (or zero) applied to s first
-  const float sign = a.sm_scale > 0.f ? 1.f : a.sm_scale < 0.f ? -1.f : 0.f;
+  const float sign = a.sm_scale < 0.f ? -1.f : a.sm_scale == 0.f ? 0.f : 1.f;
   const float scale = sign != 0.f ? fabsf(a.sm_scale) * kLog2e : 1.f;
   ItemReader reader(sh);
   Item it{};
@@ -881,6 +881,7 @@ extern "C" int pda_mla_prefill(const pda_prefill_plan_t* plan, const void* q, in
       kv_stride_token % 8 || kv_stride_head % 8 || k_rope_stride % 8)
     return PDA_ERR_ALIGNMENT;
   if (plan->batch == 0) return PDA_OK;
+  if (!on_device(plan->device)) return PDA_ERR_INVALID;
   PrefillArgs a = {};
   a.qo_indptr = qo_indptr;
   a.tok_indptr = tok_indptr;

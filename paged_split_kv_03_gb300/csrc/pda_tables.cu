@@ -300,6 +300,7 @@ extern "C" int pda_build_tables(const pda_plan_t* plan, const pda_tables* tables
       !a4(t.positions) || reinterpret_cast<uintptr_t>(t.slot_map) % 8)
     return PDA_ERR_ALIGNMENT;
   if (plan->batch == 0) return PDA_OK;
+  if (!pda::on_device(plan->device)) return PDA_ERR_INVALID;
 
   pda::TablesArgs a;
   a.t = t;

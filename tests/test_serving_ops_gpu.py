@@ -797,3 +797,97 @@ def test_serving_loop(kind):
         assert bool((out[rows:] == 7).all())
     used = sum(-(-len(h) // page) for h in history)
     assert free[0].item() == pages - used
+
+
+# ------------------------------------------------- offsets that pass 32 bits
+
+def test_append_and_expand_far_pages():
+    """A latent cache of 2^32 elements and more: the last pages are written and read."""
+    g = torch.Generator().manual_seed(2)
+    page, pages = 64, 120000  # 120000 x 64 x 576 elements = 4.4e9
+    dec = B.Decoder(ref.mla_plan(2, page=page, pages=pages), device=DEV)
+    cache = torch.zeros(pages, page, 1, 576, dtype=torch.bfloat16, device=DEV)
+    x = randn(g, 150, 1, 576)
+    slots = torch.tensor([(pages - 1 - i // page) * page + i % page for i in range(150)])
+    B.pda_append_slots(dec.plan, x.to(DEV), None, slots.to(DEV), None, cache, None, None, None,
+                       dec.scratch)
+    latent = torch.zeros(150, 576, dtype=torch.bfloat16, device=DEV)
+    kv = torch.zeros(150, 2, 256, dtype=torch.bfloat16, device=DEV)
+    w_uk, w_uv = weights(g, 2)
+    B.pda_mla_expand(dec.plan, cache, ints([pages - 1, pages - 2, pages - 3]), ints([0, 3]), ints([0, 150]),
+                     None, w_uk, w_uv, latent, kv[..., :128], kv[..., 128:], dec.scratch)
+    assert dec.status() == 0
+    assert torch.equal(latent.cpu(), x[:, 0])
+    assert int(torch.count_nonzero(cache[:100]).item()) == 0
+    y, mag = ref.product(x[:, :, :512].expand(150, 2, 512), w_uk.cpu())
+    mag = mag * ref.sum_bound(512)
+    check(kv[..., :128], y, mag + ref.BF16_HALF * (y.abs() + mag), "k")
+
+
+def test_expand_and_prefill_far_rows():
+    """More than 2^31 elements of k and v: rows and keys at the far end."""
+    heads, page, n = 128, 64, 70000  # 70000 x 128 x 256 elements = 2.3e9
+    pages = -(-n // page)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    dec = B.Decoder(ref.mla_plan(heads, page=page, pages=pages, max_kv=n), device=DEV)
+    cache = torch.randn(pages, page, 1, 576, generator=g, device=DEV).to(torch.bfloat16)
+    w = (torch.randn(heads, 256, 512, generator=g, device=DEV) * 512 ** -0.5).to(torch.bfloat16)
+    latent = torch.zeros(n, 576, dtype=torch.bfloat16, device=DEV)
+    kv = torch.zeros(n, heads, 256, dtype=torch.bfloat16, device=DEV)
+    B.pda_mla_expand(dec.plan, cache, torch.arange(pages, device=DEV).int(), ints([0, pages]),
+                     ints([0, n]), None, w[:, :128], w[:, 128:], latent, kv[..., :128], kv[..., 128:],
+                     dec.scratch)
+    assert dec.status() == 0
+    for t in (0, n // 2, n - 1):
+        y, mag = ref.product(latent[t:t + 1, None, :512].expand(1, heads, 512).cpu(), w.cpu())
+        mag = mag * ref.sum_bound(512)
+        check(kv[t:t + 1], y, mag + ref.BF16_HALF * (y.abs() + mag), f"kv of token {t}")
+    q = torch.randn(5, heads, 192, generator=g, device=DEV).to(torch.bfloat16)
+    pre = B.Prefill(dec.plan, 5, n, device=DEV)
+    out = torch.zeros(5, heads, 128, dtype=torch.bfloat16, device=DEV)
+    lse = torch.zeros(5, heads, device=DEV)
+    pre.run(q, kv[..., :128], kv[..., 128:], latent[:, 512:], ints([0, 5]), ints([0, n]), 192 ** -0.5,
+            out, lse)
+    assert pre.status() == 0
+    some = [0, 77, 127]
+    o, ob, l_, lb = ref.attention(q.cpu()[:, some], kv[:, some, :128].cpu(), kv[:, some, 128:].cpu(),
+                                  latent[:, 512:].cpu(), [0, 5], [0, n], causal=True, windows=None,
+                                  scale=192 ** -0.5)
+    check(out[:, some], o, ob, "out")
+    check(lse[:, some], l_, lb, "lse")
+
+
+def test_prefill_extreme_logits():
+    """Logits far below any usual one (all about -3e3), and a scale that is not a number."""
+    p = Pre([(3, 200), (140, 400)], 1)
+    p.q[:143, :, :192] = -15.0
+    p.kv[:600, :, :128] += 15.0
+    p.lat[:600, 512:] += 15.0
+    p.dq, p.dkv, p.dlat = p.q.to(DEV), p.kv.to(DEV), p.lat.to(DEV)
+    p.run()
+    p.compare("far below")
+    p = Pre([(3, 20)], 1, scale=math.nan)
+    p.run()
+    torch.cuda.synchronize()
+    assert bool(torch.isnan(p.out[:3].float()).all())
+
+
+def test_calls_refuse_tensors_of_other_shapes():
+    g = torch.Generator().manual_seed(0)
+    dec = B.Decoder(ref.mla_plan(4), device=DEV)
+    w = randn(g, 4, 256, 512).to(DEV)
+    out = torch.zeros(3, 4, 576, dtype=torch.bfloat16, device=DEV)
+    q = randn(g, 3, 4, 192).to(DEV)
+    for bad in (dict(q=q[..., :128]), dict(q=q.float()), dict(q=q.cpu()), dict(w=w[:3, :128]),
+                dict(w=w.transpose(1, 2)[:, :128, :128]), dict(out=out[:2]), dict(out=out[..., ::2]),
+                dict(num=torch.zeros(2, dtype=torch.int32, device=DEV)),
+                dict(num=torch.zeros(1, dtype=torch.int64, device=DEV))):
+        a = {**dict(q=q, w=w[:, :128], out=out, num=None), **bad}
+        with pytest.raises(ValueError):
+            B.pda_mla_absorb(dec.plan, a["q"], a["w"], 1.0, a["out"], a["num"], dec.scratch)
+    with pytest.raises(B.PdaError):
+        B.pda_mla_absorb(dec.plan, q, w[:, :128], 1.0, out, None, dec.scratch[8:])
+    other = ref.mla_plan(4, num_sms=152, device=1)  # a plan of another device
+    plan = B.pda_plan(other)[0]
+    with pytest.raises(B.PdaError):
+        B.pda_mla_absorb(plan, q, w[:, :128], 1.0, out, None, dec.scratch)

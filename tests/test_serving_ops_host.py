@@ -169,13 +169,31 @@ def test_expand_refusals(lib, change, code):
                               a["st"], a["sh"], a["tokens"], a["scratch"], None) == code
 
 
+def test_prefill_plan_chunks(lib):
+    """Few (head, tile) items: the keys are cut into chunks of whole tiles, at least four of
+    them, that fill the SMs about once; many items are not cut."""
+    pre, nbytes, _ = B.pda_prefill_plan(plan_of(max_kv=8192), 64, 8192)
+    assert pre.tiles == 1 and pre.splits == 8 and pre.chunk_tokens == 1024  # 16 heads, 152 SMs: 9 -> 8
+    cells = pre.splits * 64 * 16
+    assert nbytes == 256 + cells * 4 + cells * 512
+    pre, nbytes, _ = B.pda_prefill_plan(plan_of(max_kv=8192), 4096, 8192)
+    assert pre.tiles == 16 and pre.splits == 1 and nbytes == 256
+    pre, _, _ = B.pda_prefill_plan(plan_of(max_kv=600), 1, 600)
+    assert pre.splits == 1 and pre.chunk_tokens == 640
+    pre, _, _ = B.pda_prefill_plan(plan_of(max_kv=1100, batch=3), 3, 3300)
+    assert pre.tiles == 3 and pre.splits == 2 and pre.chunk_tokens % 128 == 0
+
+
 def test_prefill_plan(lib):
     pre, nbytes, rc = B.pda_prefill_plan(plan_of(batch=4), 100, 900)
     assert rc == 0 and pre.magic == B.PDA_PREFILL_MAGIC
     assert pre.struct_bytes == ctypes.sizeof(B.PdaPrefillPlan)
     assert nbytes == pre.scratch_bytes >= 256 and nbytes % 256 == 0
     assert (pre.num_qo_heads, pre.batch, pre.rows, pre.tokens) == (16, 4, 100, 900)
-    for args, code in (((plan_of(), 0, 5), B.PDA_ERR_INVALID), ((plan_of(), 5, 0), B.PDA_ERR_INVALID),
+    many = plan_of(batch=8193)
+    for args, code in (((plan_of(), 0, 5), B.PDA_ERR_INVALID), ((many, 9000, 9000), B.PDA_ERR_INVALID),
+                       ((plan_of(), 2 ** 31 - 1, 5), B.PDA_ERR_INVALID),
+                       ((plan_of(), 5, 2 ** 31 - 1), B.PDA_ERR_INVALID), ((plan_of(), 5, 0), B.PDA_ERR_INVALID),
                        ((gqa_plan(), 5, 5), B.PDA_ERR_UNSUPPORTED), ((bad_plan(), 5, 5), B.PDA_ERR_PLAN)):
         assert B.pda_prefill_plan(*args, check=False)[2] == code
     assert lib.pda_prefill_plan(None, 5, 5, ctypes.byref(pre), None) == B.PDA_ERR_NULL
@@ -202,3 +220,16 @@ def test_prefill_refusals(lib, change, code):
     pre.struct_bytes += 8
     assert lib.pda_mla_prefill(ctypes.byref(pre), *[OKP, 16 * 192, 192, OKP, OKP, 4096, 256, OKP, 576, OKP,
                                OKP, None, 1, 0.1, OKP, None, OKP, None]) == B.PDA_ERR_PLAN
+
+
+def test_no_spills_in_the_new_kernels(lib):
+    """Registers decide the softmax loop's pace: at most four spilled bytes (of the prefill's
+    item bookkeeping), none elsewhere."""
+    found = {}
+    for name, (regs, stack, st, ld) in build_mod.ptxas_reports().items():
+        for k in ("prefill", "product", "expand", "gather_latent", "append_slots", "build_tables"):
+            if k in name and "prefill_join" not in name:
+                found.setdefault(k, []).append((st, ld))
+    assert len(found) == 6, sorted(found)
+    for k, v in found.items():
+        assert max(v) <= ((4, 16) if k == "prefill" else (0, 0)), (k, v)
