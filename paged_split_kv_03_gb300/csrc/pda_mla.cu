@@ -423,6 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   const int64_t f0 = pairs * me / of, f1 = pairs * (me + 1) / of;
   if (warp == 0) {
     if (lane == 0) {
+      // the latents come from the kernel in front of this one (every CTA waits,
+      // with or without work, so that what follows follows both kernels)
+      asm volatile("griddepcontrol.wait;" ::: "memory");
       // the leader's barriers count the bytes of both CTAs
       const uint32_t a_bar = on_leader(&a_full);
       bool alive = true;
@@ -435,8 +438,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
           tile = t;
           ++tiles;
           if (rank == 0) bar_expect_tx(&a_full, 2 * kExpA);
-          // (the latents come from the kernel in front of this one)
-          if (tiles == 1) asm volatile("griddepcontrol.wait;" ::: "memory");
           for (int k = 0; k < 8; ++k)
             tma_load3_pair(su32(smem + k * 16384), &ta, k * 64, 0, t * 256 + rank * 128, a_bar);
         }

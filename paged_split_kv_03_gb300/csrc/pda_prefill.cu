@@ -744,6 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     work_role(a, sh);
   }
   __syncwarp();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   fence_before();
   __syncthreads();
   fence_after();
@@ -761,7 +762,6 @@ __global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ Pref
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t row = item / a.heads;
-  if (row >= a.rows) return;
   // the last request that starts at or before the row
   int b = 0, top = a.batch - 1;
   while (b < top) {
@@ -770,13 +770,18 @@ __global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ Pref
     else top = mid - 1;
   }
   const Request r = request_of(a, b);
-  const int i = static_cast<int>(row) - r.q0;
-  if (i < 0 || i >= r.rows) return;
-  int lo, hi;
-  const int i0 = i / kRowsItem * kRowsItem;
-  key_tiles(a, r, i0, min(kRowsItem, r.rows - i0), lo, hi);
-  const int chunks = (hi - lo + a.chunk_tiles - 1) / a.chunk_tiles;
-  if (chunks <= 1) return;  // the only chunk wrote the result
+  const int64_t i = row - r.q0;
+  int chunks = 0;
+  if (row < a.rows && i >= 0 && i < r.rows) {
+    int lo, hi;
+    const int i0 = static_cast<int>(i) / kRowsItem * kRowsItem;
+    key_tiles(a, r, i0, min(kRowsItem, r.rows - i0), lo, hi);
+    chunks = (hi - lo + a.chunk_tiles - 1) / a.chunk_tiles;
+  }
+  // all of this overlaps the first kernel's tail; its partials are read below
+  // (every thread waits, so that what follows this kernel follows both)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (chunks <= 1) return;  // the only chunk wrote the result, or not a row
   const int64_t stride = static_cast<int64_t>(a.rows) * a.heads;
   float m = -INFINITY;
   for (int s = lane; s < chunks; s += 32) m = fmaxf(m, a.part_lse[s * stride + item]);
@@ -833,13 +838,16 @@ extern "C" int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t to
                 pda::kRowsItem);
   p.tiles = static_cast<int32_t>(tiles);
   // Key chunks. With fewer items (heads x tiles) than SMs, as many chunks as
-  // fill them once, of at least four key tiles (a chunk costs its start and
-  // its partials about three tiles' time).
+  // fill them once, of at least two key tiles (40 rows on up to 700 keys, 4 heads:
+  // one chunk 17.7, three of two tiles 13.5, six of one 13.2 us). More chunks than
+  // SMs cost more than they balance (257 rows on 2157 keys, 16 heads, 96 items: one
+  // chunk 39, two 51, three 44 us; 512 rows on 4012 keys, 32 items: 2 / 4 / 6 chunks
+  // 41 / 30 / 41 us).
   const int64_t items = tiles * plan->num_qo_heads;
   const int64_t max_tiles =
       (std::min<int64_t>(plan->max_kv_len, tokens) + pda::kKeys - 1) / pda::kKeys;
   int64_t splits = std::max<int64_t>(1, plan->num_sms / std::max<int64_t>(1, items));
-  splits = std::min<int64_t>(splits, std::max<int64_t>(1, max_tiles / 4));
+  splits = std::min<int64_t>(splits, std::max<int64_t>(1, max_tiles / 2));
   const int64_t chunk = (max_tiles + splits - 1) / splits;
   splits = (max_tiles + chunk - 1) / chunk;
   p.splits = static_cast<int32_t>(splits);
@@ -923,8 +931,19 @@ extern "C" int pda_mla_prefill(const pda_prefill_plan_t* plan, const void* q, in
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
   if (a.splits > 1) {
     const int64_t warps = static_cast<int64_t>(a.rows) * a.heads;
-    prefill_join<<<static_cast<unsigned>((warps + 7) / 8), 256, 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, prefill_join, a) != cudaSuccess) {
+      cudaGetLastError();
+      return PDA_ERR_CUDA;
+    }
   }
   return PDA_OK;
 }
