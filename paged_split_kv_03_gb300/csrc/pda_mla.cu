@@ -118,10 +118,9 @@ __global__ void __launch_bounds__(256) gather_latent(const __grid_constant__ Gat
 // A CTA has 128 tokens of one head and kN columns. Bound: HBM (the weights at
 // few rows, A and C at many: 128 x 128 x 512 MACs a row tile and head are 2048
 // tensor cycles against 160 KB). Short rows cost nothing but idle MMA lanes,
-// as TMA reads no row behind the last. What a CTA needs in flight decides: all
-// of K at once for absorb and for few rows, a ring of three stages (two CTAs an
-// SM) for project at many. The output tile passes through the stages' memory so
-// that a warp writes whole 256-byte rows.
+// as TMA reads no row behind the last. What a CTA has in flight, and how many an
+// SM holds, decides (pda_mla_project). The output tile passes through the stages'
+// memory so that a warp writes whole 256-byte rows.
 
 enum { kAbsorb = 0, kProject = 1 };
 
@@ -136,11 +135,11 @@ struct ProductArgs {
   int rows, heads;
 };
 
-template <int OP, int N>
+template <int OP, int N, int STAGES>
 struct ProductCfg {
   static constexpr int kK = OP == kAbsorb ? kNope : kLat;
   static constexpr int kBlocks = kK / 64;                        // K blocks of 128 bytes
-  static constexpr int kStages = OP == kAbsorb ? kBlocks : N >= 128 ? 3 : kBlocks;
+  static constexpr int kStages = STAGES;
   static constexpr int kABytes = 128 * 128, kBBytes = N * 128, kStage = kABytes + kBBytes;
   static constexpr int kSmem = kStages * kStage + 1024;          // + alignment
   static constexpr int kTotalN = OP == kAbsorb ? kLat : kNope;
@@ -160,11 +159,11 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-template <int OP, int N, bool E4M3>
+template <int OP, int N, int STAGES, bool E4M3>
 __global__ void __launch_bounds__(192)
     product(const __grid_constant__ ProductArgs a, const __grid_constant__ CUtensorMap ta,
             const __grid_constant__ CUtensorMap tb) {
-  using C = ProductCfg<OP, N>;
+  using C = ProductCfg<OP, N, STAGES>;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t full[C::kStages], empty[C::kStages], done;
   __shared__ uint32_t tmem_slot;
@@ -331,11 +330,11 @@ __global__ void __launch_bounds__(192)
                  : "memory");
 }
 
-template <int OP, int N, bool E4M3>
+template <int OP, int N, int STAGES, bool E4M3>
 int launch_product(const ProductArgs& a, const CUtensorMap& ta, const CUtensorMap& tb,
                    cudaStream_t s) {
-  using C = ProductCfg<OP, N>;
-  const auto fn = product<OP, N, E4M3>;
+  using C = ProductCfg<OP, N, STAGES>;
+  const auto fn = product<OP, N, STAGES, E4M3>;
   if (cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess) {
     cudaGetLastError();
@@ -597,8 +596,8 @@ extern "C" int pda_mla_absorb(const pda_plan_t* plan, const void* q, int64_t q_s
     return PDA_ERR_CUDA;
   if (!on_device(plan->device)) return PDA_ERR_INVALID;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return e4m3 ? launch_product<kAbsorb, 128, true>(p, ta, tb, s)
-              : launch_product<kAbsorb, 128, false>(p, ta, tb, s);
+  return e4m3 ? launch_product<kAbsorb, 128, 2, true>(p, ta, tb, s)
+              : launch_product<kAbsorb, 128, 2, false>(p, ta, tb, s);
 }
 
 extern "C" int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const void* w_uv,
@@ -616,8 +615,11 @@ extern "C" int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const 
   p.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us) * 1000ull;
   p.rows = rows;
   p.heads = plan->num_qo_heads;
-  // With fewer (head, row tile) pairs than SMs, four CTAs share a pair's
-  // columns: each streams a quarter of the weights, all of K in flight.
+  // Few (head, row tile) pairs (half the SMs): four CTAs share a pair's columns,
+  // each streams a quarter of the weights, all of K in flight. Up to a pair an
+  // SM: one CTA an SM with half of K in flight (four stages against two or three:
+  // 5.0 against 6.8 / 5.9 us at one row of 128 heads). More: three CTAs an SM of
+  // two stages (1024 rows, 128 heads, 2 / 3 / 4 stages: 36.7 / 38.6 / 43.9 us).
   const int64_t pairs = static_cast<int64_t>(p.heads) * ((rows + 127) / 128);
   const bool few = pairs * 2 <= plan->num_sms;
   CUtensorMap ta, tb;
@@ -626,8 +628,9 @@ extern "C" int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const 
     return PDA_ERR_CUDA;
   if (!on_device(plan->device)) return PDA_ERR_INVALID;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return few ? launch_product<kProject, 32, false>(p, ta, tb, s)
-             : launch_product<kProject, 128, false>(p, ta, tb, s);
+  if (few) return launch_product<kProject, 32, 8, false>(p, ta, tb, s);
+  return pairs <= plan->num_sms ? launch_product<kProject, 128, 4, false>(p, ta, tb, s)
+                                : launch_product<kProject, 128, 2, false>(p, ta, tb, s);
 }
 
 extern "C" int pda_mla_expand(const pda_plan_t* plan, const void* k_pages,
