@@ -132,7 +132,7 @@ struct Item {
 };
 
 struct Shared {
-  uint64_t q_full[2], q_empty[2], full[kRing], empty[kRing], s_full[2], p_full[2], o_done[2],
+  uint64_t q_full[2], q_empty[2], full[kRing], empty[kRing], s_full[2], p_half[2], p_full[2], o_done[2],
       o_free[2], item_full[kItems], item_empty[kItems], landed[kRing], drain;
   uint32_t tmem;
   int abort_flag;
@@ -271,8 +271,7 @@ __device__ void mma_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t
         const bool do_pv = j >= from && j < to, do_qk = j + 1 >= from && j + 1 < to;
         if (do_pv) {
           if (j == from && !wait(sh->o_free + g, qp >> g)) break;  // the last item's O is read
-          if (!wait(sh->p_full + g, pp >> g)) break;
-          pp ^= 1u << g;
+          if (!wait(sh->p_half + g, pp >> g)) break;
         }
         if (do_pv || (g == 1 && j >= lo)) {
 #pragma unroll
@@ -280,7 +279,11 @@ __device__ void mma_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_t
             const uint32_t u = x + kUnitsK + c, slot = u % kRing;
             if (do_pv) {
               if (!wait(sh->full + slot, u / kRing)) break;
-              if (c == 0) fence_after();
+              if (c == 1) {  // the second half of P's keys
+                if (!wait(sh->p_full + g, pp >> g)) break;
+                pp ^= 1u << g;
+              }
+              fence_after();
               const uint64_t vd = v_desc + slot * (kUnit / 16);
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -584,6 +587,12 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
           asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(p1), "f"(p0));
         }
         tmem_st16(t_s + c * 16, w);
+        if (c == 1) {  // the first 64 keys: P V starts on them
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(sh->p_half + g);
+        }
       }
       float l0, l1;
       unpack2(add2(sum[0], sum[1]), l0, l1);
@@ -696,6 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(sh->q_full + g, 1);
       bar_init(sh->q_empty + g, 1);
       bar_init(sh->s_full + g, 1);
+      bar_init(sh->p_half + g, kSoftmaxWarps / 2);
       bar_init(sh->p_full + g, kSoftmaxWarps / 2);
       bar_init(sh->o_done + g, 1);
       bar_init(sh->o_free + g, kSoftmaxWarps / 2);
