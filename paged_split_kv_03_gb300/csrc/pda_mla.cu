@@ -26,8 +26,9 @@ constexpr int kQDim = kNope + kRope;
 // ------------------------------------------------------ gather of latents
 //
 // One warp per token: its request by binary search in tok_indptr, its page
-// slot, then the row dequantised to bf16. Chunks of 8 channels per lane.
-// Bound: HBM / latency; the expansion that follows writes Hq x 512 bytes a token.
+// slot, then the row dequantised to bf16. Chunks of 8 channels per lane. Bound:
+// latency (five dependent reads); the expansion that follows writes Hq x 512
+// bytes a token and its set-up overlaps this kernel.
 
 struct GatherArgs {
   const uint8_t* pages;
@@ -115,12 +116,15 @@ __global__ void __launch_bounds__(256) gather_latent(const __grid_constant__ Gat
 //   absorb   A = q_nope (K = 128), B = W_UK read the other way round: its rows
 //            are the K channels, so B is MN-major, as it lies (N = 512)
 //   project  A = o_lat (K = 512), B = W_UV (N = 128)
-// A CTA has 128 tokens of one head and kN columns. Bound: HBM (the weights at
+// A CTA has 128 tokens of one head and N columns. Bound: HBM (the weights at
 // few rows, A and C at many: 128 x 128 x 512 MACs a row tile and head are 2048
 // tensor cycles against 160 KB). Short rows cost nothing but idle MMA lanes,
 // as TMA reads no row behind the last. What a CTA has in flight, and how many an
 // SM holds, decides (pda_mla_project). The output tile passes through the stages'
-// memory so that a warp writes whole 256-byte rows.
+// memory so that a warp writes whole 256-byte rows. Measured: absorb of 1024 rows x
+// 128 heads 49 us to bf16 (4.4 TB/s, 151 of the 218 MB written, which a plain fill
+// does at 4.0 TB/s), 37 us to E4M3; project 37 us (5.0 TB/s); one row of 128 heads 6.0
+// and 5.0 us.
 
 enum { kAbsorb = 0, kProject = 1 };
 

@@ -11,22 +11,26 @@
 //
 // Bound: the tensor cores (640 flops per row, key and head). A tile of 128 rows
 // x 128 keys takes 12 + 8 MMAs, 1280 cycles; its softmax is 16384 exponentials
-// plus about four instructions each, hidden behind the other tile's MMAs. So a CTA holds two 128-row tiles (96 KB of Q, shared K and V:
-// half the L2 reads of one tile), whose S take turns:
+// plus about four instructions each, hidden behind the other tile's MMAs. So a
+// CTA holds two 128-row tiles (96 KB of Q, shared K and V: half the L2 reads of
+// one tile), whose S take turns:
 //   PV(0, j)  QK(0, j+1)  PV(1, j)  QK(1, j+1)  ...
 // S, P (over S, bf16, the MMA's A operand) and O of both fill the 512 TMEM
-// columns, so neither P nor O touches shared memory.
+// columns, so neither P nor O touches shared memory. P is handed over in halves
+// of 64 keys, as the way from S to the next S decides the pace.
+// Measured: 4096 causal rows x 128 heads 470 us (1.46 PFLOP/s, 78 % of the measured
+// bf16 rate), without a mask 760 (1.81, 97 %).
 //
 // Roles: warps 0-3 and 4-7 are the softmax of tile 0 and 1; warp 8 loads (TMA),
 // warp 9 issues the MMAs, warp 10 clears V rows behind the last key (0 x NaN),
-// warp 11 takes (head, tile, chunk) items off a counter in
-// the scratch; the warps pass items on through a ring, so that the loads and
-// MMAs of the next item start while this one's rows are written. K and V pass through a ring of 16 KB units: three of K (128 keys x 64
-// channels), two of V (64 keys x 128 channels) a tile.
+// warp 11 takes (head, tile, chunk) items off a counter in the scratch; the warps
+// pass items on through a ring, so that the loads and MMAs of the next item start
+// while this one's rows are written. K and V pass through a ring of 16 KB units:
+// three of K (128 keys x 64 channels), two of V (64 keys x 128 channels) a tile.
 //
 // Few rows: where heads x tiles are fewer than the SMs, a tile's keys are cut
 // into chunks (pda_prefill_plan), whose normalised partial outputs and log2 sums
-// a second kernel joins.
+// a second kernel joins. 64 rows on 8064 keys, 16 heads: 25.7 us, 103.7 uncut.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

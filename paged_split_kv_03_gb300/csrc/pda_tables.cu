@@ -12,8 +12,8 @@
 // Bound: latency (a decode step moves tens of kilobytes). So one launch with
 // no hand-off between CTAs: every CTA scans all the lengths itself (they stay
 // in L2: 12 bytes a request) and then lists only its own requests, a few warps
-// to each. A scan of a few hundred requests costs less than the second
-// launch, or the device-wide scan with look-back, that would share it.
+// to each. A scan of a few hundred requests costs less than the second launch,
+// or the device-wide scan with look-back, that would share it.
 
 #include <cuda_runtime.h>
 
