@@ -398,8 +398,8 @@ int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64_t k_stride
  * q_lat[t, h, 512:] = q[t, h, 128:].
  *   q      bf16 [rows, Hq, 192], strides in elements (multiples of 8)
  *   q_lat  [rows, Hq, 576] contiguous, the plan's q_dtype: bf16, or E4M3 codes
- *          RNE(sat(x * (1 / q_scale))) in fp32 (q_scale > 0; pda_decode's sm_scale
- *          takes it) */
+ *          RNE(sat(x * (1 / q_scale))) in fp32 (q_scale and its reciprocal
+ *          positive and finite; pda_decode's sm_scale takes the scale) */
 int pda_mla_absorb(const pda_plan_t* plan, const void* q, int64_t q_stride_row,
                    int64_t q_stride_head, const void* w_uk, int64_t w_stride_head, float q_scale,
                    void* q_lat, int32_t rows, const int32_t* num_rows, void* split_scratch,
@@ -456,7 +456,9 @@ typedef struct {
  * that the caller allocates as for pda_plan (256-byte aligned, zeroed once);
  * pda_get_status reads and pda_reset_status clears its status word. Calls that
  * share a scratch must not overlap: the work counters and the partial outputs
- * are in it. */
+ * are in it. plan->wait_limit_us bounds each wait of a call too; the longest one
+ * lasts about as long as three requests' 256-row tiles take (1.7 us for every 128
+ * keys each). */
 int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t tokens,
                      pda_prefill_plan_t* out_plan, size_t* scratch_bytes);
 

@@ -579,7 +579,9 @@ extern "C" int pda_mla_absorb(const pda_plan_t* plan, const void* q, int64_t q_s
   if (rc != PDA_OK || rows == 0) return rc;
   if (!q || !w_uk || !q_lat) return PDA_ERR_NULL;
   const bool e4m3 = plan->q_dtype == PDA_E4M3;
-  if (e4m3 && !(q_scale > 0.f && q_scale < INFINITY)) return PDA_ERR_INVALID;
+  // (its reciprocal too has to be a finite number)
+  if (e4m3 && !(q_scale > 0.f && q_scale < INFINITY && 1.f / q_scale < INFINITY))
+    return PDA_ERR_INVALID;
   if (q_stride_head < kQDim || q_stride_row < kQDim) return PDA_ERR_INVALID;
   if (!a16(q) || !a16(w_uk) || !a16(q_lat) || q_stride_row % 8 || q_stride_head % 8)
     return PDA_ERR_ALIGNMENT;

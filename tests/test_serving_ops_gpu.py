@@ -704,6 +704,28 @@ def test_prefill_graph_and_streams():
     b.compare("stream 2")
 
 
+def test_prefill_graphs_share_a_scratch():
+    """Two graphs over one scratch, with key chunks and without, replayed in turn."""
+    a, b = Pre([(30, 3000)], 2, seed=1), Pre([(30, 3000)], 2, seed=2)
+    b.pre = a.pre
+    assert a.pre.plan.splits > 1
+    graphs = []
+    for p in (a, b):
+        p.run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p.run()
+        graphs.append(g)
+    for _ in range(3):
+        a.out.fill_(7.0), b.out.fill_(7.0)
+        for g in graphs:
+            g.replay()
+        a.compare("first")
+        b.compare("second")
+    assert a.pre.status() == 0
+
+
 # ------------------------------------------------------- the calls together
 
 def dense_decode(q, lat, w_uk, w_uv, scale):

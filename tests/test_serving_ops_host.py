@@ -131,7 +131,7 @@ def test_absorb_refusals(lib, change, code):
 
 def test_mla_refusals_of_plans(lib):
     e4 = plan_of(kind="e4m3")
-    for s in (0.0, -1.0, float("nan"), float("inf")):
+    for s in (0.0, -1.0, float("nan"), float("inf"), 1e-40):
         assert absorb(lib, e4, qs=s) == B.PDA_ERR_INVALID
     assert absorb(lib, bad_plan()) == B.PDA_ERR_PLAN
     assert absorb(lib, gqa_plan()) == B.PDA_ERR_UNSUPPORTED
