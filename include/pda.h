@@ -125,9 +125,10 @@ typedef struct {
                               PR #54): head_dim 576 (512 latent + 64 rope), head_dim_v 512,
                               one latent cache passed as both k_pages and v_pages, V being its
                               first 512 channels; bf16, or E4M3 with an E4M3 query */
-  int32_t wait_limit_us;   /* bound of every stage-1 pipeline wait (tcgen05 path), in
-                              microseconds; 0 = 2 s. A wait that runs out sets
-                              PDA_STATUS_WAIT_TIMEOUT and its CTA gives up, writing nothing */
+  int32_t wait_limit_us;   /* bound of every pipeline wait (stage 1 on the tcgen05 path, the
+                              latent-attention calls), in microseconds; 0 = 2 s. A wait that
+                              runs out sets PDA_STATUS_WAIT_TIMEOUT and its CTA gives up: in
+                              stage 1 writing nothing; see the latent-attention calls for theirs */
   uint32_t inject;         /* test hooks, 0 in normal use: PDA_INJECT_WITHHOLD_KV */
   /* optional host copies for exact eager planning, used with host_kv_len:
    * qo_indptr[batch + 1] (rows of each request) and window[batch]; NULL = every
@@ -140,6 +141,7 @@ typedef struct {
 /* Test hook (pda_params.inject): the tcgen05 stage-1 CTAs issue no K/V
  * loads at all, so their consumers' waits run out after wait_limit_us and
  * every CTA returns with PDA_STATUS_WAIT_TIMEOUT set and nothing written.
+ * The products of latent attention issue no loads of their operands either.
  * It exercises the timeout path without a device fault. */
 #define PDA_INJECT_WITHHOLD_KV 0x1u
 

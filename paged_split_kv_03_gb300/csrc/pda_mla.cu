@@ -137,6 +137,7 @@ struct ProductArgs {
   uint64_t wait_limit_ns;
   float inv_scale;         // absorb to E4M3: 1 / q_scale, else 0
   int rows, heads;
+  uint32_t inject;         // PDA_INJECT_*, 0 in normal use
 };
 
 template <int OP, int N, int STAGES>
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(192)
   if (a.num_rows) rows = min(rows, __ldg(a.num_rows));
   const int n0 = blockIdx.x * N, h = blockIdx.y, t0 = blockIdx.z * 128;
   if (t0 >= rows) return;
+  const bool withhold = (a.inject & PDA_INJECT_WITHHOLD_KV) != 0u;
   auto load = [&](int k) {
     const int s = k % C::kStages;
     uint8_t* st = smem + s * C::kStage;
@@ -200,7 +202,7 @@ __global__ void __launch_bounds__(192)
     abort_word = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     // the first loads are on their way while TMEM is allocated
-    for (int k = 0; k < C::kStages; ++k) load(k);
+    for (int k = 0; k < C::kStages && !withhold; ++k) load(k);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -215,16 +217,16 @@ __global__ void __launch_bounds__(192)
   fence_after();
   const uint32_t tmem = tmem_slot;
   if (warp == 0) {
-    if (lane == 0) {
-      bool alive = true;
+    if (lane == 0 && !withhold) {
       int k = C::kStages;
       for (; k < C::kBlocks; ++k) {
-        if (!(alive = bar_wait(empty + k % C::kStages, ((k / C::kStages) - 1) & 1u, abort_flag, a))) break;
+        if (!bar_wait(empty + k % C::kStages, ((k / C::kStages) - 1) & 1u, abort_flag, a)) break;
         load(k);
       }
-      if (!alive || *abort_flag)  // every box issued must have landed before the CTA can exit
-        for (int i = k - C::kStages; i < k; ++i)
-          bar_drain(full + i % C::kStages, (i / C::kStages) & 1u);
+      // Every box issued must have landed before the CTA can exit. Always, not
+      // only after an abort seen here: the MMA thread's wait may run out later.
+      for (int i = k - C::kStages; i < k; ++i)
+        bar_drain(full + i % C::kStages, (i / C::kStages) & 1u);
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -596,6 +598,7 @@ extern "C" int pda_mla_absorb(const pda_plan_t* plan, const void* q, int64_t q_s
   p.inv_scale = e4m3 ? 1.f / q_scale : 0.f;
   p.rows = rows;
   p.heads = plan->num_qo_heads;
+  p.inject = plan->inject;
   CUtensorMap ta, tb;
   if (!make_map3(&ta, q, kNope, p.heads, rows, q_stride_head, q_stride_row, 64, 1, 128) ||
       !make_map3(&tb, w_uk, kLat, kNope, p.heads, kLat, w_stride_head, 64, 64, 1))
@@ -621,6 +624,7 @@ extern "C" int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const 
   p.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us) * 1000ull;
   p.rows = rows;
   p.heads = plan->num_qo_heads;
+  p.inject = plan->inject;
   // Few (head, row tile) pairs (half the SMs): four CTAs share a pair's columns,
   // each streams a quarter of the weights, all of K in flight. Up to a pair an
   // SM: one CTA an SM with half of K in flight (four stages against two or three:

@@ -1,0 +1,98 @@
+"""The bounded pipeline waits of the latent-attention kernels run out without
+a device fault.
+
+As for the decode's stage 1: the host sets a PDA_INJECT_WITHHOLD_* hook, the
+loads it names are never issued, and a short wait limit makes their consumers
+give up. What was issued has landed by then (milliseconds against
+microseconds) and is drained before a CTA leaves. The call returns with
+PDA_STATUS_WAIT_TIMEOUT, and the next normal call on the same scratch is
+right. Nothing faults, traps or spins without a bound.
+"""
+from __future__ import annotations
+
+
+import pytest
+import torch
+
+import serving_ref as ref
+from paged_split_kv_03_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+LIMIT_US = 2000
+
+
+def decoders(heads, inject, **kw):
+    """(a decoder whose calls withhold loads, a normal one) over one scratch."""
+    p = ref.mla_plan(heads, **kw)
+    good = B.Decoder(p, device=DEV)
+    p.inject, p.wait_limit_us = inject, LIMIT_US
+    bad = B.Decoder(p, device=DEV)
+    bad.scratch = good.scratch
+    return bad, good
+
+
+def timed_out(dec):
+    """Whether the call ended in a timeout and nothing else; the status is cleared."""
+    torch.cuda.synchronize()  # every wait was bounded: the kernel returned
+    bits = dec.status()
+    dec.reset_status()
+    return bits == B.PDA_STATUS_WAIT_TIMEOUT
+
+
+def close(got, want, bound, what):
+    err = (got.double().cpu() - want).abs()
+    assert bool((err <= bound).all()), f"{what}: {float((err - bound).max()):.3e} past its bound"
+
+
+# one (head, row tile) pair, all of K in flight at once / a few / many with two stages
+@pytest.mark.parametrize("rows,heads", [(1, 1), (5, 128), (300, 128)])
+def test_project_times_out(rows, heads):
+    g = torch.Generator().manual_seed(rows)
+    bad, good = decoders(heads, B.PDA_INJECT_WITHHOLD_KV)
+    o = torch.randn(rows, heads, 512, generator=g).to(torch.bfloat16)
+    w = (torch.randn(heads, 128, 512, generator=g) * 512 ** -0.5).to(torch.bfloat16)
+    do, dw = o.to(DEV), w.to(DEV)
+    out = torch.full((rows, heads, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    B.pda_mla_project(bad.plan, do, dw, out, None, bad.scratch)
+    assert timed_out(bad)
+    assert bool((out == 7).all())
+    B.pda_mla_project(good.plan, do, dw, out, None, good.scratch)
+    torch.cuda.synchronize()
+    assert good.status() == 0
+    x, mag = ref.product(o, w)
+    mag = mag * ref.sum_bound(512)
+    close(out, x, mag + ref.BF16_HALF * (x.abs() + mag), "after the timeout")
+
+
+def absorb_case(kind, rows, heads):
+    g = torch.Generator().manual_seed(rows)
+    q = torch.randn(rows, heads, 192, generator=g).to(torch.bfloat16)
+    w = (torch.randn(heads, 128, 512, generator=g) * 512 ** -0.5).to(torch.bfloat16)
+    out = torch.full((rows, heads, 576), 77, device=DEV,
+                     dtype=torch.bfloat16 if kind == "bf16" else torch.uint8)
+    return q, w, out
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,heads", [(1, 1), (200, 16)])
+def test_absorb_times_out(rows, heads, kind):
+    bad, good = decoders(heads, B.PDA_INJECT_WITHHOLD_KV, kind=kind)
+    q, w, out = absorb_case(kind, rows, heads)
+    dq, dw = q.to(DEV), w.to(DEV)
+    B.pda_mla_absorb(bad.plan, dq, dw, 0.011, out, None, bad.scratch)
+    assert timed_out(bad)
+    assert bool((out[..., :512] == 77).all())
+    B.pda_mla_absorb(good.plan, dq, dw, 0.011, out, None, good.scratch)
+    torch.cuda.synchronize()
+    assert good.status() == 0
+    x, mag = ref.product(q[..., :128], w.transpose(1, 2))
+    mag = mag * ref.sum_bound(128)
+    if kind == "bf16":
+        close(out[..., :512], x, mag + ref.BF16_HALF * (x.abs() + mag), "after the timeout")
+        assert torch.equal(out[..., 512:].cpu(), q[..., 128:])
+    else:
+        y = (x / 0.011).clamp(-448, 448)
+        mag = mag / 0.011 + 2.0 ** -23 * y.abs()
+        close(out[..., :512].view(ref.E4M3).float(), y,
+              mag + torch.clamp(ref.E4M3_HALF * (y.abs() + mag), min=ref.E4M3_SUB), "after the timeout")
