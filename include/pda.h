@@ -129,7 +129,7 @@ typedef struct {
                               latent-attention calls), in microseconds; 0 = 2 s. A wait that
                               runs out sets PDA_STATUS_WAIT_TIMEOUT and its CTA gives up: in
                               stage 1 writing nothing; see the latent-attention calls for theirs */
-  uint32_t inject;         /* test hooks, 0 in normal use: PDA_INJECT_WITHHOLD_KV */
+  uint32_t inject;         /* test hooks, 0 in normal use: PDA_INJECT_* */
   /* optional host copies for exact eager planning, used with host_kv_len:
    * qo_indptr[batch + 1] (rows of each request) and window[batch]; NULL = every
    * request has max_q_len rows / no window. The plan stays valid for any
@@ -138,12 +138,17 @@ typedef struct {
   const int32_t* host_window;
 } pda_params;
 
-/* Test hook (pda_params.inject): the tcgen05 stage-1 CTAs issue no K/V
+/* Test hooks (pda_params.inject). PDA_INJECT_WITHHOLD_KV: the tcgen05 stage-1 CTAs issue no K/V
  * loads at all, so their consumers' waits run out after wait_limit_us and
  * every CTA returns with PDA_STATUS_WAIT_TIMEOUT set and nothing written.
- * The products of latent attention issue no loads of their operands either.
- * It exercises the timeout path without a device fault. */
+ * The products of latent attention and pda_mla_expand issue no loads of their
+ * operands either; the other two hooks withhold those of one CTA of each of
+ * pda_mla_expand's CTA pairs and touch no other call.
+ * They exercise the timeout paths without a device fault. */
 #define PDA_INJECT_WITHHOLD_KV 0x1u
+#define PDA_INJECT_WITHHOLD_CTA0 0x2u
+#define PDA_INJECT_WITHHOLD_CTA1 0x4u
+#define PDA_INJECT_ALL 0x7u
 
 /* The plan: plain data, owned by the caller, copied freely. Fields are
  * documented for inspection; pda_decode reads only what pda_plan wrote. */

@@ -38,6 +38,8 @@ PDA_STATUS_TOKENS_GT_CAP = 0x400
 PDA_PLAN_MAGIC = 0x50444131
 PDA_PREFILL_MAGIC = 0x50444631
 PDA_INJECT_WITHHOLD_KV = 0x1
+PDA_INJECT_WITHHOLD_CTA0 = 0x2
+PDA_INJECT_WITHHOLD_CTA1 = 0x4
 
 # every entry point include/pda.h declares
 EXPORTED = ("pda_plan", "pda_decode", "pda_decode_stages", "pda_decode_static", "pda_append_kv",

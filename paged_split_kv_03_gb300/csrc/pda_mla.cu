@@ -373,6 +373,7 @@ struct ExpandArgs {
   uint32_t* status;
   uint64_t wait_limit_ns;
   int tokens, heads;
+  uint32_t inject;         // PDA_INJECT_*, 0 in normal use
 };
 
 constexpr int kExpStages = 5;
@@ -388,6 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   __shared__ uint64_t a_full, a_empty, full[kExpStages], empty[kExpStages], c_full[2], c_free[2], drain;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_word;
+  __shared__ uint32_t issued_units, issued_tiles;  // ring units, row tiles this CTA has loaded
   uint8_t* smem = raw + ((1024u - (su32(raw) & 1023u)) & 1023u);
   uint8_t* ring = smem + kExpA;
   volatile int* abort_flag = &abort_word;
@@ -406,6 +408,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
     }
     bar_init(&drain, 1);
     abort_word = 0;
+    issued_units = issued_tiles = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -426,6 +429,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   const int64_t pairs = static_cast<int64_t>((max(rows, 0) + 255) / 256) * a.heads;
   const int64_t me = blockIdx.x / 2, of = gridDim.x / 2;
   const int64_t f0 = pairs * me / of, f1 = pairs * (me + 1) / of;
+  const uint32_t hooks = PDA_INJECT_WITHHOLD_KV |
+                         (rank ? PDA_INJECT_WITHHOLD_CTA1 : PDA_INJECT_WITHHOLD_CTA0);
   if (warp == 0) {
     if (lane == 0) {
       // the latents come from the kernel in front of this one (every CTA waits,
@@ -433,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
       asm volatile("griddepcontrol.wait;" ::: "memory");
       // the leader's barriers count the bytes of both CTAs
       const uint32_t a_bar = on_leader(&a_full);
-      bool alive = true;
+      bool alive = (a.inject & hooks) == 0u;
       uint32_t x = 0, tiles = 0;
       int tile = -1;
       for (int64_t f = f0; f < f1 && alive; ++f) {
@@ -453,14 +458,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
           tma_load3_pair(su32(ring + s * kExpB), rank ? &tv : &tk, k * 64, 0, h, on_leader(full + s));
         }
       }
-      // Every box issued has landed before the CTA exits: its MMAs have read it.
-      // After a timeout the leader's barriers cannot tell this CTA, so it waits
-      // out the time that any load takes.
-      if (!alive || *abort_flag) {
-        const uint64_t t0 = global_ns();
-        while (global_ns() - t0 < 1000000ull) {
-        }
-      }
+      issued_units = x;
+      issued_tiles = tiles;
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
@@ -545,7 +544,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   __syncwarp();
   fence_before();
   __syncthreads();
+  if (tid == 0 && *abort_flag) cluster_store(on_cta(&abort_word, rank ^ 1u), 1u);
+  __syncwarp();
   cluster_sync();  // the pair's barriers and shared memory are used until here
+  // Every box issued must have landed before either CTA can exit. Without a
+  // timeout the MMAs have read them all. After one, in either CTA (both know by
+  // now), the leader waits on its barriers, which count both CTAs' bytes: boxes
+  // that only CTA 1 issued are announced first, those that it did not issue are
+  // taken off. Both counts are within the ring of what the MMAs released.
+  if (*abort_flag) {
+    if (tid == 0 && rank == 0) {
+      auto settle = [&](uint64_t* bar, uint32_t k, uint32_t mine, uint32_t other, uint32_t bytes,
+                        uint32_t parity) {
+        if (k >= mine) bar_expect_tx(bar, bytes);
+        else if (k >= other) bar_complete_tx(bar, bytes);
+        bar_drain(bar, parity & 1u);
+      };
+      const uint32_t x0 = issued_units, x1 = cluster_load(on_cta(&issued_units, 1));
+      const uint32_t t0 = issued_tiles, t1 = cluster_load(on_cta(&issued_tiles, 1));
+      const uint32_t x = max(x0, x1), t = max(t0, t1);
+      for (uint32_t k = x > kExpStages ? x - kExpStages : 0u; k < x; ++k)
+        settle(full + k % kExpStages, k, x0, x1, kExpB, k / kExpStages);
+      if (t) settle(&a_full, t - 1, t0, t1, kExpA, t - 1);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   fence_after();
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
@@ -694,6 +718,7 @@ extern "C" int pda_mla_expand(const pda_plan_t* plan, const void* k_pages,
   e.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us) * 1000ull;
   e.tokens = tokens;
   e.heads = plan->num_qo_heads;
+  e.inject = plan->inject;
   CUtensorMap ta, tk, tv;
   if (!make_map3(&ta, latent, kLat, 1, tokens, kLatRow, kLatRow, 64, 1, 128) ||
       !make_map3(&tk, w_uk, kLat, kNope, e.heads, kLat, w_stride_head, 64, 128, 1) ||

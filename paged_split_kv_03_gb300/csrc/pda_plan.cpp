@@ -88,7 +88,7 @@ extern "C" int pda_plan(const pda_params* p, pda_plan_t* out, size_t* split_scra
     return PDA_ERR_INVALID;
   if (p->chunk_pages < 0) return PDA_ERR_INVALID;
   if (p->kernel < PDA_KERNEL_AUTO || p->kernel > PDA_KERNEL_TC) return PDA_ERR_INVALID;
-  if (p->wait_limit_us < 0 || (p->inject & ~PDA_INJECT_WITHHOLD_KV)) return PDA_ERR_INVALID;
+  if (p->wait_limit_us < 0 || (p->inject & ~PDA_INJECT_ALL)) return PDA_ERR_INVALID;
   // 16-byte alignment of every stride ("require 16-byte aligned cache bases
   // and strides", follow-up commit on the FreeToken page)
   const int eb = elem_bytes(p->kv_dtype);

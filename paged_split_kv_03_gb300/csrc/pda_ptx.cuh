@@ -86,11 +86,20 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-// Cluster address of the leader's copy of a shared-memory variable.
-__device__ __forceinline__ uint32_t on_leader(const void* p) {
+// Cluster address of CTA `rank`'s (the leader's) copy of a shared-memory variable.
+__device__ __forceinline__ uint32_t on_cta(const void* p, uint32_t rank) {
   uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(su32(p)));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(su32(p)), "r"(rank));
   return r;
+}
+__device__ __forceinline__ uint32_t on_leader(const void* p) { return on_cta(p, 0); }
+__device__ __forceinline__ uint32_t cluster_load(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_store(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void bar_arrive_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
@@ -200,6 +209,12 @@ __device__ __forceinline__ void bar_arrive(uint64_t* b) {
 }
 __device__ __forceinline__ void bar_expect_tx(uint64_t* b, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes)
+               : "memory");
+}
+// Takes bytes off an announcement whose copy is not coming.
+__device__ __forceinline__ void bar_complete_tx(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(su32(b)),
+               "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t parity) {

@@ -96,3 +96,38 @@ def test_absorb_times_out(rows, heads, kind):
         mag = mag / 0.011 + 2.0 ** -23 * y.abs()
         close(out[..., :512].view(ref.E4M3).float(), y,
               mag + torch.clamp(ref.E4M3_HALF * (y.abs() + mag), min=ref.E4M3_SUB), "after the timeout")
+
+
+# Neither CTA of a pair loads; only the leader does (its barriers wait for bytes that do not
+# come); only the other does (bytes that were not announced).
+@pytest.mark.parametrize("hook", ["WITHHOLD_KV", "WITHHOLD_CTA0", "WITHHOLD_CTA1"])
+@pytest.mark.parametrize("tokens,heads", [(1, 1), (300, 3), (1100, 128)])
+def test_expand_times_out(tokens, heads, hook):
+    g = torch.Generator().manual_seed(tokens)
+    page = 64
+    pages = -(-tokens // page)
+    bad, good = decoders(heads, getattr(B, "PDA_INJECT_" + hook), pages=pages)
+    cache = torch.randn(pages, page, 1, 576, generator=g).to(torch.bfloat16)
+    w = (torch.randn(heads, 256, 512, generator=g) * 512 ** -0.5).to(torch.bfloat16)
+    dcache, dw = cache.to(DEV), w.to(DEV)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)
+    ptr, tok = (torch.tensor([0, n], dtype=torch.int32, device=DEV) for n in (pages, tokens))
+    latent = torch.zeros(tokens, 576, dtype=torch.bfloat16, device=DEV)
+    kv = torch.full((tokens, heads, 256), 7.0, dtype=torch.bfloat16, device=DEV)
+
+    def run(dec):
+        B.pda_mla_expand(dec.plan, dcache, table, ptr, tok, None, dw[:, :128], dw[:, 128:], latent,
+                         kv[..., :128], kv[..., 128:], dec.scratch)
+
+    run(bad)
+    assert timed_out(bad)
+    assert bool((kv == 7).all())
+    run(good)
+    torch.cuda.synchronize()
+    assert good.status() == 0
+    x = cache.reshape(-1, 576)[:tokens]
+    assert torch.equal(latent.cpu(), x)
+    some = slice(0, tokens, 37)  # every 37th token, all heads
+    y, mag = ref.product(x[some, None, :512].expand(-1, heads, 512), w)
+    mag = mag * ref.sum_bound(512)
+    close(kv[some], y, mag + ref.BF16_HALF * (y.abs() + mag), "after the timeout")
