@@ -141,8 +141,8 @@ typedef struct {
 /* Test hooks (pda_params.inject). PDA_INJECT_WITHHOLD_KV: the tcgen05 stage-1 CTAs issue no K/V
  * loads at all, so their consumers' waits run out after wait_limit_us and
  * every CTA returns with PDA_STATUS_WAIT_TIMEOUT set and nothing written.
- * The products of latent attention and pda_mla_expand issue no loads of their
- * operands either; the other two hooks withhold those of one CTA of each of
+ * The products of latent attention, pda_mla_expand and pda_mla_prefill issue no
+ * loads of their operands either; the other two hooks withhold those of one CTA of each of
  * pda_mla_expand's CTA pairs and touch no other call.
  * They exercise the timeout paths without a device fault. */
 #define PDA_INJECT_WITHHOLD_KV 0x1u
@@ -399,7 +399,11 @@ int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64_t k_stride
  * W_UK first is w_uk = w, w_uv = w + 128 * 512, w_stride_head = 256 * 512.
  * num_rows (device int32 [1], or NULL) bounds the rows as in
  * pda_append_slots; rows past it are left as they were. All sums are fp32,
- * rounded once to the output type. */
+ * rounded once to the output type. The plan's wait_limit_us bounds every wait
+ * of these calls and of a prefill; after PDA_STATUS_WAIT_TIMEOUT none of the
+ * call's outputs may be used: the rows of the CTAs that gave up are left as they
+ * were (a prefill in key chunks still joins them from what its scratch holds),
+ * others are written. The next call on the same scratch is a normal one. */
 
 /* q_lat[t, h, :512] = sum_d q[t, h, d] W_UK[h, d, :] (d < 128), and
  * q_lat[t, h, 512:] = q[t, h, 128:].
@@ -450,7 +454,8 @@ typedef struct {
   int32_t splits;         /* bound on the key chunks of a tile; 1: not split */
   int32_t chunk_tokens;   /* keys per chunk, a multiple of 128 */
   int32_t wait_limit_us;
-  int32_t reserved[3];
+  uint32_t inject;        /* pda_params.inject */
+  int32_t reserved[2];
   int64_t scratch_bytes;
 } pda_prefill_plan_t;
 

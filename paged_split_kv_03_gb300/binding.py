@@ -91,7 +91,8 @@ class PdaPrefillPlan(ctypes.Structure):
     _fields_ = [("magic", _u32), ("struct_bytes", _u32), ("num_qo_heads", _i32), ("batch", _i32),
                 ("max_kv_len", _i32), ("num_sms", _i32), ("device", _i32), ("rows", _i32),
                 ("tokens", _i32), ("tiles", _i32), ("splits", _i32), ("chunk_tokens", _i32),
-                ("wait_limit_us", _i32), ("reserved", _i32 * 3), ("scratch_bytes", _i64)]
+                ("wait_limit_us", _i32), ("inject", _u32), ("reserved", _i32 * 2),
+                ("scratch_bytes", _i64)]
 
 
 class PdaError(RuntimeError):

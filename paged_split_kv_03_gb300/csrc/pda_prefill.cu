@@ -84,6 +84,7 @@ struct PrefillArgs {
   uint64_t wait_limit_ns;
   float sm_scale;
   int heads, batch, max_kv_len, rows, tokens, causal, splits, chunk_tiles;
+  uint32_t inject;  // PDA_INJECT_*, 0 in normal use
 };
 
 // One request's geometry, and whether it takes part (else its status bits).
@@ -188,8 +189,8 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
   ItemReader reader(sh);
   Item it{};
   uint32_t x = 0, nq0 = 0, nq1 = 0;  // ring unit, Q tiles
-  uint32_t used = 0u, parity = 0u;   // `landed`: places used so far, uses of each mod 2
-  bool alive = true;
+  uint32_t tails = 0u, parity = 0u;  // `landed`: places whose last unit uses it, uses mod 2
+  bool alive = (a.inject & PDA_INJECT_WITHHOLD_KV) == 0u;
   auto dst = [&](uint32_t unit) { return ring_addr + unit % kRing * kUnit; };
   auto place = [&](uint32_t unit) {
     return alive = bar_wait(sh->empty + unit % kRing, ((unit / kRing) & 1u) ^ 1u, abort_flag, a);
@@ -212,6 +213,7 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
       const int tok = it.k0 + j * kKeys;
       for (int c = 0; c < kUnitsK && place(x); ++c, ++x) {
         uint64_t* bar = sh->full + x % kRing;
+        tails &= ~(1u << x % kRing);
         bar_expect_tx(bar, kUnit);
         if (c < 2) tma_load3(dst(x), tk, c * 64, it.head, tok, bar);
         else tma_load3(dst(x), tr, 0, 0, tok, bar);
@@ -223,8 +225,9 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
         const uint32_t slot = x % kRing;
         uint64_t* bar = j == tail ? sh->landed + slot : sh->full + slot;
         bar_expect_tx(bar, kUnit);
+        tails &= ~(1u << slot);
         if (j == tail) {
-          used |= 1u << slot;
+          tails |= 1u << slot;
           parity ^= 1u << slot;
         }
         for (int d = 0; d < 2; ++d)
@@ -232,15 +235,17 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
       }
     }
   }
-  // every box issued must have landed before the CTA can exit
-  if (!alive || *abort_flag) {
-    for (uint32_t s = 0; s < kRing; ++s)
-      if (used >> s & 1u) bar_drain(sh->landed + s, (parity >> s & 1u) ^ 1u);
-    for (uint32_t k = x > kRing ? x - kRing : 0u; k < x; ++k)
-      bar_drain(sh->full + k % kRing, (k / kRing) & 1u);
-    if (nq0) bar_drain(sh->q_full, (nq0 - 1) & 1u);
-    if (nq1) bar_drain(sh->q_full + 1, (nq1 - 1) & 1u);
+  // Every box issued must have landed before the CTA can exit: the last unit of
+  // each place (what was there before it has been read) and the last Q tiles.
+  // Always, not only after an abort seen here: another role's wait may run out
+  // later.
+  for (uint32_t k = x > kRing ? x - kRing : 0u; k < x; ++k) {
+    const uint32_t s = k % kRing;
+    if (tails >> s & 1u) bar_drain(sh->landed + s, (parity >> s & 1u) ^ 1u);
+    else bar_drain(sh->full + s, (k / kRing) & 1u);
   }
+  if (nq0) bar_drain(sh->q_full, (nq0 - 1) & 1u);
+  if (nq1) bar_drain(sh->q_full + 1, (nq1 - 1) & 1u);
 }
 
 // -------------------------------------------------------------------- MMAs
@@ -867,6 +872,7 @@ extern "C" int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t to
   p.splits = static_cast<int32_t>(splits);
   p.chunk_tokens = static_cast<int32_t>(chunk * pda::kKeys);
   p.wait_limit_us = plan->wait_limit_us;
+  p.inject = plan->inject;
   p.scratch_bytes = pda::kStatusHeaderBytes;
   if (splits > 1) {
     const int64_t cells = splits * rows * plan->num_qo_heads;
@@ -927,6 +933,7 @@ extern "C" int pda_mla_prefill(const pda_prefill_plan_t* plan, const void* q, in
   a.causal = causal ? 1 : 0;
   a.splits = plan->splits;
   a.chunk_tiles = plan->chunk_tokens / kKeys;
+  a.inject = plan->inject;
   CUtensorMap tq, tk, tr, tv;
   if (!make_map3(&tq, q, kQDim, a.heads, a.rows, q_stride_head, q_stride_row, 64, 1, kRowsTile) ||
       !make_map3(&tk, k, kNope, a.heads, a.tokens, kv_stride_head, kv_stride_token, 64, 1, kKeys) ||

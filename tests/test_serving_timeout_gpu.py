@@ -131,3 +131,46 @@ def test_expand_times_out(tokens, heads, hook):
     y, mag = ref.product(x[some, None, :512].expand(-1, heads, 512), w)
     mag = mag * ref.sum_bound(512)
     close(kv[some], y, mag + ref.BF16_HALF * (y.abs() + mag), "after the timeout")
+
+
+# Keys in one chunk (out and lse stay unwritten) and in several; a last tile that is cleared
+# behind the last key, and none. The work counters of the scratch have to survive.
+@pytest.mark.parametrize("reqs,heads,chunks", [
+    ([(1, 1)], 1, False), ([(300, 300), (5, 128)], 2, False), ([(7, 130)] * 40, 16, False),
+    ([(40, 3000)], 2, True), ([(3, 1024), (1, 900)], 4, True)])
+def test_prefill_times_out(reqs, heads, chunks):
+    g = torch.Generator().manual_seed(heads)
+    qo, tok = [0], [0]
+    for r, n in reqs:
+        qo.append(qo[-1] + r)
+        tok.append(tok[-1] + n)
+    rows, toks = qo[-1], tok[-1]
+    bad, good = decoders(heads, B.PDA_INJECT_WITHHOLD_KV, batch=len(reqs),
+                         max_kv=max(n for _, n in reqs))
+    pre = [B.Prefill(dec.plan, rows, toks, device=DEV) for dec in (bad, good)]
+    pre[1].scratch = pre[0].scratch
+    assert (pre[0].plan.splits > 1) == chunks
+    q = torch.randn(rows, heads, 192, generator=g).to(torch.bfloat16)
+    kv = torch.randn(toks, heads, 256, generator=g).to(torch.bfloat16)
+    rope = torch.randn(toks, 64, generator=g).to(torch.bfloat16)
+    dq, dkv, drope = q.to(DEV), kv.to(DEV), rope.to(DEV)
+    dqo, dtok = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in (qo, tok))
+    out = torch.full((rows, heads, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((rows, heads), 7.0, device=DEV)
+
+    def run(p):
+        p.run(dq, dkv[..., :128], dkv[..., 128:], drope, dqo, dtok, 192 ** -0.5, out, lse)
+
+    for _ in range(2):
+        run(pre[0])
+        assert timed_out(pre[0])
+        if not chunks:
+            assert bool((out == 7).all()) and bool((lse == 7).all())
+    for _ in range(2):
+        run(pre[1])
+        torch.cuda.synchronize()
+        assert pre[1].status() == 0
+    o, ob, l_, lb = ref.attention(q, kv[..., :128], kv[..., 128:], rope, qo, tok, causal=True,
+                                  windows=None, scale=192 ** -0.5)
+    close(out, o, ob, "out after the timeout")
+    close(lse, l_, lb, "lse after the timeout")
