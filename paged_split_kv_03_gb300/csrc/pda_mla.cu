@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256) gather_latent(const __grid_constant__ Gat
 // SM holds, decides (pda_mla_project). The output tile passes through the stages'
 // memory so that a warp writes whole 256-byte rows. Measured: absorb of 1024 rows x
 // 128 heads 49 us to bf16 (4.4 TB/s, 151 of the 218 MB written, which a plain fill
-// does at 4.0 TB/s), 37 us to E4M3; project 37 us (5.0 TB/s); one row of 128 heads 6.0
+// does at 4.0 TB/s), 38 us to E4M3; project 37 us (5.0 TB/s); one row of 128 heads 6.0
 // and 5.0 us.
 
 enum { kAbsorb = 0, kProject = 1 };
@@ -251,37 +251,19 @@ __global__ void __launch_bounds__(192)
     }
   } else {
     const int quad = warp & 3;
+    // the rope channels pass through: each column block takes its share of the
+    // rows, loaded here and written with the tile (a CTA that gives up writes nothing)
+    constexpr int kShare = OP == kAbsorb ? 8 * N / kLat : 1;  // rows per group of eight lanes
+    uint4 rope[kShare];
+    int t[kShare];
     if constexpr (OP == kAbsorb) {
-      // the rope channels pass through: each column block takes its share of the
-      // rows, all loads before the first store
-      constexpr int kShare = 8 * N / kLat;  // rows per group of eight lanes
-      uint4 v[kShare];
-      int t[kShare];
 #pragma unroll
       for (int i = 0; i < kShare; ++i) {
         t[i] = t0 + quad * 32 + (blockIdx.x * kShare + i) * 4 + (lane >> 3);
         if (t[i] < rows)
-          v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + t[i] * a.q_row + h * a.q_head + kNope) +
-                       (lane & 7));
+          rope[i] = __ldg(reinterpret_cast<const uint4*>(a.q + t[i] * a.q_row + h * a.q_head + kNope) +
+                          (lane & 7));
       }
-#pragma unroll
-      for (int i = 0; i < kShare; ++i) {
-        if (t[i] >= rows) continue;
-        const int64_t o = (static_cast<int64_t>(t[i]) * a.heads + h) * kLatRow + kLat + (lane & 7) * 8;
-        if constexpr (E4M3) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          uint32_t c[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            c[e] = e4m3x2(__uint_as_float(w[e] << 16) * a.inv_scale,
-                          __uint_as_float(w[e] & 0xFFFF0000u) * a.inv_scale);
-          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + o) =
-              make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-        } else {
-          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o) = v[i];
-        }
-      }
-      __syncwarp();
     }
     const bool ok = bar_wait(&done, 0, abort_flag, a);
     if (__all_sync(0xffffffffu, ok) && *abort_flag == 0 && t0 + quad * 32 < rows) {
@@ -324,6 +306,25 @@ __global__ void __launch_bounds__(192)
                                                         ((piece ^ (r & 7)) % kPieces) * 16);
         const int64_t o = (static_cast<int64_t>(t) * a.heads + h) * (OP == kAbsorb ? kLatRow : kNope) + n0;
         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + o * (E4M3 ? 1 : 2) + piece * 16) = v;
+      }
+      if constexpr (OP == kAbsorb) {
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) {
+          if (t[i] >= rows) continue;
+          const int64_t o = (static_cast<int64_t>(t[i]) * a.heads + h) * kLatRow + kLat + (lane & 7) * 8;
+          if constexpr (E4M3) {
+            const uint32_t w[4] = {rope[i].x, rope[i].y, rope[i].z, rope[i].w};
+            uint32_t c[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              c[e] = e4m3x2(__uint_as_float(w[e] << 16) * a.inv_scale,
+                            __uint_as_float(w[e] & 0xFFFF0000u) * a.inv_scale);
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.out) + o) =
+                make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+          } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + o) = rope[i];
+          }
+        }
       }
     }
   }

@@ -174,3 +174,14 @@ def test_prefill_times_out(reqs, heads, chunks):
                                   windows=None, scale=192 ** -0.5)
     close(out, o, ob, "out after the timeout")
     close(lse, l_, lb, "lse after the timeout")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,heads", [(1, 1), (200, 16)])
+def test_absorb_writes_nothing_after_a_timeout(rows, heads, kind):
+    """The rope channels, which pass through, are left unwritten with the rest."""
+    bad, _ = decoders(heads, B.PDA_INJECT_WITHHOLD_KV, kind=kind)
+    q, w, out = absorb_case(kind, rows, heads)
+    B.pda_mla_absorb(bad.plan, q.to(DEV), w.to(DEV), 0.011, out, None, bad.scratch)
+    assert timed_out(bad)
+    assert bool((out == 77).all())
