@@ -430,13 +430,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   const int64_t pairs = static_cast<int64_t>((max(rows, 0) + 255) / 256) * a.heads;
   const int64_t me = blockIdx.x / 2, of = gridDim.x / 2;
   const int64_t f0 = pairs * me / of, f1 = pairs * (me + 1) / of;
+  // The latents come from the kernel in front of this one. Every thread waits here
+  // for it (so does a CTA without work: what follows has to follow both kernels),
+  // and no bounded wait below counts its time.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t hooks = PDA_INJECT_WITHHOLD_KV |
                          (rank ? PDA_INJECT_WITHHOLD_CTA1 : PDA_INJECT_WITHHOLD_CTA0);
   if (warp == 0) {
     if (lane == 0) {
-      // the latents come from the kernel in front of this one (every CTA waits,
-      // with or without work, so that what follows follows both kernels)
-      asm volatile("griddepcontrol.wait;" ::: "memory");
       // the leader's barriers count the bytes of both CTAs
       const uint32_t a_bar = on_leader(&a_full);
       bool alive = (a.inject & hooks) == 0u;
