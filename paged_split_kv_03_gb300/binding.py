@@ -178,7 +178,9 @@ def _ptr(x) -> Optional[int]:
 _RAW_STREAM = None
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, dev=None) -> Optional[int]:
+    """The raw handle of a stream; None: the current one (of ``dev``, where it is known that
+    tensors of that device exist)."""
     if stream is None:
         global _RAW_STREAM
         if _RAW_STREAM is None:
@@ -186,7 +188,7 @@ def _stream(stream) -> Optional[int]:
             from torch._C import _cuda_getCurrentRawStream
             from torch.cuda import current_device
             _RAW_STREAM = _cuda_getCurrentRawStream, current_device
-        return _RAW_STREAM[0](_RAW_STREAM[1]())
+        return _RAW_STREAM[0](_RAW_STREAM[1]() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -267,27 +269,27 @@ def pda_append_kv(plan: PdaPlan, k_new, v_new, page_table, kv_indptr, kv_len, qo
 
 def _types():
     """(bfloat16, int32, int64, float32, float8_e4m3fn, uint8) of torch, looked up once."""
-    global _TYPES
+    global _TYPES, _INT8
     if _TYPES is None:
         import torch
+        _INT8 = torch.int8
         _TYPES = (torch.bfloat16, torch.int32, torch.int64, torch.float32, torch.float8_e4m3fn,
                   torch.uint8)
     return _TYPES
 
 
-_TYPES = None
+_TYPES = _INT8 = None
 
 
-def _chk(where: str, name: str, t, dtype, shape, tail=None) -> None:
-    """The type, sizes and strides that a call with raw pointers assumes and the library cannot
-    see: ``tail`` are the strides of the last dimensions (None: contiguous)."""
-    if (t.dtype is dtype and t.is_cuda and t.shape == shape and
+def _chk(where: str, name: str, t, dev: int, dtype, shape, tail=None) -> None:
+    """The device, type, sizes and strides that a call with raw pointers assumes and the library
+    cannot see: ``tail`` are the strides of the last dimensions (None: contiguous)."""
+    if (t.dtype is dtype and t.get_device() == dev and t.shape == shape and
             (t.is_contiguous() if tail is None else t.stride()[-len(tail):] == tail)):
         return
     if t.dtype is not dtype:
         raise ValueError(f"{where}: {name} is {t.dtype}, not {dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{where}: {name} is not on a CUDA device")
+    _chk_device(where, name, t, dev)
     if t.shape != shape:
         raise ValueError(f"{where}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     got = t.stride()
@@ -298,6 +300,66 @@ def _chk(where: str, name: str, t, dtype, shape, tail=None) -> None:
         raise ValueError(f"{where}: {name} is not contiguous")
 
 
+def _chk_device(where: str, name: str, t, dev: int) -> None:
+    got = t.get_device()
+    if got == dev:
+        return
+    if got < 0:
+        raise ValueError(f"{where}: {name} is not on a CUDA device")
+    raise PdaError(PDA_ERR_INVALID, f"{where}: {name} is on cuda:{got}, the plan on cuda:{dev};")
+
+
+def _room(t) -> int:
+    """Bytes from a tensor's first element to the end of its memory."""
+    return t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+
+
+def _chk_scratch(where: str, t, dev: int, need: int) -> None:
+    """A scratch given as a tensor: on the plan's device, at least ``need`` bytes."""
+    if t is None or isinstance(t, int) or (t.get_device() == dev and t.nbytes >= need):
+        return
+    _chk_device(where, "the scratch", t, dev)
+    if _room(t) < need:
+        raise PdaError(PDA_ERR_SCRATCH, f"{where}: {_room(t)} bytes of scratch, not {need};")
+
+
+def _cache_needs(plan: PdaPlan):
+    """(device, types of the cache, its bytes, values of its scales), looked up once a plan."""
+    try:
+        return plan.cache_needs
+    except AttributeError:
+        pass
+    bf16, _, _, _, e4m3, u8 = _types()
+    kv, mode = plan.kv_dtype, plan.scale_mode
+    typed = bf16 if kv == PDA_BF16 else e4m3 if kv == PDA_E4M3 else _INT8
+    width = 640 if mode == PDA_SCALE_MLA_BLOCK else plan.head_dim
+    nbytes = ((plan.num_pages - 1) * plan.kv_stride_page +
+              (plan.page_size - 1) * plan.kv_stride_token +
+              (plan.num_kv_heads - 1) * plan.kv_stride_head + width) * (2 if kv == PDA_BF16 else 1)
+    values = 0 if mode == PDA_SCALE_NONE else 1 if mode == PDA_SCALE_TENSOR else \
+        plan.num_pages * plan.page_size * plan.num_kv_heads * (4 if mode == PDA_SCALE_MLA_BLOCK else 1)
+    plan.cache_needs = plan.device, (typed, u8, _INT8), nbytes, values
+    return plan.cache_needs
+
+
+def _chk_cache(where: str, side: str, pages, scale, plan: PdaPlan) -> None:
+    """The cache and its scales, where given as tensors: on the plan's device, of its type
+    (or raw bytes: uint8, int8), and large enough for its pages and strides."""
+    dev, types, need, values = _cache_needs(plan)
+    if not (pages is None or isinstance(pages, int) or
+            (pages.dtype in types and pages.get_device() == dev and pages.nbytes >= need and
+             pages.is_contiguous())):
+        if pages.dtype not in types:
+            raise ValueError(f"{where}: {side}_pages is {pages.dtype}, not {types[0]} or bytes")
+        _chk_device(where, side + "_pages", pages, dev)
+        if _room(pages) < need:
+            raise ValueError(f"{where}: {side}_pages has {_room(pages)} bytes, the plan's pages {need}")
+    if values and scale is not None and not isinstance(scale, int):
+        _chk_device(where, side + "_scale", scale, dev)
+        if scale.dtype is not _TYPES[3] or scale.numel() < values or not scale.is_contiguous():
+            raise ValueError(f"{where}: {side}_scale has to hold {values} contiguous float32")
+
+
 def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, free_pages,
                      free_count, free_left, kv_len, kv_indptr, page_table, qo_indptr, tok_indptr,
                      slot_map, positions, split_scratch, stream=None, check: bool = True) -> int:
@@ -305,51 +367,52 @@ def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, f
     include/pda.h). ``block_table`` is [rows, cols] int32, ``slot_map`` int64, the others int32;
     ``request``, ``tok_indptr``, ``slot_map`` and ``positions`` may be None."""
     _, i32, i64, _, _, _ = _types()
-    where, n = "pda_build_tables", plan.batch
+    where, n, dev = "pda_build_tables", plan.batch, plan.device
     per, ptrs, one = (n,), (n + 1,), (1,)
-    _chk(where, "cached_len", cached_len, i32, per)
-    _chk(where, "new_len", new_len, i32, per)
-    _chk(where, "kv_len", kv_len, i32, per)
-    _chk(where, "kv_indptr", kv_indptr, i32, ptrs)
-    _chk(where, "qo_indptr", qo_indptr, i32, ptrs)
-    _chk(where, "free_count", free_count, i32, one)
-    _chk(where, "free_left", free_left, i32, one)
-    _chk(where, "free_pages", free_pages, i32, (free_pages.numel(),))
-    _chk(where, "page_table", page_table, i32, (page_table.numel(),))
+    _chk(where, "cached_len", cached_len, dev, i32, per)
+    _chk(where, "new_len", new_len, dev, i32, per)
+    _chk(where, "kv_len", kv_len, dev, i32, per)
+    _chk(where, "kv_indptr", kv_indptr, dev, i32, ptrs)
+    _chk(where, "qo_indptr", qo_indptr, dev, i32, ptrs)
+    _chk(where, "free_count", free_count, dev, i32, one)
+    _chk(where, "free_left", free_left, dev, i32, one)
+    _chk(where, "free_pages", free_pages, dev, i32, (free_pages.numel(),))
+    _chk(where, "page_table", page_table, dev, i32, (page_table.numel(),))
     rows, cols = block_table.shape
-    _chk(where, "block_table", block_table, i32, (rows, cols), (1,))
+    _chk(where, "block_table", block_table, dev, i32, (rows, cols), (1,))
     cap = 0x7fffffff
     if request is not None:
-        _chk(where, "request", request, i32, per)
+        _chk(where, "request", request, dev, i32, per)
         request = request.data_ptr()
     if tok_indptr is not None:
-        _chk(where, "tok_indptr", tok_indptr, i32, ptrs)
+        _chk(where, "tok_indptr", tok_indptr, dev, i32, ptrs)
         tok_indptr = tok_indptr.data_ptr()
     if slot_map is not None:
         cap = slot_map.numel()
-        _chk(where, "slot_map", slot_map, i64, (cap,))
+        _chk(where, "slot_map", slot_map, dev, i64, (cap,))
         slot_map = slot_map.data_ptr()
     if positions is not None:
-        _chk(where, "positions", positions, i32, (positions.numel(),))
+        _chk(where, "positions", positions, dev, i32, (positions.numel(),))
         cap = min(cap, positions.numel())
         positions = positions.data_ptr()
+    _chk_scratch(where, split_scratch, dev, 4)
     t = PdaTables(cached_len.data_ptr(), new_len.data_ptr(), request, block_table.data_ptr(),
                   block_table.stride(0) if rows > 1 else cols, free_pages.data_ptr(),
                   free_count.data_ptr(), free_left.data_ptr(), kv_len.data_ptr(),
                   kv_indptr.data_ptr(), page_table.data_ptr(), qo_indptr.data_ptr(), tok_indptr,
                   slot_map, positions, rows, cols, page_table.numel(), cap)
     rc = load_library().pda_build_tables(ctypes.byref(plan), ctypes.byref(t), _ptr(split_scratch),
-                                         _stream(stream))
+                                         _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
 
 
-def _num_rows(where: str, t):
+def _num_rows(where: str, t, dev: int):
     """Address of a one-element int32 device tensor, or None."""
     if t is None:
         return None
-    _chk(where, "num_rows", t, _types()[1], (1,))
+    _chk(where, "num_rows", t, dev, _types()[1], (1,))
     return t.data_ptr()
 
 
@@ -358,18 +421,22 @@ def pda_append_slots(plan: PdaPlan, k_new, v_new, slot_map, num_rows, k_pages, v
     """Append rows (bf16 [rows, Hkv, D], any row stride) through a slot map (int64 [rows]);
     ``num_rows``: an int32 device tensor of one element bounding the rows, or None."""
     bf16, _, i64, _, _, _ = _types()
-    where = "pda_append_slots"
+    where, dev = "pda_append_slots", plan.device
     rows, d = slot_map.numel(), plan.head_dim
     new, tail = (rows, plan.num_kv_heads, d), (d, 1)
-    _chk(where, "k_new", k_new, bf16, new, tail)
-    _chk(where, "slot_map", slot_map, i64, (rows,))
+    _chk(where, "k_new", k_new, dev, bf16, new, tail)
+    _chk(where, "slot_map", slot_map, dev, i64, (rows,))
     if v_new is not None:
-        _chk(where, "v_new", v_new, bf16, new, tail)
+        _chk(where, "v_new", v_new, dev, bf16, new, tail)
+    _chk_cache(where, "k", k_pages, k_scale, plan)
+    if d != 576:
+        _chk_cache(where, "v", v_pages, v_scale, plan)
+    _chk_scratch(where, split_scratch, dev, 4)
     rc = load_library().pda_append_slots(
         ctypes.byref(plan), k_new.data_ptr(), _row_stride(k_new), _ptr(v_new),
         0 if v_new is None else _row_stride(v_new), slot_map.data_ptr(), rows,
-        _num_rows(where, num_rows), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-        _ptr(split_scratch), _stream(stream))
+        _num_rows(where, num_rows, dev), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
+        _ptr(split_scratch), _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -398,16 +465,17 @@ def pda_mla_absorb(plan: PdaPlan, q, w_uk, q_scale: float, q_lat, num_rows, spli
     """The query absorbed into the latent space: q bf16 [rows, Hq, 192], w_uk bf16
     [Hq, 128, 512] (any head stride), q_lat [rows, Hq, 576] bf16 or E4M3 codes."""
     bf16, _, _, _, e4m3, u8 = _types()
-    where = "pda_mla_absorb"
+    where, dev = "pda_mla_absorb", plan.device
     rows, h = q.shape[0], plan.num_qo_heads
-    _chk(where, "q", q, bf16, (rows, h, 192), (1,))
-    _chk(where, "w_uk", w_uk, bf16, (h, 128, 512), (512, 1))
-    _chk(where, "q_lat", q_lat,
+    _chk(where, "q", q, dev, bf16, (rows, h, 192), (1,))
+    _chk(where, "w_uk", w_uk, dev, bf16, (h, 128, 512), (512, 1))
+    _chk(where, "q_lat", q_lat, dev,
          bf16 if plan.q_dtype == PDA_BF16 else u8 if q_lat.dtype is u8 else e4m3, (rows, h, 576))
+    _chk_scratch(where, split_scratch, dev, 4)
     row, head = _head_strides(q)
     rc = load_library().pda_mla_absorb(
         ctypes.byref(plan), q.data_ptr(), row, head, w_uk.data_ptr(), _row_stride(w_uk), q_scale,
-        q_lat.data_ptr(), rows, _num_rows(where, num_rows), _ptr(split_scratch), _stream(stream))
+        q_lat.data_ptr(), rows, _num_rows(where, num_rows, dev), _ptr(split_scratch), _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -418,14 +486,15 @@ def pda_mla_project(plan: PdaPlan, o_lat, w_uv, out, num_rows, split_scratch, st
     """The decode's latent output projected: o_lat bf16 [rows, Hq, 512], w_uv bf16
     [Hq, 128, 512] (any head stride), out bf16 [rows, Hq, 128]."""
     bf16 = _types()[0]
-    where = "pda_mla_project"
+    where, dev = "pda_mla_project", plan.device
     rows, h = o_lat.shape[0], plan.num_qo_heads
-    _chk(where, "o_lat", o_lat, bf16, (rows, h, 512))
-    _chk(where, "w_uv", w_uv, bf16, (h, 128, 512), (512, 1))
-    _chk(where, "out", out, bf16, (rows, h, 128))
+    _chk(where, "o_lat", o_lat, dev, bf16, (rows, h, 512))
+    _chk(where, "w_uv", w_uv, dev, bf16, (h, 128, 512), (512, 1))
+    _chk(where, "out", out, dev, bf16, (rows, h, 128))
+    _chk_scratch(where, split_scratch, dev, 4)
     rc = load_library().pda_mla_project(
         ctypes.byref(plan), o_lat.data_ptr(), w_uv.data_ptr(), _row_stride(w_uv), out.data_ptr(),
-        rows, _num_rows(where, num_rows), _ptr(split_scratch), _stream(stream))
+        rows, _num_rows(where, num_rows, dev), _ptr(split_scratch), _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -443,16 +512,18 @@ def pda_mla_expand(plan: PdaPlan, k_pages, page_table, kv_indptr, tok_indptr, k_
     """Keys and values of cached tokens: latent bf16 [tokens, 576], k and v bf16
     [tokens, Hq, 128] (strided alike) are written; w_uk and w_uv bf16 [Hq, 128, 512]."""
     bf16, i32, _, _, _, _ = _types()
-    where = "pda_mla_expand"
+    where, dev = "pda_mla_expand", plan.device
     tokens, h, ptrs = latent.shape[0], plan.num_qo_heads, (plan.batch + 1,)
-    _chk(where, "w_uk", w_uk, bf16, (h, 128, 512), (512, 1))
-    _chk(where, "w_uv", w_uv, bf16, (h, 128, 512), (512, 1))
-    _chk(where, "latent", latent, bf16, (tokens, 576))
-    _chk(where, "k", k, bf16, (tokens, h, 128), (1,))
-    _chk(where, "v", v, bf16, (tokens, h, 128), (1,))
-    _chk(where, "kv_indptr", kv_indptr, i32, ptrs)
-    _chk(where, "tok_indptr", tok_indptr, i32, ptrs)
-    _chk(where, "page_table", page_table, i32, (page_table.numel(),))
+    _chk(where, "w_uk", w_uk, dev, bf16, (h, 128, 512), (512, 1))
+    _chk(where, "w_uv", w_uv, dev, bf16, (h, 128, 512), (512, 1))
+    _chk(where, "latent", latent, dev, bf16, (tokens, 576))
+    _chk(where, "k", k, dev, bf16, (tokens, h, 128), (1,))
+    _chk(where, "v", v, dev, bf16, (tokens, h, 128), (1,))
+    _chk(where, "kv_indptr", kv_indptr, dev, i32, ptrs)
+    _chk(where, "tok_indptr", tok_indptr, dev, i32, ptrs)
+    _chk(where, "page_table", page_table, dev, i32, (page_table.numel(),))
+    _chk_cache(where, "k", k_pages, k_scale, plan)
+    _chk_scratch(where, split_scratch, dev, 4)
     w_head = _row_stride(w_uk)
     if w_head != _row_stride(w_uv):
         raise ValueError(f"{where}: w_uk and w_uv differ in their head strides")
@@ -461,7 +532,7 @@ def pda_mla_expand(plan: PdaPlan, k_pages, page_table, kv_indptr, tok_indptr, k_
         ctypes.byref(plan), _ptr(k_pages), page_table.data_ptr(), kv_indptr.data_ptr(),
         tok_indptr.data_ptr(), _ptr(k_scale), w_uk.data_ptr(), w_uv.data_ptr(), w_head,
         latent.data_ptr(), k.data_ptr(), v.data_ptr(), tok, head, tokens, _ptr(split_scratch),
-        _stream(stream))
+        _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -485,27 +556,28 @@ def pda_mla_prefill(pre: PdaPrefillPlan, q, k, v, k_rope, qo_indptr, tok_indptr,
     [tokens, Hq, 128] (strided alike), k_rope bf16 [tokens, 64], out bf16 [rows, Hq, 128],
     lse fp32 [rows, Hq] or None; rows and tokens are the plan's."""
     bf16, i32, _, f32, _, _ = _types()
-    where = "pda_mla_prefill"
+    where, dev = "pda_mla_prefill", pre.device
     rows, tokens, h, n = pre.rows, pre.tokens, pre.num_qo_heads, pre.batch
-    _chk(where, "q", q, bf16, (rows, h, 192), (1,))
-    _chk(where, "k", k, bf16, (tokens, h, 128), (1,))
-    _chk(where, "v", v, bf16, (tokens, h, 128), (1,))
-    _chk(where, "k_rope", k_rope, bf16, (tokens, 64), (1,))
-    _chk(where, "qo_indptr", qo_indptr, i32, (n + 1,))
-    _chk(where, "tok_indptr", tok_indptr, i32, (n + 1,))
-    _chk(where, "out", out, bf16, (rows, h, 128))
+    _chk(where, "q", q, dev, bf16, (rows, h, 192), (1,))
+    _chk(where, "k", k, dev, bf16, (tokens, h, 128), (1,))
+    _chk(where, "v", v, dev, bf16, (tokens, h, 128), (1,))
+    _chk(where, "k_rope", k_rope, dev, bf16, (tokens, 64), (1,))
+    _chk(where, "qo_indptr", qo_indptr, dev, i32, (n + 1,))
+    _chk(where, "tok_indptr", tok_indptr, dev, i32, (n + 1,))
+    _chk(where, "out", out, dev, bf16, (rows, h, 128))
     if window is not None:
-        _chk(where, "window", window, i32, (n,))
+        _chk(where, "window", window, dev, i32, (n,))
         window = window.data_ptr()
     if lse is not None:
-        _chk(where, "lse", lse, f32, (rows, h))
+        _chk(where, "lse", lse, dev, f32, (rows, h))
         lse = lse.data_ptr()
+    _chk_scratch(where, scratch, dev, pre.scratch_bytes)
     tok, head = _same_strides(where, k, v)
     row, qhead = _head_strides(q)
     rc = load_library().pda_mla_prefill(
         ctypes.byref(pre), q.data_ptr(), row, qhead, k.data_ptr(), v.data_ptr(), tok, head,
         k_rope.data_ptr(), _row_stride(k_rope), qo_indptr.data_ptr(), tok_indptr.data_ptr(), window,
-        1 if causal else 0, sm_scale, out.data_ptr(), lse, _ptr(scratch), _stream(stream))
+        1 if causal else 0, sm_scale, out.data_ptr(), lse, _ptr(scratch), _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -603,11 +675,12 @@ class Prefill:
     """A prefill plan plus its scratch (allocated once with torch), for up to ``rows`` query
     rows and ``tokens`` keys of the MLA plan's requests; ``run`` enqueues one pda_mla_prefill."""
 
-    def __init__(self, plan: PdaPlan, rows: int, tokens: int, device="cuda"):
+    def __init__(self, plan: PdaPlan, rows: int, tokens: int, device=None):
         import torch
         self.decode_plan = plan
         self.plan, self.scratch_bytes, _ = pda_prefill_plan(plan, rows, tokens)
-        self.scratch = torch.zeros(self.scratch_bytes, dtype=torch.uint8, device=device)
+        self.scratch = torch.zeros(self.scratch_bytes, dtype=torch.uint8,
+                                   device=f"cuda:{plan.device}" if device is None else device)
 
     def run(self, q, k, v, k_rope, qo_indptr, tok_indptr, sm_scale, out, lse, window=None,
             causal=True, stream=None):

@@ -1,0 +1,53 @@
+"""The calls around decode on the layouts that the plan allows beside the dense ones: caches
+that are views of larger memory or raw addresses, typed or as bytes, tokens and pages padded."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import serving_ref as ref
+from paged_split_kv_03_gb300 import binding as B
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+PAGE, PAGES, HEADS, TOKENS = 16, 6, 2, 50
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def forms(cache):
+    """The same memory as its plan's type, as bytes of either sign, and as an address."""
+    return [cache, cache.view(torch.uint8), cache.view(torch.int8), cache.data_ptr()]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_caches_as_views_bytes_and_addresses(kind):
+    """A layer's cache inside a pool of layers, given in each form: the same rows go in and
+    come out, the layers beside it stay as they were."""
+    g = torch.Generator().manual_seed(3)
+    dec = B.Decoder(ref.mla_plan(HEADS, kind=kind, page=PAGE, pages=PAGES), device=DEV)
+    dt = torch.bfloat16 if kind == "bf16" else torch.float8_e4m3fn
+    pool = torch.zeros(3, PAGES, PAGE, 1, 576, dtype=torch.uint8, device=DEV).to(dt)
+    scale = None if kind == "bf16" else torch.tensor([0.02], device=DEV)
+    x = torch.randn(TOKENS, 1, 576, generator=g).to(torch.bfloat16).to(DEV)
+    slots = torch.randperm(PAGE * PAGES, generator=g)[:TOKENS].to(DEV)
+    table, ptr, tok = ints(*range(PAGES)), ints(0, PAGES), ints(0, PAGE * PAGES)
+    w = (torch.randn(HEADS, 256, 512, generator=g) * 512 ** -0.5).to(torch.bfloat16).to(DEV)
+    seen = []
+    for cache in forms(pool[1]):
+        pool.view(torch.uint8).fill_(0)
+        B.pda_append_slots(dec.plan, x, None, slots, None, cache, None, scale, None, dec.scratch)
+        latent = torch.full((PAGE * PAGES, 576), 7.0, dtype=torch.bfloat16, device=DEV)
+        kv = torch.empty(PAGE * PAGES, HEADS, 256, dtype=torch.bfloat16, device=DEV)
+        B.pda_mla_expand(dec.plan, cache, table, ptr, tok, scale, w[:, :128], w[:, 128:], latent,
+                         kv[..., :128], kv[..., 128:], dec.scratch)
+        torch.cuda.synchronize()
+        assert dec.status() == 0
+        assert int(torch.count_nonzero(pool.view(torch.uint8)[0::2])) == 0
+        seen.append((pool.view(torch.uint8).cpu().clone(), latent.cpu(), kv.cpu()))
+    if kind == "bf16":
+        assert torch.equal(seen[0][1][slots.cpu()], x[:, 0].cpu())
+    for other in seen[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(seen[0], other))
