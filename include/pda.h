@@ -434,10 +434,11 @@ int pda_mla_project(const pda_plan_t* plan, const void* o_lat, const void* w_uv,
  *               of 8) shared by both
  *   tokens      rows of latent, k and v; rows past tok_indptr[batch] are left
  *               as they were
- * A token whose page id is out of range (PDA_STATUS_PAGE_OOB) or whose request
- * has more than the plan's max_kv_len tokens (PDA_STATUS_KV_LEN_GT_MAX) reads
- * as zeros. tok_indptr[batch] > tokens sets PDA_STATUS_TOKENS_GT_CAP and
- * writes the first `tokens` rows. */
+ * A token whose page id is out of range, or that lies behind its request's
+ * pages in page_table (PDA_STATUS_PAGE_OOB), or whose request has more than the
+ * plan's max_kv_len tokens (PDA_STATUS_KV_LEN_GT_MAX), reads as zeros.
+ * tok_indptr[batch] > tokens sets PDA_STATUS_TOKENS_GT_CAP and writes the first
+ * `tokens` rows. */
 int pda_mla_expand(const pda_plan_t* plan, const void* k_pages, const int32_t* page_table,
                    const int32_t* kv_indptr, const int32_t* tok_indptr, const float* k_scale,
                    const void* w_uk, const void* w_uv, int64_t w_stride_head, void* latent,

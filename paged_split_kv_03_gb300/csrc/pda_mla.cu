@@ -68,7 +68,9 @@ __global__ void __launch_bounds__(256) gather_latent(const __grid_constant__ Gat
   }
   int page = 0;
   if (ok) {
-    page = __ldg(a.page_table + __ldg(a.kv_indptr + lo) + (i >> a.page_shift));
+    // (a token behind its request's pages has none: the next entry is another request's)
+    const int p0 = __ldg(a.kv_indptr + lo), p1 = __ldg(a.kv_indptr + lo + 1);
+    page = (i >> a.page_shift) < p1 - p0 ? __ldg(a.page_table + p0 + (i >> a.page_shift)) : -1;
     if (page < 0 || page >= a.num_pages) {
       if (lane == 0) atomicOr(a.status, PDA_STATUS_PAGE_OOB);
       ok = false;

@@ -51,3 +51,25 @@ def test_caches_as_views_bytes_and_addresses(kind):
         assert torch.equal(seen[0][1][slots.cpu()], x[:, 0].cpu())
     for other in seen[1:]:
         assert all(torch.equal(a, b) for a, b in zip(seen[0], other))
+
+
+def test_expand_tokens_behind_their_pages():
+    """A request with more tokens than its entries of the page table hold: the rest reads as
+    zeros, not as the next request's pages, and says so."""
+    g = torch.Generator().manual_seed(4)
+    dec = B.Decoder(ref.mla_plan(HEADS, page=PAGE, pages=PAGES, batch=3), device=DEV)
+    cache = torch.randn(PAGES, PAGE, 1, 576, generator=g).to(torch.bfloat16)
+    table = [4, 1, 3, 0, 2]
+    tok = [0, 2 * PAGE + 5, 3 * PAGE + 5, 3 * PAGE + 25]  # requests of 2, 1 and 2 pages
+    latent = torch.full((tok[3], 576), 7.0, dtype=torch.bfloat16, device=DEV)
+    kv = torch.full((tok[3], HEADS, 256), 7.0, dtype=torch.bfloat16, device=DEV)
+    w = torch.randn(HEADS, 256, 512, generator=g).to(torch.bfloat16).to(DEV)
+    B.pda_mla_expand(dec.plan, cache.to(DEV), ints(*table), ints(0, 2, 3, 5), ints(*tok), None,
+                     w[:, :128], w[:, 128:], latent, kv[..., :128], kv[..., 128:], dec.scratch)
+    torch.cuda.synchronize()
+    assert dec.status() == B.PDA_STATUS_PAGE_OOB
+    want = torch.cat([cache[4, :, 0], cache[1, :, 0], torch.zeros(5, 576, dtype=torch.bfloat16),
+                      cache[3, :, 0], cache[0, :, 0], cache[2, :4, 0]])
+    assert torch.equal(latent.cpu(), want)
+    assert bool((kv[2 * PAGE:2 * PAGE + 5] == 0).all())
+    assert not bool((kv == 7).all(-1).any())  # every row was written
