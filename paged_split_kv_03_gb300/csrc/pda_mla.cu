@@ -385,6 +385,26 @@ constexpr int kExpOut = 8 * 2048;  // 32 rows x 64 bytes a warp
 constexpr int kExpSmem = kExpA + kExpStages * kExpB + kExpOut + 1024;
 constexpr int kExpThreads = 64 + 8 * 32;  // loads, MMAs, eight warps that write
 
+// Every box of a pair has landed when this returns: the leader's part after a
+// timeout in either CTA (without one the MMAs have read every box). The leader's
+// barriers count both CTAs' bytes; x0 and x1 ring units and t0 and t1 row tiles
+// were loaded by CTA 0 and 1, all within a ring (a tile) of what the MMAs gave back.
+// A box that only CTA 1 issued is announced first, one that it did not issue is
+// taken off. Out of line, so that a CTA's end stays short.
+__device__ __noinline__ void drain_pair(uint64_t* full, uint64_t* a_full, uint32_t x0, uint32_t x1,
+                                        uint32_t t0, uint32_t t1) {
+  auto settle = [](uint64_t* bar, uint32_t k, uint32_t mine, uint32_t other, uint32_t bytes,
+                   uint32_t parity) {
+    if (k >= mine) bar_expect_tx(bar, bytes);
+    else if (k >= other) bar_complete_tx(bar, bytes);
+    bar_drain(bar, parity & 1u);
+  };
+  const uint32_t x = max(x0, x1), t = max(t0, t1);
+  for (uint32_t k = x > kExpStages ? x - kExpStages : 0u; k < x; ++k)
+    settle(full + k % kExpStages, k, x0, x1, kExpB, k / kExpStages);
+  if (t) settle(a_full, t - 1, t0, t1, kExpA, t - 1);
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
     expand(const __grid_constant__ ExpandArgs a, const __grid_constant__ CUtensorMap ta,
            const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
@@ -551,26 +571,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kExpThreads, 1)
   if (tid == 0 && *abort_flag) cluster_store(on_cta(&abort_word, rank ^ 1u), 1u);
   __syncwarp();
   cluster_sync();  // the pair's barriers and shared memory are used until here
-  // Every box issued must have landed before either CTA can exit. Without a
-  // timeout the MMAs have read them all. After one, in either CTA (both know by
-  // now), the leader waits on its barriers, which count both CTAs' bytes: boxes
-  // that only CTA 1 issued are announced first, those that it did not issue are
-  // taken off. Both counts are within the ring of what the MMAs released.
+  // every box issued must have landed before either CTA can exit
   if (*abort_flag) {
-    if (tid == 0 && rank == 0) {
-      auto settle = [&](uint64_t* bar, uint32_t k, uint32_t mine, uint32_t other, uint32_t bytes,
-                        uint32_t parity) {
-        if (k >= mine) bar_expect_tx(bar, bytes);
-        else if (k >= other) bar_complete_tx(bar, bytes);
-        bar_drain(bar, parity & 1u);
-      };
-      const uint32_t x0 = issued_units, x1 = cluster_load(on_cta(&issued_units, 1));
-      const uint32_t t0 = issued_tiles, t1 = cluster_load(on_cta(&issued_tiles, 1));
-      const uint32_t x = max(x0, x1), t = max(t0, t1);
-      for (uint32_t k = x > kExpStages ? x - kExpStages : 0u; k < x; ++k)
-        settle(full + k % kExpStages, k, x0, x1, kExpB, k / kExpStages);
-      if (t) settle(&a_full, t - 1, t0, t1, kExpA, t - 1);
-    }
+    if (tid == 0 && rank == 0)
+      drain_pair(full, &a_full, issued_units, cluster_load(on_cta(&issued_units, 1)), issued_tiles,
+                 cluster_load(on_cta(&issued_tiles, 1)));
     __syncwarp();
     cluster_sync();
   }
