@@ -64,7 +64,7 @@ def peaks():
     return 6800.0, "fallback"
 
 
-KERNEL_SOURCES = {"stage1": ("pda_tc.cu", "pda_ptx.cuh", "pda_internal.h")}
+KERNEL_SOURCES = {"stage1": ("pda_tc.cu", "pda_ptx.cuh", "pda_cvt.cuh", "pda_internal.h")}
 
 
 def source_sha(kernel: str = "stage1") -> str:

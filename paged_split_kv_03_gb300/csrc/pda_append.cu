@@ -19,6 +19,7 @@
 #include <cstring>
 
 #include "pda.h"
+#include "pda_cvt.cuh"
 #include "pda_internal.h"
 
 namespace pda {
@@ -39,13 +40,6 @@ struct AppendArgs {
   int64_t sp, st, sh;  // cache strides, elements
   int batch, hkv, page_size, num_pages, max_q_len;
 };
-
-// Two floats -> two E4M3 codes (RNE, saturating to +-448): low byte from `lo`.
-__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // Two floats -> two symmetric int8 codes (nearest, ties to even, clamped to
 // +-127; NaN -> 0): low byte from `lo`.

@@ -3,7 +3,6 @@
 // cached latents gathered and expanded into keys and values for a prefill.
 
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -11,6 +10,7 @@
 #include <cstring>
 
 #include "pda.h"
+#include "pda_cvt.cuh"
 #include "pda_internal.h"
 #include "pda_ptx.cuh"
 
@@ -98,12 +98,9 @@ __global__ void __launch_bounds__(256) gather_latent(const __grid_constant__ Gat
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint16_t code = static_cast<uint16_t>((e < 2 ? w.x : w.y) >> ((e & 1) * 16));
-          uint32_t h;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(code));
-          const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
+          const float2 f = e4m3x2_to_f2(code);
           // one rounding to bf16: the products' operand type (2^-9 relative)
-          const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * s, f.y * s);
-          out[e] = *reinterpret_cast<const uint32_t*>(&r);
+          out[e] = bf16x2(f.x * s, f.y * s);
         }
         o = make_uint4(out[0], out[1], out[2], out[3]);
       }
@@ -153,18 +150,6 @@ struct ProductCfg {
   static constexpr int kTmem = N < 32 ? 32 : N;
   static_assert(kStages * kStage >= 128 * N * 2, "the output tile fits the stages");
 };
-
-// Two floats -> two E4M3 codes (RNE, saturating): low byte from `lo`.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 template <int OP, int N, int STAGES, bool E4M3>
 __global__ void __launch_bounds__(192)

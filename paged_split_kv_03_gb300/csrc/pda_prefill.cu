@@ -42,6 +42,7 @@
 #include <cstring>
 
 #include "pda.h"
+#include "pda_cvt.cuh"
 #include "pda_internal.h"
 #include "pda_ptx.cuh"
 
@@ -593,7 +594,7 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
           p0 = ex2(p0);
           p1 = ex2(p1);
           sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[e]) : "f"(p1), "f"(p0));
+          w[e] = bf16x2(p0, p1);
         }
         tmem_st16(t_s + c * 16, w);
         if (c == 1) {  // the first 64 keys: P V starts on them
@@ -668,11 +669,8 @@ __device__ void softmax_role(const PrefillArgs& a, Shared* sh, uint32_t tmem, in
       if (final) {
         uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const __nv_bfloat162 h =
-              __floats2bfloat162_rn(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-          w[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
+        for (int e = 0; e < 16; ++e)
+          w[e] = bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
         put(w, reinterpret_cast<char*>(a.out + at0 * kDv + c), static_cast<int64_t>(a.heads) * kDv * 2);
       } else {
 #pragma unroll
@@ -821,10 +819,8 @@ __global__ void __launch_bounds__(256) prefill_join(const __grid_constant__ Pref
     }
   }
   const float inv = sum > 0.f ? 1.f / sum : sum;
-  const __nv_bfloat162 w0 = __floats2bfloat162_rn(o[0] * inv, o[1] * inv);
-  const __nv_bfloat162 w1 = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
   *reinterpret_cast<uint2*>(a.out + item * kDv + lane * 4) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&w0), *reinterpret_cast<const uint32_t*>(&w1));
+      make_uint2(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv));
   if (lane == 0 && a.lse) a.lse[item] = sum == 0.f ? -INFINITY : (m + __log2f(sum)) * kLn2;
 }
 

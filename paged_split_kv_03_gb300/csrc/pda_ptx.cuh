@@ -264,17 +264,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t parity, volatile 
     }
   }
 }
-// The same for a converged warp, warp-uniform, with its slow part out of line.
+// The same out of line, for a thread whose few instructions count.
 template <class Args>
 __device__ __noinline__ bool bar_wait_slow(uint64_t* b, uint32_t parity, volatile int* abort_flag,
                                            const Args& a) {
   return bar_wait(b, parity, abort_flag, a);
-}
-template <class Args>
-__device__ __forceinline__ bool bar_wait_warp(uint64_t* b, uint32_t parity,
-                                              volatile int* abort_flag, const Args& a) {
-  if (__all_sync(0xffffffffu, bar_try(b, parity))) return true;
-  return __all_sync(0xffffffffu, bar_wait_slow(b, parity, abort_flag, a));
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {

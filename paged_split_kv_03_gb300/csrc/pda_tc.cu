@@ -51,6 +51,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "pda_cvt.cuh"
 #include "pda_internal.h"
 #include "pda_ptx.cuh"
 
@@ -143,12 +144,6 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// Two floats -> two E4M3 codes (RNE, saturating): low byte from `lo`.
-__device__ __forceinline__ uint16_t f2_to_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 // P of two columns as two E4M3 terms each, P = P1 + P2 (low bytes: `lo`),
 // through f16x2: P <= 2^8 rounds to f16 (11 bits), P1 = E4M3(P) and the
 // residual P - P1 (exact in f16) gives P2 = E4M3(P - P1).
@@ -159,12 +154,6 @@ __device__ __forceinline__ void p_terms(float lo, float hi, uint16_t& c1, uint16
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(b) : "h"(c1));
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(b));
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(c2) : "r"(r));
-}
-// Two E4M3 codes -> two floats (exact): .x from the low byte.
-__device__ __forceinline__ float2 e4m3x2_to_f2(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  return __half22float2(*reinterpret_cast<__half2*>(&h));
 }
 
 // Barrier of the NT softmax threads (named barrier 1) that also ORs a predicate.
@@ -1353,7 +1342,7 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
             float v1 = __uint_as_float(raw[k][e / 2] & 0xFFFF0000u) * up;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              const uint16_t c2 = f2_to_e4m3x2(v0, v1);
+              const uint16_t c2 = e4m3x2(v0, v1);
               const float2 back = e4m3x2_to_f2(c2);
               codes[t][e] = static_cast<uint8_t>(c2 & 0xFF);
               codes[t][e + 1] = static_cast<uint8_t>(c2 >> 8);
