@@ -73,3 +73,45 @@ def test_expand_tokens_behind_their_pages():
     assert torch.equal(latent.cpu(), want)
     assert bool((kv[2 * PAGE:2 * PAGE + 5] == 0).all())
     assert not bool((kv == 7).all(-1).any())  # every row was written
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "e4m3_token", "records"])
+def test_latent_cache_with_padded_tokens_and_pages(kind):
+    """Tokens and pages further apart than their data: what lies between is neither read nor
+    written, and the rows are those of the dense cache."""
+    g = torch.Generator().manual_seed(5)
+    width = 640 if kind == "records" else 576
+    x = torch.randn(TOKENS, 1, 576, generator=g).to(torch.bfloat16).to(DEV)
+    slots = torch.randperm(PAGE * PAGES, generator=g)[:TOKENS].to(DEV)
+    w = (torch.randn(HEADS, 256, 512, generator=g) * 512 ** -0.5).to(torch.bfloat16).to(DEV)
+    table, ptr, tok = ints(*reversed(range(PAGES))), ints(0, PAGES), ints(0, PAGE * PAGES)
+    seen = []
+    for tpad, ppad in ((0, 0), (16, 0), (64, 48)):
+        p = ref.mla_plan(HEADS, kind=kind, page=PAGE, pages=PAGES)
+        p.kv_stride_token = p.kv_stride_head = width + tpad
+        p.kv_stride_page = PAGE * (width + tpad) + ppad
+        dec = B.Decoder(p, device=DEV)
+        dt = torch.bfloat16 if kind == "bf16" else torch.uint8
+        # (0x7F7F is a NaN in bf16, 0x7F one in E4M3)
+        whole = torch.full((PAGES * p.kv_stride_page * (2 if kind == "bf16" else 1),), 0x7F,
+                           dtype=torch.uint8, device=DEV)
+        cache = whole.view(dt).as_strided((PAGES, PAGE, 1, width),
+                                          (p.kv_stride_page, width + tpad, width + tpad, 1))
+        cache.zero_()
+        scale = torch.tensor([0.02], device=DEV) if kind == "e4m3" else \
+            torch.ones(PAGES, PAGE, 1, device=DEV) if kind == "e4m3_token" else \
+            torch.ones(PAGES, PAGE, 1, 4, device=DEV) if kind == "records" else None
+        B.pda_append_slots(dec.plan, x, None, slots, None, cache, None, scale, None, dec.scratch)
+        latent = torch.full((PAGE * PAGES, 576), 7.0, dtype=torch.bfloat16, device=DEV)
+        kv = torch.empty(PAGE * PAGES, HEADS, 256, dtype=torch.bfloat16, device=DEV)
+        B.pda_mla_expand(dec.plan, cache, table, ptr, tok, scale, w[:, :128], w[:, 128:], latent,
+                         kv[..., :128], kv[..., 128:], dec.scratch)
+        torch.cuda.synchronize()
+        assert dec.status() == 0
+        between = torch.ones_like(whole, dtype=torch.bool)
+        between.view(dt if dt is torch.uint8 else torch.int16).as_strided(cache.shape, cache.stride()).zero_()
+        assert bool((whole[between] == 0x7F).all())
+        seen.append((cache.contiguous().view(torch.uint8).cpu(), latent.cpu(), kv.cpu(),
+                     None if scale is None else scale.cpu()))
+    for other in seen[1:]:
+        assert all(a is b is None or torch.equal(a, b) for a, b in zip(seen[0], other))
