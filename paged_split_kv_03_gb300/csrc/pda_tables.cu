@@ -315,8 +315,8 @@ extern "C" int pda_build_tables(const pda_plan_t* plan, const pda_tables* tables
   // kEntriesPerLane entries when the requests fill the capacities evenly.
   const int per_cta = (plan->batch + groups - 1) / groups;
   const int lanes = 32 * (per_cta < pda::kWarps ? pda::kWarps / per_cta : 1);
-  const int64_t entries =
-      (static_cast<int64_t>(t.page_table_cap) + t.rows_cap) / plan->batch;
+  const int64_t rows = t.slot_map || t.positions ? t.rows_cap : 0;  // none are listed without
+  const int64_t entries = (t.page_table_cap + rows) / plan->batch;
   int64_t slices = (entries + lanes * pda::kEntriesPerLane - 1) / (lanes * pda::kEntriesPerLane);
   slices = slices < 1 ? 1 : (slices > 32 ? 32 : slices);
   pda::build_tables<<<dim3(groups, static_cast<unsigned>(slices)), pda::kThreads, 0,
