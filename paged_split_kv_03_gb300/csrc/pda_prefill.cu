@@ -190,7 +190,8 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
   ItemReader reader(sh);
   Item it{};
   uint32_t x = 0, nq0 = 0, nq1 = 0;  // ring unit, Q tiles
-  uint32_t tails = 0u, parity = 0u;  // `landed`: places whose last unit uses it, uses mod 2
+  uint32_t parity = 0u;              // uses of each place's `landed` mod 2
+  uint32_t tail0 = ~0u - kRing, tail1 = tail0;  // first V units of the last two tiles that use it
   bool alive = (a.inject & PDA_INJECT_WITHHOLD_KV) == 0u;
   auto dst = [&](uint32_t unit) { return ring_addr + unit % kRing * kUnit; };
   auto place = [&](uint32_t unit) {
@@ -214,7 +215,6 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
       const int tok = it.k0 + j * kKeys;
       for (int c = 0; c < kUnitsK && place(x); ++c, ++x) {
         uint64_t* bar = sh->full + x % kRing;
-        tails &= ~(1u << x % kRing);
         bar_expect_tx(bar, kUnit);
         if (c < 2) tma_load3(dst(x), tk, c * 64, it.head, tok, bar);
         else tma_load3(dst(x), tr, 0, 0, tok, bar);
@@ -226,9 +226,8 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
         const uint32_t slot = x % kRing;
         uint64_t* bar = j == tail ? sh->landed + slot : sh->full + slot;
         bar_expect_tx(bar, kUnit);
-        tails &= ~(1u << slot);
         if (j == tail) {
-          tails |= 1u << slot;
+          if (c == 0) tail0 = tail1, tail1 = x;
           parity ^= 1u << slot;
         }
         for (int d = 0; d < 2; ++d)
@@ -237,12 +236,13 @@ __device__ void load_role(const PrefillArgs& a, Shared* sh, uint8_t* q_s, uint8_
     }
   }
   // Every box issued must have landed before the CTA can exit: the last unit of
-  // each place (what was there before it has been read) and the last Q tiles.
+  // each place (what was there before it has been read; two tiles' V at most are
+  // among them) and the last Q tiles.
   // Always, not only after an abort seen here: another role's wait may run out
   // later.
   for (uint32_t k = x > kRing ? x - kRing : 0u; k < x; ++k) {
     const uint32_t s = k % kRing;
-    if (tails >> s & 1u) bar_drain(sh->landed + s, (parity >> s & 1u) ^ 1u);
+    if (k - tail0 < kUnitsV || k - tail1 < kUnitsV) bar_drain(sh->landed + s, (parity >> s & 1u) ^ 1u);
     else bar_drain(sh->full + s, (k / kRing) & 1u);
   }
   if (nq0) bar_drain(sh->q_full, (nq0 - 1) & 1u);
