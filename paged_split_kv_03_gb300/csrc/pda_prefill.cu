@@ -398,11 +398,20 @@ __device__ void work_role(const PrefillArgs& a, Shared* sh) {
   // Heads go in groups, so that their K and V stay in L2; a group's items from the
   // last tiles (the most keys) to the first, chunks of a tile side by side. CTAs
   // take items one by one, as causal tiles differ: in steps of the grid, 4096 x
-  // 128 heads took a third longer. A group is worth `rounds` items a CTA: three
-  // where items differ (4096 causal rows x 128 heads, one / two / three / four / eight
-  // rounds: 559 / 545 / 521 / 534 / 517 us), one where they do not and L2 is all that
-  // counts (4096 x 4096 keys, no mask: 837 / 847 / 856 / 864 / 918 us).
-  const int64_t rounds = a.causal ? 3 : 1;
+  // 128 heads took a third longer. A group is worth `rounds` items a CTA: where items
+  // differ, enough that its short ones even out the long ones; where they do not, L2 is
+  // all that counts. us of a graph of calls, measured in turn with pauses between, at
+  // 1 / 2 / 3 / 4 / 6 / 8 rounds, causal:
+  //   4096 rows, 128 heads      515 / 490 / 473 / 481 / 474 / 475
+  //   4096 rows, 64 heads       318 / 258 / 256 / 249 / 251 / 250
+  //   8192 rows, 32 heads       513 / 452 / 460 / 434 / 434 / 432
+  //   8 x 1024 rows, 128 heads  409 / 407 / 401 / 393 / 378 / 374
+  // and with every key visible:
+  //   4096 rows, 128 heads      759 / 769 / 781 / 791 / 809 / 853
+  //   4096 rows, 64 heads       385 / 390 / 396 / 409 / 409 / 409
+  //   8192 rows, 64 heads       1457 / 1471 / 1483 / 1494 / 1512 / 1573
+  // (back to back, at lower clocks, the order is the same and the gaps are smaller).
+  const int64_t rounds = a.causal ? 6 : 1;
   const int64_t tiles = max(total, static_cast<int64_t>(1));
   const int64_t wish = max(static_cast<int64_t>(1), rounds * gridDim.x / (tiles * a.splits));
   const int64_t groups = max(static_cast<int64_t>(1), a.heads / wish);
