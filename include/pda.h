@@ -464,7 +464,12 @@ typedef struct {
 
 /* Plan prefills of up to `rows` query rows and `tokens` keys in all, for the
  * heads, batch (at most 8192), max_kv_len and device of `plan` (an MLA plan); both
- * >= 1. Host-only.
+ * >= 1. Host-only. Whether few rows are cut into key chunks goes by these
+ * capacities, not by the lengths on the device: where heads x tiles (256-row
+ * tiles of all requests, at most min(rows, rows / 256 + batch)) are at most half
+ * the SMs. A program whose steps differ keeps a plan for large ones and one for few
+ * rows (64 rows on 8064 keys, 16 heads: 25 us from a plan of 64 rows, 59 from
+ * one of 1024, 104 from one of 4096).
  * Writes *out_plan and, when non-NULL, *scratch_bytes (>= 256): device bytes
  * that the caller allocates as for pda_plan (256-byte aligned, zeroed once);
  * pda_get_status reads and pda_reset_status clears its status word. Calls that

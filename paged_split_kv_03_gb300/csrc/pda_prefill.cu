@@ -28,9 +28,9 @@
 // while this one's rows are written. K and V pass through a ring of 16 KB units:
 // three of K (128 keys x 64 channels), two of V (64 keys x 128 channels) a tile.
 //
-// Few rows: where heads x tiles are fewer than the SMs, a tile's keys are cut
+// Few rows: where heads x tiles are at most half the SMs, a tile's keys are cut
 // into chunks (pda_prefill_plan), whose normalised partial outputs and log2 sums
-// a second kernel joins. 64 rows on 8064 keys, 16 heads: 25.7 us, 103.7 uncut.
+// a second kernel joins. 64 rows on 8064 keys, 16 heads: 25 us, 104 uncut.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -861,10 +861,10 @@ extern "C" int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t to
       rows, (static_cast<int64_t>(rows) + static_cast<int64_t>(pda::kRowsItem - 1) * plan->batch) /
                 pda::kRowsItem);
   p.tiles = static_cast<int32_t>(tiles);
-  // Key chunks. With fewer items (heads x tiles) than SMs, as many chunks as
-  // fill them once, of at least two key tiles (40 rows on up to 700 keys, 4 heads:
-  // one chunk 17.7, three of two tiles 13.5, six of one 13.2 us). More chunks than
-  // SMs cost more than they balance (257 rows on 2157 keys, 16 heads, 96 items: one
+  // Key chunks. With at most half as many items (heads x tiles, by the capacities)
+  // as SMs, as many chunks as fit them once, of at least two key tiles (40 rows on
+  // up to 700 keys, 4 heads: one chunk 17.7, three of two tiles 13.5, six of one 13.2
+  // us). More chunks than SMs cost more than they balance (257 rows on 2157 keys, 16 heads, 96 items: one
   // chunk 39, two 51, three 44 us; 512 rows on 4012 keys, 32 items: 2 / 4 / 6 chunks
   // 41 / 30 / 41 us).
   const int64_t items = tiles * plan->num_qo_heads;
