@@ -338,7 +338,8 @@ typedef struct {
   int32_t* tok_indptr;       /* [batch + 1] written: offsets of kv_len (pda_mla_expand); or NULL */
   int64_t* slot_map;         /* [rows_cap] written: page * P + slot of each new row; or NULL */
   int32_t* positions;        /* [rows_cap] written: position of each new row; or NULL */
-  int32_t table_rows, table_cols, page_table_cap, rows_cap;
+  int32_t table_rows, table_cols, page_table_cap, rows_cap; /* block_table (page_table) may be NULL
+                                where table_cols (page_table_cap) is 0 */
 } pda_tables;
 
 /* Block tables and slot maps of one step, from the request lengths. Request

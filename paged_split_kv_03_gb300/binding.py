@@ -397,7 +397,9 @@ def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, f
         positions = positions.data_ptr()
     _chk_scratch(where, split_scratch, dev, 4)
     t = PdaTables(cached_len.data_ptr(), new_len.data_ptr(), request, block_table.data_ptr(),
-                  block_table.stride(0) if rows > 1 else cols, free_pages.data_ptr(),
+                  block_table.stride(0) if rows > 1 else cols,
+                  # (an empty list has no address: any will do, none of it is read)
+                  free_pages.data_ptr() or free_count.data_ptr(),
                   free_count.data_ptr(), free_left.data_ptr(), kv_len.data_ptr(),
                   kv_indptr.data_ptr(), page_table.data_ptr(), qo_indptr.data_ptr(), tok_indptr,
                   slot_map, positions, rows, cols, page_table.numel(), cap)

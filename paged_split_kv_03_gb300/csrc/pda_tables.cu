@@ -284,8 +284,10 @@ extern "C" int pda_build_tables(const pda_plan_t* plan, const pda_tables* tables
   if (!plan || !tables) return PDA_ERR_NULL;
   if (plan->magic != PDA_PLAN_MAGIC) return PDA_ERR_PLAN;
   const pda_tables& t = *tables;
-  if (!t.cached_len || !t.new_len || !t.block_table || !t.free_pages || !t.free_count ||
-      !t.free_left || !t.kv_len || !t.kv_indptr || !t.page_table || !t.qo_indptr)
+  // (an array of no entries may be NULL)
+  if (!t.cached_len || !t.new_len || (!t.block_table && t.table_cols) || !t.free_pages ||
+      !t.free_count || !t.free_left || !t.kv_len || !t.kv_indptr ||
+      (!t.page_table && t.page_table_cap) || !t.qo_indptr)
     return PDA_ERR_NULL;
   if (!split_scratch || reinterpret_cast<uintptr_t>(split_scratch) % 256) return PDA_ERR_SCRATCH;
   if (t.table_rows < 1 || t.table_cols < 0 || t.table_stride < t.table_cols ||

@@ -68,3 +68,30 @@ def test_token_offsets_past_int32(grow, first):
             assert pos[indptr(rows)[b] + i].item() == t
     assert left.item() == free - taken
     assert bool((table[sum(npg):] == -9).all()) and bool((pos[sum(rows):] == -9).all())
+
+
+@pytest.mark.parametrize("cols,cap", [(3, 8), (3, 0), (0, 8), (0, 0)])
+def test_arrays_without_entries(cols, cap):
+    """A free list, block table or page table of no entries (torch gives such tensors no
+    address): requests that need no page are listed, the others refused."""
+    p = B.PdaParams(num_qo_heads=1, num_kv_heads=1, head_dim=128, page_size=16, max_batch=3,
+                    max_q_len=1, max_kv_len=100, num_pages=10, kv_stride_page=16 * 128,
+                    kv_stride_token=128, kv_stride_head=128)
+    dec = B.Decoder(p, device=DEV)
+    block = torch.full((3, cols), 7, dtype=torch.int32, device=DEV)
+    kv_len, left = ints([-9] * 3), ints([-9])
+    kv_ptr, qo_ptr, tok_ptr = (ints([-9] * 4) for _ in range(3))
+    table = torch.full((cap,), -9, dtype=torch.int32, device=DEV)
+    slots, pos = ints([], torch.int64), ints([])
+    B.pda_build_tables(dec.plan, ints([16, 0, 0]), ints([0, 0, 5]), None, block, ints([]), ints([0]),
+                       left, kv_len, kv_ptr, table, qo_ptr, tok_ptr, slots, pos, dec.scratch)
+    torch.cuda.synchronize()
+    # request 0 holds a page, request 1 nothing, request 2 wants a page that there is not
+    status = (B.PDA_STATUS_NO_PAGES if cols else B.PDA_STATUS_TABLE_INVALID) | \
+        (B.PDA_STATUS_TABLE_FULL if cols and not cap else 0)
+    assert dec.status() == status
+    first = [16, 0, 0] if cols and cap else [0, 0, 0]
+    assert kv_len.tolist() == first and tok_ptr.tolist() == [0] + [first[0]] * 3
+    assert kv_ptr.tolist() == [0] + [1 if first[0] else 0] * 3
+    assert qo_ptr.tolist() == [0] * 4 and left.item() == 0
+    assert table.tolist() == ([7] + [-9] * 7 if first[0] else [-9] * cap)
