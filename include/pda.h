@@ -398,6 +398,8 @@ int pda_append_slots(const pda_plan_t* plan, const void* k_new, int64_t k_stride
  * num_qo_heads is the number of heads. Weights are bf16, heads w_stride_head
  * elements apart (a multiple of 8), rows of 512 contiguous: [Hq, 256, 512] with
  * W_UK first is w_uk = w, w_uv = w + 128 * 512, w_stride_head = 256 * 512.
+ * Rows, and tokens of pda_mla_expand, are at most 8388480 a call (row tiles of 128
+ * in a grid's z): more is PDA_ERR_INVALID.
  * num_rows (device int32 [1], or NULL) bounds the rows as in
  * pda_append_slots; rows past it are left as they were. All sums are fp32,
  * rounded once to the output type. The plan's wait_limit_us bounds every wait

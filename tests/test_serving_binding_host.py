@@ -2,6 +2,8 @@
 device, caches and scales of another type or too small for the plan, scratches that
 are too small. On the CPU: the tensors only say that they are on a CUDA device, and
 every call here is refused."""
+import ctypes
+
 import pytest
 import torch
 
@@ -125,3 +127,15 @@ def test_prefill_scratch_has_to_hold_the_plans_partials():
     refused(B.PDA_ERR_SCRATCH, B.pda_mla_prefill, pre, *args, On(scratch[256:]))
     refused(B.PDA_ERR_SCRATCH, B.pda_mla_prefill, pre, *args, On(scratch.new_zeros(256)))
     refused(B.PDA_ERR_INVALID, B.pda_mla_prefill, pre, *args, On(scratch, dev=1))
+
+
+def test_rows_of_the_latent_calls_end_where_the_header_says(lib):
+    """8388480 rows pass the checks up to the missing output, one more is refused first."""
+    plan, okp = B.pda_plan(ref.mla_plan(HEADS, num_sms=152))[0], 0x10000
+    for rows, code in ((8388480, B.PDA_ERR_NULL), (8388481, B.PDA_ERR_INVALID)):
+        assert lib.pda_mla_project(ctypes.byref(plan), okp, okp, 131072, None, rows, None, okp,
+                                   None) == code
+        assert lib.pda_mla_absorb(ctypes.byref(plan), okp, 384, 192, okp, 131072, 1.0, None, rows, None,
+                                  okp, None) == code
+        assert lib.pda_mla_expand(ctypes.byref(plan), okp, okp, okp, okp, None, okp, okp, 131072, okp, okp,
+                                  None, 512, 256, rows, okp, None) == code
