@@ -400,18 +400,21 @@ __device__ void work_role(const PrefillArgs& a, Shared* sh) {
   // take items one by one, as causal tiles differ: in steps of the grid, 4096 x
   // 128 heads took a third longer. A group is worth `rounds` items a CTA: where items
   // differ, enough that its short ones even out the long ones; where they do not, L2 is
-  // all that counts. us of a graph of calls, measured in turn with pauses between, at
+  // all that counts. us of a call on inputs that change from call to call, at
   // 1 / 2 / 3 / 4 / 6 / 8 rounds, causal:
-  //   4096 rows, 128 heads      515 / 490 / 473 / 481 / 474 / 475
-  //   4096 rows, 64 heads       318 / 258 / 256 / 249 / 251 / 250
-  //   8192 rows, 32 heads       513 / 452 / 460 / 434 / 434 / 432
-  //   8 x 1024 rows, 128 heads  409 / 407 / 401 / 393 / 378 / 374
+  //   4096 rows, 128 heads                535 / 518 / 512 / 522 / 528 / 549
+  //   4096 rows, 64 heads                 315 / 271 / 267 / 268 / 268 / 267
+  //   8192 rows, 32 heads                 525 / 494 / 483 / 473 / 470 / 470
+  //   8 x 256 to 1024 rows, 128 heads     260 / 255 / 245 / 237 / 230 / 227
+  //   1024 rows on 5120 keys, 64 heads    147 / 148 / 148 / 149 / 148 / 148
   // and with every key visible:
-  //   4096 rows, 128 heads      759 / 769 / 781 / 791 / 809 / 853
-  //   4096 rows, 64 heads       385 / 390 / 396 / 409 / 409 / 409
-  //   8192 rows, 64 heads       1457 / 1471 / 1483 / 1494 / 1512 / 1573
-  // (back to back, at lower clocks, the order is the same and the gaps are smaller).
-  const int64_t rounds = a.causal ? 6 : 1;
+  //   4096 rows, 128 heads                854 / 878 / 902 / 920 / 948 / 1002
+  //   4096 rows, 64 heads                 430 / 441 / 454 / 477 / 477 / 477
+  //   2048 rows, 64 heads                 128 / 136 / 136 / 136 / 136 / 136
+  // Six would serve many short items better than three and few long ones worse (in a
+  // graph over two states, whose addresses stay, six is the better or equal at all of
+  // them: 465 against 467 and 250 against 254 us at the first two).
+  const int64_t rounds = a.causal ? 3 : 1;
   const int64_t tiles = max(total, static_cast<int64_t>(1));
   const int64_t wish = max(static_cast<int64_t>(1), rounds * gridDim.x / (tiles * a.splits));
   const int64_t groups = max(static_cast<int64_t>(1), a.heads / wish);
@@ -864,9 +867,9 @@ extern "C" int pda_prefill_plan(const pda_plan_t* plan, int32_t rows, int32_t to
   // Key chunks. With at most half as many items (heads x tiles, by the capacities)
   // as SMs, as many chunks as fit them once, of at least two key tiles (40 rows on
   // up to 700 keys, 4 heads: one chunk 17.7, three of two tiles 13.5, six of one 13.2
-  // us). More chunks than SMs cost more than they balance (257 rows on 2157 keys, 16 heads, 96 items: one
-  // chunk 39, two 51, three 44 us; 512 rows on 4012 keys, 32 items: 2 / 4 / 6 chunks
-  // 41 / 30 / 41 us).
+  // us). More chunks than SMs cost more than they balance (257 rows on 2157 keys,
+  // 16 heads, 96 items: one chunk 39, two 51, three 44 us; 512 rows on 4012 keys, 32
+  // items: 2 / 4 / 6 chunks 41 / 30 / 41 us).
   const int64_t items = tiles * plan->num_qo_heads;
   const int64_t max_tiles =
       (std::min<int64_t>(plan->max_kv_len, tokens) + pda::kKeys - 1) / pda::kKeys;
