@@ -314,21 +314,19 @@ def _room(t) -> int:
     return t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
 
 
-def _chk_scratch(where: str, t, dev: int, need: int) -> None:
-    """A scratch given as a tensor: on the plan's device, at least ``need`` bytes."""
-    if t is None or isinstance(t, int) or (t.get_device() == dev and t.nbytes >= need):
-        return
-    _chk_device(where, "the scratch", t, dev)
-    if _room(t) < need:
-        raise PdaError(PDA_ERR_SCRATCH, f"{where}: {_room(t)} bytes of scratch, not {need};")
+def _scratch(where: str, t, dev: int, need: int):
+    """Address of a scratch; a tensor has to be on the plan's device, with ``need`` bytes."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.get_device() != dev or t.nbytes < need:
+        _chk_device(where, "the scratch", t, dev)
+        if _room(t) < need:
+            raise PdaError(PDA_ERR_SCRATCH, f"{where}: {_room(t)} bytes of scratch, not {need};")
+    return t.data_ptr()
 
 
 def _cache_needs(plan: PdaPlan):
-    """(device, types of the cache, its bytes, values of its scales), looked up once a plan."""
-    try:
-        return plan.cache_needs
-    except AttributeError:
-        pass
+    """(device, types of the cache, its bytes, values of its scales), kept with the plan."""
     bf16, _, _, _, e4m3, u8 = _types()
     kv, mode = plan.kv_dtype, plan.scale_mode
     typed = bf16 if kv == PDA_BF16 else e4m3 if kv == PDA_E4M3 else _INT8
@@ -342,22 +340,30 @@ def _cache_needs(plan: PdaPlan):
     return plan.cache_needs
 
 
-def _chk_cache(where: str, side: str, pages, scale, plan: PdaPlan) -> None:
-    """The cache and its scales, where given as tensors: on the plan's device, of its type
-    (or raw bytes: uint8, int8), and large enough for its pages and strides."""
-    dev, types, need, values = _cache_needs(plan)
-    if not (pages is None or isinstance(pages, int) or
-            (pages.dtype in types and pages.get_device() == dev and pages.nbytes >= need and
-             pages.is_contiguous())):
-        if pages.dtype not in types:
-            raise ValueError(f"{where}: {side}_pages is {pages.dtype}, not {types[0]} or bytes")
-        _chk_device(where, side + "_pages", pages, dev)
-        if _room(pages) < need:
-            raise ValueError(f"{where}: {side}_pages has {_room(pages)} bytes, the plan's pages {need}")
-    if values and scale is not None and not isinstance(scale, int):
-        _chk_device(where, side + "_scale", scale, dev)
-        if scale.dtype is not _TYPES[3] or scale.numel() < values or not scale.is_contiguous():
+def _cache(where: str, side: str, pages, scale, plan: PdaPlan):
+    """Addresses of the cache and its scales; tensors have to be on the plan's device, of its
+    type (the cache: or raw bytes, uint8 or int8), and large enough for its pages and strides."""
+    try:
+        dev, types, need, values = plan.cache_needs
+    except AttributeError:
+        dev, types, need, values = _cache_needs(plan)
+    if pages is not None and not isinstance(pages, int):
+        if not (pages.dtype in types and pages.get_device() == dev and pages.nbytes >= need and
+                pages.is_contiguous()):
+            if pages.dtype not in types:
+                raise ValueError(f"{where}: {side}_pages is {pages.dtype}, not {types[0]} or bytes")
+            _chk_device(where, side + "_pages", pages, dev)
+            if _room(pages) < need:
+                raise ValueError(
+                    f"{where}: {side}_pages has {_room(pages)} bytes, the plan's pages {need}")
+        pages = pages.data_ptr()
+    if scale is not None and not isinstance(scale, int):
+        if values and not (scale.dtype is _TYPES[3] and scale.get_device() == dev and
+                           scale.numel() >= values and scale.is_contiguous()):
+            _chk_device(where, side + "_scale", scale, dev)
             raise ValueError(f"{where}: {side}_scale has to hold {values} contiguous float32")
+        scale = scale.data_ptr()
+    return pages, scale
 
 
 def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, free_pages,
@@ -366,7 +372,7 @@ def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, f
     """Block tables and slot maps of one step from the request lengths, on the GPU (see
     include/pda.h). ``block_table`` is [rows, cols] int32, ``slot_map`` int64, the others int32;
     ``request``, ``tok_indptr``, ``slot_map`` and ``positions`` may be None."""
-    _, i32, i64, _, _, _ = _types()
+    _, i32, i64, _, _, _ = _TYPES or _types()
     where, n, dev = "pda_build_tables", plan.batch, plan.device
     per, ptrs, one = (n,), (n + 1,), (1,)
     _chk(where, "cached_len", cached_len, dev, i32, per)
@@ -395,7 +401,7 @@ def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, f
         _chk(where, "positions", positions, dev, i32, (positions.numel(),))
         cap = min(cap, positions.numel())
         positions = positions.data_ptr()
-    _chk_scratch(where, split_scratch, dev, 4)
+    split_scratch = _scratch(where, split_scratch, dev, 4)
     t = PdaTables(cached_len.data_ptr(), new_len.data_ptr(), request, block_table.data_ptr(),
                   block_table.stride(0) if rows > 1 else cols,
                   # (an empty list has no address: any will do, none of it is read)
@@ -403,7 +409,7 @@ def pda_build_tables(plan: PdaPlan, cached_len, new_len, request, block_table, f
                   free_count.data_ptr(), free_left.data_ptr(), kv_len.data_ptr(),
                   kv_indptr.data_ptr(), page_table.data_ptr(), qo_indptr.data_ptr(), tok_indptr,
                   slot_map, positions, rows, cols, page_table.numel(), cap)
-    rc = load_library().pda_build_tables(ctypes.byref(plan), ctypes.byref(t), _ptr(split_scratch),
+    rc = (_LIB or load_library()).pda_build_tables(ctypes.byref(plan), ctypes.byref(t), split_scratch,
                                          _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
@@ -414,7 +420,7 @@ def _num_rows(where: str, t, dev: int):
     """Address of a one-element int32 device tensor, or None."""
     if t is None:
         return None
-    _chk(where, "num_rows", t, dev, _types()[1], (1,))
+    _chk(where, "num_rows", t, dev, _TYPES[1], (1,))
     return t.data_ptr()
 
 
@@ -422,7 +428,7 @@ def pda_append_slots(plan: PdaPlan, k_new, v_new, slot_map, num_rows, k_pages, v
                      v_scale, split_scratch, stream=None, check: bool = True) -> int:
     """Append rows (bf16 [rows, Hkv, D], any row stride) through a slot map (int64 [rows]);
     ``num_rows``: an int32 device tensor of one element bounding the rows, or None."""
-    bf16, _, i64, _, _, _ = _types()
+    bf16, _, i64, _, _, _ = _TYPES or _types()
     where, dev = "pda_append_slots", plan.device
     rows, d = slot_map.numel(), plan.head_dim
     new, tail = (rows, plan.num_kv_heads, d), (d, 1)
@@ -430,15 +436,17 @@ def pda_append_slots(plan: PdaPlan, k_new, v_new, slot_map, num_rows, k_pages, v
     _chk(where, "slot_map", slot_map, dev, i64, (rows,))
     if v_new is not None:
         _chk(where, "v_new", v_new, dev, bf16, new, tail)
-    _chk_cache(where, "k", k_pages, k_scale, plan)
+    k_pages, k_scale = _cache(where, "k", k_pages, k_scale, plan)
     if d != 576:
-        _chk_cache(where, "v", v_pages, v_scale, plan)
-    _chk_scratch(where, split_scratch, dev, 4)
-    rc = load_library().pda_append_slots(
+        v_pages, v_scale = _cache(where, "v", v_pages, v_scale, plan)
+    else:  # one latent: no v
+        v_pages = v_scale = None
+    split_scratch = _scratch(where, split_scratch, dev, 4)
+    rc = (_LIB or load_library()).pda_append_slots(
         ctypes.byref(plan), k_new.data_ptr(), _row_stride(k_new), _ptr(v_new),
         0 if v_new is None else _row_stride(v_new), slot_map.data_ptr(), rows,
-        _num_rows(where, num_rows, dev), _ptr(k_pages), _ptr(v_pages), _ptr(k_scale), _ptr(v_scale),
-        _ptr(split_scratch), _stream(stream, dev))
+        _num_rows(where, num_rows, dev), k_pages, v_pages, k_scale, v_scale,
+        split_scratch, _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -466,18 +474,18 @@ def pda_mla_absorb(plan: PdaPlan, q, w_uk, q_scale: float, q_lat, num_rows, spli
                    stream=None, check: bool = True) -> int:
     """The query absorbed into the latent space: q bf16 [rows, Hq, 192], w_uk bf16
     [Hq, 128, 512] (any head stride), q_lat [rows, Hq, 576] bf16 or E4M3 codes."""
-    bf16, _, _, _, e4m3, u8 = _types()
+    bf16, _, _, _, e4m3, u8 = _TYPES or _types()
     where, dev = "pda_mla_absorb", plan.device
     rows, h = q.shape[0], plan.num_qo_heads
     _chk(where, "q", q, dev, bf16, (rows, h, 192), (1,))
     _chk(where, "w_uk", w_uk, dev, bf16, (h, 128, 512), (512, 1))
     _chk(where, "q_lat", q_lat, dev,
          bf16 if plan.q_dtype == PDA_BF16 else u8 if q_lat.dtype is u8 else e4m3, (rows, h, 576))
-    _chk_scratch(where, split_scratch, dev, 4)
+    split_scratch = _scratch(where, split_scratch, dev, 4)
     row, head = _head_strides(q)
-    rc = load_library().pda_mla_absorb(
+    rc = (_LIB or load_library()).pda_mla_absorb(
         ctypes.byref(plan), q.data_ptr(), row, head, w_uk.data_ptr(), _row_stride(w_uk), q_scale,
-        q_lat.data_ptr(), rows, _num_rows(where, num_rows, dev), _ptr(split_scratch), _stream(stream, dev))
+        q_lat.data_ptr(), rows, _num_rows(where, num_rows, dev), split_scratch, _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -487,16 +495,16 @@ def pda_mla_project(plan: PdaPlan, o_lat, w_uv, out, num_rows, split_scratch, st
                     check: bool = True) -> int:
     """The decode's latent output projected: o_lat bf16 [rows, Hq, 512], w_uv bf16
     [Hq, 128, 512] (any head stride), out bf16 [rows, Hq, 128]."""
-    bf16 = _types()[0]
+    bf16 = (_TYPES or _types())[0]
     where, dev = "pda_mla_project", plan.device
     rows, h = o_lat.shape[0], plan.num_qo_heads
     _chk(where, "o_lat", o_lat, dev, bf16, (rows, h, 512))
     _chk(where, "w_uv", w_uv, dev, bf16, (h, 128, 512), (512, 1))
     _chk(where, "out", out, dev, bf16, (rows, h, 128))
-    _chk_scratch(where, split_scratch, dev, 4)
-    rc = load_library().pda_mla_project(
+    split_scratch = _scratch(where, split_scratch, dev, 4)
+    rc = (_LIB or load_library()).pda_mla_project(
         ctypes.byref(plan), o_lat.data_ptr(), w_uv.data_ptr(), _row_stride(w_uv), out.data_ptr(),
-        rows, _num_rows(where, num_rows, dev), _ptr(split_scratch), _stream(stream, dev))
+        rows, _num_rows(where, num_rows, dev), split_scratch, _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -513,7 +521,7 @@ def pda_mla_expand(plan: PdaPlan, k_pages, page_table, kv_indptr, tok_indptr, k_
                    latent, k, v, split_scratch, stream=None, check: bool = True) -> int:
     """Keys and values of cached tokens: latent bf16 [tokens, 576], k and v bf16
     [tokens, Hq, 128] (strided alike) are written; w_uk and w_uv bf16 [Hq, 128, 512]."""
-    bf16, i32, _, _, _, _ = _types()
+    bf16, i32, _, _, _, _ = _TYPES or _types()
     where, dev = "pda_mla_expand", plan.device
     tokens, h, ptrs = latent.shape[0], plan.num_qo_heads, (plan.batch + 1,)
     _chk(where, "w_uk", w_uk, dev, bf16, (h, 128, 512), (512, 1))
@@ -524,16 +532,16 @@ def pda_mla_expand(plan: PdaPlan, k_pages, page_table, kv_indptr, tok_indptr, k_
     _chk(where, "kv_indptr", kv_indptr, dev, i32, ptrs)
     _chk(where, "tok_indptr", tok_indptr, dev, i32, ptrs)
     _chk(where, "page_table", page_table, dev, i32, (page_table.numel(),))
-    _chk_cache(where, "k", k_pages, k_scale, plan)
-    _chk_scratch(where, split_scratch, dev, 4)
+    k_pages, k_scale = _cache(where, "k", k_pages, k_scale, plan)
+    split_scratch = _scratch(where, split_scratch, dev, 4)
     w_head = _row_stride(w_uk)
     if w_head != _row_stride(w_uv):
         raise ValueError(f"{where}: w_uk and w_uv differ in their head strides")
     tok, head = _same_strides(where, k, v)
-    rc = load_library().pda_mla_expand(
-        ctypes.byref(plan), _ptr(k_pages), page_table.data_ptr(), kv_indptr.data_ptr(),
-        tok_indptr.data_ptr(), _ptr(k_scale), w_uk.data_ptr(), w_uv.data_ptr(), w_head,
-        latent.data_ptr(), k.data_ptr(), v.data_ptr(), tok, head, tokens, _ptr(split_scratch),
+    rc = (_LIB or load_library()).pda_mla_expand(
+        ctypes.byref(plan), k_pages, page_table.data_ptr(), kv_indptr.data_ptr(),
+        tok_indptr.data_ptr(), k_scale, w_uk.data_ptr(), w_uv.data_ptr(), w_head,
+        latent.data_ptr(), k.data_ptr(), v.data_ptr(), tok, head, tokens, split_scratch,
         _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
@@ -544,7 +552,7 @@ def pda_prefill_plan(plan: PdaPlan, rows: int, tokens: int, check: bool = True):
     """-> (PdaPrefillPlan, scratch_bytes, rc)."""
     pre = PdaPrefillPlan()
     nbytes = ctypes.c_size_t(0)
-    rc = load_library().pda_prefill_plan(ctypes.byref(plan), int(rows), int(tokens),
+    rc = (_LIB or load_library()).pda_prefill_plan(ctypes.byref(plan), int(rows), int(tokens),
                                          ctypes.byref(pre), ctypes.byref(nbytes))
     if check and rc != PDA_OK:
         raise PdaError(rc, "pda_prefill_plan")
@@ -557,7 +565,7 @@ def pda_mla_prefill(pre: PdaPrefillPlan, q, k, v, k_rope, qo_indptr, tok_indptr,
     """Expanded latent attention of ragged requests: q bf16 [rows, Hq, 192], k and v bf16
     [tokens, Hq, 128] (strided alike), k_rope bf16 [tokens, 64], out bf16 [rows, Hq, 128],
     lse fp32 [rows, Hq] or None; rows and tokens are the plan's."""
-    bf16, i32, _, f32, _, _ = _types()
+    bf16, i32, _, f32, _, _ = _TYPES or _types()
     where, dev = "pda_mla_prefill", pre.device
     rows, tokens, h, n = pre.rows, pre.tokens, pre.num_qo_heads, pre.batch
     _chk(where, "q", q, dev, bf16, (rows, h, 192), (1,))
@@ -573,13 +581,13 @@ def pda_mla_prefill(pre: PdaPrefillPlan, q, k, v, k_rope, qo_indptr, tok_indptr,
     if lse is not None:
         _chk(where, "lse", lse, dev, f32, (rows, h))
         lse = lse.data_ptr()
-    _chk_scratch(where, scratch, dev, pre.scratch_bytes)
+    scratch = _scratch(where, scratch, dev, pre.scratch_bytes)
     tok, head = _same_strides(where, k, v)
     row, qhead = _head_strides(q)
-    rc = load_library().pda_mla_prefill(
+    rc = (_LIB or load_library()).pda_mla_prefill(
         ctypes.byref(pre), q.data_ptr(), row, qhead, k.data_ptr(), v.data_ptr(), tok, head,
         k_rope.data_ptr(), _row_stride(k_rope), qo_indptr.data_ptr(), tok_indptr.data_ptr(), window,
-        1 if causal else 0, sm_scale, out.data_ptr(), lse, _ptr(scratch), _stream(stream, dev))
+        1 if causal else 0, sm_scale, out.data_ptr(), lse, scratch, _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
