@@ -216,8 +216,10 @@ AppendFn pick_mode(int mode) {
 // values are D / 8 chunks of 16 bytes, one per lane and load, so a vector of
 // head_dim 128 takes half a warp and every load and store is a full 16-byte
 // (codes: 8-byte) access; K and V of a vector are loaded together before
-// either is converted. Bound: HBM (rows x Hkv x D x (2 + elt) bytes of K and
-// V).
+// either is converted. Bound: HBM for bf16 (rows x Hkv x D x (2 + elt) bytes of K and
+// V; 32768 rows x 8 heads x 128: 41 us, 6.5 TB/s), the issue of one fp32 division a
+// value for codes (8192 rows of the same: E4M3 16 us, int8 20, floor 7.5; records,
+// one vector in flight a warp, 131072 rows: 57 us, 4.2 TB/s).
 
 struct SlotArgs {
   const __nv_bfloat16* k_new;

@@ -120,10 +120,10 @@ __global__ void __launch_bounds__(256) gather_latent(const __grid_constant__ Gat
 // tensor cycles against 160 KB). Short rows cost nothing but idle MMA lanes,
 // as TMA reads no row behind the last. What a CTA has in flight, and how many an
 // SM holds, decides (pda_mla_project). The output tile passes through the stages'
-// memory so that a warp writes whole 256-byte rows. Measured: absorb of 1024 rows x
-// 128 heads 49 us to bf16 (4.4 TB/s, 151 of the 218 MB written, which a plain fill
-// does at 4.0 TB/s), 38 us to E4M3; project 37 us (5.0 TB/s); one row of 128 heads 6.0
-// and 5.0 us.
+// memory so that a warp writes whole 256-byte rows. Measured in graphs of calls: absorb
+// of 1024 rows x 128 heads 49 us to bf16 (4.4 TB/s, 151 of the 218 MB written, which a
+// plain fill does at 4.0 TB/s), 38 us to E4M3; project 37 us (5.0 TB/s); one row of 128
+// heads 6.1 and 4.7 us.
 
 enum { kAbsorb = 0, kProject = 1 };
 
@@ -342,8 +342,8 @@ int launch_product(const ProductArgs& a, const CUtensorMap& ta, const CUtensorMa
 //
 // [k | v]_h[t] = [W_UK; W_UV]_h c_t. Bound: the tensor cores (8192 tokens x 128
 // heads: 275 GFLOP, 147 us at the measured rate) and writing k and v (537 MB, 134
-// us at the 4.0 TB/s that a plain fill reaches) alike; it takes 210 us, 141
-// without the stores. So the operands must not cost anything on top: a CTA pair
+// us at the 4.0 TB/s that a plain fill reaches) alike; it takes 211 us in a graph of
+// calls (220 as calls on changing inputs), 141 without the stores. So the operands must not cost anything on top: a CTA pair
 // takes 256 tokens, M = 256 over both SMs, N = 256 (a head's k and v). Each CTA
 // keeps its 128 latents (128 KB) in shared memory while half of the head's weights
 // (CTA 0 W_UK, CTA 1 W_UV) stream past through a ring of five 16 KB stages: 32
