@@ -484,8 +484,9 @@ def pda_mla_absorb(plan: PdaPlan, q, w_uk, q_scale: float, q_lat, num_rows, spli
     split_scratch = _scratch(where, split_scratch, dev, 4)
     row, head = _head_strides(q)
     rc = (_LIB or load_library()).pda_mla_absorb(
-        ctypes.byref(plan), q.data_ptr(), row, head, w_uk.data_ptr(), _row_stride(w_uk), q_scale,
-        q_lat.data_ptr(), rows, _num_rows(where, num_rows, dev), split_scratch, _stream(stream, dev))
+        ctypes.byref(plan), q.data_ptr(), row, head, w_uk.data_ptr(), _row_stride(w_uk),
+        float(q_scale), q_lat.data_ptr(), rows, _num_rows(where, num_rows, dev), split_scratch,
+        _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc
@@ -587,7 +588,7 @@ def pda_mla_prefill(pre: PdaPrefillPlan, q, k, v, k_rope, qo_indptr, tok_indptr,
     rc = (_LIB or load_library()).pda_mla_prefill(
         ctypes.byref(pre), q.data_ptr(), row, qhead, k.data_ptr(), v.data_ptr(), tok, head,
         k_rope.data_ptr(), _row_stride(k_rope), qo_indptr.data_ptr(), tok_indptr.data_ptr(), window,
-        1 if causal else 0, sm_scale, out.data_ptr(), lse, scratch, _stream(stream, dev))
+        1 if causal else 0, float(sm_scale), out.data_ptr(), lse, scratch, _stream(stream, dev))
     if check and rc != PDA_OK:
         raise PdaError(rc, where)
     return rc

@@ -115,3 +115,25 @@ def test_latent_cache_with_padded_tokens_and_pages(kind):
                      None if scale is None else scale.cpu()))
     for other in seen[1:]:
         assert all(a is b is None or torch.equal(a, b) for a, b in zip(seen[0], other))
+
+
+def test_scales_of_other_number_types():
+    """Scales as numpy numbers or torch scalars, as pda_decode takes them."""
+    import numpy as np
+    g = torch.Generator().manual_seed(6)
+    dec = B.Decoder(ref.mla_plan(HEADS, kind="e4m3", max_kv=TOKENS), device=DEV)
+    pre = B.Prefill(dec.plan, 3, TOKENS)
+    w = torch.randn(HEADS, 128, 512, generator=g).to(torch.bfloat16).to(DEV)
+    q = torch.randn(3, HEADS, 192, generator=g).to(torch.bfloat16).to(DEV)
+    kv = torch.randn(TOKENS, HEADS, 256, generator=g).to(torch.bfloat16).to(DEV)
+    rope = torch.randn(TOKENS, 64, generator=g).to(torch.bfloat16).to(DEV)
+    seen = []
+    for scale in (0.0625, np.float32(0.0625), np.float64(0.0625), torch.tensor(0.0625)):
+        q_lat = torch.zeros(3, HEADS, 576, dtype=torch.uint8, device=DEV)
+        out = torch.zeros(3, HEADS, 128, dtype=torch.bfloat16, device=DEV)
+        B.pda_mla_absorb(dec.plan, q, w, scale, q_lat, None, dec.scratch)
+        pre.run(q, kv[..., :128], kv[..., 128:], rope, ints(0, 3), ints(0, TOKENS), scale, out, None)
+        seen.append((q_lat.cpu(), out.cpu()))
+    assert int(torch.count_nonzero(seen[0][0])) and int(torch.count_nonzero(seen[0][1]))
+    for other in seen[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(seen[0], other))
