@@ -509,6 +509,102 @@ int pda_mla_prefill(const pda_prefill_plan_t* plan, const void* q, int64_t q_str
                     int32_t causal, float sm_scale, void* out, float* lse, void* scratch,
                     pda_stream_t stream);
 
+/* ------------------------------------------------------- pages that are shared
+ *
+ * Requests that continue from the same tokens share the pages of them: a fork lists
+ * its parent's pages in its own block table row. The pages have no counterpart of
+ * these calls. A page is live while a request holds it, however many do, and what
+ * requests hold is what their block table rows say; nothing else is counted. The rules
+ * of the calls around decode hold: nothing allocated or synchronised, `stream` only,
+ * the plan's device current, int32 index arrays on the device, and the same inputs
+ * give the same outputs. */
+
+/* Arrays of pda_fork_tables. */
+typedef struct {
+  const int32_t* parent;     /* [forks] block_table row shared from */
+  const int32_t* child;      /* [forks] block_table row written; all different, none of them a parent */
+  const int32_t* shared_len; /* [forks] tokens shared, 0 to the parent's length */
+  int32_t* block_table;      /* [table_rows, table_cols] as for pda_build_tables; NULL with no columns */
+  int64_t table_stride;
+  const int32_t* free_pages; /* free list, taken from its end */
+  const int32_t* free_count; /* [1] */
+  int32_t* free_left;        /* [1] written; not free_count itself */
+  int32_t* child_len;        /* [forks] written: shared_len, or 0 (below); not shared_len itself */
+  int32_t* copy_src;         /* [forks] written: page to copy, -1: none (pda_copy_pages) */
+  int32_t* copy_dst;         /* [forks] written: the child's page for it, or -1 */
+  int32_t* copy_tokens;      /* [forks] written: tokens of it that are shared, or 0 */
+  int32_t table_rows, table_cols, forks; /* forks: 0 to 65536 */
+} pda_forks;
+
+/* Fork requests: child row f lists the first floor(shared_len / P) pages of its
+ * parent's row. Where shared_len ends inside a page, which parent and child would
+ * both append to, the child gets a page of its own (off the free list's end, forks
+ * in order) and the copy lists name what to copy into it, in every layer's cache.
+ * A fork whose page lies past the free list (counted over all the forks up to it)
+ * is not made: child_len 0, its row left as it was; PDA_STATUS_NO_PAGES. The same
+ * for an invalid one (rows out of range or equal, shared_len negative, above the
+ * plan's max_kv_len or the columns): PDA_STATUS_TABLE_INVALID (and KV_LEN_GT_MAX).
+ * Page ids out of range are listed as they are, but not copied:
+ * PDA_STATUS_PAGE_OOB. Entries of a child's row behind shared_len stay as they were. */
+int pda_fork_tables(const pda_plan_t* plan, const pda_forks* forks, void* split_scratch,
+                    pda_stream_t stream);
+
+/* Copy pages of one cache: K, V and, where the plan's scales are per token, the
+ * scales, from page copy_src[i] to copy_dst[i]. No page may be a destination twice,
+ * or a source and a destination.
+ *   copy_tokens  [copies] tokens of each page to copy (its first ones); NULL = all
+ *   copies       entries of the lists; num_copies, when not NULL, is one device
+ *                int32: only the first min(copies, *num_copies) are taken
+ *   v_pages, v_scale  not used for latents (head_dim 576)
+ * An entry with -1 in either list is skipped; another page outside [0, num_pages)
+ * too, and sets PDA_STATUS_PAGE_OOB. */
+int pda_copy_pages(const pda_plan_t* plan, void* k_pages, void* v_pages, float* k_scale,
+                   float* v_scale, const int32_t* copy_src, const int32_t* copy_dst,
+                   const int32_t* copy_tokens, int32_t copies, const int32_t* num_copies,
+                   void* split_scratch, pda_stream_t stream);
+
+/* Arrays of pda_free_pages and pda_compact_pages. */
+typedef struct {
+  const int32_t* lengths;    /* [requests] tokens of every request that holds pages, >= 0 */
+  const int32_t* request;    /* [requests] block_table row of each, all different; NULL = row b */
+  const int32_t* block_table; /* [table_rows, table_cols] page ids; entries below ceil(length / P) count */
+  int64_t table_stride;
+  int32_t* free_pages;       /* [num_pages] written: the free list, free_left entries */
+  int32_t* free_left;        /* [1] written: its length */
+  /* pda_compact_pages only: */
+  int32_t* new_table;        /* written: the rows after the moves, as far as they count; strided as
+                                block_table, which it may be */
+  int32_t* copy_src;         /* [max_copies] written: pages to move (pda_copy_pages) */
+  int32_t* copy_dst;         /* [max_copies] written: where to */
+  int32_t* num_copies;       /* [1] written: how many */
+  int32_t requests, table_rows, table_cols, max_copies;
+} pda_pages;
+
+/* Bytes of the page_scratch of both calls (256-byte aligned, zeroed once, not
+ * shared by calls that overlap); pda_get_status reads and pda_reset_status clears its
+ * status word. */
+int pda_pages_scratch(const pda_plan_t* plan, size_t* scratch_bytes);
+
+/* The free list from what is held: every page of [0, num_pages) that no listed
+ * request holds, from the highest id to the lowest, which pda_build_tables takes
+ * first. Requests that are gone, or shorter than they were, are all that a page
+ * needs to become free. Every request that holds pages has to be listed, a kept
+ * prompt's as well. What an invalid request lists stays held: a length above the
+ * columns counts all of them (PDA_STATUS_TABLE_INVALID), above the plan's max_kv_len
+ * also PDA_STATUS_KV_LEN_GT_MAX; a negative length or a row out of range lists
+ * nothing (PDA_STATUS_TABLE_INVALID). Page ids out of range are passed over
+ * (PDA_STATUS_PAGE_OOB). Entries of free_pages behind free_left stay as they were. */
+int pda_free_pages(const pda_plan_t* plan, const pda_pages* pages, void* page_scratch,
+                   pda_stream_t stream);
+
+/* pda_free_pages, with the live pages moved to the lowest ids: the k-th highest
+ * live page goes to the k-th lowest free one, while that lies below it, for at most
+ * max_copies pages. The free list and new_table are those after the moves; the
+ * caller runs pda_copy_pages (every layer's cache, num_copies) before it uses them.
+ * Other tables that name pages (page_table, slot_map) are stale then. */
+int pda_compact_pages(const pda_plan_t* plan, const pda_pages* pages, void* page_scratch,
+                      pda_stream_t stream);
+
 /* Copy the device status word of `split_scratch` to *host_bits. Synchronises
  * `stream`. split_scratch = NULL reads the status of pda_decode_static's
  * built-in array on the plan's device (which must be current). */

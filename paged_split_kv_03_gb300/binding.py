@@ -44,8 +44,9 @@ PDA_INJECT_WITHHOLD_CTA1 = 0x4
 # every entry point include/pda.h declares
 EXPORTED = ("pda_plan", "pda_decode", "pda_decode_stages", "pda_decode_static", "pda_append_kv",
             "pda_build_tables", "pda_append_slots", "pda_mla_absorb", "pda_mla_project",
-            "pda_mla_expand", "pda_prefill_plan", "pda_mla_prefill", "pda_get_status", "pda_reset_status", "pda_strerror", "pda_version",
-            "pda_struct_sizes")
+            "pda_mla_expand", "pda_prefill_plan", "pda_mla_prefill", "pda_fork_tables",
+            "pda_copy_pages", "pda_pages_scratch", "pda_free_pages", "pda_compact_pages",
+            "pda_get_status", "pda_reset_status", "pda_strerror", "pda_version", "pda_struct_sizes")
 
 _i32, _i64, _u32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_void_p
 
@@ -93,6 +94,20 @@ class PdaPrefillPlan(ctypes.Structure):
                 ("tokens", _i32), ("tiles", _i32), ("splits", _i32), ("chunk_tokens", _i32),
                 ("wait_limit_us", _i32), ("inject", _u32), ("reserved", _i32 * 2),
                 ("scratch_bytes", _i64)]
+
+
+class PdaForks(ctypes.Structure):
+    _fields_ = [("parent", _vp), ("child", _vp), ("shared_len", _vp), ("block_table", _vp),
+                ("table_stride", _i64), ("free_pages", _vp), ("free_count", _vp),
+                ("free_left", _vp), ("child_len", _vp), ("copy_src", _vp), ("copy_dst", _vp),
+                ("copy_tokens", _vp), ("table_rows", _i32), ("table_cols", _i32), ("forks", _i32)]
+
+
+class PdaPages(ctypes.Structure):
+    _fields_ = [("lengths", _vp), ("request", _vp), ("block_table", _vp), ("table_stride", _i64),
+                ("free_pages", _vp), ("free_left", _vp), ("new_table", _vp), ("copy_src", _vp),
+                ("copy_dst", _vp), ("num_copies", _vp), ("requests", _i32), ("table_rows", _i32),
+                ("table_cols", _i32), ("max_copies", _i32)]
 
 
 class PdaError(RuntimeError):
@@ -152,6 +167,17 @@ def load_library(path: Optional[str] = None):
                                     _i64, _vp, _i64, _vp, _vp, _vp, _i32, ctypes.c_float, _vp, _vp,
                                     _vp, _vp]
     lib.pda_mla_prefill.restype = ctypes.c_int
+    lib.pda_fork_tables.argtypes = [ctypes.POINTER(PdaPlan), ctypes.POINTER(PdaForks), _vp, _vp]
+    lib.pda_fork_tables.restype = ctypes.c_int
+    lib.pda_copy_pages.argtypes = [ctypes.POINTER(PdaPlan), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                   _vp, _vp, _vp]
+    lib.pda_copy_pages.restype = ctypes.c_int
+    lib.pda_pages_scratch.argtypes = [ctypes.POINTER(PdaPlan), ctypes.POINTER(ctypes.c_size_t)]
+    lib.pda_pages_scratch.restype = ctypes.c_int
+    for name in ("pda_free_pages", "pda_compact_pages"):
+        fn = getattr(lib, name)
+        fn.argtypes = [ctypes.POINTER(PdaPlan), ctypes.POINTER(PdaPages), _vp, _vp]
+        fn.restype = ctypes.c_int
     lib.pda_get_status.argtypes = [ctypes.POINTER(PdaPlan), _vp, ctypes.POINTER(_u32), _vp]
     lib.pda_get_status.restype = ctypes.c_int
     lib.pda_reset_status.argtypes = [ctypes.POINTER(PdaPlan), _vp, _vp]
@@ -594,6 +620,140 @@ def pda_mla_prefill(pre: PdaPrefillPlan, q, k, v, k_rope, qo_indptr, tok_indptr,
     return rc
 
 
+def _table(where: str, name: str, t, dev: int):
+    """(address, row stride, rows, columns) of a block table."""
+    rows, cols = t.shape
+    _chk(where, name, t, dev, (_TYPES or _types())[1], (rows, cols), (1,))
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols, rows, cols
+
+
+def pda_fork_tables(plan: PdaPlan, parent, child, shared_len, block_table, free_pages, free_count,
+                    free_left, child_len, copy_src, copy_dst, copy_tokens, split_scratch, stream=None,
+                    check: bool = True) -> int:
+    """Fork requests (see include/pda.h): rows ``child`` of the block table share the pages of the
+    first ``shared_len`` tokens of rows ``parent``; all int32, lists of ``parent.numel()`` entries."""
+    i32 = (_TYPES or _types())[1]
+    where, dev, n = "pda_fork_tables", plan.device, parent.numel()
+    per, one = (n,), (1,)
+    for name, t in (("parent", parent), ("child", child), ("shared_len", shared_len),
+                    ("child_len", child_len), ("copy_src", copy_src), ("copy_dst", copy_dst),
+                    ("copy_tokens", copy_tokens)):
+        _chk(where, name, t, dev, i32, per)
+    _chk(where, "free_count", free_count, dev, i32, one)
+    _chk(where, "free_left", free_left, dev, i32, one)
+    _chk(where, "free_pages", free_pages, dev, i32, (free_pages.numel(),))
+    table, stride, rows, cols = _table(where, "block_table", block_table, dev)
+    split_scratch = _scratch(where, split_scratch, dev, 4)
+    f = PdaForks(parent.data_ptr(), child.data_ptr(), shared_len.data_ptr(), table, stride,
+                 # (an empty list has no address: any will do, none of it is read)
+                 free_pages.data_ptr() or free_count.data_ptr(), free_count.data_ptr(),
+                 free_left.data_ptr(), child_len.data_ptr(), copy_src.data_ptr(),
+                 copy_dst.data_ptr(), copy_tokens.data_ptr(), rows, cols, n)
+    rc = (_LIB or load_library()).pda_fork_tables(ctypes.byref(plan), ctypes.byref(f), split_scratch,
+                                                  _stream(stream, dev))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, where)
+    return rc
+
+
+def pda_copy_pages(plan: PdaPlan, k_pages, v_pages, k_scale, v_scale, copy_src, copy_dst,
+                   copy_tokens, num_copies, split_scratch, stream=None, check: bool = True) -> int:
+    """Copy pages of one cache, and their per-token scales: int32 lists ``copy_src`` and
+    ``copy_dst``; ``copy_tokens`` (int32 list) and ``num_copies`` (one int32) may be None."""
+    i32 = (_TYPES or _types())[1]
+    where, dev, n = "pda_copy_pages", plan.device, copy_src.numel()
+    _chk(where, "copy_src", copy_src, dev, i32, (n,))
+    _chk(where, "copy_dst", copy_dst, dev, i32, (n,))
+    if copy_tokens is not None:
+        _chk(where, "copy_tokens", copy_tokens, dev, i32, (n,))
+        copy_tokens = copy_tokens.data_ptr()
+    if num_copies is not None:
+        _chk(where, "num_copies", num_copies, dev, i32, (1,))
+        num_copies = num_copies.data_ptr()
+    k_pages, k_scale = _cache(where, "k", k_pages, k_scale, plan)
+    if plan.head_dim != 576:
+        v_pages, v_scale = _cache(where, "v", v_pages, v_scale, plan)
+    else:  # one latent: no v
+        v_pages = v_scale = None
+    split_scratch = _scratch(where, split_scratch, dev, 4)
+    rc = (_LIB or load_library()).pda_copy_pages(
+        ctypes.byref(plan), k_pages, v_pages, k_scale, v_scale, copy_src.data_ptr(),
+        copy_dst.data_ptr(), copy_tokens, n, num_copies, split_scratch, _stream(stream, dev))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, where)
+    return rc
+
+
+def pda_pages_scratch(plan: PdaPlan) -> int:
+    """Bytes of the scratch of pda_free_pages and pda_compact_pages (see ``Pages``)."""
+    nbytes = ctypes.c_size_t(0)
+    rc = (_LIB or load_library()).pda_pages_scratch(ctypes.byref(plan), ctypes.byref(nbytes))
+    if rc != PDA_OK:
+        raise PdaError(rc, "pda_pages_scratch")
+    return int(nbytes.value)
+
+
+def _held(where: str, plan: PdaPlan, lengths, request, block_table, free_pages, free_left, scratch):
+    """PdaPages of what both calls take, and the scratch's address."""
+    i32 = (_TYPES or _types())[1]
+    dev, n = plan.device, lengths.numel()
+    _chk(where, "lengths", lengths, dev, i32, (n,))
+    if request is not None:
+        _chk(where, "request", request, dev, i32, (n,))
+        request = request.data_ptr()
+    if free_pages.numel() < plan.num_pages:
+        raise ValueError(f"{where}: free_pages has {free_pages.numel()} entries, the plan "
+                         f"{plan.num_pages} pages")
+    _chk(where, "free_pages", free_pages, dev, i32, (free_pages.numel(),))
+    _chk(where, "free_left", free_left, dev, i32, (1,))
+    table, stride, rows, cols = _table(where, "block_table", block_table, dev)
+    if scratch is not None and not isinstance(scratch, int):
+        try:
+            need = plan.pages_needs
+        except AttributeError:
+            need = plan.pages_needs = pda_pages_scratch(plan)
+        scratch = _scratch(where, scratch, dev, need)
+    return PdaPages(lengths.data_ptr(), request, table, stride, free_pages.data_ptr(),
+                    free_left.data_ptr(), None, None, None, None, n, rows, cols, 0), scratch
+
+
+def pda_free_pages(plan: PdaPlan, lengths, request, block_table, free_pages, free_left,
+                   page_scratch, stream=None, check: bool = True) -> int:
+    """The free list from what the requests hold (see include/pda.h); ``request`` may be None."""
+    where = "pda_free_pages"
+    p, page_scratch = _held(where, plan, lengths, request, block_table, free_pages, free_left,
+                            page_scratch)
+    rc = (_LIB or load_library()).pda_free_pages(ctypes.byref(plan), ctypes.byref(p), page_scratch,
+                                                 _stream(stream, plan.device))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, where)
+    return rc
+
+
+def pda_compact_pages(plan: PdaPlan, lengths, request, block_table, new_table, free_pages,
+                      free_left, copy_src, copy_dst, num_copies, page_scratch, stream=None,
+                      check: bool = True) -> int:
+    """pda_free_pages with the live pages moved to the lowest ids, at most ``copy_src.numel()`` of
+    them; ``new_table`` is strided as ``block_table`` and may be it."""
+    where, dev = "pda_compact_pages", plan.device
+    p, page_scratch = _held(where, plan, lengths, request, block_table, free_pages, free_left,
+                            page_scratch)
+    i32, n = _TYPES[1], copy_src.numel()
+    _chk(where, "copy_src", copy_src, dev, i32, (n,))
+    _chk(where, "copy_dst", copy_dst, dev, i32, (n,))
+    _chk(where, "num_copies", num_copies, dev, i32, (1,))
+    to, stride, rows, cols = _table(where, "new_table", new_table, dev)
+    if (stride, rows, cols) != (p.table_stride, p.table_rows, p.table_cols):
+        raise ValueError(f"{where}: new_table is not strided as block_table")
+    p.new_table, p.copy_src, p.copy_dst = to, copy_src.data_ptr(), copy_dst.data_ptr()
+    p.num_copies, p.max_copies = num_copies.data_ptr(), n
+    rc = (_LIB or load_library()).pda_compact_pages(ctypes.byref(plan), ctypes.byref(p),
+                                                    page_scratch, _stream(stream, dev))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, where)
+    return rc
+
+
 def pda_get_status(plan: PdaPlan, split_scratch, stream=None) -> int:
     """Device status bits; ``split_scratch=None`` reads those of the
     built-in array that pda_decode_static uses."""
@@ -703,3 +863,19 @@ class Prefill:
 
     def reset_status(self, stream=None) -> None:
         pda_reset_status(self.decode_plan, self.scratch, stream)
+
+
+class Pages:
+    """The scratch of pda_free_pages and pda_compact_pages of a plan (allocated once with torch)."""
+
+    def __init__(self, plan: PdaPlan, device=None):
+        import torch
+        self.plan = plan
+        self.scratch = torch.zeros(pda_pages_scratch(plan), dtype=torch.uint8,
+                                   device=f"cuda:{plan.device}" if device is None else device)
+
+    def status(self, stream=None) -> int:
+        return pda_get_status(self.plan, self.scratch, stream)
+
+    def reset_status(self, stream=None) -> None:
+        pda_reset_status(self.plan, self.scratch, stream)
