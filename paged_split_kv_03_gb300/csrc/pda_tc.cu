@@ -1122,7 +1122,7 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
   const int q0 = a.qo_indptr[b];
   const int q1 = a.qo_indptr[b + 1];
   const int L = a.kv_len[b];
-  const int W = a.window ? a.window[b] : 0;
+  const int W = a.window ? min(a.window[b], L) : 0;  // (L of L tokens is all of them; tok + W stays in range)
   const int kv0 = a.kv_indptr[b];
   const int R = q1 - q0;
   if (R <= 0 || R > a.max_q_len || L < R || L > a.max_kv_len || q0 + R > a.rows_cap) {
