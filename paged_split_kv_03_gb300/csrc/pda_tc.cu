@@ -101,10 +101,10 @@ __device__ __forceinline__ void i8x4_to_f16x4(uint32_t w, uint32_t& e01, uint32_
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(e23) : "r"(hi), "r"(0x64806480u));
 }
 
-// Eight bf16 values -> eight f16 values (RNE; exact inside f16's normal range).
-__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v) {
-  auto two = [](uint32_t w) -> uint32_t {
-    const __half2 h = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+// Eight bf16 values times `by` -> eight f16 values (RNE; exact inside f16's normal range).
+__device__ __forceinline__ uint4 bf16x8_to_f16x8(uint4 v, float by) {
+  auto two = [by](uint32_t w) -> uint32_t {
+    const __half2 h = __floats2half2_rn(__uint_as_float(w << 16) * by, __uint_as_float(w & 0xFFFF0000u) * by);
     return *reinterpret_cast<const uint32_t*>(&h);
   };
   return make_uint4(two(v.x), two(v.y), two(v.z), two(v.w));
@@ -447,6 +447,7 @@ __device__ __forceinline__ void softmax_role(const DecodeArgs& a, const SoftmaxC
   for (int j = 0; j < x.ntiles; ++j) {
     const int tok = x.t_begin + j * kTok + r;
     float row_scale = qk_scale, log2_vs = 0.f, inv_vs = 1.f;
+    if constexpr (C::kF16Ops) row_scale *= x.colscale[0];
     if constexpr (SMODE == PDA_SCALE_TOKEN_HEAD) {
       const float ks = ks_a;
       float vs = vs_a;
@@ -1257,13 +1258,35 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
                 static_cast<const uint8_t*>(a.q) +
                 (((int64_t)(q0 + n / hpc) * a.hq + head0 + n % hpc) * D) * C::kElt + cch * 16));
         }
+        float by = 1.f;
+        if constexpr (C::kF16Ops) {
+          // f16 operands: where the CTA's largest |Q| is not in [2^-6, 2^12), its power of
+          // two is taken out first (and put back into the logit scale)
+          uint32_t top = 0u;
+#pragma unroll
+          for (int it = 0; it < kIters; ++it) {
+            const uint32_t w[4] = {qv[it].x, qv[it].y, qv[it].z, qv[it].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] << 16 & 0x7FFF0000u, w[e] & 0x7FFF0000u));
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          if (lane == 0) red[sw] = __uint_as_float(top);
+          group_sync<C::kSmThreads>();
+#pragma unroll
+          for (int w = 0; w < C::kSmWarps; ++w) top = max(top, __float_as_uint(red[w]));
+          int ex = static_cast<int>(top >> 23) - 127;
+          if (top == 0u || ex == 128 || (ex >= -6 && ex < 12)) ex = 0;
+          ex = max(-126, min(126, ex));
+          by = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+          if (st == 0) colscale[0] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        }
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
           const int idx = st + it * C::kSmThreads;
           const int n = idx / kPadChunks, cch = idx % kPadChunks;
           if (n < N) {
             uint4 v = qv[it];
-            if constexpr (C::kF16Ops) v = bf16x8_to_f16x8(v);  // f16 operands (converted caches)
+            if constexpr (C::kF16Ops) v = bf16x8_to_f16x8(v, by);
             const int byte = cch * 16;
             *reinterpret_cast<uint4*>(q_s + (byte / 128) * C::kQAtomBytes + sw128(n, byte % 128)) = v;
           }
