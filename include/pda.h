@@ -605,6 +605,76 @@ int pda_free_pages(const pda_plan_t* plan, const pda_pages* pages, void* page_sc
 int pda_compact_pages(const pda_plan_t* plan, const pda_pages* pages, void* page_scratch,
                       pda_stream_t stream);
 
+/* ------------------------------------------------ decode behind shared prefixes
+ *
+ * pda_decode for requests that continue from the same tokens: the pages that the
+ * block tables of a group's requests have in common in front are read once, for the
+ * rows of all of them, and only a request's own tokens are read for it alone. The
+ * results are pda_decode's. Caches of head_dim 64, 128 and 256 in every kv dtype and
+ * scale mode, pages of 8 tokens and more; the latent of MLA (head_dim 576) and
+ * head_dim 512 are PDA_ERR_UNSUPPORTED: share its pages, and call pda_decode. */
+
+/* The plan: plain data, as pda_plan_t. */
+typedef struct {
+  uint32_t magic;         /* PDA_SHARED_MAGIC once planned */
+  uint32_t struct_bytes;  /* sizeof(pda_shared_plan_t) as compiled */
+  pda_plan_t own;         /* the requests' own tokens: stage 1 of pda_decode */
+  int32_t groups;
+  int32_t max_kv_len;     /* of the plan given; own.max_kv_len bounds the own tokens */
+  int64_t first_offset, main_lse_offset, main_o_offset, area_lse_offset, area_o_offset;
+  int64_t scratch_bytes;
+  int32_t reserved[4];
+} pda_shared_plan_t;
+
+#define PDA_SHARED_MAGIC 0x50445331u /* "PDS1" */
+
+/* Arrays of one step (device pointers). */
+typedef struct {
+  const int32_t* page_table;   /* the step's tables, as for pda_decode (pda_build_tables) */
+  const int32_t* kv_indptr;    /* [batch + 1] */
+  const int32_t* kv_len;       /* [batch] */
+  const int32_t* qo_indptr;    /* [batch + 1] */
+  const int32_t* window;       /* [batch] or NULL */
+  const int32_t* group_indptr; /* [groups + 1] the requests of each group, side by side: from 0 to
+                                  batch; NULL = one group of all (groups 1) */
+  int32_t* prefix;             /* [groups, 2] written: tokens [first, end) of the prefix that the
+                                  group's rows see */
+  int32_t* own_indptr;         /* [batch] written: a request's own pages in page_table; not kv_indptr */
+  int32_t* own_len;            /* [batch] written: its own tokens; not kv_len */
+} pda_shared_tables;
+
+/* Plan decodes of the plan's batch in `groups` groups (1 to 8192), with at most
+ * max_own_len own tokens a request (0: the plan's max_kv_len; a tight bound plans
+ * better chunks). A request that has more is left unwritten by pda_decode_shared
+ * (PDA_STATUS_KV_LEN_GT_MAX). Host-only. Writes *out_plan and, when non-NULL,
+ * *scratch_bytes, which the caller allocates as for pda_plan (256-byte aligned,
+ * zeroed once, not shared by calls that overlap); pda_get_status with &out_plan->own
+ * reads and pda_reset_status clears its status word. */
+int pda_shared_plan(const pda_plan_t* plan, int32_t groups, int32_t max_own_len,
+                    pda_shared_plan_t* out_plan, size_t* scratch_bytes);
+
+/* What the requests of each group share, once a step: with L tokens and R rows of a
+ * request, the prefix ends behind the whole pages whose ids all its requests list
+ * alike, at most (L - R) / P of them, so that every row stands behind it; `first` is
+ * the first token that a row sees (0 without windows), rounded down to a page, at most
+ * `end`. Own tokens are the L - end behind it, R of them at least. A request without
+ * rows takes no part (own_len 0), nor does an invalid one (own_len -1; L < R, R out
+ * of range or L above max_kv_len, with pda_decode's status bits); a page id out of
+ * range ends a prefix. A group whose bounds are no requests is left unwritten
+ * (PDA_STATUS_TABLE_INVALID). */
+int pda_share_tables(const pda_shared_plan_t* plan, const pda_shared_tables* tables, void* scratch,
+                     pda_stream_t stream);
+
+/* Decode on the tables that pda_share_tables filled, as pda_decode: q, the caches,
+ * scales, out, lse (or NULL), sm_scale and max_q_len are its arguments. An invalid
+ * request's rows are left unwritten, with its status bits; so are those of a request
+ * with more own tokens than planned. Keys and values that a row does not see for its window
+ * have to be finite where another row of its group sees them. */
+int pda_decode_shared(const pda_shared_plan_t* plan, const void* q, const void* k_pages,
+                      const void* v_pages, const pda_shared_tables* tables, int32_t max_q_len,
+                      float sm_scale, const float* k_scale, const float* v_scale, void* out,
+                      float* lse, void* scratch, pda_stream_t stream);
+
 /* Copy the device status word of `split_scratch` to *host_bits. Synchronises
  * `stream`. split_scratch = NULL reads the status of pda_decode_static's
  * built-in array on the plan's device (which must be current). */

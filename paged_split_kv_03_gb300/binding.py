@@ -37,6 +37,7 @@ PDA_STATUS_TABLE_FULL = 0x200
 PDA_STATUS_TOKENS_GT_CAP = 0x400
 PDA_PLAN_MAGIC = 0x50444131
 PDA_PREFILL_MAGIC = 0x50444631
+PDA_SHARED_MAGIC = 0x50445331
 PDA_INJECT_WITHHOLD_KV = 0x1
 PDA_INJECT_WITHHOLD_CTA0 = 0x2
 PDA_INJECT_WITHHOLD_CTA1 = 0x4
@@ -46,6 +47,7 @@ EXPORTED = ("pda_plan", "pda_decode", "pda_decode_stages", "pda_decode_static", 
             "pda_build_tables", "pda_append_slots", "pda_mla_absorb", "pda_mla_project",
             "pda_mla_expand", "pda_prefill_plan", "pda_mla_prefill", "pda_fork_tables",
             "pda_copy_pages", "pda_pages_scratch", "pda_free_pages", "pda_compact_pages",
+            "pda_shared_plan", "pda_share_tables", "pda_decode_shared",
             "pda_get_status", "pda_reset_status", "pda_strerror", "pda_version", "pda_struct_sizes")
 
 _i32, _i64, _u32, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_void_p
@@ -108,6 +110,18 @@ class PdaPages(ctypes.Structure):
                 ("free_pages", _vp), ("free_left", _vp), ("new_table", _vp), ("copy_src", _vp),
                 ("copy_dst", _vp), ("num_copies", _vp), ("requests", _i32), ("table_rows", _i32),
                 ("table_cols", _i32), ("max_copies", _i32)]
+
+
+class PdaSharedPlan(ctypes.Structure):
+    _fields_ = [("magic", _u32), ("struct_bytes", _u32), ("own", PdaPlan), ("groups", _i32),
+                ("max_kv_len", _i32), ("first_offset", _i64), ("main_lse_offset", _i64),
+                ("main_o_offset", _i64), ("area_lse_offset", _i64), ("area_o_offset", _i64),
+                ("scratch_bytes", _i64), ("reserved", _i32 * 4)]
+
+
+class PdaSharedTables(ctypes.Structure):
+    _fields_ = [(k, _vp) for k in ("page_table", "kv_indptr", "kv_len", "qo_indptr", "window",
+                                   "group_indptr", "prefix", "own_indptr", "own_len")]
 
 
 class PdaError(RuntimeError):
@@ -178,6 +192,16 @@ def load_library(path: Optional[str] = None):
         fn = getattr(lib, name)
         fn.argtypes = [ctypes.POINTER(PdaPlan), ctypes.POINTER(PdaPages), _vp, _vp]
         fn.restype = ctypes.c_int
+    lib.pda_shared_plan.argtypes = [ctypes.POINTER(PdaPlan), _i32, _i32,
+                                    ctypes.POINTER(PdaSharedPlan), ctypes.POINTER(ctypes.c_size_t)]
+    lib.pda_shared_plan.restype = ctypes.c_int
+    lib.pda_share_tables.argtypes = [ctypes.POINTER(PdaSharedPlan), ctypes.POINTER(PdaSharedTables),
+                                     _vp, _vp]
+    lib.pda_share_tables.restype = ctypes.c_int
+    lib.pda_decode_shared.argtypes = [ctypes.POINTER(PdaSharedPlan), _vp, _vp, _vp,
+                                      ctypes.POINTER(PdaSharedTables), _i32, ctypes.c_float, _vp, _vp,
+                                      _vp, _vp, _vp, _vp]
+    lib.pda_decode_shared.restype = ctypes.c_int
     lib.pda_get_status.argtypes = [ctypes.POINTER(PdaPlan), _vp, ctypes.POINTER(_u32), _vp]
     lib.pda_get_status.restype = ctypes.c_int
     lib.pda_reset_status.argtypes = [ctypes.POINTER(PdaPlan), _vp, _vp]
@@ -754,6 +778,87 @@ def pda_compact_pages(plan: PdaPlan, lengths, request, block_table, new_table, f
     return rc
 
 
+def pda_shared_plan(plan: PdaPlan, groups: int, max_own_len: int = 0, check: bool = True):
+    """-> (PdaSharedPlan, scratch_bytes, rc)."""
+    sp = PdaSharedPlan()
+    nbytes = ctypes.c_size_t(0)
+    rc = (_LIB or load_library()).pda_shared_plan(ctypes.byref(plan), int(groups), int(max_own_len),
+                                                  ctypes.byref(sp), ctypes.byref(nbytes))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, "pda_shared_plan")
+    return sp, int(nbytes.value), rc
+
+
+def _shared_tables(where: str, sp: PdaSharedPlan, page_table, kv_indptr, kv_len, qo_indptr, window,
+                   group_indptr, prefix, own_indptr, own_len):
+    """PdaSharedTables of a step's arrays, all int32."""
+    i32 = (_TYPES or _types())[1]
+    own = sp.own
+    dev, n, groups = own.device, own.batch, sp.groups
+    _chk(where, "page_table", page_table, dev, i32, (page_table.numel(),))
+    _chk(where, "kv_indptr", kv_indptr, dev, i32, (n + 1,))
+    _chk(where, "kv_len", kv_len, dev, i32, (n,))
+    _chk(where, "qo_indptr", qo_indptr, dev, i32, (n + 1,))
+    _chk(where, "prefix", prefix, dev, i32, (groups, 2))
+    _chk(where, "own_indptr", own_indptr, dev, i32, (n,))
+    _chk(where, "own_len", own_len, dev, i32, (n,))
+    if window is not None:
+        _chk(where, "window", window, dev, i32, (n,))
+        window = window.data_ptr()
+    if group_indptr is not None:
+        _chk(where, "group_indptr", group_indptr, dev, i32, (groups + 1,))
+        group_indptr = group_indptr.data_ptr()
+    return PdaSharedTables(page_table.data_ptr(), kv_indptr.data_ptr(), kv_len.data_ptr(),
+                           qo_indptr.data_ptr(), window, group_indptr, prefix.data_ptr(),
+                           own_indptr.data_ptr(), own_len.data_ptr())
+
+
+def pda_share_tables(sp: PdaSharedPlan, page_table, kv_indptr, kv_len, qo_indptr, window,
+                     group_indptr, prefix, own_indptr, own_len, scratch, stream=None,
+                     check: bool = True) -> int:
+    """The prefixes that the requests of each group share (see include/pda.h): ``prefix``
+    [groups, 2], ``own_indptr`` and ``own_len`` [batch] are written; ``window`` and
+    ``group_indptr`` may be None."""
+    where = "pda_share_tables"
+    t = _shared_tables(where, sp, page_table, kv_indptr, kv_len, qo_indptr, window, group_indptr,
+                       prefix, own_indptr, own_len)
+    dev = sp.own.device
+    scratch = _scratch(where, scratch, dev, sp.scratch_bytes)
+    rc = (_LIB or load_library()).pda_share_tables(ctypes.byref(sp), ctypes.byref(t), scratch,
+                                                   _stream(stream, dev))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, where)
+    return rc
+
+
+def pda_decode_shared(sp: PdaSharedPlan, q, k_pages, v_pages, page_table, kv_indptr, kv_len,
+                      qo_indptr, max_q_len: int, window, group_indptr, prefix, own_indptr, own_len,
+                      sm_scale: float, k_scale, v_scale, out, lse, scratch, stream=None,
+                      check: bool = True) -> int:
+    """pda_decode on the tables of pda_share_tables: q [rows, Hq, D] bf16 or E4M3 codes, out
+    [rows, Hq, D] bf16, lse [rows, Hq] float32 or None."""
+    bf16, _, _, f32, e4m3, u8 = _TYPES or _types()
+    where, own = "pda_decode_shared", sp.own
+    dev, rows = own.device, q.shape[0]
+    shape = (rows, own.num_qo_heads, own.head_dim)
+    _chk(where, "q", q, dev, bf16 if own.q_dtype == PDA_BF16 else u8 if q.dtype is u8 else e4m3, shape)
+    _chk(where, "out", out, dev, bf16, shape)
+    if lse is not None:
+        _chk(where, "lse", lse, dev, f32, shape[:2])
+        lse = lse.data_ptr()
+    t = _shared_tables(where, sp, page_table, kv_indptr, kv_len, qo_indptr, window, group_indptr,
+                       prefix, own_indptr, own_len)
+    k_pages, k_scale = _cache(where, "k", k_pages, k_scale, own)
+    v_pages, v_scale = _cache(where, "v", v_pages, v_scale, own)
+    scratch = _scratch(where, scratch, dev, sp.scratch_bytes)
+    rc = (_LIB or load_library()).pda_decode_shared(
+        ctypes.byref(sp), q.data_ptr(), k_pages, v_pages, ctypes.byref(t), int(max_q_len),
+        float(sm_scale), k_scale, v_scale, out.data_ptr(), lse, scratch, _stream(stream, dev))
+    if check and rc != PDA_OK:
+        raise PdaError(rc, where)
+    return rc
+
+
 def pda_get_status(plan: PdaPlan, split_scratch, stream=None) -> int:
     """Device status bits; ``split_scratch=None`` reads those of the
     built-in array that pda_decode_static uses."""
@@ -879,3 +984,20 @@ class Pages:
 
     def reset_status(self, stream=None) -> None:
         pda_reset_status(self.plan, self.scratch, stream)
+
+
+class Shared:
+    """A plan of decodes behind shared prefixes plus its scratch (allocated once with torch), for
+    ``groups`` groups of the plan's batch and up to ``max_own_len`` own tokens a request."""
+
+    def __init__(self, plan: PdaPlan, groups: int = 1, max_own_len: int = 0, device=None):
+        import torch
+        self.plan, self.scratch_bytes, _ = pda_shared_plan(plan, groups, max_own_len)
+        self.scratch = torch.zeros(self.scratch_bytes, dtype=torch.uint8,
+                                   device=f"cuda:{plan.device}" if device is None else device)
+
+    def status(self, stream=None) -> int:
+        return pda_get_status(self.plan.own, self.scratch, stream)
+
+    def reset_status(self, stream=None) -> None:
+        pda_reset_status(self.plan.own, self.scratch, stream)

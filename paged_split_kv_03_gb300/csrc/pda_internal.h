@@ -50,6 +50,8 @@ struct DecodeArgs {
   int tma_slot_dim;       // tcgen05 path: tensor-map coordinate holding the slot (1 or 2)
   uint64_t wait_limit_ns; // tcgen05 path: bound of every pipeline wait
   uint32_t inject;        // PDA_INJECT_* test hooks set by the host (0 in normal use)
+  int final_splits;       // splits of a request whose results stage 1 writes itself: 1, or 0 where
+                          // all are partials, to be joined with those of a shared prefix
 };
 
 // The KV range one (request, split) covers. Every kernel derives it from the
@@ -121,6 +123,13 @@ int check_decode_args(const pda_plan_t* plan, const void* q, const void* k_pages
                       const int32_t* kv_len, const int32_t* qo_indptr, int32_t max_q_len,
                       const float* k_scale, const float* v_scale, const void* out,
                       const float* lse);
+
+// The arguments of both stages of one pda_decode call (checked before).
+DecodeArgs decode_args(const pda_plan_t* plan, const void* q, const void* k_pages,
+                       const void* v_pages, const int32_t* page_table, const int32_t* kv_indptr,
+                       const int32_t* kv_len, const int32_t* qo_indptr, int32_t max_q_len,
+                       const int32_t* window, float sm_scale, const float* k_scale,
+                       const float* v_scale, void* out, float* lse, void* split_scratch);
 
 // Whether `device` is the current one.
 inline bool on_device(int device) {

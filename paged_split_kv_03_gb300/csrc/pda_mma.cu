@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) stage1_mma(const __grid_constant_
   }
   __syncthreads();
 
-  const bool single = sr.num_splits == 1;
+  const bool single = sr.num_splits == a.final_splits;
   constexpr int kC4 = D / 4;
   for (int idx = tid; idx < M * kC4; idx += kThreads) {
     const int m = idx / kC4, c4 = idx % kC4;

@@ -412,28 +412,12 @@ int check_decode_args(const pda_plan_t* plan, const void* q, const void* k_pages
   return PDA_OK;
 }
 
-}  // namespace pda
-
-extern "C" int pda_decode_stages(const pda_plan_t* plan, const void* q, const void* k_pages,
-                                 const void* v_pages, const int32_t* page_table,
-                                 const int32_t* kv_indptr, const int32_t* kv_len,
-                                 const int32_t* qo_indptr, int32_t max_q_len,
-                                 const int32_t* window, float sm_scale, const float* k_scale,
-                                 const float* v_scale, void* out, float* lse,
-                                 void* split_scratch, uint32_t stages, pda_stream_t stream) {
-  if (!plan) return PDA_ERR_NULL;
-  if (stages == 0 || (stages & ~(PDA_STAGE_PARTIAL | PDA_STAGE_MERGE))) return PDA_ERR_INVALID;
-  if (plan->magic != PDA_PLAN_MAGIC) return PDA_ERR_PLAN;
-  if (!q || !k_pages || !v_pages || !page_table || !kv_indptr || !kv_len || !qo_indptr || !out)
-    return PDA_ERR_NULL;
-  if (!split_scratch) return PDA_ERR_SCRATCH;
-  if (reinterpret_cast<uintptr_t>(split_scratch) % 256) return PDA_ERR_SCRATCH;
-  const int rc0 = pda::check_decode_args(plan, q, k_pages, v_pages, page_table, kv_indptr, kv_len,
-                                         qo_indptr, max_q_len, k_scale, v_scale, out, lse);
-  if (rc0 != PDA_OK) return rc0;
-  if (plan->batch == 0) return PDA_OK;
-
-  pda::DecodeArgs a;
+DecodeArgs decode_args(const pda_plan_t* plan, const void* q, const void* k_pages,
+                       const void* v_pages, const int32_t* page_table, const int32_t* kv_indptr,
+                       const int32_t* kv_len, const int32_t* qo_indptr, int32_t max_q_len,
+                       const int32_t* window, float sm_scale, const float* k_scale,
+                       const float* v_scale, void* out, float* lse, void* split_scratch) {
+  DecodeArgs a;
   std::memset(&a, 0, sizeof a);
   a.q = q;
   a.k = k_pages;
@@ -476,7 +460,35 @@ extern "C" int pda_decode_stages(const pda_plan_t* plan, const void* q, const vo
   a.wait_limit_ns = static_cast<uint64_t>(plan->wait_limit_us > 0 ? plan->wait_limit_us : 2000000) *
                     1000ull;
   a.inject = plan->inject;
-  for (int r = 0; r <= pda::kMaxQLen; ++r) a.hpc[r] = plan->heads_per_cta[r];
+  a.final_splits = 1;
+  for (int r = 0; r <= kMaxQLen; ++r) a.hpc[r] = plan->heads_per_cta[r];
+  return a;
+}
+
+}  // namespace pda
+
+extern "C" int pda_decode_stages(const pda_plan_t* plan, const void* q, const void* k_pages,
+                                 const void* v_pages, const int32_t* page_table,
+                                 const int32_t* kv_indptr, const int32_t* kv_len,
+                                 const int32_t* qo_indptr, int32_t max_q_len,
+                                 const int32_t* window, float sm_scale, const float* k_scale,
+                                 const float* v_scale, void* out, float* lse,
+                                 void* split_scratch, uint32_t stages, pda_stream_t stream) {
+  if (!plan) return PDA_ERR_NULL;
+  if (stages == 0 || (stages & ~(PDA_STAGE_PARTIAL | PDA_STAGE_MERGE))) return PDA_ERR_INVALID;
+  if (plan->magic != PDA_PLAN_MAGIC) return PDA_ERR_PLAN;
+  if (!q || !k_pages || !v_pages || !page_table || !kv_indptr || !kv_len || !qo_indptr || !out)
+    return PDA_ERR_NULL;
+  if (!split_scratch) return PDA_ERR_SCRATCH;
+  if (reinterpret_cast<uintptr_t>(split_scratch) % 256) return PDA_ERR_SCRATCH;
+  const int rc0 = pda::check_decode_args(plan, q, k_pages, v_pages, page_table, kv_indptr, kv_len,
+                                         qo_indptr, max_q_len, k_scale, v_scale, out, lse);
+  if (rc0 != PDA_OK) return rc0;
+  if (plan->batch == 0) return PDA_OK;
+
+  const pda::DecodeArgs a = pda::decode_args(plan, q, k_pages, v_pages, page_table, kv_indptr, kv_len,
+                                             qo_indptr, max_q_len, window, sm_scale, k_scale, v_scale,
+                                             out, lse, split_scratch);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int rc = PDA_OK;
   if (stages & PDA_STAGE_PARTIAL)

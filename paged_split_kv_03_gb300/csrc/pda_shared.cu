@@ -1,0 +1,1462 @@
+// pda_shared.cu -- decode attention for requests that share a long prefix: the
+// prefix's keys and values meet the rows of all of them at once, on the
+// 5th-generation tensor cores; each request's own tokens go through stage 1 of
+// pda_decode, and a join adds both up.
+//
+// Mathematics: with the keys of a row split into those of the prefix, in segments s,
+// and its own, in chunks c, each part gives a normalised output o and a log2 sum
+// x of its weights; out = sum 2^(x - X) o with X the log2 sum of all of them. A row
+// of a group stands at or behind the prefix's end, so it sees all of it but for its
+// window. A segment is flash attention: for 128 rows (query rows x heads of a GQA
+// group, packed without gaps), over tiles of 128 keys, S = Q K^T, an online softmax
+// in log2 units with a lazy maximum (moved when a logit passes it by more than 8, so
+// weights stay <= 2^8 and are exact in l and O), O += P V. P is rounded to the
+// operands' 16-bit type, l sums the unrounded weights in fp32.
+//
+// Types: bf16 caches run bf16 MMAs. E4M3 and int8 codes are widened exactly to f16 and
+// run f16 MMAs with an f16 query: an E4M3 query is exact in it, a bf16 row too, once
+// its power of two is taken out (below 2^-14 of it rounded at 2^-25). Scales per
+// tensor meet the logits and the output; scales per token and head meet S and P in
+// fp32, the value scale as its log2, so that P <= 2^8 whatever the scale.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "pda.h"
+#include "pda_cvt.cuh"
+#include "pda_internal.h"
+#include "pda_ptx.cuh"
+
+namespace pda {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMInit = -3.0e38f;  // before any key: finite, so that ex2(-inf - m) = 0
+constexpr float kTh = 8.0f;         // lazy rescale threshold, log2 units
+
+constexpr int kKeys = 128;     // keys of a tile
+constexpr int kTile = 128;     // rows of a softmax warpgroup
+constexpr int kUnit = 16384;   // bytes of a ring unit
+constexpr int kItems = 3;      // slots of the segment ring
+constexpr int kScales = 4;     // slots of the ring of per-token scales, a tile each
+constexpr int kCoarse = 256;   // prefix entries, 32 groups each
+constexpr int kMaxGroups = 32 * kCoarse;
+constexpr int kTmemCols = 512;
+constexpr int kO = 2 * kKeys;  // first TMEM column of O; two S in front of it
+constexpr int kMinTiles = 1;   // least key tiles of a CTA
+
+// ------------------------------------------------- the groups and their prefixes
+
+struct SharedArgs {
+  const void* q;
+  const int32_t* page_table;
+  const int32_t* qo_indptr;
+  const int32_t* kv_len;
+  const int32_t* window;
+  const int32_t* group_indptr;  // NULL: one group of all requests
+  const int32_t* prefix;        // [groups][2] tokens
+  const int32_t* own_indptr;
+  const int32_t* own_len;
+  const float* k_scale;
+  const float* v_scale;
+  float* main_o;    // [kv head][row x group][D] fp32: segments that start their item
+  float* main_x;    // ... and their log2 sums
+  float* area_o;    // [CTA][rows of an item][D]: the segment a CTA starts inside an item
+  float* area_x;
+  int64_t* first;   // [groups] first unit of each group, and in front the units of a CTA
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  float sm_scale;
+  int batch, groups, hq, hkv, group, page_size, num_pages, max_q_len;
+  int64_t rows_cap;
+  int q8;
+  uint32_t inject;
+};
+
+// A group's rows and its prefix's key tiles.
+struct Group {
+  int b0, b1, q0, rows, tile0, tiles, end;
+  uint32_t bad;
+};
+__device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
+  Group r;
+  r.b0 = a.group_indptr ? __ldg(a.group_indptr + g) : 0;
+  r.b1 = a.group_indptr ? __ldg(a.group_indptr + g + 1) : a.batch;
+  r.bad = r.b0 < 0 || r.b1 < r.b0 || r.b1 > a.batch ? PDA_STATUS_TABLE_INVALID : 0u;
+  r.q0 = r.rows = r.tile0 = r.tiles = r.end = 0;
+  if (r.bad) return r;
+  r.q0 = __ldg(a.qo_indptr + r.b0);
+  const int64_t rows = static_cast<int64_t>(__ldg(a.qo_indptr + r.b1)) - r.q0;
+  if (r.q0 < 0 || rows < 0 || r.q0 + rows > a.rows_cap) {
+    r.bad = PDA_STATUS_ROWS_GT_CAP;
+    return r;
+  }
+  r.rows = static_cast<int>(rows);
+  const int from = max(0, __ldg(a.prefix + 2 * g));
+  r.end = __ldg(a.prefix + 2 * g + 1);
+  if (r.rows == 0 || r.end <= from) return r;
+  r.tile0 = from / kKeys;
+  r.tiles = (r.end - 1) / kKeys + 1 - r.tile0;
+  return r;
+}
+
+// Work in units of a key tile of an item (a block of packed rows of a kv head):
+// group by group, then kv heads, blocks, tiles. CTA c has units [c n, (c + 1) n).
+template <int kRows>
+__device__ __forceinline__ int blocks_of(const SharedArgs& a, const Group& r) {
+  return static_cast<int>((static_cast<int64_t>(r.rows) * a.group + kRows - 1) / kRows);
+}
+template <int kRows>
+__device__ __forceinline__ int64_t units_of(const SharedArgs& a, const Group& r) {
+  return static_cast<int64_t>(a.hkv) * blocks_of<kRows>(a, r) * r.tiles;
+}
+
+// One segment: key tiles [t0, t1) of an item.
+struct Item {
+  int head;    // kv head; -1: no more
+  int row0;    // first packed row of the block (of the group: row x group + head)
+  int rows;    // packed rows, 1..kRows
+  int q0;      // the group's first row in q
+  int b0, b1;  // its requests
+  int t0, t1;
+  int end;     // the prefix's end, tokens
+  int table;   // offset of the prefix's pages in page_table
+  int cut;     // the segment does not start its item: its partials go to the CTA's area
+};
+
+struct Shared {
+  uint64_t q_full[2], q_empty[2], full[16], empty[16], raw_full[4], raw_empty[4], sc_full[kScales],
+      sc_empty[kScales], s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], item_full[kItems],
+      item_empty[kItems], drain;
+  uint32_t tmem;
+  int abort_flag;
+  Item items[kItems];
+  int64_t coarse[kCoarse];
+};
+
+// ------------------------------------------------------------ configuration
+template <int D, bool k8, bool kTok>
+struct Cfg {
+  static constexpr int kG = D <= 128 ? 2 : 1;  // row tiles of an item
+  static constexpr int kRows = kG * kTile;
+  static constexpr int kU = D / 64;            // ring units of a K tile, and of a V tile
+  static constexpr int kVKeys = 8192 / D;      // keys of a V unit
+  static constexpr int kQBytes = kG * kU * kUnit;
+  // 8-bit caches: codes land in raw slots of kRawKeys keys, as they lie in the cache
+  static constexpr int kRawKeys = D <= 128 ? 128 : 64;
+  static constexpr int kRawBytes = kRawKeys * D;
+  static constexpr int kRawTile = kKeys / kRawKeys;  // slots of a K or V tile
+  static constexpr int kRaw = !k8 ? 0 : D == 64 ? 4 : D == 128 ? (kTok ? 3 : 4) : kTok ? 3 : 2;
+  static constexpr int kRing = !k8 ? (D == 64 ? 8 : 10) : D == 64 ? 8 : D == 128 || kTok ? 6 : 8;
+  static constexpr int kScaleBytes = kTok ? (kScales * 3 + 2) * kKeys * 4 : 0;
+  static constexpr int kSmem = kQBytes + kRing * kUnit + kRaw * kRawBytes + kScaleBytes +
+                               static_cast<int>(sizeof(Shared));
+  static constexpr int kSoft = 4 * kG;              // softmax warps, a thread per row
+  static constexpr int kMmaWarp = kSoft, kWorkWarp = kSoft + 1, kProd0 = kSoft + 2;
+  // warps that issue loads, and warps that widen codes: the last four are either
+  static constexpr int kProds = k8 ? 2 : 6;
+  static constexpr int kConv0 = kSoft + 4;
+  static constexpr int kThreads = 32 * (kSoft + 8);
+  static constexpr int kReaders = kSoft + 1 + kProds + (k8 ? 4 : 0);  // arrivals that free an item
+  static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA an SM");
+  static_assert(kRing <= 16 && kRaw <= 4, "barriers");
+};
+
+struct ItemReader {
+  Shared* sh;
+  uint32_t n = 0;
+  __device__ explicit ItemReader(Shared* s) : sh(s) {}
+  // One thread: the next segment, or false after the last one (or an abort).
+  __device__ bool next_one(Item& it, const SharedArgs& a) {
+    const uint32_t slot = n % kItems;
+    if (!bar_wait(sh->item_full + slot, (n / kItems) & 1u, &sh->abort_flag, a)) return false;
+    it = sh->items[slot];
+    bar_arrive(sh->item_empty + slot);
+    ++n;
+    return it.head >= 0;
+  }
+  // A whole warp (one arrival); warp-uniform.
+  __device__ bool next_warp(Item& it, const SharedArgs& a) {
+    const uint32_t slot = n % kItems;
+    const bool ok = bar_wait(sh->item_full + slot, (n / kItems) & 1u, &sh->abort_flag, a);
+    if (!__all_sync(0xffffffffu, ok)) return false;
+    it = sh->items[slot];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) bar_arrive(sh->item_empty + slot);
+    ++n;
+    return it.head >= 0;
+  }
+};
+
+// 4-D tiled TMA load of one box (channel, slot, kv head, page).
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int c, int slot, int head,
+                                         int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c), "r"(slot), "r"(head), "r"(page), "r"(su32(bar))
+      : "memory");
+}
+
+// The order in which the K and V tiles of a segment of n pass through the ring, which
+// is the MMAs': with two row tiles K0 V0 K1 V1 ..., with two S of one row tile
+// K0 K1 V0 K2 V1 ... . Place i of 2n -> (V?, tile).
+template <int kG>
+__device__ __forceinline__ void ring_order(int i, int n, int& v, int& j) {
+  if constexpr (kG == 2) {
+    v = i & 1;
+    j = i >> 1;
+  } else {
+    if (i == 2 * n - 1) v = 1, j = n - 1;
+    else if (i == 0) v = 0, j = 0;
+    else v = (i & 1) ^ 1, j = v ? i / 2 - 1 : (i + 1) / 2;
+  }
+}
+
+// ------------------------------------------------------------------- loads
+//
+// A unit is one warp's, warps in turn; its boxes (a page's tokens x 128 bytes) are
+// its lanes'. A page behind the prefix is one past the cache: such a box reads as zeros.
+template <class C, int D, bool k8>
+__device__ __forceinline__ void load_role(const SharedArgs& a, Shared* sh, uint8_t* ring, uint8_t* raw,
+                                          const CUtensorMap* tk, const CUtensorMap* tv, int pw) {
+  volatile int* abort_flag = &sh->abort_flag;
+  const int lane = threadIdx.x & 31;
+  ItemReader reader(sh);
+  Item it{};
+  uint32_t x = 0;  // units (raw slots) so far, of all warps
+  bool alive = (a.inject & PDA_INJECT_WITHHOLD_KV) == 0u;
+  constexpr int kPer = k8 ? C::kRawTile : C::kU;  // units of a tile
+  constexpr uint32_t kSlots = k8 ? (C::kRaw ? C::kRaw : 1) : C::kRing;
+  uint64_t* full = k8 ? sh->raw_full : sh->full;
+  uint64_t* empty = k8 ? sh->raw_empty : sh->empty;
+  const uint32_t base = su32(k8 ? raw : ring);
+  const uint32_t slot_bytes = k8 ? C::kRawBytes : kUnit;
+  const int P = a.page_size;
+  while (alive && reader.next_warp(it, a)) {
+    const int n = it.t1 - it.t0;
+    for (int i = 0; i < 2 * n && alive; ++i) {
+      int v, j;
+      ring_order<C::kG>(i, n, v, j);
+      const int key0 = (it.t0 + j) * kKeys;
+      for (int c = 0; c < kPer; ++c, ++x) {
+        if (x % C::kProds != static_cast<uint32_t>(pw)) continue;
+        // this lane's box: `rows` keys from `key` on, channels from `chan` on
+        const int unit_keys = k8 ? C::kRawKeys : v ? C::kVKeys : kKeys;
+        const int rows = min(P, unit_keys), boxes = unit_keys / rows;
+        const int atoms = !k8 && v ? C::kU : 1;
+        const int at = lane % boxes, atom = lane / boxes;
+        const int key = key0 + (k8 || v ? c * unit_keys : 0) + at * rows;
+        const int chan = k8 ? 0 : (v ? atom : c) * 64;
+        const bool mine = atom < atoms;
+        int page = a.num_pages;
+        if (mine && key < it.end) {
+          page = __ldg(a.page_table + it.table + key / P);
+          if (page < 0 || page > a.num_pages) page = a.num_pages;
+        }
+        const uint32_t slot = x % kSlots;
+        int good = 1;
+        if (lane == 0) {
+          good = bar_wait(empty + slot, ((x / kSlots) & 1u) ^ 1u, abort_flag, a);
+          if (good) bar_expect_tx(full + slot, slot_bytes);
+        }
+        if (!__shfl_sync(0xffffffffu, good, 0)) {
+          alive = false;
+          break;
+        }
+        if (mine) {
+          const uint32_t row_bytes = k8 ? D : 128;
+          const uint32_t dst = base + slot * slot_bytes + atom * (unit_keys * 128) + at * rows * row_bytes;
+          tma_page(dst, v ? tv : tk, chan, key % P, it.head, page, full + slot);
+        }
+      }
+    }
+  }
+  // every box issued must have landed before the CTA can exit
+  if (lane == 0)
+    for (uint32_t k = x > kSlots ? x - kSlots : 0u; k < x; ++k)
+      if (k % C::kProds == static_cast<uint32_t>(pw)) bar_drain(full + k % kSlots, (k / kSlots) & 1u);
+}
+
+// -------------------------------------------------------------------- MMAs
+template <class C, int D, bool k8>
+__device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring) {
+  volatile int* abort_flag = &sh->abort_flag;
+  constexpr uint32_t tmem = 0;  // all columns are ours: they start at 0
+  constexpr uint32_t fmt = k8 ? 0u : 1u, R = C::kRing;
+  const uint32_t id_s = idesc(fmt, 0, kKeys), id_o = idesc(fmt, 0, D, 1u);
+  const uint64_t q_desc = sdesc(su32(q_s), 16, 1024), k_desc = sdesc(su32(ring), 16, 1024),
+                 v_desc = sdesc(su32(ring), C::kVKeys * 128, 1024);
+  ItemReader reader(sh);
+  Item it{};
+  uint32_t x = 0;                      // ring units in front of the segment
+  uint32_t seq0 = 0, seq1 = 0;         // tiles so far of each row tile
+  uint32_t qn0 = 0, qn1 = 0;           // segments so far of each row tile
+  bool alive = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return alive = bar_try(bar, parity & 1u) || bar_wait_slow(bar, parity & 1u, abort_flag, a);
+  };
+  // S = Q K^T of row tile g into S buffer b; K at unit u
+  auto qk = [&](int g, int b, uint32_t u, bool release) {
+#pragma unroll
+    for (int c = 0; c < C::kU; ++c) {
+      const uint32_t slot = (u + c) % R;
+      if (!wait(sh->full + slot, (u + c) / R)) return;
+      if (c == 0) fence_after();
+      const uint64_t kd = k_desc + slot * (kUnit / 16);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        mma<false>(tmem + b * kKeys, q_desc + (g * C::kU + c) * (kUnit / 16) + kk * 2, kd + kk * 2, id_s,
+                   (c | kk) != 0);
+      if (release) mma_commit(sh->empty + slot);
+    }
+    mma_commit(sh->s_full + b);
+  };
+  // O += P V of row tile g, P over S buffer b; V at unit u
+  auto pv = [&](int g, int b, uint32_t u, uint32_t parity, bool first, bool release) {
+    if (!wait(sh->p_half + b, parity)) return;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {  // 16 keys a step
+      constexpr int kSteps = C::kVKeys / 16;
+      const uint32_t slot = (u + kk / kSteps) % R;
+      if (kk % kSteps == 0 && !wait(sh->full + slot, (u + kk / kSteps) / R)) return;
+      if (kk == 4 && !wait(sh->p_full + b, parity)) return;
+      if (kk % kSteps == 0 || kk == 4) fence_after();
+      mma_ts(tmem + kO + g * D, tmem + b * kKeys + kk * 8,
+             v_desc + slot * (kUnit / 16) + (kk % kSteps) * 128, id_o, kk || !first ? 1u : 0u);
+      if (release && kk % kSteps == kSteps - 1) mma_commit(sh->empty + slot);
+    }
+    mma_commit(sh->o_done + b);
+  };
+  while (alive && reader.next_one(it, a)) {
+    const int n = it.t1 - it.t0;
+    if constexpr (C::kG == 2) {
+      const bool two = it.rows > kTile;
+      for (int j = -1; j < n && alive; ++j) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (g && !two) break;
+          const bool last = g || !two;  // the units' last reader
+          const uint32_t xv = x + (2 * j + 1) * C::kU, xk = x + (2 * j + 2) * C::kU;
+          uint32_t& seq = g ? seq1 : seq0;
+          uint32_t& qn = g ? qn1 : qn0;
+          if (j >= 0) {
+            if (j == 0 && !wait(sh->o_free + g, (qn - 1) ^ 1u)) break;  // the last segment's O is read
+            pv(g, g, xv, seq, j == 0, last);
+            if (!alive) break;
+            ++seq;
+          }
+          if (j + 1 < n) {
+            if (j + 1 == 0) {
+              if (!wait(sh->q_full + g, qn)) break;
+              ++qn;
+            }
+            qk(g, g, xk, last);
+            if (!alive) break;
+            if (j + 2 == n) mma_commit(sh->q_empty + g);
+          }
+        }
+      }
+    } else {
+      auto at_k = [&](int j) { return x + (j == 0 ? 0 : 2 * j - 1) * C::kU; };
+      auto at_v = [&](int j) { return x + min(2 * j + 2, 2 * n - 1) * C::kU; };
+      if (!wait(sh->q_full, qn0)) break;
+      ++qn0;
+      qk(0, seq0 & 1u, at_k(0), true);
+      if (alive && n > 1) qk(0, (seq0 + 1) & 1u, at_k(1), true);
+      if (alive && n <= 2) mma_commit(sh->q_empty);
+      for (int j = 0; j < n && alive; ++j) {
+        if (j == 0 && !wait(sh->o_free, (qn0 - 1) ^ 1u)) break;
+        pv(0, seq0 & 1u, at_v(j), seq0 >> 1, j == 0, true);
+        if (!alive) break;
+        ++seq0;
+        if (j + 2 < n) {
+          qk(0, (seq0 + 1) & 1u, at_k(j + 2), true);
+          if (j + 3 == n) mma_commit(sh->q_empty);
+        }
+      }
+    }
+    x += 2 * n * C::kU;
+  }
+  // nothing issued may still run when TMEM is released
+  mma_commit(&sh->drain);
+  bar_drain(&sh->drain, 0);
+}
+
+// ------------------------------------------------------ codes widened to f16
+//
+// Four warps: a raw slot's codes, 16 at a time, into the ring's units, and the tile's
+// scales per token (loaded a tile ahead) into a ring of their own.
+__device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, bool i8) {
+  uint32_t r[4];
+  const uint32_t w[2] = {lo, hi};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (i8) {
+      // with u = x + 128, the f16 word 0x6400 | u is 1024 + u: subtract 1152
+      const uint32_t u = w[k] ^ 0x80808080u;
+      uint32_t p, q;
+      asm("prmt.b32 %0, %1, %2, 0x5140;" : "=r"(p) : "r"(u), "r"(0x64646464u));
+      asm("prmt.b32 %0, %1, %2, 0x7362;" : "=r"(q) : "r"(u), "r"(0x64646464u));
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[2 * k]) : "r"(p), "r"(0x64806480u));
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[2 * k + 1]) : "r"(q), "r"(0x64806480u));
+    } else {
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r[2 * k]) : "h"(static_cast<uint16_t>(w[k] & 0xFFFFu)));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r[2 * k + 1]) : "h"(static_cast<uint16_t>(w[k] >> 16)));
+    }
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <class C, int D, bool kI8, bool kTok>
+__device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint8_t* ring,
+                                           const uint8_t* raw, float* scales) {
+  const int t = threadIdx.x - 32 * C::kConv0, lane = threadIdx.x & 31;
+  ItemReader reader(sh);
+  Item it{};
+  uint32_t x = 0, y = 0, s = 0;  // ring units, raw slots, tiles of scales
+  constexpr uint32_t R = C::kRing, RR = C::kRaw;
+  const int P = a.page_size;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = bar_wait(bar, parity & 1u, &sh->abort_flag, a);
+    return __all_sync(0xffffffffu, ok);
+  };
+  const float qk = a.sm_scale * kLog2e;
+  float ks = 1.f, vs = 1.f;  // of this thread's key in the next tile
+  auto load_scales = [&](int tile) {
+    const int key = tile * kKeys + t;
+    ks = vs = 1.f;
+    if (key < it.end) {
+      const int page = __ldg(a.page_table + it.table + key / P);
+      if (page >= 0 && page < a.num_pages) {
+        const int64_t at = (static_cast<int64_t>(page) * P + key % P) * a.hkv + it.head;
+        ks = __ldg(a.k_scale + at);
+        vs = __ldg(a.v_scale + at);
+      }
+    }
+  };
+  while (reader.next_warp(it, a)) {
+    const int n = it.t1 - it.t0;
+    if constexpr (kTok) load_scales(it.t0);
+    for (int i = 0; i < 2 * n; ++i) {
+      int v, j;
+      ring_order<C::kG>(i, n, v, j);
+      if constexpr (kTok) {
+        if (!v) {  // the K tiles come in order
+          const uint32_t slot = s % kScales;
+          if (!wait(sh->sc_empty + slot, (s / kScales) ^ 1u)) return;
+          float* to = scales + slot * 3 * kKeys;
+          const float v2 = vs > 0.f ? vs : 1.f;
+          to[t] = ks * qk;
+          to[kKeys + t] = __log2f(v2);
+          to[2 * kKeys + t] = __frcp_rn(v2);
+          __syncwarp();
+          if (lane == 0) bar_arrive(sh->sc_full + slot);
+          ++s;
+          if (j + 1 < n) load_scales(it.t0 + j + 1);
+        }
+      }
+      // the units this tile's codes go to
+      for (int c = 0; c < C::kU; ++c)
+        if (!wait(sh->empty + (x + c) % R, ((x + c) / R) ^ 1u)) return;
+      for (int h = 0; h < C::kRawTile; ++h, ++y) {
+        const uint32_t slot = y % RR;
+        if (!wait(sh->raw_full + slot, y / RR)) return;
+        const uint8_t* src = raw + slot * C::kRawBytes;
+        constexpr int kRowPieces = D / 16;
+#pragma unroll 4
+        for (int p = 0; p < C::kRawKeys * kRowPieces / 128; ++p) {
+          const int idx = p * 128 + t;
+          const int row = idx / kRowPieces, piece = idx % kRowPieces;
+          const uint4 w = *reinterpret_cast<const uint4*>(src + idx * 16);
+          const uint4 lo = widen8(w.x, w.y, kI8), hi = widen8(w.z, w.w, kI8);
+          const int key = h * C::kRawKeys + row, atom = piece >> 2, chunk = (piece & 3) * 2;
+          // K: a unit per 64 channels; V: a unit per kVKeys keys, its atoms one after another
+          const uint32_t u = v ? x + key / C::kVKeys : x + atom;
+          const int r = v ? key % C::kVKeys : key;
+          uint8_t* dst = ring + u % R * kUnit + (v ? atom * (C::kVKeys * 128) : 0);
+          // (a row's atoms share banks: every other one writes its halves in turn)
+          const int flip = atom & 1;
+          *reinterpret_cast<uint4*>(dst + sw128(r, (chunk + flip) * 16)) = flip ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + sw128(r, (chunk + 1 - flip) * 16)) = flip ? lo : hi;
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(sh->raw_empty + slot);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        for (int c = 0; c < C::kU; ++c) bar_arrive(sh->full + (x + c) % R);
+      x += C::kU;
+    }
+  }
+}
+
+// --------------------------------------------------------------- the work list
+template <int kRows>
+__device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh) {
+  const int lane = threadIdx.x & 31;
+  int64_t total = 0;
+  uint32_t bits = 0u;
+  for (int g0 = 0; g0 < a.groups; g0 += 32) {
+    int64_t n = 0;
+    if (g0 + lane < a.groups) {
+      const Group r = group_of(a, g0 + lane);
+      bits |= r.bad;
+      n = units_of<kRows>(a, r);
+    }
+    int64_t x = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 0) sh->coarse[g0 >> 5] = total;
+    if (blockIdx.x == 0 && g0 + lane < a.groups) a.first[1 + g0 + lane] = total + x - n;
+    total += __shfl_sync(0xffffffffu, x, 31);
+  }
+  __syncwarp();
+  const int64_t per = max(static_cast<int64_t>(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
+  if (blockIdx.x == 0) {
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0) {
+      a.first[0] = per;
+      if (bits) atomicOr(a.status, bits);
+    }
+  }
+  int64_t pos = blockIdx.x * per;
+  const int64_t stop = min(total, pos + per);
+  uint32_t n = 0;
+  for (;;) {
+    Item it = {};
+    it.head = -1;
+    if (pos < stop) {
+      int c = 0, top = (a.groups + 31) / 32 - 1;
+      while (c < top) {
+        const int mid = (c + top + 1) >> 1;
+        if (sh->coarse[mid] <= pos) c = mid;
+        else top = mid - 1;
+      }
+      const int g = 32 * c + lane;
+      Group r = {};
+      if (g < a.groups) r = group_of(a, g);
+      const int64_t mine = g < a.groups ? units_of<kRows>(a, r) : 0;
+      int64_t upto = mine;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+      }
+      const int64_t want = pos - sh->coarse[c];
+      const int src = __ffs(__ballot_sync(0xffffffffu, upto > want)) - 1;
+      const int64_t in = want - __shfl_sync(0xffffffffu, upto - mine, src);
+      r.b0 = __shfl_sync(0xffffffffu, r.b0, src);
+      r.b1 = __shfl_sync(0xffffffffu, r.b1, src);
+      r.q0 = __shfl_sync(0xffffffffu, r.q0, src);
+      r.rows = __shfl_sync(0xffffffffu, r.rows, src);
+      r.tile0 = __shfl_sync(0xffffffffu, r.tile0, src);
+      r.tiles = __shfl_sync(0xffffffffu, r.tiles, src);
+      r.end = __shfl_sync(0xffffffffu, r.end, src);
+      const int blocks = blocks_of<kRows>(a, r);
+      const int item = static_cast<int>(in / r.tiles), t = static_cast<int>(in % r.tiles);
+      it.head = item / blocks;
+      it.row0 = item % blocks * kRows;
+      it.rows = static_cast<int>(min(static_cast<int64_t>(kRows),
+                                     static_cast<int64_t>(r.rows) * a.group - it.row0));
+      it.q0 = r.q0;
+      it.b0 = r.b0;
+      it.b1 = r.b1;
+      it.t0 = r.tile0 + t;
+      it.t1 = it.t0 + static_cast<int>(min(static_cast<int64_t>(r.tiles - t), stop - pos));
+      it.end = r.end;
+      it.cut = t > 0;
+      // the prefix's pages stand in front of a request's own, where it has any
+      it.table = 0;
+      for (int b0 = r.b0; b0 < r.b1; b0 += 32) {
+        const int b = b0 + lane;
+        const uint32_t has =
+            __ballot_sync(0xffffffffu, b < r.b1 && __ldg(a.own_len + min(b, r.b1 - 1)) > 0);
+        if (has) {
+          it.table = __ldg(a.own_indptr + b0 + __ffs(has) - 1) - r.end / a.page_size;
+          break;
+        }
+      }
+      pos += it.t1 - it.t0;
+    }
+    const uint32_t slot = n % kItems;
+    bool ok = true;
+    if (n >= kItems) ok = bar_wait(sh->item_empty + slot, ((n / kItems) - 1) & 1u, &sh->abort_flag, a);
+    if (!__all_sync(0xffffffffu, ok)) break;
+    if (lane == 0) {
+      sh->items[slot] = it;
+      bar_arrive(sh->item_full + slot);
+    }
+    __syncwarp();
+    ++n;
+    if (it.head < 0) break;
+  }
+}
+
+// ------------------------------------------------------------------ softmax
+
+// Packed row m of a group: row m / group of its rows, head m % group of the kv head.
+// Its query into 128-byte-swizzled blocks of 64 channels, in the operands' type;
+// returns the power of two taken out of it.
+template <class C, int D, bool k8>
+__device__ __forceinline__ float load_query(const SharedArgs& a, const Item& it, uint8_t* q_s, int r, int m) {
+  const bool live = m < it.row0 + it.rows;
+  const int64_t row = static_cast<int64_t>(it.q0) + (live ? m / a.group : 0);
+  const int head = it.head * a.group + (live ? m % a.group : 0);
+  const int64_t at = (row * a.hq + head) * D;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if constexpr (!k8) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+#pragma unroll 8
+    for (int c = 0; c < D / 8; ++c)
+      *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) = live ? __ldg(src + c) : zero;
+    return 1.f;
+  } else {
+    if (a.q8) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at);
+#pragma unroll 4
+      for (int c = 0; c < D / 16; ++c) {
+        const uint4 w = live ? __ldg(src + c) : zero;
+        uint8_t* dst = q_s + (c >> 2) * kUnit;
+        *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32)) = widen8(w.x, w.y, false);
+        *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32 + 16)) = widen8(w.z, w.w, false);
+      }
+      return 1.f;
+    }
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
+    uint32_t top = 0u;  // largest magnitude's bits
+#pragma unroll 8
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 w = live ? __ldg(src + c) : zero;
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = max(top, max(v[e] << 16 & 0x7FFF0000u, v[e] & 0x7FFF0000u));
+    }
+    // 2^-6 <= largest < 2^12: as it is; NaN and infinity too
+    int ex = static_cast<int>(top >> 23) - 127;
+    if (top == 0u || ex == 128 || (ex >= -6 && ex < 12)) ex = 0;
+    ex = max(-126, min(126, ex));
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+#pragma unroll 8
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 w = live ? __ldg(src + c) : zero;
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const __half2 p = __floats2half2_rn(__uint_as_float(v[e] << 16) * down,
+                                            __uint_as_float(v[e] & 0xFFFF0000u) * down);
+        h[e] = *reinterpret_cast<const uint32_t*>(&p);
+      }
+      *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) =
+          make_uint4(h[0], h[1], h[2], h[3]);
+    }
+    return __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+  }
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// A thread per row, its 128 logits in registers.
+template <class C, int D, bool k8, bool kTok>
+__device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, uint8_t* q_s,
+                                             const float* scales, uint32_t tmem, int warp) {
+  volatile int* abort_flag = &sh->abort_flag;
+  const int lane = threadIdx.x & 31, quad = warp & 3, g = warp >> 2;
+  const int r = quad * 32 + lane;  // row of the tile
+  const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+  const uint32_t t_o = tmem + lanes + kO + g * D;
+  // logits in log2 units: s * scale, with the sign (or zero) applied to s first
+  float logit = a.sm_scale * kLog2e, v_final = 1.f;
+  if (k8 && !kTok) {
+    logit *= __ldg(a.k_scale);
+    v_final = __ldg(a.v_scale);
+  }
+  const float sign = kTok ? 1.f : logit < 0.f ? -1.f : logit == 0.f ? 0.f : 1.f;
+  ItemReader reader(sh);
+  Item it{};
+  uint32_t n = 0, qn = 0, sc = 0;  // key tiles, segments of this row tile; tiles of scales
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = bar_wait(bar, parity & 1u, abort_flag, a);
+    return __all_sync(0xffffffffu, ok);
+  };
+  auto buf = [&](uint32_t k) { return C::kG == 2 ? g : static_cast<int>(k & 1u); };
+  auto par = [&](uint32_t k) { return C::kG == 2 ? k : k >> 1; };
+  while (reader.next_warp(it, a)) {
+    const int tile_rows = min(kTile, it.rows - g * kTile);
+    if (tile_rows <= 0) {
+      if constexpr (kTok) {  // the tiles' scales are let go all the same
+        for (int j = it.t0; j < it.t1; ++j, ++sc) {
+          if (!wait(sh->sc_full + sc % kScales, sc / kScales)) return;
+          if (lane == 0) bar_arrive(sh->sc_empty + sc % kScales);
+        }
+      }
+      continue;
+    }
+    const int m0 = it.row0 + g * kTile + r;
+    if (!wait(sh->q_empty + g, qn ^ 1u)) return;
+    const float up = load_query<C, D, k8>(a, it, q_s + g * C::kU * kUnit, r, m0);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) bar_arrive(sh->q_full + g);
+    ++qn;
+    const bool fix = kTok && __any_sync(0xffffffffu, up != 1.f);
+    float scale = 1.f;
+    if constexpr (!kTok) scale = (sign != 0.f ? fabsf(logit) : 1.f) * up;
+    // first key this row sees
+    int first = 0;
+    if (a.window && r < tile_rows) {
+      const int row = it.q0 + m0 / a.group;
+      int b = it.b0, top = it.b1 - 1;
+      while (b < top) {
+        const int mid = (b + top + 1) >> 1;
+        if (__ldg(a.qo_indptr + mid) <= row) b = mid;
+        else top = mid - 1;
+      }
+      const int w = __ldg(a.window + b);
+      if (w > 0) first = max(0, __ldg(a.kv_len + b) - (__ldg(a.qo_indptr + b + 1) - row) - w + 1);
+    }
+    float m = kMInit, l = 0.f;
+    for (int j = it.t0; j < it.t1; ++j, ++n, ++sc) {
+      const int b = buf(n);
+      const uint32_t t_s = tmem + lanes + b * kKeys;
+      const float* sp = scales + sc % kScales * 3 * kKeys;
+      if constexpr (kTok)
+        if (!wait(sh->sc_full + sc % kScales, sc / kScales)) return;
+      if (!wait(sh->s_full + b, par(n))) return;
+      fence_after();
+      const int k0 = j * kKeys;
+      const bool hide = __any_sync(0xffffffffu, first > k0) || k0 + kKeys > it.end;
+      const float *kp = sp, *lp = sp + kKeys;
+      if (hide || sign != 1.f || fix) {
+        // some row does not see the whole tile: mask S where it stands
+#pragma unroll 1
+        for (int c = 0; c < kKeys; c += 32) {
+          uint32_t s[32];
+          tmem_ld32(t_s + c, s);
+          tmem_wait_ld<32>(s);
+          const int last = it.end - 1 - k0 - c, from = first - k0 - c;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            float x = __uint_as_float(s[e]) * sign;
+            if constexpr (kTok) x = fmaf(x * up, kp[c + e], lp[c + e]);
+            s[e] = e > last || e < from ? 0xff800000u : __float_as_uint(x);
+          }
+          tmem_st32(t_s + c, s);
+        }
+        tmem_wait_st();
+        kp = scales + kScales * 3 * kKeys;  // 1, and 0
+        lp = kp + kKeys;
+      }
+      uint32_t s[kKeys];
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 32) tmem_ld32(t_s + c, s + c);
+      tmem_wait_ld<kKeys>(s);
+      if constexpr (kTok) {
+#pragma unroll
+        for (int e = 0; e < kKeys; e += 4) {
+          const float4 k4 = *reinterpret_cast<const float4*>(kp + e);
+          const float4 l4 = *reinterpret_cast<const float4*>(lp + e);
+          float x0, x1;
+          unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pack2(k4.x, k4.y),
+                       pack2(l4.x, l4.y)), x0, x1);
+          s[e] = __float_as_uint(x0);
+          s[e + 1] = __float_as_uint(x1);
+          unpack2(fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), pack2(k4.z, k4.w),
+                       pack2(l4.z, l4.w)), x0, x1);
+          s[e + 2] = __float_as_uint(x0);
+          s[e + 3] = __float_as_uint(x1);
+        }
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
+#pragma unroll
+      for (int e = 4; e < kKeys - 4; e += 8)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          mx[c] = max3(mx[c], __uint_as_float(s[e + c]), __uint_as_float(s[e + 4 + c]));
+#pragma unroll
+      for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(s[kKeys - 4 + c]));
+      const float ms = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+      const bool move = ms > m + kTh;
+      if (__any_sync(0xffffffffu, move)) {
+        const float f = move ? ex2(m - ms) : 1.f;
+        if (move) m = ms;
+        l *= f;
+        if (j > it.t0) {  // O holds something: the MMA in front of this one must be done
+          if (!wait(sh->o_done + buf(n - 1), par(n - 1))) return;
+          fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tmem_ld16(t_o + c, o);
+            tmem_wait_ld<16>(o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st16(t_o + c, o);
+          }
+        }
+      }
+      // P over the columns of S, two keys a column
+      const uint64_t scale2 = pack2(scale, scale), m2 = pack2(-m, -m);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int k = c * 32 + e * 2;
+          const uint64_t sk = pack2(__uint_as_float(s[k]), __uint_as_float(s[k + 1]));
+          float p0, p1;
+          unpack2(kTok ? add2(sk, m2) : fma2(sk, scale2, m2), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          if constexpr (kTok) {
+            const float2 iv = *reinterpret_cast<const float2*>(sp + 2 * kKeys + k);
+            sum[e & 1] = fma2(pack2(p0, p1), pack2(iv.x, iv.y), sum[e & 1]);
+          } else {
+            sum[e & 1] = add2(sum[e & 1], pack2(p0, p1));
+          }
+          w[e] = k8 ? f16x2(p0, p1) : bf16x2(p0, p1);
+        }
+        tmem_st16(t_s + c * 16, w);
+        if (c == 1) {  // the first 64 keys: P V starts on them
+          tmem_wait_st();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(sh->p_half + b);
+        }
+      }
+      float l0, l1;
+      unpack2(add2(sum[0], sum[1]), l0, l1);
+      l += l0 + l1;
+      tmem_wait_st();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        bar_arrive(sh->p_full + b);
+        if constexpr (kTok) bar_arrive(sh->sc_empty + sc % kScales);
+      }
+    }
+    // the rows' partial outputs
+    if (!wait(sh->o_done + buf(n - 1), par(n - 1))) return;
+    fence_after();
+    const float inv = l > 0.f ? v_final / l : l;  // no key: 0; NaN stays
+    const int64_t at = it.cut ? static_cast<int64_t>(blockIdx.x) * C::kRows + g * kTile
+                              : (it.head * a.rows_cap + it.q0) * a.group + it.row0 + g * kTile;
+    float* part = (it.cut ? a.area_o : a.main_o) + at * D;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 16) {
+      uint32_t v[16];
+      __syncwarp();
+      tmem_ld16(t_o + c, v);
+      tmem_wait_ld<16>(v);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
+      // Four lanes exchange 16-byte pieces, so that a store writes 64 bytes of
+      // each of eight rows and not 16 of thirty-two.
+#pragma unroll
+      for (int d = 1; d <= 2; d <<= 1) {
+        const bool hi = (lane & d) != 0;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          if (p & d) continue;  // piece p and piece p + d
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t& keep = v[p * 4 + e];
+            uint32_t& give = v[(p + d) * 4 + e];
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? keep : give, d);
+            if (hi) keep = got;
+            else give = got;
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int rr = quad * 32 + (lane & ~3) + k;
+        if (rr < tile_rows)
+          *reinterpret_cast<uint4*>(part + static_cast<int64_t>(rr) * D + c + (lane & 3) * 4) =
+              make_uint4(v[k * 4], v[k * 4 + 1], v[k * 4 + 2], v[k * 4 + 3]);
+      }
+    }
+    __syncwarp();
+    fence_before();
+    if (lane == 0) bar_arrive(sh->o_free + g);
+    if (r < tile_rows) (it.cut ? a.area_x : a.main_x)[at + r] = l == 0.f ? -INFINITY : m + __log2f(l);
+  }
+}
+
+template <int D, bool k8, bool kI8, bool kTok>
+__global__ void __launch_bounds__(Cfg<D, k8, kTok>::kThreads, 1)
+    shared_prefix(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tk,
+                  const __grid_constant__ CUtensorMap tv) {
+  using C = Cfg<D, k8, kTok>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* q_s = smem;
+  uint8_t* ring = smem + C::kQBytes;
+  uint8_t* raw = ring + C::kRing * kUnit;
+  float* scales = reinterpret_cast<float*>(raw + C::kRaw * C::kRawBytes);
+  Shared* sh = reinterpret_cast<Shared*>(smem + C::kSmem - sizeof(Shared));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (su32(smem) % 1024u) {  // the swizzled tiles need it
+    if (tid == 0) atomicOr(a.status, PDA_STATUS_SMEM_MISALIGNED);
+    return;
+  }
+  if (tid == 0) {
+    for (int g = 0; g < 2; ++g) {
+      bar_init(sh->q_full + g, 4);
+      bar_init(sh->q_empty + g, 1);
+      bar_init(sh->s_full + g, 1);
+      bar_init(sh->p_half + g, 4);
+      bar_init(sh->p_full + g, 4);
+      bar_init(sh->o_done + g, 1);
+      bar_init(sh->o_free + g, 4);
+    }
+    for (int u = 0; u < C::kRing; ++u) {
+      bar_init(sh->full + u, k8 ? 4 : 1);
+      bar_init(sh->empty + u, 1);
+    }
+    for (int u = 0; u < C::kRaw; ++u) {
+      bar_init(sh->raw_full + u, 1);
+      bar_init(sh->raw_empty + u, 4);
+    }
+    for (int u = 0; u < kScales; ++u) {
+      bar_init(sh->sc_full + u, 4);
+      bar_init(sh->sc_empty + u, C::kSoft);
+    }
+    for (int u = 0; u < kItems; ++u) {
+      bar_init(sh->item_full + u, 1);
+      bar_init(sh->item_empty + u, C::kReaders);
+    }
+    bar_init(&sh->drain, 1);
+    sh->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (kTok && tid < kKeys) {
+    scales[kScales * 3 * kKeys + tid] = 1.f;
+    scales[kScales * 3 * kKeys + kKeys + tid] = 0.f;
+  }
+  if (warp == C::kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     su32(&sh->tmem)),
+                 "r"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh->tmem;
+  // registers a thread: 192 x 256 + 64 x 256 with two row tiles (128 x 512 at the
+  // launch), 216 x 128 + 104 x 256 with one (168 x 384)
+  if (warp < C::kSoft) {
+    if constexpr (C::kG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+  } else {
+    if constexpr (C::kG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  }
+  if (warp < C::kSoft) {
+    softmax_role<C, D, k8, kTok>(a, sh, q_s, scales, tmem, warp);
+  } else if (warp == C::kMmaWarp) {
+    if (elect_one()) mma_role<C, D, k8>(a, sh, q_s, ring);
+  } else if (warp == C::kWorkWarp) {
+    work_role<C::kRows>(a, sh);
+  } else if (k8 && warp >= C::kConv0) {
+    if constexpr (k8) widen_role<C, D, kI8, kTok>(a, sh, ring, raw, scales);
+  } else {
+    load_role<C, D, k8>(a, sh, ring, raw, &tk, &tv, warp - C::kProd0);
+  }
+  __syncwarp();
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == C::kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
+                 : "memory");
+}
+
+// -------------------------------------------------------------------- join
+//
+// One warp per (request, row, head): the prefix's segments in order, then the own
+// chunks. Bound: reading the partials (L2).
+template <int D>
+__global__ void __launch_bounds__(256) shared_join(const __grid_constant__ SharedArgs a,
+                                                   const __grid_constant__ DecodeArgs o) {
+  constexpr int kRows = D <= 128 ? 2 * kTile : kTile;
+  constexpr int kV = D / 32;  // channels of a lane
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t per_b = static_cast<int64_t>(o.max_q_len) * a.hq;
+  const int b = static_cast<int>(item / per_b);
+  if (b >= a.batch) return;
+  const int i = static_cast<int>(item % per_b) / a.hq, head = static_cast<int>(item % a.hq);
+  const int q0 = __ldg(a.qo_indptr + b), R = __ldg(a.qo_indptr + b + 1) - q0;
+  const int L = __ldg(a.own_len + b), W = a.window ? __ldg(a.window + b) : 0;
+  if (i >= R || R > o.max_q_len || L < R || L > o.max_kv_len || q0 < 0 || q0 + R > a.rows_cap) return;
+  int g = 0, top = a.groups - 1;  // the last group that starts at or before the request
+  while (g < top) {
+    const int mid = (g + top + 1) >> 1;
+    if (__ldg(a.group_indptr + mid) <= b) g = mid;
+    else top = mid - 1;
+  }
+  const Group gr = group_of(a, g);
+  const int own = split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
+  const int h = head / a.group;
+  const int64_t m = static_cast<int64_t>(q0 + i - gr.q0) * a.group + head % a.group;  // packed row
+  const int block = static_cast<int>(m / kRows), r = static_cast<int>(m % kRows);
+  int64_t c0 = 0;  // CTA of the item's first segment
+  int segs = 0;
+  if (gr.tiles > 0) {
+    const int64_t per = a.first[0];
+    const int64_t u = a.first[1 + g] + (static_cast<int64_t>(h) * blocks_of<kRows>(a, gr) + block) * gr.tiles;
+    c0 = u / per;
+    segs = static_cast<int>((u + gr.tiles - 1) / per - c0) + 1;
+  }
+  const int64_t head_row = (h * a.rows_cap + gr.q0) * a.group + m;  // in main
+  const int64_t own_row = static_cast<int64_t>(q0 + i) * a.hq + head, own_step = o.rows_cap * a.hq;
+  const int parts = segs + own;
+  auto place = [&](int s, const float*& x, const float*& v) {
+    if (s >= segs) {
+      const int64_t at = (s - segs) * own_step + own_row;
+      x = o.part_lse + at;
+      v = o.part_o + at * D;
+    } else if (s == 0) {
+      x = a.main_x + head_row;
+      v = a.main_o + head_row * D;
+    } else {
+      const int64_t at = (c0 + s) * kRows + r;
+      x = a.area_x + at;
+      v = a.area_o + at * D;
+    }
+  };
+  constexpr int kBatch = 8;
+  float M = -INFINITY, sum = 0.f, acc[kV];
+#pragma unroll
+  for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+  for (int s0 = 0; s0 < parts; s0 += kBatch) {
+    float x[kBatch], v[kBatch][kV];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      x[k] = -INFINITY;
+      if (s0 + k < parts) {
+        const float *px, *pv;
+        place(s0 + k, px, pv);
+        x[k] = *px;
+#pragma unroll
+        for (int e = 0; e < kV; e += 2) {
+          const float2 t = *reinterpret_cast<const float2*>(pv + lane * kV + e);
+          v[k][e] = t.x;
+          v[k][e + 1] = t.y;
+        }
+      }
+    }
+    float top_x = M;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) top_x = fmaxf(top_x, x[k]);
+    if (top_x > M) {
+      const float f = exp2f(M - top_x);  // M = -inf: nothing summed yet
+      sum *= f;
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] *= f;
+      M = top_x;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (s0 + k >= parts) break;
+      const float w = x[k] == -INFINITY ? 0.f : exp2f(x[k] - M);
+      sum += w;
+      // a part without a visible key counts for nothing, whatever it holds
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc[e] = w != 0.f ? fmaf(w, v[k][e], acc[e]) : acc[e];
+    }
+  }
+  const float inv = sum > 0.f ? 1.f / sum : sum;  // (NaN stays)
+  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.out) + own_row * D + lane * kV;
+#pragma unroll
+  for (int e = 0; e < kV; e += 2)
+    *reinterpret_cast<uint32_t*>(dst + e) = bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && o.lse) o.lse[own_row] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------- the prefixes themselves
+//
+// Mathematics: the whole pages in front of a group's rows whose ids are those of its
+// first request: n = min over requests of the equal leading ids, at most (L - R) / P.
+//
+// Bound: latency. A cluster of CTAs per group, a warp per request; a warp stops where
+// another has found a shorter prefix.
+constexpr int kShareThreads = 256;
+constexpr int kShareWarps = kShareThreads / 32;
+
+struct TablesArgs {
+  pda_shared_tables t;
+  int32_t* status;
+  int batch, groups, page_size, max_q_len, max_kv_len, num_pages;
+};
+
+__global__ void __launch_bounds__(kShareThreads) share_tables(const __grid_constant__ TablesArgs a) {
+  __shared__ int sh_pages, sh_low;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t ctas, rank;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  rank = cluster_rank();
+  const int g = blockIdx.x / ctas;
+  if (threadIdx.x == 0) sh_pages = sh_low = INT_MAX;
+  cluster_sync();
+  const int b0 = a.t.group_indptr ? __ldg(a.t.group_indptr + g) : 0;
+  int b1 = a.t.group_indptr ? __ldg(a.t.group_indptr + g + 1) : a.batch;
+  uint32_t bits = 0u;
+  const bool valid = b0 >= 0 && b1 >= b0 && b1 <= a.batch;
+  if (!valid) {
+    bits = PDA_STATUS_TABLE_INVALID;
+    b1 = b0;
+  }
+  // a request that takes part: its rows and length, else its status bits
+  auto fits = [&](int b, int& rows, int& len) -> bool {
+    const int64_t r = static_cast<int64_t>(__ldg(a.t.qo_indptr + b + 1)) - __ldg(a.t.qo_indptr + b);
+    len = __ldg(a.t.kv_len + b);
+    rows = static_cast<int>(r);
+    if (r == 0) return false;
+    uint32_t bad = 0u;
+    if (r < 0 || r > a.max_q_len) bad |= PDA_STATUS_ROWS_GT_MAX;
+    if (len < r) bad |= PDA_STATUS_KV_LEN_LT_ROWS;
+    if (len > a.max_kv_len) bad |= PDA_STATUS_KV_LEN_GT_MAX;
+    bits |= bad;
+    return !bad;
+  };
+  int lead = -1;  // the first one
+  for (int c = b0; c < b1 && lead < 0; c += 32) {
+    int rows, len;
+    const uint32_t has = __ballot_sync(0xffffffffu, c + lane < b1 && fits(c + lane, rows, len));
+    if (has) lead = c + __ffs(has) - 1;
+  }
+  int* best = &sh_pages;  // the leader's words are the cluster's
+  const uint32_t pages_at = on_leader(best), low_at = on_leader(&sh_low);
+  auto least = [](uint32_t at, int v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+  };
+  if (lead >= 0) {
+    const int32_t* theirs = a.t.page_table + __ldg(a.t.kv_indptr + lead);
+    const int most = __ldg(a.t.kv_indptr + lead + 1) - __ldg(a.t.kv_indptr + lead);
+    for (int b = b0 + static_cast<int>(rank) * kShareWarps + warp; b < b1;
+         b += static_cast<int>(ctas) * kShareWarps) {
+      int rows, len;
+      if (!fits(b, rows, len)) continue;
+      const int at = __ldg(a.t.kv_indptr + b);
+      const int32_t* mine = a.t.page_table + at;
+      int n = min(min((len - rows) / a.page_size, most), __ldg(a.t.kv_indptr + b + 1) - at);
+      n = min(max(n, 0), static_cast<int>(cluster_load(pages_at)));
+      int equal = n;
+      for (int j = 0; j < n; j += 128) {
+        bool ok[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int e = j + k * 32 + lane;
+          ok[k] = true;
+          if (e < n) {
+            const int id = __ldg(mine + e);
+            ok[k] = id == __ldg(theirs + e) && id >= 0 && id < a.num_pages;
+          }
+        }
+        int stop = -1;
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          const uint32_t differ = __ballot_sync(0xffffffffu, !ok[k]);
+          if (differ) stop = j + k * 32 + __ffs(differ) - 1;
+        }
+        if (stop >= 0) {
+          equal = stop;
+          break;
+        }
+      }
+      if (lane == 0) {
+        const int w = a.t.window ? __ldg(a.t.window + b) : 0;
+        least(pages_at, equal);
+        least(low_at, w > 0 ? static_cast<int>(max(static_cast<int64_t>(0),
+                                                   static_cast<int64_t>(len) - rows - w + 1))
+                            : 0);
+      }
+    }
+  }
+  cluster_sync();
+  int pages = lead >= 0 ? static_cast<int>(cluster_load(pages_at)) : 0;
+  int low = lead >= 0 ? static_cast<int>(cluster_load(low_at)) : 0;
+  cluster_sync();  // (the leader's words are read)
+  const int end = pages * a.page_size;
+  if (rank == 0) {
+    if (threadIdx.x == 0 && valid) {
+      a.t.prefix[2 * g] = min(low / a.page_size * a.page_size, end);
+      a.t.prefix[2 * g + 1] = end;
+    }
+    for (int b = b0 + static_cast<int>(threadIdx.x); b < b1; b += kShareThreads) {
+      int rows, len;
+      const bool ok = fits(b, rows, len);
+      a.t.own_indptr[b] = __ldg(a.t.kv_indptr + b) + pages;
+      a.t.own_len[b] = rows == 0 ? 0 : ok ? len - end : -1;
+    }
+    if (bits) atomicOr(a.status, static_cast<int>(bits));
+  }
+}
+
+// ---------------------------------------------------------------- dispatch
+using PrefixFn = void (*)(SharedArgs, CUtensorMap, CUtensorMap);
+struct Kernel {
+  PrefixFn fn;
+  int smem, threads, v_keys;
+};
+template <int D, bool k8, bool kI8, bool kTok>
+Kernel kernel_of() {
+  using C = Cfg<D, k8, kTok>;
+  return {shared_prefix<D, k8, kI8, kTok>, C::kSmem, C::kThreads, k8 ? C::kRawKeys : C::kVKeys};
+}
+template <int D>
+Kernel kernel_for(const pda_plan_t& p) {
+  const bool tok = p.scale_mode == PDA_SCALE_TOKEN_HEAD;
+  if (p.kv_dtype == PDA_BF16) return kernel_of<D, false, false, false>();
+  if (p.kv_dtype == PDA_INT8) return tok ? kernel_of<D, true, true, true>() : kernel_of<D, true, true, false>();
+  return tok ? kernel_of<D, true, false, true>() : kernel_of<D, true, false, false>();
+}
+Kernel kernel_for(const pda_plan_t& p) {
+  return p.head_dim == 64 ? kernel_for<64>(p) : p.head_dim == 128 ? kernel_for<128>(p) : kernel_for<256>(p);
+}
+
+// Tensor map of the cache, (channel, slot, kv head, page): boxes of `rows` tokens x 64
+// bf16 channels (swizzled), or x a head's codes (as they lie).
+bool page_map(CUtensorMap* m, const void* base, const pda_plan_t& p, int rows) {
+  EncodeFn enc = encoder();
+  if (!enc) return false;
+  const bool wide = p.kv_dtype == PDA_BF16;
+  const int64_t eb = wide ? 2 : 1;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim), static_cast<cuuint64_t>(p.page_size),
+                              static_cast<cuuint64_t>(p.num_kv_heads), static_cast<cuuint64_t>(p.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.kv_stride_token * eb),
+                                 static_cast<cuuint64_t>(p.kv_stride_head * eb),
+                                 static_cast<cuuint64_t>(p.kv_stride_page * eb)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(wide ? 64 : p.head_dim),
+                             static_cast<cuuint32_t>(std::min(p.page_size, rows)), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, wide ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
+             const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int64_t up256(int64_t n) { return (n + 255) / 256 * 256; }
+
+bool a4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
+int check_plan(const pda_shared_plan_t* sp) {
+  if (!sp) return PDA_ERR_NULL;
+  if (sp->magic != PDA_SHARED_MAGIC || sp->struct_bytes != sizeof(pda_shared_plan_t) ||
+      sp->own.magic != PDA_PLAN_MAGIC)
+    return PDA_ERR_PLAN;
+  return PDA_OK;
+}
+
+int check_tables(const pda_shared_plan_t* sp, const pda_shared_tables* t) {
+  if (!t->page_table || !t->kv_indptr || !t->kv_len || !t->qo_indptr || !t->prefix || !t->own_indptr ||
+      !t->own_len)
+    return PDA_ERR_NULL;
+  if (!t->group_indptr && sp->groups != 1) return PDA_ERR_NULL;
+  if (t->own_len == t->kv_len || t->own_indptr == t->kv_indptr) return PDA_ERR_INVALID;
+  if (!a4(t->page_table) || !a4(t->kv_indptr) || !a4(t->kv_len) || !a4(t->qo_indptr) || !a4(t->window) ||
+      !a4(t->group_indptr) || !a4(t->prefix) || !a4(t->own_indptr) || !a4(t->own_len))
+    return PDA_ERR_ALIGNMENT;
+  return PDA_OK;
+}
+
+}  // namespace
+}  // namespace pda
+
+extern "C" int pda_shared_plan(const pda_plan_t* plan, int32_t groups, int32_t max_own_len,
+                               pda_shared_plan_t* out_plan, size_t* scratch_bytes) {
+  using namespace pda;
+  if (!plan || !out_plan) return PDA_ERR_NULL;
+  if (plan->magic != PDA_PLAN_MAGIC) return PDA_ERR_PLAN;
+  if ((plan->head_dim != 64 && plan->head_dim != 128 && plan->head_dim != 256) || plan->page_size < 8)
+    return PDA_ERR_UNSUPPORTED;
+  if (groups < 1 || groups > kMaxGroups || max_own_len < 0) return PDA_ERR_INVALID;
+  if (max_own_len == 0 || max_own_len > plan->max_kv_len) max_own_len = plan->max_kv_len;
+  pda_params p;
+  std::memset(&p, 0, sizeof p);
+  p.num_qo_heads = plan->num_qo_heads;
+  p.num_kv_heads = plan->num_kv_heads;
+  p.head_dim = plan->head_dim;
+  p.page_size = plan->page_size;
+  p.q_dtype = plan->q_dtype;
+  p.kv_dtype = plan->kv_dtype;
+  p.scale_mode = plan->scale_mode;
+  p.max_batch = plan->max_batch;
+  p.max_q_len = plan->max_q_len;
+  p.max_kv_len = max_own_len;
+  p.num_pages = plan->num_pages;
+  p.kv_stride_page = plan->kv_stride_page;
+  p.kv_stride_token = plan->kv_stride_token;
+  p.kv_stride_head = plan->kv_stride_head;
+  p.device = plan->device;
+  p.num_sms = plan->num_sms;
+  p.batch = plan->batch;
+  p.kernel = plan->kernel;
+  p.wait_limit_us = plan->wait_limit_us;
+  p.inject = plan->inject;
+  pda_shared_plan_t sp;
+  std::memset(&sp, 0, sizeof sp);
+  const int rc = pda_plan(&p, &sp.own, nullptr);
+  if (rc != PDA_OK) return rc;
+  sp.magic = PDA_SHARED_MAGIC;
+  sp.struct_bytes = sizeof sp;
+  sp.groups = groups;
+  sp.max_kv_len = plan->max_kv_len;
+  const int64_t d = plan->head_dim, rows = d <= 128 ? 2 * kTile : kTile;
+  const int64_t cells = sp.own.rows_cap * plan->num_qo_heads;
+  const int64_t area = static_cast<int64_t>(plan->num_sms) * rows;
+  int64_t at = kStatusHeaderBytes;
+  auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += up256(bytes);
+    return here;
+  };
+  sp.own.scratch_lse_offset = take(sp.own.max_splits * cells * 4);
+  sp.own.scratch_o_offset = take(sp.own.max_splits * cells * d * 4);
+  sp.first_offset = take((1 + static_cast<int64_t>(groups)) * 8);
+  sp.main_lse_offset = take(cells * 4);
+  sp.main_o_offset = take(cells * d * 4);
+  sp.area_lse_offset = take(area * 4);
+  sp.area_o_offset = take(area * d * 4);
+  sp.own.scratch_bytes = sp.scratch_bytes = at;
+  *out_plan = sp;
+  if (scratch_bytes) *scratch_bytes = static_cast<size_t>(at);
+  return PDA_OK;
+}
+
+extern "C" int pda_share_tables(const pda_shared_plan_t* sp, const pda_shared_tables* tables, void* scratch,
+                                pda_stream_t stream) {
+  using namespace pda;
+  int rc = check_plan(sp);
+  if (rc != PDA_OK) return rc;
+  if (!tables) return PDA_ERR_NULL;
+  if ((rc = check_tables(sp, tables)) != PDA_OK) return rc;
+  if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256) return PDA_ERR_SCRATCH;
+  if (!on_device(sp->own.device)) return PDA_ERR_INVALID;
+  TablesArgs a = {};
+  a.t = *tables;
+  a.status = static_cast<int32_t*>(scratch);
+  a.batch = sp->own.batch;
+  a.groups = sp->groups;
+  a.page_size = sp->own.page_size;
+  a.max_q_len = sp->own.max_q_len;
+  a.max_kv_len = sp->max_kv_len;
+  a.num_pages = sp->own.num_pages;
+  // eight CTAs a group, where a group's requests have a warp each for it
+  const unsigned ctas = static_cast<int64_t>(sp->groups) * kShareWarps < sp->own.batch ? 8 : 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(sp->groups) * ctas);
+  cfg.blockDim = dim3(kShareThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, share_tables, a) != cudaSuccess) {
+    cudaGetLastError();
+    return PDA_ERR_CUDA;
+  }
+  return PDA_OK;
+}
+
+extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, const void* k_pages,
+                                 const void* v_pages, const pda_shared_tables* tables, int32_t max_q_len,
+                                 float sm_scale, const float* k_scale, const float* v_scale, void* out,
+                                 float* lse, void* scratch, pda_stream_t stream) {
+  using namespace pda;
+  int rc = check_plan(sp);
+  if (rc != PDA_OK) return rc;
+  if (!tables) return PDA_ERR_NULL;
+  const pda_shared_tables& t = *tables;
+  if ((rc = check_tables(sp, tables)) != PDA_OK) return rc;
+  if (!scratch || reinterpret_cast<uintptr_t>(scratch) % 256) return PDA_ERR_SCRATCH;
+  const pda_plan_t* plan = &sp->own;
+  rc = check_decode_args(plan, q, k_pages, v_pages, t.page_table, t.own_indptr, t.own_len, t.qo_indptr,
+                         max_q_len, k_scale, v_scale, out, lse);
+  if (rc != PDA_OK) return rc;
+  if (!on_device(plan->device)) return PDA_ERR_INVALID;
+  DecodeArgs o = decode_args(plan, q, k_pages, v_pages, t.page_table, t.own_indptr, t.own_len,
+                             t.qo_indptr, max_q_len, t.window, sm_scale, k_scale, v_scale, out, lse, scratch);
+  o.final_splits = 0;
+  SharedArgs a = {};
+  char* base = static_cast<char*>(scratch);
+  a.q = q;
+  a.page_table = t.page_table;
+  a.qo_indptr = t.qo_indptr;
+  a.kv_len = t.kv_len;
+  a.window = t.window;
+  a.group_indptr = t.group_indptr;
+  a.prefix = t.prefix;
+  a.own_indptr = t.own_indptr;
+  a.own_len = t.own_len;
+  a.k_scale = o.k_scale;
+  a.v_scale = o.v_scale;
+  a.main_x = reinterpret_cast<float*>(base + sp->main_lse_offset);
+  a.main_o = reinterpret_cast<float*>(base + sp->main_o_offset);
+  a.area_x = reinterpret_cast<float*>(base + sp->area_lse_offset);
+  a.area_o = reinterpret_cast<float*>(base + sp->area_o_offset);
+  a.first = reinterpret_cast<int64_t*>(base + sp->first_offset);
+  a.status = o.status;
+  a.wait_limit_ns = o.wait_limit_ns;
+  a.sm_scale = sm_scale;
+  a.batch = o.batch;
+  a.groups = sp->groups;
+  a.hq = o.hq;
+  a.hkv = o.hkv;
+  a.group = o.group;
+  a.page_size = o.page_size;
+  a.num_pages = o.num_pages;
+  a.max_q_len = max_q_len;
+  a.rows_cap = o.rows_cap;
+  a.q8 = plan->q_dtype == PDA_E4M3;
+  a.inject = o.inject;
+  const Kernel k = kernel_for(*plan);
+  CUtensorMap tk, tv;
+  if (!page_map(&tk, k_pages, *plan, plan->kv_dtype == PDA_BF16 ? kKeys : k.v_keys) ||
+      !page_map(&tv, v_pages, *plan, k.v_keys))
+    return PDA_ERR_CUDA;
+  if (cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           k.smem) != cudaSuccess) {
+    cudaGetLastError();
+    return PDA_ERR_CUDA;
+  }
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  k.fn<<<static_cast<unsigned>(plan->num_sms), k.threads, k.smem, s>>>(a, tk, tv);
+  if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
+  rc = plan->kernel == PDA_KERNEL_TC ? launch_stage1_tc(plan, o, s) : launch_stage1_mma(plan, o, s);
+  if (rc != PDA_OK) return rc;
+  const int64_t warps = static_cast<int64_t>(a.batch) * max_q_len * a.hq;
+  const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
+  switch (plan->head_dim) {
+    case 64: shared_join<64><<<grid, 256, 0, s>>>(a, o); break;
+    case 128: shared_join<128><<<grid, 256, 0, s>>>(a, o); break;
+    default: shared_join<256><<<grid, 256, 0, s>>>(a, o); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+}

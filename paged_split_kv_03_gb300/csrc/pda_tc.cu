@@ -1692,7 +1692,7 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
     x.t_begin = t_begin;
     x.t_end = t_end;
     x.ntiles = ntiles;
-    x.single = sr.num_splits == 1;
+    x.single = sr.num_splits == a.final_splits;
     if constexpr (C::kMix) {
       softmax_rec<C>(a, x, warp, lane, tid);
     } else if constexpr (NMAX <= 16) {
