@@ -13,11 +13,15 @@
 // weights stay <= 2^8 and are exact in l and O), O += P V. P is rounded to the
 // operands' 16-bit type, l sums the unrounded weights in fp32.
 //
-// Types: bf16 caches run bf16 MMAs. E4M3 and int8 codes are widened exactly to f16 and
-// run f16 MMAs with an f16 query: an E4M3 query is exact in it, a bf16 row too, once
-// its power of two is taken out (below 2^-14 of it rounded at 2^-25). Scales per
-// tensor meet the logits and the output; scales per token and head meet S and P in
-// fp32, the value scale as its log2, so that P <= 2^8 whatever the scale.
+// Types: bf16 caches run bf16 MMAs. E4M3 keys (head_dim 128 and 256) are operands as
+// they are: an E4M3 query meets them directly, a bf16 row as the sum of two E4M3 terms
+// of it times a power of two that takes its largest element to [224, 448): exact for
+// elements from 2^-11 of that on, rounded at 2^-19 of it below. Values, and int8 keys
+// and those of head_dim 64, are widened exactly to f16 and meet an f16 P (query). P in
+// E4M3 terms would need no widening but four conversions for each pair of weights, 2048
+// cycles a tile of 128 x 128 against the 1024 of its MMAs. Scales per tensor meet the
+// logits and the output; scales per token and head meet S and P in fp32, the value
+// scale as its log2, so that P <= 2^8 whatever the scale.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -133,9 +137,9 @@ struct Item {
 };
 
 struct Shared {
-  uint64_t q_full[2], q_empty[2], full[16], empty[16], raw_full[4], raw_empty[4], sc_full[kScales],
-      sc_empty[kScales], s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], item_full[kItems],
-      item_empty[kItems], drain;
+  uint64_t q_full[2], q_empty[2], k_full[8], k_empty[8], v_full[8], v_empty[8], raw_full[4], raw_empty[4],
+      sc_full[kScales], sc_empty[kScales], s_full[2], p_half[2], p_full[2], o_done[2], o_free[2],
+      item_full[kItems], item_empty[kItems], drain;
   uint32_t tmem;
   int abort_flag;
   Item items[kItems];
@@ -143,31 +147,44 @@ struct Shared {
 };
 
 // ------------------------------------------------------------ configuration
-template <int D, bool k8, bool kTok>
+template <int D, bool k8, bool kI8, bool kTok>
 struct Cfg {
   static constexpr int kG = D <= 128 ? 2 : 1;  // row tiles of an item
   static constexpr int kRows = kG * kTile;
-  static constexpr int kU = D / 64;            // ring units of a K tile, and of a V tile
-  static constexpr int kVKeys = 8192 / D;      // keys of a V unit
-  static constexpr int kQBytes = kG * kU * kUnit;
-  // 8-bit caches: codes land in raw slots of kRawKeys keys, as they lie in the cache
+  static constexpr bool kDirect = k8 && !kI8 && D >= 128;  // E4M3 keys as they are
+  static constexpr int kQTerms = kDirect ? 2 : 1;
+  // 16 KB units of a K tile (128 keys x 128 bytes) and of a V tile (kVKeys keys x D)
+  static constexpr int kUK = kDirect ? D / 128 : D / 64;
+  static constexpr int kUV = D / 64;
+  static constexpr int kVKeys = 8192 / D;
+  static constexpr int kQTile = kQTerms * kUK * kUnit;  // bytes of a row tile's query
+  static constexpr int kQBytes = kG * kQTile;
+  // rings of K and of V units
+  static constexpr int kRK = D == 64 ? 4 : !k8 ? 5 : D == 256 && !kTok ? 4 : 3;
+  static constexpr int kRV = D == 64 ? 4 : !k8 ? 5 : kDirect || D == 256 ? 4 : 3;
+  // 8-bit caches: codes to widen land in raw slots of kRawKeys keys, as they lie in the cache
   static constexpr int kRawKeys = D <= 128 ? 128 : 64;
   static constexpr int kRawBytes = kRawKeys * D;
   static constexpr int kRawTile = kKeys / kRawKeys;  // slots of a K or V tile
-  static constexpr int kRaw = !k8 ? 0 : D == 64 ? 4 : D == 128 ? (kTok ? 3 : 4) : kTok ? 3 : 2;
-  static constexpr int kRing = !k8 ? (D == 64 ? 8 : 10) : D == 64 ? 8 : D == 128 || kTok ? 6 : 8;
+  static constexpr int kRaw = !k8 ? 0 : D == 64 ? 4 : D == 128 && !(kDirect && kTok) ? 3 : 2;
   static constexpr int kScaleBytes = kTok ? (kScales * 3 + 2) * kKeys * 4 : 0;
-  static constexpr int kSmem = kQBytes + kRing * kUnit + kRaw * kRawBytes + kScaleBytes +
+  static constexpr int kRings = (kRK + kRV) * kUnit;
+  static constexpr int kSmem = kQBytes + kRings + kRaw * kRawBytes + kScaleBytes +
                                static_cast<int>(sizeof(Shared));
   static constexpr int kSoft = 4 * kG;              // softmax warps, a thread per row
   static constexpr int kMmaWarp = kSoft, kWorkWarp = kSoft + 1, kProd0 = kSoft + 2;
-  // warps that issue loads, and warps that widen codes: the last four are either
+  // warps that issue loads (two, or with nothing to widen six: even ones K, odd ones V),
+  // and warps that widen codes
   static constexpr int kProds = k8 ? 2 : 6;
-  static constexpr int kConv0 = kSoft + 4;
-  static constexpr int kThreads = 32 * (kSoft + 8);
-  static constexpr int kReaders = kSoft + 1 + kProds + (k8 ? 4 : 0);  // arrivals that free an item
+  static constexpr int kConv0 = kSoft + 4, kConv = !k8 ? 0 : kG == 1 ? 8 : 4;
+  static constexpr int kWarps = kSoft + 4 + (k8 ? kConv : 4);
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kReaders = kSoft + 1 + kProds + kConv;  // arrivals that free an item
   static_assert(kSmem <= 227 * 1024 && kSmem > 114 * 1024, "one CTA an SM");
-  static_assert(kRing <= 16 && kRaw <= 4, "barriers");
+  static_assert(kRK <= 8 && kRV <= 8 && kRaw <= 4, "barriers");
+  // two row tiles hold V_j and K_{j+1} whole; a K tile is widened from all its raw slots
+  static_assert(kG == 1 || (kRK >= kUK && kRV >= kUV), "a tile fits");
+  static_assert(!k8 || kRaw >= kRawTile, "a raw tile fits");
 };
 
 struct ItemReader {
@@ -206,11 +223,11 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// The order in which the K and V tiles of a segment of n pass through the ring, which
-// is the MMAs': with two row tiles K0 V0 K1 V1 ..., with two S of one row tile
-// K0 K1 V0 K2 V1 ... . Place i of 2n -> (V?, tile).
+// The order in which the K and V tiles of a segment of n are needed: with two row tiles
+// K0 V0 K1 V1 ..., with two S of one row tile K0 K1 V0 K2 V1 ... . Place i of 2n ->
+// (V?, tile).
 template <int kG>
-__device__ __forceinline__ void ring_order(int i, int n, int& v, int& j) {
+__device__ __forceinline__ void tile_order(int i, int n, int& v, int& j) {
   if constexpr (kG == 2) {
     v = i & 1;
     j = i >> 1;
@@ -223,116 +240,134 @@ __device__ __forceinline__ void ring_order(int i, int n, int& v, int& j) {
 
 // ------------------------------------------------------------------- loads
 //
-// A unit is one warp's, warps in turn; its boxes (a page's tokens x 128 bytes) are
-// its lanes'. A page behind the prefix is one past the cache: such a box reads as zeros.
+// Even warps load K, odd ones V, a unit (or raw slot) a warp in turn; its boxes (a page's
+// tokens x 128 bytes, or a head's codes) are its lanes'. A page behind the prefix is one
+// past the cache: such a box reads as zeros.
 template <class C, int D, bool k8>
-__device__ __forceinline__ void load_role(const SharedArgs& a, Shared* sh, uint8_t* ring, uint8_t* raw,
+__device__ __forceinline__ void load_role(const SharedArgs& a, Shared* sh, uint8_t* rings, uint8_t* raw,
                                           const CUtensorMap* tk, const CUtensorMap* tv, int pw) {
   volatile int* abort_flag = &sh->abort_flag;
   const int lane = threadIdx.x & 31;
+  const int v = pw & 1;
+  const uint32_t turn = static_cast<uint32_t>(pw >> 1);
+  constexpr uint32_t kTurns = C::kProds / 2;
   ItemReader reader(sh);
   Item it{};
-  uint32_t x = 0;  // units (raw slots) so far, of all warps
   bool alive = (a.inject & PDA_INJECT_WITHHOLD_KV) == 0u;
-  constexpr int kPer = k8 ? C::kRawTile : C::kU;  // units of a tile
-  constexpr uint32_t kSlots = k8 ? (C::kRaw ? C::kRaw : 1) : C::kRing;
-  uint64_t* full = k8 ? sh->raw_full : sh->full;
-  uint64_t* empty = k8 ? sh->raw_empty : sh->empty;
-  const uint32_t base = su32(k8 ? raw : ring);
-  const uint32_t slot_bytes = k8 ? C::kRawBytes : kUnit;
+  // where this warp's tiles go: a ring, or raw slots (in the order of all tiles)
+  const bool to_raw = k8 && (v || !C::kDirect);
+  const uint32_t slots = to_raw ? (C::kRaw ? C::kRaw : 1) : v ? C::kRV : C::kRK;
+  uint64_t* full = to_raw ? sh->raw_full : v ? sh->v_full : sh->k_full;
+  uint64_t* empty = to_raw ? sh->raw_empty : v ? sh->v_empty : sh->k_empty;
+  const uint32_t base = su32(to_raw ? raw : rings + (v ? C::kRK * kUnit : 0));
+  const uint32_t slot_bytes = to_raw ? C::kRawBytes : kUnit;
+  const int units = to_raw ? C::kRawTile : v ? C::kUV : C::kUK;
+  const int unit_keys = to_raw ? C::kRawKeys : v ? C::kVKeys : kKeys;
   const int P = a.page_size;
+  const int rows = min(P, unit_keys), boxes = unit_keys / rows;  // powers of two
+  const int atoms = !k8 && v ? C::kUV : 1;
+  const int at = lane % boxes, atom = lane / boxes;
+  const uint32_t box = atom * (unit_keys * 128) + at * rows * (to_raw ? D : 128);
+  const CUtensorMap* map = v ? tv : tk;
+  uint32_t x = 0, issued = 0u, parity = 0u;  // units so far; slots this warp loaded last, and when
   while (alive && reader.next_warp(it, a)) {
     const int n = it.t1 - it.t0;
     for (int i = 0; i < 2 * n && alive; ++i) {
-      int v, j;
-      ring_order<C::kG>(i, n, v, j);
+      int tv_, j;
+      tile_order<C::kG>(i, n, tv_, j);
+      if (tv_ != v) {
+        // raw slots are shared with the other side's tiles, unless those are not widened
+        if (to_raw && !C::kDirect)
+          for (int c = 0; c < C::kRawTile; ++c, ++x) issued &= ~(1u << x % slots);
+        continue;
+      }
       const int key0 = (it.t0 + j) * kKeys;
-      for (int c = 0; c < kPer; ++c, ++x) {
-        if (x % C::kProds != static_cast<uint32_t>(pw)) continue;
-        // this lane's box: `rows` keys from `key` on, channels from `chan` on
-        const int unit_keys = k8 ? C::kRawKeys : v ? C::kVKeys : kKeys;
-        const int rows = min(P, unit_keys), boxes = unit_keys / rows;
-        const int atoms = !k8 && v ? C::kU : 1;
-        const int at = lane % boxes, atom = lane / boxes;
-        const int key = key0 + (k8 || v ? c * unit_keys : 0) + at * rows;
-        const int chan = k8 ? 0 : (v ? atom : c) * 64;
+      for (int c = 0; c < units; ++c, ++x) {
+        if (!to_raw && x % kTurns != turn) {
+          issued &= ~(1u << x % slots);
+          continue;
+        }
+        const int key = key0 + (to_raw || v ? c * unit_keys : 0) + at * rows;
+        const int chan = to_raw ? 0 : k8 ? c * 128 : (v ? atom : c) * 64;
         const bool mine = atom < atoms;
         int page = a.num_pages;
         if (mine && key < it.end) {
           page = __ldg(a.page_table + it.table + key / P);
           if (page < 0 || page > a.num_pages) page = a.num_pages;
         }
-        const uint32_t slot = x % kSlots;
+        const uint32_t slot = x % slots;
         int good = 1;
         if (lane == 0) {
-          good = bar_wait(empty + slot, ((x / kSlots) & 1u) ^ 1u, abort_flag, a);
+          good = bar_wait(empty + slot, ((x / slots) & 1u) ^ 1u, abort_flag, a);
           if (good) bar_expect_tx(full + slot, slot_bytes);
         }
         if (!__shfl_sync(0xffffffffu, good, 0)) {
           alive = false;
           break;
         }
-        if (mine) {
-          const uint32_t row_bytes = k8 ? D : 128;
-          const uint32_t dst = base + slot * slot_bytes + atom * (unit_keys * 128) + at * rows * row_bytes;
-          tma_page(dst, v ? tv : tk, chan, key % P, it.head, page, full + slot);
-        }
+        if (mine) tma_page(base + slot * slot_bytes + box, map, chan, key % P, it.head, page, full + slot);
+        issued |= 1u << slot;
+        parity = (parity & ~(1u << slot)) | (x / slots & 1u) << slot;
       }
     }
   }
-  // every box issued must have landed before the CTA can exit
+  // Every box issued must have landed before the CTA can exit: the last unit of each slot
+  // where it is this warp's (the one in front of another warp's has been read).
   if (lane == 0)
-    for (uint32_t k = x > kSlots ? x - kSlots : 0u; k < x; ++k)
-      if (k % C::kProds == static_cast<uint32_t>(pw)) bar_drain(full + k % kSlots, (k / kSlots) & 1u);
+    for (uint32_t k = 0; k < slots; ++k)
+      if (issued >> k & 1u) bar_drain(full + k, parity >> k & 1u);
 }
 
 // -------------------------------------------------------------------- MMAs
 template <class C, int D, bool k8>
-__device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_t* q_s, uint8_t* ring) {
+__device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_t* q_s, uint8_t* rings) {
   volatile int* abort_flag = &sh->abort_flag;
   constexpr uint32_t tmem = 0;  // all columns are ours: they start at 0
-  constexpr uint32_t fmt = k8 ? 0u : 1u, R = C::kRing;
+  constexpr uint32_t fmt = k8 ? 0u : 1u;
   const uint32_t id_s = idesc(fmt, 0, kKeys), id_o = idesc(fmt, 0, D, 1u);
-  const uint64_t q_desc = sdesc(su32(q_s), 16, 1024), k_desc = sdesc(su32(ring), 16, 1024),
-                 v_desc = sdesc(su32(ring), C::kVKeys * 128, 1024);
+  const uint64_t q_desc = sdesc(su32(q_s), 16, 1024), k_desc = sdesc(su32(rings), 16, 1024),
+                 v_desc = sdesc(su32(rings) + C::kRK * kUnit, C::kVKeys * 128, 1024);
+  const int terms = C::kDirect && !a.q8 ? 2 : 1;
   ItemReader reader(sh);
   Item it{};
-  uint32_t x = 0;                      // ring units in front of the segment
-  uint32_t seq0 = 0, seq1 = 0;         // tiles so far of each row tile
-  uint32_t qn0 = 0, qn1 = 0;           // segments so far of each row tile
+  uint32_t t = 0;               // key tiles in front of the segment
+  uint32_t seq0 = 0, seq1 = 0;  // tiles so far of each row tile
+  uint32_t qn0 = 0, qn1 = 0;    // segments so far of each row tile
   bool alive = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return alive = bar_try(bar, parity & 1u) || bar_wait_slow(bar, parity & 1u, abort_flag, a);
   };
-  // S = Q K^T of row tile g into S buffer b; K at unit u
-  auto qk = [&](int g, int b, uint32_t u, bool release) {
+  // S = Q K^T of row tile g and key tile j of all into S buffer b
+  auto qk = [&](int g, int b, uint32_t j, bool release) {
 #pragma unroll
-    for (int c = 0; c < C::kU; ++c) {
-      const uint32_t slot = (u + c) % R;
-      if (!wait(sh->full + slot, (u + c) / R)) return;
+    for (int c = 0; c < C::kUK; ++c) {
+      const uint32_t u = j * C::kUK + c, slot = u % C::kRK;
+      if (!wait(sh->k_full + slot, u / C::kRK)) return;
       if (c == 0) fence_after();
       const uint64_t kd = k_desc + slot * (kUnit / 16);
+      for (int h = 0; h < (C::kDirect ? terms : 1); ++h) {
+        const uint64_t qd = q_desc + (g * (C::kQTile / 16) + (h * C::kUK + c) * (kUnit / 16));
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        mma<false>(tmem + b * kKeys, q_desc + (g * C::kU + c) * (kUnit / 16) + kk * 2, kd + kk * 2, id_s,
-                   (c | kk) != 0);
-      if (release) mma_commit(sh->empty + slot);
+        for (int kk = 0; kk < 4; ++kk)
+          mma<C::kDirect>(tmem + b * kKeys, qd + kk * 2, kd + kk * 2, id_s, (c | kk | h) != 0);
+      }
+      if (release) mma_commit(sh->k_empty + slot);
     }
     mma_commit(sh->s_full + b);
   };
-  // O += P V of row tile g, P over S buffer b; V at unit u
-  auto pv = [&](int g, int b, uint32_t u, uint32_t parity, bool first, bool release) {
+  // O += P V of row tile g and key tile j, P over S buffer b
+  auto pv = [&](int g, int b, uint32_t j, uint32_t parity, bool first, bool release) {
     if (!wait(sh->p_half + b, parity)) return;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {  // 16 keys a step
       constexpr int kSteps = C::kVKeys / 16;
-      const uint32_t slot = (u + kk / kSteps) % R;
-      if (kk % kSteps == 0 && !wait(sh->full + slot, (u + kk / kSteps) / R)) return;
+      const uint32_t u = j * C::kUV + kk / kSteps, slot = u % C::kRV;
+      if (kk % kSteps == 0 && !wait(sh->v_full + slot, u / C::kRV)) return;
       if (kk == 4 && !wait(sh->p_full + b, parity)) return;
       if (kk % kSteps == 0 || kk == 4) fence_after();
       mma_ts(tmem + kO + g * D, tmem + b * kKeys + kk * 8,
              v_desc + slot * (kUnit / 16) + (kk % kSteps) * 128, id_o, kk || !first ? 1u : 0u);
-      if (release && kk % kSteps == kSteps - 1) mma_commit(sh->empty + slot);
+      if (release && kk % kSteps == kSteps - 1) mma_commit(sh->v_empty + slot);
     }
     mma_commit(sh->o_done + b);
   };
@@ -345,12 +380,11 @@ __device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_
         for (int g = 0; g < 2; ++g) {
           if (g && !two) break;
           const bool last = g || !two;  // the units' last reader
-          const uint32_t xv = x + (2 * j + 1) * C::kU, xk = x + (2 * j + 2) * C::kU;
           uint32_t& seq = g ? seq1 : seq0;
           uint32_t& qn = g ? qn1 : qn0;
           if (j >= 0) {
             if (j == 0 && !wait(sh->o_free + g, (qn - 1) ^ 1u)) break;  // the last segment's O is read
-            pv(g, g, xv, seq, j == 0, last);
+            pv(g, g, t + j, seq, j == 0, last);
             if (!alive) break;
             ++seq;
           }
@@ -359,32 +393,30 @@ __device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_
               if (!wait(sh->q_full + g, qn)) break;
               ++qn;
             }
-            qk(g, g, xk, last);
+            qk(g, g, t + j + 1, last);
             if (!alive) break;
             if (j + 2 == n) mma_commit(sh->q_empty + g);
           }
         }
       }
     } else {
-      auto at_k = [&](int j) { return x + (j == 0 ? 0 : 2 * j - 1) * C::kU; };
-      auto at_v = [&](int j) { return x + min(2 * j + 2, 2 * n - 1) * C::kU; };
       if (!wait(sh->q_full, qn0)) break;
       ++qn0;
-      qk(0, seq0 & 1u, at_k(0), true);
-      if (alive && n > 1) qk(0, (seq0 + 1) & 1u, at_k(1), true);
+      qk(0, seq0 & 1u, t, true);
+      if (alive && n > 1) qk(0, (seq0 + 1) & 1u, t + 1, true);
       if (alive && n <= 2) mma_commit(sh->q_empty);
       for (int j = 0; j < n && alive; ++j) {
         if (j == 0 && !wait(sh->o_free, (qn0 - 1) ^ 1u)) break;
-        pv(0, seq0 & 1u, at_v(j), seq0 >> 1, j == 0, true);
+        pv(0, seq0 & 1u, t + j, seq0 >> 1, j == 0, true);
         if (!alive) break;
         ++seq0;
         if (j + 2 < n) {
-          qk(0, (seq0 + 1) & 1u, at_k(j + 2), true);
+          qk(0, (seq0 + 1) & 1u, t + j + 2, true);
           if (j + 3 == n) mma_commit(sh->q_empty);
         }
       }
     }
-    x += 2 * n * C::kU;
+    t += n;
   }
   // nothing issued may still run when TMEM is released
   mma_commit(&sh->drain);
@@ -393,8 +425,8 @@ __device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_
 
 // ------------------------------------------------------ codes widened to f16
 //
-// Four warps: a raw slot's codes, 16 at a time, into the ring's units, and the tile's
-// scales per token (loaded a tile ahead) into a ring of their own.
+// A raw slot's codes, 16 at a time, into the units of a ring, and the tile's scales per
+// token (loaded a tile ahead) into a ring of their own.
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, bool i8) {
   uint32_t r[4];
   const uint32_t w[2] = {lo, hi};
@@ -417,24 +449,38 @@ __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, bool i8) {
 }
 
 template <class C, int D, bool kI8, bool kTok>
-__device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint8_t* ring,
+__device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint8_t* rings,
                                            const uint8_t* raw, float* scales) {
+  constexpr int kT = 32 * C::kConv;  // threads
   const int t = threadIdx.x - 32 * C::kConv0, lane = threadIdx.x & 31;
   ItemReader reader(sh);
   Item it{};
-  uint32_t x = 0, y = 0, s = 0;  // ring units, raw slots, tiles of scales
-  constexpr uint32_t R = C::kRing, RR = C::kRaw;
+  uint32_t xk = 0, xv = 0, y = 0, s = 0;  // units of K and of V, raw slots, tiles of scales
+  constexpr uint32_t RR = C::kRaw;
+  constexpr int kRowPieces = D / 16;
   const int P = a.page_size;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = bar_wait(bar, parity & 1u, &sh->abort_flag, a);
     return __all_sync(0xffffffffu, ok);
+  };
+  auto hand_over = [&](uint64_t* bar) {
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) bar_arrive(bar);
+  };
+  // 16 codes at `src` to the 32 bytes from 16-byte piece `chunk` on of row r
+  auto put = [&](const uint8_t* src, uint8_t* dst, int r, int chunk, int flip) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src);
+    const uint4 lo = widen8(w.x, w.y, kI8), hi = widen8(w.z, w.w, kI8);
+    *reinterpret_cast<uint4*>(dst + sw128(r, (chunk + flip) * 16)) = flip ? hi : lo;
+    *reinterpret_cast<uint4*>(dst + sw128(r, (chunk + 1 - flip) * 16)) = flip ? lo : hi;
   };
   const float qk = a.sm_scale * kLog2e;
   float ks = 1.f, vs = 1.f;  // of this thread's key in the next tile
   auto load_scales = [&](int tile) {
     const int key = tile * kKeys + t;
     ks = vs = 1.f;
-    if (key < it.end) {
+    if (t < kKeys && key < it.end) {
       const int page = __ldg(a.page_table + it.table + key / P);
       if (page >= 0 && page < a.num_pages) {
         const int64_t at = (static_cast<int64_t>(page) * P + key % P) * a.hkv + it.head;
@@ -448,54 +494,63 @@ __device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint
     if constexpr (kTok) load_scales(it.t0);
     for (int i = 0; i < 2 * n; ++i) {
       int v, j;
-      ring_order<C::kG>(i, n, v, j);
-      if constexpr (kTok) {
-        if (!v) {  // the K tiles come in order
+      tile_order<C::kG>(i, n, v, j);
+      if (!v) {  // the K tiles come in order
+        if constexpr (kTok) {
           const uint32_t slot = s % kScales;
           if (!wait(sh->sc_empty + slot, (s / kScales) ^ 1u)) return;
-          float* to = scales + slot * 3 * kKeys;
-          const float v2 = vs > 0.f ? vs : 1.f;
-          to[t] = ks * qk;
-          to[kKeys + t] = __log2f(v2);
-          to[2 * kKeys + t] = __frcp_rn(v2);
+          if (t < kKeys) {
+            float* to = scales + slot * 3 * kKeys;
+            const float v2 = vs > 0.f ? vs : 1.f;
+            to[t] = ks * qk;
+            to[kKeys + t] = __log2f(v2);
+            to[2 * kKeys + t] = __frcp_rn(v2);
+          }
           __syncwarp();
           if (lane == 0) bar_arrive(sh->sc_full + slot);
           ++s;
           if (j + 1 < n) load_scales(it.t0 + j + 1);
         }
-      }
-      // the units this tile's codes go to
-      for (int c = 0; c < C::kU; ++c)
-        if (!wait(sh->empty + (x + c) % R, ((x + c) / R) ^ 1u)) return;
-      for (int h = 0; h < C::kRawTile; ++h, ++y) {
-        const uint32_t slot = y % RR;
-        if (!wait(sh->raw_full + slot, y / RR)) return;
-        const uint8_t* src = raw + slot * C::kRawBytes;
-        constexpr int kRowPieces = D / 16;
-#pragma unroll 4
-        for (int p = 0; p < C::kRawKeys * kRowPieces / 128; ++p) {
-          const int idx = p * 128 + t;
-          const int row = idx / kRowPieces, piece = idx % kRowPieces;
-          const uint4 w = *reinterpret_cast<const uint4*>(src + idx * 16);
-          const uint4 lo = widen8(w.x, w.y, kI8), hi = widen8(w.z, w.w, kI8);
-          const int key = h * C::kRawKeys + row, atom = piece >> 2, chunk = (piece & 3) * 2;
-          // K: a unit per 64 channels; V: a unit per kVKeys keys, its atoms one after another
-          const uint32_t u = v ? x + key / C::kVKeys : x + atom;
-          const int r = v ? key % C::kVKeys : key;
-          uint8_t* dst = ring + u % R * kUnit + (v ? atom * (C::kVKeys * 128) : 0);
-          // (a row's atoms share banks: every other one writes its halves in turn)
-          const int flip = atom & 1;
-          *reinterpret_cast<uint4*>(dst + sw128(r, (chunk + flip) * 16)) = flip ? hi : lo;
-          *reinterpret_cast<uint4*>(dst + sw128(r, (chunk + 1 - flip) * 16)) = flip ? lo : hi;
+        if constexpr (!C::kDirect) {
+          // a unit holds 64 channels of all keys, a raw slot all channels of its keys
+          for (int h = 0; h < C::kRawTile; ++h)
+            if (!wait(sh->raw_full + (y + h) % RR, (y + h) / RR)) return;
+          for (int c = 0; c < C::kUK; ++c, ++xk) {
+            const uint32_t slot = xk % C::kRK;
+            if (!wait(sh->k_empty + slot, (xk / C::kRK) ^ 1u)) return;
+            uint8_t* dst = rings + slot * kUnit;
+#pragma unroll
+            for (int p = 0; p < 512 / kT; ++p) {
+              const int idx = p * kT + t, key = idx >> 2, piece = idx & 3;
+              put(raw + (y + key / C::kRawKeys) % RR * C::kRawBytes + key % C::kRawKeys * D + c * 64 + piece * 16,
+                  dst, key, piece * 2, 0);
+            }
+            hand_over(sh->k_full + slot);
+          }
+          if (lane == 0)
+            for (int h = 0; h < C::kRawTile; ++h) bar_arrive(sh->raw_empty + (y + h) % RR);
+          y += C::kRawTile;
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(sh->raw_empty + slot);
+        continue;
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (int c = 0; c < C::kU; ++c) bar_arrive(sh->full + (x + c) % R);
-      x += C::kU;
+      constexpr int kUnits = C::kRawKeys / C::kVKeys;  // of a raw slot
+      for (int h = 0; h < C::kRawTile; ++h, ++y) {
+        if (!wait(sh->raw_full + y % RR, y / RR)) return;
+        for (int c = 0; c < kUnits; ++c, ++xv) {
+          const uint32_t slot = xv % C::kRV;
+          if (!wait(sh->v_empty + slot, (xv / C::kRV) ^ 1u)) return;
+          const uint8_t* src = raw + y % RR * C::kRawBytes + c * (C::kVKeys * D);
+          uint8_t* dst = rings + (C::kRK + slot) * kUnit;
+#pragma unroll
+          for (int p = 0; p < 512 / kT; ++p) {
+            const int idx = p * kT + t, r = idx / kRowPieces, piece = idx % kRowPieces, atom = piece >> 2;
+            // (a row's atoms share banks: every other one writes its halves in turn)
+            put(src + idx * 16, dst + atom * (C::kVKeys * 128), r, (piece & 3) * 2, atom & 1);
+          }
+          hand_over(sh->v_full + slot);
+        }
+        if (lane == 0) bar_arrive(sh->raw_empty + y % RR);
+      }
     }
   }
 }
@@ -504,24 +559,33 @@ __device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint
 template <int kRows>
 __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh) {
   const int lane = threadIdx.x & 31;
-  int64_t total = 0;
+  // a group, its units, and where its prefix's pages stand: in front of the own ones of
+  // its first request that has some (nearly always its first one)
+  auto look = [&](int g, Group& r, int& table) -> int64_t {
+    r = {};
+    table = -1;
+    if (g >= a.groups) return 0;
+    r = group_of(a, g);
+    if (!r.bad && r.b1 > r.b0 && __ldg(a.own_len + r.b0) > 0) table = __ldg(a.own_indptr + r.b0);
+    return units_of<kRows>(a, r);
+  };
+  int64_t total = 0, mine = 0, upto = 0;  // units; of this lane's group, and with those in front of it
   uint32_t bits = 0u;
+  Group r;
+  int table, known = -1;  // the 32 groups whose lanes hold `r`
   for (int g0 = 0; g0 < a.groups; g0 += 32) {
-    int64_t n = 0;
-    if (g0 + lane < a.groups) {
-      const Group r = group_of(a, g0 + lane);
-      bits |= r.bad;
-      n = units_of<kRows>(a, r);
-    }
-    int64_t x = n;
+    mine = look(g0 + lane, r, table);
+    bits |= r.bad;
+    known = g0 >> 5;
+    upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-      if (lane >= d) x += y;
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
     }
-    if (lane == 0) sh->coarse[g0 >> 5] = total;
-    if (blockIdx.x == 0 && g0 + lane < a.groups) a.first[1 + g0 + lane] = total + x - n;
-    total += __shfl_sync(0xffffffffu, x, 31);
+    if (lane == 0) sh->coarse[known] = total;
+    if (blockIdx.x == 0 && g0 + lane < a.groups) a.first[1 + g0 + lane] = total + upto - mine;
+    total += __shfl_sync(0xffffffffu, upto, 31);
   }
   __syncwarp();
   const int64_t per = max(static_cast<int64_t>(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
@@ -545,50 +609,42 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh) {
         if (sh->coarse[mid] <= pos) c = mid;
         else top = mid - 1;
       }
-      const int g = 32 * c + lane;
-      Group r = {};
-      if (g < a.groups) r = group_of(a, g);
-      const int64_t mine = g < a.groups ? units_of<kRows>(a, r) : 0;
-      int64_t upto = mine;
+      if (c != known) {
+        known = c;
+        mine = look(32 * c + lane, r, table);
+        upto = mine;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
-        if (lane >= d) upto += y;
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
+          if (lane >= d) upto += y;
+        }
       }
       const int64_t want = pos - sh->coarse[c];
       const int src = __ffs(__ballot_sync(0xffffffffu, upto > want)) - 1;
       const int64_t in = want - __shfl_sync(0xffffffffu, upto - mine, src);
-      r.b0 = __shfl_sync(0xffffffffu, r.b0, src);
-      r.b1 = __shfl_sync(0xffffffffu, r.b1, src);
-      r.q0 = __shfl_sync(0xffffffffu, r.q0, src);
-      r.rows = __shfl_sync(0xffffffffu, r.rows, src);
-      r.tile0 = __shfl_sync(0xffffffffu, r.tile0, src);
-      r.tiles = __shfl_sync(0xffffffffu, r.tiles, src);
-      r.end = __shfl_sync(0xffffffffu, r.end, src);
-      const int blocks = blocks_of<kRows>(a, r);
-      const int item = static_cast<int>(in / r.tiles), t = static_cast<int>(in % r.tiles);
+      const int b0 = __shfl_sync(0xffffffffu, r.b0, src), b1 = __shfl_sync(0xffffffffu, r.b1, src);
+      const int rows = __shfl_sync(0xffffffffu, r.rows, src);
+      const int tiles = __shfl_sync(0xffffffffu, r.tiles, src);
+      const int blocks = static_cast<int>((static_cast<int64_t>(rows) * a.group + kRows - 1) / kRows);
+      const int item = static_cast<int>(in / tiles), t = static_cast<int>(in % tiles);
       it.head = item / blocks;
       it.row0 = item % blocks * kRows;
       it.rows = static_cast<int>(min(static_cast<int64_t>(kRows),
-                                     static_cast<int64_t>(r.rows) * a.group - it.row0));
-      it.q0 = r.q0;
-      it.b0 = r.b0;
-      it.b1 = r.b1;
-      it.t0 = r.tile0 + t;
-      it.t1 = it.t0 + static_cast<int>(min(static_cast<int64_t>(r.tiles - t), stop - pos));
-      it.end = r.end;
+                                     static_cast<int64_t>(rows) * a.group - it.row0));
+      it.q0 = __shfl_sync(0xffffffffu, r.q0, src);
+      it.b0 = b0;
+      it.b1 = b1;
+      it.t0 = __shfl_sync(0xffffffffu, r.tile0, src) + t;
+      it.t1 = it.t0 + static_cast<int>(min(static_cast<int64_t>(tiles - t), stop - pos));
+      it.end = __shfl_sync(0xffffffffu, r.end, src);
       it.cut = t > 0;
-      // the prefix's pages stand in front of a request's own, where it has any
-      it.table = 0;
-      for (int b0 = r.b0; b0 < r.b1; b0 += 32) {
-        const int b = b0 + lane;
+      it.table = __shfl_sync(0xffffffffu, table, src);
+      for (int b = b0; it.table < 0 && b < b1; b += 32) {
         const uint32_t has =
-            __ballot_sync(0xffffffffu, b < r.b1 && __ldg(a.own_len + min(b, r.b1 - 1)) > 0);
-        if (has) {
-          it.table = __ldg(a.own_indptr + b0 + __ffs(has) - 1) - r.end / a.page_size;
-          break;
-        }
+            __ballot_sync(0xffffffffu, b + lane < b1 && __ldg(a.own_len + min(b + lane, b1 - 1)) > 0);
+        if (has) it.table = __ldg(a.own_indptr + b + __ffs(has) - 1);
       }
+      it.table -= it.end / a.page_size;
       pos += it.t1 - it.t0;
     }
     const uint32_t slot = n % kItems;
@@ -608,8 +664,8 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh) {
 // ------------------------------------------------------------------ softmax
 
 // Packed row m of a group: row m / group of its rows, head m % group of the kv head.
-// Its query into 128-byte-swizzled blocks of 64 channels, in the operands' type;
-// returns the power of two taken out of it.
+// Its query into 128-byte-swizzled units of a row tile, in the operands' type; returns
+// the power of two taken out of it.
 template <class C, int D, bool k8>
 __device__ __forceinline__ float load_query(const SharedArgs& a, const Item& it, uint8_t* q_s, int r, int m) {
   const bool live = m < it.row0 + it.rows;
@@ -629,9 +685,13 @@ __device__ __forceinline__ float load_query(const SharedArgs& a, const Item& it,
 #pragma unroll 4
       for (int c = 0; c < D / 16; ++c) {
         const uint4 w = live ? __ldg(src + c) : zero;
-        uint8_t* dst = q_s + (c >> 2) * kUnit;
-        *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32)) = widen8(w.x, w.y, false);
-        *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32 + 16)) = widen8(w.z, w.w, false);
+        if constexpr (C::kDirect) {
+          *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) = w;
+        } else {
+          uint8_t* dst = q_s + (c >> 2) * kUnit;
+          *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32)) = widen8(w.x, w.y, false);
+          *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32 + 16)) = widen8(w.z, w.w, false);
+        }
       }
       return 1.f;
     }
@@ -644,24 +704,54 @@ __device__ __forceinline__ float load_query(const SharedArgs& a, const Item& it,
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = max(top, max(v[e] << 16 & 0x7FFF0000u, v[e] & 0x7FFF0000u));
     }
-    // 2^-6 <= largest < 2^12: as it is; NaN and infinity too
     int ex = static_cast<int>(top >> 23) - 127;
-    if (top == 0u || ex == 128 || (ex >= -6 && ex < 12)) ex = 0;
+    if constexpr (C::kDirect) {
+      // to [224, 448): 1.75 x 2^8 is E4M3's largest
+      ex += (top & 0x7FFFFFu) <= 0x600000u ? -8 : -7;
+      if (top == 0u || top >= 0x7F800000u) ex = 0;
+    } else if (top == 0u || ex == 128 || (ex >= -6 && ex < 12)) {
+      ex = 0;  // 2^-6 <= largest < 2^12: as it is; NaN and infinity too
+    }
     ex = max(-126, min(126, ex));
     const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-#pragma unroll 8
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 w = live ? __ldg(src + c) : zero;
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-      uint32_t h[4];
+    if constexpr (C::kDirect) {
+#pragma unroll 4
+      for (int c = 0; c < D / 16; ++c) {
+        uint32_t t1[4], t2[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __half2 p = __floats2half2_rn(__uint_as_float(v[e] << 16) * down,
-                                            __uint_as_float(v[e] & 0xFFFF0000u) * down);
-        h[e] = *reinterpret_cast<const uint32_t*>(&p);
+        for (int h = 0; h < 2; ++h) {
+          const uint4 w = live ? __ldg(src + 2 * c + h) : zero;
+          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x0 = __uint_as_float(v[e] << 16) * down, x1 = __uint_as_float(v[e] & 0xFFFF0000u) * down;
+            const uint16_t c1 = e4m3x2(x0, x1);
+            const float2 back = e4m3x2_to_f2(c1);
+            const uint16_t c2 = e4m3x2(x0 - back.x, x1 - back.y);
+            const int k = h * 2 + (e >> 1);
+            t1[k] = e & 1 ? t1[k] | static_cast<uint32_t>(c1) << 16 : c1;
+            t2[k] = e & 1 ? t2[k] | static_cast<uint32_t>(c2) << 16 : c2;
+          }
+        }
+        uint8_t* dst = q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16);
+        *reinterpret_cast<uint4*>(dst) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+        *reinterpret_cast<uint4*>(dst + C::kUK * kUnit) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
       }
-      *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) =
-          make_uint4(h[0], h[1], h[2], h[3]);
+    } else {
+#pragma unroll 8
+      for (int c = 0; c < D / 8; ++c) {
+        const uint4 w = live ? __ldg(src + c) : zero;
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __half2 p = __floats2half2_rn(__uint_as_float(v[e] << 16) * down,
+                                              __uint_as_float(v[e] & 0xFFFF0000u) * down);
+          h[e] = *reinterpret_cast<const uint32_t*>(&p);
+        }
+        *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+      }
     }
     return __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
   }
@@ -670,6 +760,12 @@ __device__ __forceinline__ float load_query(const SharedArgs& a, const Item& it,
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 
@@ -711,12 +807,11 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
     }
     const int m0 = it.row0 + g * kTile + r;
     if (!wait(sh->q_empty + g, qn ^ 1u)) return;
-    const float up = load_query<C, D, k8>(a, it, q_s + g * C::kU * kUnit, r, m0);
+    const float up = load_query<C, D, k8>(a, it, q_s + g * C::kQTile, r, m0);
     fence_async_smem();
     __syncwarp();
     if (lane == 0) bar_arrive(sh->q_full + g);
     ++qn;
-    const bool fix = kTok && __any_sync(0xffffffffu, up != 1.f);
     float scale = 1.f;
     if constexpr (!kTok) scale = (sign != 0.f ? fabsf(logit) : 1.f) * up;
     // first key this row sees
@@ -744,7 +839,8 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
       const int k0 = j * kKeys;
       const bool hide = __any_sync(0xffffffffu, first > k0) || k0 + kKeys > it.end;
       const float *kp = sp, *lp = sp + kKeys;
-      if (hide || sign != 1.f || fix) {
+      float done = up;
+      if (hide || sign != 1.f) {
         // some row does not see the whole tile: mask S where it stands
 #pragma unroll 1
         for (int c = 0; c < kKeys; c += 32) {
@@ -763,23 +859,25 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
         tmem_wait_st();
         kp = scales + kScales * 3 * kKeys;  // 1, and 0
         lp = kp + kKeys;
+        done = 1.f;
       }
       uint32_t s[kKeys];
 #pragma unroll
       for (int c = 0; c < kKeys; c += 32) tmem_ld32(t_s + c, s + c);
       tmem_wait_ld<kKeys>(s);
       if constexpr (kTok) {
+        const uint64_t up2 = pack2(done, done);
 #pragma unroll
         for (int e = 0; e < kKeys; e += 4) {
           const float4 k4 = *reinterpret_cast<const float4*>(kp + e);
           const float4 l4 = *reinterpret_cast<const float4*>(lp + e);
           float x0, x1;
-          unpack2(fma2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), pack2(k4.x, k4.y),
-                       pack2(l4.x, l4.y)), x0, x1);
+          unpack2(fma2(mul2(pack2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), up2),
+                       pack2(k4.x, k4.y), pack2(l4.x, l4.y)), x0, x1);
           s[e] = __float_as_uint(x0);
           s[e + 1] = __float_as_uint(x1);
-          unpack2(fma2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), pack2(k4.z, k4.w),
-                       pack2(l4.z, l4.w)), x0, x1);
+          unpack2(fma2(mul2(pack2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), up2),
+                       pack2(k4.z, k4.w), pack2(l4.z, l4.w)), x0, x1);
           s[e + 2] = __float_as_uint(x0);
           s[e + 3] = __float_as_uint(x1);
         }
@@ -904,17 +1002,17 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
 }
 
 template <int D, bool k8, bool kI8, bool kTok>
-__global__ void __launch_bounds__(Cfg<D, k8, kTok>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
     shared_prefix(const __grid_constant__ SharedArgs a, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv) {
-  using C = Cfg<D, k8, kTok>;
+  using C = Cfg<D, k8, kI8, kTok>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* q_s = smem;
-  uint8_t* ring = smem + C::kQBytes;
-  uint8_t* raw = ring + C::kRing * kUnit;
+  uint8_t* rings = smem + C::kQBytes;
+  uint8_t* raw = rings + C::kRings;
   float* scales = reinterpret_cast<float*>(raw + C::kRaw * C::kRawBytes);
   Shared* sh = reinterpret_cast<Shared*>(smem + C::kSmem - sizeof(Shared));
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
   if (su32(smem) % 1024u) {  // the swizzled tiles need it
     if (tid == 0) atomicOr(a.status, PDA_STATUS_SMEM_MISALIGNED);
     return;
@@ -929,16 +1027,20 @@ __global__ void __launch_bounds__(Cfg<D, k8, kTok>::kThreads, 1)
       bar_init(sh->o_done + g, 1);
       bar_init(sh->o_free + g, 4);
     }
-    for (int u = 0; u < C::kRing; ++u) {
-      bar_init(sh->full + u, k8 ? 4 : 1);
-      bar_init(sh->empty + u, 1);
+    for (int u = 0; u < C::kRK; ++u) {
+      bar_init(sh->k_full + u, k8 && !C::kDirect ? C::kConv : 1);
+      bar_init(sh->k_empty + u, 1);
+    }
+    for (int u = 0; u < C::kRV; ++u) {
+      bar_init(sh->v_full + u, k8 ? C::kConv : 1);
+      bar_init(sh->v_empty + u, 1);
     }
     for (int u = 0; u < C::kRaw; ++u) {
       bar_init(sh->raw_full + u, 1);
-      bar_init(sh->raw_empty + u, 4);
+      bar_init(sh->raw_empty + u, C::kConv);
     }
-    for (int u = 0; u < kScales; ++u) {
-      bar_init(sh->sc_full + u, 4);
+    for (int u = 0; u < (kTok ? kScales : 0); ++u) {
+      bar_init(sh->sc_full + u, C::kConv);
       bar_init(sh->sc_empty + u, C::kSoft);
     }
     for (int u = 0; u < kItems; ++u) {
@@ -965,25 +1067,26 @@ __global__ void __launch_bounds__(Cfg<D, k8, kTok>::kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh->tmem;
-  // registers a thread: 192 x 256 + 64 x 256 with two row tiles (128 x 512 at the
-  // launch), 216 x 128 + 104 x 256 with one (168 x 384)
+  // registers a thread: with two row tiles 192 x 256 + 64 x 256 (128 x 512 at the launch),
+  // with one 216 x 128 + 104 x 256 (168 x 384), or 96 x 384 with codes to widen (128 x 512)
   if (warp < C::kSoft) {
     if constexpr (C::kG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
   } else {
     if constexpr (C::kG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    else if constexpr (k8) asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
   }
   if (warp < C::kSoft) {
     softmax_role<C, D, k8, kTok>(a, sh, q_s, scales, tmem, warp);
   } else if (warp == C::kMmaWarp) {
-    if (elect_one()) mma_role<C, D, k8>(a, sh, q_s, ring);
+    if (elect_one()) mma_role<C, D, k8>(a, sh, q_s, rings);
   } else if (warp == C::kWorkWarp) {
     work_role<C::kRows>(a, sh);
   } else if (k8 && warp >= C::kConv0) {
-    if constexpr (k8) widen_role<C, D, kI8, kTok>(a, sh, ring, raw, scales);
+    if constexpr (k8) widen_role<C, D, kI8, kTok>(a, sh, rings, raw, scales);
   } else {
-    load_role<C, D, k8>(a, sh, ring, raw, &tk, &tv, warp - C::kProd0);
+    load_role<C, D, k8>(a, sh, rings, raw, &tk, &tv, warp - C::kProd0);
   }
   __syncwarp();
   fence_before();
@@ -1221,12 +1324,15 @@ __global__ void __launch_bounds__(kShareThreads) share_tables(const __grid_const
 using PrefixFn = void (*)(SharedArgs, CUtensorMap, CUtensorMap);
 struct Kernel {
   PrefixFn fn;
-  int smem, threads, v_keys;
+  int smem, threads;
+  int k_keys, v_keys;  // most tokens of a K box and of a V box
+  bool direct;
 };
 template <int D, bool k8, bool kI8, bool kTok>
 Kernel kernel_of() {
-  using C = Cfg<D, k8, kTok>;
-  return {shared_prefix<D, k8, kI8, kTok>, C::kSmem, C::kThreads, k8 ? C::kRawKeys : C::kVKeys};
+  using C = Cfg<D, k8, kI8, kTok>;
+  return {shared_prefix<D, k8, kI8, kTok>, C::kSmem, C::kThreads,
+          k8 && !C::kDirect ? C::kRawKeys : kKeys, k8 ? C::kRawKeys : C::kVKeys, C::kDirect};
 }
 template <int D>
 Kernel kernel_for(const pda_plan_t& p) {
@@ -1239,9 +1345,9 @@ Kernel kernel_for(const pda_plan_t& p) {
   return p.head_dim == 64 ? kernel_for<64>(p) : p.head_dim == 128 ? kernel_for<128>(p) : kernel_for<256>(p);
 }
 
-// Tensor map of the cache, (channel, slot, kv head, page): boxes of `rows` tokens x 64
-// bf16 channels (swizzled), or x a head's codes (as they lie).
-bool page_map(CUtensorMap* m, const void* base, const pda_plan_t& p, int rows) {
+// Tensor map of the cache, (channel, slot, kv head, page): boxes of `rows` tokens x 128
+// bytes (swizzled: an operand), or x a head's codes (as they lie).
+bool page_map(CUtensorMap* m, const void* base, const pda_plan_t& p, int rows, bool operand) {
   EncodeFn enc = encoder();
   if (!enc) return false;
   const bool wide = p.kv_dtype == PDA_BF16;
@@ -1251,12 +1357,12 @@ bool page_map(CUtensorMap* m, const void* base, const pda_plan_t& p, int rows) {
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(p.kv_stride_token * eb),
                                  static_cast<cuuint64_t>(p.kv_stride_head * eb),
                                  static_cast<cuuint64_t>(p.kv_stride_page * eb)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(wide ? 64 : p.head_dim),
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(operand ? 128 / eb : p.head_dim),
                              static_cast<cuuint32_t>(std::min(p.page_size, rows)), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return enc(m, wide ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 4,
              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             operand ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1438,8 +1544,9 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
   a.inject = o.inject;
   const Kernel k = kernel_for(*plan);
   CUtensorMap tk, tv;
-  if (!page_map(&tk, k_pages, *plan, plan->kv_dtype == PDA_BF16 ? kKeys : k.v_keys) ||
-      !page_map(&tv, v_pages, *plan, k.v_keys))
+  const bool wide = plan->kv_dtype == PDA_BF16;
+  if (!page_map(&tk, k_pages, *plan, k.k_keys, wide || k.direct) ||
+      !page_map(&tv, v_pages, *plan, k.v_keys, wide))
     return PDA_ERR_CUDA;
   if (cudaFuncSetAttribute(reinterpret_cast<const void*>(k.fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                            k.smem) != cudaSuccess) {
