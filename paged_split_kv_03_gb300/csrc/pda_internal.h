@@ -107,13 +107,17 @@ PDA_HD bool work_item(const DecodeArgs& a, int64_t bid, WorkItem& w) {
 // Launchers and resource queries of the two stage-1 variants and stage 2.
 int mma_smem_bytes(const pda_plan_t* plan);
 int mma_ctas_per_sm(const pda_plan_t* plan);
-int launch_stage1_mma(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s);
+int launch_stage1_mma(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s,
+                      bool overlap = false);
 bool tc_supported(const pda_plan_t* plan);
 int tc_rows_limit(const pda_plan_t* plan);
 int tc_variant_rows(const pda_plan_t* plan);
 int tc_smem_bytes(const pda_plan_t* plan);
 int tc_ctas_per_sm(const pda_plan_t* plan);
-int launch_stage1_tc(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s);
+// (overlap: beside the kernel in front of it in the stream, whose CTAs let it start and do
+// not depend on it; stage 1 ends behind that kernel)
+int launch_stage1_tc(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s,
+                     bool overlap = false);
 int launch_stage2(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s);
 
 // Host-side checks of pda_decode's arguments (plan, pointers, alignment,
@@ -145,5 +149,14 @@ inline bool on_device(int device) {
 // pda_decode_static) on the current device, which must be `device`; looked
 // up afresh unless `s` is capturing a graph (then the last lookup is used).
 int static_scratch(int device, cudaStream_t s, void** out);
+
+#ifdef __CUDACC__
+// Stage 1's first CTA, on each of its ways out: where the launch overlaps the kernel in
+// front of it, what follows stage 1 follows both. (One CTA is enough, and the others make
+// room; without such a launch there is nothing to wait for.)
+__device__ __forceinline__ void end_behind_previous() {
+  if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+#endif
 
 }  // namespace pda

@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1) stage1_mma(const __grid_constant_
       else if (R > 0 && q0 + R > a.rows_cap) bits |= PDA_STATUS_ROWS_GT_CAP;
       if (bits) atomicOr(a.status, bits);
     }
+    end_behind_previous();
     return;
   }
   const int hpc = a.hpc[R];
@@ -547,6 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1) stage1_mma(const __grid_constant_
       if (c4 == 0) a.part_lse[prow] = lse2;
     }
   }
+  end_behind_previous();
 }
 
 // ------------------------------------------------------------------ stage 2
@@ -819,7 +821,7 @@ int mma_ctas_per_sm(const pda_plan_t* p) {
   return n < 1 ? 1 : (n > 4 ? 4 : n);
 }
 
-int launch_stage1_mma(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s) {
+int launch_stage1_mma(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s, bool overlap) {
   KernelFn k1 = stage1_for(plan);
   if (!k1) return PDA_ERR_UNSUPPORTED;
   const int smem = plan->stage1_smem_bytes;
@@ -833,6 +835,11 @@ int launch_stage1_mma(const pda_plan_t* plan, const DecodeArgs& args, cudaStream
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, k1, args) != cudaSuccess) {
     cudaGetLastError();
     return PDA_ERR_CUDA;

@@ -82,6 +82,7 @@ struct SharedArgs {
   int batch, groups, hq, hkv, group, page_size, num_pages, max_q_len;
   int64_t rows_cap;
   int q8;
+  int ctas;  // of the prefix kernel
   uint32_t inject;
 };
 
@@ -121,6 +122,10 @@ __device__ __forceinline__ int blocks_of(const SharedArgs& a, const Group& r) {
 template <int kRows>
 __device__ __forceinline__ int64_t units_of(const SharedArgs& a, const Group& r) {
   return static_cast<int64_t>(a.hkv) * blocks_of<kRows>(a, r) * r.tiles;
+}
+
+__device__ __forceinline__ int64_t units_of_cta(int64_t total, int ctas) {
+  return max(static_cast<int64_t>(kMinTiles), (total + ctas - 1) / ctas);
 }
 
 // One segment: key tiles [t0, t1) of an item.
@@ -588,7 +593,7 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh) {
     total += __shfl_sync(0xffffffffu, upto, 31);
   }
   __syncwarp();
-  const int64_t per = max(static_cast<int64_t>(kMinTiles), (total + gridDim.x - 1) / gridDim.x);
+  const int64_t per = units_of_cta(total, a.ctas);
   if (blockIdx.x == 0) {
     bits = __reduce_or_sync(0xffffffffu, bits);
     if (lane == 0) {
@@ -1067,6 +1072,8 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = sh->tmem;
+  // the requests' own tokens (stage 1) start where CTAs of this kernel leave room
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // registers a thread: with two row tiles 192 x 256 + 64 x 256 (128 x 512 at the launch),
   // with one 216 x 128 + 104 x 256 (168 x 384), or 96 x 384 with codes to widen (128 x 512)
   if (warp < C::kSoft) {
@@ -1100,7 +1107,8 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
 // -------------------------------------------------------------------- join
 //
 // One warp per (request, row, head): the prefix's segments in order, then the own
-// chunks. Bound: reading the partials (L2).
+// chunks. Bound: reading the partials (L2); where they are is worked out while the
+// kernels in front end.
 template <int D>
 __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ SharedArgs a,
                                                    const __grid_constant__ DecodeArgs o) {
@@ -1110,27 +1118,51 @@ __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ Share
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t per_b = static_cast<int64_t>(o.max_q_len) * a.hq;
   const int b = static_cast<int>(item / per_b);
-  if (b >= a.batch) return;
   const int i = static_cast<int>(item % per_b) / a.hq, head = static_cast<int>(item % a.hq);
-  const int q0 = __ldg(a.qo_indptr + b), R = __ldg(a.qo_indptr + b + 1) - q0;
-  const int L = __ldg(a.own_len + b), W = a.window ? __ldg(a.window + b) : 0;
-  if (i >= R || R > o.max_q_len || L < R || L > o.max_kv_len || q0 < 0 || q0 + R > a.rows_cap) return;
-  int g = 0, top = a.groups - 1;  // the last group that starts at or before the request
-  while (g < top) {
-    const int mid = (g + top + 1) >> 1;
-    if (__ldg(a.group_indptr + mid) <= b) g = mid;
-    else top = mid - 1;
+  bool live = b < a.batch;
+  int q0 = 0, own = 0, segs = 0;
+  int64_t c0 = 0, m = 0;  // CTA of the item's first segment; packed row
+  Group gr = {};
+  int g = 0;
+  if (live) {
+    q0 = __ldg(a.qo_indptr + b);
+    const int R = __ldg(a.qo_indptr + b + 1) - q0;
+    const int L = __ldg(a.own_len + b), W = a.window ? __ldg(a.window + b) : 0;
+    live = i < R && R <= o.max_q_len && L >= R && L <= o.max_kv_len && q0 >= 0 && q0 + R <= a.rows_cap;
+    if (live) own = split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
   }
-  const Group gr = group_of(a, g);
-  const int own = split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
+  if (live) {
+    int top = a.groups - 1;  // the last group that starts at or before the request
+    while (g < top) {
+      const int mid = (g + top + 1) >> 1;
+      if (__ldg(a.group_indptr + mid) <= b) g = mid;
+      else top = mid - 1;
+    }
+    gr = group_of(a, g);
+    m = static_cast<int64_t>(q0 + i - gr.q0) * a.group + head % a.group;
+  }
   const int h = head / a.group;
-  const int64_t m = static_cast<int64_t>(q0 + i - gr.q0) * a.group + head % a.group;  // packed row
+  int64_t first = 0, per = 0;
+  if (a.groups <= 32) {  // the work's cut again, a group a lane: no load to wait for
+    const int64_t n = lane < a.groups ? units_of<kRows>(a, group_of(a, lane)) : 0;
+    int64_t upto = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += y;
+    }
+    per = units_of_cta(__shfl_sync(0xffffffffu, upto, 31), a.ctas);
+    first = __shfl_sync(0xffffffffu, upto - n, g);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!live) return;
+  if (a.groups > 32) {
+    per = a.first[0];
+    first = a.first[1 + g];
+  }
   const int block = static_cast<int>(m / kRows), r = static_cast<int>(m % kRows);
-  int64_t c0 = 0;  // CTA of the item's first segment
-  int segs = 0;
   if (gr.tiles > 0) {
-    const int64_t per = a.first[0];
-    const int64_t u = a.first[1 + g] + (static_cast<int64_t>(h) * blocks_of<kRows>(a, gr) + block) * gr.tiles;
+    const int64_t u = first + (static_cast<int64_t>(h) * blocks_of<kRows>(a, gr) + block) * gr.tiles;
     c0 = u / per;
     segs = static_cast<int>((u + gr.tiles - 1) / per - c0) + 1;
   }
@@ -1151,7 +1183,7 @@ __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ Share
       v = a.area_o + at * D;
     }
   };
-  constexpr int kBatch = 8;
+  constexpr int kBatch = D <= 128 ? 16 : 8;
   float M = -INFINITY, sum = 0.f, acc[kV];
 #pragma unroll
   for (int e = 0; e < kV; ++e) acc[e] = 0.f;
@@ -1164,11 +1196,19 @@ __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ Share
         const float *px, *pv;
         place(s0 + k, px, pv);
         x[k] = *px;
+        if constexpr (kV == 2) {
+          const float2 t = *reinterpret_cast<const float2*>(pv + lane * 2);
+          v[k][0] = t.x;
+          v[k][1] = t.y;
+        } else {
 #pragma unroll
-        for (int e = 0; e < kV; e += 2) {
-          const float2 t = *reinterpret_cast<const float2*>(pv + lane * kV + e);
-          v[k][e] = t.x;
-          v[k][e + 1] = t.y;
+          for (int e = 0; e < kV; e += 4) {
+            const float4 t = *reinterpret_cast<const float4*>(pv + lane * kV + e);
+            v[k][e] = t.x;
+            v[k][e + 1] = t.y;
+            v[k][e + 2] = t.z;
+            v[k][e + 3] = t.w;
+          }
         }
       }
     }
@@ -1194,9 +1234,12 @@ __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ Share
   }
   const float inv = sum > 0.f ? 1.f / sum : sum;  // (NaN stays)
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.out) + own_row * D + lane * kV;
+  uint32_t w[kV / 2];
 #pragma unroll
-  for (int e = 0; e < kV; e += 2)
-    *reinterpret_cast<uint32_t*>(dst + e) = bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  for (int e = 0; e < kV; e += 2) w[e / 2] = bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if constexpr (kV == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
+  else if constexpr (kV == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   if (lane == 0 && o.lse) o.lse[own_row] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * kLn2;
 }
 
@@ -1542,6 +1585,7 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
   a.rows_cap = o.rows_cap;
   a.q8 = plan->q_dtype == PDA_E4M3;
   a.inject = o.inject;
+  a.ctas = plan->num_sms;
   const Kernel k = kernel_for(*plan);
   CUtensorMap tk, tv;
   const bool wide = plan->kv_dtype == PDA_BF16;
@@ -1554,16 +1598,24 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
     return PDA_ERR_CUDA;
   }
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  k.fn<<<static_cast<unsigned>(plan->num_sms), k.threads, k.smem, s>>>(a, tk, tv);
+  k.fn<<<static_cast<unsigned>(a.ctas), k.threads, k.smem, s>>>(a, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-  rc = plan->kernel == PDA_KERNEL_TC ? launch_stage1_tc(plan, o, s) : launch_stage1_mma(plan, o, s);
+  rc = plan->kernel == PDA_KERNEL_TC ? launch_stage1_tc(plan, o, s, true) : launch_stage1_mma(plan, o, s, true);
   if (rc != PDA_OK) return rc;
   const int64_t warps = static_cast<int64_t>(a.batch) * max_q_len * a.hq;
-  const unsigned grid = static_cast<unsigned>((warps + 7) / 8);
-  switch (plan->head_dim) {
-    case 64: shared_join<64><<<grid, 256, 0, s>>>(a, o); break;
-    case 128: shared_join<128><<<grid, 256, 0, s>>>(a, o); break;
-    default: shared_join<256><<<grid, 256, 0, s>>>(a, o); break;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto* join = plan->head_dim == 64 ? shared_join<64> : plan->head_dim == 128 ? shared_join<128> : shared_join<256>;
+  if (cudaLaunchKernelEx(&cfg, join, a, o) != cudaSuccess) {
+    cudaGetLastError();
+    return PDA_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  return PDA_OK;
 }

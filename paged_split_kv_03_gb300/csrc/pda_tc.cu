@@ -1135,6 +1135,7 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
       else if (R > 0 && q0 + R > a.rows_cap) bits |= PDA_STATUS_ROWS_GT_CAP;
       if (bits) atomicOr(a.status, bits);
     }
+    end_behind_previous();
     return;
   }
   const int hpc = a.hpc[R];
@@ -1724,6 +1725,7 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
   // ---- teardown: everyone done with TMEM and shared memory
   __syncwarp();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  end_behind_previous();
   fence_before();
   __syncthreads();
   fence_after();
@@ -1906,7 +1908,7 @@ static unsigned tc_threads(const pda_plan_t* p) {
   return static_cast<unsigned>(tc_select(p, p->rows_per_cta, GetThreads()));
 }
 
-int launch_stage1_tc(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s) {
+int launch_stage1_tc(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_t s, bool overlap) {
   DecodeArgs a = args;
   CUtensorMap mk, mv;
   int slot_dim = 1;
@@ -1932,6 +1934,11 @@ int launch_stage1_tc(const pda_plan_t* plan, const DecodeArgs& args, cudaStream_
   cfg.blockDim = dim3(tc_threads(plan));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, k1, a, mk, mv) != cudaSuccess) {
     cudaGetLastError();
     return PDA_ERR_CUDA;
