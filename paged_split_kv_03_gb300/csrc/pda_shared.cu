@@ -243,6 +243,13 @@ __device__ __forceinline__ void tile_order(int i, int n, int& v, int& j) {
   }
 }
 
+// The place of tile j of K (V) in that order.
+template <int kG>
+__device__ __forceinline__ uint32_t tile_place(int v, int j, int n) {
+  if constexpr (kG == 2) return 2 * j + v;
+  else return v ? min(2 * j + 2, 2 * n - 1) : max(0, 2 * j - 1);
+}
+
 // ------------------------------------------------------------------- loads
 //
 // Even warps load K, odd ones V, a unit (or raw slot) a warp in turn; its boxes (a page's
@@ -274,53 +281,53 @@ __device__ __forceinline__ void load_role(const SharedArgs& a, Shared* sh, uint8
   const int at = lane % boxes, atom = lane / boxes;
   const uint32_t box = atom * (unit_keys * 128) + at * rows * (to_raw ? D : 128);
   const CUtensorMap* map = v ? tv : tk;
-  uint32_t x = 0, issued = 0u, parity = 0u;  // units so far; slots this warp loaded last, and when
+  // the page of this lane's box of unit c of tile j (the lookup of a unit is under way
+  // while the one in front of it waits for its place)
+  const bool mine = atom < atoms;
+  auto first_key = [&](int j, int c) {
+    return (it.t0 + j) * kKeys + (to_raw || v ? c * unit_keys : 0) + at * rows;
+  };
+  auto page_of = [&](int j, int c) {
+    const int key = first_key(j, c);
+    if (!mine || key >= it.end) return a.num_pages;
+    return __ldg(a.page_table + it.table + key / P);
+  };
+  uint32_t t = 0, last = 0;  // key tiles in front of the segment; units up to here
   while (alive && reader.next_warp(it, a)) {
-    const int n = it.t1 - it.t0;
-    for (int i = 0; i < 2 * n && alive; ++i) {
-      int tv_, j;
-      tile_order<C::kG>(i, n, tv_, j);
-      if (tv_ != v) {
-        // raw slots are shared with the other side's tiles, unless those are not widened
-        if (to_raw && !C::kDirect)
-          for (int c = 0; c < C::kRawTile; ++c, ++x) issued &= ~(1u << x % slots);
-        continue;
+    const uint32_t n = it.t1 - it.t0, u0 = t * units, u1 = u0 + n * units;
+    uint32_t u = u0 + (turn + kTurns - u0 % kTurns) % kTurns;
+    int page = u < u1 ? page_of((u - u0) / units, (u - u0) % units) : 0;
+    for (; u < u1; u += kTurns) {
+      const int j = (u - u0) / units, c = (u - u0) % units;
+      int ahead = 0;
+      if (u + kTurns < u1) ahead = page_of((u + kTurns - u0) / units, (u + kTurns - u0) % units);
+      // raw slots are shared by both sides' tiles, unless K needs none
+      const uint32_t x = !to_raw || C::kDirect ? u : 2 * u0 + tile_place<C::kG>(v, j, n) * units + c;
+      const uint32_t slot = x % slots;
+      int good = 1;
+      if (lane == 0) {
+        good = bar_wait(empty + slot, ((x / slots) & 1u) ^ 1u, abort_flag, a);
+        if (good) bar_expect_tx(full + slot, slot_bytes);
       }
-      const int key0 = (it.t0 + j) * kKeys;
-      for (int c = 0; c < units; ++c, ++x) {
-        if (!to_raw && x % kTurns != turn) {
-          issued &= ~(1u << x % slots);
-          continue;
-        }
-        const int key = key0 + (to_raw || v ? c * unit_keys : 0) + at * rows;
-        const int chan = to_raw ? 0 : k8 ? c * 128 : (v ? atom : c) * 64;
-        const bool mine = atom < atoms;
-        int page = a.num_pages;
-        if (mine && key < it.end) {
-          page = __ldg(a.page_table + it.table + key / P);
-          if (page < 0 || page > a.num_pages) page = a.num_pages;
-        }
-        const uint32_t slot = x % slots;
-        int good = 1;
-        if (lane == 0) {
-          good = bar_wait(empty + slot, ((x / slots) & 1u) ^ 1u, abort_flag, a);
-          if (good) bar_expect_tx(full + slot, slot_bytes);
-        }
-        if (!__shfl_sync(0xffffffffu, good, 0)) {
-          alive = false;
-          break;
-        }
-        if (mine) tma_page(base + slot * slot_bytes + box, map, chan, key % P, it.head, page, full + slot);
-        issued |= 1u << slot;
-        parity = (parity & ~(1u << slot)) | (x / slots & 1u) << slot;
+      if (!__shfl_sync(0xffffffffu, good, 0)) {
+        alive = false;
+        break;
       }
+      if (page < 0 || page > a.num_pages) page = a.num_pages;
+      const int chan = to_raw ? 0 : k8 ? c * 128 : (v ? atom : c) * 64;
+      if (mine)
+        tma_page(base + slot * slot_bytes + box, map, chan, first_key(j, c) % P, it.head, page, full + slot);
+      page = ahead;
+      last = x + 1;
     }
+    t += n;
+    if (alive) last = !to_raw || C::kDirect ? u1 : 2 * u1;
   }
-  // Every box issued must have landed before the CTA can exit: the last unit of each slot
-  // where it is this warp's (the one in front of another warp's has been read).
+  // every box issued must have landed before the CTA can exit: the last unit of each slot,
+  // whichever warp's it is (after a wait that ran out another warp's may not be coming)
   if (lane == 0)
-    for (uint32_t k = 0; k < slots; ++k)
-      if (issued >> k & 1u) bar_drain(full + k, parity >> k & 1u);
+    for (uint32_t k = last > slots ? last - slots : 0u; k < last; ++k)
+      if (alive || k % kTurns == turn) bar_drain(full + k % slots, (k / slots) & 1u);
 }
 
 // -------------------------------------------------------------------- MMAs
@@ -481,22 +488,28 @@ __device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint
     *reinterpret_cast<uint4*>(dst + sw128(r, (chunk + 1 - flip) * 16)) = flip ? lo : hi;
   };
   const float qk = a.sm_scale * kLog2e;
-  float ks = 1.f, vs = 1.f;  // of this thread's key in the next tile
-  auto load_scales = [&](int tile) {
+  // of this thread's key: the scales of the next tile, the page of the one behind it
+  float ks = 1.f, vs = 1.f;
+  int page = -1;
+  auto load_page = [&](int tile) {
     const int key = tile * kKeys + t;
+    page = t < kKeys && key < it.end ? __ldg(a.page_table + it.table + key / P) : -1;
+  };
+  auto load_scales = [&](int tile) {
     ks = vs = 1.f;
-    if (t < kKeys && key < it.end) {
-      const int page = __ldg(a.page_table + it.table + key / P);
-      if (page >= 0 && page < a.num_pages) {
-        const int64_t at = (static_cast<int64_t>(page) * P + key % P) * a.hkv + it.head;
-        ks = __ldg(a.k_scale + at);
-        vs = __ldg(a.v_scale + at);
-      }
+    if (page >= 0 && page < a.num_pages) {
+      const int64_t at = (static_cast<int64_t>(page) * P + (tile * kKeys + t) % P) * a.hkv + it.head;
+      ks = __ldg(a.k_scale + at);
+      vs = __ldg(a.v_scale + at);
     }
   };
   while (reader.next_warp(it, a)) {
     const int n = it.t1 - it.t0;
-    if constexpr (kTok) load_scales(it.t0);
+    if constexpr (kTok) {
+      load_page(it.t0);
+      load_scales(it.t0);
+      load_page(it.t0 + 1);
+    }
     for (int i = 0; i < 2 * n; ++i) {
       int v, j;
       tile_order<C::kG>(i, n, v, j);
@@ -514,7 +527,8 @@ __device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint
           __syncwarp();
           if (lane == 0) bar_arrive(sh->sc_full + slot);
           ++s;
-          if (j + 1 < n) load_scales(it.t0 + j + 1);
+          load_scales(it.t0 + j + 1);  // (behind the segment: not used)
+          load_page(it.t0 + j + 2);
         }
         if constexpr (!C::kDirect) {
           // a unit holds 64 channels of all keys, a raw slot all channels of its keys
