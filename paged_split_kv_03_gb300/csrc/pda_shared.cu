@@ -32,6 +32,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "pda.h"
 #include "pda_cvt.cuh"
@@ -51,11 +52,10 @@ constexpr int kTile = 128;     // rows of a softmax warpgroup
 constexpr int kUnit = 16384;   // bytes of a ring unit
 constexpr int kItems = 3;      // slots of the segment ring
 constexpr int kScales = 4;     // slots of the ring of per-token scales, a tile each
-constexpr int kCoarse = 256;   // prefix entries, 32 groups each
+constexpr int kCoarse = 64;    // prefix entries, 32 groups each
 constexpr int kMaxGroups = 32 * kCoarse;
 constexpr int kTmemCols = 512;
 constexpr int kO = 2 * kKeys;  // first TMEM column of O; two S in front of it
-constexpr int kMinTiles = 1;   // least key tiles of a CTA
 
 // ------------------------------------------------- the groups and their prefixes
 
@@ -75,7 +75,7 @@ struct SharedArgs {
   float* main_x;    // ... and their log2 sums
   float* area_o;    // [CTA][rows of an item][D]: the segment a CTA starts inside an item
   float* area_x;
-  int64_t* first;   // [groups] first unit of each group, and in front the units of a CTA
+  int* first;       // the cut (per, pay), then [groups] where each group's work starts
   uint32_t* status;
   uint64_t wait_limit_ns;
   float sm_scale;
@@ -83,6 +83,7 @@ struct SharedArgs {
   int64_t rows_cap;
   int q8;
   int ctas;  // of the prefix kernel
+  int one;   // what a tile of a block of at most 128 rows counts
   uint32_t inject;
 };
 
@@ -113,19 +114,44 @@ __device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
   return r;
 }
 
-// Work in units of a key tile of an item (a block of packed rows of a kv head):
-// group by group, then kv heads, blocks, tiles. CTA c has units [c n, (c + 1) n).
-template <int kRows>
-__device__ __forceinline__ int blocks_of(const SharedArgs& a, const Group& r) {
-  return static_cast<int>((static_cast<int64_t>(r.rows) * a.group + kRows - 1) / kRows);
+// How the work is cut. An item is a block of kRows packed rows of a kv head, over the
+// prefix's key tiles; group by group, then kv heads, then blocks, the items stand on one
+// axis, and CTA c has the stretch [c per, (c + 1) per) of it: the tiles that begin there. A
+// tile counts kFull, or `one` in a last block of one row tile, whose time is that of
+// its loads. An item is longer by `pay` in front of its tiles: a CTA's further segment
+// costs it a query load and an epilogue, about three tiles' time (64 requests behind 8192
+// tokens, 64 / 8 heads of 128: CTAs of two segments ended at 34 us, the others at 23).
+// Without it where a CTA has less than two tiles: most would be left without any. The
+// plan keeps the axis below 2^31.
+constexpr int kFull = 8, kPay = 3 * kFull;
+template <int kG>
+struct Work {
+  int blocks = 0, tiles = 0, last = 0;  // last: what a tile of the last block counts
+  __device__ __forceinline__ Work() {}
+  __device__ __forceinline__ Work(const SharedArgs& a, const Group& r) {
+    const int packed = r.rows * a.group;
+    tiles = r.tiles;
+    if (tiles == 0) return;
+    blocks = (packed + kG * kTile - 1) / (kG * kTile);
+    last = kG == 1 || packed - (blocks - 1) * (kG * kTile) > kTile ? kFull : a.one;
+  }
+  __device__ __forceinline__ int full(int pay) const { return kFull * tiles + pay; }
+  // of a kv head
+  __device__ __forceinline__ int head(int pay) const {
+    return blocks ? (blocks - 1) * full(pay) + last * tiles + pay : 0;
+  }
+};
+__device__ __forceinline__ void cut_of(int work, int items, int ctas, int& per, int& pay) {
+  pay = work <= ctas * (2 * kFull - 1) ? 0 : kPay;
+  per = max(kFull, static_cast<int>((static_cast<uint32_t>(work + pay * items) + ctas - 1) / static_cast<uint32_t>(ctas)));
 }
-template <int kRows>
-__device__ __forceinline__ int64_t units_of(const SharedArgs& a, const Group& r) {
-  return static_cast<int64_t>(a.hkv) * blocks_of<kRows>(a, r) * r.tiles;
-}
-
-__device__ __forceinline__ int64_t units_of_cta(int64_t total, int ctas) {
-  return max(static_cast<int64_t>(kMinTiles), (total + ctas - 1) / ctas);
+__device__ __forceinline__ int scan32(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
 }
 
 // One segment: key tiles [t0, t1) of an item.
@@ -143,12 +169,14 @@ struct Item {
 
 struct Shared {
   uint64_t q_full[2], q_empty[2], k_full[8], k_empty[8], v_full[8], v_empty[8], raw_full[4], raw_empty[4],
-      sc_full[kScales], sc_empty[kScales], s_full[2], p_half[2], p_full[2], o_done[2], o_free[2],
+      sc_full[kScales], sc_empty[kScales], s_full[2], p_half[2], p_full[2], o_done[2], o_free[2], odd_done,
       item_full[kItems], item_empty[kItems], drain;
   uint32_t tmem;
   int abort_flag;
   Item items[kItems];
-  int64_t coarse[kCoarse];
+  int coarse[kCoarse];           // work in front of every 32 groups
+  int coarse_items[kCoarse];     // items there
+  float2 rows[kTile];            // a row's power of two; then its maximum and sum in the odd tiles
 };
 
 // ------------------------------------------------------------ configuration
@@ -343,13 +371,14 @@ __device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_
   ItemReader reader(sh);
   Item it{};
   uint32_t t = 0;               // key tiles in front of the segment
-  uint32_t seq0 = 0, seq1 = 0;  // tiles so far of each row tile
-  uint32_t qn0 = 0, qn1 = 0;    // segments so far of each row tile
+  uint32_t seq0 = 0, seq1 = 0;  // tiles so far of each softmax warpgroup
+  uint32_t qn0 = 0, qn1 = 0;    // queries so far of each row tile
+  uint32_t on0 = 0, on1 = 0;    // segments so far of each O
   bool alive = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     return alive = bar_try(bar, parity & 1u) || bar_wait_slow(bar, parity & 1u, abort_flag, a);
   };
-  // S = Q K^T of row tile g and key tile j of all into S buffer b
+  // S = Q K^T of row tile g and key tile j (of all the CTA's) into S buffer b
   auto qk = [&](int g, int b, uint32_t j, bool release) {
 #pragma unroll
     for (int c = 0; c < C::kUK; ++c) {
@@ -367,7 +396,7 @@ __device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_
     }
     mma_commit(sh->s_full + b);
   };
-  // O += P V of row tile g and key tile j, P over S buffer b
+  // O_g += P V of key tile j, P over S buffer b
   auto pv = [&](int g, int b, uint32_t j, uint32_t parity, bool first, bool release) {
     if (!wait(sh->p_half + b, parity)) return;
 #pragma unroll
@@ -385,47 +414,55 @@ __device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_
   };
   while (alive && reader.next_one(it, a)) {
     const int n = it.t1 - it.t0;
-    if constexpr (C::kG == 2) {
-      const bool two = it.rows > kTile;
+    if (C::kG == 2 && it.rows > kTile) {
+      // two row tiles take turns
       for (int j = -1; j < n && alive; ++j) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          if (g && !two) break;
-          const bool last = g || !two;  // the units' last reader
           uint32_t& seq = g ? seq1 : seq0;
           uint32_t& qn = g ? qn1 : qn0;
+          uint32_t& on = g ? on1 : on0;
           if (j >= 0) {
-            if (j == 0 && !wait(sh->o_free + g, (qn - 1) ^ 1u)) break;  // the last segment's O is read
-            pv(g, g, t + j, seq, j == 0, last);
+            if (j == 0 && !wait(sh->o_free + g, on++ ^ 1u)) break;  // the last segment's O is read
+            pv(g, g, t + j, seq, j == 0, g == 1);
             if (!alive) break;
             ++seq;
           }
           if (j + 1 < n) {
-            if (j + 1 == 0) {
-              if (!wait(sh->q_full + g, qn)) break;
-              ++qn;
-            }
-            qk(g, g, t + j + 1, last);
+            if (j + 1 == 0 && !wait(sh->q_full + g, qn++)) break;
+            qk(g, g, t + j + 1, g == 1);
             if (!alive) break;
             if (j + 2 == n) mma_commit(sh->q_empty + g);
           }
         }
       }
     } else {
-      if (!wait(sh->q_full, qn0)) break;
-      ++qn0;
-      qk(0, seq0 & 1u, t, true);
-      if (alive && n > 1) qk(0, (seq0 + 1) & 1u, t + 1, true);
+      // One row tile, S one key tile ahead of P. With kG = 2 the key tiles take turns
+      // between both softmax warpgroups and two O, which the first adds up at the end;
+      // with kG = 1 between two S of the one warpgroup.
+      auto buf = [&](int j) { return C::kG == 2 ? static_cast<uint32_t>(j & 1) : (seq0 + j) & 1u; };
+      const uint32_t s0 = seq0, s1 = seq1;
+      const uint32_t b0 = buf(0), b1 = buf(1);
+      if (!wait(sh->q_full, qn0++)) break;
+      qk(0, b0, t, true);
+      if (alive && n > 1) qk(0, b1, t + 1, true);
       if (alive && n <= 2) mma_commit(sh->q_empty);
       for (int j = 0; j < n && alive; ++j) {
-        if (j == 0 && !wait(sh->o_free, (qn0 - 1) ^ 1u)) break;
-        pv(0, seq0 & 1u, t + j, seq0 >> 1, j == 0, true);
-        if (!alive) break;
-        ++seq0;
-        if (j + 2 < n) {
-          qk(0, (seq0 + 1) & 1u, t + j + 2, true);
+        const uint32_t b = j & 1 ? b1 : b0;
+        const int g = C::kG == 2 ? j & 1 : 0;
+        if (j <= g && !wait(sh->o_free + g, (g ? on1++ : on0++) ^ 1u)) break;
+        const uint32_t parity = C::kG == 2 ? (g ? s1 : s0) + (j >> 1) : (s0 + j) >> 1;
+        pv(g, b, t + j, parity, j <= g, true);
+        if (alive && j + 2 < n) {
+          qk(0, b, t + j + 2, true);
           if (j + 3 == n) mma_commit(sh->q_empty);
         }
+      }
+      if constexpr (C::kG == 2) {
+        seq0 += (n + 1) >> 1;
+        seq1 += n >> 1;
+      } else {
+        seq0 += n;
       }
     }
     t += n;
@@ -575,96 +612,128 @@ __device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint
 }
 
 // --------------------------------------------------------------- the work list
-template <int kRows>
-__device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh) {
-  const int lane = threadIdx.x & 31;
-  // a group, its units, and where its prefix's pages stand: in front of the own ones of
-  // its first request that has some (nearly always its first one)
-  auto look = [&](int g, Group& r, int& table) -> int64_t {
+// The first 32 groups, a group a lane, and where each one's prefix stands in page_table: in
+// front of the own pages of its first request that has some (nearly always its first).
+template <int kG>
+struct Look {
+  Group r = {};
+  Work<kG> w;
+  int table = -1;
+  __device__ __forceinline__ void at(const SharedArgs& a, int g) {
     r = {};
+    w = Work<kG>();
     table = -1;
-    if (g >= a.groups) return 0;
+    if (g >= a.groups) return;
     r = group_of(a, g);
-    if (!r.bad && r.b1 > r.b0 && __ldg(a.own_len + r.b0) > 0) table = __ldg(a.own_indptr + r.b0);
-    return units_of<kRows>(a, r);
-  };
-  int64_t total = 0, mine = 0, upto = 0;  // units; of this lane's group, and with those in front of it
+    w = Work<kG>(a, r);
+    if (!r.bad && r.b1 > r.b0) {
+      const int own = __ldg(a.own_len + r.b0), page = __ldg(a.own_indptr + r.b0);
+      if (own > 0) table = page;
+    }
+  }
+};
+
+template <int kG>
+__device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<kG> look) {
+  constexpr int kRows = kG * kTile;
+  const int lane = threadIdx.x & 31;
+  int work = 0, items = 0;
+  int lane_work = 0, lane_items = 0;  // in front of this lane's group, among the 32
   uint32_t bits = 0u;
-  Group r;
-  int table, known = -1;  // the 32 groups whose lanes hold `r`
+  int known = 0;  // the 32 groups that `look` holds
+  auto sums = [&](int& w32, int& i32) {
+    const int w = a.hkv * look.w.head(0), i = a.hkv * look.w.blocks;
+    if (a.groups == 1) {
+      lane_work = lane_items = 0;
+      w32 = __shfl_sync(0xffffffffu, w, 0);
+      i32 = __shfl_sync(0xffffffffu, i, 0);
+      return;
+    }
+    const int wx = scan32(w, lane), ix = scan32(i, lane);
+    lane_work = wx - w;
+    lane_items = ix - i;
+    w32 = __shfl_sync(0xffffffffu, wx, 31);
+    i32 = __shfl_sync(0xffffffffu, ix, 31);
+  };
+#pragma unroll 1
   for (int g0 = 0; g0 < a.groups; g0 += 32) {
-    mine = look(g0 + lane, r, table);
-    bits |= r.bad;
-    known = g0 >> 5;
-    upto = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
+    if (g0) {
+      known = g0 >> 5;
+      look.at(a, g0 + lane);
     }
-    if (lane == 0) sh->coarse[known] = total;
-    if (blockIdx.x == 0 && g0 + lane < a.groups) a.first[1 + g0 + lane] = total + upto - mine;
-    total += __shfl_sync(0xffffffffu, upto, 31);
-  }
-  __syncwarp();
-  const int64_t per = units_of_cta(total, a.ctas);
-  if (blockIdx.x == 0) {
-    bits = __reduce_or_sync(0xffffffffu, bits);
+    bits |= look.r.bad;
+    int w32, i32;
+    sums(w32, i32);
     if (lane == 0) {
-      a.first[0] = per;
-      if (bits) atomicOr(a.status, bits);
+      sh->coarse[known] = work;
+      sh->coarse_items[known] = items;
     }
+    work += w32;
+    items += i32;
   }
-  int64_t pos = blockIdx.x * per;
-  const int64_t stop = min(total, pos + per);
+  int per, pay;
+  cut_of(work, items, a.ctas, per, pay);
+  __syncwarp();
+  int pos = blockIdx.x * per;  // (a CTA too many stands at most `per` behind the end)
+  const int stop = min(work + pay * items, pos + per);
   uint32_t n = 0;
   for (;;) {
     Item it = {};
     it.head = -1;
-    if (pos < stop) {
+#pragma unroll 1
+    while (pos < stop) {
       int c = 0, top = (a.groups + 31) / 32 - 1;
       while (c < top) {
         const int mid = (c + top + 1) >> 1;
-        if (sh->coarse[mid] <= pos) c = mid;
+        if (sh->coarse[mid] + pay * sh->coarse_items[mid] <= pos) c = mid;
         else top = mid - 1;
       }
       if (c != known) {
         known = c;
-        mine = look(32 * c + lane, r, table);
-        upto = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
-          if (lane >= d) upto += y;
-        }
+        look.at(a, 32 * c + lane);
+        int w32, i32;
+        sums(w32, i32);
       }
-      const int64_t want = pos - sh->coarse[c];
-      const int src = __ffs(__ballot_sync(0xffffffffu, upto > want)) - 1;
-      const int64_t in = want - __shfl_sync(0xffffffffu, upto - mine, src);
-      const int b0 = __shfl_sync(0xffffffffu, r.b0, src), b1 = __shfl_sync(0xffffffffu, r.b1, src);
-      const int rows = __shfl_sync(0xffffffffu, r.rows, src);
-      const int tiles = __shfl_sync(0xffffffffu, r.tiles, src);
-      const int blocks = static_cast<int>((static_cast<int64_t>(rows) * a.group + kRows - 1) / kRows);
-      const int item = static_cast<int>(in / tiles), t = static_cast<int>(in % tiles);
-      it.head = item / blocks;
-      it.row0 = item % blocks * kRows;
-      it.rows = static_cast<int>(min(static_cast<int64_t>(kRows),
-                                     static_cast<int64_t>(rows) * a.group - it.row0));
-      it.q0 = __shfl_sync(0xffffffffu, r.q0, src);
-      it.b0 = b0;
-      it.b1 = b1;
-      it.t0 = __shfl_sync(0xffffffffu, r.tile0, src) + t;
-      it.t1 = it.t0 + static_cast<int>(min(static_cast<int64_t>(tiles - t), stop - pos));
-      it.end = __shfl_sync(0xffffffffu, r.end, src);
-      it.cut = t > 0;
-      it.table = __shfl_sync(0xffffffffu, table, src);
-      for (int b = b0; it.table < 0 && b < b1; b += 32) {
+      const int start = sh->coarse[c] + lane_work + pay * (sh->coarse_items[c] + lane_items);
+      const int head = look.w.head(pay);
+      const int src = __ffs(__ballot_sync(0xffffffffu, start + a.hkv * head > pos)) - 1;
+      auto from = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
+      const int blocks = from(look.w.blocks), tiles = from(look.w.tiles), last = from(look.w.last);
+      const uint32_t head_len = from(head), full = from(look.w.full(pay));
+      uint32_t in = pos - from(start);
+      const int h = in / head_len;
+      in -= h * head_len;
+      const int block = min(static_cast<int>(in / full), blocks - 1);
+      in -= block * full;
+      const uint32_t w = block == blocks - 1 ? last : kFull;
+      // tiles that begin in front of a place of the item
+      auto tiles_to = [&](uint32_t x) {
+        return x <= static_cast<uint32_t>(pay) ? 0 : min(static_cast<int>((x - pay + w - 1) / w), tiles);
+      };
+      const uint32_t to = min(w * tiles + pay, in + (stop - pos));
+      const int t0 = tiles_to(in), t1 = tiles_to(to);
+      pos += to - in;
+      if (t0 == t1) continue;
+      const int rows = from(look.r.rows), tile0 = from(look.r.tile0);
+      it.head = h;
+      it.row0 = block * kRows;
+      it.rows = min(kRows, rows * a.group - it.row0);
+      it.q0 = from(look.r.q0);
+      it.b0 = from(look.r.b0);
+      it.b1 = from(look.r.b1);
+      it.t0 = tile0 + t0;
+      it.t1 = tile0 + t1;
+      it.end = from(look.r.end);
+      it.cut = t0 > 0;
+      it.table = from(look.table);
+#pragma unroll 1
+      for (int b = it.b0; it.table < 0 && b < it.b1; b += 32) {
         const uint32_t has =
-            __ballot_sync(0xffffffffu, b + lane < b1 && __ldg(a.own_len + min(b + lane, b1 - 1)) > 0);
+            __ballot_sync(0xffffffffu, b + lane < it.b1 && __ldg(a.own_len + min(b + lane, it.b1 - 1)) > 0);
         if (has) it.table = __ldg(a.own_indptr + b + __ffs(has) - 1);
       }
       it.table -= it.end / a.page_size;
-      pos += it.t1 - it.t0;
+      break;
     }
     const uint32_t slot = n % kItems;
     bool ok = true;
@@ -678,101 +747,133 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh) {
     ++n;
     if (it.head < 0) break;
   }
+  // the first CTA says what is wrong with groups, and writes the cut down for the join
+  // where the groups are too many for its lanes
+  if (blockIdx.x) return;
+  bits = __reduce_or_sync(0xffffffffu, bits);
+  if (lane == 0) {
+    a.first[0] = per;
+    a.first[1] = pay;
+    if (bits) atomicOr(a.status, bits);
+  }
+  if (a.groups <= 32) return;
+#pragma unroll 1
+  for (int g0 = 0; g0 < a.groups; g0 += 32) {
+    look.at(a, g0 + lane);
+    int w32, i32;
+    sums(w32, i32);
+    if (g0 + lane < a.groups)
+      a.first[2 + g0 + lane] = sh->coarse[g0 >> 5] + lane_work + pay * (sh->coarse_items[g0 >> 5] + lane_items);
+  }
 }
 
 // ------------------------------------------------------------------ softmax
 
-// Packed row m of a group: row m / group of its rows, head m % group of the kv head.
-// Its query into 128-byte-swizzled units of a row tile, in the operands' type; returns
-// the power of two taken out of it.
+// The queries of a warp's 32 rows into 128-byte-swizzled units of a row tile, in the
+// operands' type; returns the power of two taken out of this lane's row. `at` is its
+// element in q, or -1: zeros. Neighbouring lanes take a row's neighbouring 16 bytes. The
+// loops are kept short: this runs once a segment, and instructions that are not in the
+// SM's cache cost more than their execution (head_dim 256, 16 steps unrolled: 4.5 us).
 template <class C, int D, bool k8>
-__device__ __forceinline__ float load_query(const SharedArgs& a, const Item& it, uint8_t* q_s, int r, int m) {
-  const bool live = m < it.row0 + it.rows;
-  const int64_t row = static_cast<int64_t>(it.q0) + (live ? m / a.group : 0);
-  const int head = it.head * a.group + (live ? m % a.group : 0);
-  const int64_t at = (row * a.hq + head) * D;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ float load_query(const SharedArgs& a, uint8_t* q_s, int row0, int64_t at) {
+  const int lane = threadIdx.x & 31;
   if constexpr (!k8) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-#pragma unroll 8
-    for (int c = 0; c < D / 8; ++c)
-      *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) = live ? __ldg(src + c) : zero;
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // of a row; rows
+    const int c = lane % kLanes;
+    const uint32_t dst = su32(q_s) + (c >> 3) * kUnit;
+#pragma unroll 4
+    for (int s = 0; s < 32 / kAtOnce; ++s) {
+      const int r = s * kAtOnce + lane / kLanes;
+      const int64_t from = __shfl_sync(0xffffffffu, at, r);
+      // (no bytes to read: zeros)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + sw128(row0 + r, (c & 7) * 16)),
+                   "l"(static_cast<const __nv_bfloat16*>(a.q) + max(from, static_cast<int64_t>(0)) + c * 8),
+                   "r"(from >= 0 ? 16 : 0)
+                   : "memory");
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     return 1.f;
   } else {
+    float up = 1.f;
+    auto load = [&](auto&& use, int bytes_shift, auto lanes_c) {
+      constexpr int kLanes = decltype(lanes_c)::value;  // of a row
+      constexpr int kAtOnce = 32 / kLanes;              // rows
+      constexpr int kSteps = 32 / kAtOnce, kBatch = kSteps < 8 ? kSteps : 8;
+      const int chunk = lane % kLanes;
+#pragma unroll 1
+      for (int s0 = 0; s0 < kSteps; s0 += kBatch) {
+        uint4 v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int64_t from = __shfl_sync(0xffffffffu, at, (s0 + k) * kAtOnce + lane / kLanes);
+          v[k] = make_uint4(0, 0, 0, 0);
+          if (from >= 0)
+            v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + (from << bytes_shift)) + chunk);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const float u = use(v[k], row0 + (s0 + k) * kAtOnce + lane / kLanes, chunk);
+          const float mine = __shfl_sync(0xffffffffu, u, lane % kAtOnce * kLanes);
+          if (lane / kAtOnce == s0 + k) up = mine;
+        }
+      }
+    };
     if (a.q8) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.q) + at);
-#pragma unroll 4
-      for (int c = 0; c < D / 16; ++c) {
-        const uint4 w = live ? __ldg(src + c) : zero;
+      load([&](uint4 v, int r, int c) {
         if constexpr (C::kDirect) {
-          *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) = w;
+          *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) = v;
         } else {
           uint8_t* dst = q_s + (c >> 2) * kUnit;
-          *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32)) = widen8(w.x, w.y, false);
-          *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32 + 16)) = widen8(w.z, w.w, false);
+          *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32)) = widen8(v.x, v.y, false);
+          *reinterpret_cast<uint4*>(dst + sw128(r, (c & 3) * 32 + 16)) = widen8(v.z, v.w, false);
         }
-      }
-      return 1.f;
+        return 1.f;
+      }, 0, std::integral_constant<int, D / 16>());
+      return up;
     }
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at);
-    uint32_t top = 0u;  // largest magnitude's bits
-#pragma unroll 8
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 w = live ? __ldg(src + c) : zero;
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    load([&](uint4 q, int r, int c) {
+      const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+      uint32_t top = 0u;  // largest magnitude's bits, of the row
 #pragma unroll
       for (int e = 0; e < 4; ++e) top = max(top, max(v[e] << 16 & 0x7FFF0000u, v[e] & 0x7FFF0000u));
-    }
-    int ex = static_cast<int>(top >> 23) - 127;
-    if constexpr (C::kDirect) {
-      // to [224, 448): 1.75 x 2^8 is E4M3's largest
-      ex += (top & 0x7FFFFFu) <= 0x600000u ? -8 : -7;
-      if (top == 0u || top >= 0x7F800000u) ex = 0;
-    } else if (top == 0u || ex == 128 || (ex >= -6 && ex < 12)) {
-      ex = 0;  // 2^-6 <= largest < 2^12: as it is; NaN and infinity too
-    }
-    ex = max(-126, min(126, ex));
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-    if constexpr (C::kDirect) {
-#pragma unroll 4
-      for (int c = 0; c < D / 16; ++c) {
-        uint32_t t1[4], t2[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 w = live ? __ldg(src + 2 * c + h) : zero;
-          const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x0 = __uint_as_float(v[e] << 16) * down, x1 = __uint_as_float(v[e] & 0xFFFF0000u) * down;
-            const uint16_t c1 = e4m3x2(x0, x1);
-            const float2 back = e4m3x2_to_f2(c1);
-            const uint16_t c2 = e4m3x2(x0 - back.x, x1 - back.y);
-            const int k = h * 2 + (e >> 1);
-            t1[k] = e & 1 ? t1[k] | static_cast<uint32_t>(c1) << 16 : c1;
-            t2[k] = e & 1 ? t2[k] | static_cast<uint32_t>(c2) << 16 : c2;
-          }
-        }
-        uint8_t* dst = q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16);
-        *reinterpret_cast<uint4*>(dst) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-        *reinterpret_cast<uint4*>(dst + C::kUK * kUnit) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+      for (int d = 1; d < D / 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+      int ex = static_cast<int>(top >> 23) - 127;
+      if constexpr (C::kDirect) {
+        // to [224, 448): 1.75 x 2^8 is E4M3's largest
+        ex += (top & 0x7FFFFFu) <= 0x600000u ? -8 : -7;
+        if (top == 0u || top >= 0x7F800000u) ex = 0;
+      } else if (top == 0u || ex == 128 || (ex >= -6 && ex < 12)) {
+        ex = 0;  // 2^-6 <= largest < 2^12: as it is; NaN and infinity too
       }
-    } else {
-#pragma unroll 8
-      for (int c = 0; c < D / 8; ++c) {
-        const uint4 w = live ? __ldg(src + c) : zero;
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-        uint32_t h[4];
+      ex = max(-126, min(126, ex));
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+      uint32_t w[4], w2[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __half2 p = __floats2half2_rn(__uint_as_float(v[e] << 16) * down,
-                                              __uint_as_float(v[e] & 0xFFFF0000u) * down);
-          h[e] = *reinterpret_cast<const uint32_t*>(&p);
+      for (int e = 0; e < 4; ++e) {
+        const float x0 = __uint_as_float(v[e] << 16) * down, x1 = __uint_as_float(v[e] & 0xFFFF0000u) * down;
+        if constexpr (C::kDirect) {
+          const uint32_t c1 = e4m3x2(x0, x1);
+          const float2 back = e4m3x2_to_f2(static_cast<uint16_t>(c1));
+          const uint32_t c2 = e4m3x2(x0 - back.x, x1 - back.y);
+          w[e >> 1] = e & 1 ? w[e >> 1] | c1 << 16 : c1;
+          w2[e >> 1] = e & 1 ? w2[e >> 1] | c2 << 16 : c2;
+        } else {
+          const __half2 p = __floats2half2_rn(x0, x1);
+          w[e] = *reinterpret_cast<const uint32_t*>(&p);
         }
+      }
+      if constexpr (C::kDirect) {
+        uint8_t* dst = q_s + (c >> 4) * kUnit + sw128(r, (c & 15) * 8);
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(dst + C::kUK * kUnit) = make_uint2(w2[0], w2[1]);
+      } else {
         *reinterpret_cast<uint4*>(q_s + (c >> 3) * kUnit + sw128(r, (c & 7) * 16)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
+            make_uint4(w[0], w[1], w[2], w[3]);
       }
-    }
-    return __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+      return __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+    }, 1, std::integral_constant<int, D / 8>());
+    return up;
   }
 }
 
@@ -806,7 +907,7 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
   const float sign = kTok ? 1.f : logit < 0.f ? -1.f : logit == 0.f ? 0.f : 1.f;
   ItemReader reader(sh);
   Item it{};
-  uint32_t n = 0, qn = 0, sc = 0;  // key tiles, segments of this row tile; tiles of scales
+  uint32_t n = 0, qn = 0, sc = 0, odds = 0;  // key tiles, queries, tiles of scales, odd tiles added
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = bar_wait(bar, parity & 1u, abort_flag, a);
     return __all_sync(0xffffffffu, ok);
@@ -814,8 +915,12 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
   auto buf = [&](uint32_t k) { return C::kG == 2 ? g : static_cast<int>(k & 1u); };
   auto par = [&](uint32_t k) { return C::kG == 2 ? k : k >> 1; };
   while (reader.next_warp(it, a)) {
-    const int tile_rows = min(kTile, it.rows - g * kTile);
-    if (tile_rows <= 0) {
+    // the key tiles in turns with the other warpgroup, or this one's row tile on all
+    const bool turns = C::kG == 2 && it.rows <= kTile;
+    const int rt = turns ? 0 : g;
+    const int tile_rows = min(kTile, it.rows - rt * kTile);
+    const int j0 = it.t0 + (turns ? g : 0);  // first key tile of this warpgroup
+    if (j0 >= it.t1) {
       if constexpr (kTok) {  // the tiles' scales are let go all the same
         for (int j = it.t0; j < it.t1; ++j, ++sc) {
           if (!wait(sh->sc_full + sc % kScales, sc / kScales)) return;
@@ -824,15 +929,22 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
       }
       continue;
     }
-    const int m0 = it.row0 + g * kTile + r;
-    if (!wait(sh->q_empty + g, qn ^ 1u)) return;
-    const float up = load_query<C, D, k8>(a, it, q_s + g * C::kQTile, r, m0);
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) bar_arrive(sh->q_full + g);
-    ++qn;
-    float scale = 1.f;
-    if constexpr (!kTok) scale = (sign != 0.f ? fabsf(logit) : 1.f) * up;
+    const int m0 = it.row0 + rt * kTile + r;
+    float up = 1.f;
+    if (rt == g) {
+      int64_t at = -1;
+      if (r < tile_rows)
+        at = ((static_cast<int64_t>(it.q0) + m0 / a.group) * a.hq + it.head * a.group + m0 % a.group) * D;
+      if (!wait(sh->q_empty + g, qn ^ 1u)) return;
+      up = load_query<C, D, k8>(a, q_s + g * C::kQTile, quad * 32, at);
+      if (turns) sh->rows[r].x = up;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(sh->q_full + g);
+      ++qn;
+    }
+    const float plain = sign != 0.f ? fabsf(logit) : 1.f;
+    float scale = kTok ? 1.f : plain * up;
     // first key this row sees
     int first = 0;
     if (a.window && r < tile_rows) {
@@ -847,7 +959,14 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
       if (w > 0) first = max(0, __ldg(a.kv_len + b) - (__ldg(a.qo_indptr + b + 1) - row) - w + 1);
     }
     float m = kMInit, l = 0.f;
-    for (int j = it.t0; j < it.t1; ++j, ++n, ++sc) {
+    for (int j = it.t0; j < it.t1; ++j, ++sc) {
+      if (turns && ((j - it.t0) & 1) != g) {
+        if constexpr (kTok) {
+          if (!wait(sh->sc_full + sc % kScales, sc / kScales)) return;
+          if (lane == 0) bar_arrive(sh->sc_empty + sc % kScales);
+        }
+        continue;
+      }
       const int b = buf(n);
       const uint32_t t_s = tmem + lanes + b * kKeys;
       const float* sp = scales + sc % kScales * 3 * kKeys;
@@ -855,6 +974,10 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
         if (!wait(sh->sc_full + sc % kScales, sc / kScales)) return;
       if (!wait(sh->s_full + b, par(n))) return;
       fence_after();
+      if (rt != g && j == j0) {  // (the query is there)
+        up = sh->rows[r].x;
+        if constexpr (!kTok) scale = plain * up;
+      }
       const int k0 = j * kKeys;
       const bool hide = __any_sync(0xffffffffu, first > k0) || k0 + kKeys > it.end;
       const float *kp = sp, *lp = sp + kKeys;
@@ -917,7 +1040,7 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
         const float f = move ? ex2(m - ms) : 1.f;
         if (move) m = ms;
         l *= f;
-        if (j > it.t0) {  // O holds something: the MMA in front of this one must be done
+        if (j > j0) {  // O holds something: the MMA in front of this one must be done
           if (!wait(sh->o_done + buf(n - 1), par(n - 1))) return;
           fence_after();
 #pragma unroll 1
@@ -971,51 +1094,86 @@ __device__ __forceinline__ void softmax_role(const SharedArgs& a, Shared* sh, ui
         bar_arrive(sh->p_full + b);
         if constexpr (kTok) bar_arrive(sh->sc_empty + sc % kScales);
       }
+      ++n;
     }
     // the rows' partial outputs
     if (!wait(sh->o_done + buf(n - 1), par(n - 1))) return;
     fence_after();
+    const bool odd = turns && it.t1 - it.t0 > 1;  // there are odd tiles' O and sums
+    if (odd && g == 1) {
+      sh->rows[r] = make_float2(m, l);
+      fence_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sh->odd_done);
+      continue;
+    }
+    float f0 = 1.f, f1 = 0.f;
+    if (odd) {
+      if (!wait(&sh->odd_done, odds++)) return;
+      fence_after();
+      const float2 other = sh->rows[r];
+      const float top = fmaxf(m, other.x);
+      f0 = ex2(m - top);
+      f1 = ex2(other.x - top);
+      l = l * f0 + other.y * f1;
+      m = top;
+    }
     const float inv = l > 0.f ? v_final / l : l;  // no key: 0; NaN stays
-    const int64_t at = it.cut ? static_cast<int64_t>(blockIdx.x) * C::kRows + g * kTile
-                              : (it.head * a.rows_cap + it.q0) * a.group + it.row0 + g * kTile;
+    f0 *= inv;
+    f1 *= inv;
+    const int64_t at = it.cut ? static_cast<int64_t>(blockIdx.x) * C::kRows + rt * kTile
+                              : (it.head * a.rows_cap + it.q0) * a.group + it.row0 + rt * kTile;
     float* part = (it.cut ? a.area_o : a.main_o) + at * D;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 16) {
-      uint32_t v[16];
+    for (int c = 0; c < D; c += 32) {
+      uint32_t v[32];
       __syncwarp();
-      tmem_ld16(t_o + c, v);
-      tmem_wait_ld<16>(v);
+      tmem_ld32(t_o + c, v);
+      tmem_wait_ld<32>(v);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * inv);
+      for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f0);
+      if (odd) {
+        uint32_t w[32];
+        tmem_ld32(t_o + D + c, w);
+        tmem_wait_ld<32>(w);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(fmaf(__uint_as_float(w[e]), f1, __uint_as_float(v[e])));
+      }
       // Four lanes exchange 16-byte pieces, so that a store writes 64 bytes of
       // each of eight rows and not 16 of thirty-two.
 #pragma unroll
-      for (int d = 1; d <= 2; d <<= 1) {
-        const bool hi = (lane & d) != 0;
+      for (int half = 0; half < 32; half += 16) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          if (p & d) continue;  // piece p and piece p + d
+        for (int d = 1; d <= 2; d <<= 1) {
+          const bool hi = (lane & d) != 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t& keep = v[p * 4 + e];
-            uint32_t& give = v[(p + d) * 4 + e];
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? keep : give, d);
-            if (hi) keep = got;
-            else give = got;
+          for (int p = 0; p < 4; ++p) {
+            if (p & d) continue;  // piece p and piece p + d
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t& keep = v[half + p * 4 + e];
+              uint32_t& give = v[half + (p + d) * 4 + e];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? keep : give, d);
+              if (hi) keep = got;
+              else give = got;
+            }
           }
         }
-      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int rr = quad * 32 + (lane & ~3) + k;
-        if (rr < tile_rows)
-          *reinterpret_cast<uint4*>(part + static_cast<int64_t>(rr) * D + c + (lane & 3) * 4) =
-              make_uint4(v[k * 4], v[k * 4 + 1], v[k * 4 + 2], v[k * 4 + 3]);
+        for (int k = 0; k < 4; ++k) {
+          const int rr = quad * 32 + (lane & ~3) + k;
+          if (rr < tile_rows)
+            *reinterpret_cast<uint4*>(part + static_cast<int64_t>(rr) * D + c + half + (lane & 3) * 4) =
+                make_uint4(v[half + k * 4], v[half + k * 4 + 1], v[half + k * 4 + 2], v[half + k * 4 + 3]);
+        }
       }
     }
     __syncwarp();
     fence_before();
-    if (lane == 0) bar_arrive(sh->o_free + g);
+    if (lane == 0) {
+      bar_arrive(sh->o_free + g);
+      if (odd) bar_arrive(sh->o_free + 1);
+    }
     if (r < tile_rows) (it.cut ? a.area_x : a.main_x)[at + r] = l == 0.f ? -INFINITY : m + __log2f(l);
   }
 }
@@ -1066,6 +1224,7 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
       bar_init(sh->item_full + u, 1);
       bar_init(sh->item_empty + u, C::kReaders);
     }
+    bar_init(&sh->odd_done, 4);
     bar_init(&sh->drain, 1);
     sh->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1074,6 +1233,8 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
     scales[kScales * 3 * kKeys + tid] = 1.f;
     scales[kScales * 3 * kKeys + kKeys + tid] = 0.f;
   }
+  Look<C::kG> look;
+  if (warp == C::kWorkWarp) look.at(a, tid & 31);  // (under way while the rest is set up)
   if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      su32(&sh->tmem)),
@@ -1103,7 +1264,7 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
   } else if (warp == C::kMmaWarp) {
     if (elect_one()) mma_role<C, D, k8>(a, sh, q_s, rings);
   } else if (warp == C::kWorkWarp) {
-    work_role<C::kRows>(a, sh);
+    work_role<C::kG>(a, sh, look);
   } else if (k8 && warp >= C::kConv0) {
     if constexpr (k8) widen_role<C, D, kI8, kTok>(a, sh, rings, raw, scales);
   } else {
@@ -1126,7 +1287,7 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ SharedArgs a,
                                                    const __grid_constant__ DecodeArgs o) {
-  constexpr int kRows = D <= 128 ? 2 * kTile : kTile;
+  constexpr int kG = D <= 128 ? 2 : 1, kRows = kG * kTile;
   constexpr int kV = D / 32;  // channels of a lane
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -1135,7 +1296,8 @@ __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ Share
   const int i = static_cast<int>(item % per_b) / a.hq, head = static_cast<int>(item % a.hq);
   bool live = b < a.batch;
   int q0 = 0, own = 0, segs = 0;
-  int64_t c0 = 0, m = 0;  // CTA of the item's first segment; packed row
+  int64_t c0 = 0;  // CTA of the item's first segment
+  int m = 0;       // packed row
   Group gr = {};
   int g = 0;
   if (live) {
@@ -1153,32 +1315,33 @@ __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ Share
       else top = mid - 1;
     }
     gr = group_of(a, g);
-    m = static_cast<int64_t>(q0 + i - gr.q0) * a.group + head % a.group;
+    m = (q0 + i - gr.q0) * a.group + head % a.group;
   }
   const int h = head / a.group;
-  int64_t first = 0, per = 0;
+  int first = 0, per = 1, pay = 0;
   if (a.groups <= 32) {  // the work's cut again, a group a lane: no load to wait for
-    const int64_t n = lane < a.groups ? units_of<kRows>(a, group_of(a, lane)) : 0;
-    int64_t upto = n;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, upto, d);
-      if (lane >= d) upto += y;
-    }
-    per = units_of_cta(__shfl_sync(0xffffffffu, upto, 31), a.ctas);
-    first = __shfl_sync(0xffffffffu, upto - n, g);
+    Work<kG> w;
+    if (lane < a.groups) w = Work<kG>(a, group_of(a, lane));
+    const int mine = a.hkv * w.head(0), items = a.hkv * w.blocks;
+    const int work = scan32(mine, lane), upto = scan32(items, lane);
+    cut_of(__shfl_sync(0xffffffffu, work, 31), __shfl_sync(0xffffffffu, upto, 31), a.ctas, per, pay);
+    first = __shfl_sync(0xffffffffu, work - mine + pay * (upto - items), g);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!live) return;
   if (a.groups > 32) {
     per = a.first[0];
-    first = a.first[1 + g];
+    pay = a.first[1];
+    first = a.first[2 + g];
   }
-  const int block = static_cast<int>(m / kRows), r = static_cast<int>(m % kRows);
+  const int block = m / kRows, r = m % kRows;
   if (gr.tiles > 0) {
-    const int64_t u = first + (static_cast<int64_t>(h) * blocks_of<kRows>(a, gr) + block) * gr.tiles;
+    const Work<kG> w(a, gr);
+    const int count = block == w.blocks - 1 ? w.last : kFull;
+    // its first and its last tile
+    const int u = first + h * w.head(pay) + block * w.full(pay) + pay;
     c0 = u / per;
-    segs = static_cast<int>((u + gr.tiles - 1) / per - c0) + 1;
+    segs = (u + (gr.tiles - 1) * count) / per - static_cast<int>(c0) + 1;
   }
   const int64_t head_row = (h * a.rows_cap + gr.q0) * a.group + m;  // in main
   const int64_t own_row = static_cast<int64_t>(q0 + i) * a.hq + head, own_step = o.rows_cap * a.hq;
@@ -1491,6 +1654,12 @@ extern "C" int pda_shared_plan(const pda_plan_t* plan, int32_t groups, int32_t m
   sp.max_kv_len = plan->max_kv_len;
   const int64_t d = plan->head_dim, rows = d <= 128 ? 2 * kTile : kTile;
   const int64_t cells = sp.own.rows_cap * plan->num_qo_heads;
+  // all tiles of all items, what they count and `pay` for each stay in 31 bits
+  const int64_t blocks = sp.own.rows_cap * plan->group / rows + groups;
+  const int64_t tiles = plan->max_kv_len / kKeys + 2;
+  if (sp.own.rows_cap * plan->group > INT_MAX ||
+      static_cast<double>(blocks) * plan->num_kv_heads * (kFull * static_cast<double>(tiles) + kPay) > 2.0e9)
+    return PDA_ERR_INVALID;
   const int64_t area = static_cast<int64_t>(plan->num_sms) * rows;
   int64_t at = kStatusHeaderBytes;
   auto take = [&](int64_t bytes) {
@@ -1500,7 +1669,7 @@ extern "C" int pda_shared_plan(const pda_plan_t* plan, int32_t groups, int32_t m
   };
   sp.own.scratch_lse_offset = take(sp.own.max_splits * cells * 4);
   sp.own.scratch_o_offset = take(sp.own.max_splits * cells * d * 4);
-  sp.first_offset = take((1 + static_cast<int64_t>(groups)) * 8);
+  sp.first_offset = take((2 + static_cast<int64_t>(groups)) * 4);
   sp.main_lse_offset = take(cells * 4);
   sp.main_o_offset = take(cells * d * 4);
   sp.area_lse_offset = take(area * 4);
@@ -1584,7 +1753,7 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
   a.main_o = reinterpret_cast<float*>(base + sp->main_o_offset);
   a.area_x = reinterpret_cast<float*>(base + sp->area_lse_offset);
   a.area_o = reinterpret_cast<float*>(base + sp->area_o_offset);
-  a.first = reinterpret_cast<int64_t*>(base + sp->first_offset);
+  a.first = reinterpret_cast<int*>(base + sp->first_offset);
   a.status = o.status;
   a.wait_limit_ns = o.wait_limit_ns;
   a.sm_scale = sm_scale;
@@ -1600,6 +1769,7 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
   a.q8 = plan->q_dtype == PDA_E4M3;
   a.inject = o.inject;
   a.ctas = plan->num_sms;
+  a.one = plan->head_dim == 256 ? kFull : plan->kv_dtype != PDA_BF16 || plan->head_dim == 64 ? 5 : 7;
   const Kernel k = kernel_for(*plan);
   CUtensorMap tk, tv;
   const bool wide = plan->kv_dtype == PDA_BF16;
