@@ -25,7 +25,7 @@ LIB = os.path.join(LIBDIR, "libpda.so")
 
 SOURCES = ["pda_plan.cpp", "pda_mma.cu", "pda_tc.cu", "pda_noalloc.cu", "pda_append.cu",
            "pda_tables.cu", "pda_mla.cu", "pda_prefill.cu", "pda_pages.cu",
-           "pda_shared.cu"]
+           "pda_shared.cu", "pda_own.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,560 @@
+// pda_own.cu -- the requests' own tokens behind a shared prefix, and the join with what the
+// prefix kernel left of the prefix. Few own tokens a request have a kernel here (more go
+// through stage 1 of pda_decode); it joins its rows itself, or leaves that to a kernel
+// of its own where a row has many parts and few CTAs would have to read them.
+//
+// Mathematics: see pda_shared.cu; the own tokens are ordinary causal (and windowed)
+// attention of R rows x the heads of a GQA group, 16 of them a CTA. out = (sum_s 2^(x_s - X)
+// o_s + 2^(m - X) O) / (sum_s 2^(x_s - X) + 2^(m - X) l) over the prefix's segments s, with
+// (m, l, O) the own tokens' maximum, sum and unnormalised output.
+//
+// Bound: latency, then HBM. Own contexts are short (a few hundred tokens), and stage 1
+// takes 8.7 us for a CTA with 16 or 256 of them, two CTAs an SM: 17 us of 64 requests with 8
+// kv heads. So here nothing goes through shared memory on its way to the tensor
+// cores: a warp takes 16 tokens at a time into mma.sync fragments straight from the
+// cache. Which channel a lane's fragment element stands for is free, as long as Q (for
+// S, a sum over channels) and O (whose columns are channels) agree, so a lane holds 16
+// neighbouring bytes of a token. Three CTAs of four warps an SM keep 96 KB in flight.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "pda.h"
+#include "pda_cvt.cuh"
+#include "pda_internal.h"
+#include "pda_shared.cuh"
+
+namespace pda {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kRows = 16;          // packed rows (query row x head of the group) of a CTA
+constexpr int kStep = 16;          // tokens of a warp's step
+constexpr int kMaxTiles = 4;       // most row tiles of a request: each reads its tokens again
+constexpr int kMaxTokens = 1024;   // most own tokens: four warps share them
+// Parts of a row from which on the join has a kernel of its own, with kJoinWarps warps a row:
+// 12 requests, 2 kv heads (76 parts a row): 86 us in the own tokens' kernel.
+constexpr int kManyParts = 24, kJoinWarps = 4;
+
+template <int D, bool k8>
+struct Cfg {
+  static constexpr int kPieces = D * (k8 ? 1 : 2) / 64;    // 16-byte pieces of a K row a lane has
+  static constexpr int kVCh = k8 && D >= 128 ? 16 : 8;     // channels of a lane's piece of a V row
+  static constexpr int kSets = D / (8 * kVCh);             // such pieces
+  static constexpr int kStride = D + 4;                    // floats of a row of O in shared memory
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kOBytes = kWarps * kRows * kStride * 4;
+  static constexpr int kSmem = kQBytes + kOBytes + kWarps * kRows * 8 + kRows * 4;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// d += a b, 16 x 8 x 16.
+template <bool kF16>
+__device__ __forceinline__ void mma16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (kF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, bool high) {
+  return __byte_perm(x, y, high ? 0x7632 : 0x5410);
+}
+
+template <int D, bool k8, bool kI8, bool kTok>
+__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) own_join(const __grid_constant__ SharedArgs a,
+                                                     const __grid_constant__ DecodeArgs o) {
+  using C = Cfg<D, k8>;
+  constexpr int kG = D <= 128 ? 2 : 1;
+  constexpr int eb = k8 ? 1 : 2;
+  extern __shared__ __align__(16) uint8_t smem[];
+  uint8_t* q_s = smem;  // [16][D] in 16 bits, a row's 16-byte pieces XORed with its low bits
+  float* o_s = reinterpret_cast<float*>(smem + C::kQBytes);  // [warp][16][kStride]
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::kQBytes + C::kOBytes);  // [warp][16]
+  float* up_s = reinterpret_cast<float*>(ml_s + kWarps * kRows);  // a row's power of two
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
+  const int b = blockIdx.x / a.hkv, h = blockIdx.x % a.hkv;
+  const int q0 = __ldg(a.qo_indptr + b), R = __ldg(a.qo_indptr + b + 1) - q0;
+  const int L = __ldg(a.own_len + b), own = __ldg(a.own_indptr + b);
+  const int W = a.window ? __ldg(a.window + b) : 0;
+  const int m0 = blockIdx.y * kRows, M = R * a.group;
+  if (R <= 0 || R > o.max_q_len || L < R || L > o.max_kv_len || q0 < 0 || q0 + R > a.rows_cap || m0 >= M) {
+    if (tid == 0 && h == 0 && blockIdx.y == 0) {
+      uint32_t bits = 0u;
+      if (R < 0 || R > o.max_q_len) bits = PDA_STATUS_ROWS_GT_MAX;
+      else if (R > 0 && L < R) bits = PDA_STATUS_KV_LEN_LT_ROWS;
+      else if (R > 0 && L > o.max_kv_len) bits = PDA_STATUS_KV_LEN_GT_MAX;
+      else if (R > 0 && q0 + R > a.rows_cap) bits = PDA_STATUS_ROWS_GT_CAP;
+      // (share_tables has said what is wrong where it left a request out)
+      if (bits && L != -1) atomicOr(a.status, bits);
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+
+  // ---- the queries: eight lanes a row, 16 bits a channel
+  {
+    const int r = tid >> 3, m = m0 + r;
+    const bool live = m < M;
+    const int64_t at = ((static_cast<int64_t>(q0) + (live ? m / a.group : 0)) * a.hq + h * a.group +
+                        (live ? m % a.group : 0)) * D;
+    constexpr int kEach = D / 64;  // 16-byte pieces a lane writes
+    const int p0 = tid & 7;
+    uint4 v[kEach];
+    float up = 1.f;
+    if (k8 && a.q8) {
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        uint2 c = make_uint2(0, 0);
+        if (live)
+          c = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.q) + at) + p0 + 8 * k);
+        widen4(c.x, v[k].x, v[k].y, false);
+        widen4(c.y, v[k].z, v[k].w, false);
+      }
+    } else {
+      uint32_t top = 0u;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        v[k] = make_uint4(0, 0, 0, 0);
+        if (live)
+          v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + at) + p0 + 8 * k);
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = max(top, max(w[e] << 16 & 0x7FFF0000u, w[e] & 0x7FFF0000u));
+      }
+      if constexpr (k8) {
+        // f16 operands: a row whose largest element is not in [2^-6, 2^12) without its
+        // power of two
+#pragma unroll
+        for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        int ex = static_cast<int>(top >> 23) - 127;
+        if (top == 0u || ex == 128 || (ex >= -6 && ex < 12)) ex = 0;
+        ex = max(-126, min(126, ex));
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+        up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+          uint32_t* w = &v[k].x;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            w[e] = f16x2(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xFFFF0000u) * down);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k)
+      *reinterpret_cast<uint4*>(q_s + r * (D * 2) + (((p0 + 8 * k) ^ (r & 7)) << 4)) = v[k];
+    if (p0 == 0) up_s[r] = up;
+  }
+  __syncthreads();
+
+  // ---- a warp's steps of 16 tokens
+  float logit = a.sm_scale * kLog2e, v_final = 1.f;
+  if (k8 && !kTok) {
+    logit *= __ldg(a.k_scale);
+    v_final = __ldg(a.v_scale);
+  }
+  // rows g and g + 8 of the tile: what they see
+  int last[2], lo[2];
+  float scale[2], m_[2] = {kMInit, kMInit}, l_[2] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int m = m0 + g + 8 * k;
+    last[k] = m < M ? L - R + m / a.group : -1;
+    lo[k] = W > 0 ? last[k] - min(W, L) + 1 : 0;  // (L of L tokens is all of them)
+    scale[k] = logit * up_s[g + 8 * k];
+  }
+  const int from = W > 0 ? max(0, L - R - min(W, L) + 1) / kStep : 0;
+  const int steps = (L + kStep - 1) / kStep;
+  const int P = a.page_size, shift = 31 - __clz(P);
+  const int32_t* pages = a.page_table + own;
+  const uint8_t* k_base = static_cast<const uint8_t*>(o.k) + static_cast<int64_t>(h) * o.sh * eb;
+  const uint8_t* v_base = static_cast<const uint8_t*>(o.v) + static_cast<int64_t>(h) * o.sh * eb;
+  const int n_pages = (L + P - 1) >> shift;
+  // the pages of a step's first and last eight tokens
+  auto page_at = [&](int t) { return t >> shift < n_pages ? __ldg(pages + (t >> shift)) : -1; };
+  float acc[D / 8][4];
+#pragma unroll
+  for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+  int s = from + warp;
+  int pg[2] = {-1, -1};
+  if (s < steps) {
+    pg[0] = page_at(s * kStep);
+    pg[1] = page_at(s * kStep + 8);
+  }
+  bool oob = false;
+#pragma unroll 1
+  for (; s < steps; s += kWarps) {
+    const int t0 = s * kStep;
+    // bytes of each half's first token, or -1
+    int64_t at[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = t0 + 8 * e;
+      const bool ok = pg[e] >= 0 && pg[e] < a.num_pages;
+      oob |= !ok && t < L;
+      at[e] = ok ? (pg[e] * o.sp + (t & (P - 1)) * o.st) * eb : -1;
+    }
+    const int held[2] = {pg[0], pg[1]};
+    pg[0] = page_at(t0 + kWarps * kStep);
+    pg[1] = page_at(t0 + kWarps * kStep + 8);
+    // K: token g of each half, 16-byte pieces q, q + 4, ... of its row
+    uint4 kv[2][C::kPieces];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < C::kPieces; ++i) {
+        kv[e][i] = make_uint4(0, 0, 0, 0);
+        if (at[e] >= 0 && t0 + 8 * e + g < L)
+          kv[e][i] = __ldg(reinterpret_cast<const uint4*>(k_base + at[e] + g * o.st * eb) + q + 4 * i);
+      }
+    // V: tokens 2q and 2q + 1 of each half, the g-th piece of each set of channels
+    constexpr int kVWords = C::kVCh * eb / 4;
+    uint32_t vv[C::kSets][4][kVWords];
+    auto load_v = [&](int set) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int half = e >> 1, t = t0 + 8 * half + 2 * q + (e & 1);
+#pragma unroll
+        for (int w = 0; w < kVWords; ++w) vv[set][e][w] = 0u;
+        if (at[half] >= 0 && t < L) {
+          const uint8_t* src = v_base + at[half] + (2 * q + (e & 1)) * o.st * eb + (set * 8 + g) * (C::kVCh * eb);
+          if constexpr (kVWords == 4) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
+            vv[set][e][0] = x.x;
+            vv[set][e][1] = x.y;
+            vv[set][e][2] = x.z;
+            vv[set][e][3] = x.w;
+          } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
+            vv[set][e][0] = x.x;
+            vv[set][e][1] = x.y;
+          }
+        }
+      }
+    };
+    // (as many sets as fit the registers beside K and O)
+    constexpr int kEarly = D == 256 && !k8 ? 0 : C::kSets;
+#pragma unroll
+    for (int set = 0; set < kEarly; ++set) load_v(set);
+    float ks[2][2], vs[2][2];  // of tokens 2q, 2q + 1 of each half
+    if constexpr (kTok) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int t = t0 + 8 * e + 2 * q + c;
+          ks[e][c] = vs[e][c] = 1.f;
+          if (at[e] >= 0 && t < L) {
+            const int64_t x = (static_cast<int64_t>(held[e]) * P + (t & (P - 1))) * a.hkv + h;
+            ks[e][c] = __ldg(a.k_scale + x);
+            const float f = __ldg(a.v_scale + x);
+            vs[e][c] = f > 0.f ? f : 1.f;
+          }
+        }
+    }
+    // S of 16 rows x 2 x 8 tokens
+    float sc[2][4] = {};
+#pragma unroll
+    for (int i = 0; i < C::kPieces; ++i) {
+      if constexpr (k8) {
+        uint32_t qa[8], qb[8];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int piece = (2 * (q + 4 * i) + c) ^ g;
+          const uint4 x = *reinterpret_cast<const uint4*>(q_s + g * (D * 2) + piece * 16);
+          const uint4 y = *reinterpret_cast<const uint4*>(q_s + (g + 8) * (D * 2) + piece * 16);
+          qa[4 * c] = x.x, qa[4 * c + 1] = x.y, qa[4 * c + 2] = x.z, qa[4 * c + 3] = x.w;
+          qb[4 * c] = y.x, qb[4 * c + 1] = y.y, qb[4 * c + 2] = y.z, qb[4 * c + 3] = y.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t w[4] = {kv[e][i].x, kv[e][i].y, kv[e][i].z, kv[e][i].w};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x, y;
+            widen4(w[c], x, y, kI8);
+            mma16<true>(sc[e], qa[2 * c], qb[2 * c], qa[2 * c + 1], qb[2 * c + 1], x, y);
+          }
+        }
+      } else {
+        const int piece = (q + 4 * i) ^ g;
+        const uint4 x = *reinterpret_cast<const uint4*>(q_s + g * (D * 2) + piece * 16);
+        const uint4 y = *reinterpret_cast<const uint4*>(q_s + (g + 8) * (D * 2) + piece * 16);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mma16<false>(sc[e], x.x, y.x, x.y, y.y, kv[e][i].x, kv[e][i].y);
+          mma16<false>(sc[e], x.z, y.z, x.w, y.w, kv[e][i].z, kv[e][i].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int set = kEarly; set < C::kSets; ++set) load_v(set);
+    // logits in log2 units, the rows' maxima, weights
+    uint32_t p[2][2];  // [half][row g, g + 8], two tokens each
+    float f[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float mx = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float& x = sc[e][2 * k + c];
+          const int t = t0 + 8 * e + 2 * q + c;
+          x *= scale[k];
+          if constexpr (kTok) x = fmaf(x, ks[e][c], __log2f(vs[e][c]));
+          if (t > last[k] || t < lo[k]) x = -INFINITY;
+          mx = fmaxf(mx, x);
+        }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const float to = fmaxf(m_[k], mx);
+      f[k] = ex2(m_[k] - to);
+      m_[k] = to;
+      l_[k] *= f[k];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float w0 = ex2(sc[e][2 * k] - to), w1 = ex2(sc[e][2 * k + 1] - to);
+        if constexpr (kTok) l_[k] += w0 / vs[e][0] + w1 / vs[e][1];
+        else l_[k] += w0 + w1;
+        p[e][k] = k8 ? f16x2(w0, w1) : bf16x2(w0, w1);
+      }
+    }
+    if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+      for (int n = 0; n < D / 8; ++n) {
+        acc[n][0] *= f[0];
+        acc[n][1] *= f[0];
+        acc[n][2] *= f[1];
+        acc[n][3] *= f[1];
+      }
+    }
+    // O: column g of n-tile `set kVCh + j` is channel (set 8 + g) kVCh + j
+#pragma unroll
+    for (int set = 0; set < C::kSets; ++set)
+#pragma unroll
+      for (int w = 0; w < kVWords; ++w) {
+        uint32_t x[4][2];  // the word's channels in pairs, of each token
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (k8) {
+            widen4(vv[set][e][w], x[e][0], x[e][1], kI8);
+          } else {
+            x[e][0] = vv[set][e][w];
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < (k8 ? 2 : 1); ++c)
+#pragma unroll
+          for (int hi = 0; hi < 2; ++hi) {
+            const int j = w * (k8 ? 4 : 2) + c * 2 + hi;
+            mma16<k8>(acc[set * C::kVCh + j], p[0][0], p[0][1], p[1][0], p[1][1], pick(x[0][c], x[1][c], hi),
+                      pick(x[2][c], x[3][c], hi));
+          }
+      }
+  }
+  if (oob) atomicOr(a.status, PDA_STATUS_PAGE_OOB);
+  // ---- the warps' parts to shared memory
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    l_[k] += __shfl_xor_sync(0xffffffffu, l_[k], 1);
+    l_[k] += __shfl_xor_sync(0xffffffffu, l_[k], 2);
+    if (q == 0) ml_s[warp * kRows + g + 8 * k] = make_float2(m_[k], l_[k]);
+    float* row = o_s + (warp * kRows + g + 8 * k) * C::kStride;
+#pragma unroll
+    for (int set = 0; set < C::kSets; ++set)
+#pragma unroll
+      for (int j = 0; j < C::kVCh; ++j) {
+        // columns 2q and 2q + 1
+        row[(set * 8 + 2 * q) * C::kVCh + j] = acc[set * C::kVCh + j][2 * k];
+        row[(set * 8 + 2 * q + 1) * C::kVCh + j] = acc[set * C::kVCh + j][2 * k + 1];
+      }
+  }
+  constexpr int kV = D / 32;
+  // ---- a warp's rows: own parts, then the prefix's
+  auto own_parts = [&](Join<kV>& join, int r) {
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) join.raise(ml_s[w * kRows + r].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 ml = ml_s[w * kRows + r];
+      const float f = exp2f(ml.x - join.top);
+      const float* src = o_s + (w * kRows + r) * C::kStride + lane * kV;
+      join.sum = fmaf(f, ml.y, join.sum);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) join.acc[e] = fmaf(f, src[e] * v_final, join.acc[e]);
+    }
+  };
+  if (a.parts_apart) {
+    __syncthreads();
+#pragma unroll 1
+    for (int r = warp; r < kRows && m0 + r < M; r += kWarps) {
+      Join<kV> join;
+      own_parts(join, r);
+      const int64_t at = (static_cast<int64_t>(q0) + (m0 + r) / a.group) * a.hq + h * a.group + (m0 + r) % a.group;
+      join.keep(o.part_lse + at, o.part_o + at * D);
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+  Parts<kG> parts(a, b);
+  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's parts are there
+  parts.late(a);
+#pragma unroll 1
+  for (int r = warp; r < kRows && m0 + r < M; r += kWarps) {
+    const int i = (m0 + r) / a.group, head = h * a.group + (m0 + r) % a.group;
+    Join<kV> join;
+    own_parts(join, r);
+    const RowParts<kG, D> row(a, parts, h, (q0 + i - parts.gr.q0) * a.group + (m0 + r) % a.group);
+    join.template add<(D <= 128 ? 12 : 8)>(row.segs, [&](int s2, const float*& x, const float*& v) { row.part(a, s2, x, v); });
+    join.write(o, (static_cast<int64_t>(q0) + i) * a.hq + head);
+  }
+}
+
+// ------------------------------------------------------------- the join alone
+//
+// S warps per (request, row, head): the prefix's segments in order, then the own tokens'
+// parts; with several warps each takes a share of them in turn. Bound: reading the parts
+// (L2); where they are is worked out while the kernels in front end.
+template <int D, int S>
+__global__ void __launch_bounds__(256) shared_join(const __grid_constant__ SharedArgs a,
+                                                   const __grid_constant__ DecodeArgs o) {
+  constexpr int kG = D <= 128 ? 2 : 1, kV = D / 32;
+  __shared__ float acc_s[S > 1 ? 8 : 1][S > 1 ? D : 1];
+  __shared__ float2 ml[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % S;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * (8 / S) + warp / S;
+  const int64_t per_b = static_cast<int64_t>(o.max_q_len) * a.hq;
+  const int b = static_cast<int>(item / per_b);
+  const int i = static_cast<int>(item % per_b) / a.hq, head = static_cast<int>(item % a.hq), h = head / a.group;
+  bool live = b < a.batch;
+  int q0 = 0, own = 0;
+  if (live) {
+    q0 = __ldg(a.qo_indptr + b);
+    const int R = __ldg(a.qo_indptr + b + 1) - q0;
+    const int L = __ldg(a.own_len + b), W = a.window ? __ldg(a.window + b) : 0;
+    live = i < R && R <= o.max_q_len && L >= R && L <= o.max_kv_len && q0 >= 0 && q0 + R <= a.rows_cap;
+    if (live) own = a.parts_apart ? 1 : split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
+  }
+  Parts<kG> parts(a, live ? b : 0);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (S == 1 && !live) return;
+  Join<kV> join;
+  const int64_t own_row = static_cast<int64_t>(q0 + i) * a.hq + head, own_step = o.rows_cap * a.hq;
+  if (live) {
+    parts.late(a);
+    const RowParts<kG, D> row(a, parts, h, (q0 + i - parts.gr.q0) * a.group + head % a.group);
+    const int all = row.segs + own;
+    join.template add<(D <= 128 ? 16 : 8)>((all - sub + S - 1) / S, [&](int k, const float*& x, const float*& v) {
+      const int s = k * S + sub;
+      if (s < row.segs) return row.part(a, s, x, v);
+      const int64_t at = (s - row.segs) * own_step + own_row;
+      x = o.part_lse + at;
+      v = o.part_o + at * D;
+    });
+  }
+  if constexpr (S > 1) {
+    if (sub) {
+      if (lane == 0) ml[warp] = make_float2(join.top, join.sum);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) acc_s[warp][lane * kV + e] = join.acc[e];
+    }
+    __syncthreads();
+    if (sub || !live) return;
+#pragma unroll 1
+    for (int w = warp + 1; w < warp + S; ++w) {
+      const float2 x = ml[w];
+      join.raise(x.x);
+      const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - join.top);
+      join.sum = fmaf(f, x.y, join.sum);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) join.acc[e] = fmaf(f, acc_s[w][lane * kV + e], join.acc[e]);
+    }
+  }
+  join.write(o, own_row);
+}
+
+using JoinFn = void (*)(SharedArgs, DecodeArgs);
+struct Kernel {
+  JoinFn fn;
+  int smem;
+};
+template <int D>
+Kernel kernel_for(const pda_plan_t* p) {
+  const bool tok = p->scale_mode == PDA_SCALE_TOKEN_HEAD;
+  const int s8 = Cfg<D, true>::kSmem;
+  if (p->kv_dtype == PDA_BF16) return {own_join<D, false, false, false>, Cfg<D, false>::kSmem};
+  if (p->kv_dtype == PDA_INT8) return {tok ? own_join<D, true, true, true> : own_join<D, true, true, false>, s8};
+  return {tok ? own_join<D, true, false, true> : own_join<D, true, false, false>, s8};
+}
+
+int launch(JoinFn fn, dim3 grid, unsigned threads, int smem, const SharedArgs& a, const DecodeArgs& o,
+           cudaStream_t s) {
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           smem) != cudaSuccess) {
+    cudaGetLastError();
+    return PDA_ERR_CUDA;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, fn, a, o) == cudaSuccess) return PDA_OK;
+  cudaGetLastError();
+  return PDA_ERR_CUDA;
+}
+
+}  // namespace
+
+bool own_here(const pda_plan_t* own) {
+  return own->max_q_len * own->group <= kMaxTiles * kRows && own->max_kv_len <= kMaxTokens;
+}
+
+bool parts_apart(const pda_plan_t* own) { return own->num_sms > kManyParts * own->num_kv_heads; }
+
+int launch_own(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, cudaStream_t s) {
+  const Kernel k = own->head_dim == 64    ? kernel_for<64>(own)
+                   : own->head_dim == 128 ? kernel_for<128>(own)
+                                          : kernel_for<256>(own);
+  const dim3 grid(static_cast<unsigned>(a.batch * a.hkv),
+                  static_cast<unsigned>((o.max_q_len * a.group + kRows - 1) / kRows));
+  return launch(k.fn, grid, kThreads, k.smem, a, o, s);
+}
+
+int launch_join(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, cudaStream_t s) {
+  const bool many = parts_apart(own);
+  const int64_t warps = static_cast<int64_t>(a.batch) * o.max_q_len * a.hq * (many ? kJoinWarps : 1);
+  const JoinFn one = own->head_dim == 64    ? shared_join<64, 1>
+                     : own->head_dim == 128 ? shared_join<128, 1>
+                                            : shared_join<256, 1>;
+  const JoinFn four = own->head_dim == 64    ? shared_join<64, kJoinWarps>
+                      : own->head_dim == 128 ? shared_join<128, kJoinWarps>
+                                             : shared_join<256, kJoinWarps>;
+  return launch(many ? four : one, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, 0, a, o, s);
+}
+
+}  // namespace pda

@@ -38,17 +38,13 @@
 #include "pda_cvt.cuh"
 #include "pda_internal.h"
 #include "pda_ptx.cuh"
+#include "pda_shared.cuh"
 
 namespace pda {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kMInit = -3.0e38f;  // before any key: finite, so that ex2(-inf - m) = 0
 constexpr float kTh = 8.0f;         // lazy rescale threshold, log2 units
 
-constexpr int kKeys = 128;     // keys of a tile
-constexpr int kTile = 128;     // rows of a softmax warpgroup
 constexpr int kUnit = 16384;   // bytes of a ring unit
 constexpr int kItems = 3;      // slots of the segment ring
 constexpr int kScales = 4;     // slots of the ring of per-token scales, a tile each
@@ -56,103 +52,6 @@ constexpr int kCoarse = 64;    // prefix entries, 32 groups each
 constexpr int kMaxGroups = 32 * kCoarse;
 constexpr int kTmemCols = 512;
 constexpr int kO = 2 * kKeys;  // first TMEM column of O; two S in front of it
-
-// ------------------------------------------------- the groups and their prefixes
-
-struct SharedArgs {
-  const void* q;
-  const int32_t* page_table;
-  const int32_t* qo_indptr;
-  const int32_t* kv_len;
-  const int32_t* window;
-  const int32_t* group_indptr;  // NULL: one group of all requests
-  const int32_t* prefix;        // [groups][2] tokens
-  const int32_t* own_indptr;
-  const int32_t* own_len;
-  const float* k_scale;
-  const float* v_scale;
-  float* main_o;    // [kv head][row x group][D] fp32: segments that start their item
-  float* main_x;    // ... and their log2 sums
-  float* area_o;    // [CTA][rows of an item][D]: the segment a CTA starts inside an item
-  float* area_x;
-  int* first;       // the cut (per, pay), then [groups] where each group's work starts
-  uint32_t* status;
-  uint64_t wait_limit_ns;
-  float sm_scale;
-  int batch, groups, hq, hkv, group, page_size, num_pages, max_q_len;
-  int64_t rows_cap;
-  int q8;
-  int ctas;  // of the prefix kernel
-  int one;   // what a tile of a block of at most 128 rows counts
-  uint32_t inject;
-};
-
-// A group's rows and its prefix's key tiles.
-struct Group {
-  int b0, b1, q0, rows, tile0, tiles, end;
-  uint32_t bad;
-};
-__device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
-  Group r;
-  r.b0 = a.group_indptr ? __ldg(a.group_indptr + g) : 0;
-  r.b1 = a.group_indptr ? __ldg(a.group_indptr + g + 1) : a.batch;
-  r.bad = r.b0 < 0 || r.b1 < r.b0 || r.b1 > a.batch ? PDA_STATUS_TABLE_INVALID : 0u;
-  r.q0 = r.rows = r.tile0 = r.tiles = r.end = 0;
-  if (r.bad) return r;
-  r.q0 = __ldg(a.qo_indptr + r.b0);
-  const int64_t rows = static_cast<int64_t>(__ldg(a.qo_indptr + r.b1)) - r.q0;
-  if (r.q0 < 0 || rows < 0 || r.q0 + rows > a.rows_cap) {
-    r.bad = PDA_STATUS_ROWS_GT_CAP;
-    return r;
-  }
-  r.rows = static_cast<int>(rows);
-  const int from = max(0, __ldg(a.prefix + 2 * g));
-  r.end = __ldg(a.prefix + 2 * g + 1);
-  if (r.rows == 0 || r.end <= from) return r;
-  r.tile0 = from / kKeys;
-  r.tiles = (r.end - 1) / kKeys + 1 - r.tile0;
-  return r;
-}
-
-// How the work is cut. An item is a block of kRows packed rows of a kv head, over the
-// prefix's key tiles; group by group, then kv heads, then blocks, the items stand on one
-// axis, and CTA c has the stretch [c per, (c + 1) per) of it: the tiles that begin there. A
-// tile counts kFull, or `one` in a last block of one row tile, whose time is that of
-// its loads. An item is longer by `pay` in front of its tiles: a CTA's further segment
-// costs it a query load and an epilogue, about three tiles' time (64 requests behind 8192
-// tokens, 64 / 8 heads of 128: CTAs of two segments ended at 34 us, the others at 23).
-// Without it where a CTA has less than two tiles: most would be left without any. The
-// plan keeps the axis below 2^31.
-constexpr int kFull = 8, kPay = 3 * kFull;
-template <int kG>
-struct Work {
-  int blocks = 0, tiles = 0, last = 0;  // last: what a tile of the last block counts
-  __device__ __forceinline__ Work() {}
-  __device__ __forceinline__ Work(const SharedArgs& a, const Group& r) {
-    const int packed = r.rows * a.group;
-    tiles = r.tiles;
-    if (tiles == 0) return;
-    blocks = (packed + kG * kTile - 1) / (kG * kTile);
-    last = kG == 1 || packed - (blocks - 1) * (kG * kTile) > kTile ? kFull : a.one;
-  }
-  __device__ __forceinline__ int full(int pay) const { return kFull * tiles + pay; }
-  // of a kv head
-  __device__ __forceinline__ int head(int pay) const {
-    return blocks ? (blocks - 1) * full(pay) + last * tiles + pay : 0;
-  }
-};
-__device__ __forceinline__ void cut_of(int work, int items, int ctas, int& per, int& pay) {
-  pay = work <= ctas * (2 * kFull - 1) ? 0 : kPay;
-  per = max(kFull, static_cast<int>((static_cast<uint32_t>(work + pay * items) + ctas - 1) / static_cast<uint32_t>(ctas)));
-}
-__device__ __forceinline__ int scan32(int x, int lane) {
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, d);
-    if (lane >= d) x += y;
-  }
-  return x;
-}
 
 // One segment: key tiles [t0, t1) of an item.
 struct Item {
@@ -206,9 +105,8 @@ struct Cfg {
                                static_cast<int>(sizeof(Shared));
   static constexpr int kSoft = 4 * kG;              // softmax warps, a thread per row
   static constexpr int kMmaWarp = kSoft, kWorkWarp = kSoft + 1, kProd0 = kSoft + 2;
-  // warps that issue loads (two, or with nothing to widen six: even ones K, odd ones V),
-  // and warps that widen codes
-  static constexpr int kProds = k8 ? 2 : 6;
+  // warps that issue loads (see there), and warps that widen codes
+  static constexpr int kProds = !k8 ? 6 : kDirect ? 2 : 1;
   static constexpr int kConv0 = kSoft + 4, kConv = !k8 ? 0 : kG == 1 ? 8 : 4;
   static constexpr int kWarps = kSoft + 4 + (k8 ? kConv : 4);
   static constexpr int kThreads = 32 * kWarps;
@@ -271,70 +169,80 @@ __device__ __forceinline__ void tile_order(int i, int n, int& v, int& j) {
   }
 }
 
-// The place of tile j of K (V) in that order.
-template <int kG>
-__device__ __forceinline__ uint32_t tile_place(int v, int j, int n) {
-  if constexpr (kG == 2) return 2 * j + v;
-  else return v ? min(2 * j + 2, 2 * n - 1) : max(0, 2 * j - 1);
-}
-
 // ------------------------------------------------------------------- loads
 //
-// Even warps load K, odd ones V, a unit (or raw slot) a warp in turn; its boxes (a page's
-// tokens x 128 bytes, or a head's codes) are its lanes'. A page behind the prefix is one
+// Even warps load K, odd ones V, a unit (or raw slot) a warp in turn; one warp loads both
+// where both are widened, as they share the raw slots. A unit's boxes (a page's tokens x
+// 128 bytes, or a head's codes) are its warp's lanes'. A page behind the prefix is one
 // past the cache: such a box reads as zeros.
+//
+// A wait tells a slot's rounds apart by their parity only, so no warp may stand two
+// rounds in front of what has been read: with at least as many slots as warps in turn,
+// the unit in front of a warp's unit was let in behind the round before the last one.
 template <class C, int D, bool k8>
 __device__ __forceinline__ void load_role(const SharedArgs& a, Shared* sh, uint8_t* rings, uint8_t* raw,
                                           const CUtensorMap* tk, const CUtensorMap* tv, int pw) {
+  constexpr bool kBoth = k8 && !C::kDirect;
   volatile int* abort_flag = &sh->abort_flag;
   const int lane = threadIdx.x & 31;
-  const int v = pw & 1;
-  const uint32_t turn = static_cast<uint32_t>(pw >> 1);
-  constexpr uint32_t kTurns = C::kProds / 2;
+  const uint32_t turn = kBoth ? 0u : static_cast<uint32_t>(pw >> 1);
+  constexpr uint32_t kTurns = kBoth ? 1 : C::kProds / 2;
+  static_assert(C::kRK >= kTurns && C::kRV >= kTurns, "slots for all warps in turn");
   ItemReader reader(sh);
   Item it{};
   bool alive = (a.inject & PDA_INJECT_WITHHOLD_KV) == 0u;
-  // where this warp's tiles go: a ring, or raw slots (in the order of all tiles)
-  const bool to_raw = k8 && (v || !C::kDirect);
-  const uint32_t slots = to_raw ? (C::kRaw ? C::kRaw : 1) : v ? C::kRV : C::kRK;
-  uint64_t* full = to_raw ? sh->raw_full : v ? sh->v_full : sh->k_full;
-  uint64_t* empty = to_raw ? sh->raw_empty : v ? sh->v_empty : sh->k_empty;
-  const uint32_t base = su32(to_raw ? raw : rings + (v ? C::kRK * kUnit : 0));
+  // where this warp's tiles go: a ring, or raw slots
+  const int side = kBoth ? 0 : pw & 1;  // 1: V
+  const bool to_raw = kBoth || (k8 && side);
+  const uint32_t slots = to_raw ? (C::kRaw ? C::kRaw : 1) : side ? C::kRV : C::kRK;
+  uint64_t* full = to_raw ? sh->raw_full : side ? sh->v_full : sh->k_full;
+  uint64_t* empty = to_raw ? sh->raw_empty : side ? sh->v_empty : sh->k_empty;
+  const uint32_t base = su32(to_raw ? raw : rings + (side ? C::kRK * kUnit : 0));
   const uint32_t slot_bytes = to_raw ? C::kRawBytes : kUnit;
-  const int units = to_raw ? C::kRawTile : v ? C::kUV : C::kUK;
-  const int unit_keys = to_raw ? C::kRawKeys : v ? C::kVKeys : kKeys;
+  const int units = to_raw ? C::kRawTile : side ? C::kUV : C::kUK;
+  const int unit_keys = to_raw ? C::kRawKeys : side ? C::kVKeys : kKeys;
   const int P = a.page_size;
   const int rows = min(P, unit_keys), boxes = unit_keys / rows;  // powers of two
-  const int atoms = !k8 && v ? C::kUV : 1;
+  const int atoms = !k8 && side ? C::kUV : 1;
   const int at = lane % boxes, atom = lane / boxes;
   const uint32_t box = atom * (unit_keys * 128) + at * rows * (to_raw ? D : 128);
-  const CUtensorMap* map = v ? tv : tk;
-  // the page of this lane's box of unit c of tile j (the lookup of a unit is under way
-  // while the one in front of it waits for its place)
   const bool mine = atom < atoms;
-  auto first_key = [&](int j, int c) {
-    return (it.t0 + j) * kKeys + (to_raw || v ? c * unit_keys : 0) + at * rows;
+  const int per = kBoth ? 2 * units : units;  // this warp's kind of units a key tile
+  // unit k of the segment: its tile, its place in it, and K or V
+  auto unit_of = [&](uint32_t k, int n, int& v, int& j, int& c) {
+    if constexpr (kBoth) {
+      tile_order<C::kG>(static_cast<int>(k / units), n, v, j);
+    } else {
+      v = side;
+      j = static_cast<int>(k / units);
+    }
+    c = static_cast<int>(k % units);
   };
-  auto page_of = [&](int j, int c) {
+  auto first_key = [&](int j, int c) {
+    return (it.t0 + j) * kKeys + (to_raw || side ? c * unit_keys : 0) + at * rows;
+  };
+  // the page of this lane's box (the lookup of a unit is under way while the one in front
+  // of it waits for its place)
+  auto page_of = [&](uint32_t k, int n) {
+    int v, j, c;
+    unit_of(k, n, v, j, c);
     const int key = first_key(j, c);
     if (!mine || key >= it.end) return a.num_pages;
     return __ldg(a.page_table + it.table + key / P);
   };
   uint32_t t = 0, last = 0;  // key tiles in front of the segment; units up to here
   while (alive && reader.next_warp(it, a)) {
-    const uint32_t n = it.t1 - it.t0, u0 = t * units, u1 = u0 + n * units;
+    const uint32_t n = it.t1 - it.t0, u0 = t * per, u1 = u0 + n * per;
     uint32_t u = u0 + (turn + kTurns - u0 % kTurns) % kTurns;
-    int page = u < u1 ? page_of((u - u0) / units, (u - u0) % units) : 0;
+    int page = u < u1 ? page_of(u - u0, n) : 0;
     for (; u < u1; u += kTurns) {
-      const int j = (u - u0) / units, c = (u - u0) % units;
-      int ahead = 0;
-      if (u + kTurns < u1) ahead = page_of((u + kTurns - u0) / units, (u + kTurns - u0) % units);
-      // raw slots are shared by both sides' tiles, unless K needs none
-      const uint32_t x = !to_raw || C::kDirect ? u : 2 * u0 + tile_place<C::kG>(v, j, n) * units + c;
-      const uint32_t slot = x % slots;
+      int v, j, c, ahead = 0;
+      unit_of(u - u0, n, v, j, c);
+      if (u + kTurns < u1) ahead = page_of(u + kTurns - u0, n);
+      const uint32_t slot = u % slots;
       int good = 1;
       if (lane == 0) {
-        good = bar_wait(empty + slot, ((x / slots) & 1u) ^ 1u, abort_flag, a);
+        good = bar_wait(empty + slot, ((u / slots) & 1u) ^ 1u, abort_flag, a);
         if (good) bar_expect_tx(full + slot, slot_bytes);
       }
       if (!__shfl_sync(0xffffffffu, good, 0)) {
@@ -342,14 +250,15 @@ __device__ __forceinline__ void load_role(const SharedArgs& a, Shared* sh, uint8
         break;
       }
       if (page < 0 || page > a.num_pages) page = a.num_pages;
-      const int chan = to_raw ? 0 : k8 ? c * 128 : (v ? atom : c) * 64;
+      const int chan = to_raw ? 0 : k8 ? c * 128 : (side ? atom : c) * 64;
       if (mine)
-        tma_page(base + slot * slot_bytes + box, map, chan, first_key(j, c) % P, it.head, page, full + slot);
+        tma_page(base + slot * slot_bytes + box, v ? tv : tk, chan, first_key(j, c) % P, it.head, page,
+                 full + slot);
       page = ahead;
-      last = x + 1;
+      last = u + 1;
     }
     t += n;
-    if (alive) last = !to_raw || C::kDirect ? u1 : 2 * u1;
+    if (alive) last = u1;
   }
   // every box issued must have landed before the CTA can exit: the last unit of each slot,
   // whichever warp's it is (after a wait that ran out another warp's may not be coming)
@@ -477,24 +386,10 @@ __device__ __forceinline__ void mma_role(const SharedArgs& a, Shared* sh, uint8_
 // A raw slot's codes, 16 at a time, into the units of a ring, and the tile's scales per
 // token (loaded a tile ahead) into a ring of their own.
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi, bool i8) {
-  uint32_t r[4];
-  const uint32_t w[2] = {lo, hi};
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (i8) {
-      // with u = x + 128, the f16 word 0x6400 | u is 1024 + u: subtract 1152
-      const uint32_t u = w[k] ^ 0x80808080u;
-      uint32_t p, q;
-      asm("prmt.b32 %0, %1, %2, 0x5140;" : "=r"(p) : "r"(u), "r"(0x64646464u));
-      asm("prmt.b32 %0, %1, %2, 0x7362;" : "=r"(q) : "r"(u), "r"(0x64646464u));
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[2 * k]) : "r"(p), "r"(0x64806480u));
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r[2 * k + 1]) : "r"(q), "r"(0x64806480u));
-    } else {
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r[2 * k]) : "h"(static_cast<uint16_t>(w[k] & 0xFFFFu)));
-      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r[2 * k + 1]) : "h"(static_cast<uint16_t>(w[k] >> 16)));
-    }
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  uint4 r;
+  widen4(lo, r.x, r.y, i8);
+  widen4(hi, r.z, r.w, i8);
+  return r;
 }
 
 template <class C, int D, bool kI8, bool kTok>
@@ -875,12 +770,6 @@ __device__ __forceinline__ float load_query(const SharedArgs& a, uint8_t* q_s, i
     }, 1, std::integral_constant<int, D / 8>());
     return up;
   }
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
@@ -1267,7 +1156,7 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
     work_role<C::kG>(a, sh, look);
   } else if (k8 && warp >= C::kConv0) {
     if constexpr (k8) widen_role<C, D, kI8, kTok>(a, sh, rings, raw, scales);
-  } else {
+  } else if (warp < C::kProd0 + C::kProds) {
     load_role<C, D, k8>(a, sh, rings, raw, &tk, &tv, warp - C::kProd0);
   }
   __syncwarp();
@@ -1277,147 +1166,6 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
   if (warp == C::kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols)
                  : "memory");
-}
-
-// -------------------------------------------------------------------- join
-//
-// One warp per (request, row, head): the prefix's segments in order, then the own
-// chunks. Bound: reading the partials (L2); where they are is worked out while the
-// kernels in front end.
-template <int D>
-__global__ void __launch_bounds__(256) shared_join(const __grid_constant__ SharedArgs a,
-                                                   const __grid_constant__ DecodeArgs o) {
-  constexpr int kG = D <= 128 ? 2 : 1, kRows = kG * kTile;
-  constexpr int kV = D / 32;  // channels of a lane
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const int64_t per_b = static_cast<int64_t>(o.max_q_len) * a.hq;
-  const int b = static_cast<int>(item / per_b);
-  const int i = static_cast<int>(item % per_b) / a.hq, head = static_cast<int>(item % a.hq);
-  bool live = b < a.batch;
-  int q0 = 0, own = 0, segs = 0;
-  int64_t c0 = 0;  // CTA of the item's first segment
-  int m = 0;       // packed row
-  Group gr = {};
-  int g = 0;
-  if (live) {
-    q0 = __ldg(a.qo_indptr + b);
-    const int R = __ldg(a.qo_indptr + b + 1) - q0;
-    const int L = __ldg(a.own_len + b), W = a.window ? __ldg(a.window + b) : 0;
-    live = i < R && R <= o.max_q_len && L >= R && L <= o.max_kv_len && q0 >= 0 && q0 + R <= a.rows_cap;
-    if (live) own = split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
-  }
-  if (live) {
-    int top = a.groups - 1;  // the last group that starts at or before the request
-    while (g < top) {
-      const int mid = (g + top + 1) >> 1;
-      if (__ldg(a.group_indptr + mid) <= b) g = mid;
-      else top = mid - 1;
-    }
-    gr = group_of(a, g);
-    m = (q0 + i - gr.q0) * a.group + head % a.group;
-  }
-  const int h = head / a.group;
-  int first = 0, per = 1, pay = 0;
-  if (a.groups <= 32) {  // the work's cut again, a group a lane: no load to wait for
-    Work<kG> w;
-    if (lane < a.groups) w = Work<kG>(a, group_of(a, lane));
-    const int mine = a.hkv * w.head(0), items = a.hkv * w.blocks;
-    const int work = scan32(mine, lane), upto = scan32(items, lane);
-    cut_of(__shfl_sync(0xffffffffu, work, 31), __shfl_sync(0xffffffffu, upto, 31), a.ctas, per, pay);
-    first = __shfl_sync(0xffffffffu, work - mine + pay * (upto - items), g);
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!live) return;
-  if (a.groups > 32) {
-    per = a.first[0];
-    pay = a.first[1];
-    first = a.first[2 + g];
-  }
-  const int block = m / kRows, r = m % kRows;
-  if (gr.tiles > 0) {
-    const Work<kG> w(a, gr);
-    const int count = block == w.blocks - 1 ? w.last : kFull;
-    // its first and its last tile
-    const int u = first + h * w.head(pay) + block * w.full(pay) + pay;
-    c0 = u / per;
-    segs = (u + (gr.tiles - 1) * count) / per - static_cast<int>(c0) + 1;
-  }
-  const int64_t head_row = (h * a.rows_cap + gr.q0) * a.group + m;  // in main
-  const int64_t own_row = static_cast<int64_t>(q0 + i) * a.hq + head, own_step = o.rows_cap * a.hq;
-  const int parts = segs + own;
-  auto place = [&](int s, const float*& x, const float*& v) {
-    if (s >= segs) {
-      const int64_t at = (s - segs) * own_step + own_row;
-      x = o.part_lse + at;
-      v = o.part_o + at * D;
-    } else if (s == 0) {
-      x = a.main_x + head_row;
-      v = a.main_o + head_row * D;
-    } else {
-      const int64_t at = (c0 + s) * kRows + r;
-      x = a.area_x + at;
-      v = a.area_o + at * D;
-    }
-  };
-  constexpr int kBatch = D <= 128 ? 16 : 8;
-  float M = -INFINITY, sum = 0.f, acc[kV];
-#pragma unroll
-  for (int e = 0; e < kV; ++e) acc[e] = 0.f;
-  for (int s0 = 0; s0 < parts; s0 += kBatch) {
-    float x[kBatch], v[kBatch][kV];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      x[k] = -INFINITY;
-      if (s0 + k < parts) {
-        const float *px, *pv;
-        place(s0 + k, px, pv);
-        x[k] = *px;
-        if constexpr (kV == 2) {
-          const float2 t = *reinterpret_cast<const float2*>(pv + lane * 2);
-          v[k][0] = t.x;
-          v[k][1] = t.y;
-        } else {
-#pragma unroll
-          for (int e = 0; e < kV; e += 4) {
-            const float4 t = *reinterpret_cast<const float4*>(pv + lane * kV + e);
-            v[k][e] = t.x;
-            v[k][e + 1] = t.y;
-            v[k][e + 2] = t.z;
-            v[k][e + 3] = t.w;
-          }
-        }
-      }
-    }
-    float top_x = M;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) top_x = fmaxf(top_x, x[k]);
-    if (top_x > M) {
-      const float f = exp2f(M - top_x);  // M = -inf: nothing summed yet
-      sum *= f;
-#pragma unroll
-      for (int e = 0; e < kV; ++e) acc[e] *= f;
-      M = top_x;
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (s0 + k >= parts) break;
-      const float w = x[k] == -INFINITY ? 0.f : exp2f(x[k] - M);
-      sum += w;
-      // a part without a visible key counts for nothing, whatever it holds
-#pragma unroll
-      for (int e = 0; e < kV; ++e) acc[e] = w != 0.f ? fmaf(w, v[k][e], acc[e]) : acc[e];
-    }
-  }
-  const float inv = sum > 0.f ? 1.f / sum : sum;  // (NaN stays)
-  __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.out) + own_row * D + lane * kV;
-  uint32_t w[kV / 2];
-#pragma unroll
-  for (int e = 0; e < kV; e += 2) w[e / 2] = bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if constexpr (kV == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
-  else if constexpr (kV == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (lane == 0 && o.lse) o.lse[own_row] = sum == 0.f ? -INFINITY : (M + __log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------- the prefixes themselves
@@ -1667,8 +1415,10 @@ extern "C" int pda_shared_plan(const pda_plan_t* plan, int32_t groups, int32_t m
     at += up256(bytes);
     return here;
   };
-  sp.own.scratch_lse_offset = take(sp.own.max_splits * cells * 4);
-  sp.own.scratch_o_offset = take(sp.own.max_splits * cells * d * 4);
+  // parts of the own tokens: stage 1's, or one a row, or none that are kept
+  const int64_t parts = !own_here(&sp.own) ? sp.own.max_splits * cells : parts_apart(&sp.own) ? cells : 0;
+  sp.own.scratch_lse_offset = take(parts * 4);
+  sp.own.scratch_o_offset = take(parts * d * 4);
   sp.first_offset = take((2 + static_cast<int64_t>(groups)) * 4);
   sp.main_lse_offset = take(cells * 4);
   sp.main_o_offset = take(cells * d * 4);
@@ -1784,22 +1534,10 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   k.fn<<<static_cast<unsigned>(a.ctas), k.threads, k.smem, s>>>(a, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-  rc = plan->kernel == PDA_KERNEL_TC ? launch_stage1_tc(plan, o, s, true) : launch_stage1_mma(plan, o, s, true);
-  if (rc != PDA_OK) return rc;
-  const int64_t warps = static_cast<int64_t>(a.batch) * max_q_len * a.hq;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  auto* join = plan->head_dim == 64 ? shared_join<64> : plan->head_dim == 128 ? shared_join<128> : shared_join<256>;
-  if (cudaLaunchKernelEx(&cfg, join, a, o) != cudaSuccess) {
-    cudaGetLastError();
-    return PDA_ERR_CUDA;
-  }
-  return PDA_OK;
+  const bool here = own_here(plan), apart = parts_apart(plan);
+  a.parts_apart = here && apart;
+  if (here) rc = launch_own(plan, a, o, s);
+  else if (plan->kernel == PDA_KERNEL_TC) rc = launch_stage1_tc(plan, o, s, true);
+  else rc = launch_stage1_mma(plan, o, s, true);
+  return rc == PDA_OK && (!here || apart) ? launch_join(plan, a, o, s) : rc;
 }

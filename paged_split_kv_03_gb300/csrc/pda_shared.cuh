@@ -1,0 +1,296 @@
+// pda_shared.cuh -- what the kernels of decode behind shared prefixes have in common: their
+// arguments, the groups and how the work on their prefixes is cut, and the join of a row's
+// parts. Internal to each translation unit but for the arguments and launchers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "pda.h"
+#include "pda_cvt.cuh"
+#include "pda_internal.h"
+
+namespace pda {
+
+struct SharedArgs {
+  const void* q;
+  const int32_t* page_table;
+  const int32_t* qo_indptr;
+  const int32_t* kv_len;
+  const int32_t* window;
+  const int32_t* group_indptr;  // NULL: one group of all requests
+  const int32_t* prefix;        // [groups][2] tokens
+  const int32_t* own_indptr;
+  const int32_t* own_len;
+  const float* k_scale;
+  const float* v_scale;
+  float* main_o;    // [kv head][row x group][D] fp32: segments that start their item
+  float* main_x;    // ... and their log2 sums
+  float* area_o;    // [CTA][rows of an item][D]: the segment a CTA starts inside an item
+  float* area_x;
+  int* first;       // the cut (per, pay), then [groups] where each group's work starts
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  float sm_scale;
+  int batch, groups, hq, hkv, group, page_size, num_pages, max_q_len;
+  int64_t rows_cap;
+  int q8;
+  int ctas;  // of the prefix kernel
+  int one;   // what a tile of a block of at most 128 rows counts
+  int parts_apart;  // own tokens' kernel: its parts go to stage 1's place, one a row, for the join
+  uint32_t inject;
+};
+
+// Whether the requests' own tokens have a kernel of their own here (else stage 1), and
+// whether the join has one (else that kernel's last part). They start beside the kernel in
+// front of them and end behind the prefix kernel.
+bool own_here(const pda_plan_t* own);
+bool parts_apart(const pda_plan_t* own);
+int launch_own(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, cudaStream_t s);
+int launch_join(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, cudaStream_t s);
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMInit = -3.0e38f;  // before any key: finite, so that ex2(-inf - m) = 0
+constexpr int kKeys = 128;          // keys of a prefix tile
+constexpr int kTile = 128;          // packed rows of a row tile
+
+// A group's rows and its prefix's key tiles.
+struct Group {
+  int b0, b1, q0, rows, tile0, tiles, end;
+  uint32_t bad;
+};
+__device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
+  Group r;
+  r.b0 = a.group_indptr ? __ldg(a.group_indptr + g) : 0;
+  r.b1 = a.group_indptr ? __ldg(a.group_indptr + g + 1) : a.batch;
+  r.bad = r.b0 < 0 || r.b1 < r.b0 || r.b1 > a.batch ? PDA_STATUS_TABLE_INVALID : 0u;
+  r.q0 = r.rows = r.tile0 = r.tiles = r.end = 0;
+  if (r.bad) return r;
+  r.q0 = __ldg(a.qo_indptr + r.b0);
+  const int64_t rows = static_cast<int64_t>(__ldg(a.qo_indptr + r.b1)) - r.q0;
+  if (r.q0 < 0 || rows < 0 || r.q0 + rows > a.rows_cap) {
+    r.bad = PDA_STATUS_ROWS_GT_CAP;
+    return r;
+  }
+  r.rows = static_cast<int>(rows);
+  const int from = max(0, __ldg(a.prefix + 2 * g));
+  r.end = __ldg(a.prefix + 2 * g + 1);
+  if (r.rows == 0 || r.end <= from) return r;
+  r.tile0 = from / kKeys;
+  r.tiles = (r.end - 1) / kKeys + 1 - r.tile0;
+  return r;
+}
+
+// How the work is cut. An item is a block of kRows packed rows of a kv head, over the
+// prefix's key tiles; group by group, then kv heads, then blocks, the items stand on one
+// axis, and CTA c has the stretch [c per, (c + 1) per) of it: the tiles that begin there. A
+// tile counts kFull, or `one` in a last block of one row tile, whose time is that of
+// its loads. An item is longer by `pay` in front of its tiles: a CTA's further segment
+// costs it a query load and an epilogue, about three tiles' time (64 requests behind 8192
+// tokens, 64 / 8 heads of 128: CTAs of two segments ended at 34 us, the others at 23).
+// Without it where a CTA has less than two tiles: most would be left without any. The
+// plan keeps the axis below 2^31.
+constexpr int kFull = 8, kPay = 3 * kFull;
+template <int kG>
+struct Work {
+  int blocks = 0, tiles = 0, last = 0;  // last: what a tile of the last block counts
+  __device__ __forceinline__ Work() {}
+  __device__ __forceinline__ Work(const SharedArgs& a, const Group& r) {
+    const int packed = r.rows * a.group;
+    tiles = r.tiles;
+    if (tiles == 0) return;
+    blocks = (packed + kG * kTile - 1) / (kG * kTile);
+    last = kG == 1 || packed - (blocks - 1) * (kG * kTile) > kTile ? kFull : a.one;
+  }
+  __device__ __forceinline__ int full(int pay) const { return kFull * tiles + pay; }
+  // of a kv head
+  __device__ __forceinline__ int head(int pay) const {
+    return blocks ? (blocks - 1) * full(pay) + last * tiles + pay : 0;
+  }
+};
+__device__ __forceinline__ void cut_of(int work, int items, int ctas, int& per, int& pay) {
+  pay = work <= ctas * (2 * kFull - 1) ? 0 : kPay;
+  per = max(kFull, static_cast<int>((static_cast<uint32_t>(work + pay * items) + ctas - 1) / static_cast<uint32_t>(ctas)));
+}
+__device__ __forceinline__ int scan32(int x, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+// Where a row's parts of its group's prefix are.
+template <int kG>
+struct Parts {
+  Group gr;
+  int g = 0, first = 0, per = 1, pay = 0;
+  // Of the group of request b; a whole warp. What the prefix kernel wrote down (more groups
+  // than lanes) is read by `late`, behind that kernel.
+  __device__ __forceinline__ Parts(const SharedArgs& a, int b) {
+    const int lane = threadIdx.x & 31;
+    int top = a.groups - 1;  // the last group that starts at or before the request
+    while (g < top) {
+      const int mid = (g + top + 1) >> 1;
+      if (__ldg(a.group_indptr + mid) <= b) g = mid;
+      else top = mid - 1;
+    }
+    gr = group_of(a, g);
+    if (a.groups > 32) return;
+    Work<kG> w;
+    if (lane < a.groups) w = Work<kG>(a, a.groups == 1 ? gr : group_of(a, lane));
+    const int mine = a.hkv * w.head(0), items = a.hkv * w.blocks;
+    int work = mine, upto = items;
+    if (a.groups > 1) {
+      work = scan32(mine, lane);
+      upto = scan32(items, lane);
+    }
+    const int last = a.groups > 1 ? 31 : 0;
+    cut_of(__shfl_sync(0xffffffffu, work, last), __shfl_sync(0xffffffffu, upto, last), a.ctas, per, pay);
+    first = __shfl_sync(0xffffffffu, work - mine + pay * (upto - items), g);
+  }
+  __device__ __forceinline__ void late(const SharedArgs& a) {
+    if (a.groups <= 32) return;
+    per = a.first[0];
+    pay = a.first[1];
+    first = a.first[2 + g];
+  }
+};
+// ... of packed row m and kv head h: how many, and each one's log2 sum and output.
+template <int kG, int D>
+struct RowParts {
+  int segs = 0, c0 = 0, r = 0;
+  int64_t head_row = 0;
+  __device__ __forceinline__ RowParts(const SharedArgs& a, const Parts<kG>& p, int h, int m) {
+    constexpr int kRows = kG * kTile;
+    const int block = m / kRows;
+    r = m % kRows;
+    head_row = (h * a.rows_cap + p.gr.q0) * a.group + m;
+    if (p.gr.tiles == 0) return;
+    const Work<kG> w(a, p.gr);
+    const int count = block == w.blocks - 1 ? w.last : kFull;
+    // its first and its last tile
+    const int u = p.first + h * w.head(p.pay) + block * w.full(p.pay) + p.pay;
+    c0 = u / p.per;
+    segs = (u + (p.gr.tiles - 1) * count) / p.per - c0 + 1;
+  }
+  __device__ __forceinline__ void part(const SharedArgs& a, int s, const float*& x, const float*& v) const {
+    const int64_t at = s == 0 ? head_row : static_cast<int64_t>(c0 + s) * (kG * kTile) + r;
+    x = (s == 0 ? a.main_x : a.area_x) + at;
+    v = (s == 0 ? a.main_o : a.area_o) + at * D;
+  }
+};
+
+// The running sum of a row's parts, kV channels a lane.
+template <int kV>
+struct Join {
+  float top = -INFINITY, sum = 0.f, acc[kV];
+  __device__ __forceinline__ Join() {
+#pragma unroll
+    for (int e = 0; e < kV; ++e) acc[e] = 0.f;
+  }
+  __device__ __forceinline__ void raise(float to) {
+    if (!(to > top)) return;
+    const float f = exp2f(top - to);  // -inf: nothing summed yet
+    sum *= f;
+#pragma unroll
+    for (int e = 0; e < kV; ++e) acc[e] *= f;
+    top = to;
+  }
+  // kBatch parts at most at a time, their loads in front of their use
+  template <int kBatch, class Place>
+  __device__ __forceinline__ void add(int parts, Place&& place) {
+    const int lane = threadIdx.x & 31;
+    for (int s0 = 0; s0 < parts; s0 += kBatch) {
+      float x[kBatch], v[kBatch][kV];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        x[k] = -INFINITY;
+        if (s0 + k < parts) {
+          const float *px, *pv;
+          place(s0 + k, px, pv);
+          x[k] = *px;
+          if constexpr (kV == 2) {
+            const float2 t = *reinterpret_cast<const float2*>(pv + lane * 2);
+            v[k][0] = t.x;
+            v[k][1] = t.y;
+          } else {
+#pragma unroll
+            for (int e = 0; e < kV; e += 4) {
+              const float4 t = *reinterpret_cast<const float4*>(pv + lane * kV + e);
+              v[k][e] = t.x;
+              v[k][e + 1] = t.y;
+              v[k][e + 2] = t.z;
+              v[k][e + 3] = t.w;
+            }
+          }
+        }
+      }
+      float to = top;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) to = fmaxf(to, x[k]);
+      raise(to);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (s0 + k >= parts) break;
+        const float w = x[k] == -INFINITY ? 0.f : exp2f(x[k] - top);
+        sum += w;
+        // a part without a visible key counts for nothing, whatever it holds
+#pragma unroll
+        for (int e = 0; e < kV; ++e) acc[e] = w != 0.f ? fmaf(w, v[k][e], acc[e]) : acc[e];
+      }
+    }
+  }
+  // as one more part
+  __device__ __forceinline__ void keep(float* x, float* v) const {
+    const int lane = threadIdx.x & 31;
+    const float inv = sum > 0.f ? 1.f / sum : sum;  // (NaN stays)
+#pragma unroll
+    for (int e = 0; e < kV; ++e) v[lane * kV + e] = acc[e] * inv;
+    if (lane == 0) *x = sum == 0.f ? -INFINITY : top + __log2f(sum);
+  }
+  // the row's results; `row`: of out and lse
+  __device__ __forceinline__ void write(const DecodeArgs& o, int64_t row) const {
+    const int lane = threadIdx.x & 31;
+    const float inv = sum > 0.f ? 1.f / sum : sum;  // (NaN stays)
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.out) + row * (32 * kV) + lane * kV;
+    uint32_t w[kV / 2];
+#pragma unroll
+    for (int e = 0; e < kV; e += 2) w[e / 2] = bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    if constexpr (kV == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
+    else if constexpr (kV == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (lane == 0 && o.lse) o.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+  }
+};
+
+// Four 8-bit codes (int8, or E4M3) -> four f16, exactly.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& lo, uint32_t& hi, bool i8) {
+  if (i8) {
+    // with u = x + 128, the f16 word 0x6400 | u is 1024 + u: subtract 1152
+    const uint32_t u = w ^ 0x80808080u;
+    uint32_t p, q;
+    asm("prmt.b32 %0, %1, %2, 0x5140;" : "=r"(p) : "r"(u), "r"(0x64646464u));
+    asm("prmt.b32 %0, %1, %2, 0x7362;" : "=r"(q) : "r"(u), "r"(0x64646464u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(p), "r"(0x64806480u));
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(q), "r"(0x64806480u));
+  } else {
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(w & 0xFFFFu)));
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(w >> 16)));
+  }
+}
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+}  // namespace
+}  // namespace pda

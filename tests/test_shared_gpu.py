@@ -26,19 +26,21 @@ def check(got, want, bound, what):
         f"{what}: error {err[worst]:.3e}, bound {lim[worst]:.3e}, value {want[fine][worst]:.3e}"
 
 
-def parity(w, max_own=0, sm_scale=None, shared=None):
+def parity(w, sm_scale=None, shared=None):
+    """Both ways of the own tokens: planned for any number of them (stage 1, then the join), and
+    for no more than there are (one kernel, where they are few)."""
     dec = B.Decoder(w.params, device=DEV)
-    sh = shared or B.Shared(dec.plan, len(w.gp) - 1, max_own)
-    t = S.device_tables(w)
-    out, lse = S.run(w, sh, t, sm_scale=sm_scale)
-    torch.cuda.synchronize()
     (prefix, ptr, own), status = S.share(w)
-    assert t.prefix.reshape(-1).tolist() == prefix
-    assert t.own_indptr.tolist() == ptr and t.own_len.tolist() == own
     o, ob, l, lb = S.attention(w, sm_scale)
-    check(out, o, ob, "out")
-    check(lse, l, lb, "lse")
-    assert sh.status() == status
+    for sh in [shared] if shared else [B.Shared(dec.plan, len(w.gp) - 1, n) for n in (0, max(own + [1]))]:
+        t = S.device_tables(w)
+        out, lse = S.run(w, sh, t, sm_scale=sm_scale)
+        torch.cuda.synchronize()
+        assert t.prefix.reshape(-1).tolist() == prefix
+        assert t.own_indptr.tolist() == ptr and t.own_len.tolist() == own
+        check(out, o, ob, "out")
+        check(lse, l, lb, "lse")
+        assert sh.status() == status
     return sh, t
 
 
@@ -84,11 +86,19 @@ def test_rows_and_heads(dim, hkv, group, requests, rows, kind):
                   dev=DEV, seed=requests))
 
 
-@pytest.mark.parametrize("kind,dim", [("bf16", 128), ("bf16", 256), ("e4m3_token", 128),
-                                      ("e4m3_tensor", 256), ("int8_tensor", 64)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kind", KINDS)
 def test_long_prefix(kind, dim):
     """Many segments of an item over the CTAs, and CTAs that start inside one."""
     parity(S.make([(1301, reqs(9, own=300, rows=2))], kind=kind, dim=dim, hkv=2, group=4, dev=DEV))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_items(kind, dim):
+    """Several segments a CTA: items of two row tiles, of one, of a few tiles and of many."""
+    groups = [(17, reqs(30)), (3, reqs(5)), (40, reqs(9, rows=2)), (1, reqs(1)), (90, reqs(26))]
+    parity(S.make(groups, kind=kind, dim=dim, page=128, hkv=8, group=3, hnd=True, dev=DEV, spare=1))
 
 
 @pytest.mark.parametrize("kind,dim", [("bf16", 128), ("bf16", 64), ("e4m3_token", 256)])
