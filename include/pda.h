@@ -643,7 +643,7 @@ typedef struct {
   int32_t* own_len;            /* [batch] written: its own tokens; not kv_len */
 } pda_shared_tables;
 
-/* Plan decodes of the plan's batch in `groups` groups (1 to 2048), with at most
+/* Plan decodes of the plan's batch in `groups` groups (1 to 1024), with at most
  * max_own_len own tokens a request (0: the plan's max_kv_len; a tight bound plans
  * better chunks). A request that has more is left unwritten by pda_decode_shared
  * (PDA_STATUS_KV_LEN_GT_MAX). Host-only. Writes *out_plan and, when non-NULL,

@@ -1,7 +1,6 @@
 // pda_own.cu -- the requests' own tokens behind a shared prefix, and the join with what the
-// prefix kernel left of the prefix. Few own tokens a request have a kernel here (more go
-// through stage 1 of pda_decode); it joins its rows itself, or leaves that to a kernel
-// of its own where a row has many parts and few CTAs would have to read them.
+// prefix kernel left of the prefix: one kernel where the own tokens are few, else the join
+// alone behind stage 1 of pda_decode.
 //
 // Mathematics: see pda_shared.cu; the own tokens are ordinary causal (and windowed)
 // attention of R rows x the heads of a GQA group, 16 of them a CTA. out = (sum_s 2^(x_s - X)
@@ -14,7 +13,9 @@
 // cores: a warp takes 16 tokens at a time into mma.sync fragments straight from the
 // cache. Which channel a lane's fragment element stands for is free, as long as Q (for
 // S, a sum over channels) and O (whose columns are channels) agree, so a lane holds 16
-// neighbouring bytes of a token. Three CTAs of four warps an SM keep 96 KB in flight.
+// neighbouring bytes of a token. Twelve warps an SM (eight at head_dim 256) keep 96 KB in
+// flight. Few rows are shared by a cluster of CTAs, its tokens and then the rows of its
+// join: one that joins 16 rows of 76 parts each alone takes 30 us for it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -31,14 +32,11 @@
 namespace pda {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kMaxWarps = 4;
 constexpr int kRows = 16;          // packed rows (query row x head of the group) of a CTA
 constexpr int kStep = 16;          // tokens of a warp's step
 constexpr int kMaxTiles = 4;       // most row tiles of a request: each reads its tokens again
 constexpr int kMaxTokens = 1024;   // most own tokens: four warps share them
-// Parts of a row from which on the join has a kernel of its own, with kJoinWarps warps a row:
-// 12 requests, 2 kv heads (76 parts a row): 86 us in the own tokens' kernel.
-constexpr int kManyParts = 24, kJoinWarps = 4;
 
 template <int D, bool k8>
 struct Cfg {
@@ -47,8 +45,9 @@ struct Cfg {
   static constexpr int kSets = D / (8 * kVCh);             // such pieces
   static constexpr int kStride = D + 4;                    // floats of a row of O in shared memory
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kOBytes = kWarps * kRows * kStride * 4;
-  static constexpr int kSmem = kQBytes + kOBytes + kWarps * kRows * 8 + kRows * 4;
+  static constexpr int kOBytes = kRows * kStride * 4;      // of a warp
+  static constexpr int smem(int warps) { return kQBytes + warps * (kOBytes + kRows * 8) + kRows * 4; }
+  static constexpr int kWarpsSm = D == 256 ? 8 : 12;       // by their registers
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -70,29 +69,54 @@ __device__ __forceinline__ void mma16(float* d, uint32_t a0, uint32_t a1, uint32
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// A variable's address in CTA `rank` of the cluster, and loads there.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(r)
+               : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float4 load4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ float2 load2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, bool high) {
   return __byte_perm(x, y, high ? 0x7632 : 0x5410);
 }
 
 template <int D, bool k8, bool kI8, bool kTok>
-__global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) own_join(const __grid_constant__ SharedArgs a,
+__global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(const __grid_constant__ SharedArgs a,
                                                      const __grid_constant__ DecodeArgs o) {
   using C = Cfg<D, k8>;
   constexpr int kG = D <= 128 ? 2 : 1;
   constexpr int eb = k8 ? 1 : 2;
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* q_s = smem;  // [16][D] in 16 bits, a row's 16-byte pieces XORed with its low bits
+  const int warps = blockDim.x >> 5;
   float* o_s = reinterpret_cast<float*>(smem + C::kQBytes);  // [warp][16][kStride]
-  float2* ml_s = reinterpret_cast<float2*>(smem + C::kQBytes + C::kOBytes);  // [warp][16]
-  float* up_s = reinterpret_cast<float*>(ml_s + kWarps * kRows);  // a row's power of two
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::kQBytes + warps * C::kOBytes);  // [warp][16]
+  float* up_s = reinterpret_cast<float*>(ml_s + warps * kRows);  // a row's power of two
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int b = blockIdx.x / a.hkv, h = blockIdx.x % a.hkv;
+  uint32_t ctas;  // of the cluster
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  const int rank = blockIdx.x % ctas, item = blockIdx.x / ctas;
+  const int b = item / a.hkv, h = item % a.hkv;
   const int q0 = __ldg(a.qo_indptr + b), R = __ldg(a.qo_indptr + b + 1) - q0;
   const int L = __ldg(a.own_len + b), own = __ldg(a.own_indptr + b);
   const int W = a.window ? __ldg(a.window + b) : 0;
   const int m0 = blockIdx.y * kRows, M = R * a.group;
   if (R <= 0 || R > o.max_q_len || L < R || L > o.max_kv_len || q0 < 0 || q0 + R > a.rows_cap || m0 >= M) {
-    if (tid == 0 && h == 0 && blockIdx.y == 0) {
+    if (tid == 0 && h == 0 && blockIdx.y == 0 && rank == 0) {
       uint32_t bits = 0u;
       if (R < 0 || R > o.max_q_len) bits = PDA_STATUS_ROWS_GT_MAX;
       else if (R > 0 && L < R) bits = PDA_STATUS_KV_LEN_LT_ROWS;
@@ -106,8 +130,9 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) own_join(const __g
   }
 
   // ---- the queries: eight lanes a row, 16 bits a channel
-  {
-    const int r = tid >> 3, m = m0 + r;
+#pragma unroll 1
+  for (int r = tid >> 3; r < kRows; r += blockDim.x >> 3) {
+    const int m = m0 + r;
     const bool live = m < M;
     const int64_t at = ((static_cast<int64_t>(q0) + (live ? m / a.group : 0)) * a.hq + h * a.group +
                         (live ? m % a.group : 0)) * D;
@@ -191,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) own_join(const __g
   for (int n = 0; n < D / 8; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-  int s = from + warp;
+  int s = from + rank * warps + warp;
+  const int stride = ctas * warps;
   int pg[2] = {-1, -1};
   if (s < steps) {
     pg[0] = page_at(s * kStep);
@@ -199,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) own_join(const __g
   }
   bool oob = false;
 #pragma unroll 1
-  for (; s < steps; s += kWarps) {
+  for (; s < steps; s += stride) {
     const int t0 = s * kStep;
     // bytes of each half's first token, or -1
     int64_t at[2];
@@ -211,8 +237,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) own_join(const __g
       at[e] = ok ? (pg[e] * o.sp + (t & (P - 1)) * o.st) * eb : -1;
     }
     const int held[2] = {pg[0], pg[1]};
-    pg[0] = page_at(t0 + kWarps * kStep);
-    pg[1] = page_at(t0 + kWarps * kStep + 8);
+    pg[0] = page_at(t0 + stride * kStep);
+    pg[1] = page_at(t0 + stride * kStep + 8);
     // K: token g of each half, 16-byte pieces q, q + 4, ... of its row
     uint4 kv[2][C::kPieces];
 #pragma unroll
@@ -386,61 +412,107 @@ __global__ void __launch_bounds__(kThreads, D == 256 ? 2 : 3) own_join(const __g
         row[(set * 8 + 2 * q + 1) * C::kVCh + j] = acc[set * C::kVCh + j][2 * k + 1];
       }
   }
-  constexpr int kV = D / 32;
-  // ---- a warp's rows: own parts, then the prefix's
-  auto own_parts = [&](Join<kV>& join, int r) {
+  // ---- the rows, half a warp each, or a warp where there are warps for it (its halves then
+  // take the prefix's parts in turns): the cluster's own parts, then the prefix's
+  using J = Join<D, 16>;
+  constexpr int kV = J::kV;
+  // `count` parts from other places in shared memory, their loads in front of their use (a
+  // load from another CTA takes 200 ns and more)
+  auto gather = [&](J& join, int count, auto&& at_ml, auto&& at_o, float times) {
+    float2 ml[4];
+    float v[4][kV];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) join.raise(ml_s[w * kRows + r].x);
+    for (int c = 0; c < 4; ++c) {
+      ml[c] = make_float2(-INFINITY, 0.f);
+      if (c >= count) continue;
+      ml[c] = load2(at_ml(c));
+      const uint32_t src = at_o(c) + J::first() * 4;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = ml_s[w * kRows + r];
-      const float f = exp2f(ml.x - join.top);
-      const float* src = o_s + (w * kRows + r) * C::kStride + lane * kV;
-      join.sum = fmaf(f, ml.y, join.sum);
+      for (int e = 0; e < kV; e += 4) {
+        const float4 x = load4(src + e * 4);
+        v[c][e] = x.x;
+        v[c][e + 1] = x.y;
+        v[c][e + 2] = x.z;
+        v[c][e + 3] = x.w;
+      }
+    }
 #pragma unroll
-      for (int e = 0; e < kV; ++e) join.acc[e] = fmaf(f, src[e] * v_final, join.acc[e]);
+    for (int c = 0; c < 4; ++c) join.raise(ml[c].x);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (c >= count) continue;
+      const float f = exp2f(ml[c].x - join.top);
+      join.sum = fmaf(f, ml[c].y, join.sum);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) join.acc[e] = fmaf(f, v[c][e] * times, join.acc[e]);
     }
   };
-  if (a.parts_apart) {
-    __syncthreads();
-#pragma unroll 1
-    for (int r = warp; r < kRows && m0 + r < M; r += kWarps) {
-      Join<kV> join;
-      own_parts(join, r);
-      const int64_t at = (static_cast<int64_t>(q0) + (m0 + r) / a.group) * a.hq + h * a.group + (m0 + r) % a.group;
-      join.keep(o.part_lse + at, o.part_o + at * D);
-    }
-    if (blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
-  }
+  auto ml_of = [&](int w, int r, uint32_t cta) { return in_cta(ml_s + w * kRows + r, cta); };
+  auto o_of = [&](int w, int r, uint32_t cta) { return in_cta(o_s + (w * kRows + r) * C::kStride, cta); };
+  const int live = min(kRows, M - m0), hw = lane >> 4;
   Parts<kG> parts(a, b);
   __syncthreads();
+  if (ctas > 1) {  // one part a CTA, in the first warp's place
+#pragma unroll 1
+    for (int r = 2 * warp + hw; r < live; r += 2 * warps) {
+      J join;
+      gather(join, warps, [&](int w) { return ml_of(w, r, rank); }, [&](int w) { return o_of(w, r, rank); }, 1.f);
+#pragma unroll
+      for (int e = 0; e < kV; ++e) o_s[r * C::kStride + J::first() + e] = join.acc[e];
+      // (every lane of the half has read the first warp's maximum: their loads are used)
+      __syncwarp(0xffffu << (16 * hw));
+      if (J::first() == 0) ml_s[r] = make_float2(join.top, join.sum);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's parts are there
   parts.late(a);
+  const bool turns = stride >= live;
+  const int r0 = turns ? rank * warps + warp : 2 * (rank * warps + warp) + hw;
 #pragma unroll 1
-  for (int r = warp; r < kRows && m0 + r < M; r += kWarps) {
-    const int i = (m0 + r) / a.group, head = h * a.group + (m0 + r) % a.group;
-    Join<kV> join;
-    own_parts(join, r);
-    const RowParts<kG, D> row(a, parts, h, (q0 + i - parts.gr.q0) * a.group + (m0 + r) % a.group);
-    join.template add<(D <= 128 ? 12 : 8)>(row.segs, [&](int s2, const float*& x, const float*& v) { row.part(a, s2, x, v); });
-    join.write(o, (static_cast<int64_t>(q0) + i) * a.hq + head);
+  for (int r = r0; r < live; r += turns ? stride : 2 * stride) {
+    J join;
+    if (!turns || hw == 0) {
+      if (ctas > 1)
+        gather(join, static_cast<int>(ctas), [&](int c) { return ml_of(0, r, c); }, [&](int c) { return o_of(0, r, c); },
+               v_final);
+      else
+        gather(join, warps, [&](int w) { return ml_of(w, r, rank); }, [&](int w) { return o_of(w, r, rank); }, v_final);
+    }
+    const int i = (m0 + r) / a.group, hh = (m0 + r) % a.group;
+    const RowParts<kG, D> row(a, parts, h, (q0 + i - parts.gr.q0) * a.group + hh);
+    const int step = turns ? 2 : 1, at = turns ? hw : 0;
+    join.template add<80 / kV>((row.segs - at + step - 1) / step,
+                               [&](int k, const float*& x, const float*& v) { row.part(a, k * step + at, x, v); });
+    if (turns) {
+      __syncwarp();
+      const float top = __shfl_xor_sync(0xffffffffu, join.top, 16), sum = __shfl_xor_sync(0xffffffffu, join.sum, 16);
+      const float mine = join.top, to = fmaxf(mine, top);
+      const float f0 = mine == -INFINITY ? 0.f : exp2f(mine - to), f1 = top == -INFINITY ? 0.f : exp2f(top - to);
+      join.top = to;
+      join.sum = join.sum * f0 + sum * f1;
+#pragma unroll
+      for (int e = 0; e < kV; ++e)
+        join.acc[e] = join.acc[e] * f0 + __shfl_xor_sync(0xffffffffu, join.acc[e], 16) * f1;
+      if (hw) continue;
+    }
+    join.write(o, (static_cast<int64_t>(q0) + i) * a.hq + h * a.group + hh);
   }
+  __syncwarp();
+  if (ctas > 1) cluster_sync();  // the others have read this CTA's parts
 }
 
 // ------------------------------------------------------------- the join alone
 //
-// S warps per (request, row, head): the prefix's segments in order, then the own tokens'
-// parts; with several warps each takes a share of them in turn. Bound: reading the parts
-// (L2); where they are is worked out while the kernels in front end.
-template <int D, int S>
-__global__ void __launch_bounds__(256) shared_join(const __grid_constant__ SharedArgs a,
-                                                   const __grid_constant__ DecodeArgs o) {
-  constexpr int kG = D <= 128 ? 2 : 1, kV = D / 32;
-  __shared__ float acc_s[S > 1 ? 8 : 1][S > 1 ? D : 1];
-  __shared__ float2 ml[8];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % S;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (8 / S) + warp / S;
+// One warp per (request, row, head): the prefix's segments in order, then stage 1's
+// chunks. Bound: reading the parts (L2); where they are is worked out while the kernels
+// in front end.
+template <int D>
+__global__ void __launch_bounds__(256, 3) shared_join(const __grid_constant__ SharedArgs a,
+                                                      const __grid_constant__ DecodeArgs o) {
+  constexpr int kG = D <= 128 ? 2 : 1;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t per_b = static_cast<int64_t>(o.max_q_len) * a.hq;
   const int b = static_cast<int>(item / per_b);
   const int i = static_cast<int>(item % per_b) / a.hq, head = static_cast<int>(item % a.hq), h = head / a.group;
@@ -451,78 +523,62 @@ __global__ void __launch_bounds__(256) shared_join(const __grid_constant__ Share
     const int R = __ldg(a.qo_indptr + b + 1) - q0;
     const int L = __ldg(a.own_len + b), W = a.window ? __ldg(a.window + b) : 0;
     live = i < R && R <= o.max_q_len && L >= R && L <= o.max_kv_len && q0 >= 0 && q0 + R <= a.rows_cap;
-    if (live) own = a.parts_apart ? 1 : split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
+    if (live) own = split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
   }
   Parts<kG> parts(a, live ? b : 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (S == 1 && !live) return;
-  Join<kV> join;
+  if (!live) return;
+  parts.late(a);
+  const RowParts<kG, D> row(a, parts, h, (q0 + i - parts.gr.q0) * a.group + head % a.group);
   const int64_t own_row = static_cast<int64_t>(q0 + i) * a.hq + head, own_step = o.rows_cap * a.hq;
-  if (live) {
-    parts.late(a);
-    const RowParts<kG, D> row(a, parts, h, (q0 + i - parts.gr.q0) * a.group + head % a.group);
-    const int all = row.segs + own;
-    join.template add<(D <= 128 ? 16 : 8)>((all - sub + S - 1) / S, [&](int k, const float*& x, const float*& v) {
-      const int s = k * S + sub;
-      if (s < row.segs) return row.part(a, s, x, v);
-      const int64_t at = (s - row.segs) * own_step + own_row;
-      x = o.part_lse + at;
-      v = o.part_o + at * D;
-    });
-  }
-  if constexpr (S > 1) {
-    if (sub) {
-      if (lane == 0) ml[warp] = make_float2(join.top, join.sum);
-#pragma unroll
-      for (int e = 0; e < kV; ++e) acc_s[warp][lane * kV + e] = join.acc[e];
-    }
-    __syncthreads();
-    if (sub || !live) return;
-#pragma unroll 1
-    for (int w = warp + 1; w < warp + S; ++w) {
-      const float2 x = ml[w];
-      join.raise(x.x);
-      const float f = x.x == -INFINITY ? 0.f : exp2f(x.x - join.top);
-      join.sum = fmaf(f, x.y, join.sum);
-#pragma unroll
-      for (int e = 0; e < kV; ++e) join.acc[e] = fmaf(f, acc_s[w][lane * kV + e], join.acc[e]);
-    }
-  }
+  Join<D, 32> join;
+  join.template add<(D <= 128 ? 8 : 4)>(row.segs + own, [&](int s, const float*& x, const float*& v) {
+    if (s < row.segs) return row.part(a, s, x, v);
+    const int64_t at = (s - row.segs) * own_step + own_row;
+    x = o.part_lse + at;
+    v = o.part_o + at * D;
+  });
   join.write(o, own_row);
 }
 
 using JoinFn = void (*)(SharedArgs, DecodeArgs);
 struct Kernel {
   JoinFn fn;
-  int smem;
+  int (*smem)(int warps);
+  int warps_sm;
 };
 template <int D>
 Kernel kernel_for(const pda_plan_t* p) {
+  using C16 = Cfg<D, false>;
+  using C8 = Cfg<D, true>;
   const bool tok = p->scale_mode == PDA_SCALE_TOKEN_HEAD;
-  const int s8 = Cfg<D, true>::kSmem;
-  if (p->kv_dtype == PDA_BF16) return {own_join<D, false, false, false>, Cfg<D, false>::kSmem};
-  if (p->kv_dtype == PDA_INT8) return {tok ? own_join<D, true, true, true> : own_join<D, true, true, false>, s8};
-  return {tok ? own_join<D, true, false, true> : own_join<D, true, false, false>, s8};
+  if (p->kv_dtype == PDA_BF16) return {own_join<D, false, false, false>, C16::smem, C16::kWarpsSm};
+  if (p->kv_dtype == PDA_INT8)
+    return {tok ? own_join<D, true, true, true> : own_join<D, true, true, false>, C8::smem, C8::kWarpsSm};
+  return {tok ? own_join<D, true, false, true> : own_join<D, true, false, false>, C8::smem, C8::kWarpsSm};
 }
 
-int launch(JoinFn fn, dim3 grid, unsigned threads, int smem, const SharedArgs& a, const DecodeArgs& o,
-           cudaStream_t s) {
+int launch(JoinFn fn, dim3 grid, unsigned threads, int smem, unsigned cluster, const SharedArgs& a,
+           const DecodeArgs& o, cudaStream_t s) {
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(reinterpret_cast<const void*>(fn), cudaFuncAttributeMaxDynamicSharedMemorySize,
                            smem) != cudaSuccess) {
     cudaGetLastError();
     return PDA_ERR_CUDA;
   }
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, fn, a, o) == cudaSuccess) return PDA_OK;
   cudaGetLastError();
   return PDA_ERR_CUDA;
@@ -534,27 +590,35 @@ bool own_here(const pda_plan_t* own) {
   return own->max_q_len * own->group <= kMaxTiles * kRows && own->max_kv_len <= kMaxTokens;
 }
 
-bool parts_apart(const pda_plan_t* own) { return own->num_sms > kManyParts * own->num_kv_heads; }
-
 int launch_own(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, cudaStream_t s) {
   const Kernel k = own->head_dim == 64    ? kernel_for<64>(own)
                    : own->head_dim == 128 ? kernel_for<128>(own)
                                           : kernel_for<256>(own);
-  const dim3 grid(static_cast<unsigned>(a.batch * a.hkv),
-                  static_cast<unsigned>((o.max_q_len * a.group + kRows - 1) / kRows));
-  return launch(k.fn, grid, kThreads, k.smem, a, o, s);
+  const int tiles = (o.max_q_len * a.group + kRows - 1) / kRows;
+  const int64_t items = static_cast<int64_t>(a.batch) * a.hkv * tiles;
+  // Few items: clusters of up to four CTAs, while all of them have an SM. Many: as few
+  // warps a CTA as end sooner, where four would leave a last wave of few CTAs (a step of
+  // 16 tokens takes about 2 us with all SMs at it, a CTA's start and join 6; half of the
+  // most tokens taken for all).
+  int cluster = 1, warps = kMaxWarps;
+  while (cluster < 4 && items * cluster * 2 <= own->num_sms) cluster *= 2;
+  if (cluster == 1) {
+    const int steps = std::max(1, own->max_kv_len / (2 * kStep));
+    double best = 1e30;
+    for (int w = kMaxWarps; w >= 1; --w) {
+      const int64_t slots = static_cast<int64_t>(k.warps_sm / w) * own->num_sms;
+      const double us = static_cast<double>((items + slots - 1) / slots) * ((steps + w - 1) / w * 2.0 + 6.0);
+      if (us < best) best = us, warps = w;
+    }
+  }
+  const dim3 grid(static_cast<unsigned>(a.batch * a.hkv * cluster), static_cast<unsigned>(tiles));
+  return launch(k.fn, grid, 32u * warps, k.smem(warps), static_cast<unsigned>(cluster), a, o, s);
 }
 
 int launch_join(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, cudaStream_t s) {
-  const bool many = parts_apart(own);
-  const int64_t warps = static_cast<int64_t>(a.batch) * o.max_q_len * a.hq * (many ? kJoinWarps : 1);
-  const JoinFn one = own->head_dim == 64    ? shared_join<64, 1>
-                     : own->head_dim == 128 ? shared_join<128, 1>
-                                            : shared_join<256, 1>;
-  const JoinFn four = own->head_dim == 64    ? shared_join<64, kJoinWarps>
-                      : own->head_dim == 128 ? shared_join<128, kJoinWarps>
-                                             : shared_join<256, kJoinWarps>;
-  return launch(many ? four : one, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, 0, a, o, s);
+  const int64_t warps = static_cast<int64_t>(a.batch) * o.max_q_len * a.hq;
+  const JoinFn fn = own->head_dim == 64 ? shared_join<64> : own->head_dim == 128 ? shared_join<128> : shared_join<256>;
+  return launch(fn, dim3(static_cast<unsigned>((warps + 7) / 8)), 256, 0, 1, a, o, s);
 }
 
 }  // namespace pda

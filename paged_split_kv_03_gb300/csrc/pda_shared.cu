@@ -48,7 +48,7 @@ constexpr float kTh = 8.0f;         // lazy rescale threshold, log2 units
 constexpr int kUnit = 16384;   // bytes of a ring unit
 constexpr int kItems = 3;      // slots of the segment ring
 constexpr int kScales = 4;     // slots of the ring of per-token scales, a tile each
-constexpr int kCoarse = 64;    // prefix entries, 32 groups each
+constexpr int kCoarse = 32;    // prefix entries, 32 groups each
 constexpr int kMaxGroups = 32 * kCoarse;
 constexpr int kTmemCols = 512;
 constexpr int kO = 2 * kKeys;  // first TMEM column of O; two S in front of it
@@ -75,6 +75,7 @@ struct Shared {
   Item items[kItems];
   int coarse[kCoarse];           // work in front of every 32 groups
   int coarse_items[kCoarse];     // items there
+  int coarse_singles[kCoarse];   // tiles of single row tiles there
   float2 rows[kTile];            // a row's power of two; then its maximum and sum in the odd tiles
 };
 
@@ -532,24 +533,28 @@ template <int kG>
 __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<kG> look) {
   constexpr int kRows = kG * kTile;
   const int lane = threadIdx.x & 31;
-  int work = 0, items = 0;
-  int lane_work = 0, lane_items = 0;  // in front of this lane's group, among the 32
+  int work = 0, items = 0, singles = 0;
+  int lane_work = 0, lane_items = 0, lane_singles = 0;  // in front of this lane's group, among the 32
   uint32_t bits = 0u;
   int known = 0;  // the 32 groups that `look` holds
-  auto sums = [&](int& w32, int& i32) {
-    const int w = a.hkv * look.w.head(0), i = a.hkv * look.w.blocks;
-    if (a.groups == 1) {
-      lane_work = lane_items = 0;
-      w32 = __shfl_sync(0xffffffffu, w, 0);
-      i32 = __shfl_sync(0xffffffffu, i, 0);
-      return;
+  auto sums = [&](int& w32, int& i32, int& s32) {
+    const int w = a.hkv * look.w.head(Cut()), i = a.hkv * look.w.blocks;
+    const int s = look.w.single ? a.hkv * look.w.tiles : 0;
+    int wx = w, ix = i, sx = s, last = 0;
+    if (a.groups > 1) {
+      wx = scan32(w, lane);
+      ix = scan32(i, lane);
+      sx = scan32(s, lane);
+      last = 31;
     }
-    const int wx = scan32(w, lane), ix = scan32(i, lane);
     lane_work = wx - w;
     lane_items = ix - i;
-    w32 = __shfl_sync(0xffffffffu, wx, 31);
-    i32 = __shfl_sync(0xffffffffu, ix, 31);
+    lane_singles = sx - s;
+    w32 = __shfl_sync(0xffffffffu, wx, last);
+    i32 = __shfl_sync(0xffffffffu, ix, last);
+    s32 = __shfl_sync(0xffffffffu, sx, last);
   };
+  int w32, i32, s32;
 #pragma unroll 1
   for (int g0 = 0; g0 < a.groups; g0 += 32) {
     if (g0) {
@@ -557,20 +562,23 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<
       look.at(a, g0 + lane);
     }
     bits |= look.r.bad;
-    int w32, i32;
-    sums(w32, i32);
+    sums(w32, i32, s32);
     if (lane == 0) {
       sh->coarse[known] = work;
       sh->coarse_items[known] = items;
+      sh->coarse_singles[known] = singles;
     }
     work += w32;
     items += i32;
+    singles += s32;
   }
-  int per, pay;
-  cut_of(work, items, a.ctas, per, pay);
+  const Cut cut(a, work, singles, items);
+  const int per = cut.per, pay = cut.pay;
+  auto place = [&](int w, int i, int s) { return w - s * (kFull - cut.one) + i * pay; };
+  auto coarse = [&](int c) { return place(sh->coarse[c], sh->coarse_items[c], sh->coarse_singles[c]); };
   __syncwarp();
   int pos = blockIdx.x * per;  // (a CTA too many stands at most `per` behind the end)
-  const int stop = min(work + pay * items, pos + per);
+  const int stop = min(place(work, items, singles), pos + per);
   uint32_t n = 0;
   for (;;) {
     Item it = {};
@@ -580,21 +588,21 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<
       int c = 0, top = (a.groups + 31) / 32 - 1;
       while (c < top) {
         const int mid = (c + top + 1) >> 1;
-        if (sh->coarse[mid] + pay * sh->coarse_items[mid] <= pos) c = mid;
+        if (coarse(mid) <= pos) c = mid;
         else top = mid - 1;
       }
       if (c != known) {
         known = c;
         look.at(a, 32 * c + lane);
-        int w32, i32;
-        sums(w32, i32);
+        sums(w32, i32, s32);
       }
-      const int start = sh->coarse[c] + lane_work + pay * (sh->coarse_items[c] + lane_items);
-      const int head = look.w.head(pay);
+      const int start = coarse(c) + place(lane_work, lane_items, lane_singles);
+      const int head = look.w.head(cut);
       const int src = __ffs(__ballot_sync(0xffffffffu, start + a.hkv * head > pos)) - 1;
       auto from = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
-      const int blocks = from(look.w.blocks), tiles = from(look.w.tiles), last = from(look.w.last);
-      const uint32_t head_len = from(head), full = from(look.w.full(pay));
+      const int blocks = from(look.w.blocks), tiles = from(look.w.tiles);
+      const int last = from(look.w.weight(cut, look.w.blocks - 1));
+      const uint32_t head_len = from(head), full = from(look.w.full(cut));
       uint32_t in = pos - from(start);
       const int h = in / head_len;
       in -= h * head_len;
@@ -649,16 +657,15 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<
   if (lane == 0) {
     a.first[0] = per;
     a.first[1] = pay;
+    a.first[2] = cut.one;
     if (bits) atomicOr(a.status, bits);
   }
   if (a.groups <= 32) return;
 #pragma unroll 1
   for (int g0 = 0; g0 < a.groups; g0 += 32) {
     look.at(a, g0 + lane);
-    int w32, i32;
-    sums(w32, i32);
-    if (g0 + lane < a.groups)
-      a.first[2 + g0 + lane] = sh->coarse[g0 >> 5] + lane_work + pay * (sh->coarse_items[g0 >> 5] + lane_items);
+    sums(w32, i32, s32);
+    if (g0 + lane < a.groups) a.first[3 + g0 + lane] = coarse(g0 >> 5) + place(lane_work, lane_items, lane_singles);
   }
 }
 
@@ -1173,10 +1180,12 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
 // Mathematics: the whole pages in front of a group's rows whose ids are those of its
 // first request: n = min over requests of the equal leading ids, at most (L - R) / P.
 //
-// Bound: latency. A cluster of CTAs per group, a warp per request; a warp stops where
-// another has found a shorter prefix.
+// Bound: latency. A cluster of CTAs per group; its warps take stretches of the requests'
+// lists in turn, the first of all requests first, and leave out those behind what another
+// has found to be the end.
 constexpr int kShareThreads = 256;
 constexpr int kShareWarps = kShareThreads / 32;
+constexpr int kStretch = 256;  // ids of a stretch
 
 struct TablesArgs {
   pda_shared_tables t;
@@ -1228,43 +1237,44 @@ __global__ void __launch_bounds__(kShareThreads) share_tables(const __grid_const
   if (lead >= 0) {
     const int32_t* theirs = a.t.page_table + __ldg(a.t.kv_indptr + lead);
     const int most = __ldg(a.t.kv_indptr + lead + 1) - __ldg(a.t.kv_indptr + lead);
-    for (int b = b0 + static_cast<int>(rank) * kShareWarps + warp; b < b1;
-         b += static_cast<int>(ctas) * kShareWarps) {
+    const int n_req = b1 - b0, step = static_cast<int>(ctas) * kShareWarps;
+    const int stretches = (max(most, 0) + kStretch - 1) / kStretch;
+    // (at least one: it notes the request's first token seen, and its own length)
+    const int64_t work = static_cast<int64_t>(n_req) * max(stretches, 1);
+    for (int64_t k = static_cast<int64_t>(rank) * kShareWarps + warp; k < work; k += step) {
+      const int stretch = static_cast<int>(k / n_req), b = b0 + static_cast<int>(k % n_req);
+      const int j0 = stretch * kStretch;
+      if (j0 && j0 >= static_cast<int>(cluster_load(pages_at))) break;  // as are all behind it
       int rows, len;
       if (!fits(b, rows, len)) continue;
       const int at = __ldg(a.t.kv_indptr + b);
       const int32_t* mine = a.t.page_table + at;
-      int n = min(min((len - rows) / a.page_size, most), __ldg(a.t.kv_indptr + b + 1) - at);
-      n = min(max(n, 0), static_cast<int>(cluster_load(pages_at)));
-      int equal = n;
-      for (int j = 0; j < n; j += 128) {
-        bool ok[4];
+      const int all = max(0, min(min((len - rows) / a.page_size, most), __ldg(a.t.kv_indptr + b + 1) - at));
+      const int n = min(all, j0 + kStretch);
+      int equal = all;
+      bool ok[kStretch / 32];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int e = j + k * 32 + lane;
-          ok[k] = true;
-          if (e < n) {
-            const int id = __ldg(mine + e);
-            ok[k] = id == __ldg(theirs + e) && id >= 0 && id < a.num_pages;
-          }
-        }
-        int stop = -1;
-#pragma unroll
-        for (int k = 3; k >= 0; --k) {
-          const uint32_t differ = __ballot_sync(0xffffffffu, !ok[k]);
-          if (differ) stop = j + k * 32 + __ffs(differ) - 1;
-        }
-        if (stop >= 0) {
-          equal = stop;
-          break;
+      for (int e = 0; e < kStretch / 32; ++e) {
+        const int j = j0 + e * 32 + lane;
+        ok[e] = true;
+        if (j < n) {
+          const int id = __ldg(mine + j);
+          ok[e] = id == __ldg(theirs + j) && id >= 0 && id < a.num_pages;
         }
       }
+#pragma unroll
+      for (int e = kStretch / 32 - 1; e >= 0; --e) {
+        const uint32_t differ = __ballot_sync(0xffffffffu, !ok[e]);
+        if (differ) equal = j0 + e * 32 + __ffs(differ) - 1;
+      }
       if (lane == 0) {
-        const int w = a.t.window ? __ldg(a.t.window + b) : 0;
         least(pages_at, equal);
-        least(low_at, w > 0 ? static_cast<int>(max(static_cast<int64_t>(0),
-                                                   static_cast<int64_t>(len) - rows - w + 1))
-                            : 0);
+        if (stretch == 0) {
+          const int w = a.t.window ? __ldg(a.t.window + b) : 0;
+          least(low_at, w > 0 ? static_cast<int>(max(static_cast<int64_t>(0),
+                                                     static_cast<int64_t>(len) - rows - w + 1))
+                              : 0);
+        }
       }
     }
   }
@@ -1415,11 +1425,10 @@ extern "C" int pda_shared_plan(const pda_plan_t* plan, int32_t groups, int32_t m
     at += up256(bytes);
     return here;
   };
-  // parts of the own tokens: stage 1's, or one a row, or none that are kept
-  const int64_t parts = !own_here(&sp.own) ? sp.own.max_splits * cells : parts_apart(&sp.own) ? cells : 0;
+  const int64_t parts = own_here(&sp.own) ? 0 : sp.own.max_splits * cells;  // of stage 1
   sp.own.scratch_lse_offset = take(parts * 4);
   sp.own.scratch_o_offset = take(parts * d * 4);
-  sp.first_offset = take((2 + static_cast<int64_t>(groups)) * 4);
+  sp.first_offset = take((3 + static_cast<int64_t>(groups)) * 4);
   sp.main_lse_offset = take(cells * 4);
   sp.main_o_offset = take(cells * d * 4);
   sp.area_lse_offset = take(area * 4);
@@ -1448,8 +1457,9 @@ extern "C" int pda_share_tables(const pda_shared_plan_t* sp, const pda_shared_ta
   a.max_q_len = sp->own.max_q_len;
   a.max_kv_len = sp->max_kv_len;
   a.num_pages = sp->own.num_pages;
-  // eight CTAs a group, where a group's requests have a warp each for it
-  const unsigned ctas = static_cast<int64_t>(sp->groups) * kShareWarps < sp->own.batch ? 8 : 1;
+  // (eight CTAs a group at most, while they are not more than four an SM)
+  unsigned ctas = 8;
+  while (ctas > 1 && static_cast<int64_t>(sp->groups) * ctas > 4LL * sp->own.num_sms) ctas /= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
@@ -1534,10 +1544,7 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   k.fn<<<static_cast<unsigned>(a.ctas), k.threads, k.smem, s>>>(a, tk, tv);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-  const bool here = own_here(plan), apart = parts_apart(plan);
-  a.parts_apart = here && apart;
-  if (here) rc = launch_own(plan, a, o, s);
-  else if (plan->kernel == PDA_KERNEL_TC) rc = launch_stage1_tc(plan, o, s, true);
-  else rc = launch_stage1_mma(plan, o, s, true);
-  return rc == PDA_OK && (!here || apart) ? launch_join(plan, a, o, s) : rc;
+  if (own_here(plan)) return launch_own(plan, a, o, s);
+  rc = plan->kernel == PDA_KERNEL_TC ? launch_stage1_tc(plan, o, s, true) : launch_stage1_mma(plan, o, s, true);
+  return rc == PDA_OK ? launch_join(plan, a, o, s) : rc;
 }

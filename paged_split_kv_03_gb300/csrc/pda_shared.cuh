@@ -31,7 +31,7 @@ struct SharedArgs {
   float* main_x;    // ... and their log2 sums
   float* area_o;    // [CTA][rows of an item][D]: the segment a CTA starts inside an item
   float* area_x;
-  int* first;       // the cut (per, pay), then [groups] where each group's work starts
+  int* first;       // the cut (per, pay, one), then [groups] where each group's work starts
   uint32_t* status;
   uint64_t wait_limit_ns;
   float sm_scale;
@@ -40,15 +40,12 @@ struct SharedArgs {
   int q8;
   int ctas;  // of the prefix kernel
   int one;   // what a tile of a block of at most 128 rows counts
-  int parts_apart;  // own tokens' kernel: its parts go to stage 1's place, one a row, for the join
   uint32_t inject;
 };
 
-// Whether the requests' own tokens have a kernel of their own here (else stage 1), and
-// whether the join has one (else that kernel's last part). They start beside the kernel in
-// front of them and end behind the prefix kernel.
+// Whether the requests' own tokens and the join are one kernel (else stage 1, then the
+// join). Both start beside the kernel in front of them and end behind the prefix kernel.
 bool own_here(const pda_plan_t* own);
-bool parts_apart(const pda_plan_t* own);
 int launch_own(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, cudaStream_t s);
 int launch_join(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, cudaStream_t s);
 
@@ -89,35 +86,47 @@ __device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
 
 // How the work is cut. An item is a block of kRows packed rows of a kv head, over the
 // prefix's key tiles; group by group, then kv heads, then blocks, the items stand on one
-// axis, and CTA c has the stretch [c per, (c + 1) per) of it: the tiles that begin there. A
-// tile counts kFull, or `one` in a last block of one row tile, whose time is that of
-// its loads. An item is longer by `pay` in front of its tiles: a CTA's further segment
-// costs it a query load and an epilogue, about three tiles' time (64 requests behind 8192
-// tokens, 64 / 8 heads of 128: CTAs of two segments ended at 34 us, the others at 23).
-// Without it where a CTA has less than two tiles: most would be left without any. The
-// plan keeps the axis below 2^31.
+// axis, and CTA c has the stretch [c per, (c + 1) per) of it: the tiles that begin there.
+// Where the CTAs have less than two tiles each, a tile counts kFull. Else it counts `one`
+// in a last block of one row tile, whose time is that of its loads, and an item is
+// longer by `pay` in front of its tiles: a CTA's further segment costs it a query load
+// and an epilogue, about three tiles' time (64 requests behind 8192 tokens, 64 / 8 heads
+// of 128: CTAs of two segments ended at 34 us, the others at 23). The plan keeps the axis
+// below 2^31.
 constexpr int kFull = 8, kPay = 3 * kFull;
+struct Cut {
+  int per = 1, pay = 0, one = kFull;
+  __device__ __forceinline__ Cut() {}
+  // from the work at kFull a tile, the tiles of single row tiles, and the items
+  __device__ __forceinline__ Cut(const SharedArgs& a, int work, int singles, int items) {
+    if (work > a.ctas * (2 * kFull - 1)) {
+      pay = kPay;
+      one = a.one;
+    }
+    const uint32_t all = work - singles * (kFull - one) + pay * items;
+    per = max(kFull, static_cast<int>((all + a.ctas - 1) / static_cast<uint32_t>(a.ctas)));
+  }
+};
 template <int kG>
 struct Work {
-  int blocks = 0, tiles = 0, last = 0;  // last: what a tile of the last block counts
+  int blocks = 0, tiles = 0;
+  bool single = false;  // the last block has one row tile, of two
   __device__ __forceinline__ Work() {}
   __device__ __forceinline__ Work(const SharedArgs& a, const Group& r) {
     const int packed = r.rows * a.group;
     tiles = r.tiles;
     if (tiles == 0) return;
     blocks = (packed + kG * kTile - 1) / (kG * kTile);
-    last = kG == 1 || packed - (blocks - 1) * (kG * kTile) > kTile ? kFull : a.one;
+    single = kG == 2 && packed - (blocks - 1) * (kG * kTile) <= kTile;
   }
-  __device__ __forceinline__ int full(int pay) const { return kFull * tiles + pay; }
+  __device__ __forceinline__ int full(const Cut& c) const { return kFull * tiles + c.pay; }
+  // of a tile of block b
+  __device__ __forceinline__ int weight(const Cut& c, int b) const { return single && b == blocks - 1 ? c.one : kFull; }
   // of a kv head
-  __device__ __forceinline__ int head(int pay) const {
-    return blocks ? (blocks - 1) * full(pay) + last * tiles + pay : 0;
+  __device__ __forceinline__ int head(const Cut& c) const {
+    return blocks ? (blocks - 1) * full(c) + weight(c, blocks - 1) * tiles + c.pay : 0;
   }
 };
-__device__ __forceinline__ void cut_of(int work, int items, int ctas, int& per, int& pay) {
-  pay = work <= ctas * (2 * kFull - 1) ? 0 : kPay;
-  per = max(kFull, static_cast<int>((static_cast<uint32_t>(work + pay * items) + ctas - 1) / static_cast<uint32_t>(ctas)));
-}
 __device__ __forceinline__ int scan32(int x, int lane) {
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -131,7 +140,8 @@ __device__ __forceinline__ int scan32(int x, int lane) {
 template <int kG>
 struct Parts {
   Group gr;
-  int g = 0, first = 0, per = 1, pay = 0;
+  Cut cut;
+  int g = 0, first = 0;
   // Of the group of request b; a whole warp. What the prefix kernel wrote down (more groups
   // than lanes) is read by `late`, behind that kernel.
   __device__ __forceinline__ Parts(const SharedArgs& a, int b) {
@@ -146,21 +156,25 @@ struct Parts {
     if (a.groups > 32) return;
     Work<kG> w;
     if (lane < a.groups) w = Work<kG>(a, a.groups == 1 ? gr : group_of(a, lane));
-    const int mine = a.hkv * w.head(0), items = a.hkv * w.blocks;
-    int work = mine, upto = items;
+    const int mine = a.hkv * w.head(Cut()), singles = w.single ? a.hkv * w.tiles : 0, items = a.hkv * w.blocks;
+    int upto = mine, upto_s = singles, upto_i = items;
     if (a.groups > 1) {
-      work = scan32(mine, lane);
-      upto = scan32(items, lane);
+      upto = scan32(mine, lane);
+      upto_s = scan32(singles, lane);
+      upto_i = scan32(items, lane);
     }
     const int last = a.groups > 1 ? 31 : 0;
-    cut_of(__shfl_sync(0xffffffffu, work, last), __shfl_sync(0xffffffffu, upto, last), a.ctas, per, pay);
-    first = __shfl_sync(0xffffffffu, work - mine + pay * (upto - items), g);
+    cut = Cut(a, __shfl_sync(0xffffffffu, upto, last), __shfl_sync(0xffffffffu, upto_s, last),
+              __shfl_sync(0xffffffffu, upto_i, last));
+    const int before = upto - mine - (upto_s - singles) * (kFull - cut.one) + (upto_i - items) * cut.pay;
+    first = __shfl_sync(0xffffffffu, before, g);
   }
   __device__ __forceinline__ void late(const SharedArgs& a) {
     if (a.groups <= 32) return;
-    per = a.first[0];
-    pay = a.first[1];
-    first = a.first[2 + g];
+    cut.per = a.first[0];
+    cut.pay = a.first[1];
+    cut.one = a.first[2];
+    first = a.first[3 + g];
   }
 };
 // ... of packed row m and kv head h: how many, and each one's log2 sum and output.
@@ -168,6 +182,7 @@ template <int kG, int D>
 struct RowParts {
   int segs = 0, c0 = 0, r = 0;
   int64_t head_row = 0;
+  __device__ __forceinline__ RowParts() {}
   __device__ __forceinline__ RowParts(const SharedArgs& a, const Parts<kG>& p, int h, int m) {
     constexpr int kRows = kG * kTile;
     const int block = m / kRows;
@@ -175,11 +190,11 @@ struct RowParts {
     head_row = (h * a.rows_cap + p.gr.q0) * a.group + m;
     if (p.gr.tiles == 0) return;
     const Work<kG> w(a, p.gr);
-    const int count = block == w.blocks - 1 ? w.last : kFull;
     // its first and its last tile
-    const int u = p.first + h * w.head(p.pay) + block * w.full(p.pay) + p.pay;
-    c0 = u / p.per;
-    segs = (u + (p.gr.tiles - 1) * count) / p.per - c0 + 1;
+    const uint32_t u = p.first + h * w.head(p.cut) + block * w.full(p.cut) + p.cut.pay;
+    const uint32_t per = p.cut.per;
+    c0 = u / per;
+    segs = (u + (p.gr.tiles - 1) * w.weight(p.cut, block)) / per - c0 + 1;
   }
   __device__ __forceinline__ void part(const SharedArgs& a, int s, const float*& x, const float*& v) const {
     const int64_t at = s == 0 ? head_row : static_cast<int64_t>(c0 + s) * (kG * kTile) + r;
@@ -188,14 +203,16 @@ struct RowParts {
   }
 };
 
-// The running sum of a row's parts, kV channels a lane.
-template <int kV>
+// The running sum of a row's parts, in kLanes neighbouring lanes.
+template <int D, int kLanes>
 struct Join {
+  static constexpr int kV = D / kLanes;  // channels of a lane
   float top = -INFINITY, sum = 0.f, acc[kV];
   __device__ __forceinline__ Join() {
 #pragma unroll
     for (int e = 0; e < kV; ++e) acc[e] = 0.f;
   }
+  static __device__ __forceinline__ int first() { return threadIdx.x % kLanes * kV; }
   __device__ __forceinline__ void raise(float to) {
     if (!(to > top)) return;
     const float f = exp2f(top - to);  // -inf: nothing summed yet
@@ -207,7 +224,7 @@ struct Join {
   // kBatch parts at most at a time, their loads in front of their use
   template <int kBatch, class Place>
   __device__ __forceinline__ void add(int parts, Place&& place) {
-    const int lane = threadIdx.x & 31;
+#pragma unroll 1
     for (int s0 = 0; s0 < parts; s0 += kBatch) {
       float x[kBatch], v[kBatch][kV];
 #pragma unroll
@@ -218,13 +235,13 @@ struct Join {
           place(s0 + k, px, pv);
           x[k] = *px;
           if constexpr (kV == 2) {
-            const float2 t = *reinterpret_cast<const float2*>(pv + lane * 2);
+            const float2 t = *reinterpret_cast<const float2*>(pv + first());
             v[k][0] = t.x;
             v[k][1] = t.y;
           } else {
 #pragma unroll
             for (int e = 0; e < kV; e += 4) {
-              const float4 t = *reinterpret_cast<const float4*>(pv + lane * kV + e);
+              const float4 t = *reinterpret_cast<const float4*>(pv + first() + e);
               v[k][e] = t.x;
               v[k][e + 1] = t.y;
               v[k][e + 2] = t.z;
@@ -248,26 +265,23 @@ struct Join {
       }
     }
   }
-  // as one more part
-  __device__ __forceinline__ void keep(float* x, float* v) const {
-    const int lane = threadIdx.x & 31;
-    const float inv = sum > 0.f ? 1.f / sum : sum;  // (NaN stays)
-#pragma unroll
-    for (int e = 0; e < kV; ++e) v[lane * kV + e] = acc[e] * inv;
-    if (lane == 0) *x = sum == 0.f ? -INFINITY : top + __log2f(sum);
-  }
   // the row's results; `row`: of out and lse
   __device__ __forceinline__ void write(const DecodeArgs& o, int64_t row) const {
-    const int lane = threadIdx.x & 31;
     const float inv = sum > 0.f ? 1.f / sum : sum;  // (NaN stays)
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.out) + row * (32 * kV) + lane * kV;
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(o.out) + row * D + first();
     uint32_t w[kV / 2];
 #pragma unroll
     for (int e = 0; e < kV; e += 2) w[e / 2] = bf16x2(acc[e] * inv, acc[e + 1] * inv);
-    if constexpr (kV == 2) *reinterpret_cast<uint32_t*>(dst) = w[0];
-    else if constexpr (kV == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (lane == 0 && o.lse) o.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
+    if constexpr (kV == 2) {
+      *reinterpret_cast<uint32_t*>(dst) = w[0];
+    } else if constexpr (kV == 4) {
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kV / 2; e += 4)
+        *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+    }
+    if (first() == 0 && o.lse) o.lse[row] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * kLn2;
   }
 };
 
