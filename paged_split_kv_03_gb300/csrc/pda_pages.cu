@@ -65,6 +65,7 @@ __device__ __forceinline__ Fork fork_of(const ForkArgs& a, int i) {
 __global__ void __launch_bounds__(kThreads) fork_tables(const __grid_constant__ ForkArgs a) {
   __shared__ int sums[kWarps];
   __shared__ int upto_s[kThreads];  // pages taken up to and with each of this CTA's forks
+  grid_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n = a.f.forks;
   const int per_cta = (n + gridDim.x - 1) / gridDim.x;
@@ -172,6 +173,7 @@ struct CopyArgs {
 };
 
 __global__ void __launch_bounds__(kThreads) copy_pages(const __grid_constant__ CopyArgs a) {
+  grid_wait();
   int n = a.copies;
   if (a.num_copies) n = min(n, __ldg(a.num_copies));
   const int64_t units = static_cast<int64_t>(max(n, 0)) * a.sides * a.pieces;
@@ -255,6 +257,24 @@ __device__ __forceinline__ int entries_of(const PagesArgs& a, int r, int64_t& ro
   return a.p.table_cols;
 }
 
+// Marks kAtOnce ids (-1: none) in `bits`, their loads together and atomics for unset bits only
+// (ids that many requests share are set once and read often).
+constexpr int kAtOnce = 4;
+__device__ __forceinline__ void mark(const PagesArgs& a, uint32_t* bits, const int (&id)[kAtOnce], uint32_t& bad) {
+  uint32_t held[kAtOnce];
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k) {
+    held[k] = 0xffffffffu;
+    if (id[k] >= 0 && id[k] < a.num_pages) held[k] = *const_cast<volatile uint32_t*>(bits + (id[k] >> 5));
+    else if (id[k] != -1) bad |= PDA_STATUS_PAGE_OOB;
+  }
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k) {
+    const uint32_t bit = 1u << (id[k] & 31);
+    if (!(held[k] & bit)) atomicOr(bits + (id[k] >> 5), bit);
+  }
+}
+
 __global__ void __launch_bounds__(kThreads) mark_pages(const __grid_constant__ PagesArgs a) {
   grid_launch();
   uint32_t bad = 0u;
@@ -263,77 +283,83 @@ __global__ void __launch_bounds__(kThreads) mark_pages(const __grid_constant__ P
     const int n = entries_of(a, r, row, bad);
     const int32_t* ids = a.p.block_table + row * a.p.table_stride;
     const int step = static_cast<int>(gridDim.y) * kThreads;
-#pragma unroll 4
-    for (int j = blockIdx.y * kThreads + threadIdx.x; j < n; j += step) {
-      const int id = __ldg(ids + j);
-      if (id < 0 || id >= a.num_pages) {
-        bad |= PDA_STATUS_PAGE_OOB;
-        continue;
+    for (int j0 = blockIdx.y * kThreads + threadIdx.x; j0 < n; j0 += kAtOnce * step) {
+      int id[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        id[k] = -1;
+        if (j0 + k * step < n) {
+          id[k] = __ldg(ids + j0 + k * step);
+          if (id[k] == -1) bad |= PDA_STATUS_PAGE_OOB;
+        }
       }
-      const uint32_t bit = 1u << (id & 31);
-      volatile uint32_t* word = a.bits + (id >> 5);
-      if (!(*word & bit)) atomicOr(a.bits + (id >> 5), bit);
+      mark(a, a.bits, id, bad);
     }
   }
   if (bad) atomicOr(a.status, bad);
 }
 
-__device__ __forceinline__ uint32_t free_word(const PagesArgs& a, int w) {
-  const uint32_t live = *(a.bits + w);
+__device__ __forceinline__ uint32_t free_word(const PagesArgs& a, const uint32_t* bits, int w) {
   const int left = a.num_pages - (w << 5);
-  return ~live & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
+  return ~bits[w] & (left >= 32 ? 0xffffffffu : (1u << left) - 1u);
 }
 
-// Sum over the block of one value per thread.
+// Sum over the block of one value per thread. (One-shot code is bound by its instructions'
+// way from memory, so it is kept short here and below.)
+template <int kT>
 __device__ __forceinline__ int block_sum(int v, int* sh) {
+  const int lane = threadIdx.x & 31;
   v = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
+  if (lane == 0) sh[threadIdx.x >> 5] = v;
   __syncthreads();
-  int t = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) t += sh[w];
-  return t;
+  return __reduce_add_sync(0xffffffffu, lane < kT / 32 ? sh[lane] : 0);
 }
 
-__global__ void __launch_bounds__(kThreads) list_pages(const __grid_constant__ PagesArgs a) {
-  __shared__ int sh[kWarps];
-  grid_launch();
-  grid_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int w0 = blockIdx.x * a.words_per_cta, w1 = min(a.words, w0 + a.words_per_cta);
-  int all = 0, before = 0;
-  for (int w = tid; w < a.words; w += kThreads) {
-    const int f = __popc(free_word(a, w));
-    all += f;
-    before += w < w0 ? f : 0;
+// Free ids of words [from, to), from a multiple of 4, over the block's threads.
+template <int kT>
+__device__ __forceinline__ int count_free(const PagesArgs& a, const uint32_t* bits, int from, int to) {
+  int n = 0;
+  // (whole vectors stay inside the marks, whose memory is a multiple of 256 bytes; the last
+  // word's ids past the cache, and words from `to` on, do not count)
+#pragma unroll(kT == kThreads ? 4 : 1)
+  for (int w = from + 4 * static_cast<int>(threadIdx.x); w < to; w += 4 * kT) {
+    const uint4 v = *reinterpret_cast<const uint4*>(bits + w);
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (w + e < to) n += __popc(~x[e]);
   }
-  all = block_sum(all, sh);
-  before = block_sum(before, sh);
-  const int live = a.num_pages - all;
-  int moves = 0;
+  if (threadIdx.x == 0 && to == a.words && from < to) n -= (a.words << 5) - a.num_pages;
+  return n;
+}
+
+// Lists the free ids of words [w0, w1) (multiples of 4, or the end) and the moves there.
+template <int kT>
+__device__ __forceinline__ void list_words(const PagesArgs& a, const uint32_t* bits, int32_t* below, int w0, int w1,
+                                           bool writes, int* sh, int& live, int& moves) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int before = block_sum<kT>(count_free<kT>(a, bits, 0, w0), sh);
+  const int all = before + block_sum<kT>(count_free<kT>(a, bits, w0, a.words), sh);
+  live = a.num_pages - all;
+  moves = 0;
   if (a.compact) {
     // holes below the live count
-    int holes = 0;
-    for (int w = tid; w <= live >> 5 && w < a.words; w += kThreads) {
-      uint32_t f = free_word(a, w);
-      if (w == live >> 5) f &= (1u << (live & 31)) - 1u;
-      holes += __popc(f);
-    }
-    moves = min(block_sum(holes, sh), a.p.max_copies);
+    int holes = count_free<kT>(a, bits, 0, live >> 5);
+    if (threadIdx.x == 0 && (live & 31)) holes += __popc(free_word(a, bits, live >> 5) & ((1u << (live & 31)) - 1u));
+    moves = min(block_sum<kT>(holes, sh), a.p.max_copies);
   }
-  if (blockIdx.x == 0 && tid == 0) {
+  if (writes && threadIdx.x == 0) {
     *a.p.free_left = all;
-    if (a.compact) {
-      *a.p.num_copies = moves;
-      a.head[1] = live;
-      a.head[2] = moves;
-    }
+    if (a.compact) *a.p.num_copies = moves;
   }
   // a warp to 32 words at a time: the words' prefix, then a word a step, a lane an id
-  for (int g = w0; g < w1; g += 32 * kWarps) {
-    const int w = g + warp * 32 + lane;
-    const uint32_t mine = w < w1 ? free_word(a, w) : 0u;
+  constexpr int kW = kT / 32;
+  const int each = max(1, min(32, (w1 - w0 + kW - 1) / kW));  // words of a warp's turn
+#pragma unroll 1
+  for (int g = w0; g < w1; g += each * kW) {
+    const int w = g + warp * each + lane;
+    const uint32_t mine = lane < each && w < w1 ? free_word(a, bits, w) : 0u;
     const int count = __popc(mine);
     int x = count;
 #pragma unroll
@@ -344,15 +370,13 @@ __global__ void __launch_bounds__(kThreads) list_pages(const __grid_constant__ P
     __syncthreads();
     if (lane == 31) sh[warp] = x;
     __syncthreads();
-    int start = before + x - count;
-#pragma unroll
-    for (int v = 0; v < kWarps; ++v) {
-      if (v < warp) start += sh[v];
-      before += sh[v];
-    }
-    if (a.compact && w < w1) a.below[w] = start;
-    for (int k = 0; k < 32; ++k) {
-      const int wk = g + warp * 32 + k;
+    const int of_warp = lane < kW ? sh[lane] : 0;
+    const int start = before + x - count + __reduce_add_sync(0xffffffffu, lane < warp ? of_warp : 0);
+    before += __reduce_add_sync(0xffffffffu, of_warp);
+    if (a.compact && lane < each && w < w1) below[w] = start;
+#pragma unroll 1
+    for (int k = 0; k < each; ++k) {
+      const int wk = g + warp * each + k;
       if (wk >= w1) break;  // (the same for the whole warp)
       const uint32_t f = __shfl_sync(0xffffffffu, mine, k);
       const int fb = __shfl_sync(0xffffffffu, start, k) + __popc(f & ((1u << lane) - 1u));
@@ -369,18 +393,44 @@ __global__ void __launch_bounds__(kThreads) list_pages(const __grid_constant__ P
       }
     }
   }
+}
+
+__global__ void __launch_bounds__(kThreads) list_pages(const __grid_constant__ PagesArgs a) {
+  __shared__ int sh[kWarps];
+  grid_launch();
+  grid_wait();
+  const int w0 = blockIdx.x * a.words_per_cta, w1 = min(a.words, w0 + a.words_per_cta);
+  int live, moves;
+  list_words<kThreads>(a, a.bits, a.below, w0, w1, blockIdx.x == 0, sh, live, moves);
+  if (a.compact) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      a.head[1] = live;
+      a.head[2] = moves;
+    }
+    return;
+  }
   // the last CTA to get here clears the marks for the next call (compaction: later)
-  if (a.compact) return;
   __shared__ int last;
   __syncthreads();
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     __threadfence();
     last = atomicAdd(a.head, 1) == static_cast<int>(gridDim.x) - 1;
   }
   __syncthreads();
   if (!last) return;
-  for (int w = tid; w < a.words; w += kThreads) a.bits[w] = 0u;
-  if (tid == 0) a.head[0] = 0;
+  for (int w = threadIdx.x; w < a.words; w += kThreads) a.bits[w] = 0u;
+  if (threadIdx.x == 0) a.head[0] = 0;
+}
+
+// What page `id` is called after the moves.
+__device__ __forceinline__ int renamed(const PagesArgs& a, const uint32_t* bits, const int32_t* below, int live,
+                                       int moves, int id) {
+  if (moves == 0 || id < live || id >= a.num_pages) return id;
+  const int w = id >> 5;
+  const uint32_t f = free_word(a, bits, w);
+  const int fb = below[w] + __popc(f & ((1u << (id & 31)) - 1u));
+  const int k = live - 1 - (id - fb);
+  return !(f >> (id & 31) & 1u) && k < moves ? a.p.copy_dst[k] : id;
 }
 
 // The tables after the moves.
@@ -394,17 +444,8 @@ __global__ void __launch_bounds__(kThreads) renumber(const __grid_constant__ Pag
     const int32_t* ids = a.p.block_table + row * a.p.table_stride;
     int32_t* to = a.p.new_table + row * a.p.table_stride;
     const int step = static_cast<int>(gridDim.y) * kThreads;
-    for (int j = blockIdx.y * kThreads + threadIdx.x; j < n; j += step) {
-      int id = ids[j];
-      if (moves > 0 && id >= live && id < a.num_pages) {
-        const int w = id >> 5;
-        const uint32_t f = free_word(a, w);
-        const int fb = a.below[w] + __popc(f & ((1u << (id & 31)) - 1u));
-        const int k = live - 1 - (id - fb);
-        if (!(f >> (id & 31) & 1u) && k < moves) id = a.p.copy_dst[k];
-      }
-      to[j] = id;
-    }
+    for (int j = blockIdx.y * kThreads + threadIdx.x; j < n; j += step)
+      to[j] = renamed(a, a.bits, a.below, live, moves, ids[j]);
   }
   __shared__ int last;
   __syncthreads();
@@ -416,6 +457,67 @@ __global__ void __launch_bounds__(kThreads) renumber(const __grid_constant__ Pag
   if (!last) return;
   for (int w = threadIdx.x; w < a.words; w += kThreads) a.bits[w] = 0u;
   if (threadIdx.x == 0) a.head[0] = 0;
+}
+
+// All of it in one CTA, the marks in shared memory, where the tables and the cache are small.
+constexpr int kOnceThreads = 1024;
+constexpr int kOnceRequests = 512;
+constexpr int kOnceEntries = 16 * kOnceThreads;  // most entries of the tables
+constexpr int kOnceWords = 4096;                 // most words of marks
+
+__global__ void __launch_bounds__(kOnceThreads) pages_once(const __grid_constant__ PagesArgs a) {
+  extern __shared__ __align__(16) uint32_t marks[];  // [words up to a multiple of 4], then `below`
+  __shared__ int sh[kOnceThreads / 32];
+  __shared__ int row_s[kOnceRequests], n_s[kOnceRequests];
+  const int words4 = (a.words + 3) / 4 * 4;
+  int32_t* below = reinterpret_cast<int32_t*>(marks + words4);
+  uint32_t bad = 0u;
+#pragma unroll 1
+  for (int w = threadIdx.x; w < words4; w += kOnceThreads) marks[w] = 0u;
+  if (threadIdx.x < a.p.requests) {
+    int64_t row;
+    n_s[threadIdx.x] = entries_of(a, threadIdx.x, row, bad);
+    row_s[threadIdx.x] = static_cast<int>(row);
+  }
+  __syncthreads();
+  const int cols = max(1, a.p.table_cols), rows_on = kOnceThreads / cols, cols_on = kOnceThreads - rows_on * cols;
+  auto each = [&](auto&& use) {  // kAtOnce entries (or -1: none) at a time
+    int r = threadIdx.x / cols, j = threadIdx.x - r * cols;
+#pragma unroll 1
+    while (r < a.p.requests) {
+      int id[kAtOnce];
+      int64_t at[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        at[k] = r < a.p.requests && j < n_s[r] ? row_s[r] * a.p.table_stride + j : -1;
+        id[k] = at[k] >= 0 ? a.p.block_table[at[k]] : -1;
+        r += rows_on;
+        j += cols_on;
+        if (j >= cols) {
+          j -= cols;
+          ++r;
+        }
+      }
+      use(id, at);
+    }
+  };
+  each([&](const int (&id)[kAtOnce], const int64_t (&at)[kAtOnce]) {
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (at[k] >= 0 && id[k] == -1) bad |= PDA_STATUS_PAGE_OOB;
+    mark(a, marks, id, bad);
+  });
+  if (bad) atomicOr(a.status, bad);
+  __syncthreads();
+  int live, moves;
+  list_words<kOnceThreads>(a, marks, below, 0, a.words, true, sh, live, moves);
+  if (!a.compact) return;
+  __syncthreads();  // (the moves' targets and `below` are there)
+  each([&](const int (&id)[kAtOnce], const int64_t (&at)[kAtOnce]) {
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (at[k] >= 0) a.p.new_table[at[k]] = renamed(a, marks, below, live, moves, id[k]);
+  });
 }
 
 bool a4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
@@ -478,13 +580,18 @@ int list_call(const pda_plan_t* plan, const pda_pages* pages, void* scratch, pda
   a.max_kv_len = plan->max_kv_len;
   a.num_pages = plan->num_pages;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (words <= kOnceWords && static_cast<int64_t>(p.requests) * p.table_cols <= kOnceEntries &&
+      p.requests <= kOnceRequests) {
+    pages_once<<<1, kOnceThreads, static_cast<size_t>((words + 3) / 4 * 4 * 8), s>>>(a);
+    return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  }
   const unsigned gx = static_cast<unsigned>(std::max(1, std::min(p.requests, 4 * plan->num_sms)));
   const unsigned gy = static_cast<unsigned>(
       std::max(1, std::min(64, (p.table_cols + 4 * kThreads - 1) / (4 * kThreads))));
   mark_pages<<<dim3(gx, gy), kThreads, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
-  // (a CTA's warps list 32 words each)
-  const int64_t least = 32 * kWarps;
+  // (a CTA's warps list 8 words each, or more)
+  const int64_t least = 8 * kWarps;
   const int64_t per = std::max(least, (words + plan->num_sms - 1) / plan->num_sms);
   a.words_per_cta = static_cast<int>(std::min<int64_t>((per + least - 1) / least * least, INT_MAX / 2));
   const unsigned gl = static_cast<unsigned>((words + a.words_per_cta - 1) / a.words_per_cta);
@@ -581,8 +688,8 @@ extern "C" int pda_copy_pages(const pda_plan_t* plan, void* k_pages, void* v_pag
   a.scale_floats = per_head * a.heads;
   const int64_t units = static_cast<int64_t>(copies) * a.sides * a.pieces;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, 8LL * plan->num_sms));
-  copy_pages<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  return cudaGetLastError() == cudaSuccess ? PDA_OK : PDA_ERR_CUDA;
+  // (behind pda_fork_tables its launch is under way while that kernel runs)
+  return launch_next(copy_pages, dim3(grid), reinterpret_cast<cudaStream_t>(stream), a);
 }
 
 extern "C" int pda_pages_scratch(const pda_plan_t* plan, size_t* scratch_bytes) {
