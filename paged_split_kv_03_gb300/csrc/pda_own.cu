@@ -224,31 +224,35 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
     pg[1] = page_at(s * kStep + 8);
   }
   bool oob = false;
-#pragma unroll 1
-  for (; s < steps; s += stride) {
-    const int t0 = s * kStep;
-    // bytes of each half's first token, or -1
-    int64_t at[2];
+  // bytes of each half's first token, or -1; its page; K: token g of each half, 16-byte
+  // pieces q, q + 4, ... of its row
+  int64_t at[2];
+  int held[2];
+  uint4 kv[2][C::kPieces];
+  auto load_k = [&](int t0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int t = t0 + 8 * e;
       const bool ok = pg[e] >= 0 && pg[e] < a.num_pages;
       oob |= !ok && t < L;
       at[e] = ok ? (pg[e] * o.sp + (t & (P - 1)) * o.st) * eb : -1;
-    }
-    const int held[2] = {pg[0], pg[1]};
-    pg[0] = page_at(t0 + stride * kStep);
-    pg[1] = page_at(t0 + stride * kStep + 8);
-    // K: token g of each half, 16-byte pieces q, q + 4, ... of its row
-    uint4 kv[2][C::kPieces];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
+      held[e] = pg[e];
+      pg[e] = page_at(t + stride * kStep);
 #pragma unroll
       for (int i = 0; i < C::kPieces; ++i) {
         kv[e][i] = make_uint4(0, 0, 0, 0);
-        if (at[e] >= 0 && t0 + 8 * e + g < L)
+        if (at[e] >= 0 && t + g < L)
           kv[e][i] = __ldg(reinterpret_cast<const uint4*>(k_base + at[e] + g * o.st * eb) + q + 4 * i);
       }
+    }
+  };
+  // the next step's K is under way during this one's softmax and O (if it fits the registers)
+  constexpr bool kAhead = k8 && !kTok;
+  if (kAhead) load_k(s * kStep);
+#pragma unroll 1
+  for (; s < steps; s += stride) {
+    const int t0 = s * kStep;
+    if (!kAhead) load_k(t0);
     // V: tokens 2q and 2q + 1 of each half, the g-th piece of each set of channels
     constexpr int kVWords = C::kVCh * eb / 4;
     uint32_t vv[C::kSets][4][kVWords];
@@ -331,6 +335,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
     }
 #pragma unroll
     for (int set = kEarly; set < C::kSets; ++set) load_v(set);
+    if (kAhead) load_k(t0 + stride * kStep);
     // logits in log2 units, the rows' maxima, weights
     uint32_t p[2][2];  // [half][row g, g + 8], two tokens each
     float f[2];
@@ -415,10 +420,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
   // ---- the rows, half a warp each, or a warp where there are warps for it (its halves then
   // take the prefix's parts in turns): the cluster's own parts, then the prefix's
   using J = Join<D, 16>;
-  constexpr int kV = J::kV;
+  constexpr int kV = J::kV, kBatch = D == 256 ? 80 : 48;
   // `count` parts from other places in shared memory, their loads in front of their use (a
   // load from another CTA takes 200 ns and more)
-  auto gather = [&](J& join, int count, auto&& at_ml, auto&& at_o, float times) {
+  // (part c: the first warp's of CTA c, or warp c's of this CTA)
+  auto gather = [&](J& join, int count, bool apart, int r, float times) {
+    auto at_ml = [&](int c) { return in_cta(ml_s + (apart ? 0 : c * kRows) + r, apart ? c : rank); };
+    auto at_o = [&](int c) { return in_cta(o_s + ((apart ? 0 : c * kRows) + r) * C::kStride, apart ? c : rank); };
     float2 ml[4];
     float v[4][kV];
 #pragma unroll
@@ -447,8 +455,6 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
       for (int e = 0; e < kV; ++e) join.acc[e] = fmaf(f, v[c][e] * times, join.acc[e]);
     }
   };
-  auto ml_of = [&](int w, int r, uint32_t cta) { return in_cta(ml_s + w * kRows + r, cta); };
-  auto o_of = [&](int w, int r, uint32_t cta) { return in_cta(o_s + (w * kRows + r) * C::kStride, cta); };
   const int live = min(kRows, M - m0), hw = lane >> 4;
   Parts<kG> parts(a, b);
   __syncthreads();
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
 #pragma unroll 1
     for (int r = 2 * warp + hw; r < live; r += 2 * warps) {
       J join;
-      gather(join, warps, [&](int w) { return ml_of(w, r, rank); }, [&](int w) { return o_of(w, r, rank); }, 1.f);
+      gather(join, warps, false, r, 1.f);
 #pragma unroll
       for (int e = 0; e < kV; ++e) o_s[r * C::kStride + J::first() + e] = join.acc[e];
       // (every lane of the half has read the first warp's maximum: their loads are used)
@@ -466,25 +472,27 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
     __syncwarp();
     cluster_sync();
   }
+  const int packed = (q0 - parts.gr.q0) * a.group + m0;  // the first row, in the group
+  RowParts<kG, D> row(a, parts, h, packed);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the prefix's parts are there
+  const bool late = a.groups > 32;
   parts.late(a);
+  const int block_end = late ? 0 : kG * kTile - row.r;  // rows behind it (or all) need places of their own
   const bool turns = stride >= live;
   const int r0 = turns ? rank * warps + warp : 2 * (rank * warps + warp) + hw;
 #pragma unroll 1
   for (int r = r0; r < live; r += turns ? stride : 2 * stride) {
     J join;
     if (!turns || hw == 0) {
-      if (ctas > 1)
-        gather(join, static_cast<int>(ctas), [&](int c) { return ml_of(0, r, c); }, [&](int c) { return o_of(0, r, c); },
-               v_final);
-      else
-        gather(join, warps, [&](int w) { return ml_of(w, r, rank); }, [&](int w) { return o_of(w, r, rank); }, v_final);
+      gather(join, ctas > 1 ? ctas : warps, ctas > 1, r, v_final);
     }
-    const int i = (m0 + r) / a.group, hh = (m0 + r) % a.group;
-    const RowParts<kG, D> row(a, parts, h, (q0 + i - parts.gr.q0) * a.group + hh);
-    const int step = turns ? 2 : 1, at = turns ? hw : 0;
-    join.template add<80 / kV>((row.segs - at + step - 1) / step,
-                               [&](int k, const float*& x, const float*& v) { row.part(a, k * step + at, x, v); });
+    if (r >= block_end) row = RowParts<kG, D>(a, parts, h, packed + r);
+    const int off = r >= block_end ? 0 : r, step = turns ? 2 : 1, at = turns ? hw : 0;
+    join.template add<kBatch / kV>((row.segs - at + step - 1) >> (step - 1), [&](int k, const float*& x, const float*& v) {
+      row.part(a, k * step + at, x, v);
+      x += off;
+      v += off * D;
+    });
     if (turns) {
       __syncwarp();
       const float top = __shfl_xor_sync(0xffffffffu, join.top, 16), sum = __shfl_xor_sync(0xffffffffu, join.sum, 16);
@@ -497,7 +505,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
         join.acc[e] = join.acc[e] * f0 + __shfl_xor_sync(0xffffffffu, join.acc[e], 16) * f1;
       if (hw) continue;
     }
-    join.write(o, (static_cast<int64_t>(q0) + i) * a.hq + h * a.group + hh);
+    const int i = (m0 + r) / a.group;
+    join.write(o, (static_cast<int64_t>(q0) + i) * a.hq + h * a.group + m0 + r - i * a.group);
   }
   __syncwarp();
   if (ctas > 1) cluster_sync();  // the others have read this CTA's parts
