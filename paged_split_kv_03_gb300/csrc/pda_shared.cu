@@ -16,7 +16,7 @@
 // Types: bf16 caches run bf16 MMAs. E4M3 keys (head_dim 128 and 256) are operands as
 // they are: an E4M3 query meets them directly, a bf16 row as the sum of two E4M3 terms
 // of it times a power of two that takes its largest element to [224, 448): exact for
-// elements from 2^-11 of that on, rounded at 2^-19 of it below. Values, and int8 keys
+// elements from 2^-11 of that on, off by 2^-18 of it at most below. Values, and int8 keys
 // and those of head_dim 64, are widened exactly to f16 and meet an f16 P (query). P in
 // E4M3 terms would need no widening but four conversions for each pair of weights, 2048
 // cycles a tile of 128 x 128 against the 1024 of its MMAs. Scales per tensor meet the

@@ -121,9 +121,13 @@ def attention(w, sm_scale=None):
     """(out, bound, lse, lse bound) in 64 bits.
 
     With d the largest error of a logit (D products summed in fp32: a step, 2^-23, each; a
-    query as two E4M3 terms: 2^-22 of its largest element each; the scales and the
-    exponential: 2^-20 of the logit), a weight is off by 2 d relative (its own logit and
-    the sum's). It is rounded before it meets v: to bf16 (2^-8), f16 (2^-11) or two E4M3
+    query as two E4M3 terms: 2^-22 of its largest element for each of D; the scales and
+    the exponential: 2^-20 of the logit), a weight is off by 2 d relative (its own logit
+    and the sum's). Two terms of 4 bits hold a bf16 element's 8; only below 2^-11 of the
+    largest, which the first term takes to [224, 448), is the second short of bits: off by
+    half of E4M3's smallest step, 2^-10 of 224, 2^-17.8 of the largest. Of the normal
+    elements here one in a thousand is that small, so a row has one or two, with 2^-22 for
+    each of 64 and more others. It is rounded before it meets v: to bf16 (2^-8), f16 (2^-11) or two E4M3
     terms of it (2^-4 of 2^-4); terms below their normal range are off by half their
     smallest step, 2^-10 of a weight of one, f16's by 2^-25. Sums of L products are fp32,
     their parts joined in fp32 (a step for each), the output rounded to bf16."""

@@ -219,6 +219,22 @@ def test_compact(name, most):
     run_held(held_case(**HELD[name]), most=most, in_place=most == 5, extra=len(name) % 2)
 
 
+@pytest.mark.parametrize("name", sorted(HELD))
+def test_marks_in_memory(name):
+    """The same behind more pages than one CTA marks in shared memory."""
+    c = held_case(**{**HELD[name], "spare": 131073 + len(name)})
+    run_held(c, extra=1)
+    run_held(c, most=40, in_place=len(name) % 2 == 0)
+
+
+@pytest.mark.parametrize("n,cols", [(512, 32), (513, 3), (512, 33), (16, 1024), (1, 16385)])
+def test_about_what_one_cta_takes(n, cols):
+    r = random.Random(n)
+    c = held_case([r.randint(0, 16 * cols) for _ in range(n)], cols=cols, shared=0.7, spare=9)
+    run_held(c)
+    run_held(c, most=20)
+
+
 def test_rows_named_twice():
     c = held_case([100, 60], spare=30)
     c["request"], c["lens"] = c["request"] + c["request"][:1], [100, 60, 70]
