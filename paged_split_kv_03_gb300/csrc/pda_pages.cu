@@ -459,61 +459,101 @@ __global__ void __launch_bounds__(kThreads) renumber(const __grid_constant__ Pag
   if (threadIdx.x == 0) a.head[0] = 0;
 }
 
-// All of it in one CTA, the marks in shared memory, where the tables and the cache are small.
+// The marks of a CTA in shared memory: what many requests share is set there, where a word
+// of marks in memory that every CTA sets at once takes its atomics one by one (512 requests
+// of 1024 pages, half of them shared: 15 us).
 constexpr int kOnceThreads = 1024;
-constexpr int kOnceRequests = 512;
-constexpr int kOnceEntries = 16 * kOnceThreads;  // most entries of the tables
-constexpr int kOnceWords = 4096;                 // most words of marks
+constexpr int kOnceRequests = 512;               // most requests at a time
+constexpr int kOnceEntries = 16 * kOnceThreads;  // entries of the tables that a CTA takes
+constexpr int kOnceWords = 4096;                 // most words of marks where one CTA does it all
+constexpr int kMarkWords = 16384;                // ... where CTAs mark theirs
 
-__global__ void __launch_bounds__(kOnceThreads) pages_once(const __grid_constant__ PagesArgs a) {
-  extern __shared__ __align__(16) uint32_t marks[];  // [words up to a multiple of 4], then `below`
-  __shared__ int sh[kOnceThreads / 32];
-  __shared__ int row_s[kOnceRequests], n_s[kOnceRequests];
-  const int words4 = (a.words + 3) / 4 * 4;
-  int32_t* below = reinterpret_cast<int32_t*>(marks + words4);
-  uint32_t bad = 0u;
-#pragma unroll 1
-  for (int w = threadIdx.x; w < words4; w += kOnceThreads) marks[w] = 0u;
-  if (threadIdx.x < a.p.requests) {
+struct Rows {
+  int row[kOnceRequests], n[kOnceRequests];
+};
+// Requests first, first + step, ... (`count` of them): their rows and entries. All threads.
+__device__ __forceinline__ void rows_of(const PagesArgs& a, Rows& rows, int first, int step, int count, uint32_t& bad) {
+  __syncthreads();
+  if (threadIdx.x < count) {
     int64_t row;
-    n_s[threadIdx.x] = entries_of(a, threadIdx.x, row, bad);
-    row_s[threadIdx.x] = static_cast<int>(row);
+    rows.n[threadIdx.x] = entries_of(a, first + static_cast<int>(threadIdx.x) * step, row, bad);
+    rows.row[threadIdx.x] = static_cast<int>(row);
   }
   __syncthreads();
+}
+// Their entries, kAtOnce at a time: use(ids, places in the tables); no place: -1.
+template <class F>
+__device__ __forceinline__ void each_entry(const PagesArgs& a, const Rows& rows, int count, F&& use) {
   const int cols = max(1, a.p.table_cols), rows_on = kOnceThreads / cols, cols_on = kOnceThreads - rows_on * cols;
-  auto each = [&](auto&& use) {  // kAtOnce entries (or -1: none) at a time
-    int r = threadIdx.x / cols, j = threadIdx.x - r * cols;
+  int r = threadIdx.x / cols, j = threadIdx.x - r * cols;
 #pragma unroll 1
-    while (r < a.p.requests) {
-      int id[kAtOnce];
-      int64_t at[kAtOnce];
+  while (r < count) {
+    int id[kAtOnce];
+    int64_t at[kAtOnce];
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        at[k] = r < a.p.requests && j < n_s[r] ? row_s[r] * a.p.table_stride + j : -1;
-        id[k] = at[k] >= 0 ? a.p.block_table[at[k]] : -1;
-        r += rows_on;
-        j += cols_on;
-        if (j >= cols) {
-          j -= cols;
-          ++r;
-        }
+    for (int k = 0; k < kAtOnce; ++k) {
+      at[k] = r < count && j < rows.n[r] ? rows.row[r] * a.p.table_stride + j : -1;
+      id[k] = at[k] >= 0 ? a.p.block_table[at[k]] : -1;
+      r += rows_on;
+      j += cols_on;
+      if (j >= cols) {
+        j -= cols;
+        ++r;
       }
-      use(id, at);
     }
-  };
-  each([&](const int (&id)[kAtOnce], const int64_t (&at)[kAtOnce]) {
+    use(id, at);
+  }
+}
+__device__ __forceinline__ void mark_rows(const PagesArgs& a, const Rows& rows, int count, uint32_t* marks,
+                                          uint32_t& bad) {
+  each_entry(a, rows, count, [&](const int (&id)[kAtOnce], const int64_t (&at)[kAtOnce]) {
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k)
       if (at[k] >= 0 && id[k] == -1) bad |= PDA_STATUS_PAGE_OOB;
     mark(a, marks, id, bad);
   });
+}
+
+__global__ void __launch_bounds__(kOnceThreads) mark_shared(const __grid_constant__ PagesArgs a) {
+  extern __shared__ __align__(16) uint32_t marks[];  // [words]
+  __shared__ Rows rows;
+  grid_launch();
+  uint32_t bad = 0u;
+#pragma unroll 1
+  for (int w = threadIdx.x; w < a.words; w += kOnceThreads) marks[w] = 0u;
+  const int step = static_cast<int>(gridDim.x);
+#pragma unroll 1
+  for (int r = blockIdx.x; r < a.p.requests; r += kOnceRequests * step) {
+    const int count = min(kOnceRequests, (a.p.requests - r + step - 1) / step);
+    rows_of(a, rows, r, step, count, bad);
+    mark_rows(a, rows, count, marks, bad);
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int w = threadIdx.x; w < a.words; w += kOnceThreads)
+    if (marks[w]) atomicOr(a.bits + w, marks[w]);
+  if (bad) atomicOr(a.status, bad);
+}
+
+// All of it in one CTA, where the tables and the cache are small.
+__global__ void __launch_bounds__(kOnceThreads) pages_once(const __grid_constant__ PagesArgs a) {
+  extern __shared__ __align__(16) uint32_t marks[];  // [words up to a multiple of 4], then `below`
+  __shared__ Rows rows;
+  __shared__ int sh[kOnceThreads / 32];
+  const int words4 = (a.words + 3) / 4 * 4;
+  int32_t* below = reinterpret_cast<int32_t*>(marks + words4);
+  uint32_t bad = 0u;
+#pragma unroll 1
+  for (int w = threadIdx.x; w < words4; w += kOnceThreads) marks[w] = 0u;
+  rows_of(a, rows, 0, 1, a.p.requests, bad);
+  mark_rows(a, rows, a.p.requests, marks, bad);
   if (bad) atomicOr(a.status, bad);
   __syncthreads();
   int live, moves;
   list_words<kOnceThreads>(a, marks, below, 0, a.words, true, sh, live, moves);
   if (!a.compact) return;
   __syncthreads();  // (the moves' targets and `below` are there)
-  each([&](const int (&id)[kAtOnce], const int64_t (&at)[kAtOnce]) {
+  each_entry(a, rows, a.p.requests, [&](const int (&id)[kAtOnce], const int64_t (&at)[kAtOnce]) {
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k)
       if (at[k] >= 0) a.p.new_table[at[k]] = renamed(a, marks, below, live, moves, id[k]);
@@ -588,7 +628,20 @@ int list_call(const pda_plan_t* plan, const pda_pages* pages, void* scratch, pda
   const unsigned gx = static_cast<unsigned>(std::max(1, std::min(p.requests, 4 * plan->num_sms)));
   const unsigned gy = static_cast<unsigned>(
       std::max(1, std::min(64, (p.table_cols + 4 * kThreads - 1) / (4 * kThreads))));
-  mark_pages<<<dim3(gx, gy), kThreads, 0, s>>>(a);
+  if (words <= kMarkWords) {
+    if (words > 8192 && cudaFuncSetAttribute(reinterpret_cast<const void*>(mark_shared),
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kMarkWords * 4) != cudaSuccess) {
+      cudaGetLastError();
+      return PDA_ERR_CUDA;
+    }
+    const int64_t ctas = (static_cast<int64_t>(p.requests) * p.table_cols + kOnceEntries - 1) / kOnceEntries;
+    const unsigned g = static_cast<unsigned>(
+        std::max<int64_t>(1, std::min<int64_t>({ctas, p.requests, plan->num_sms})));
+    mark_shared<<<g, kOnceThreads, static_cast<size_t>(words * 4), s>>>(a);
+  } else {
+    mark_pages<<<dim3(gx, gy), kThreads, 0, s>>>(a);
+  }
   if (cudaGetLastError() != cudaSuccess) return PDA_ERR_CUDA;
   // (a CTA's warps list 8 words each, or more)
   const int64_t least = 8 * kWarps;

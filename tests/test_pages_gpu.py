@@ -220,14 +220,15 @@ def test_compact(name, most):
 
 
 @pytest.mark.parametrize("name", sorted(HELD))
-def test_marks_in_memory(name):
-    """The same behind more pages than one CTA marks in shared memory."""
-    c = held_case(**{**HELD[name], "spare": 131073 + len(name)})
+@pytest.mark.parametrize("pages", [131073, 400000, 524289])
+def test_many_pages(name, pages):
+    """The same behind more pages than one CTA lists, and than a CTA marks in shared memory."""
+    c = held_case(**{**HELD[name], "spare": pages + len(name)})
     run_held(c, extra=1)
     run_held(c, most=40, in_place=len(name) % 2 == 0)
 
 
-@pytest.mark.parametrize("n,cols", [(512, 32), (513, 3), (512, 33), (16, 1024), (1, 16385)])
+@pytest.mark.parametrize("n,cols", [(512, 32), (513, 3), (512, 33), (16, 1024), (1, 16385), (1030, 70)])
 def test_about_what_one_cta_takes(n, cols):
     r = random.Random(n)
     c = held_case([r.randint(0, 16 * cols) for _ in range(n)], cols=cols, shared=0.7, spare=9)

@@ -193,7 +193,7 @@ def test_binding_refuses(lib):
 def test_no_spills(lib):
     found = {}
     for name, (regs, stack, st, ld) in build_mod.ptxas_reports().items():
-        for k in ("fork_tables", "copy_pages", "mark_pages", "list_pages", "renumber", "pages_once"):
+        for k in ("fork_tables", "copy_pages", "mark_pages", "list_pages", "renumber", "pages_once", "mark_shared"):
             if k in name:
                 found[k] = (stack, st, ld)
-    assert len(found) == 6 and set(found.values()) == {(0, 0, 0)}, found
+    assert len(found) == 7 and set(found.values()) == {(0, 0, 0)}, found
