@@ -38,16 +38,24 @@ constexpr int kStep = 16;          // tokens of a warp's step
 constexpr int kMaxTiles = 4;       // most row tiles of a request: each reads its tokens again
 constexpr int kMaxTokens = 1024;   // most own tokens: four warps share them
 
-template <int D, bool k8>
+constexpr int kStages = 2;         // steps of a warp in shared memory
+
+template <int D, bool k8, bool kTok>
 struct Cfg {
   static constexpr int kPieces = D * (k8 ? 1 : 2) / 64;    // 16-byte pieces of a K row a lane has
   static constexpr int kVCh = k8 && D >= 128 ? 16 : 8;     // channels of a lane's piece of a V row
   static constexpr int kSets = D / (8 * kVCh);             // such pieces
   static constexpr int kStride = D + 4;                    // floats of a row of O in shared memory
   static constexpr int kQBytes = kRows * D * 2;
-  static constexpr int kOBytes = kRows * kStride * 4;      // of a warp
-  static constexpr int smem(int warps) { return kQBytes + warps * (kOBytes + kRows * 8) + kRows * 4; }
-  static constexpr int kWarpsSm = D == 256 ? 8 : 12;       // by their registers
+  static constexpr int kVBytes = kVCh * (k8 ? 1 : 2);      // of a piece of a V row
+  // a step's bytes of a warp: K, V, and the scales of four tokens a lane
+  static constexpr int kKStage = 32 * 2 * kPieces * 16, kVStage = 32 * kSets * 4 * kVBytes;
+  static constexpr int kStage = kKStage + kVStage + (kTok ? 32 * 8 * 4 : 0);
+  // a warp's stages, and O in their place behind its last step
+  static constexpr int kOBytes = kRows * kStride * 4;
+  static constexpr int kRegion = kStages * kStage > kOBytes ? kStages * kStage : kOBytes;
+  static constexpr int smem(int warps) { return kQBytes + warps * (kRegion + kRows * 8) + kRows * 4; }
+  static constexpr int kWarpsSm = D < 256 ? 12 : k8 ? 8 : 6;  // by their registers or stages
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -94,17 +102,35 @@ __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t y, bool high) {
   return __byte_perm(x, y, high ? 0x7632 : 0x5410);
 }
 
+// Copies to shared memory, nothing read and zeros written where !ok; the end of a group of
+// them; a wait until one group is under way at most.
+template <int kBytes>
+__device__ __forceinline__ void copy_to(const void* dst, const void* src, bool ok) {
+  const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(src), "r"(ok ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(to), "l"(src), "n"(kBytes), "r"(ok ? kBytes : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kUnderWay>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kUnderWay) : "memory");
+}
+
 template <int D, bool k8, bool kI8, bool kTok>
 __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(const __grid_constant__ SharedArgs a,
                                                      const __grid_constant__ DecodeArgs o) {
-  using C = Cfg<D, k8>;
+  using C = Cfg<D, k8, kTok>;
   constexpr int kG = D <= 128 ? 2 : 1;
   constexpr int eb = k8 ? 1 : 2;
   extern __shared__ __align__(16) uint8_t smem[];
   uint8_t* q_s = smem;  // [16][D] in 16 bits, a row's 16-byte pieces XORed with its low bits
   const int warps = blockDim.x >> 5;
-  float* o_s = reinterpret_cast<float*>(smem + C::kQBytes);  // [warp][16][kStride]
-  float2* ml_s = reinterpret_cast<float2*>(smem + C::kQBytes + warps * C::kOBytes);  // [warp][16]
+  float* o_s = reinterpret_cast<float*>(smem + C::kQBytes);  // [warp][16][kStride], kRegion bytes apart
+  constexpr int kApart = C::kRegion / 4;
+  float2* ml_s = reinterpret_cast<float2*>(smem + C::kQBytes + warps * C::kRegion);  // [warp][16]
   float* up_s = reinterpret_cast<float*>(ml_s + warps * kRows);  // a row's power of two
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   uint32_t ctas;  // of the cluster
@@ -128,6 +154,60 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
     if (blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
+
+  // ---- a warp's steps of 16 tokens, kStages - 1 of them under way in front of the one at
+  // work; a lane copies what it uses itself, so nothing has to wait for other lanes
+  const int from = W > 0 ? max(0, L - R - min(W, L) + 1) / kStep : 0;
+  const int steps = (L + kStep - 1) / kStep;
+  const int P = a.page_size, shift = 31 - __clz(P);
+  const int32_t* pages = a.page_table + own;
+  const uint8_t* k_base = static_cast<const uint8_t*>(o.k) + static_cast<int64_t>(h) * o.sh * eb;
+  const uint8_t* v_base = static_cast<const uint8_t*>(o.v) + static_cast<int64_t>(h) * o.sh * eb;
+  const int n_pages = (L + P - 1) >> shift;
+  // the pages of a step's first and last eight tokens
+  auto page_at = [&](int t) { return t >> shift < n_pages ? __ldg(pages + (t >> shift)) : -1; };
+  const int stride = ctas * warps;
+  int s = from + rank * warps + warp, next = s, stage = 0;  // the step at work, the one to copy
+  int pg[2] = {page_at(s * kStep), page_at(s * kStep + 8)};  // the pages of `next`
+  bool oob = false;
+  uint8_t* slots = smem + C::kQBytes + warp * C::kRegion;
+  auto copy_step = [&](int to) {
+    uint8_t* k_to = slots + to * C::kStage + lane * 16;
+    uint8_t* v_to = slots + to * C::kStage + C::kKStage + lane * C::kVBytes;
+    float* f_to = reinterpret_cast<float*>(slots + to * C::kStage + C::kKStage + C::kVStage) + lane;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int t = next * kStep + 8 * e, page = pg[e];
+      const bool ok = page >= 0 && page < a.num_pages;
+      oob |= !ok && t < L;
+      const int64_t at = ok ? (page * o.sp + (t & (P - 1)) * o.st) * eb : 0;
+      pg[e] = page_at(t + stride * kStep);
+      // K: token g of the half, 16-byte pieces q, q + 4, ... of its row
+      const bool k_ok = ok && t + g < L;
+      const uint8_t* k_at = k_base + at + (k_ok ? g * o.st * eb : 0) + q * 16;
+#pragma unroll
+      for (int i = 0; i < C::kPieces; ++i) copy_to<16>(k_to + (e * C::kPieces + i) * 512, k_at + i * 64, k_ok);
+      // V: tokens 2q and 2q + 1 of the half, the g-th piece of each set of channels
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = 2 * q + c;
+        const bool v_ok = ok && t + row < L;
+        const uint8_t* v_at = v_base + at + (v_ok ? row * o.st * eb : 0) + g * C::kVBytes;
+#pragma unroll
+        for (int set = 0; set < C::kSets; ++set)
+          copy_to<C::kVBytes>(v_to + (set * 4 + 2 * e + c) * (32 * C::kVBytes), v_at + set * 8 * C::kVBytes, v_ok);
+        if constexpr (kTok) {
+          const int64_t x = v_ok ? (static_cast<int64_t>(page) * P + ((t + row) & (P - 1))) * a.hkv + h : 0;
+          copy_to<4>(f_to + (4 * e + 2 * c) * 32, a.k_scale + x, v_ok);
+          copy_to<4>(f_to + (4 * e + 2 * c + 1) * 32, a.v_scale + x, v_ok);
+        }
+      }
+    }
+    copies_end();
+    next += stride;
+  };
+#pragma unroll 1
+  for (int k = 0; k < kStages; ++k) copy_step(k);
 
   // ---- the queries: eight lanes a row, 16 bits a channel
 #pragma unroll 1
@@ -202,106 +282,35 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
     lo[k] = W > 0 ? last[k] - min(W, L) + 1 : 0;  // (L of L tokens is all of them)
     scale[k] = logit * up_s[g + 8 * k];
   }
-  const int from = W > 0 ? max(0, L - R - min(W, L) + 1) / kStep : 0;
-  const int steps = (L + kStep - 1) / kStep;
-  const int P = a.page_size, shift = 31 - __clz(P);
-  const int32_t* pages = a.page_table + own;
-  const uint8_t* k_base = static_cast<const uint8_t*>(o.k) + static_cast<int64_t>(h) * o.sh * eb;
-  const uint8_t* v_base = static_cast<const uint8_t*>(o.v) + static_cast<int64_t>(h) * o.sh * eb;
-  const int n_pages = (L + P - 1) >> shift;
-  // the pages of a step's first and last eight tokens
-  auto page_at = [&](int t) { return t >> shift < n_pages ? __ldg(pages + (t >> shift)) : -1; };
   float acc[D / 8][4];
 #pragma unroll
   for (int n = 0; n < D / 8; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
-  int s = from + rank * warps + warp;
-  const int stride = ctas * warps;
-  int pg[2] = {-1, -1};
-  if (s < steps) {
-    pg[0] = page_at(s * kStep);
-    pg[1] = page_at(s * kStep + 8);
-  }
-  bool oob = false;
-  // bytes of each half's first token, or -1; its page; K: token g of each half, 16-byte
-  // pieces q, q + 4, ... of its row
-  int64_t at[2];
-  int held[2];
-  uint4 kv[2][C::kPieces];
-  auto load_k = [&](int t0) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int t = t0 + 8 * e;
-      const bool ok = pg[e] >= 0 && pg[e] < a.num_pages;
-      oob |= !ok && t < L;
-      at[e] = ok ? (pg[e] * o.sp + (t & (P - 1)) * o.st) * eb : -1;
-      held[e] = pg[e];
-      pg[e] = page_at(t + stride * kStep);
-#pragma unroll
-      for (int i = 0; i < C::kPieces; ++i) {
-        kv[e][i] = make_uint4(0, 0, 0, 0);
-        if (at[e] >= 0 && t + g < L)
-          kv[e][i] = __ldg(reinterpret_cast<const uint4*>(k_base + at[e] + g * o.st * eb) + q + 4 * i);
-      }
-    }
-  };
-  // the next step's K is under way during this one's softmax and O (if it fits the registers)
-  constexpr bool kAhead = k8 && !kTok;
-  if (kAhead) load_k(s * kStep);
 #pragma unroll 1
   for (; s < steps; s += stride) {
     const int t0 = s * kStep;
-    if (!kAhead) load_k(t0);
-    // V: tokens 2q and 2q + 1 of each half, the g-th piece of each set of channels
-    constexpr int kVWords = C::kVCh * eb / 4;
-    uint32_t vv[C::kSets][4][kVWords];
-    auto load_v = [&](int set) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int half = e >> 1, t = t0 + 8 * half + 2 * q + (e & 1);
-#pragma unroll
-        for (int w = 0; w < kVWords; ++w) vv[set][e][w] = 0u;
-        if (at[half] >= 0 && t < L) {
-          const uint8_t* src = v_base + at[half] + (2 * q + (e & 1)) * o.st * eb + (set * 8 + g) * (C::kVCh * eb);
-          if constexpr (kVWords == 4) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
-            vv[set][e][0] = x.x;
-            vv[set][e][1] = x.y;
-            vv[set][e][2] = x.z;
-            vv[set][e][3] = x.w;
-          } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(src));
-            vv[set][e][0] = x.x;
-            vv[set][e][1] = x.y;
-          }
-        }
-      }
-    };
-    // (as many sets as fit the registers beside K and O)
-    constexpr int kEarly = D == 256 && !k8 ? 0 : C::kSets;
-#pragma unroll
-    for (int set = 0; set < kEarly; ++set) load_v(set);
+    copies_wait<kStages - 1>();
+    const uint8_t* mine = slots + stage * C::kStage;
     float ks[2][2], vs[2][2];  // of tokens 2q, 2q + 1 of each half
     if constexpr (kTok) {
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const int t = t0 + 8 * e + 2 * q + c;
-          ks[e][c] = vs[e][c] = 1.f;
-          if (at[e] >= 0 && t < L) {
-            const int64_t x = (static_cast<int64_t>(held[e]) * P + (t & (P - 1))) * a.hkv + h;
-            ks[e][c] = __ldg(a.k_scale + x);
-            const float f = __ldg(a.v_scale + x);
-            vs[e][c] = f > 0.f ? f : 1.f;
-          }
+          const float* f = reinterpret_cast<const float*>(mine + C::kKStage + C::kVStage) + (4 * e + 2 * c) * 32 + lane;
+          ks[e][c] = f[0];
+          vs[e][c] = f[32] > 0.f ? f[32] : 1.f;
         }
     }
     // S of 16 rows x 2 x 8 tokens
     float sc[2][4] = {};
 #pragma unroll
     for (int i = 0; i < C::kPieces; ++i) {
+      uint4 kv[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        kv[e] = *reinterpret_cast<const uint4*>(mine + (e * C::kPieces + i) * 512 + lane * 16);
       if constexpr (k8) {
         uint32_t qa[8], qb[8];
 #pragma unroll
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint32_t w[4] = {kv[e][i].x, kv[e][i].y, kv[e][i].z, kv[e][i].w};
+          const uint32_t w[4] = {kv[e].x, kv[e].y, kv[e].z, kv[e].w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t x, y;
@@ -328,14 +337,11 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
         const uint4 y = *reinterpret_cast<const uint4*>(q_s + (g + 8) * (D * 2) + piece * 16);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mma16<false>(sc[e], x.x, y.x, x.y, y.y, kv[e][i].x, kv[e][i].y);
-          mma16<false>(sc[e], x.z, y.z, x.w, y.w, kv[e][i].z, kv[e][i].w);
+          mma16<false>(sc[e], x.x, y.x, x.y, y.y, kv[e].x, kv[e].y);
+          mma16<false>(sc[e], x.z, y.z, x.w, y.w, kv[e].z, kv[e].w);
         }
       }
     }
-#pragma unroll
-    for (int set = kEarly; set < C::kSets; ++set) load_v(set);
-    if (kAhead) load_k(t0 + stride * kStep);
     // logits in log2 units, the rows' maxima, weights
     uint32_t p[2][2];  // [half][row g, g + 8], two tokens each
     float f[2];
@@ -378,16 +384,29 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
     }
     // O: column g of n-tile `set kVCh + j` is channel (set 8 + g) kVCh + j
 #pragma unroll
-    for (int set = 0; set < C::kSets; ++set)
+    for (int set = 0; set < C::kSets; ++set) {
+      constexpr int kVWords = C::kVBytes / 4;
+      uint32_t vv[4][kVWords];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint8_t* src = mine + C::kKStage + (set * 4 + e) * (32 * C::kVBytes) + lane * C::kVBytes;
+        if constexpr (kVWords == 4) {
+          const uint4 x = *reinterpret_cast<const uint4*>(src);
+          vv[e][0] = x.x, vv[e][1] = x.y, vv[e][2] = x.z, vv[e][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(src);
+          vv[e][0] = x.x, vv[e][1] = x.y;
+        }
+      }
 #pragma unroll
       for (int w = 0; w < kVWords; ++w) {
         uint32_t x[4][2];  // the word's channels in pairs, of each token
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if constexpr (k8) {
-            widen4(vv[set][e][w], x[e][0], x[e][1], kI8);
+            widen4(vv[e][w], x[e][0], x[e][1], kI8);
           } else {
-            x[e][0] = vv[set][e][w];
+            x[e][0] = vv[e][w];
           }
         }
 #pragma unroll
@@ -399,7 +418,12 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
                       pick(x[2][c], x[3][c], hi));
           }
       }
+    }
+    __syncwarp();
+    copy_step(stage);  // (what it held has been used)
+    stage ^= 1;
   }
+  copies_wait<0>();
   if (oob) atomicOr(a.status, PDA_STATUS_PAGE_OOB);
   // ---- the warps' parts to shared memory
 #pragma unroll
@@ -407,7 +431,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
     l_[k] += __shfl_xor_sync(0xffffffffu, l_[k], 1);
     l_[k] += __shfl_xor_sync(0xffffffffu, l_[k], 2);
     if (q == 0) ml_s[warp * kRows + g + 8 * k] = make_float2(m_[k], l_[k]);
-    float* row = o_s + (warp * kRows + g + 8 * k) * C::kStride;
+    float* row = o_s + warp * kApart + (g + 8 * k) * C::kStride;
 #pragma unroll
     for (int set = 0; set < C::kSets; ++set)
 #pragma unroll
@@ -426,7 +450,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
   // (part c: the first warp's of CTA c, or warp c's of this CTA)
   auto gather = [&](J& join, int count, bool apart, int r, float times) {
     auto at_ml = [&](int c) { return in_cta(ml_s + (apart ? 0 : c * kRows) + r, apart ? c : rank); };
-    auto at_o = [&](int c) { return in_cta(o_s + ((apart ? 0 : c * kRows) + r) * C::kStride, apart ? c : rank); };
+    auto at_o = [&](int c) { return in_cta(o_s + (apart ? 0 : c * kApart) + r * C::kStride, apart ? c : rank); };
     float2 ml[4];
     float v[4][kV];
 #pragma unroll
@@ -558,13 +582,16 @@ struct Kernel {
 };
 template <int D>
 Kernel kernel_for(const pda_plan_t* p) {
-  using C16 = Cfg<D, false>;
-  using C8 = Cfg<D, true>;
+  using C16 = Cfg<D, false, false>;
+  using C8 = Cfg<D, true, false>;
+  using C8T = Cfg<D, true, true>;
   const bool tok = p->scale_mode == PDA_SCALE_TOKEN_HEAD;
   if (p->kv_dtype == PDA_BF16) return {own_join<D, false, false, false>, C16::smem, C16::kWarpsSm};
   if (p->kv_dtype == PDA_INT8)
-    return {tok ? own_join<D, true, true, true> : own_join<D, true, true, false>, C8::smem, C8::kWarpsSm};
-  return {tok ? own_join<D, true, false, true> : own_join<D, true, false, false>, C8::smem, C8::kWarpsSm};
+    return tok ? Kernel{own_join<D, true, true, true>, C8T::smem, C8T::kWarpsSm}
+               : Kernel{own_join<D, true, true, false>, C8::smem, C8::kWarpsSm};
+  return tok ? Kernel{own_join<D, true, false, true>, C8T::smem, C8T::kWarpsSm}
+             : Kernel{own_join<D, true, false, false>, C8::smem, C8::kWarpsSm};
 }
 
 int launch(JoinFn fn, dim3 grid, unsigned threads, int smem, unsigned cluster, const SharedArgs& a,
@@ -615,7 +642,7 @@ int launch_own(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, 
     const int steps = std::max(1, own->max_kv_len / (2 * kStep));
     double best = 1e30;
     for (int w = kMaxWarps; w >= 1; --w) {
-      const int64_t slots = static_cast<int64_t>(k.warps_sm / w) * own->num_sms;
+      const int64_t slots = static_cast<int64_t>(std::min(k.warps_sm / w, 227 * 1024 / (k.smem(w) + 1024))) * own->num_sms;
       const double us = static_cast<double>((items + slots - 1) / slots) * ((steps + w - 1) / w * 2.0 + 6.0);
       if (us < best) best = us, warps = w;
     }
