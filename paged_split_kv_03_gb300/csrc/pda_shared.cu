@@ -530,14 +530,14 @@ struct Look {
 };
 
 template <int kG>
-__device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<kG> look) {
-  constexpr int kRows = kG * kTile;
-  const int lane = threadIdx.x & 31;
+struct WorkList {
+  Look<kG> look;
   int work = 0, items = 0, singles = 0;
   int lane_work = 0, lane_items = 0, lane_singles = 0;  // in front of this lane's group, among the 32
   uint32_t bits = 0u;
   int known = 0;  // the 32 groups that `look` holds
-  auto sums = [&](int& w32, int& i32, int& s32) {
+  Cut cut;
+  __device__ __forceinline__ void sums(const SharedArgs& a, int lane, int& w32, int& i32, int& s32) {
     const int w = a.hkv * look.w.head(Cut()), i = a.hkv * look.w.blocks;
     const int s = look.w.single ? a.hkv * look.w.tiles : 0;
     int wx = w, ix = i, sx = s, last = 0;
@@ -553,16 +553,26 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<
     w32 = __shfl_sync(0xffffffffu, wx, last);
     i32 = __shfl_sync(0xffffffffu, ix, last);
     s32 = __shfl_sync(0xffffffffu, sx, last);
-  };
+  }
+  __device__ __forceinline__ int place(int w, int i, int s) const { return w - s * (kFull - cut.one) + i * cut.pay; }
+  __device__ __forceinline__ int coarse(const Shared* sh, int c) const {
+    return place(sh->coarse[c], sh->coarse_items[c], sh->coarse_singles[c]);
+  }
+  __device__ __forceinline__ void prepare(const SharedArgs& a, Shared* sh);
+  __device__ __forceinline__ void run(const SharedArgs& a, Shared* sh);
+};
+
+// The cut (while the CTA sets up).
+template <int kG>
+__device__ __forceinline__ void WorkList<kG>::prepare(const SharedArgs& a, Shared* sh) {
+  const int lane = threadIdx.x & 31;
   int w32, i32, s32;
 #pragma unroll 1
   for (int g0 = 0; g0 < a.groups; g0 += 32) {
-    if (g0) {
-      known = g0 >> 5;
-      look.at(a, g0 + lane);
-    }
+    known = g0 >> 5;
+    look.at(a, g0 + lane);
     bits |= look.r.bad;
-    sums(w32, i32, s32);
+    sums(a, lane, w32, i32, s32);
     if (lane == 0) {
       sh->coarse[known] = work;
       sh->coarse_items[known] = items;
@@ -572,11 +582,16 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<
     items += i32;
     singles += s32;
   }
-  const Cut cut(a, work, singles, items);
-  const int per = cut.per, pay = cut.pay;
-  auto place = [&](int w, int i, int s) { return w - s * (kFull - cut.one) + i * pay; };
-  auto coarse = [&](int c) { return place(sh->coarse[c], sh->coarse_items[c], sh->coarse_singles[c]); };
+  cut = Cut(a, work, singles, items);
   __syncwarp();
+}
+
+// This CTA's segments, in turn.
+template <int kG>
+__device__ __forceinline__ void WorkList<kG>::run(const SharedArgs& a, Shared* sh) {
+  constexpr int kRows = kG * kTile;
+  const int lane = threadIdx.x & 31, per = cut.per, pay = cut.pay;
+  int w32, i32, s32;
   int pos = blockIdx.x * per;  // (a CTA too many stands at most `per` behind the end)
   const int stop = min(place(work, items, singles), pos + per);
   uint32_t n = 0;
@@ -588,15 +603,15 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<
       int c = 0, top = (a.groups + 31) / 32 - 1;
       while (c < top) {
         const int mid = (c + top + 1) >> 1;
-        if (coarse(mid) <= pos) c = mid;
+        if (coarse(sh, mid) <= pos) c = mid;
         else top = mid - 1;
       }
       if (c != known) {
         known = c;
         look.at(a, 32 * c + lane);
-        sums(w32, i32, s32);
+        sums(a, lane, w32, i32, s32);
       }
-      const int start = coarse(c) + place(lane_work, lane_items, lane_singles);
+      const int start = coarse(sh, c) + place(lane_work, lane_items, lane_singles);
       const int head = look.w.head(cut);
       const int src = __ffs(__ballot_sync(0xffffffffu, start + a.hkv * head > pos)) - 1;
       auto from = [&](int v) { return __shfl_sync(0xffffffffu, v, src); };
@@ -664,8 +679,8 @@ __device__ __forceinline__ void work_role(const SharedArgs& a, Shared* sh, Look<
 #pragma unroll 1
   for (int g0 = 0; g0 < a.groups; g0 += 32) {
     look.at(a, g0 + lane);
-    sums(w32, i32, s32);
-    if (g0 + lane < a.groups) a.first[3 + g0 + lane] = coarse(g0 >> 5) + place(lane_work, lane_items, lane_singles);
+    sums(a, lane, w32, i32, s32);
+    if (g0 + lane < a.groups) a.first[3 + g0 + lane] = coarse(sh, g0 >> 5) + place(lane_work, lane_items, lane_singles);
   }
 }
 
@@ -1090,47 +1105,49 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
     if (tid == 0) atomicOr(a.status, PDA_STATUS_SMEM_MISALIGNED);
     return;
   }
-  if (tid == 0) {
-    for (int g = 0; g < 2; ++g) {
-      bar_init(sh->q_full + g, 4);
-      bar_init(sh->q_empty + g, 1);
-      bar_init(sh->s_full + g, 1);
-      bar_init(sh->p_half + g, 4);
-      bar_init(sh->p_full + g, 4);
-      bar_init(sh->o_done + g, 1);
-      bar_init(sh->o_free + g, 4);
+  if (warp == 0) {  // a lane a barrier of each kind
+    if (tid < 2) {
+      bar_init(sh->q_full + tid, 4);
+      bar_init(sh->q_empty + tid, 1);
+      bar_init(sh->s_full + tid, 1);
+      bar_init(sh->p_half + tid, 4);
+      bar_init(sh->p_full + tid, 4);
+      bar_init(sh->o_done + tid, 1);
+      bar_init(sh->o_free + tid, 4);
     }
-    for (int u = 0; u < C::kRK; ++u) {
-      bar_init(sh->k_full + u, k8 && !C::kDirect ? C::kConv : 1);
-      bar_init(sh->k_empty + u, 1);
+    if (tid < C::kRK) {
+      bar_init(sh->k_full + tid, k8 && !C::kDirect ? C::kConv : 1);
+      bar_init(sh->k_empty + tid, 1);
     }
-    for (int u = 0; u < C::kRV; ++u) {
-      bar_init(sh->v_full + u, k8 ? C::kConv : 1);
-      bar_init(sh->v_empty + u, 1);
+    if (tid < C::kRV) {
+      bar_init(sh->v_full + tid, k8 ? C::kConv : 1);
+      bar_init(sh->v_empty + tid, 1);
     }
-    for (int u = 0; u < C::kRaw; ++u) {
-      bar_init(sh->raw_full + u, 1);
-      bar_init(sh->raw_empty + u, C::kConv);
+    if (k8 && tid < C::kRaw) {
+      bar_init(sh->raw_full + tid, 1);
+      bar_init(sh->raw_empty + tid, k8 ? C::kConv : 1);
     }
-    for (int u = 0; u < (kTok ? kScales : 0); ++u) {
-      bar_init(sh->sc_full + u, C::kConv);
-      bar_init(sh->sc_empty + u, C::kSoft);
+    if (kTok && tid < kScales) {
+      bar_init(sh->sc_full + tid, kTok ? C::kConv : 1);
+      bar_init(sh->sc_empty + tid, C::kSoft);
     }
-    for (int u = 0; u < kItems; ++u) {
-      bar_init(sh->item_full + u, 1);
-      bar_init(sh->item_empty + u, C::kReaders);
+    if (tid < kItems) {
+      bar_init(sh->item_full + tid, 1);
+      bar_init(sh->item_empty + tid, C::kReaders);
     }
-    bar_init(&sh->odd_done, 4);
-    bar_init(&sh->drain, 1);
-    sh->abort_flag = 0;
+    if (tid == 0) {
+      bar_init(&sh->odd_done, 4);
+      bar_init(&sh->drain, 1);
+      sh->abort_flag = 0;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (kTok && tid < kKeys) {
     scales[kScales * 3 * kKeys + tid] = 1.f;
     scales[kScales * 3 * kKeys + kKeys + tid] = 0.f;
   }
-  Look<C::kG> look;
-  if (warp == C::kWorkWarp) look.at(a, tid & 31);  // (under way while the rest is set up)
+  WorkList<C::kG> list;
+  if (warp == C::kWorkWarp) list.prepare(a, sh);
   if (warp == C::kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      su32(&sh->tmem)),
@@ -1160,7 +1177,7 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
   } else if (warp == C::kMmaWarp) {
     if (elect_one()) mma_role<C, D, k8>(a, sh, q_s, rings);
   } else if (warp == C::kWorkWarp) {
-    work_role<C::kG>(a, sh, look);
+    list.run(a, sh);
   } else if (k8 && warp >= C::kConv0) {
     if constexpr (k8) widen_role<C, D, kI8, kTok>(a, sh, rings, raw, scales);
   } else if (warp < C::kProd0 + C::kProds) {
