@@ -173,8 +173,9 @@ def test_binding_refuses(lib):
 
 
 def test_spills(lib):
-    """Bytes spilled (stores + loads) by builds of the new kernels: none in most; the prefix
-    kernel's are outside its softmax loop (a role has 64 to 104 registers beside it)."""
+    """Bytes spilled (stores + loads) by builds of the new kernels that are accepted now: the
+    prefix kernel compiles to 128 registers for roles that run with 64 to 216, the most with
+    int8 codes and scales per token; the own tokens' kernel spills next to nothing."""
     found = {k: [] for k in ("shared_prefix", "own_join", "shared_join", "share_tables")}
     for name, (regs, stack, st, ld) in build_mod.ptxas_reports().items():
         for k in found:
@@ -183,4 +184,4 @@ def test_spills(lib):
     assert [len(found[k]) for k in found] == [15, 15, 3, 1], found
     assert max(found["shared_join"] + found["share_tables"]) <= 8, found
     assert max(found["own_join"]) <= 24, found
-    assert max(found["shared_prefix"]) <= 300, found
+    assert max(found["shared_prefix"]) <= 320, found
