@@ -660,15 +660,15 @@ int pda_shared_plan(const pda_plan_t* plan, int32_t groups, int32_t max_own_len,
  * `end`. Own tokens are the L - end behind it, R of them at least. A request without
  * rows takes no part (own_len 0), nor does an invalid one (own_len -1; L < R, R out
  * of range or L above max_kv_len, with pda_decode's status bits); a page id out of
- * range ends a prefix. A group whose bounds are no requests is left unwritten
- * (PDA_STATUS_TABLE_INVALID). */
+ * range ends a prefix. A group whose bounds are no requests is left unwritten, and so are
+ * requests of no group (PDA_STATUS_TABLE_INVALID). */
 int pda_share_tables(const pda_shared_plan_t* plan, const pda_shared_tables* tables, void* scratch,
                      pda_stream_t stream);
 
 /* Decode on the tables that pda_share_tables filled, as pda_decode: q, the caches,
  * scales, out, lse (or NULL), sm_scale and max_q_len are its arguments. An invalid
  * request's rows are left unwritten, with its status bits; so are those of a request
- * with more own tokens than planned. Keys and values that a row does not see for its window
+ * with more own tokens than planned, and of one in no group or in an invalid one. Keys and values that a row does not see for its window
  * have to be finite where another row of its group sees them. */
 int pda_decode_shared(const pda_shared_plan_t* plan, const void* q, const void* k_pages,
                       const void* v_pages, const pda_shared_tables* tables, int32_t max_q_len,

@@ -486,8 +486,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
       for (int e = 0; e < kV; ++e) join.acc[e] = fmaf(f, v[c][e] * times, join.acc[e]);
     }
   };
-  const int live = min(kRows, M - m0), hw = lane >> 4;
   Parts<kG> parts(a, b);
+  const bool covered = parts.covers(b);
+  if (!covered && tid == 0 && h == 0 && m0 == 0 && rank == 0) atomicOr(a.status, PDA_STATUS_TABLE_INVALID);
+  const int live = covered ? min(kRows, M - m0) : 0, hw = lane >> 4;
   __syncthreads();
   if (ctas > 1) {  // one part a CTA, in the first warp's place
 #pragma unroll 1
@@ -566,6 +568,10 @@ __global__ void __launch_bounds__(256, 3) shared_join(const __grid_constant__ Sh
     if (live) own = split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
   }
   Parts<kG> parts(a, live ? b : 0);
+  if (live && !parts.covers(b)) {
+    if ((threadIdx.x & 31) == 0) atomicOr(a.status, PDA_STATUS_TABLE_INVALID);
+    live = false;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!live) return;
   parts.late(a);

@@ -1237,6 +1237,7 @@ __global__ void __launch_bounds__(kShareThreads) share_tables(const __grid_const
     bits = PDA_STATUS_TABLE_INVALID;
     b1 = b0;
   }
+  if ((g == 0 && b0 != 0) || (g == a.groups - 1 && b1 != a.batch)) bits = PDA_STATUS_TABLE_INVALID;
   // a request that takes part: its rows and length, else its status bits
   auto fits = [&](int b, int& rows, int& len) -> bool {
     const int64_t r = static_cast<int64_t>(__ldg(a.t.qo_indptr + b + 1)) - __ldg(a.t.qo_indptr + b);
@@ -1552,6 +1553,7 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
   a.page_size = o.page_size;
   a.num_pages = o.num_pages;
   a.max_q_len = max_q_len;
+  a.max_kv_len = sp->max_kv_len;
   a.rows_cap = o.rows_cap;
   a.q8 = plan->q_dtype == PDA_E4M3;
   a.inject = o.inject;

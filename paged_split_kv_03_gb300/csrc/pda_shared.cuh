@@ -35,7 +35,7 @@ struct SharedArgs {
   uint32_t* status;
   uint64_t wait_limit_ns;
   float sm_scale;
-  int batch, groups, hq, hkv, group, page_size, num_pages, max_q_len;
+  int batch, groups, hq, hkv, group, page_size, num_pages, max_q_len, max_kv_len;
   int64_t rows_cap;
   int q8;
   int ctas;  // of the prefix kernel
@@ -78,7 +78,8 @@ __device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
   r.rows = static_cast<int>(rows);
   const int from = max(0, __ldg(a.prefix + 2 * g));
   r.end = __ldg(a.prefix + 2 * g + 1);
-  if (r.rows == 0 || r.end <= from) return r;
+  if (r.end > a.max_kv_len) r.bad = PDA_STATUS_TABLE_INVALID;  // (not pda_share_tables')
+  if (r.bad || r.rows == 0 || r.end <= from) return r;
   r.tile0 = from / kKeys;
   r.tiles = (r.end - 1) / kKeys + 1 - r.tile0;
   return r;
@@ -169,6 +170,8 @@ struct Parts {
     const int before = upto - mine - (upto_s - singles) * (kFull - cut.one) + (upto_i - items) * cut.pay;
     first = __shfl_sync(0xffffffffu, before, g);
   }
+  // Whether request b is one of a group that can be decoded.
+  __device__ __forceinline__ bool covers(int b) const { return !gr.bad && b >= gr.b0 && b < gr.b1; }
   __device__ __forceinline__ void late(const SharedArgs& a) {
     if (a.groups <= 32) return;
     cut.per = a.first[0];
@@ -188,7 +191,7 @@ struct RowParts {
     const int block = m / kRows;
     r = m % kRows;
     head_row = (h * a.rows_cap + p.gr.q0) * a.group + m;
-    if (p.gr.tiles == 0) return;
+    if (p.gr.tiles == 0 || m < 0 || m >= p.gr.rows * a.group) return;
     const Work<kG> w(a, p.gr);
     // its first and its last tile
     const uint32_t u = p.first + h * w.head(p.cut) + block * w.full(p.cut) + p.cut.pay;

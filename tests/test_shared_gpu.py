@@ -228,6 +228,48 @@ def test_groups_out_of_range():
     assert t.prefix[0].tolist() == [0, 64]
 
 
+@pytest.mark.parametrize("own", [300, 0])
+@pytest.mark.parametrize("bounds", [[0, 2, 4], [1, 3, 6], [0, 2, 9], [0, 3, 2], [-1, 3, 6], [5, 6, 6]])
+def test_requests_of_no_group(bounds, own):
+    """What the last step left in the tables is not decoded for them."""
+    w = S.make([(9, reqs(3)), (12, reqs(3))], dev=DEV)
+    w.params.max_kv_len = 4000
+    dec = B.Decoder(w.params, device=DEV)
+    sh, t = B.Shared(dec.plan, 2, own), S.device_tables(w)
+    S.run(w, sh, t)
+    torch.cuda.synchronize()
+    assert sh.status() == 0
+    t.group_indptr = S.ints(bounds, DEV)
+    out, lse = S.run(w, sh, t)
+    torch.cuda.synchronize()
+    assert sh.status() == B.PDA_STATUS_TABLE_INVALID
+    o, ob, l, lb = S.attention(w)
+    valid = [a >= 0 and b >= a and b <= 6 for a, b in zip(bounds, bounds[1:])]
+    for b in range(6):
+        if not any(ok and x <= b < y for ok, x, y in zip(valid, bounds, bounds[1:])):
+            o[b], l[b] = math.nan, math.nan
+    check(out, o, ob, "out")
+    check(lse, l, lb, "lse")
+
+
+def test_prefixes_that_are_not_of_the_tables():
+    """A prefix longer than any request may be is not read."""
+    w = S.make([(9, reqs(3)), (12, reqs(3))], dev=DEV)
+    w.params.max_kv_len = 4000
+    dec = B.Decoder(w.params, device=DEV)
+    for own in (100, 0):
+        sh, t = B.Shared(dec.plan, 2, own), S.device_tables(w)
+        S.run(w, sh, t)
+        t.prefix[1] = S.ints([0, 2 ** 31 - 1], DEV)
+        out, lse = S.run(w, sh, t, share=False)
+        torch.cuda.synchronize()
+        assert sh.status() == B.PDA_STATUS_TABLE_INVALID
+        o, ob, l, lb = S.attention(w)
+        o[3:], l[3:] = math.nan, math.nan
+        check(out, o, ob, "out")
+        check(lse, l, lb, "lse")
+
+
 def test_no_lse_and_fewer_rows_than_planned():
     w = S.make([(20, reqs(5, rows=2))], dev=DEV)
     w.params.max_q_len, w.params.max_batch, w.params.batch = 8, 16, 5
