@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
 
   // ---- a warp's steps of 16 tokens, kStages - 1 of them under way in front of the one at
   // work; a lane copies what it uses itself, so nothing has to wait for other lanes
-  const int from = W > 0 ? max(0, L - R - min(W, L) + 1) / kStep : 0;
+  const int low = W > 0 ? max(0, L - R - min(W, L) + 1) : 0;  // the first token that a row sees
+  const int from = low / kStep;
   const int steps = (L + kStep - 1) / kStep;
   const int P = a.page_size, shift = 31 - __clz(P);
   const int32_t* pages = a.page_table + own;
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
       const int64_t at = ok ? (page * o.sp + (t & (P - 1)) * o.st) * eb : 0;
       pg[e] = page_at(t + stride * kStep);
       // K: token g of the half, 16-byte pieces q, q + 4, ... of its row
-      const bool k_ok = ok && t + g < L;
+      const bool k_ok = ok && t + g < L && t + g >= low;
       const uint8_t* k_at = k_base + at + (k_ok ? g * o.st * eb : 0) + q * 16;
 #pragma unroll
       for (int i = 0; i < C::kPieces; ++i) copy_to<16>(k_to + (e * C::kPieces + i) * 512, k_at + i * 64, k_ok);
@@ -198,7 +199,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const int row = 2 * q + c;
-        const bool v_ok = ok && t + row < L;
+        const bool v_ok = ok && t + row < L && t + row >= low;
         const uint8_t* v_at = v_base + at + (v_ok ? row * o.st * eb : 0) + g * C::kVBytes;
 #pragma unroll
         for (int set = 0; set < C::kSets; ++set)

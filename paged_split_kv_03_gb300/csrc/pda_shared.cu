@@ -70,6 +70,7 @@ struct Item {
   int q0;      // the group's first row in q
   int b0, b1;  // its requests
   int t0, t1;
+  int low;     // the first token of the prefix that a row sees, rounded down to a page
   int end;     // the prefix's end, tokens
   int table;   // offset of the prefix's pages in page_table
   int cut;     // the segment does not start its item: its partials go to the CTA's area
@@ -183,8 +184,8 @@ __device__ __forceinline__ void tile_order(int i, int n, int& v, int& j) {
 //
 // Even warps load K, odd ones V, a unit (or raw slot) a warp in turn; one warp loads both
 // where both are widened, as they share the raw slots. A unit's boxes (a page's tokens x
-// 128 bytes, or a head's codes) are its warp's lanes'. A page behind the prefix is one
-// past the cache: such a box reads as zeros.
+// 128 bytes, or a head's codes) are its warp's lanes'. A page behind the prefix, or in
+// front of what any row sees, is one past the cache: such a box reads as zeros.
 //
 // A wait tells a slot's rounds apart by their parity only, so no warp may stand two
 // rounds in front of what has been read: with at least as many slots as warps in turn,
@@ -237,7 +238,7 @@ __device__ __forceinline__ void load_role(const SharedArgs& a, Shared* sh, uint8
     int v, j, c;
     unit_of(k, n, v, j, c);
     const int key = first_key(j, c);
-    if (!mine || key >= it.end) return a.num_pages;
+    if (!mine || key < it.low || key >= it.end) return a.num_pages;
     return __ldg(a.page_table + it.table + key / P);
   };
   uint32_t t = 0, last = 0;  // key tiles in front of the segment; units up to here
@@ -650,6 +651,7 @@ __device__ __forceinline__ void WorkList<kG>::run(const SharedArgs& a, Shared* s
       it.b1 = from(look.r.b1);
       it.t0 = tile0 + t0;
       it.t1 = tile0 + t1;
+      it.low = from(look.r.low);
       it.end = from(look.r.end);
       it.cut = t0 > 0;
       it.table = from(look.table);

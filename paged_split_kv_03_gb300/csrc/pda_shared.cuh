@@ -59,7 +59,7 @@ constexpr int kTile = 128;          // packed rows of a row tile
 
 // A group's rows and its prefix's key tiles.
 struct Group {
-  int b0, b1, q0, rows, tile0, tiles, end;
+  int b0, b1, q0, rows, tile0, tiles, low, end;  // tokens [low, end), from tile0's first on
   uint32_t bad;
 };
 __device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
@@ -67,7 +67,7 @@ __device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
   r.b0 = a.group_indptr ? __ldg(a.group_indptr + g) : 0;
   r.b1 = a.group_indptr ? __ldg(a.group_indptr + g + 1) : a.batch;
   r.bad = r.b0 < 0 || r.b1 < r.b0 || r.b1 > a.batch ? PDA_STATUS_TABLE_INVALID : 0u;
-  r.q0 = r.rows = r.tile0 = r.tiles = r.end = 0;
+  r.q0 = r.rows = r.tile0 = r.tiles = r.low = r.end = 0;
   if (r.bad) return r;
   r.q0 = __ldg(a.qo_indptr + r.b0);
   const int64_t rows = static_cast<int64_t>(__ldg(a.qo_indptr + r.b1)) - r.q0;
@@ -76,11 +76,11 @@ __device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
     return r;
   }
   r.rows = static_cast<int>(rows);
-  const int from = max(0, __ldg(a.prefix + 2 * g));
+  r.low = max(0, __ldg(a.prefix + 2 * g));
   r.end = __ldg(a.prefix + 2 * g + 1);
   if (r.end > a.max_kv_len) r.bad = PDA_STATUS_TABLE_INVALID;  // (not pda_share_tables')
-  if (r.bad || r.rows == 0 || r.end <= from) return r;
-  r.tile0 = from / kKeys;
+  if (r.bad || r.rows == 0 || r.end <= r.low) return r;
+  r.tile0 = r.low / kKeys;
   r.tiles = (r.end - 1) / kKeys + 1 - r.tile0;
   return r;
 }

@@ -228,6 +228,29 @@ def test_groups_out_of_range():
     assert t.prefix[0].tolist() == [0, 64]
 
 
+@pytest.mark.parametrize("max_kv", [1000, 4000])  # own tokens by one kernel; by pda_decode's
+@pytest.mark.parametrize("page", [8, 16, 64])
+@pytest.mark.parametrize("kind,dim", [("bf16", 128), ("e4m3_token", 128), ("bf16", 256), ("int8_tensor", 64),
+                                      ("e4m3_tensor", 256)])
+def test_windows_leave_pages_behind(kind, dim, page, max_kv):
+    """Pages in front of every row's window may hold anything, as after they were freed."""
+    rs = [(70, 1), (33, 2), (200, 1), (90, 3)]
+    w = S.make([(600 // page, rs), (200 // page, rs)], kind=kind, dim=dim, page=page, dev=DEV,
+               windows=[100, 333, 230, 95, 40, 35, 52, 150])
+    w.params.max_kv_len = max_kv
+    seen = set()
+    for b, n in enumerate(w.kv_len):
+        low = max(0, n - w.rows[b] - w.windows[b] + 1)
+        seen.update(w.tables[b][low // page:])
+    gone = [i for i in range(w.pages) if i not in seen]
+    assert len(gone) > 300 // page
+    for c, s in zip(w.cache, w.scale):
+        c[gone] = -128 if c.dtype is torch.int8 else 0x7f if c.dtype is torch.uint8 else math.nan
+        if s is not None and s.dim() > 1:
+            s[gone] = math.nan
+    parity(w)
+
+
 @pytest.mark.parametrize("own", [300, 0])
 @pytest.mark.parametrize("bounds", [[0, 2, 4], [1, 3, 6], [0, 2, 9], [0, 3, 2], [-1, 3, 6], [5, 6, 6]])
 def test_requests_of_no_group(bounds, own):
