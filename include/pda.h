@@ -668,9 +668,10 @@ int pda_share_tables(const pda_shared_plan_t* plan, const pda_shared_tables* tab
 /* Decode on the tables that pda_share_tables filled, as pda_decode: q, the caches,
  * scales, out, lse (or NULL), sm_scale and max_q_len are its arguments. An invalid
  * request's rows are left unwritten, with its status bits; so are those of a request
- * with more own tokens than planned, and of one in no group or in an invalid one. Keys and values that a row does not see for its window
- * have to be finite where another row of its group sees them; pages that no row of the group
- * sees may hold anything. */
+ * with more own tokens than planned, and of one in no group or in an invalid one.
+ * Keys and values that a row does not see for its window have to be finite where
+ * another row of its group sees them; pages that no row of the group sees may hold
+ * anything. */
 int pda_decode_shared(const pda_shared_plan_t* plan, const void* q, const void* k_pages,
                       const void* v_pages, const pda_shared_tables* tables, int32_t max_q_len,
                       float sm_scale, const float* k_scale, const float* v_scale, void* out,
