@@ -1274,7 +1274,12 @@ __global__ void __launch_bounds__(kShareThreads) share_tables(const __grid_const
     for (int64_t k = static_cast<int64_t>(rank) * kShareWarps + warp; k < work; k += step) {
       const int stretch = static_cast<int>(k / n_req), b = b0 + static_cast<int>(k % n_req);
       const int j0 = stretch * kStretch;
-      if (j0 && j0 >= static_cast<int>(cluster_load(pages_at))) break;  // as are all behind it
+      if (j0) {
+        // (one lane's reading, as others lower the word meanwhile: all lanes leave or none)
+        int seen = 0;
+        if (lane == 0) seen = static_cast<int>(cluster_load(pages_at));
+        if (j0 >= __shfl_sync(0xffffffffu, seen, 0)) break;  // as are all behind it
+      }
       int rows, len;
       if (!fits(b, rows, len)) continue;
       const int at = __ldg(a.t.kv_indptr + b);
