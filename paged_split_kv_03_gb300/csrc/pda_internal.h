@@ -52,6 +52,10 @@ struct DecodeArgs {
   uint32_t inject;        // PDA_INJECT_* test hooks set by the host (0 in normal use)
   int final_splits;       // splits of a request whose results stage 1 writes itself: 1, or 0 where
                           // all are partials, to be joined with those of a shared prefix
+  // bounds of the groups of requests that share a prefix, or NULL: stage 1 leaves out
+  // requests of no group, whose page_table places and lengths nobody has written
+  const int32_t* group_indptr;
+  int groups;
 };
 
 // The KV range one (request, split) covers. Every kernel derives it from the
@@ -151,6 +155,40 @@ inline bool on_device(int device) {
 int static_scratch(int device, cudaStream_t s, void** out);
 
 #ifdef __CUDACC__
+// The group that lists request b: the first whose bounds, indptr[g] and the next, hold it and
+// are requests of the batch; -1: none. NULL: one group of all. A whole warp. (The loads of
+// 128 groups are under way together: one round trip where a search by halves takes seven.)
+__device__ __forceinline__ int group_of_request(const int32_t* indptr, int groups, int batch, int b) {
+  if (!indptr) return 0;
+  constexpr int kAtOnce = 4;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int g0 = 0; g0 < groups; g0 += 32 * kAtOnce) {
+    int lo[kAtOnce], hi[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int g = g0 + 32 * k + lane;
+      lo[k] = hi[k] = -1;
+      if (g < groups) {
+        lo[k] = __ldg(indptr + g);
+        hi[k] = __ldg(indptr + g + 1);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t has = __ballot_sync(0xffffffffu, lo[k] >= 0 && lo[k] <= b && b < hi[k] && hi[k] <= batch);
+      if (has) return g0 + 32 * k + __ffs(has) - 1;
+    }
+  }
+  return -1;
+}
+
+// The same for stage 1, as a call: its registers are full (inlined, two builds spill), and only
+// decodes behind shared prefixes make it.
+static __device__ __noinline__ bool no_group_lists(const int32_t* indptr, int groups, int batch, int b) {
+  return group_of_request(indptr, groups, batch, b) < 0;
+}
+
 // Stage 1's first CTA, on each of its ways out: where the launch overlaps the kernel in
 // front of it, what follows stage 1 follows both. (One CTA is enough, and the others make
 // room; without such a launch there is nothing to wait for.)

@@ -183,6 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1) stage1_mma(const __grid_constant_
   WorkItem wi;
   if (!work_item(a, blockIdx.x, wi)) return;
   const int hb = wi.hb, split = wi.split, hkv = wi.hkv, b = wi.b;
+  if (a.group_indptr && no_group_lists(a.group_indptr, a.groups, a.batch, b)) {  // (the join says so)
+    end_behind_previous();
+    return;
+  }
   const int q0 = a.qo_indptr[b];
   const int R = a.qo_indptr[b + 1] - q0;
   const int L = a.kv_len[b];

@@ -148,15 +148,19 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
   const int L = __ldg(a.own_len + b), own = __ldg(a.own_indptr + b);
   const int W = a.window ? __ldg(a.window + b) : 0;
   const int m0 = blockIdx.y * kRows, M = R * a.group;
-  if (R <= 0 || R > o.max_q_len || L < R || L > o.max_kv_len || q0 < 0 || q0 + R > a.rows_cap || m0 >= M) {
+  // (own_len and own_indptr of a request of no group are not pda_share_tables')
+  const int group = group_of_request(a.group_indptr, a.groups, a.batch, b);
+  if (group < 0 || R <= 0 || R > o.max_q_len || L < R || L > o.max_kv_len || q0 < 0 || q0 + R > a.rows_cap ||
+      m0 >= M) {
     if (tid == 0 && h == 0 && blockIdx.y == 0 && rank == 0) {
       uint32_t bits = 0u;
       if (R < 0 || R > o.max_q_len) bits = PDA_STATUS_ROWS_GT_MAX;
+      else if (R > 0 && group < 0) bits = PDA_STATUS_TABLE_INVALID;
       else if (R > 0 && L < R) bits = PDA_STATUS_KV_LEN_LT_ROWS;
       else if (R > 0 && L > o.max_kv_len) bits = PDA_STATUS_KV_LEN_GT_MAX;
       else if (R > 0 && q0 + R > a.rows_cap) bits = PDA_STATUS_ROWS_GT_CAP;
       // (share_tables has said what is wrong where it left a request out)
-      if (bits && L != -1) atomicOr(a.status, bits);
+      if (bits && (L != -1 || group < 0)) atomicOr(a.status, bits);
     }
     if (blockIdx.x == 0 && blockIdx.y == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -487,10 +491,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
       for (int e = 0; e < kV; ++e) join.acc[e] = fmaf(f, v[c][e] * times, join.acc[e]);
     }
   };
-  Parts<kG> parts(a, b);
-  const bool covered = parts.covers(b);
-  if (!covered && tid == 0 && h == 0 && m0 == 0 && rank == 0) atomicOr(a.status, PDA_STATUS_TABLE_INVALID);
-  const int live = covered ? min(kRows, M - m0) : 0, hw = lane >> 4;
+  Parts<kG> parts(a, group);
+  if (!parts.valid() && tid == 0 && h == 0 && m0 == 0 && rank == 0) atomicOr(a.status, PDA_STATUS_TABLE_INVALID);
+  const int live = parts.valid() ? min(kRows, M - m0) : 0, hw = lane >> 4;
   __syncthreads();
   if (ctas > 1) {  // one part a CTA, in the first warp's place
 #pragma unroll 1
@@ -568,8 +571,9 @@ __global__ void __launch_bounds__(256, 3) shared_join(const __grid_constant__ Sh
     live = i < R && R <= o.max_q_len && L >= R && L <= o.max_kv_len && q0 >= 0 && q0 + R <= a.rows_cap;
     if (live) own = split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
   }
-  Parts<kG> parts(a, live ? b : 0);
-  if (live && !parts.covers(b)) {
+  const int group = live ? group_of_request(a.group_indptr, a.groups, a.batch, b) : 0;
+  Parts<kG> parts(a, max(group, 0));
+  if (live && (group < 0 || !parts.valid())) {
     if ((threadIdx.x & 31) == 0) atomicOr(a.status, PDA_STATUS_TABLE_INVALID);
     live = false;
   }

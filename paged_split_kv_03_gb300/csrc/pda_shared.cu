@@ -1531,6 +1531,8 @@ extern "C" int pda_decode_shared(const pda_shared_plan_t* sp, const void* q, con
   DecodeArgs o = decode_args(plan, q, k_pages, v_pages, t.page_table, t.own_indptr, t.own_len,
                              t.qo_indptr, max_q_len, t.window, sm_scale, k_scale, v_scale, out, lse, scratch);
   o.final_splits = 0;
+  o.group_indptr = t.group_indptr;
+  o.groups = sp->groups;
   SharedArgs a = {};
   char* base = static_cast<char*>(scratch);
   a.q = q;

@@ -142,17 +142,11 @@ template <int kG>
 struct Parts {
   Group gr;
   Cut cut;
-  int g = 0, first = 0;
-  // Of the group of request b; a whole warp. What the prefix kernel wrote down (more groups
+  int g, first = 0;
+  // Of group `of`; a whole warp. What the prefix kernel wrote down (more groups
   // than lanes) is read by `late`, behind that kernel.
-  __device__ __forceinline__ Parts(const SharedArgs& a, int b) {
+  __device__ __forceinline__ Parts(const SharedArgs& a, int of) : g(of) {
     const int lane = threadIdx.x & 31;
-    int top = a.groups - 1;  // the last group that starts at or before the request
-    while (g < top) {
-      const int mid = (g + top + 1) >> 1;
-      if (__ldg(a.group_indptr + mid) <= b) g = mid;
-      else top = mid - 1;
-    }
     gr = group_of(a, g);
     if (a.groups > 32) return;
     Work<kG> w;
@@ -170,8 +164,8 @@ struct Parts {
     const int before = upto - mine - (upto_s - singles) * (kFull - cut.one) + (upto_i - items) * cut.pay;
     first = __shfl_sync(0xffffffffu, before, g);
   }
-  // Whether request b is one of a group that can be decoded.
-  __device__ __forceinline__ bool covers(int b) const { return !gr.bad && b >= gr.b0 && b < gr.b1; }
+  // Whether its requests can be decoded.
+  __device__ __forceinline__ bool valid() const { return !gr.bad; }
   __device__ __forceinline__ void late(const SharedArgs& a) {
     if (a.groups <= 32) return;
     cut.per = a.first[0];

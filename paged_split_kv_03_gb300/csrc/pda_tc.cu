@@ -1119,6 +1119,10 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
   WorkItem wi;
   if (!work_item(a, blockIdx.x, wi)) return;
   const int hb = wi.hb, split = wi.split, hkv = wi.hkv, b = wi.b;
+  if (a.group_indptr && no_group_lists(a.group_indptr, a.groups, a.batch, b)) {  // (the join says so)
+    end_behind_previous();
+    return;
+  }
   // the request's scalars, loaded together (one round trip)
   const int q0 = a.qo_indptr[b];
   const int q1 = a.qo_indptr[b + 1];

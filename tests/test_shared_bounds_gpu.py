@@ -1,7 +1,8 @@
 """Where decode behind shared prefixes ends what it reads: lists that part while other warps
-compare them."""
+compare them, and requests of no group."""
 from __future__ import annotations
 
+import math
 import random
 import types
 
@@ -11,6 +12,7 @@ import torch
 import pages_ref as ref
 import shared_ref as S
 from paged_split_kv_03_gb300 import binding as B
+from test_shared_gpu import check, reqs
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -50,3 +52,33 @@ def test_lists_that_part_while_others_compare(groups):
         B.pda_share_tables(sh.plan, *S.args(t), sh.scratch)
         assert t.prefix.tolist() == want
     assert sh.status() == 0
+
+
+@pytest.mark.parametrize("own", [300, 0])  # own tokens by one kernel; by pda_decode's stage 1
+@pytest.mark.parametrize("kind,dim", [("bf16", 128), ("bf16", 64), ("e4m3_token", 256)])
+@pytest.mark.parametrize("bounds", [[0, 2, 4], [1, 3, 6], [0, 3, 2], [-1, 3, 6], [5, 6, 6], [7, 9, 8]])
+def test_places_of_requests_of_no_group_are_not_looked_up(bounds, kind, dim, own):
+    """No step has written their lengths and places: what stands there leads to page ids out of
+    range (and would be seen in the status), and is left as it is."""
+    w = S.make([(9, reqs(3)), (12, reqs(3))], kind=kind, dim=dim, dev=DEV)
+    w.params.max_kv_len = 4000
+    dec = B.Decoder(w.params, device=DEV)
+    sh, t = B.Shared(dec.plan, 2, own), S.device_tables(w)
+    t.page_table = ints(w.page_table + [w.pages + 7] * 40)
+    t.group_indptr = ints(bounds)
+    t.own_indptr.fill_(len(w.page_table))
+    t.own_len.fill_(30)
+    out, lse = S.run(w, sh, t)
+    torch.cuda.synchronize()
+    o, ob, l, lb = S.attention(w)
+    valid = [(x, y) for x, y in zip(bounds, bounds[1:]) if 0 <= x <= y <= 6]
+    for b in range(6):
+        if not any(x <= b < y for x, y in valid):
+            o[b], l[b] = math.nan, math.nan
+            assert int(t.own_len[b]) == 30 and int(t.own_indptr[b]) == len(w.page_table)
+    if valid:
+        check(out, o, ob, "out")
+        check(lse, l, lb, "lse")
+    else:
+        assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+    assert sh.status() == B.PDA_STATUS_TABLE_INVALID
