@@ -1276,9 +1276,8 @@ __global__ void __launch_bounds__(kShareThreads) share_tables(const __grid_const
       const int j0 = stretch * kStretch;
       if (j0) {
         // (one lane's reading, as others lower the word meanwhile: all lanes leave or none)
-        int seen = 0;
-        if (lane == 0) seen = static_cast<int>(cluster_load(pages_at));
-        if (j0 >= __shfl_sync(0xffffffffu, seen, 0)) break;  // as are all behind it
+        const int seen = __shfl_sync(0xffffffffu, static_cast<int>(cluster_load(pages_at)), 0);
+        if (j0 >= seen) break;  // as are all behind it
       }
       int rows, len;
       if (!fits(b, rows, len)) continue;
