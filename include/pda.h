@@ -636,7 +636,7 @@ typedef struct {
   const int32_t* qo_indptr;    /* [batch + 1] */
   const int32_t* window;       /* [batch] or NULL */
   const int32_t* group_indptr; /* [groups + 1] the requests of each group, side by side: from 0 to
-                                  batch; NULL = one group of all (groups 1) */
+                                  batch, none below one in front; NULL = one group of all (groups 1) */
   int32_t* prefix;             /* [groups, 2] written: tokens [first, end) of the prefix that the
                                   group's rows see */
   int32_t* own_indptr;         /* [batch] written: a request's own pages in page_table; not kv_indptr */
@@ -660,8 +660,9 @@ int pda_shared_plan(const pda_plan_t* plan, int32_t groups, int32_t max_own_len,
  * `end`. Own tokens are the L - end behind it, R of them at least. A request without
  * rows takes no part (own_len 0), nor does an invalid one (own_len -1; L < R, R out
  * of range or L above max_kv_len, with pda_decode's status bits); a page id out of
- * range ends a prefix. A group whose bounds are no requests is left unwritten, and so are
- * requests of no group (PDA_STATUS_TABLE_INVALID). */
+ * range ends a prefix. A group whose bounds are no requests, or one that starts in front of
+ * an earlier bound, is left unwritten, and so are requests of no valid group
+ * (PDA_STATUS_TABLE_INVALID). */
 int pda_share_tables(const pda_shared_plan_t* plan, const pda_shared_tables* tables, void* scratch,
                      pda_stream_t stream);
 

@@ -155,13 +155,15 @@ inline bool on_device(int device) {
 int static_scratch(int device, cudaStream_t s, void** out);
 
 #ifdef __CUDACC__
-// The group that lists request b: the first whose bounds, indptr[g] and the next, hold it and
-// are requests of the batch; -1: none. NULL: one group of all. A whole warp. (The loads of
-// 128 groups are under way together: one round trip where a search by halves takes seven.)
+// The group that lists request b: its bounds, indptr[g] and the next, hold the request, are
+// requests of the batch, and no bound in front is above them (so no two groups that are decoded
+// list the same request); -1: none. NULL: one group of all. A whole warp. (The loads of 128
+// groups are under way together: one round trip where a search by halves takes seven.)
 __device__ __forceinline__ int group_of_request(const int32_t* indptr, int groups, int batch, int b) {
   if (!indptr) return 0;
   constexpr int kAtOnce = 4;
   const int lane = threadIdx.x & 31;
+  int top = -1;  // the highest bound in front
 #pragma unroll 1
   for (int g0 = 0; g0 < groups; g0 += 32 * kAtOnce) {
     int lo[kAtOnce], hi[kAtOnce];
@@ -177,7 +179,10 @@ __device__ __forceinline__ int group_of_request(const int32_t* indptr, int group
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const uint32_t has = __ballot_sync(0xffffffffu, lo[k] >= 0 && lo[k] <= b && b < hi[k] && hi[k] <= batch);
-      if (has) return g0 + 32 * k + __ffs(has) - 1;
+      // (the first group that holds it decides: its end is a bound above the request)
+      const int at = has ? __ffs(has) - 1 : 32;
+      top = max(top, __reduce_max_sync(0xffffffffu, lane < at ? lo[k] : -1));
+      if (has) return __shfl_sync(0xffffffffu, lo[k], at) >= top ? g0 + 32 * k + at : -1;
     }
   }
   return -1;

@@ -86,6 +86,7 @@ struct Shared {
   int coarse[kCoarse];           // work in front of every 32 groups
   int coarse_items[kCoarse];     // items there
   int coarse_singles[kCoarse];   // tiles of single row tiles there
+  int coarse_top[kCoarse];       // the highest bound there
   float2 rows[kTile];            // a row's power of two; then its maximum and sum in the odd tiles
 };
 
@@ -525,12 +526,12 @@ struct Look {
   Group r = {};
   Work<kG> w;
   int table = -1;
-  __device__ __forceinline__ void at(const SharedArgs& a, int g) {
+  // (`top`: the highest bound in front of the 32)
+  __device__ __forceinline__ void at(const SharedArgs& a, int g, int& top) {
     r = {};
-    w = Work<kG>();
     table = -1;
-    if (g >= a.groups) return;
-    r = group_of(a, g);
+    if (g < a.groups) r = group_of(a, g);
+    if (a.groups > 1) no_overlap(r, g < a.groups, top);
     w = Work<kG>(a, r);
     if (!r.bad && r.b1 > r.b0) {
       const int own = __ldg(a.own_len + r.b0), page = __ldg(a.own_indptr + r.b0);
@@ -576,11 +577,12 @@ struct WorkList {
 template <int kG>
 __device__ __forceinline__ void WorkList<kG>::prepare(const SharedArgs& a, Shared* sh) {
   const int lane = threadIdx.x & 31;
-  int w32, i32, s32;
+  int w32, i32, s32, top = INT_MIN;
 #pragma unroll 1
   for (int g0 = 0; g0 < a.groups; g0 += 32) {
     known = g0 >> 5;
-    look.at(a, g0 + lane);
+    if (lane == 0) sh->coarse_top[known] = top;
+    look.at(a, g0 + lane, top);
     bits |= look.r.bad;
     sums(a, lane, w32, i32, s32);
     if (lane == 0) {
@@ -618,7 +620,8 @@ __device__ __forceinline__ void WorkList<kG>::run(const SharedArgs& a, Shared* s
       }
       if (c != known) {
         known = c;
-        look.at(a, 32 * c + lane);
+        int before = sh->coarse_top[c];
+        look.at(a, 32 * c + lane, before);
         sums(a, lane, w32, i32, s32);
       }
       const int start = coarse(sh, c) + place(lane_work, lane_items, lane_singles);
@@ -689,7 +692,8 @@ __device__ __forceinline__ void WorkList<kG>::run(const SharedArgs& a, Shared* s
   if (a.groups <= 32) return;
 #pragma unroll 1
   for (int g0 = 0; g0 < a.groups; g0 += 32) {
-    look.at(a, g0 + lane);
+    int before = sh->coarse_top[g0 >> 5];
+    look.at(a, g0 + lane, before);
     sums(a, lane, w32, i32, s32);
     if (g0 + lane < a.groups) a.first[3 + g0 + lane] = coarse(sh, g0 >> 5) + place(lane_work, lane_items, lane_singles);
   }
@@ -1234,7 +1238,9 @@ __global__ void __launch_bounds__(kShareThreads) share_tables(const __grid_const
   const int b0 = a.t.group_indptr ? __ldg(a.t.group_indptr + g) : 0;
   int b1 = a.t.group_indptr ? __ldg(a.t.group_indptr + g + 1) : a.batch;
   uint32_t bits = 0u;
-  const bool valid = b0 >= 0 && b1 >= b0 && b1 <= a.batch;
+  int top = INT_MIN;  // no bound in front may be above the group's (no_overlap)
+  for (int i = lane; i < g; i += 32) top = max(top, __ldg(a.t.group_indptr + i));
+  const bool valid = b0 >= 0 && b1 >= b0 && b1 <= a.batch && b0 >= __reduce_max_sync(0xffffffffu, top);
   if (!valid) {
     bits = PDA_STATUS_TABLE_INVALID;
     b1 = b0;

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -85,6 +86,26 @@ __device__ __forceinline__ Group group_of(const SharedArgs& a, int g) {
   return r;
 }
 
+// A group a lane: bad where a bound in front (of a lane in front, or `top`) is above its first
+// request, so that no two valid groups list the same one. The highest bound so far to `top`.
+__device__ __forceinline__ void no_overlap(Group& r, bool live, int& top) {
+  const int lo = live ? r.b0 : INT_MIN;
+  if (__any_sync(0xffffffffu, live && (lo < top || r.b1 < lo))) {  // (bounds that never fall: nothing to do)
+    int x = lo;
+#pragma unroll 1
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if ((threadIdx.x & 31) >= d) x = max(x, y);
+    }
+    x = __shfl_up_sync(0xffffffffu, x, 1);
+    if (live && lo < ((threadIdx.x & 31) ? max(x, top) : top)) {
+      r.bad |= PDA_STATUS_TABLE_INVALID;
+      r.rows = r.tiles = 0;
+    }
+  }
+  top = max(top, __reduce_max_sync(0xffffffffu, lo));
+}
+
 // How the work is cut. An item is a block of kRows packed rows of a kv head, over the
 // prefix's key tiles; group by group, then kv heads, then blocks, the items stand on one
 // axis, and CTA c has the stretch [c per, (c + 1) per) of it: the tiles that begin there.
@@ -143,14 +164,22 @@ struct Parts {
   Group gr;
   Cut cut;
   int g, first = 0;
-  // Of group `of`; a whole warp. What the prefix kernel wrote down (more groups
+  // Of group `of` (group_of_request's); a whole warp. What the prefix kernel wrote down (more groups
   // than lanes) is read by `late`, behind that kernel.
   __device__ __forceinline__ Parts(const SharedArgs& a, int of) : g(of) {
     const int lane = threadIdx.x & 31;
     gr = group_of(a, g);
     if (a.groups > 32) return;
     Work<kG> w;
-    if (lane < a.groups) w = Work<kG>(a, a.groups == 1 ? gr : group_of(a, lane));
+    if (a.groups == 1) {
+      if (lane == 0) w = Work<kG>(a, gr);
+    } else {
+      Group mine = {};
+      if (lane < a.groups) mine = group_of(a, lane);
+      int top = INT_MIN;
+      no_overlap(mine, lane < a.groups, top);
+      w = Work<kG>(a, mine);
+    }
     const int mine = a.hkv * w.head(Cut()), singles = w.single ? a.hkv * w.tiles : 0, items = a.hkv * w.blocks;
     int upto = mine, upto_s = singles, upto_i = items;
     if (a.groups > 1) {

@@ -1,5 +1,5 @@
 """Where decode behind shared prefixes ends what it reads: lists that part while other warps
-compare them, and requests of no group."""
+compare them, requests of no group, and bounds of groups that fall."""
 from __future__ import annotations
 
 import math
@@ -82,3 +82,35 @@ def test_places_of_requests_of_no_group_are_not_looked_up(bounds, kind, dim, own
     else:
         assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
     assert sh.status() == B.PDA_STATUS_TABLE_INVALID
+
+
+@pytest.mark.parametrize("own", [300, 0])
+@pytest.mark.parametrize("dim", [128, 256])
+@pytest.mark.parametrize("bounds", [
+    [0, 5, 3, 6], [0, 3, 2, 6], [0, 6, 0, 6], [4, 6, 0, 4], [3, 3, 0, 6], [0, 3, 2, 3, 6], [0, 2, 9, 2, 6],
+    [0] * 20 + [3, 2] + [3] * 20 + [6], [0] * 70 + [5, 4, 5] + [5] * 70 + [6], [1] * 40 + [0] * 40 + [6]])
+def test_groups_that_would_list_the_same_requests(bounds, dim, own):
+    """Of two groups with a request in common the later one is not decoded, and its requests'
+    places are left alone."""
+    w = S.make([(9, reqs(3)), (12, reqs(3))], dim=dim, dev=DEV)
+    w.params.max_kv_len = 4000
+    dec = B.Decoder(w.params, device=DEV)
+    groups = len(bounds) - 1
+    sh, t = B.Shared(dec.plan, groups, own), S.device_tables(w)
+    t.group_indptr, t.prefix = ints(bounds), ints([[-9, -9]] * groups)
+    out, lse = S.run(w, sh, t)
+    torch.cuda.synchronize()
+    assert sh.status() == B.PDA_STATUS_TABLE_INVALID
+    o, ob, l, lb = S.attention(w)
+    valid = [0 <= x <= y <= 6 and x >= max(bounds[:g + 1]) for g, (x, y) in enumerate(zip(bounds, bounds[1:]))]
+    listed = [b for b in range(6)
+              if any(ok and x <= b < y for ok, x, y in zip(valid, bounds, bounds[1:]))]
+    assert [row[1] == -9 for row in t.prefix.tolist()] == [not ok for ok in valid]
+    assert [b for b in range(6) if int(t.own_len[b]) != -9] == listed
+    for b in set(range(6)) - set(listed):
+        o[b], l[b] = math.nan, math.nan
+    if listed:
+        check(out, o, ob, "out")
+        check(lse, l, lb, "lse")
+    else:
+        assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
