@@ -390,6 +390,7 @@ __device__ __forceinline__ void softmax_role(const DecodeArgs& a, const SoftmaxC
 
   float qk_scale = a.sm_scale * kLog2e;  // logits in log2 units
   if constexpr (C::kQSplit) qk_scale *= x.colscale[0];  // the query's 2^-a
+  if constexpr (C::kF16Ops) qk_scale *= 65536.f;        // (columns' scales are 2^-16 of the rows' powers)
   float v_final = 1.f;
   if constexpr (SMODE == PDA_SCALE_TENSOR) {
     qk_scale *= __ldg(a.k_scale);
@@ -447,7 +448,6 @@ __device__ __forceinline__ void softmax_role(const DecodeArgs& a, const SoftmaxC
   for (int j = 0; j < x.ntiles; ++j) {
     const int tok = x.t_begin + j * kTok + r;
     float row_scale = qk_scale, log2_vs = 0.f, inv_vs = 1.f;
-    if constexpr (C::kF16Ops) row_scale *= x.colscale[0];
     if constexpr (SMODE == PDA_SCALE_TOKEN_HEAD) {
       const float ks = ks_a;
       float vs = vs_a;
@@ -494,7 +494,8 @@ __device__ __forceinline__ void softmax_role(const DecodeArgs& a, const SoftmaxC
         } else {
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < KC; ++e) s[ch * KC + e] = v[e];
+          for (int e = 0; e < KC; ++e)  // (f16 operands: times the column's power of two, exact)
+            s[ch * KC + e] = C::kF16Ops ? v[e] * x.colscale[c0 + ch * KC + e] : v[e];
         }
       }
     }
@@ -1243,7 +1244,7 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
       if (st < C::kNmax) {
 #pragma unroll
         for (int f = 0; f < C::kFrames; ++f) m_used[f * C::kNmax + st] = kMInit;
-        colscale[st] = 1.f;
+        if constexpr (!C::kF16Ops) colscale[st] = 1.f;  // (f16 operands: with the query, below)
       }
       // ---- query operand Q^T (K-major, 128-byte swizzle), rows n < N (zero
       // past M); every load is issued before the first store, so the tile
@@ -1263,32 +1264,30 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
                 static_cast<const uint8_t*>(a.q) +
                 (((int64_t)(q0 + n / hpc) * a.hq + head0 + n % hpc) * D) * C::kElt + cch * 16));
         }
-        float by = 1.f;
-        if constexpr (C::kF16Ops) {
-          // f16 operands: where the CTA's largest |Q| is not in [2^-6, 2^12), its power of
-          // two is taken out first (and put back into the logit scale)
-          uint32_t top = 0u;
-#pragma unroll
-          for (int it = 0; it < kIters; ++it) {
-            const uint32_t w[4] = {qv[it].x, qv[it].y, qv[it].z, qv[it].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] << 16 & 0x7FFF0000u, w[e] & 0x7FFF0000u));
-          }
-          top = __reduce_max_sync(0xffffffffu, top);
-          if (lane == 0) red[sw] = __uint_as_float(top);
-          group_sync<C::kSmThreads>();
-#pragma unroll
-          for (int w = 0; w < C::kSmWarps; ++w) top = max(top, __float_as_uint(red[w]));
-          int ex = static_cast<int>(top >> 23) - 127;
-          if (top == 0u || ex == 128 || (ex >= -6 && ex < 12)) ex = 0;
-          ex = max(-126, min(126, ex));
-          by = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-          if (st == 0) colscale[0] = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
-        }
 #pragma unroll
         for (int it = 0; it < kIters; ++it) {
           const int idx = st + it * C::kSmThreads;
           const int n = idx / kPadChunks, cch = idx % kPadChunks;
+          float by = 1.f;
+          if constexpr (C::kF16Ops) {
+            // f16 operands: a row whose largest |Q| is not in [2^-6, 2^16), which f16 holds
+            // without loss down to 2^-8 of it and more, goes in without its power of two, which
+            // the logits get back. Each row for itself: a row of ordinary size beside one of
+            // 2^15 would lose bits that count with the same power taken out.
+            static_assert(kPadChunks <= 32 && 32 % kPadChunks == 0, "a row is one warp's");
+            const uint32_t w[4] = {qv[it].x, qv[it].y, qv[it].z, qv[it].w};
+            uint32_t top = 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] << 16 & 0x7FFF0000u, w[e] & 0x7FFF0000u));
+#pragma unroll
+            for (int d = 1; d < kPadChunks; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            int ex = static_cast<int>(top >> 23) - 127;
+            if (top == 0u || ex == 128 || (ex >= -6 && ex < 16)) ex = 0;
+            ex = max(-110, min(126, ex));
+            by = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+            // (2^-16 of it: S is below 2^16, so that their product stays in range)
+            if (cch == 0 && n < C::kNmax) colscale[n] = __uint_as_float(static_cast<uint32_t>(111 + ex) << 23);
+          }
           if (n < N) {
             uint4 v = qv[it];
             if constexpr (C::kF16Ops) v = bf16x8_to_f16x8(v, by);
