@@ -65,7 +65,7 @@ constexpr float kTh = 8.0f;        // lazy rescale threshold, log2 units (P <= 2
 constexpr float kLog2e = 1.4426950408889634f;
 // running maximum before any key: finite, so a column with no visible key
 // so far gives ex2(-inf - kMInit) = 0 rather than NaN
-constexpr float kMInit = -1.0e30f;
+constexpr float kMInit = -3.0e38f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ------------------------------------------------------------------ helpers
