@@ -437,7 +437,8 @@ __device__ __forceinline__ void widen_role(const SharedArgs& a, Shared* sh, uint
   int page = -1;
   auto load_page = [&](int tile) {
     const int key = tile * kKeys + t;
-    page = t < kKeys && key < it.end ? __ldg(a.page_table + it.table + key / P) : -1;
+    // (as load_role: pages in front of what any row sees may hold anything)
+    page = t < kKeys && key >= it.low && key < it.end ? __ldg(a.page_table + it.table + key / P) : -1;
   };
   auto load_scales = [&](int tile) {
     ks = vs = 1.f;

@@ -1,5 +1,5 @@
 """Where decode behind shared prefixes ends what it reads: lists that part while other warps
-compare them, requests of no group, and bounds of groups that fall."""
+compare them, requests of no group, bounds of groups that fall, and pages behind every window."""
 from __future__ import annotations
 
 import math
@@ -12,7 +12,7 @@ import torch
 import pages_ref as ref
 import shared_ref as S
 from paged_split_kv_03_gb300 import binding as B
-from test_shared_gpu import check, reqs
+from test_shared_gpu import check, parity, reqs
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda", 0)
@@ -114,3 +114,25 @@ def test_groups_that_would_list_the_same_requests(bounds, dim, own):
         check(lse, l, lb, "lse")
     else:
         assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("max_kv", [1000, 4000])  # own tokens by one kernel; by pda_decode's
+@pytest.mark.parametrize("left", [1e-39, 1e-45, math.inf, -1.0, 0.0])
+@pytest.mark.parametrize("kind,dim", [("e4m3_token", 64), ("e4m3_token", 128), ("int8_token", 128),
+                                      ("e4m3_token", 256)])
+def test_scales_of_pages_behind_every_window(kind, dim, left, max_kv):
+    """What is left in the scales of pages that no row sees counts for nothing."""
+    page = 16
+    rs = [(70, 1), (33, 2), (200, 1), (90, 3)]
+    w = S.make([(40, rs), (13, rs)], kind=kind, dim=dim, page=page, dev=DEV,
+               windows=[100, 333, 230, 95, 40, 35, 52, 150])
+    w.params.max_kv_len = max_kv
+    seen = set()
+    for b, n in enumerate(w.kv_len):
+        low = max(0, n - w.rows[b] - w.windows[b] + 1)
+        seen.update(w.tables[b][low // page:])
+    gone = [i for i in range(w.pages) if i not in seen]
+    assert len(gone) > 18
+    for s in w.scale:
+        s[gone] = left
+    parity(w)
