@@ -177,21 +177,23 @@ struct CopyArgs {
 
 __global__ void __launch_bounds__(kThreads) copy_pages(const __grid_constant__ CopyArgs a) {
   grid_wait();
+  // (the lists by plain loads: the kernel in front, beside which this one has started, may have
+  // written them, and the read-only path is for memory that nobody writes meanwhile)
   int n = a.copies;
-  if (a.num_copies) n = min(n, __ldg(a.num_copies));
+  if (a.num_copies) n = min(n, *a.num_copies);
   const int64_t units = static_cast<int64_t>(max(n, 0)) * a.sides * a.pieces;
   bool oob = false;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int piece = static_cast<int>(u % a.pieces);
     const int64_t r = u / a.pieces;
     const int side = static_cast<int>(r % a.sides), c = static_cast<int>(r / a.sides);
-    const int src = __ldg(a.src + c), dst = __ldg(a.dst + c);
+    const int src = a.src[c], dst = a.dst[c];
     if (src == -1 || dst == -1 || src == dst) continue;
     if (src < 0 || dst < 0 || src >= a.num_pages || dst >= a.num_pages) {
       oob = true;
       continue;
     }
-    const int tokens = a.tokens ? max(0, min(a.page_size, __ldg(a.tokens + c))) : a.page_size;
+    const int tokens = a.tokens ? max(0, min(a.page_size, a.tokens[c])) : a.page_size;
     const uint8_t* from = a.side[side] + src * a.page_bytes;
     uint8_t* to = a.side[side] + dst * a.page_bytes;
     const int run = a.layout == 0 ? tokens * a.heads * a.row_vecs
