@@ -669,7 +669,8 @@ int pda_share_tables(const pda_shared_plan_t* plan, const pda_shared_tables* tab
 /* Decode on the tables that pda_share_tables filled, as pda_decode: q, the caches,
  * scales, out, lse (or NULL), sm_scale and max_q_len are its arguments. An invalid
  * request's rows are left unwritten, with its status bits; so are those of a request
- * with more own tokens than planned, and of one in no group or in an invalid one.
+ * with more own tokens than planned, of one in no group or in an invalid one, and of one whose
+ * rows are not among its group's (where another's are fewer than none).
  * Keys and values that a row does not see for its window have to be finite where
  * another row of its group sees them; pages that no row of the group sees may hold
  * anything. */

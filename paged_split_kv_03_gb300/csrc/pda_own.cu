@@ -492,8 +492,9 @@ __global__ void __launch_bounds__(32 * kMaxWarps, D == 256 ? 2 : 3) own_join(con
     }
   };
   Parts<kG> parts(a, group);
-  if (!parts.valid() && tid == 0 && h == 0 && m0 == 0 && rank == 0) atomicOr(a.status, PDA_STATUS_TABLE_INVALID);
-  const int live = parts.valid() ? min(kRows, M - m0) : 0, hw = lane >> 4;
+  const uint32_t bad = parts.bad(q0, R);
+  if (bad && tid == 0 && h == 0 && m0 == 0 && rank == 0) atomicOr(a.status, bad);
+  const int live = bad ? 0 : min(kRows, M - m0), hw = lane >> 4;
   __syncthreads();
   if (ctas > 1) {  // one part a CTA, in the first warp's place
 #pragma unroll 1
@@ -563,18 +564,19 @@ __global__ void __launch_bounds__(256, 3) shared_join(const __grid_constant__ Sh
   const int b = static_cast<int>(item / per_b);
   const int i = static_cast<int>(item % per_b) / a.hq, head = static_cast<int>(item % a.hq), h = head / a.group;
   bool live = b < a.batch;
-  int q0 = 0, own = 0;
+  int q0 = 0, R = 0, own = 0;
   if (live) {
     q0 = __ldg(a.qo_indptr + b);
-    const int R = __ldg(a.qo_indptr + b + 1) - q0;
+    R = __ldg(a.qo_indptr + b + 1) - q0;
     const int L = __ldg(a.own_len + b), W = a.window ? __ldg(a.window + b) : 0;
     live = i < R && R <= o.max_q_len && L >= R && L <= o.max_kv_len && q0 >= 0 && q0 + R <= a.rows_cap;
     if (live) own = split_range(L, R, W, a.page_size, chunk_for(o, b)).num_splits;
   }
   const int group = live ? group_of_request(a.group_indptr, a.groups, a.batch, b) : 0;
   Parts<kG> parts(a, max(group, 0));
-  if (live && (group < 0 || !parts.valid())) {
-    if ((threadIdx.x & 31) == 0) atomicOr(a.status, PDA_STATUS_TABLE_INVALID);
+  const uint32_t bad = group < 0 ? PDA_STATUS_TABLE_INVALID : parts.bad(q0, R);
+  if (live && bad) {
+    if ((threadIdx.x & 31) == 0) atomicOr(a.status, bad);
     live = false;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");

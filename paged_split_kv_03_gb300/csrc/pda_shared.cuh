@@ -193,8 +193,12 @@ struct Parts {
     const int before = upto - mine - (upto_s - singles) * (kFull - cut.one) + (upto_i - items) * cut.pay;
     first = __shfl_sync(0xffffffffu, before, g);
   }
-  // Whether its requests can be decoded.
-  __device__ __forceinline__ bool valid() const { return !gr.bad; }
+  // What keeps its request of rows [q0, q0 + R) from being decoded: rows that the prefix kernel
+  // has not seen (a request of fewer than none among the group's) would be without the prefix.
+  __device__ __forceinline__ uint32_t bad(int q0, int R) const {
+    if (gr.bad) return PDA_STATUS_TABLE_INVALID;
+    return gr.tiles && (q0 < gr.q0 || q0 + R > gr.q0 + gr.rows) ? PDA_STATUS_ROWS_GT_MAX : 0u;
+  }
   __device__ __forceinline__ void late(const SharedArgs& a) {
     if (a.groups <= 32) return;
     cut.per = a.first[0];

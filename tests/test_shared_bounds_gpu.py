@@ -1,5 +1,6 @@
 """Where decode behind shared prefixes ends what it reads: lists that part while other warps
-compare them, requests of no group, bounds of groups that fall, and pages behind every window."""
+compare them, requests of no group, bounds of groups that fall, pages behind every window, and
+rows that are not their group's."""
 from __future__ import annotations
 
 import math
@@ -136,3 +137,21 @@ def test_scales_of_pages_behind_every_window(kind, dim, left, max_kv):
     for s in w.scale:
         s[gone] = left
     parity(w)
+
+
+@pytest.mark.parametrize("own", [300, 0])
+@pytest.mark.parametrize("dim", [128, 256])
+def test_rows_outside_their_group(dim, own):
+    """A request of fewer than no rows takes those of the one in front out of the group's: they
+    are left alone, and not decoded without the prefix."""
+    w = S.make([(9, [(30, 3), (20, 1)]), (4, [(30, 1)])], dim=dim, dev=DEV)
+    w.qo, w.rows = [0, 3, 1, 1], [3, -2, 0]
+    w.params.max_kv_len = 4000
+    dec = B.Decoder(w.params, device=DEV)
+    sh, t = B.Shared(dec.plan, 2, own), S.device_tables(w)
+    t.qo_indptr = ints(w.qo)
+    out, lse = S.run(w, sh, t)
+    torch.cuda.synchronize()
+    assert t.prefix.tolist()[0] == [0, (174 - 3) // 16 * 16]  # the one valid request's whole pages
+    assert sh.status() == B.PDA_STATUS_ROWS_GT_MAX
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
