@@ -66,6 +66,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // running maximum before any key: finite, so a column with no visible key
 // so far gives ex2(-inf - kMInit) = 0 rather than NaN
 constexpr float kMInit = -3.0e38f;
+constexpr float kOne16 = 1.f / 65536.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ------------------------------------------------------------------ helpers
@@ -390,7 +391,17 @@ __device__ __forceinline__ void softmax_role(const DecodeArgs& a, const SoftmaxC
 
   float qk_scale = a.sm_scale * kLog2e;  // logits in log2 units
   if constexpr (C::kQSplit) qk_scale *= x.colscale[0];  // the query's 2^-a
-  if constexpr (C::kF16Ops) qk_scale *= 65536.f;        // (columns' scales are 2^-16 of the rows' powers)
+  if constexpr (C::kF16Ops) {
+    // Whether some row went in without its power of two. The columns' scales are 2^-16 of
+    // these, which the logit scale makes up for; all of it is exact. (The flag waits in shared memory,
+    // a word a warp: the loop's registers are full.)
+    bool any = false;
+#pragma unroll
+    for (int n = 0; n < C::kNmax; n += 32) any = any || x.colscale[min(n + lane, C::kNmax - 1)] != kOne16;
+    any = __any_sync(0xffffffffu, any);
+    if (lane == 0) x.linv[warp - 2] = any ? 1.f / kOne16 : 1.f;
+    __syncwarp();
+  }
   float v_final = 1.f;
   if constexpr (SMODE == PDA_SCALE_TENSOR) {
     qk_scale *= __ldg(a.k_scale);
@@ -448,6 +459,7 @@ __device__ __forceinline__ void softmax_role(const DecodeArgs& a, const SoftmaxC
   for (int j = 0; j < x.ntiles; ++j) {
     const int tok = x.t_begin + j * kTok + r;
     float row_scale = qk_scale, log2_vs = 0.f, inv_vs = 1.f;
+    if constexpr (C::kF16Ops) row_scale *= x.linv[warp - 2];
     if constexpr (SMODE == PDA_SCALE_TOKEN_HEAD) {
       const float ks = ks_a;
       float vs = vs_a;
@@ -481,6 +493,20 @@ __device__ __forceinline__ void softmax_role(const DecodeArgs& a, const SoftmaxC
     float s[NH];
     if (alive) {
       const uint32_t scol = tl + (j & 1) * C::kSCols + c0;
+      if constexpr (C::kF16Ops) {
+        if (x.linv[warp - 2] != 1.f) {  // rows get their powers back where S stands
+#pragma unroll 1
+          for (int ch = 0; ch < NCK; ++ch) {
+            float v[KC];
+            tmem_ldk<KC>(scol + ch * KC, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < KC; ++e) v[e] *= x.colscale[c0 + ch * KC + e];
+            tmem_stk<KC>(scol + ch * KC, v);
+          }
+          tmem_wait_st();
+        }
+      }
 #pragma unroll
       for (int ch = 0; ch < NCK; ++ch) {
         float v[KC];
@@ -494,8 +520,7 @@ __device__ __forceinline__ void softmax_role(const DecodeArgs& a, const SoftmaxC
         } else {
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < KC; ++e)  // (f16 operands: times the column's power of two, exact)
-            s[ch * KC + e] = C::kF16Ops ? v[e] * x.colscale[c0 + ch * KC + e] : v[e];
+          for (int e = 0; e < KC; ++e) s[ch * KC + e] = v[e];
         }
       }
     }
@@ -1285,7 +1310,8 @@ __global__ void __launch_bounds__(TcCfg<D, KVT, QT, SMODE, NMAX>::kThreads,
             if (top == 0u || ex == 128 || (ex >= -6 && ex < 16)) ex = 0;
             ex = max(-110, min(126, ex));
             by = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-            // (2^-16 of it: S is below 2^16, so that their product stays in range)
+            // (2^-16 of it, kOne16 for rows as they are: S is below 2^16, so that their product
+            // stays in range)
             if (cch == 0 && n < C::kNmax) colscale[n] = __uint_as_float(static_cast<uint32_t>(111 + ex) << 23);
           }
           if (n < N) {
