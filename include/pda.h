@@ -213,7 +213,10 @@ int pda_plan(const pda_params* params, pda_plan_t* out_plan, size_t* split_scrat
  *   sm_scale   logit scale (times the query's E4M3 scale when q is E4M3)
  *   k_scale,   NULL (bf16), fp32 [1] (per tensor) or fp32 [num_pages, P, Hkv]
  *              (E4M3 / int8)
- *   v_scale    (per token and kv head), device memory
+ *   v_scale    (per token and kv head), device memory; v_scale per token and head
+ *              not below 2^-90 of the largest one that a row sees: the weights are
+ *              summed with it, and that of a token with a smaller one may be lost
+ *              (a subnormal one: NaN)
  *   out        [qo_indptr[batch], Hq, head_dim_v] bf16
  *   lse        [qo_indptr[batch], Hq] fp32 natural-log LSE, or NULL
  *   split_scratch  plan->scratch_bytes of device memory (see pda_plan)
@@ -673,7 +676,8 @@ int pda_share_tables(const pda_shared_plan_t* plan, const pda_shared_tables* tab
  * rows are not among its group's (where another's are fewer than none).
  * Keys and values that a row does not see for its window have to be finite where
  * another row of its group sees them; pages that no row of the group sees may hold
- * anything. */
+ * anything, and so may their scales. After PDA_STATUS_WAIT_TIMEOUT the rows' values mean
+ * nothing. */
 int pda_decode_shared(const pda_shared_plan_t* plan, const void* q, const void* k_pages,
                       const void* v_pages, const pda_shared_tables* tables, int32_t max_q_len,
                       float sm_scale, const float* k_scale, const float* v_scale, void* out,

@@ -654,8 +654,8 @@ int launch_own(const pda_plan_t* own, const SharedArgs& a, const DecodeArgs& o, 
   const int64_t items = static_cast<int64_t>(a.batch) * a.hkv * tiles;
   // Few items: clusters of up to four CTAs, while all of them have an SM. Many: as few
   // warps a CTA as end sooner, where four would leave a last wave of few CTAs (a step of
-  // 16 tokens takes about 2 us with all SMs at it, a CTA's start and join 6; half of the
-  // most tokens taken for all).
+  // 16 tokens takes about 2 us with all SMs at it, a CTA's start and join 6, both from 64
+  // requests with 8 kv heads of 128; half of the most tokens taken for all).
   int cluster = 1, warps = kMaxWarps;
   while (cluster < 4 && items * cluster * 2 <= own->num_sms) cluster *= 2;
   if (cluster == 1) {

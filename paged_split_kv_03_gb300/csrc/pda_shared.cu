@@ -1215,7 +1215,7 @@ __global__ void __launch_bounds__(Cfg<D, k8, kI8, kTok>::kThreads, 1)
 //
 // Bound: latency. A cluster of CTAs per group; its warps take stretches of the requests'
 // lists in turn, the first of all requests first, and leave out those behind what another
-// has found to be the end. 64 requests of 80 pages: 5.0 us, 512 of 704 in 64 groups: 7.2
+// has found to be the end. 64 requests of 80 pages: 4.6 us, 512 of 704 in 64 groups: 7.9
 // (a group's lists by one CTA: 17.8).
 constexpr int kShareThreads = 256;
 constexpr int kShareWarps = kShareThreads / 32;
